@@ -386,10 +386,177 @@ typedef struct la_notebank_route_args {
 } la_notebank_route_args;
 la_status la_notebank_route(const la_notebank_route_args* args, void* stream);
 
+/* ---- The other layers of a hybrid model: the short causal convolution, the
+ * selective state space scan and masked window attention over a prompt, each
+ * with its one-token step.  (BASED, paper Sec. 4: 1.3B models mix Taylor
+ * linear attention, sliding-window attention and short convolutions; gated
+ * DeltaNet and Mamba backbones carry a 4-tap convolution in front of their
+ * recurrence, NoteBank App. C.6, Eq. (20).)
+ *
+ * Rules they share, beside the conventions at the top of this header:
+ *   - [B, N, C] activations are la_tensor views whose stride_h is ignored;
+ *     the channel axis is contiguous; base pointers and the b and t strides
+ *     are 16-byte aligned.  C itself may be any size >= 1.
+ *   - lens: NULL (every sequence has N tokens) or [B] int64 on the device:
+ *     tokens lens[b]..N-1 of sequence b are padding.  Padding is not read
+ *     into any result (it may hold NaN), output rows of padding are left as
+ *     they were, and the state is the one after token lens[b] - 1.  A length
+ *     outside [0, N] skips the whole sequence (nothing of it is written) and
+ *     sets the device status word (LA_ERR_INVALID_ARGUMENT).
+ *   - outputs must not overlap inputs, except a state updated in place
+ *     (state_out == state_in). */
+
+/* Causal depthwise convolution over a prompt.
+ *   y_t[c] = act(bias[c] + sum_{i<W} w[c,i] x_{t-W+1+i}[c]),   act = identity or SiLU
+ *   x, y  : [B, N, C] in_dtype / out_dtype views
+ *   w     : [C, W] w_dtype contiguous (tap W-1 meets the token itself), W in 2..4
+ *   bias  : [C] w_dtype or NULL; w and bias 16-byte aligned
+ *   state : [B, W-1, C] in_dtype contiguous, the last W-1 inputs, oldest first;
+ *           state_in NULL = zeros; state_out required, may alias state_in.
+ * fp32 arithmetic. */
+typedef struct la_conv_prefill_args {
+  int64_t B, N, C, W;
+  la_dtype in_dtype, out_dtype, w_dtype;
+  la_tensor x, y;
+  const void* w;
+  const void* bias;
+  const void* state_in;
+  void* state_out;
+  const int64_t* lens;
+  int32_t silu;
+} la_conv_prefill_args;
+la_status la_conv_prefill(const la_conv_prefill_args* args, void* stream);
+
+/* The same for one token of each of S sequences (x, out: [S, C] rows,
+ * x_stride / out_stride elements apart, rows 16-byte aligned; state [S, W-1, C]
+ * contiguous; state_out may alias state_in).  Launched as a programmatic
+ * dependent, as la_decode_step. */
+typedef struct la_conv_decode_args {
+  int64_t S, C, W;
+  la_dtype in_dtype, out_dtype, w_dtype;
+  const void* x;
+  int64_t x_stride;
+  void* out;
+  int64_t out_stride;
+  const void* w;
+  const void* bias;
+  const void* state_in;
+  void* state_out;
+  int32_t silu;
+} la_conv_decode_args;
+la_status la_conv_decode_step(const la_conv_decode_args* args, void* stream);
+
+/* Selective state space scan over a prompt (diagonal state transition):
+ *   dt_t[c]  = f(delta_t[c] + delta_bias[c]),      f = softplus or identity
+ *   h_t[c,s] = exp(dt_t[c] A[c,s]) h_{t-1}[c,s] + dt_t[c] u_t[c] B_t[g,s]
+ *   y_t[c]   = (sum_s C_t[g,s] h_t[c,s] + D[c] u_t[c]) * silu(z_t[c])
+ * with g = c / (C / G).  Eq. (1) of NoteBank Sec. 2 with a diagonal A_t that
+ * depends on the token, per (channel, state).
+ *   u, delta, z : [B, N, C] in_dtype views (z.ptr NULL: no gate)
+ *   Bm, Cm      : [B, G, N, n] in_dtype views (stride_h = group); the state
+ *                 axis is contiguous, any element alignment; C % G == 0
+ *   A           : [C, n] fp32 contiguous (negative where the state decays)
+ *   D, delta_bias : [C] fp32 or NULL
+ *   y           : [B, N, C] out_dtype view
+ *   h_in, h_out : [B, C, n] fp32 contiguous; h_in NULL = zeros; h_out required,
+ *                 may alias h_in.  n in 1..64.
+ * fp32 arithmetic and state.  Problems with few channels and many tokens are
+ * scanned in time segments, whose states need the workspace that
+ * la_ssm_prefill_workspace_size returns (often 0; a function of the sizes
+ * only; 16-byte aligned, dead when the call's work has finished).  A call
+ * with a smaller workspace fails with LA_ERR_WORKSPACE. */
+typedef struct la_ssm_prefill_args {
+  int64_t B, N, C, n, G;
+  la_dtype in_dtype, out_dtype;
+  la_tensor u, delta, z, y;
+  la_tensor Bm, Cm;
+  const float* A;
+  const float* D;
+  const float* delta_bias;
+  const float* h_in;
+  float* h_out;
+  const int64_t* lens;
+  int32_t delta_softplus;
+} la_ssm_prefill_args;
+size_t la_ssm_prefill_workspace_size(const la_ssm_prefill_args* args);
+la_status la_ssm_prefill(const la_ssm_prefill_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same for one token of each of S sequences: u, delta, z, out are [S, C]
+ * rows (stride_b elements apart, any element alignment; stride_h, stride_t
+ * ignored), Bm, Cm [S, G, n] (stride_b, stride_h), states [S, C, n] fp32
+ * contiguous (state_out may alias state_in).  Launched as a programmatic
+ * dependent, as la_decode_step. */
+typedef struct la_ssm_decode_args {
+  int64_t S, C, n, G;
+  la_dtype in_dtype, out_dtype;
+  la_tensor u, delta, z, out;
+  la_tensor Bm, Cm;
+  const float* A;
+  const float* D;
+  const float* delta_bias;
+  const float* state_in;
+  float* state_out;
+  int32_t delta_softplus;
+} la_ssm_decode_args;
+la_status la_ssm_decode_step(const la_ssm_decode_args* args, void* stream);
+
+/* Softmax attention of a prompt's queries, the window layers of BASED (BASED
+ * notes Sec. 2.4) with what other models add to the scores and masks:
+ *   s_ij = cap tanh(scale q_i.k_j / cap) - slope_h |p_i - j|     (cap = 0: no cap)
+ *   o_i  = sum_j softmax_j(s_ij) v_j   over the keys that query i sees
+ * Query i stands at key position p_i = q_pos0 + i and sees the keys j with
+ *   max(key_lo[b,i], p_i - window + 1) <= j < key_hi[b,i],  0 <= j < Nk (lens[b])
+ * (window 0: no window; key_lo NULL: 0; key_hi NULL: p_i + 1, the causal
+ * mask).  One interval per query expresses packed documents (key_lo = the
+ * document's first token), bidirectional prefixes (key_hi = the prefix's end)
+ * and queries that see nothing, whose output is zero.  Masked keys and values
+ * reach no output, whatever they hold (NaN included).
+ *   q, o   : [B, H, Nq, d] views;  k, v : [B, H_kv, Nk, d] views, H % H_kv == 0
+ *            (query head h reads key head h / (H / H_kv)); d a multiple of 8 in [8, 128]
+ *   slopes : [H] fp32 or NULL;  key_lo, key_hi : [B, Nq] int32 or NULL
+ *   lens   : as above, over Nk; queries with p_i >= lens[b] are padding
+ *   q_pos0 : 0 <= q_pos0 and q_pos0 + Nq <= Nk (Nq < Nk: the queries go on
+ *            from keys of earlier calls)
+ *   k_cache, v_cache : NULL, or [B, H_kv, window, d] in_dtype contiguous rings
+ *            (1 <= window <= 256): the last min(lens[b], window) tokens are
+ *            stored for la_swa_decode_step / la_swa_biased_decode_step (token
+ *            p in slot p % window; other slots are left as they were).
+ * bf16 inputs: products on the tensor cores with fp32 sums and statistics,
+ * the softmax weights rounded to bf16 for their product with v.  fp32 inputs:
+ * fp32 throughout. */
+typedef struct la_swa_prefill_args {
+  int64_t B, H, H_kv, Nq, Nk, d, window;
+  la_dtype in_dtype, out_dtype;
+  la_tensor q, k, v, o;
+  float scale, softcap;
+  const float* slopes;
+  const int32_t* key_lo;
+  const int32_t* key_hi;
+  int64_t q_pos0;
+  const int64_t* lens;
+  void* k_cache;
+  void* v_cache;
+} la_swa_prefill_args;
+la_status la_swa_prefill(const la_swa_prefill_args* args, void* stream);
+
+/* la_swa_decode_step with grouped heads, capped scores and a distance bias.
+ * Arguments as in la_swa_decode_args (base.q, base.out: [S, H, d]; base.k,
+ * base.v: [S, H_kv, d]; base.k_cache, base.v_cache: [S, H_kv, window, d]);
+ * slopes [H] fp32 or NULL, softcap 0 = no cap.  H % H_kv == 0, H / H_kv <= 16.
+ * A negative position skips that sequence and sets the device status word. */
+typedef struct la_swa_biased_decode_args {
+  la_swa_decode_args base;
+  int64_t H_kv;
+  float softcap;
+  const float* slopes;
+} la_swa_biased_decode_args;
+la_status la_swa_biased_decode_step(const la_swa_biased_decode_args* args, void* stream);
+
 /* Synchronises `stream`, then reports (and clears when `clear` != 0) the
  * device-side status word: LA_ERR_TIMEOUT when a bounded wait expired,
  * LA_ERR_INVALID_ARGUMENT when la_state_gather skipped an out-of-range
- * index, la_swa_decode_step met a negative position or la_notebank_address
+ * index, la_swa_decode_step or la_swa_biased_decode_step met a negative
+ * position, a prefill a sequence length out of range or la_notebank_address
  * a bad span or coordinate, else LA_OK; LA_ERR_CUDA if the synchronisation
  * failed. */
 la_status la_device_status(void* stream, int clear);

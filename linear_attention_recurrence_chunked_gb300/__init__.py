@@ -72,7 +72,8 @@ class DecodeArgs(ctypes.Structure):
 EXPORTED = ("la_based_prefill", "la_gdn_prefill", "la_gated_prefill", "la_decode_step", "la_based_prefill_workspace_size",
             "la_gdn_prefill_workspace_size", "la_gdn_prefill_workspace_size_min", "la_gdn_prefill_noalloc", "la_device_status",
             "la_state_rescale", "la_state_gather", "la_swa_decode_step", "la_notebank_scores", "la_notebank_address",
-            "la_notebank_route", "la_selftest_bounded_wait", "la_status_string", "la_abi_version",
+            "la_notebank_route", "la_conv_prefill", "la_conv_decode_step", "la_ssm_prefill_workspace_size", "la_ssm_prefill",
+            "la_ssm_decode_step", "la_swa_prefill", "la_swa_biased_decode_step", "la_selftest_bounded_wait", "la_status_string", "la_abi_version",
             "la_last_cuda_error", "la_cuda_error_name")
 
 
@@ -101,6 +102,54 @@ class SwaDecodeArgs(ctypes.Structure):
                 ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("pos", ctypes.c_void_p),
                 ("out", ctypes.c_void_p), ("scale", ctypes.c_float)]
+
+
+class ConvPrefillArgs(ctypes.Structure):
+    _fields_ = [("B", _i64), ("N", _i64), ("C", _i64), ("W", _i64),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
+                ("x", LATensor), ("y", LATensor), ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("state_in", ctypes.c_void_p), ("state_out", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("silu", ctypes.c_int32)]
+
+
+class ConvDecodeArgs(ctypes.Structure):
+    _fields_ = [("S", _i64), ("C", _i64), ("W", _i64),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
+                ("x", ctypes.c_void_p), ("x_stride", _i64), ("out", ctypes.c_void_p), ("out_stride", _i64),
+                ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("state_in", ctypes.c_void_p), ("state_out", ctypes.c_void_p), ("silu", ctypes.c_int32)]
+
+
+class SsmPrefillArgs(ctypes.Structure):
+    _fields_ = [("B", _i64), ("N", _i64), ("C", _i64), ("n", _i64), ("G", _i64),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("u", LATensor), ("delta", LATensor), ("z", LATensor), ("y", LATensor),
+                ("Bm", LATensor), ("Cm", LATensor),
+                ("A", ctypes.c_void_p), ("D", ctypes.c_void_p), ("delta_bias", ctypes.c_void_p),
+                ("h_in", ctypes.c_void_p), ("h_out", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("delta_softplus", ctypes.c_int32)]
+
+
+class SsmDecodeArgs(ctypes.Structure):
+    _fields_ = [("S", _i64), ("C", _i64), ("n", _i64), ("G", _i64),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("u", LATensor), ("delta", LATensor), ("z", LATensor), ("out", LATensor),
+                ("Bm", LATensor), ("Cm", LATensor),
+                ("A", ctypes.c_void_p), ("D", ctypes.c_void_p), ("delta_bias", ctypes.c_void_p),
+                ("state_in", ctypes.c_void_p), ("state_out", ctypes.c_void_p), ("delta_softplus", ctypes.c_int32)]
+
+
+class SwaPrefillArgs(ctypes.Structure):
+    _fields_ = [("B", _i64), ("H", _i64), ("H_kv", _i64), ("Nq", _i64), ("Nk", _i64), ("d", _i64), ("window", _i64),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("q", LATensor), ("k", LATensor), ("v", LATensor), ("o", LATensor),
+                ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("key_lo", ctypes.c_void_p), ("key_hi", ctypes.c_void_p), ("q_pos0", _i64), ("lens", ctypes.c_void_p),
+                ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p)]
+
+
+class SwaBiasedDecodeArgs(ctypes.Structure):
+    _fields_ = [("base", SwaDecodeArgs), ("H_kv", _i64), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p)]
 
 
 class LAError(RuntimeError):
@@ -155,6 +204,20 @@ def load_library(path: str | None = None):
     lib.la_notebank_address.argtypes = [ctypes.POINTER(NotebankAddressArgs), vp]
     lib.la_notebank_route.restype = ctypes.c_int
     lib.la_notebank_route.argtypes = [ctypes.POINTER(NotebankRouteArgs), vp]
+    lib.la_conv_prefill.restype = ctypes.c_int
+    lib.la_conv_prefill.argtypes = [ctypes.POINTER(ConvPrefillArgs), vp]
+    lib.la_conv_decode_step.restype = ctypes.c_int
+    lib.la_conv_decode_step.argtypes = [ctypes.POINTER(ConvDecodeArgs), vp]
+    lib.la_ssm_prefill_workspace_size.restype = ctypes.c_size_t
+    lib.la_ssm_prefill_workspace_size.argtypes = [ctypes.POINTER(SsmPrefillArgs)]
+    lib.la_ssm_prefill.restype = ctypes.c_int
+    lib.la_ssm_prefill.argtypes = [ctypes.POINTER(SsmPrefillArgs), vp, ctypes.c_size_t, vp]
+    lib.la_ssm_decode_step.restype = ctypes.c_int
+    lib.la_ssm_decode_step.argtypes = [ctypes.POINTER(SsmDecodeArgs), vp]
+    lib.la_swa_prefill.restype = ctypes.c_int
+    lib.la_swa_prefill.argtypes = [ctypes.POINTER(SwaPrefillArgs), vp]
+    lib.la_swa_biased_decode_step.restype = ctypes.c_int
+    lib.la_swa_biased_decode_step.argtypes = [ctypes.POINTER(SwaBiasedDecodeArgs), vp]
     lib.la_state_rescale.restype = ctypes.c_int
     lib.la_state_rescale.argtypes = [vp, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_float, vp]
     lib.la_state_gather.restype = ctypes.c_int
@@ -540,6 +603,274 @@ def la_notebank_route(rho, u, R: int, positions=None, want_scores: bool = False,
     if st != LA_OK:
         raise LAError(st, "la_notebank_route")
     return top, winner, votes, s
+
+
+# ---------------------------------------------------------------------------
+# the other layers of a hybrid model: convolution, selective scan, window attention
+
+
+def _same_device(first, **others):
+    """Every tensor given lives on `first`'s CUDA device."""
+    _check_cuda(first, *others.values())
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, the first argument on {first.device}")
+
+
+def _expect(name, t, shape, dtype, contiguous=True):
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not contiguous and t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+
+
+def _axis_stride(t, i):
+    """Stride of axis i; 0 where the axis has one entry and its stride says nothing."""
+    return t.stride(i) if t.shape[i] > 1 else 0
+
+
+def _rows3(t) -> LATensor:
+    """[B,N,C] tensor -> view (stride_h unused); None -> a null view."""
+    return LATensor(None, 0, 0, 0) if t is None else LATensor(t.data_ptr(), _axis_stride(t, 0), 0, _axis_stride(t, 1))
+
+
+def _heads4(t) -> LATensor:
+    return LATensor(t.data_ptr(), *(_axis_stride(t, i) for i in range(3)))
+
+
+def _new_rows(shape, dtype, device, zero=False):
+    """An output whose rows start on 16-byte boundaries whatever the last size is."""
+    pad = -(-shape[-1] // 8) * 8
+    t = (torch.zeros if zero else torch.empty)((*shape[:-1], pad), dtype=dtype, device=device)
+    return t[..., :shape[-1]]
+
+
+def _call(fn_name, device, stream, *args):
+    """Call an entry point with `device` current, on `stream` or that device's current stream."""
+    with torch.cuda.device(device):
+        handle = _stream_handle(stream if stream is not None else torch.cuda.current_stream(device))
+        st = getattr(load_library(), fn_name)(*args, handle)
+    if st != LA_OK:
+        raise LAError(st, fn_name)
+
+
+def la_conv_prefill(x, w, bias=None, state_in=None, lens=None, silu: bool = True, y=None, state_out=None,
+                    out_dtype=None, stream=None):
+    """Short causal depthwise convolution of a prompt.  Returns (y, state_out).
+
+    x: [B,N,C] (fp32 or bf16, channels contiguous, rows 16-byte aligned); w:
+    [C,W], W in 2..4, and bias [C] or None, both fp32 or both bf16; state:
+    [B,W-1,C] in x's dtype, the last inputs, oldest first (None: zeros; state_out
+    may be state_in).  lens: None or int64 [B] on the device: later tokens are
+    padding, their rows of y stay as they were (zeros in a y made here)."""
+    _same_device(x, w=w, bias=bias, state_in=state_in, lens=lens, y=y, state_out=state_out)
+    if x.dim() != 3 or w.dim() != 2:
+        raise ValueError("x must be [B,N,C] and w [C,W]")
+    B, N, C = x.shape
+    W = w.shape[1]
+    _expect("x", x, (B, N, C), x.dtype, contiguous=False)
+    _expect("w", w, (C, W), w.dtype)
+    _expect("bias", bias, (C,), w.dtype)
+    _expect("lens", lens, (B,), torch.int64)
+    for name, t in (("state_in", state_in), ("state_out", state_out)):
+        _expect(name, t, (B, W - 1, C), x.dtype)
+    if y is None:
+        y = _new_rows((B, N, C), out_dtype or x.dtype, x.device, zero=lens is not None)
+    _expect("y", y, (B, N, C), y.dtype, contiguous=False)
+    if state_out is None:
+        state_out = torch.empty((B, max(W - 1, 0), C), dtype=x.dtype, device=x.device)
+        if lens is not None:  # a sequence whose length is out of range is left as it was
+            state_out.copy_(state_in) if state_in is not None else state_out.zero_()
+    a = ConvPrefillArgs(B, N, C, W, _dtype_code(x.dtype), _dtype_code(y.dtype), _dtype_code(w.dtype), _rows3(x),
+                        _rows3(y), _ptr(w), _ptr(bias), _ptr(state_in), _ptr(state_out), _ptr(lens), int(bool(silu)))
+    _call("la_conv_prefill", x.device, stream, ctypes.byref(a))
+    return y, state_out
+
+
+def la_conv_decode_step(x, w, state, bias=None, silu: bool = True, out=None, state_out=None, out_dtype=None,
+                        stream=None):
+    """The convolution's step for one token of each sequence.  x: [S,C] (rows
+    16-byte aligned); w, bias as in la_conv_prefill; state: [S,W-1,C], updated in
+    place unless state_out is given.  Returns out [S,C]."""
+    _same_device(x, w=w, state=state, bias=bias, out=out, state_out=state_out)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [S,C] and w [C,W]")
+    S, C = x.shape
+    W = w.shape[1]
+    state_out = state if state_out is None else state_out
+    _expect("x", x, (S, C), x.dtype, contiguous=False)
+    _expect("w", w, (C, W), w.dtype)
+    _expect("bias", bias, (C,), w.dtype)
+    _expect("state", state, (S, W - 1, C), x.dtype)
+    _expect("state_out", state_out, (S, W - 1, C), x.dtype)
+    if out is None:
+        out = _new_rows((S, C), out_dtype or x.dtype, x.device)
+    _expect("out", out, (S, C), out.dtype, contiguous=False)
+    a = ConvDecodeArgs(S, C, W, _dtype_code(x.dtype), _dtype_code(out.dtype), _dtype_code(w.dtype), _ptr(x),
+                       _axis_stride(x, 0), _ptr(out), _axis_stride(out, 0), _ptr(w), _ptr(bias), _ptr(state),
+                       _ptr(state_out), int(bool(silu)))
+    _call("la_conv_decode_step", x.device, stream, ctypes.byref(a))
+    return out
+
+
+def _ssm_prefill_args(u, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus, h_in, lens, y, h_out):
+    B, N, C = u.shape
+    return SsmPrefillArgs(B, N, C, A.shape[1], Bm.shape[1], _dtype_code(u.dtype), _dtype_code(y.dtype), _rows3(u),
+                          _rows3(delta), _rows3(z), _rows3(y), _heads4(Bm), _heads4(Cm), _ptr(A), _ptr(D),
+                          _ptr(delta_bias), _ptr(h_in), _ptr(h_out), _ptr(lens), int(bool(delta_softplus)))
+
+
+def la_ssm_prefill_workspace_size(u, delta, A, Bm, Cm) -> int:
+    a = _ssm_prefill_args(u, delta, A, Bm, Cm, None, None, None, True, None, None, u, None)
+    return int(load_library().la_ssm_prefill_workspace_size(ctypes.byref(a)))
+
+
+def la_ssm_prefill(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, delta_softplus: bool = True, h_in=None,
+                   lens=None, y=None, h_out=None, out_dtype=None, workspace=None, stream=None):
+    """Selective state space scan of a prompt.  Returns (y, h_out).
+
+        dt = softplus(delta + delta_bias)   (delta + delta_bias without delta_softplus)
+        h <- exp(dt A) h + dt u B;   y = (C h + D u) silu(z)
+
+    u, delta, z: [B,N,C] (fp32 or bf16, rows 16-byte aligned); A: fp32 [C,n];
+    Bm, Cm: [B,G,N,n] in u's dtype (channel c reads group c // (C // G)); D,
+    delta_bias: fp32 [C] or None; h: fp32 [B,C,n] (h_out may be h_in); lens as in
+    la_conv_prefill; workspace: uint8 device tensor of at least
+    la_ssm_prefill_workspace_size bytes, allocated here by default."""
+    _same_device(u, delta=delta, A=A, Bm=Bm, Cm=Cm, D=D, z=z, delta_bias=delta_bias, h_in=h_in, lens=lens, y=y,
+                 h_out=h_out, workspace=workspace)
+    if u.dim() != 3 or A.dim() != 2 or Bm.dim() != 4:
+        raise ValueError("u must be [B,N,C], A [C,n] and Bm, Cm [B,G,N,n]")
+    B, N, C = u.shape
+    n, G = A.shape[1], Bm.shape[1]
+    for name, t in (("u", u), ("delta", delta), ("z", z)):
+        _expect(name, t, (B, N, C), u.dtype, contiguous=False)
+    for name, t in (("Bm", Bm), ("Cm", Cm)):
+        _expect(name, t, (B, G, N, n), u.dtype, contiguous=False)
+    _expect("A", A, (C, n), torch.float32)
+    for name, t in (("D", D), ("delta_bias", delta_bias)):
+        _expect(name, t, (C,), torch.float32)
+    for name, t in (("h_in", h_in), ("h_out", h_out)):
+        _expect(name, t, (B, C, n), torch.float32)
+    _expect("lens", lens, (B,), torch.int64)
+    if y is None:
+        y = _new_rows((B, N, C), out_dtype or u.dtype, u.device, zero=lens is not None)
+    _expect("y", y, (B, N, C), y.dtype, contiguous=False)
+    if h_out is None:
+        h_out = torch.empty((B, C, n), dtype=torch.float32, device=u.device)
+        if lens is not None:
+            h_out.copy_(h_in) if h_in is not None else h_out.zero_()
+    a = _ssm_prefill_args(u, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus, h_in, lens, y, h_out)
+    need = int(load_library().la_ssm_prefill_workspace_size(ctypes.byref(a)))
+    ws, ws_bytes = _workspace(need, workspace, u.device)
+    _call("la_ssm_prefill", u.device, stream, ctypes.byref(a), _ptr(ws) if isinstance(ws, torch.Tensor) else ws,
+          ws_bytes)
+    return y, h_out
+
+
+def la_ssm_decode_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None, delta_softplus: bool = True,
+                       out=None, state_out=None, out_dtype=None, stream=None):
+    """The scan's step for one token of each sequence.  u, delta, z: [S,C]; Bm,
+    Cm: [S,G,n]; state: fp32 [S,C,n], updated in place unless state_out is given;
+    the rest as in la_ssm_prefill.  Returns out [S,C]."""
+    _same_device(u, delta=delta, A=A, Bm=Bm, Cm=Cm, state=state, D=D, z=z, delta_bias=delta_bias, out=out,
+                 state_out=state_out)
+    if u.dim() != 2 or A.dim() != 2 or Bm.dim() != 3:
+        raise ValueError("u must be [S,C], A [C,n] and Bm, Cm [S,G,n]")
+    S, C = u.shape
+    n, G = A.shape[1], Bm.shape[1]
+    state_out = state if state_out is None else state_out
+    for name, t in (("u", u), ("delta", delta), ("z", z)):
+        _expect(name, t, (S, C), u.dtype, contiguous=False)
+    for name, t in (("Bm", Bm), ("Cm", Cm)):
+        _expect(name, t, (S, G, n), u.dtype, contiguous=False)
+    _expect("A", A, (C, n), torch.float32)
+    for name, t in (("D", D), ("delta_bias", delta_bias)):
+        _expect(name, t, (C,), torch.float32)
+    for name, t in (("state", state), ("state_out", state_out)):
+        _expect(name, t, (S, C, n), torch.float32)
+    if out is None:
+        out = torch.empty((S, C), dtype=out_dtype or u.dtype, device=u.device)
+    _expect("out", out, (S, C), out.dtype, contiguous=False)
+    row = lambda t: LATensor(None, 0, 0, 0) if t is None else LATensor(t.data_ptr(), _axis_stride(t, 0), 0, 0)  # noqa: E731
+    grp = lambda t: LATensor(t.data_ptr(), _axis_stride(t, 0), _axis_stride(t, 1), 0)  # noqa: E731
+    a = SsmDecodeArgs(S, C, n, G, _dtype_code(u.dtype), _dtype_code(out.dtype), row(u), row(delta), row(z), row(out),
+                      grp(Bm), grp(Cm), _ptr(A), _ptr(D), _ptr(delta_bias), _ptr(state), _ptr(state_out),
+                      int(bool(delta_softplus)))
+    _call("la_ssm_decode_step", u.device, stream, ctypes.byref(a))
+    return out
+
+
+def la_swa_prefill(q, k, v, window: int = 0, scale: float | None = None, softcap: float = 0.0, slopes=None,
+                   key_lo=None, key_hi=None, q_pos0: int | None = None, lens=None, o=None, k_cache=None, v_cache=None,
+                   out_dtype=None, stream=None):
+    """Softmax attention of a prompt's queries.  Returns o [B,H,Nq,d].
+
+    q: [B,H,Nq,d], k, v: [B,H_kv,Nk,d] (fp32 or bf16; H a multiple of H_kv; d a
+    multiple of 8 up to 128).  Query i stands at key position p = q_pos0 + i
+    (default: the last Nq of Nk) and sees the keys from max(key_lo[b,i], p -
+    window + 1) to key_hi[b,i] - 1 (int32 [B,Nq]; default: every key up to p;
+    window 0: unbounded); a query that sees nothing gives zeros.  Scores: softcap
+    tanh(scale q.k / softcap) (0: no cap) - slopes[h] |p - j| (fp32 [H] or None).
+    lens: None or int64 [B]: later keys are not seen and later queries' rows of o
+    stay as they were.  k_cache, v_cache: [B,H_kv,window,d] rings to fill for
+    la_swa_decode_step and la_swa_biased_decode_step (window <= 256)."""
+    _same_device(q, k=k, v=v, slopes=slopes, key_lo=key_lo, key_hi=key_hi, lens=lens, o=o, k_cache=k_cache,
+                 v_cache=v_cache)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B,H,Nq,d] and k, v [B,H_kv,Nk,d]")
+    B, H, Nq, d = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    _expect("q", q, (B, H, Nq, d), q.dtype, contiguous=False)
+    for name, t in (("k", k), ("v", v)):
+        _expect(name, t, (B, Hkv, Nk, d), q.dtype, contiguous=False)
+    _expect("slopes", slopes, (H,), torch.float32)
+    for name, t in (("key_lo", key_lo), ("key_hi", key_hi)):
+        _expect(name, t, (B, Nq), torch.int32)
+    _expect("lens", lens, (B,), torch.int64)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _expect(name, t, (B, Hkv, window, d), q.dtype)
+    if o is None:
+        o = (torch.zeros if lens is not None else torch.empty)((B, H, Nq, d), dtype=out_dtype or q.dtype, device=q.device)
+    _expect("o", o, (B, H, Nq, d), o.dtype, contiguous=False)
+    a = SwaPrefillArgs(B, H, Hkv, Nq, Nk, d, int(window), _dtype_code(q.dtype), _dtype_code(o.dtype), _heads4(q),
+                       _heads4(k), _heads4(v), _heads4(o), float(scale if scale is not None else d ** -0.5),
+                       float(softcap), _ptr(slopes), _ptr(key_lo), _ptr(key_hi),
+                       int(q_pos0 if q_pos0 is not None else Nk - Nq), _ptr(lens), _ptr(k_cache), _ptr(v_cache))
+    _call("la_swa_prefill", q.device, stream, ctypes.byref(a))
+    return o
+
+
+def la_swa_biased_decode_step(q, k, v, k_cache, v_cache, pos, softcap: float = 0.0, slopes=None, out=None,
+                              scale: float | None = None, out_dtype=None, stream=None):
+    """la_swa_decode_step with grouped heads, capped scores and a distance bias:
+    q: [S,H,d]; k, v: [S,H_kv,d]; k_cache, v_cache: [S,H_kv,window,d]; pos: int64
+    [S]; softcap and slopes as in la_swa_prefill.  Returns out [S,H,d]."""
+    _same_device(q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, pos=pos, slopes=slopes, out=out)
+    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [S,H,d], k, v [S,H_kv,d] and the caches [S,H_kv,window,d]")
+    S, H, d = q.shape
+    Hkv, window = k.shape[1], k_cache.shape[2]
+    _expect("q", q, (S, H, d), q.dtype)
+    for name, t in (("k", k), ("v", v)):
+        _expect(name, t, (S, Hkv, d), q.dtype)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _expect(name, t, (S, Hkv, window, d), q.dtype)
+    _expect("pos", pos, (S,), torch.int64)
+    _expect("slopes", slopes, (H,), torch.float32)
+    if out is None:
+        out = torch.empty((S, H, d), dtype=out_dtype or q.dtype, device=q.device)
+    _expect("out", out, (S, H, d), out.dtype)
+    base = SwaDecodeArgs(S, H, d, window, _dtype_code(q.dtype), _dtype_code(out.dtype), _ptr(q), _ptr(k), _ptr(v),
+                         _ptr(k_cache), _ptr(v_cache), _ptr(pos), _ptr(out),
+                         float(scale if scale is not None else d ** -0.5))
+    a = SwaBiasedDecodeArgs(base, Hkv, float(softcap), _ptr(slopes))
+    _call("la_swa_biased_decode_step", q.device, stream, ctypes.byref(a))
+    return out
 
 
 def la_device_status(stream=None, clear: bool = True) -> int:

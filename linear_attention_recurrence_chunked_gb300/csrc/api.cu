@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "kernels.h"
 #include "la.h"
 
@@ -396,6 +398,217 @@ la_status la_notebank_route(const la_notebank_route_args* a, void* stream) {
   L.rho = a->rho; L.u = a->u; L.positions = a->positions; L.s = a->s;
   L.winner = a->winner; L.votes = a->votes; L.top = a->top;
   return from_cuda(la::launch_notebank_route(L, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// Whether the product of sizes in [0, kMaxDim] stays within `limit`.
+bool within(int64_t limit, std::initializer_list<int64_t> sizes) {
+  int64_t p = 1;
+  for (const int64_t s : sizes) {
+    if (s == 0) return true;
+    if (p > limit / s) return false;
+    p *= s;
+  }
+  return true;
+}
+bool valid_size(int64_t s) { return s >= 0 && s <= kMaxDim; }
+
+// [B, N, C] view: as a [B, 1, N, C] one; an output's sequences must not lie on one another
+bool valid_rows(la_tensor x, int64_t B, int64_t N, int64_t C, la_dtype dt, bool output) {
+  x.stride_h = 0;
+  return valid_view(x, B, 1, N, C, dt) && !(output && B > 1 && N > 0 && x.stride_b < (N > 1 ? x.stride_t : C));
+}
+bool valid_elem(const void* p, la_dtype dt) { return p && (reinterpret_cast<uintptr_t>(p) % elem_bytes(dt)) == 0; }
+bool valid_strides(const la_tensor& x) { return x.stride_b >= 0 && x.stride_h >= 0 && x.stride_t >= 0; }
+
+}  // namespace
+
+la_status la_conv_prefill(const la_conv_prefill_args* a, void* stream) {
+  if (!a) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_size(a->B) || !valid_size(a->N) || !valid_size(a->C)) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_dtype(a->in_dtype) || !valid_dtype(a->out_dtype) || !valid_dtype(a->w_dtype)) return LA_ERR_INVALID_ARGUMENT;
+  if (a->W < 2 || a->W > 4) return LA_ERR_UNSUPPORTED;
+  if (a->B == 0 || a->C == 0) return LA_OK;
+  if (!within(int64_t(1) << 40, {a->B, a->N + 1, a->C})) return LA_ERR_UNSUPPORTED;
+  if (!valid_rows(a->x, a->B, a->N, a->C, a->in_dtype, false) || !valid_rows(a->y, a->B, a->N, a->C, a->out_dtype, true))
+    return LA_ERR_INVALID_ARGUMENT;
+  if (a->N > 0 && a->x.ptr == a->y.ptr) return LA_ERR_INVALID_ARGUMENT;  // a run's history may be overwritten
+  if (!a->w || !a->state_out || !aligned16(a->w) || !aligned16(a->bias) || !aligned16(a->state_in) ||
+      !aligned16(a->state_out) || !aligned8(a->lens))
+    return LA_ERR_INVALID_ARGUMENT;
+  unsigned* status = device_status_ptr();
+  if (!status) return LA_ERR_CUDA;
+  la::ConvLaunch L{};
+  L.B = a->B; L.N = a->N; L.C = a->C; L.W = (int)a->W;
+  L.in_bf16 = a->in_dtype == LA_DTYPE_BF16; L.out_bf16 = a->out_dtype == LA_DTYPE_BF16;
+  L.w_bf16 = a->w_dtype == LA_DTYPE_BF16;
+  L.x = a->x.ptr; L.x_sb = a->x.stride_b; L.x_st = a->x.stride_t;
+  L.y = a->y.ptr; L.y_sb = a->y.stride_b; L.y_st = a->y.stride_t;
+  L.w = a->w; L.bias = a->bias; L.state_in = a->state_in; L.state_out = a->state_out;
+  L.lens = a->lens; L.silu = a->silu; L.status = status;
+  return from_cuda(la::launch_conv_prefill(L, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_conv_decode_step(const la_conv_decode_args* a, void* stream) {
+  if (!a) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_size(a->S) || !valid_size(a->C)) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_dtype(a->in_dtype) || !valid_dtype(a->out_dtype) || !valid_dtype(a->w_dtype)) return LA_ERR_INVALID_ARGUMENT;
+  if (a->W < 2 || a->W > 4) return LA_ERR_UNSUPPORTED;
+  if (a->S == 0 || a->C == 0) return LA_OK;
+  if (!within(int64_t(1) << 40, {a->S, a->C})) return LA_ERR_UNSUPPORTED;
+  const la_tensor x{const_cast<void*>(a->x), 0, 0, a->x_stride}, y{a->out, 0, 0, a->out_stride};
+  if (!valid_rows(x, 1, a->S, a->C, a->in_dtype, false) || !valid_rows(y, 1, a->S, a->C, a->out_dtype, true))
+    return LA_ERR_INVALID_ARGUMENT;
+  if (!a->w || !a->state_in || !a->state_out || !aligned16(a->w) || !aligned16(a->bias) || !aligned16(a->state_in) ||
+      !aligned16(a->state_out))
+    return LA_ERR_INVALID_ARGUMENT;
+  la::ConvLaunch L{};
+  L.B = a->S; L.N = 1; L.C = a->C; L.W = (int)a->W;
+  L.in_bf16 = a->in_dtype == LA_DTYPE_BF16; L.out_bf16 = a->out_dtype == LA_DTYPE_BF16;
+  L.w_bf16 = a->w_dtype == LA_DTYPE_BF16;
+  L.x = a->x; L.x_sb = a->x_stride;
+  L.y = a->out; L.y_sb = a->out_stride;
+  L.w = a->w; L.bias = a->bias; L.state_in = a->state_in; L.state_out = a->state_out;
+  L.silu = a->silu;
+  return from_cuda(la::launch_conv_decode(L, static_cast<cudaStream_t>(stream)));
+}
+
+static bool ssm_shape(const la_ssm_prefill_args* a) {
+  return a && a->B > 0 && a->C > 0 && a->G > 0 && a->B <= 65535 && a->C % a->G == 0 && valid_size(a->N) && a->n >= 1 && a->n <= 64 &&
+         a->C <= kMaxDim && within(kMaxElems, {a->B, a->C, a->n}) && within(kMaxElems, {a->B, a->N + 1, a->C});
+}
+
+size_t la_ssm_prefill_workspace_size(const la_ssm_prefill_args* a) {
+  return ssm_shape(a) ? la::ssm_workspace_bytes(a->B, a->N, a->C, (int)a->n, a->G) : 0;
+}
+
+la_status la_ssm_prefill(const la_ssm_prefill_args* a, void* ws, size_t ws_bytes, void* stream) {
+  if (!a) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_size(a->B) || !valid_size(a->N) || !valid_size(a->C) || a->G < 1 || a->C % a->G != 0) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_dtype(a->in_dtype) || !valid_dtype(a->out_dtype)) return LA_ERR_INVALID_ARGUMENT;
+  if (a->n < 1 || a->n > 64) return LA_ERR_UNSUPPORTED;
+  if (a->B == 0 || a->C == 0) return LA_OK;
+  if (!ssm_shape(a)) return LA_ERR_UNSUPPORTED;
+  const int64_t B = a->B, N = a->N, C = a->C;
+  if (!valid_rows(a->u, B, N, C, a->in_dtype, false) || !valid_rows(a->delta, B, N, C, a->in_dtype, false) ||
+      (a->z.ptr && !valid_rows(a->z, B, N, C, a->in_dtype, false)) || !valid_rows(a->y, B, N, C, a->out_dtype, true))
+    return LA_ERR_INVALID_ARGUMENT;
+  if (N > 0 && (!valid_elem(a->Bm.ptr, a->in_dtype) || !valid_elem(a->Cm.ptr, a->in_dtype) || !valid_strides(a->Bm) || !valid_strides(a->Cm)))
+    return LA_ERR_INVALID_ARGUMENT;
+  if (!a->A || !a->h_out || !aligned4(a->A) || !aligned4(a->D) || !aligned4(a->delta_bias) || !aligned16(a->h_in) ||
+      !aligned16(a->h_out) || !aligned8(a->lens))
+    return LA_ERR_INVALID_ARGUMENT;
+  const size_t need = la_ssm_prefill_workspace_size(a);
+  if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need)) return LA_ERR_WORKSPACE;
+  unsigned* status = device_status_ptr();
+  if (!status) return LA_ERR_CUDA;
+  la::SsmLaunch L{};
+  L.B = B; L.N = N; L.C = C; L.G = a->G; L.n = (int)a->n;
+  L.in_bf16 = a->in_dtype == LA_DTYPE_BF16; L.out_bf16 = a->out_dtype == LA_DTYPE_BF16;
+  L.u = a->u.ptr; L.u_sb = a->u.stride_b; L.u_st = a->u.stride_t;
+  L.delta = a->delta.ptr; L.d_sb = a->delta.stride_b; L.d_st = a->delta.stride_t;
+  L.z = a->z.ptr; L.z_sb = a->z.stride_b; L.z_st = a->z.stride_t;
+  L.y = a->y.ptr; L.y_sb = a->y.stride_b; L.y_st = a->y.stride_t;
+  L.Bm = view(a->Bm); L.Cm = view(a->Cm);
+  L.A = a->A; L.D = a->D; L.delta_bias = a->delta_bias; L.h_in = a->h_in; L.h_out = a->h_out;
+  L.lens = a->lens; L.softplus = a->delta_softplus; L.status = status;
+  return from_cuda(la::launch_ssm_prefill(L, ws, ws_bytes, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_ssm_decode_step(const la_ssm_decode_args* a, void* stream) {
+  if (!a) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_size(a->S) || !valid_size(a->C) || a->G < 1 || a->C % a->G != 0) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_dtype(a->in_dtype) || !valid_dtype(a->out_dtype)) return LA_ERR_INVALID_ARGUMENT;
+  if (a->n < 1 || a->n > 64) return LA_ERR_UNSUPPORTED;
+  if (a->S == 0 || a->C == 0) return LA_OK;
+  if (a->S > 4 * 65535 || !within(kMaxElems, {a->S, a->C, a->n})) return LA_ERR_UNSUPPORTED;
+  for (const la_tensor* t : {&a->u, &a->delta, &a->Bm, &a->Cm})
+    if (!valid_elem(t->ptr, a->in_dtype) || !valid_strides(*t)) return LA_ERR_INVALID_ARGUMENT;
+  if (a->z.ptr && (!valid_elem(a->z.ptr, a->in_dtype) || !valid_strides(a->z))) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_elem(a->out.ptr, a->out_dtype) || !valid_strides(a->out) || (a->S > 1 && a->out.stride_b < a->C))
+    return LA_ERR_INVALID_ARGUMENT;
+  if (!a->A || !a->state_in || !a->state_out || !aligned4(a->A) || !aligned4(a->D) || !aligned4(a->delta_bias) ||
+      !aligned16(a->state_in) || !aligned16(a->state_out))
+    return LA_ERR_INVALID_ARGUMENT;
+  la::SsmLaunch L{};
+  L.B = a->S; L.N = 1; L.C = a->C; L.G = a->G; L.n = (int)a->n;
+  L.in_bf16 = a->in_dtype == LA_DTYPE_BF16; L.out_bf16 = a->out_dtype == LA_DTYPE_BF16;
+  L.u = a->u.ptr; L.u_sb = a->u.stride_b;
+  L.delta = a->delta.ptr; L.d_sb = a->delta.stride_b;
+  L.z = a->z.ptr; L.z_sb = a->z.stride_b;
+  L.y = a->out.ptr; L.y_sb = a->out.stride_b;
+  L.Bm = view(a->Bm); L.Cm = view(a->Cm);
+  L.A = a->A; L.D = a->D; L.delta_bias = a->delta_bias; L.h_in = a->state_in; L.h_out = a->state_out;
+  L.softplus = a->delta_softplus;
+  return from_cuda(la::launch_ssm_decode(L, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_swa_prefill(const la_swa_prefill_args* a, void* stream) {
+  if (!a) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_size(a->B) || !valid_size(a->H) || !valid_size(a->Nq) || !valid_size(a->Nk) || !valid_size(a->window) || a->H_kv < 1 ||
+      a->H % a->H_kv != 0 || a->q_pos0 < 0 || a->q_pos0 > a->Nk || a->Nq > a->Nk - a->q_pos0)
+    return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_dtype(a->in_dtype) || !valid_dtype(a->out_dtype)) return LA_ERR_INVALID_ARGUMENT;
+  if (!(a->softcap >= 0.f) || a->softcap > 3.402823466e38f || (a->k_cache == nullptr) != (a->v_cache == nullptr))
+    return LA_ERR_INVALID_ARGUMENT;
+  if (a->d < 8 || a->d > 128 || a->d % 8 != 0) return LA_ERR_UNSUPPORTED;
+  if (a->k_cache && (a->window < 1 || a->window > 256)) return LA_ERR_UNSUPPORTED;
+  if (a->Nk > INT32_MAX - 512) return LA_ERR_UNSUPPORTED;  // key positions are 32-bit
+  if (a->B == 0 || a->H == 0 || a->Nk == 0) return LA_OK;
+  if (!within((int64_t(1) << 31) - 1, {a->B, a->H, (a->Nq + 63) / 64}) || !within((int64_t(1) << 31) - 1, {a->B, a->H_kv, 256}))
+    return LA_ERR_UNSUPPORTED;
+  if (!valid_view(a->q, a->B, a->H, a->Nq, a->d, a->in_dtype) || !valid_view(a->k, a->B, a->H_kv, a->Nk, a->d, a->in_dtype) ||
+      !valid_view(a->v, a->B, a->H_kv, a->Nk, a->d, a->in_dtype) || !valid_view(a->o, a->B, a->H, a->Nq, a->d, a->out_dtype))
+    return LA_ERR_INVALID_ARGUMENT;
+  if (a->Nq > 0 && ((a->B > 1 && a->o.stride_b == 0) || (a->H > 1 && a->o.stride_h == 0))) return LA_ERR_INVALID_ARGUMENT;
+  if (!aligned4(a->slopes) || !aligned4(a->key_lo) || !aligned4(a->key_hi) || !aligned8(a->lens) || !aligned16(a->k_cache) ||
+      !aligned16(a->v_cache))
+    return LA_ERR_INVALID_ARGUMENT;
+  unsigned* status = device_status_ptr();
+  if (!status) return LA_ERR_CUDA;
+  la::SwaPrefillLaunch L{};
+  L.B = a->B; L.H = a->H; L.Hkv = a->H_kv; L.Nq = a->Nq; L.Nk = a->Nk; L.d = (int)a->d;
+  L.window = a->window; L.q_pos0 = a->q_pos0;
+  L.in_bf16 = a->in_dtype == LA_DTYPE_BF16; L.out_bf16 = a->out_dtype == LA_DTYPE_BF16;
+  L.q = view(a->q); L.k = view(a->k); L.v = view(a->v);
+  L.o = a->o.ptr; L.o_sb = a->o.stride_b; L.o_sh = a->o.stride_h; L.o_st = a->o.stride_t;
+  L.scale = a->scale; L.softcap = a->softcap; L.slopes = a->slopes; L.key_lo = a->key_lo; L.key_hi = a->key_hi;
+  L.lens = a->lens; L.k_cache = a->k_cache; L.v_cache = a->v_cache; L.status = status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a->Nq > 0) {
+    const cudaError_t e = la::launch_swa_prefill_simt(L, s);
+    if (e != cudaSuccess) return from_cuda(e);
+  }
+  return a->k_cache ? from_cuda(la::launch_swa_fill_rings(L, s)) : LA_OK;
+}
+
+la_status la_swa_biased_decode_step(const la_swa_biased_decode_args* args, void* stream) {
+  if (!args) return LA_ERR_INVALID_ARGUMENT;
+  const la_swa_decode_args* a = &args->base;
+  if (a->S < 0 || a->H < 0 || a->S > kMaxDim || a->H > kMaxDim || args->H_kv < 1 || a->H % args->H_kv != 0) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_dtype(a->in_dtype) || !valid_dtype(a->out_dtype)) return LA_ERR_INVALID_ARGUMENT;
+  if (!(args->softcap >= 0.f) || args->softcap > 3.402823466e38f) return LA_ERR_INVALID_ARGUMENT;
+  if (a->d < 8 || a->d > 128 || a->d % 8 != 0 || a->window < 1 || a->window > 256 || a->H / args->H_kv > 16) return LA_ERR_UNSUPPORTED;
+  if (a->S == 0 || a->H == 0) return LA_OK;
+  if (!within((int64_t(1) << 31) - 1, {a->S, a->H})) return LA_ERR_UNSUPPORTED;
+  if (!a->q || !a->k || !a->v || !a->k_cache || !a->v_cache || !a->pos || !a->out) return LA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->k_cache) || !aligned16(a->v_cache) ||
+      !aligned16(a->out) || !aligned8(a->pos) || !aligned4(args->slopes))
+    return LA_ERR_INVALID_ARGUMENT;
+  unsigned* status = device_status_ptr();
+  if (!status) return LA_ERR_CUDA;
+  la::SwaBiasedDecodeLaunch L{};
+  L.base.S = a->S; L.base.H = a->H; L.base.d = (int)a->d; L.base.window = (int)a->window;
+  L.base.in_bf16 = a->in_dtype == LA_DTYPE_BF16;
+  L.base.out_bf16 = a->out_dtype == LA_DTYPE_BF16;
+  L.base.q = a->q; L.base.k = a->k; L.base.v = a->v; L.base.k_cache = a->k_cache; L.base.v_cache = a->v_cache;
+  L.base.pos = a->pos; L.base.out = a->out; L.base.scale = a->scale; L.base.status = status;
+  L.Hkv = args->H_kv; L.softcap = args->softcap; L.slopes = args->slopes;
+  return from_cuda(la::launch_swa_biased_decode(L, static_cast<cudaStream_t>(stream)));
 }
 
 la_status la_selftest_bounded_wait(int arrive, int64_t limit_ns, void* stream) {

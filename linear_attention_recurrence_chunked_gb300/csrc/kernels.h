@@ -143,4 +143,69 @@ cudaError_t launch_notebank_scores(const NotebankScoresLaunch& a, cudaStream_t s
 cudaError_t launch_notebank_address(const NotebankAddressLaunch& a, unsigned* status, cudaStream_t stream);
 cudaError_t launch_notebank_route(const NotebankRouteLaunch& a, cudaStream_t stream);
 
+// Short causal convolution (conv.cu).  The step is the prompt form's data with one token per sequence.
+struct ConvLaunch {
+  int64_t B, N, C;
+  int W;
+  bool in_bf16, out_bf16, w_bf16;
+  const void* x;
+  int64_t x_sb, x_st;
+  void* y;
+  int64_t y_sb, y_st;
+  const void *w, *bias, *state_in;
+  void* state_out;
+  const int64_t* lens;  // [B] or null
+  int silu;
+  unsigned* status;     // device status word (a length out of range sets kStatusBadIndex)
+};
+cudaError_t launch_conv_prefill(const ConvLaunch& a, cudaStream_t stream);
+cudaError_t launch_conv_decode(const ConvLaunch& a, cudaStream_t stream);  // N = 1, no lens
+
+// Selective state space scan (ssm.cu).  The step has N = 1 and no lens.
+struct SsmLaunch {
+  int64_t B, N, C, G;
+  int n;
+  bool in_bf16, out_bf16;
+  const void *u, *delta, *z;
+  int64_t u_sb, u_st, d_sb, d_st, z_sb, z_st;
+  void* y;
+  int64_t y_sb, y_st;
+  View4 Bm, Cm;         // [B, G, N, n]
+  const float *A, *D, *delta_bias, *h_in;
+  float* h_out;
+  const int64_t* lens;
+  int softplus;
+  unsigned* status;
+};
+size_t ssm_workspace_bytes(int64_t B, int64_t N, int64_t C, int n, int64_t G);
+cudaError_t launch_ssm_prefill(const SsmLaunch& a, void* ws, size_t ws_bytes, cudaStream_t stream);
+cudaError_t launch_ssm_decode(const SsmLaunch& a, cudaStream_t stream);
+
+// Masked window attention over a prompt (swa_prefill.cu: fp32 and the rings; swa_prefill_tc.cu: bf16).
+struct SwaPrefillLaunch {
+  int64_t B, H, Hkv, Nq, Nk;
+  int d;
+  int64_t window, q_pos0;
+  bool in_bf16, out_bf16;
+  View4 q, k, v;
+  void* o;
+  int64_t o_sb, o_sh, o_st;
+  float scale, softcap;
+  const float* slopes;
+  const int32_t *key_lo, *key_hi;
+  const int64_t* lens;
+  void *k_cache, *v_cache;
+  unsigned* status;
+};
+cudaError_t launch_swa_prefill_simt(const SwaPrefillLaunch& a, cudaStream_t stream);
+cudaError_t launch_swa_fill_rings(const SwaPrefillLaunch& a, cudaStream_t stream);
+
+struct SwaBiasedDecodeLaunch {
+  SwaDecodeLaunch base;
+  int64_t Hkv;
+  float softcap;
+  const float* slopes;
+};
+cudaError_t launch_swa_biased_decode(const SwaBiasedDecodeLaunch& a, cudaStream_t stream);
+
 }  // namespace la

@@ -1,0 +1,127 @@
+// layers.cuh -- device helpers shared by the convolution, the selective scan and the masked window
+// attention: 16-byte vectors of either element type, and the scalar functions of their epilogues.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace la {
+
+// elements of T in a 16-byte vector
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+__device__ __forceinline__ void unpack_vec(uint4 u, float (&o)[8]) {  // 8 bf16
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = __uint_as_float(w[i] << 16);
+    o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void unpack_vec(uint4 u, float (&o)[4]) {  // 4 fp32
+  o[0] = __uint_as_float(u.x); o[1] = __uint_as_float(u.y); o[2] = __uint_as_float(u.z); o[3] = __uint_as_float(u.w);
+}
+
+// Raw vector of the elements [0, valid) at p (zero beyond); `vec` says that a 16-byte access is allowed.
+template <typename T>
+__device__ __forceinline__ uint4 load_raw(const T* p, int valid, bool vec) {
+  if (vec && valid >= kVec<T>) return *reinterpret_cast<const uint4*>(p);
+  uint4 u = make_uint4(0u, 0u, 0u, 0u);
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+  for (int i = 0; i < kVec<T>; ++i) {
+    if (i < valid) {
+      if constexpr (sizeof(T) == 2) w[i / 2] |= (uint32_t)__bfloat16_as_ushort(p[i]) << (16 * (i & 1));
+      else w[i] = __float_as_uint(p[i]);
+    }
+  }
+  return u;
+}
+template <typename T>
+__device__ __forceinline__ void store_raw(T* p, uint4 u, int valid, bool vec) {
+  if (vec && valid >= kVec<T>) {
+    *reinterpret_cast<uint4*>(p) = u;
+    return;
+  }
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < kVec<T>; ++i) {
+    if (i < valid) {
+      if constexpr (sizeof(T) == 2) p[i] = __ushort_as_bfloat16((unsigned short)(w[i / 2] >> (16 * (i & 1))));
+      else p[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+
+// N consecutive floats as TOut (round to nearest even); `vec`: the address is aligned to the vector
+// (16 bytes, or 8 for four bf16).
+template <int N>
+__device__ __forceinline__ void store_floats(float* p, const float (&x)[N], int valid, bool vec) {
+  if (vec && valid >= N) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < valid) p[i] = x[i];
+}
+template <int N>
+__device__ __forceinline__ void store_floats(__nv_bfloat16* p, const float (&x)[N], int valid, bool vec) {
+  if (vec && valid >= N) {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    if constexpr (N == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < valid) p[i] = __float2bfloat16_rn(x[i]);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// x / (1 + exp(-x)).  exp(-x) overflows to infinity below x = -88, where the quotient is the limit 0.
+__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+
+// log(1 + exp(x)) = max(x, 0) + log1p(e), e = exp(-|x|).  The logarithm of 1 + e would lose the small
+// values that a step size takes (e = 1e-3 keeps 13 bits of it), so log1p(e) = 2 atanh(r), r = e / (2 + e)
+// in (0, 1/3], by its series r + r^3/3 + r^5/5 + ...: the first term left out, r^17 / 17, is below
+// 2^-29 of r.
+__device__ __forceinline__ float softplus(float x) {
+  const float e = __expf(-fabsf(x));
+  const float r = __fdividef(e, 2.f + e), q = r * r;
+  float p = 1.f / 15.f;
+  p = fmaf(p, q, 1.f / 13.f);
+  p = fmaf(p, q, 1.f / 11.f);
+  p = fmaf(p, q, 1.f / 9.f);
+  p = fmaf(p, q, 1.f / 7.f);
+  p = fmaf(p, q, 1.f / 5.f);
+  p = fmaf(p, q, 1.f / 3.f);
+  p = fmaf(p, q, 1.f);
+  const float s = fmaxf(x, 0.f) + 2.f * r * p;
+  return x != x ? x : s;
+}
+
+// Tokens of sequence b, or -1 (and the status bit) where its length lies outside [0, N].
+__device__ __forceinline__ int64_t sequence_length(const int64_t* lens, int64_t b, int64_t N, unsigned* status, bool report) {
+  if (!lens) return N;
+  const int64_t n = lens[b];
+  if (n >= 0 && n <= N) return n;
+  if (report) atomicOr(status, kStatusBadIndex);
+  return -1;
+}
+
+}  // namespace la

@@ -1,0 +1,467 @@
+"""GPU parity of the short causal convolution, the selective state space scan and masked window attention over
+prompts, and of their one-token steps, against fp64 definitions with per-entry error bounds."""
+import numpy as np
+import pytest
+import torch
+
+import linear_attention_recurrence_chunked_gb300 as la
+from tests import layers_oracle as ref
+from tests.helpers import cuda_device
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float32
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def randn(g, *shape, dtype=FP, scale=1.0):
+    return (torch.randn(shape, generator=g) * scale).to(dtype)
+
+
+def pad_rows(t, dev, fill=float("nan")):
+    """The tensor on the device as rows of a wider buffer: row starts on 16 bytes, what lies between unreadable as numbers."""
+    C = t.shape[-1]
+    wide = torch.full((*t.shape[:-1], -(-C // 8) * 8 + 8), fill, dtype=t.dtype, device=dev)
+    wide[..., :C] = t.to(dev)
+    return wide[..., :C]
+
+
+def on(dev, *ts):
+    return [None if t is None else t.to(dev) for t in ts]
+
+
+# ------------------------------------------------------------------------------------------ convolution
+@pytest.mark.parametrize("B,N,C,W,dtype,w_dtype,out,silu,bias,state,lens", [
+    (1, 1, 8, 4, BF, BF, BF, True, True, True, None),
+    (2, 2, 1, 4, BF, FP, FP, True, False, True, None),
+    (3, 77, 1001, 4, BF, BF, BF, True, True, False, [77, 0, 2]),
+    (2, 33, 12, 3, FP, BF, FP, False, True, True, [1, 33]),
+    (2, 40, 20, 2, FP, FP, BF, True, False, True, None),
+    (1, 300, 264, 3, BF, BF, FP, False, False, True, [299]),
+    (4, 9, 64, 4, FP, FP, FP, True, True, True, [0, 1, 3, 9]),
+])
+def test_conv_prefill(B, N, C, W, dtype, w_dtype, out, silu, bias, state, lens):
+    dev = cuda_device()
+    g = gen(N * 7 + C)
+    x, w = randn(g, B, N, C, dtype=dtype), randn(g, C, W, dtype=w_dtype, scale=0.5)
+    bs = randn(g, C, dtype=w_dtype) if bias else None
+    st = randn(g, B, W - 1, C, dtype=dtype) if state else None
+    y_ref, bound, last = ref.conv(x, w, bs, st, lens, silu, out)
+    xd = pad_rows(x, dev)
+    ln = None
+    if lens is not None:
+        ln = torch.tensor(lens, dtype=torch.int64, device=dev)
+        for b, n in enumerate(lens):
+            xd[b, n:] = float("nan")  # padding reaches nothing
+    y = pad_rows(torch.full((B, N, C), 5.0, dtype=out), dev)
+    wd, bd, sd = on(dev, w, bs, st)
+    got, s_out = la.la_conv_prefill(xd, wd, bias=bd, state_in=sd, lens=ln, silu=silu, y=y)
+    ref.check(got, y_ref, bound)
+    assert torch.equal(s_out.double().cpu(), torch.from_numpy(last))
+    for b, n in enumerate(lens or []):
+        assert torch.all(got[b, n:] == 5.0)  # rows of padding stay
+    if sd is not None:  # in place
+        la.la_conv_prefill(xd, wd, bias=bd, state_in=sd, state_out=sd, lens=ln, silu=silu)
+        assert torch.equal(sd, s_out)
+    assert la.la_device_status() == la.LA_OK
+
+
+@pytest.mark.parametrize("dtype,W,C", [(BF, 4, 72), (FP, 3, 13), (BF, 2, 9)])
+def test_conv_steps_continue_a_prompt(dtype, W, C):
+    dev = cuda_device()
+    S, N, steps = 3, 21, 6
+    g = gen(C)
+    x, w, bias = randn(g, S, N + steps, C, dtype=dtype), randn(g, C, W, dtype=dtype, scale=0.5), randn(g, C, dtype=dtype)
+    y_ref, bound, last = ref.conv(x, w, bias, None, None, True, dtype)
+    xd, wd, bd = pad_rows(x, dev), w.to(dev), bias.to(dev)
+    _, state = la.la_conv_prefill(xd[:, :N], wd, bias=bd)
+    for t in range(steps):
+        out = la.la_conv_decode_step(xd[:, N + t], wd, state, bias=bd)
+        ref.check(out, y_ref[:, N + t], bound[:, N + t])
+    assert torch.equal(state.double().cpu(), torch.from_numpy(last))
+
+
+# ------------------------------------------------------------------------------------------ selective scan
+def ssm_inputs(B, N, C, n, G, dtype, z, seed):
+    g = gen(seed)
+    A = -(0.05 + torch.rand((C, n), generator=g) * 4)
+    t = {"u": randn(g, B, N, C, dtype=dtype), "delta": randn(g, B, N, C, dtype=dtype), "A": A,
+         "Bm": randn(g, B, G, N, n, dtype=dtype), "Cm": randn(g, B, G, N, n, dtype=dtype), "D": randn(g, C),
+         "z": randn(g, B, N, C, dtype=dtype) if z else None, "bias": randn(g, C) - 3, "h": randn(g, B, C, n)}
+    return t
+
+
+@pytest.mark.parametrize("B,N,C,n,G,dtype,out,z,softplus,state,lens", [
+    (1, 1, 8, 16, 1, BF, BF, True, True, True, None),
+    (2, 37, 40, 16, 2, BF, BF, True, True, True, [37, 0]),
+    (2, 70, 33, 4, 1, FP, FP, False, True, True, None),
+    (1, 65, 130, 8, 1, BF, FP, True, True, False, [33]),
+    (3, 129, 24, 24, 3, FP, FP, True, True, True, [129, 128, 1]),
+    (1, 100, 10, 64, 2, BF, BF, False, True, True, None),
+    (1, 50, 16, 33, 1, FP, BF, True, True, True, None),
+    (2, 31, 7, 1, 1, FP, FP, True, True, False, None),
+    (1, 40, 21, 7, 3, BF, BF, True, False, True, None),
+    (1, 2000, 48, 16, 1, BF, BF, True, True, True, None),      # time segments
+    (2, 1500, 24, 8, 1, FP, FP, True, True, True, [700, 1499]),
+])
+def test_ssm_prefill(B, N, C, n, G, dtype, out, z, softplus, state, lens):
+    dev = cuda_device()
+    t = ssm_inputs(B, N, C, n, G, dtype, z, N + C)
+    if not softplus:
+        t["delta"] = t["delta"].abs() * 0.2
+        t["bias"] = t["bias"].abs() * 0.1
+    h0 = t["h"] if state else None
+    y_ref, bound, h_ref, h_bound = ref.ssm(t["u"], t["delta"], t["A"], t["Bm"], t["Cm"], t["D"], t["z"], t["bias"],
+                                           softplus, h0, lens, out, segment=N)
+    ud, dd = pad_rows(t["u"], dev), pad_rows(t["delta"], dev)
+    zd = pad_rows(t["z"], dev) if z else None
+    # B and C as slices of one projection, at an odd offset
+    proj = torch.full((B, N, 2 * G * n + 1), float("nan"), dtype=dtype, device=dev)
+    proj[..., 1:] = torch.cat([t["Bm"].transpose(1, 2).reshape(B, N, G * n), t["Cm"].transpose(1, 2).reshape(B, N, G * n)], -1).to(dev)
+    Bd = proj[..., 1:1 + G * n].unflatten(-1, (G, n)).transpose(1, 2)
+    Cd = proj[..., 1 + G * n:].unflatten(-1, (G, n)).transpose(1, 2)
+    ln = None
+    if lens is not None:
+        ln = torch.tensor(lens, dtype=torch.int64, device=dev)
+        for b, m in enumerate(lens):
+            for x in (ud, dd, zd, proj):
+                if x is not None:
+                    x[b, m:] = float("nan")
+    y = pad_rows(torch.full((B, N, C), 5.0, dtype=out), dev)
+    Ad, Dd, bd, hd = on(dev, t["A"], t["D"], t["bias"], h0)
+    kw = dict(D=Dd, z=zd, delta_bias=bd, delta_softplus=softplus, lens=ln)
+    got, h = la.la_ssm_prefill(ud, dd, Ad, Bd, Cd, h_in=hd, y=y, **kw)
+    ref.check(h, h_ref, h_bound)
+    ref.check(got, y_ref, bound)
+    for b, m in enumerate(lens or []):
+        assert torch.all(got[b, m:] == 5.0)
+    if hd is not None:  # in place, the same bits
+        _, h2 = la.la_ssm_prefill(ud, dd, Ad, Bd, Cd, h_in=hd, h_out=hd, **kw)
+        assert torch.equal(h2, h)
+    assert la.la_device_status() == la.LA_OK
+
+
+def test_ssm_long_memory():
+    """States that forget over thousands of tokens: the decays' errors must not add up to a bias."""
+    dev = cuda_device()
+    B, N, C, n = 1, 6000, 32, 16
+    t = ssm_inputs(B, N, C, n, 1, BF, False, 5)
+    t["A"] = t["A"] * 0 - torch.linspace(0.2, 1.5, n)
+    t["bias"] = torch.full((C,), -7.5)  # steps near 5e-4
+    y_ref, bound, h_ref, _ = ref.ssm(t["u"], t["delta"], t["A"], t["Bm"], t["Cm"], t["D"], None, t["bias"], True, None, None, FP,
+                                     segment=256)
+    u, delta, A, Bm, Cm, D, bias = on(dev, *(t[k] for k in ("u", "delta", "A", "Bm", "Cm", "D", "bias")))
+    y, h = la.la_ssm_prefill(u, delta, A, Bm, Cm, D=D, delta_bias=bias, out_dtype=FP)
+    err = np.linalg.norm(h.double().cpu().numpy() - h_ref) / np.linalg.norm(h_ref)
+    # about 3000 tokens of memory; each rounding of 2^-24 enters at random: sqrt(3000) 2^-24 = 3.3e-6, three of them a step
+    assert err < 1e-5
+    ref.check(y, y_ref, bound)
+
+
+@pytest.mark.parametrize("dtype,n,G,C", [(BF, 16, 1, 40), (FP, 24, 2, 18), (BF, 7, 1, 9), (BF, 64, 1, 12), (FP, 4, 1, 70), (BF, 8, 3, 33)])
+def test_ssm_steps_continue_a_prompt(dtype, n, G, C):
+    dev = cuda_device()
+    S, N, steps = 5, 19, 5
+    t = ssm_inputs(S, N + steps, C, n, G, dtype, True, C + n)
+    y_ref, bound, h_ref, h_bound = ref.ssm(t["u"], t["delta"], t["A"], t["Bm"], t["Cm"], t["D"], t["z"], t["bias"], True, None, None, dtype)
+    u, delta, z = (pad_rows(t[k], dev) for k in ("u", "delta", "z"))
+    A, Bm, Cm, D, bias = on(dev, *(t[k] for k in ("A", "Bm", "Cm", "D", "bias")))
+    kw = dict(D=D, delta_bias=bias)
+    _, h = la.la_ssm_prefill(u[:, :N], delta[:, :N], A, Bm[:, :, :N], Cm[:, :, :N], z=z[:, :N], **kw)
+    for i in range(N, N + steps):
+        before = h.clone()
+        other = torch.empty_like(h)
+        out2 = la.la_ssm_decode_step(u[:, i], delta[:, i], A, Bm[:, :, i], Cm[:, :, i], h, z=z[:, i], state_out=other, **kw)
+        assert torch.equal(h, before)
+        out = la.la_ssm_decode_step(u[:, i], delta[:, i], A, Bm[:, :, i], Cm[:, :, i], h, z=z[:, i], **kw)
+        assert torch.equal(h, other) and torch.equal(out, out2)
+        ref.check(out, y_ref[:, i], bound[:, i])
+    ref.check(h, h_ref, h_bound)
+
+
+# ------------------------------------------------------------------------------------------ attention
+def swa_case(B, H, Hkv, Nq, Nk, d, dtype, seed):
+    g = gen(seed)
+    return (randn(g, B, Nq, H, d, dtype=dtype, scale=1.5).transpose(1, 2), randn(g, B, Nk, Hkv, d, dtype=dtype, scale=1.5).transpose(1, 2),
+            randn(g, B, Nk, Hkv, d, dtype=dtype).transpose(1, 2))
+
+
+def slopes_of(H):
+    return torch.exp2(-8.0 * torch.arange(1, H + 1, dtype=torch.float32) / H)
+
+
+def run_swa(q, k, v, out, window=0, softcap=0.0, slopes=None, key_lo=None, key_hi=None, q_pos0=None, lens=None, cache=False):
+    dev = cuda_device()
+    B, H, Nq, d = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    pos0 = Nk - Nq if q_pos0 is None else q_pos0
+    rows = ref.spans(Nq, Nk, B, window, key_lo, key_hi, pos0, lens)
+    o_ref, bound = ref.swa(q, k, v, d ** -0.5, softcap, slopes, rows, pos0, out)
+    qd, kd, vd, sl, lo, hi = on(dev, q, k, v, slopes, key_lo, key_hi)
+    ln = None
+    if lens is not None:
+        ln = torch.tensor(lens, dtype=torch.int64, device=dev)
+        for b, n in enumerate(lens):
+            kd[b, :, n:] = float("nan")
+            vd[b, :, n:] = float("nan")
+            qd[b, :, max(0, n - pos0):] = float("nan")
+    o = torch.full((B, Nq, H, d), 5.0, dtype=out, device=dev).transpose(1, 2)
+    kc = torch.full((B, Hkv, window, d), 3.0, dtype=q.dtype, device=dev) if cache else None
+    vc = torch.full((B, Hkv, window, d), 3.0, dtype=q.dtype, device=dev) if cache else None
+    la.la_swa_prefill(qd, kd, vd, window=window, softcap=softcap, slopes=sl, key_lo=lo, key_hi=hi, q_pos0=q_pos0, lens=ln, o=o,
+                      k_cache=kc, v_cache=vc)
+    assert la.la_device_status() == la.LA_OK
+    ref.check(o, o_ref, bound)
+    for b in range(B):
+        for i in range(Nq):
+            if rows[b][i] is None:
+                assert torch.all(o[b, :, i] == 5.0)
+            elif rows[b][i][0] == rows[b][i][1]:
+                assert torch.all(o[b, :, i] == 0.0)
+    if cache:
+        for b in range(B):
+            n = Nk if lens is None else lens[b]
+            want_k, want_v = torch.full((Hkv, window, d), 3.0, dtype=q.dtype), torch.full((Hkv, window, d), 3.0, dtype=q.dtype)
+            for p in range(max(0, n - window), n):
+                want_k[:, p % window], want_v[:, p % window] = k[b, :, p], v[b, :, p]
+            assert torch.equal(kc[b].cpu(), want_k) and torch.equal(vc[b].cpu(), want_v)
+    return o
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (FP, FP), (BF, FP), (FP, BF)])
+@pytest.mark.parametrize("B,H,Hkv,Nq,Nk,d,window,softcap,slopes,lens,cache", [
+    (1, 2, 2, 1, 1, 64, 0, 0.0, False, None, False),
+    (2, 4, 2, 77, 77, 64, 64, 0.0, False, None, True),
+    (1, 3, 1, 300, 300, 128, 0, 0.0, False, None, False),
+    (2, 4, 4, 130, 130, 40, 17, 0.0, True, [130, 64], True),
+    (2, 6, 3, 133, 333, 96, 200, 20.0, True, None, True),
+    (1, 8, 1, 129, 257, 8, 0, 30.0, False, None, False),
+    (3, 2, 1, 256, 256, 72, 1, 0.0, False, [0, 1, 255], True),
+    (1, 2, 2, 400, 400, 128, 130, 50.0, True, [399], True),
+])
+def test_swa_prefill(B, H, Hkv, Nq, Nk, d, window, softcap, slopes, lens, cache, dtype, out):
+    q, k, v = swa_case(B, H, Hkv, Nq, Nk, d, dtype, Nq + d)
+    run_swa(q, k, v, out, window, softcap, slopes_of(H) if slopes else None, lens=lens, cache=cache)
+
+
+def intervals(B, N, docs, prefix, empty):
+    """Packed documents of the given lengths, a bidirectional prefix in each, every `empty`-th row sees nothing."""
+    lo, hi = torch.zeros((B, N), dtype=torch.int32), torch.zeros((B, N), dtype=torch.int32)
+    for b in range(B):
+        at, which = 0, b
+        while at < N:
+            end = min(N, at + docs[which % len(docs)])
+            for i in range(at, end):
+                lo[b, i], hi[b, i] = at, max(i + 1, min(end, at + prefix))
+                if empty and i % empty == empty - 1:
+                    hi[b, i] = lo[b, i]
+            at, which = end, which + 1
+    return lo, hi
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("N,docs,prefix,empty,window,d", [
+    (300, [1, 70, 128, 5], 0, 0, 0, 64), (300, [90, 40], 33, 7, 0, 128), (515, [200, 3, 129], 20, 5, 50, 96),
+    (140, [140], 140, 0, 0, 64), (260, [64], 64, 2, 0, 32)])
+def test_swa_documents_and_prefixes(N, docs, prefix, empty, window, d, dtype):
+    q, k, v = swa_case(2, 4, 2, N, N, d, dtype, N)
+    lo, hi = intervals(2, N, docs, prefix, empty)
+    run_swa(q, k, v, dtype, window=window, slopes=slopes_of(4), key_lo=lo, key_hi=hi)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_swa_out_of_range_intervals_are_clamped_and_no_row_sees_anything(dtype):
+    q, k, v = swa_case(1, 2, 2, 150, 150, 64, dtype, 3)
+    lo = torch.full((1, 150), -(1 << 31), dtype=torch.int32)
+    hi = torch.full((1, 150), (1 << 31) - 1, dtype=torch.int32)
+    run_swa(q, k, v, dtype, key_lo=lo, key_hi=hi)           # everything sees everything
+    run_swa(q, k, v, dtype, window=9, key_lo=lo, key_hi=hi)  # and from 8 back to the end
+    run_swa(q, k, v, dtype, key_lo=hi, key_hi=lo)            # nothing
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_swa_masked_keys_and_values_reach_nothing(bad, dtype):
+    """One token's key and value are not finite: queries that do not see it keep their bits."""
+    dev = cuda_device()
+    N, at, window = 300, 141, 60
+    q, k, v = (t.to(dev) for t in swa_case(1, 4, 2, N, N, 64, dtype, 9))
+    clean = la.la_swa_prefill(q, k, v, window=window)
+    k, v = k.clone(), v.clone()
+    k[0, :, at] = bad
+    v[0, :, at, 5] = bad
+    o = la.la_swa_prefill(q, k, v, window=window)
+    sees = torch.zeros(N, dtype=torch.bool, device=dev)
+    sees[at:at + window] = True
+    assert torch.isfinite(o[:, :, ~sees]).all()
+    assert (o[:, :, ~sees].float() - clean[:, :, ~sees].float()).abs().max() < 2e-2  # another order of sums at most
+    v2 = v.clone()
+    k2, _ = swa_case(1, 4, 2, N, N, 64, dtype, 9)[1].to(dev), None
+    o2 = la.la_swa_prefill(q, k2, v2, window=window)
+    assert torch.isnan(o2[0, :, at:at + window, 5]).all() or torch.isinf(o2[0, :, at:at + window, 5]).all()
+    assert torch.isfinite(o2[0, :, :, 6]).all()
+
+
+@pytest.mark.parametrize("dtype,H,Hkv,d,window,softcap,slopes", [
+    (BF, 4, 4, 64, 64, 0.0, False), (BF, 8, 2, 128, 256, 30.0, True), (FP, 6, 3, 40, 33, 20.0, True), (BF, 16, 1, 72, 100, 0.0, True),
+    (FP, 3, 1, 128, 256, 0.0, False), (BF, 2, 2, 8, 1, 0.0, True), (BF, 12, 4, 96, 200, 50.0, False)])
+def test_swa_steps_continue_a_prompt(dtype, H, Hkv, d, window, softcap, slopes):
+    dev = cuda_device()
+    S, N, steps = 3, 90, 6
+    q, k, v = swa_case(S, H, Hkv, N + steps, N + steps, d, dtype, d + H)
+    sl = slopes_of(H) if slopes else None
+    lens = [N, 0, 17]
+    rows = ref.spans(N + steps, N + steps, S, window, None, None, 0, None)
+    o_ref, bound = ref.swa(q, k, v, d ** -0.5, softcap, sl, rows, 0, dtype)
+    qd, kd, vd, sld = on(dev, q, k, v, sl)
+    kc, vc = (torch.zeros((S, Hkv, window, d), dtype=dtype, device=dev) for _ in range(2))
+    ln = torch.tensor(lens, dtype=torch.int64, device=dev)
+    la.la_swa_prefill(qd[:, :, :N], kd[:, :, :N], vd[:, :, :N], window=window, softcap=softcap, slopes=sld, lens=ln, k_cache=kc, v_cache=vc)
+    for t in range(steps):
+        at = [n + t for n in lens]
+        qt, kt, vt = (torch.stack([x[s, :, at[s]] for s in range(S)]) for x in (qd, kd, vd))
+        out = la.la_swa_biased_decode_step(qt, kt, vt, kc, vc, ln + t, softcap=softcap, slopes=sld)
+        want = np.stack([o_ref[s, :, at[s]] for s in range(S)])
+        ref.check(out, want, np.stack([bound[s, :, at[s]] for s in range(S)]))
+        for s in range(S):
+            assert torch.equal(kc[s, :, at[s] % window], kt[s]) and torch.equal(vc[s, :, at[s] % window], vt[s])
+
+
+def test_swa_biased_step_without_extras_meets_the_plain_step():
+    dev = cuda_device()
+    S, H, d, w = 7, 4, 64, 64
+    g = gen(1)
+    q, k, v = (randn(g, S, H, d, dtype=BF).to(dev) for _ in range(3))
+    kc, vc = (randn(g, S, H, w, d, dtype=BF).to(dev) for _ in range(2))
+    pos = torch.tensor([0, 1, 63, 64, 65, 1000, 1 << 40], dtype=torch.int64, device=dev)
+    k1, v1, k2, v2 = kc.clone(), vc.clone(), kc.clone(), vc.clone()
+    a = la.la_swa_decode_step(q, k, v, k1, v1, pos, out_dtype=FP)
+    b = la.la_swa_biased_decode_step(q, k, v, k2, v2, pos, out_dtype=FP)
+    assert torch.equal(k1, k2) and torch.equal(v1, v2)
+    # both sum up to 64 fp32 terms in their own order
+    assert (a - b).abs().max() < 64 * 2 ** -23 * 8
+
+
+# ------------------------------------------------------------------------------------------ errors, streams, graphs
+def test_lengths_and_positions_out_of_range_are_reported_and_skipped():
+    dev = cuda_device()
+    x, w = torch.randn((3, 10, 16), device=dev), torch.randn((16, 4), device=dev)
+    lens = torch.tensor([11, 4, -1], dtype=torch.int64, device=dev)
+    y = torch.full_like(x, 7.0)
+    _, st = la.la_conv_prefill(x, w, lens=lens, y=y)
+    assert la.la_device_status() == la.LA_ERR_INVALID_ARGUMENT and la.la_device_status() == la.LA_OK
+    assert torch.all(y[0] == 7.0) and torch.all(y[2] == 7.0) and torch.all(y[1, 4:] == 7.0) and not torch.any(y[1, :4] == 7.0)
+    assert torch.all(st[0] == 0) and torch.all(st[2] == 0)
+    A, bc = -torch.rand((16, 16), device=dev), torch.randn((3, 1, 10, 16), device=dev)
+    y = torch.full_like(x, 7.0)
+    _, h = la.la_ssm_prefill(x, x, A, bc, bc, lens=lens, y=y)
+    assert la.la_device_status() == la.LA_ERR_INVALID_ARGUMENT
+    assert torch.all(y[0] == 7.0) and torch.all(y[2] == 7.0) and torch.all(h[0] == 0) and torch.isfinite(h).all()
+    q = torch.randn((3, 2, 10, 64), device=dev, dtype=BF)
+    o = torch.full_like(q, 7.0)
+    kc, vc = torch.zeros((3, 2, 8, 64), device=dev, dtype=BF), torch.zeros((3, 2, 8, 64), device=dev, dtype=BF)
+    la.la_swa_prefill(q, q, q, window=8, lens=lens, o=o, k_cache=kc, v_cache=vc)
+    assert la.la_device_status() == la.LA_ERR_INVALID_ARGUMENT
+    assert torch.all(o[0] == 7.0) and torch.all(o[2] == 7.0) and torch.all(kc[0] == 0) and torch.any(kc[1] != 0)
+    out = torch.full((2, 2, 64), 7.0, device=dev, dtype=BF)
+    qs = torch.randn((2, 2, 64), device=dev, dtype=BF)
+    rings = [torch.zeros((2, 2, 8, 64), device=dev, dtype=BF) for _ in range(2)]
+    la.la_swa_biased_decode_step(qs, qs, qs, *rings, torch.tensor([-1, 0], device=dev), out=out)
+    assert la.la_device_status() == la.LA_ERR_INVALID_ARGUMENT
+    assert torch.all(out[0] == 7.0) and torch.all(rings[0][0] == 0) and not torch.any(out[1] == 7.0)
+
+
+def hybrid(dev, B, N, seed):
+    """Inputs of one convolution, one scan and one attention layer of a small hybrid model."""
+    g = gen(seed)
+    C, n, H, Hkv, d = 64, 16, 4, 2, 32
+    t = {"x": randn(g, B, N, C, dtype=BF), "w": randn(g, C, 4, dtype=BF, scale=0.5), "bias": randn(g, C, dtype=BF), "delta": randn(g, B, N, C, dtype=BF),
+         "z": randn(g, B, N, C, dtype=BF), "A": -(0.2 + torch.rand((C, n), generator=g)), "D": randn(g, C), "dt_bias": randn(g, C) - 3,
+         "Bm": randn(g, B, 1, N, n, dtype=BF), "Cm": randn(g, B, 1, N, n, dtype=BF), "k": randn(g, B, Hkv, N, d, dtype=BF), "v": randn(g, B, Hkv, N, d, dtype=BF)}
+    return {name: x.to(dev) for name, x in t.items()}
+
+
+def prompt_pass(t, N, window, lens=None, workspace=None):
+    B = t["x"].shape[0]
+    y, conv = la.la_conv_prefill(t["x"][:, :N], t["w"], bias=t["bias"], lens=lens)
+    y, h = la.la_ssm_prefill(y, t["delta"][:, :N], t["A"], t["Bm"][:, :, :N], t["Cm"][:, :, :N], D=t["D"], z=t["z"][:, :N],
+                             delta_bias=t["dt_bias"], lens=lens, workspace=workspace)
+    kc, vc = (torch.zeros((B, 2, window, 32), dtype=BF, device=y.device) for _ in range(2))
+    q = torch.cat([y, y], -1).unflatten(-1, (4, 32)).transpose(1, 2)
+    o = la.la_swa_prefill(q, t["k"][:, :, :N], t["v"][:, :, :N], window=window, softcap=20.0, slopes=t["D"][:4].abs().contiguous(), lens=lens,
+                          k_cache=kc, v_cache=vc)
+    return o, conv, h, kc, vc
+
+
+def token_pass(t, i, conv, h, kc, vc, pos):
+    y = la.la_conv_decode_step(t["x"][:, i], t["w"], conv, bias=t["bias"])
+    y = la.la_ssm_decode_step(y, t["delta"][:, i], t["A"], t["Bm"][:, :, i], t["Cm"][:, :, i], h, D=t["D"], z=t["z"][:, i], delta_bias=t["dt_bias"])
+    q = torch.cat([y, y], -1).unflatten(-1, (4, 32))
+    return la.la_swa_biased_decode_step(q, t["k"][:, :, i].contiguous(), t["v"][:, :, i].contiguous(), kc, vc, pos, softcap=20.0,
+                                        slopes=t["D"][:4].abs().contiguous())
+
+
+def test_layers_together_prompt_then_tokens():
+    """A prompt through convolution, scan and attention, then tokens one by one: the same as the longer prompt at once."""
+    dev = cuda_device()
+    B, N, steps, window = 2, 150, 5, 40
+    t = hybrid(dev, B, N + steps, 4)
+    whole, conv_w, h_w, kc_w, vc_w = prompt_pass(t, N + steps, window)
+    o, conv, h, kc, vc = prompt_pass(t, N, window)
+    assert torch.equal(o, whole[:, :, :N])  # causal: later tokens change nothing, bit for bit
+    for i in range(N, N + steps):
+        out = token_pass(t, i, conv, h, kc, vc, torch.full((B,), i, dtype=torch.int64, device=dev))
+        # both sides round the scan's output and the result to bf16; the weights' rounding is one more
+        assert (out.float() - whole[:, :, i].float()).abs().max() < 4 * 2 ** -8 * whole.float().abs().max()
+    assert torch.equal(conv, conv_w) and torch.equal(kc, kc_w) and torch.equal(vc, vc_w)
+    assert (h - h_w).abs().max() <= 1e-5 * h_w.abs().max()
+    assert la.la_device_status() == la.LA_OK
+
+
+def test_layers_captured_replayed_and_on_another_stream():
+    dev = cuda_device()
+    B, N, window = 1, 1200, 40
+    t = hybrid(dev, B, N, 6)
+    eager = prompt_pass(t, N, window)
+    side = torch.cuda.Stream(dev)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = prompt_pass(t, N, window)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = prompt_pass(t, N, window)
+    x0 = t["x"].clone()
+    t["x"].zero_()
+    graph.replay()
+    t["x"].copy_(x0)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b, c in zip(eager, other, captured):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_steps_captured_and_replayed():
+    dev = cuda_device()
+    B, N, window = 2, 30, 16
+    t = hybrid(dev, B, N + 1, 8)
+    _, conv, h, kc, vc = prompt_pass(t, N, window)
+    saved = [x.clone() for x in (conv, h, kc, vc)]
+    pos = torch.full((B,), N, dtype=torch.int64, device=dev)
+    want = token_pass(t, N, conv, h, kc, vc, pos)
+    after = [x.clone() for x in (conv, h, kc, vc)]
+    for x, s in zip((conv, h, kc, vc), saved):
+        x.copy_(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = token_pass(t, N, conv, h, kc, vc, pos)
+    for x, s in zip((conv, h, kc, vc), saved):
+        x.copy_(s)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    for x, s in zip((conv, h, kc, vc), after):
+        assert torch.equal(x, s)
