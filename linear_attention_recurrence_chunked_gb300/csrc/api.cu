@@ -580,7 +580,8 @@ la_status la_swa_prefill(const la_swa_prefill_args* a, void* stream) {
   L.lens = a->lens; L.k_cache = a->k_cache; L.v_cache = a->v_cache; L.status = status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a->Nq > 0) {
-    const cudaError_t e = la::launch_swa_prefill_simt(L, s);
+    cudaError_t e = L.in_bf16 ? la::launch_swa_prefill_tc(L, s) : cudaErrorNotSupported;
+    if (e == cudaErrorNotSupported) e = la::launch_swa_prefill_simt(L, s);
     if (e != cudaSuccess) return from_cuda(e);
   }
   return a->k_cache ? from_cuda(la::launch_swa_fill_rings(L, s)) : LA_OK;

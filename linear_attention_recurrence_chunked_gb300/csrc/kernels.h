@@ -197,6 +197,8 @@ struct SwaPrefillLaunch {
   void *k_cache, *v_cache;
   unsigned* status;
 };
+// bf16 inputs; cudaErrorNotSupported (nothing launched) where TMA cannot describe the strides
+cudaError_t launch_swa_prefill_tc(const SwaPrefillLaunch& a, cudaStream_t stream);
 cudaError_t launch_swa_prefill_simt(const SwaPrefillLaunch& a, cudaStream_t stream);
 cudaError_t launch_swa_fill_rings(const SwaPrefillLaunch& a, cudaStream_t stream);
 
