@@ -610,21 +610,25 @@ def la_notebank_route(rho, u, R: int, positions=None, want_scores: bool = False,
 
 
 def _same_device(first, **others):
-    """Every tensor given lives on `first`'s CUDA device."""
-    _check_cuda(first, *others.values())
+    """Index of the CUDA device that `first` and every other tensor given live on."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("all tensors must live on a CUDA device")
     for name, t in others.items():
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"{name} is on {t.device}, the first argument on {first.device}")
+    return index
 
 
 def _expect(name, t, shape, dtype, contiguous=True):
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if not contiguous and t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if contiguous:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    elif t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
         raise ValueError(f"the last axis of {name} must be contiguous")
 
 
@@ -644,16 +648,21 @@ def _heads4(t) -> LATensor:
 
 def _new_rows(shape, dtype, device, zero=False):
     """An output whose rows start on 16-byte boundaries whatever the last size is."""
-    pad = -(-shape[-1] // 8) * 8
-    t = (torch.zeros if zero else torch.empty)((*shape[:-1], pad), dtype=dtype, device=device)
-    return t[..., :shape[-1]]
+    make = torch.zeros if zero else torch.empty
+    if shape[-1] % 8 == 0:
+        return make(shape, dtype=dtype, device=device)
+    return make((*shape[:-1], -(-shape[-1] // 8) * 8), dtype=dtype, device=device)[..., :shape[-1]]
 
 
-def _call(fn_name, device, stream, *args):
-    """Call an entry point with `device` current, on `stream` or that device's current stream."""
-    with torch.cuda.device(device):
-        handle = _stream_handle(stream if stream is not None else torch.cuda.current_stream(device))
-        st = getattr(load_library(), fn_name)(*args, handle)
+def _call(fn_name, index, stream, *args):
+    """Call an entry point with device `index` current, on `stream` or that device's current stream."""
+    fn = getattr(load_library(), fn_name)
+    handle = _stream_handle(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, handle)
     if st != LA_OK:
         raise LAError(st, fn_name)
 
@@ -667,7 +676,7 @@ def la_conv_prefill(x, w, bias=None, state_in=None, lens=None, silu: bool = True
     [B,W-1,C] in x's dtype, the last inputs, oldest first (None: zeros; state_out
     may be state_in).  lens: None or int64 [B] on the device: later tokens are
     padding, their rows of y stay as they were (zeros in a y made here)."""
-    _same_device(x, w=w, bias=bias, state_in=state_in, lens=lens, y=y, state_out=state_out)
+    index = _same_device(x, w=w, bias=bias, state_in=state_in, lens=lens, y=y, state_out=state_out)
     if x.dim() != 3 or w.dim() != 2:
         raise ValueError("x must be [B,N,C] and w [C,W]")
     B, N, C = x.shape
@@ -687,7 +696,7 @@ def la_conv_prefill(x, w, bias=None, state_in=None, lens=None, silu: bool = True
             state_out.copy_(state_in) if state_in is not None else state_out.zero_()
     a = ConvPrefillArgs(B, N, C, W, _dtype_code(x.dtype), _dtype_code(y.dtype), _dtype_code(w.dtype), _rows3(x),
                         _rows3(y), _ptr(w), _ptr(bias), _ptr(state_in), _ptr(state_out), _ptr(lens), int(bool(silu)))
-    _call("la_conv_prefill", x.device, stream, ctypes.byref(a))
+    _call("la_conv_prefill", index, stream, ctypes.byref(a))
     return y, state_out
 
 
@@ -696,7 +705,7 @@ def la_conv_decode_step(x, w, state, bias=None, silu: bool = True, out=None, sta
     """The convolution's step for one token of each sequence.  x: [S,C] (rows
     16-byte aligned); w, bias as in la_conv_prefill; state: [S,W-1,C], updated in
     place unless state_out is given.  Returns out [S,C]."""
-    _same_device(x, w=w, state=state, bias=bias, out=out, state_out=state_out)
+    index = _same_device(x, w=w, state=state, bias=bias, out=out, state_out=state_out)
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [S,C] and w [C,W]")
     S, C = x.shape
@@ -713,7 +722,7 @@ def la_conv_decode_step(x, w, state, bias=None, silu: bool = True, out=None, sta
     a = ConvDecodeArgs(S, C, W, _dtype_code(x.dtype), _dtype_code(out.dtype), _dtype_code(w.dtype), _ptr(x),
                        _axis_stride(x, 0), _ptr(out), _axis_stride(out, 0), _ptr(w), _ptr(bias), _ptr(state),
                        _ptr(state_out), int(bool(silu)))
-    _call("la_conv_decode_step", x.device, stream, ctypes.byref(a))
+    _call("la_conv_decode_step", index, stream, ctypes.byref(a))
     return out
 
 
@@ -741,7 +750,7 @@ def la_ssm_prefill(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, delta_s
     delta_bias: fp32 [C] or None; h: fp32 [B,C,n] (h_out may be h_in); lens as in
     la_conv_prefill; workspace: uint8 device tensor of at least
     la_ssm_prefill_workspace_size bytes, allocated here by default."""
-    _same_device(u, delta=delta, A=A, Bm=Bm, Cm=Cm, D=D, z=z, delta_bias=delta_bias, h_in=h_in, lens=lens, y=y,
+    index = _same_device(u, delta=delta, A=A, Bm=Bm, Cm=Cm, D=D, z=z, delta_bias=delta_bias, h_in=h_in, lens=lens, y=y,
                  h_out=h_out, workspace=workspace)
     if u.dim() != 3 or A.dim() != 2 or Bm.dim() != 4:
         raise ValueError("u must be [B,N,C], A [C,n] and Bm, Cm [B,G,N,n]")
@@ -767,7 +776,7 @@ def la_ssm_prefill(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, delta_s
     a = _ssm_prefill_args(u, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus, h_in, lens, y, h_out)
     need = int(load_library().la_ssm_prefill_workspace_size(ctypes.byref(a)))
     ws, ws_bytes = _workspace(need, workspace, u.device)
-    _call("la_ssm_prefill", u.device, stream, ctypes.byref(a), _ptr(ws) if isinstance(ws, torch.Tensor) else ws,
+    _call("la_ssm_prefill", index, stream, ctypes.byref(a), _ptr(ws) if isinstance(ws, torch.Tensor) else ws,
           ws_bytes)
     return y, h_out
 
@@ -777,7 +786,7 @@ def la_ssm_decode_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=No
     """The scan's step for one token of each sequence.  u, delta, z: [S,C]; Bm,
     Cm: [S,G,n]; state: fp32 [S,C,n], updated in place unless state_out is given;
     the rest as in la_ssm_prefill.  Returns out [S,C]."""
-    _same_device(u, delta=delta, A=A, Bm=Bm, Cm=Cm, state=state, D=D, z=z, delta_bias=delta_bias, out=out,
+    index = _same_device(u, delta=delta, A=A, Bm=Bm, Cm=Cm, state=state, D=D, z=z, delta_bias=delta_bias, out=out,
                  state_out=state_out)
     if u.dim() != 2 or A.dim() != 2 or Bm.dim() != 3:
         raise ValueError("u must be [S,C], A [C,n] and Bm, Cm [S,G,n]")
@@ -801,7 +810,7 @@ def la_ssm_decode_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=No
     a = SsmDecodeArgs(S, C, n, G, _dtype_code(u.dtype), _dtype_code(out.dtype), row(u), row(delta), row(z), row(out),
                       grp(Bm), grp(Cm), _ptr(A), _ptr(D), _ptr(delta_bias), _ptr(state), _ptr(state_out),
                       int(bool(delta_softplus)))
-    _call("la_ssm_decode_step", u.device, stream, ctypes.byref(a))
+    _call("la_ssm_decode_step", index, stream, ctypes.byref(a))
     return out
 
 
@@ -819,7 +828,7 @@ def la_swa_prefill(q, k, v, window: int = 0, scale: float | None = None, softcap
     lens: None or int64 [B]: later keys are not seen and later queries' rows of o
     stay as they were.  k_cache, v_cache: [B,H_kv,window,d] rings to fill for
     la_swa_decode_step and la_swa_biased_decode_step (window <= 256)."""
-    _same_device(q, k=k, v=v, slopes=slopes, key_lo=key_lo, key_hi=key_hi, lens=lens, o=o, k_cache=k_cache,
+    index = _same_device(q, k=k, v=v, slopes=slopes, key_lo=key_lo, key_hi=key_hi, lens=lens, o=o, k_cache=k_cache,
                  v_cache=v_cache)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B,H,Nq,d] and k, v [B,H_kv,Nk,d]")
@@ -841,7 +850,7 @@ def la_swa_prefill(q, k, v, window: int = 0, scale: float | None = None, softcap
                        _heads4(k), _heads4(v), _heads4(o), float(scale if scale is not None else d ** -0.5),
                        float(softcap), _ptr(slopes), _ptr(key_lo), _ptr(key_hi),
                        int(q_pos0 if q_pos0 is not None else Nk - Nq), _ptr(lens), _ptr(k_cache), _ptr(v_cache))
-    _call("la_swa_prefill", q.device, stream, ctypes.byref(a))
+    _call("la_swa_prefill", index, stream, ctypes.byref(a))
     return o
 
 
@@ -850,7 +859,7 @@ def la_swa_biased_decode_step(q, k, v, k_cache, v_cache, pos, softcap: float = 0
     """la_swa_decode_step with grouped heads, capped scores and a distance bias:
     q: [S,H,d]; k, v: [S,H_kv,d]; k_cache, v_cache: [S,H_kv,window,d]; pos: int64
     [S]; softcap and slopes as in la_swa_prefill.  Returns out [S,H,d]."""
-    _same_device(q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, pos=pos, slopes=slopes, out=out)
+    index = _same_device(q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, pos=pos, slopes=slopes, out=out)
     if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [S,H,d], k, v [S,H_kv,d] and the caches [S,H_kv,window,d]")
     S, H, d = q.shape
@@ -869,7 +878,7 @@ def la_swa_biased_decode_step(q, k, v, k_cache, v_cache, pos, softcap: float = 0
                          _ptr(k_cache), _ptr(v_cache), _ptr(pos), _ptr(out),
                          float(scale if scale is not None else d ** -0.5))
     a = SwaBiasedDecodeArgs(base, Hkv, float(softcap), _ptr(slopes))
-    _call("la_swa_biased_decode_step", q.device, stream, ctypes.byref(a))
+    _call("la_swa_biased_decode_step", index, stream, ctypes.byref(a))
     return out
 
 
