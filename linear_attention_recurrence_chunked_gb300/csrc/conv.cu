@@ -43,8 +43,8 @@ __device__ __forceinline__ void load_taps(const void* w, const void* bias, int64
   for (int j = 0; j < V; ++j) bs[j] = bias != nullptr && j < valid ? to_f(bp[j]) : 0.f;
 }
 
-template <typename TIn, typename TOut, typename TW, int W>
-__global__ void __launch_bounds__(kThreads)
+template <typename TIn, typename TOut, typename TW, int W, bool FULL>
+__global__ void __launch_bounds__(kThreads, 2)
 conv_prefill_kernel(const ConvLaunch a, int64_t vecs, int64_t runs, int run_len) {
   constexpr int V = kVec<TIn>;
   const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -54,8 +54,8 @@ conv_prefill_kernel(const ConvLaunch a, int64_t vecs, int64_t runs, int run_len)
   const int64_t t0 = run * run_len;
   if (n < 0 || (t0 >= n && run > 0)) return;
   const int64_t c0 = vec * V, t1 = min(t0 + run_len, n);
-  const int valid = (int)min((int64_t)V, a.C - c0);
-  const bool state_vec = a.C % V == 0;
+  const int valid = FULL ? V : (int)min((int64_t)V, a.C - c0);  // FULL: C is a multiple of V
+  const bool state_vec = FULL;
   const TIn* x = reinterpret_cast<const TIn*>(a.x) + b * a.x_sb + c0;
   const TIn* s_in = a.state_in ? reinterpret_cast<const TIn*>(a.state_in) + b * (W - 1) * a.C + c0 : nullptr;
 
@@ -152,7 +152,10 @@ cudaError_t launch_typed(const ConvLaunch& a, bool decode, cudaStream_t stream) 
   while (run_len > 4 && a.B * vecs * ((a.N + run_len - 1) / run_len) < 152 * 1024) run_len /= 2;
   const int64_t runs = std::max<int64_t>(1, (a.N + run_len - 1) / run_len);
   const int64_t grid = (a.B * vecs * runs + kThreads - 1) / kThreads;
-  conv_prefill_kernel<TIn, TOut, TW, W><<<(unsigned)grid, kThreads, 0, stream>>>(a, vecs, runs, run_len);
+  if (a.C % kVec<TIn> == 0)
+    conv_prefill_kernel<TIn, TOut, TW, W, true><<<(unsigned)grid, kThreads, 0, stream>>>(a, vecs, runs, run_len);
+  else
+    conv_prefill_kernel<TIn, TOut, TW, W, false><<<(unsigned)grid, kThreads, 0, stream>>>(a, vecs, runs, run_len);
   return cudaGetLastError();
 }
 
