@@ -101,7 +101,7 @@ __device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __ex
 // in (0, 1/3], by its series r + r^3/3 + r^5/5 + ...: the first term left out, r^17 / 17, is below
 // 2^-29 of r.
 __device__ __forceinline__ float softplus(float x) {
-  const float e = __expf(-fabsf(x));
+  const float e = expf(-fabsf(x));  // not the fast form: its error, 1.2 |x| ulp, would reach every state
   const float r = __fdividef(e, 2.f + e), q = r * r;
   float p = 1.f / 15.f;
   p = fmaf(p, q, 1.f / 13.f);
