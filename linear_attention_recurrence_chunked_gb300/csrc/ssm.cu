@@ -3,25 +3,64 @@
 //   y = (sum_s C[g,s] h[c,s] + D u) silu(z)
 // per token, channel c of group g and state s (NoteBank Sec. 2 Eq. (1) with a diagonal A_t).
 //
-// Per (token, channel, state) the scan needs one exponential and about four fp32 operations, per (token,
-// channel) four 2-byte elements of memory: with 16 states the special-function unit (16 results per SM and
-// clock) bounds it at three times the memory time.  The decay differs per (channel, state), so no chunk
-// form on the tensor cores exists: the tokens are walked in order, with the channels and states in
-// parallel.  L lanes share a channel, four states in each lane's registers; B_t, C_t and (dt, dt u) of a
-// tile of tokens are staged in shared memory, where each (token, channel)'s softplus is computed once.
-// The readout's sum over a channel's lanes is a reduce-scatter over four tokens at a time.
+// Per (token, channel, state) the scan needs one exponential and four fp32 operations, per (token, channel)
+// four 2-byte elements of memory: with 16 states the special-function unit (16 results per SM and clock)
+// bounds it at three times the memory time.  The decay differs per (channel, state), so no chunk form on
+// the tensor cores exists: the tokens are walked in order, with the channels and states in parallel.
+//
+// A block has four scan warps, four layout warps and four output warps, which work on tiles of tokens in turn
+// through shared memory, one barrier a tile.  While the scan warps walk tile i, the layout warps prepare tile
+// i + 1 (the step sizes with their softplus, once per (token, channel), and B_t, C_t in fp32), with the raw
+// inputs of the tiles behind it on their way, and the output warps add up the readout of tile i - 1, apply
+// the skip term and the gate and store it.  In the scan L lanes share kCh channels; a lane holds four states
+// of each, as pairs for the paired fp32 operations.  The inputs of the next tokens are read before the parts
+// of the readout are written: the compiler keeps that order (it cannot tell the two apart), and the other one
+// would put a shared-memory round trip, an exponential and four operations in a row for every token.
 #include <algorithm>
+#include <mutex>
 
 #include "layers.cuh"
+#include "tc.cuh"
 
 namespace la {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kK = 4;  // states per lane
+constexpr int kScan = 128;    // threads of the four scan warps
+constexpr int kOutput = 128;  // and of the output warps
+// Channels per scan lane.  Two halve a state's share of the reads of B and C (a lane's bytes count there, 128
+// a clock and SM, also where lanes read the same), which bound the scan with one, but leave half the blocks.
+// 4 x 16384 x 2048 channels, 16 states: 807 us with two, 928 us with one; with at most one block of one channel
+// per lane on each SM, one channel is faster.
+constexpr int layout_threads(int ch) { return ch * kScan; }
+constexpr int block_threads(int ch) { return kScan + layout_threads(ch) + kOutput; }
+// tokens whose inputs a scan lane reads ahead: one block with two channels per lane has an SM's registers for
+// itself
+constexpr int read_ahead(int ch) { return ch == 2 ? 4 : 2; }
+constexpr int kK = 4;              // states per lane
 
-// tokens of a tile: enough to make its loads and barriers rare, few enough for shared memory
-constexpr int tile_tokens(int L) { return L >= 8 ? 64 : 32; }
+// Paired fp32 operations: two independent lanes of a 64-bit register pair.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 ex2_2(f32x2 x) {
+  float lo, hi;
+  unpack2(x, lo, hi);
+  return pack2(ex2(lo), ex2(hi));
+}
 
 // A log2(e), kept finite so that a step of dt = 0 changes nothing even for the lowest A
 __device__ __forceinline__ float log2_rate(float A) {
@@ -41,184 +80,342 @@ enum Mode { kFull, kLocal, kFinal };
 
 __host__ __device__ constexpr int lanes_of(int n) { return n <= 4 ? 1 : n <= 8 ? 2 : n <= 16 ? 4 : n <= 32 ? 8 : 16; }
 
-template <int L, typename TIn, typename TOut, int MODE>
-__global__ void __launch_bounds__(kThreads)
-ssm_scan_kernel(const SsmLaunch a, Segments seg, float* ws_h, float* ws_dt) {
-  constexpr int CT = kThreads / L, TT = tile_tokens(L), NP = L * kK;
-  constexpr int V = kVec<TIn>, VPR = CT / V > 0 ? CT / V : 1;  // vectors per row of the tile
-  constexpr int NVEC = TT * VPR, NVI = (NVEC + kThreads - 1) / kThreads;
-  constexpr int NB = TT * NP / kThreads;
-  __shared__ __align__(16) float2 s_dt[TT][CT];  // (dt, dt u); the readout replaces dt
-  __shared__ __align__(16) float s_B[TT][NP], s_C[MODE == kLocal ? 1 : TT][NP];
+// Four states' B and C for one lane.
+struct LaneBC {
+  ulonglong2 b, c;
+};
 
-  const int tid = threadIdx.x, l = tid % L, ch = tid / L;
+template <int L, int kCh, typename TIn>
+struct Tile {
+  static constexpr int TT = L >= 4 ? 32 : 8 * L;  // tokens
+  static constexpr int CT = kCh * kScan / L;      // channels of a block
+  static constexpr int kRaw = sizeof(TIn) == 2 ? 5 : 4;  // tiles of raw inputs: from the one being stored to the last on its way
+  struct Raw {
+    TIn u[TT * CT], delta[TT * CT], z[TT * CT], bc[2][TT * L * kK];
+  };
+  struct Work {
+    float2 dt[TT][CT];                            // (dt, dt u)
+    LaneBC bc[TT][L];
+    float y[kCh][TT][kScan];                      // the lanes' parts of the readout
+  };
+  Work work[2];
+  Raw raw[kRaw];
+  // Place of channel c in row r of dt, and of its lanes' parts in y (in units of L).  Eight neighbouring
+  // layout or output threads, which hold vectors of channels, and the scan's lanes, which hold neighbouring
+  // channels, both meet different banks.  The places repeat every kPeriod rows.
+  static constexpr int kPeriod = L >= 4 * kCh ? L / 2 / kCh : 1;
+  __device__ static __forceinline__ int dt_at(int r, int c) {
+    return kCh == 1 ? c ^ ((((r * CT + c) >> 4) & 3) << 1) : c ^ ((((r * (CT / 2) + (c >> 1)) >> 3) & 3) << 1);
+  }
+  __device__ static __forceinline__ int y_at(int r, int c) {
+    return kCh == 1 ? c ^ (((r * CT + c) >> 3) & 7) : (c >> 1) ^ (((r * (CT / 2) + (c >> 1)) >> 3) & 3);
+  }
+};
+
+template <int L, int kCh, typename TIn, typename TOut, int MODE>
+__global__ void __launch_bounds__(block_threads(kCh), kCh == 2 ? 1 : 2)
+ssm_scan_kernel(const SsmLaunch a, Segments seg, float* ws_h, float* ws_dt) {
+  using T = Tile<L, kCh, TIn>;
+  constexpr int CT = T::CT, TT = T::TT, kLayout = layout_threads(kCh), kAhead = read_ahead(kCh);
+  extern __shared__ __align__(16) uint8_t ssm_smem[];
+  T& sm = *reinterpret_cast<T*>(ssm_smem);
+
+  const int tid = threadIdx.x;
   const int64_t Cg = a.C / a.G, tiles = (Cg + CT - 1) / CT;
   const int64_t g = blockIdx.x / tiles, b = blockIdx.y;
   const int64_t c_base = g * Cg + (blockIdx.x % tiles) * CT, c_end = (g + 1) * Cg;
   const int64_t sid = blockIdx.z;
   const int64_t len = sequence_length(a.lens, b, a.N, a.status, blockIdx.x == 0 && sid == 0 && tid == 0);
   if (len < 0) return;  // uniform over the block
-  const int64_t t0 = sid * seg.len, t1 = min(t0 + seg.len, len);
+  const int64_t t0 = sid * seg.len;
+  const int tokens = t0 < len ? (int)(min(t0 + seg.len, len) - t0) : 0;
+  const int count = (tokens + TT - 1) / TT;  // tiles
 
-  const int64_t c = c_base + ch;
-  const bool live = c < c_end;
-  float A2[kK], h[kK];
-  const int64_t hrow = (b * a.C + c) * a.n;
-  const int64_t wrow = ((b * seg.count + sid) * a.C + c) * a.n;
+  if (tid < kScan) {
+    // ================================================================ scan warps
+    const int l = tid % L, p = tid / L;
+    const int64_t c = c_base + p * kCh;
+    f32x2 A01[kCh], A23[kCh], h01[kCh], h23[kCh];
+    float dt_sum[kCh];
 #pragma unroll
-  for (int k = 0; k < kK; ++k) {
-    const int s = l * kK + k;
-    const bool on = live && s < a.n;
-    A2[k] = on ? log2_rate(a.A[c * a.n + s]) : 0.f;
-    h[k] = 0.f;
-    if (MODE == kFull && on && a.h_in) h[k] = a.h_in[hrow + s];
-    if (MODE == kFinal && on) h[k] = ws_h[wrow + s];
-  }
-  float dt_sum = 0.f;
-
-  const TIn* u_p = reinterpret_cast<const TIn*>(a.u) + b * a.u_sb;
-  const TIn* d_p = reinterpret_cast<const TIn*>(a.delta) + b * a.d_sb;
-  const TIn* z_p = MODE != kLocal && a.z ? reinterpret_cast<const TIn*>(a.z) + b * a.z_sb : nullptr;
-  const TIn* B_p = reinterpret_cast<const TIn*>(a.Bm.ptr) + b * a.Bm.sb + g * a.Bm.sh;
-  const TIn* C_p = reinterpret_cast<const TIn*>(a.Cm.ptr) + b * a.Cm.sb + g * a.Cm.sh;
-  TOut* y_p = reinterpret_cast<TOut*>(a.y) + b * a.y_sb;
-  const bool vec = (c_base * sizeof(TIn)) % 16 == 0;             // rows are 16-byte aligned, c_base may not be
-  const bool yvec = (c_base * sizeof(TOut)) % (V * sizeof(TOut)) == 0;
-
-  // this thread's vectors of the tile: row i / VPR, channels c_base + V (i % VPR)
-  uint4 ru[NVI], rd[NVI], rz[NVI];
-  TIn rB[NB], rC[NB];
-  auto fetch = [&](int64_t t) {
+    for (int e = 0; e < kCh; ++e) {
+      float A2[kK], h[kK];
 #pragma unroll
-    for (int i = 0; i < NVI; ++i) {
-      const int e = tid + i * kThreads, r = e / VPR, v = e % VPR;
-      const int64_t cc = c_base + v * V;
-      const int valid = (NVEC % kThreads == 0 || e < NVEC) && t + r < t1 ? (int)max((int64_t)0, min((int64_t)min(V, CT), c_end - cc)) : 0;
-      if (valid > 0) {
-        ru[i] = load_raw(u_p + (t + r) * a.u_st + cc, valid, vec);
-        rd[i] = load_raw(d_p + (t + r) * a.d_st + cc, valid, vec);
-        if (z_p) rz[i] = load_raw(z_p + (t + r) * a.z_st + cc, valid, vec);
+      for (int k = 0; k < kK; ++k) {
+        const int s = l * kK + k;
+        const bool on = c + e < c_end && s < a.n;
+        A2[k] = on ? log2_rate(a.A[(c + e) * a.n + s]) : 0.f;
+        h[k] = 0.f;
+        if (MODE == kFull && on && a.h_in) h[k] = a.h_in[(b * a.C + c + e) * a.n + s];
+        if (MODE == kFinal && on) h[k] = ws_h[((b * seg.count + sid) * a.C + c + e) * a.n + s];
       }
+      A01[e] = pack2(A2[0], A2[1]);
+      A23[e] = pack2(A2[2], A2[3]);
+      h01[e] = pack2(h[0], h[1]);
+      h23[e] = pack2(h[2], h[3]);
+      dt_sum[e] = 0.f;
     }
+    int dt_at[T::kPeriod], y_at[T::kPeriod];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int e = tid + i * kThreads, r = e / NP, s = e % NP;
-      const bool on = t + r < t1 && s < a.n;
-      rB[i] = on ? B_p[(t + r) * a.Bm.st + s] : TIn(0.f);
-      if (MODE != kLocal) rC[i] = on ? C_p[(t + r) * a.Cm.st + s] : TIn(0.f);
+    for (int r = 0; r < T::kPeriod; ++r) {
+      dt_at[r] = T::dt_at(r, p * kCh);
+      y_at[r] = T::y_at(r, p * kCh) * L + l;
     }
-  };
-  if (t0 < t1) fetch(t0);
-
-  for (int64_t t = t0; t < t1; t += TT) {
-    // ---- the tile's step sizes and B, C into shared memory; a token behind the end changes nothing (dt = 0)
-    uint4 cu[NVI], cz[NVI];
-#pragma unroll
-    for (int i = 0; i < NVI; ++i) {
-      cu[i] = ru[i];
-      cz[i] = rz[i];
-      const int e = tid + i * kThreads, r = e / VPR, v = e % VPR;
-      if (NVEC % kThreads != 0 && e >= NVEC) continue;
-      float fu[V], fd[V];
-      unpack_vec(ru[i], fu);
-      unpack_vec(rd[i], fd);
-#pragma unroll
-      for (int j = 0; j < V && j < CT; ++j) {
-        const int64_t cc = c_base + v * V + j;
-        float dt = 0.f, dtu = 0.f;
-        if (t + r < t1 && cc < c_end) {
-          const float x = a.delta_bias ? fd[j] + a.delta_bias[cc] : fd[j];
-          dt = a.softplus ? softplus(x) : x;
-          dtu = dt * fu[j];
-        }
-        s_dt[r][v * V + j] = make_float2(dt, dtu);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int e = tid + i * kThreads;
-      s_B[e / NP][e % NP] = to_f(rB[i]);
-      if (MODE != kLocal) s_C[e / NP][e % NP] = to_f(rC[i]);
-    }
-    __syncthreads();
-    if (t + TT < t1) fetch(t + TT);
-    // ---- the recurrence, four tokens at a time
-#pragma unroll 2
-    for (int r = 0; r < TT; r += 4) {
-      float acc[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 d = s_dt[r + q][ch];
-        const float4 Bv = *reinterpret_cast<const float4*>(&s_B[r + q][l * kK]);
-        const float Bk[4] = {Bv.x, Bv.y, Bv.z, Bv.w};
-#pragma unroll
-        for (int k = 0; k < kK; ++k) h[k] = fmaf(ex2(d.x * A2[k]), h[k], d.y * Bk[k]);
-        if constexpr (MODE == kLocal) {
-          dt_sum += d.x;
+    struct In {
+      float dt[kCh], dtu[kCh];
+      LaneBC bc;
+    };
+    __syncthreads();  // tile 0 is laid out
+    for (int i = 0; i < count; ++i) {
+      typename T::Work& q = sm.work[i & 1];
+      auto read = [&](int r) {
+        In x;
+        if constexpr (kCh == 1) {
+          const float2 d = q.dt[r][dt_at[r % T::kPeriod]];
+          x.dt[0] = d.x;
+          x.dtu[0] = d.y;
         } else {
-          const float4 Cv = *reinterpret_cast<const float4*>(&s_C[r + q][l * kK]);
-          acc[q] = fmaf(Cv.x, h[0], Cv.y * h[1]) + fmaf(Cv.z, h[2], Cv.w * h[3]);
+          const float4 d = *reinterpret_cast<const float4*>(&q.dt[r][dt_at[r % T::kPeriod]]);
+          x.dt[0] = d.x;
+          x.dtu[0] = d.y;
+          x.dt[kCh - 1] = d.z;
+          x.dtu[kCh - 1] = d.w;
         }
-      }
-      if constexpr (MODE != kLocal) {
-        // sum over the channel's lanes; the halving steps leave token `q` with its share of the lanes
-        if constexpr (L == 1) {
+        x.bc = q.bc[r][l];
+        return x;
+      };
+      In cur[kAhead], next[kAhead];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) s_dt[r + q][ch].x = acc[q];
-        } else {
-          const bool up1 = (l & (L / 2)) != 0;
-          float p0 = up1 ? acc[2] : acc[0], p1 = up1 ? acc[3] : acc[1];
-          p0 += __shfl_xor_sync(kFullMask, up1 ? acc[0] : acc[2], L / 2);
-          p1 += __shfl_xor_sync(kFullMask, up1 ? acc[1] : acc[3], L / 2);
-          if constexpr (L == 2) {
-            s_dt[r + 2 * up1][ch].x = p0;
-            s_dt[r + 2 * up1 + 1][ch].x = p1;
-          } else {
-            const bool up2 = (l & (L / 4)) != 0;
-            float p = up2 ? p1 : p0;
-            p += __shfl_xor_sync(kFullMask, up2 ? p0 : p1, L / 4);
+      for (int k = 0; k < kAhead; ++k) cur[k] = read(k);
 #pragma unroll
-            for (int off = L / 8; off >= 1; off >>= 1) p += __shfl_xor_sync(kFullMask, p, off);
-            if (l % (L / 4) == 0) s_dt[r + 2 * up1 + up2][ch].x = p;
-          }
+      for (int r = 0; r < TT; r += kAhead) {
+        if (r + kAhead < TT) {
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) next[k] = read(r + kAhead + k);
         }
-      }
-    }
-    __syncthreads();
-    // ---- skip term, gate and store; each thread reads the entries it writes for the next tile
-    if constexpr (MODE != kLocal) {
+        float y[kAhead][kCh];
 #pragma unroll
-      for (int i = 0; i < NVI; ++i) {
-        const int e = tid + i * kThreads, r = e / VPR, v = e % VPR;
-        const int64_t cc = c_base + v * V;
-        const int valid = (NVEC % kThreads == 0 || e < NVEC) && t + r < t1 ? (int)max((int64_t)0, min((int64_t)min(V, CT), c_end - cc)) : 0;
-        if (valid > 0) {
-          float fu[V], fz[V], o[V];
-          unpack_vec(cu[i], fu);
-          unpack_vec(cz[i], fz);
+        for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            o[j] = 0.f;
-            if (j < valid) {
-              o[j] = s_dt[r][v * V + j].x;
-              if (a.D) o[j] = fmaf(a.D[cc + j], fu[j], o[j]);
-              if (z_p) o[j] *= silu(fz[j]);
+          for (int e = 0; e < kCh; ++e) {
+            const In& x = cur[k];
+            const f32x2 dt2 = pack2(x.dt[e], x.dt[e]), dtu2 = pack2(x.dtu[e], x.dtu[e]);
+            h01[e] = fma2(ex2_2(mul2(dt2, A01[e])), h01[e], mul2(dtu2, x.bc.b.x));
+            h23[e] = fma2(ex2_2(mul2(dt2, A23[e])), h23[e], mul2(dtu2, x.bc.b.y));
+            if constexpr (MODE == kLocal) {
+              dt_sum[e] += x.dt[e];
+            } else {
+              float lo, hi;
+              unpack2(fma2(x.bc.c.y, h23[e], mul2(x.bc.c.x, h01[e])), lo, hi);
+              y[k][e] = lo + hi;
             }
           }
-          store_floats(y_p + (t + r) * a.y_st + cc, o, valid, yvec);
+        if constexpr (MODE != kLocal) {
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int e = 0; e < kCh; ++e) q.y[e][r + k][y_at[(r + k) % T::kPeriod]] = y[k][e];
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) cur[k] = next[k];
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int e = 0; e < kCh; ++e) {
+      float h[kK];
+      unpack2(h01[e], h[0], h[1]);
+      unpack2(h23[e], h[2], h[3]);
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+        const int s = l * kK + k;
+        if (c + e < c_end && s < a.n) {
+          if (MODE == kLocal) ws_h[((b * seg.count + sid) * a.C + c + e) * a.n + s] = h[k];
+          else if (MODE == kFull || sid == seg.count - 1) a.h_out[(b * a.C + c + e) * a.n + s] = h[k];
         }
       }
+      if (MODE == kLocal && l == 0 && c + e < c_end) ws_dt[(b * seg.count + sid) * a.C + c + e] = dt_sum[e];
     }
+    return;
   }
+
+  // A layout or output thread's vectors of a tile: rows r0 + i RS, V channels from v0 on.
+  constexpr int V = kVec<TIn>, VPR = CT / V;
+  const int ht = tid < kScan + kLayout ? tid - kScan : tid - kScan - kLayout;
+  const int r0 = ht / VPR, v0 = ht % VPR * V;
+  const int64_t cv = c_base + v0;
+  const int valid = (int)max((int64_t)0, min((int64_t)V, c_end - cv));
+  const bool gate = MODE != kLocal && a.z != nullptr;
+
+  if (tid < kScan + kLayout) {
+    // ================================================================ layout warps
+    constexpr int RS = kLayout / VPR, NVI = (TT + RS - 1) / RS;
+    auto slot = [&](int i) { return ((r0 + i * RS) * VPR + ht % VPR) * V; };  // of vector i in a raw tile
+    auto in_tile = [&](int i) { return TT % RS == 0 || r0 + i * RS < TT; };
+    constexpr int NP = L * kK, BS = kLayout / NP, NB = (TT + BS - 1) / BS;  // a thread's elements of B and C: BS rows apart
+    // rows are 16-byte aligned, but a group's first channel may not be, nor rows of B and C
+    const bool vec = (c_base * sizeof(TIn)) % 16 == 0 && valid == V;
+    const int rb = ht / NP, sb = ht % NP;
+    const TIn* u_p = reinterpret_cast<const TIn*>(a.u) + b * a.u_sb + (t0 + r0) * a.u_st + cv;
+    const TIn* d_p = reinterpret_cast<const TIn*>(a.delta) + b * a.d_sb + (t0 + r0) * a.d_st + cv;
+    const TIn* z_p = reinterpret_cast<const TIn*>(a.z) + b * a.z_sb + (t0 + r0) * a.z_st + cv;
+    const TIn* B_p = reinterpret_cast<const TIn*>(a.Bm.ptr) + b * a.Bm.sb + g * a.Bm.sh + t0 * a.Bm.st;
+    const TIn* C_p = reinterpret_cast<const TIn*>(a.Cm.ptr) + b * a.Cm.sb + g * a.Cm.sh + t0 * a.Cm.st;
+    const bool bc_vec = a.n == NP && ((reinterpret_cast<uintptr_t>(B_p) | reinterpret_cast<uintptr_t>(C_p) |
+                                       (uintptr_t)((a.Bm.st | a.Cm.st) * (int64_t)sizeof(TIn))) & 15u) == 0 && NP % V == 0;
+    float bias[V];
+    int dt_at[NVI][V / 2];  // where the channels of a vector lie in a tile
 #pragma unroll
-  for (int k = 0; k < kK; ++k) {
-    const int s = l * kK + k;
-    if (live && s < a.n) {
-      if (MODE == kLocal) ws_h[wrow + s] = h[k];
-      else if (MODE == kFull || sid == seg.count - 1) a.h_out[hrow + s] = h[k];
+    for (int j = 0; j < V; ++j) bias[j] = a.delta_bias && j < valid ? a.delta_bias[cv + j] : 0.f;
+#pragma unroll
+    for (int i = 0; i < NVI; ++i)
+#pragma unroll
+      for (int j = 0; j < V; j += 2) dt_at[i][j / 2] = (r0 + i * RS) * CT + T::dt_at(r0 + i * RS, v0 + j);
+
+    // one vector of a raw tile: asynchronously, or by elements where it is partial or not aligned
+    auto copy = [&](TIn* dst, const TIn* src, int n, bool whole) {
+      if (whole) tc::cp_async16(tc::smem_u32(dst), src, 16u);
+      else *reinterpret_cast<uint4*>(dst) = load_raw(src, n, false);
+    };
+    auto fetch = [&](int k) {  // raw inputs of tile k; what lies behind the end is not read
+      if (k < count) {
+        typename T::Raw& w = sm.raw[k % T::kRaw];
+        const int left = tokens - k * TT;
+#pragma unroll
+        for (int i = 0; i < NVI; ++i) {
+          const int r = k * TT + i * RS;
+          if (in_tile(i) && r0 + i * RS < left && valid > 0) {
+            copy(w.u + slot(i), u_p + r * a.u_st, valid, vec);
+            copy(w.delta + slot(i), d_p + r * a.d_st, valid, vec);
+            if (gate) copy(w.z + slot(i), z_p + r * a.z_st, valid, vec);
+          }
+        }
+        if (bc_vec) {
+          constexpr int per = NP / V > 0 ? NP / V : 1;  // vectors per row
+          for (int e = ht; e < 2 * TT * per; e += kLayout) {
+            const int m = e / (TT * per), r = e / per % TT, v = e % per * V;
+            if (r < left && (MODE != kLocal || m == 0))
+              copy(w.bc[m] + r * NP + v, (m ? C_p + (int64_t)(k * TT + r) * a.Cm.st : B_p + (int64_t)(k * TT + r) * a.Bm.st) + v, V, true);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const int r = rb + i * BS;
+            if (r < TT && r < left && sb < a.n) {
+              w.bc[0][r * NP + sb] = B_p[(int64_t)(k * TT + r) * a.Bm.st + sb];
+              if (MODE != kLocal) w.bc[1][r * NP + sb] = C_p[(int64_t)(k * TT + r) * a.Cm.st + sb];
+            }
+          }
+        }
+      }
+      tc::cp_async_commit();  // a group per tile, also for none
+    };
+    auto lay_out = [&](int k) {  // a token behind the end changes nothing (dt = 0, B = C = 0)
+      const typename T::Raw& w = sm.raw[k % T::kRaw];
+      typename T::Work& q = sm.work[k & 1];
+      const int left = tokens - k * TT;
+#pragma unroll
+      for (int i = 0; i < NVI; ++i) {
+        if (!in_tile(i)) continue;
+        float fu[V], fd[V], dt[V];
+        const bool on = r0 + i * RS < left && valid > 0;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        unpack_vec(on ? *reinterpret_cast<const uint4*>(w.u + slot(i)) : zero, fu);
+        unpack_vec(on ? *reinterpret_cast<const uint4*>(w.delta + slot(i)) : zero, fd);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float x = fd[j] + bias[j];
+          dt[j] = a.softplus ? softplus(x) : x;
+          if (!on) dt[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < V; j += 2)
+          *reinterpret_cast<float4*>(&q.dt[0][0] + dt_at[i][j / 2]) = make_float4(dt[j], dt[j] * fu[j], dt[j + 1], dt[j + 1] * fu[j + 1]);
+      }
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int r = rb + i * BS;
+        if (TT % BS != 0 && r >= TT) continue;
+        const bool on = r < left && sb < a.n;
+        float* x = reinterpret_cast<float*>(&q.bc[r][sb / kK]) + sb % kK;
+        x[0] = on ? to_f(w.bc[0][r * NP + sb]) : 0.f;
+        if (MODE != kLocal) x[kK] = on ? to_f(w.bc[1][r * NP + sb]) : 0.f;
+      }
+    };
+    // Tile k is on its way from iteration k - kAheadTiles on; its raw inputs stay until its outputs are
+    // stored in iteration k + 1.  The four layout warps exchange B and C among themselves: barrier 1.
+    constexpr int kAheadTiles = T::kRaw - 2;
+    for (int k = 0; k < kAheadTiles; ++k) fetch(k);
+    auto arrived = [&]() {  // the oldest of kAheadTiles groups has landed, for all layout warps
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAheadTiles - 1) : "memory");
+      tc::named_bar_sync(1, kLayout);
+    };
+    arrived();
+    if (count > 0) lay_out(0);
+    __syncthreads();  // tile 0 is laid out
+    for (int i = 0; i < count; ++i) {
+      fetch(i + kAheadTiles);
+      arrived();
+      if (i + 1 < count) lay_out(i + 1);
+      __syncthreads();
     }
+    tc::cp_async_wait_all();
+  } else {
+    // ================================================================ output warps
+    constexpr int RS = kOutput / VPR, NVI = (TT + RS - 1) / RS;
+    auto slot = [&](int i) { return ((r0 + i * RS) * VPR + ht % VPR) * V; };
+    auto in_tile = [&](int i) { return TT % RS == 0 || r0 + i * RS < TT; };
+    TOut* y_p = reinterpret_cast<TOut*>(a.y) + b * a.y_sb + (t0 + r0) * a.y_st + cv;
+    const bool yvec = c_base % V == 0;
+    float skip[V];
+    int y_at[NVI][V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) skip[j] = MODE != kLocal && a.D && j < valid ? a.D[cv + j] : 0.f;
+#pragma unroll
+    for (int i = 0; i < NVI; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int r = r0 + i * RS;
+        y_at[i][j] = ((v0 + j) % kCh) * (TT * kScan) + r * kScan + T::y_at(r, v0 + j) * L;
+      }
+    auto store = [&](int k) {  // readout, skip term and gate of tile k
+      const typename T::Raw& w = sm.raw[k % T::kRaw];
+      const typename T::Work& q = sm.work[k & 1];
+#pragma unroll
+      for (int i = 0; i < NVI; ++i) {
+        if (!in_tile(i) || r0 + i * RS >= tokens - k * TT || valid == 0) continue;
+        float fu[V], fz[V], o[V];
+        unpack_vec(*reinterpret_cast<const uint4*>(w.u + slot(i)), fu);
+        if (gate) unpack_vec(*reinterpret_cast<const uint4*>(w.z + slot(i)), fz);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float* part = &q.y[0][0][0] + y_at[i][j];
+          float y;
+          if constexpr (L >= 4) {
+            y = 0.f;
+#pragma unroll
+            for (int e = 0; e < L; e += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(part + e);
+              y += (x.x + x.y) + (x.z + x.w);
+            }
+          } else if constexpr (L == 2) {
+            y = part[0] + part[1];
+          } else {
+            y = part[0];
+          }
+          y = fmaf(skip[j], fu[j], y);
+          o[j] = gate ? y * silu(fz[j]) : y;
+        }
+        store_floats(y_p + (int64_t)(k * TT + i * RS) * a.y_st, o, valid, yvec);
+      }
+    };
+    __syncthreads();  // tile 0 is laid out
+    for (int i = 0; i < count; ++i) {
+      if (MODE != kLocal && i > 0) store(i - 1);
+      __syncthreads();
+    }
+    if (MODE != kLocal && count > 0) store(count - 1);
   }
-  if (MODE == kLocal && live && l == 0) ws_dt[(b * seg.count + sid) * a.C + c] = dt_sum;
 }
 
 // The state that enters each segment, in place of the segment's local state: over a segment a state
@@ -320,37 +517,50 @@ ssm_decode_kernel(const SsmLaunch a) {
   }
 }
 
+// Blocks of one sequence batch with `ch` channels per lane.
+int64_t scan_blocks(int64_t B, int64_t C, int n, int64_t G, int ch) {
+  const int CT = ch * kScan / lanes_of(n);
+  return B * G * ((C / G + CT - 1) / CT);
+}
+
 Segments plan(int64_t B, int64_t N, int64_t C, int n, int64_t G) {
-  const int L = lanes_of(n), CT = kThreads / L, TT = tile_tokens(L);
-  const int64_t blocks = B * G * ((C / G + CT - 1) / CT);
   // A segmented scan does the exponentials twice, so it pays from about three segments' worth of idle SMs
   // on, and segments of a few tiles at least.
-  const int64_t want = std::min<int64_t>(304 / std::max<int64_t>(blocks, 1), N / (4 * TT));
+  constexpr int kTile = 32;
+  const int64_t want = std::min<int64_t>(304 / std::max<int64_t>(scan_blocks(B, C, n, G, 1), 1), N / (4 * kTile));
   if (want < 3) return Segments{1, N};
-  const int64_t len = ((N + want - 1) / want + TT - 1) / TT * TT;
+  const int64_t len = ((N + want - 1) / want + kTile - 1) / kTile * kTile;
   return Segments{(int)((N + len - 1) / len), len};
+}
+
+template <int L, int kCh, typename TIn, typename TOut, int MODE>
+cudaError_t launch_mode(const SsmLaunch& a, const Segments& seg, int segments, float* ws_h, float* ws_dt, cudaStream_t stream) {
+  using T = Tile<L, kCh, TIn>;
+  const auto kernel = ssm_scan_kernel<L, kCh, TIn, TOut, MODE>;
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [&] { attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(T)); });
+  if (attr != cudaSuccess) return attr;
+  const dim3 grid((unsigned)(a.G * ((a.C / a.G + T::CT - 1) / T::CT)), (unsigned)a.B, (unsigned)segments);
+  kernel<<<grid, block_threads(kCh), sizeof(T), stream>>>(a, seg, ws_h, ws_dt);
+  return cudaGetLastError();
 }
 
 template <int L, typename TIn, typename TOut>
 cudaError_t launch_scan(const SsmLaunch& a, void* ws, const Segments& seg, cudaStream_t stream) {
-  constexpr int CT = kThreads / L;
-  const dim3 grid((unsigned)(a.G * ((a.C / a.G + CT - 1) / CT)), (unsigned)a.B, (unsigned)seg.count);
   if (seg.count == 1) {
-    ssm_scan_kernel<L, TIn, TOut, kFull><<<grid, kThreads, 0, stream>>>(a, seg, nullptr, nullptr);
-    return cudaGetLastError();
+    return scan_blocks(a.B, a.C, a.n, a.G, 1) > 152 ? launch_mode<L, 2, TIn, TOut, kFull>(a, seg, 1, nullptr, nullptr, stream)
+                                                    : launch_mode<L, 1, TIn, TOut, kFull>(a, seg, 1, nullptr, nullptr, stream);
   }
   float* ws_h = static_cast<float*>(ws);
   float* ws_dt = ws_h + a.B * seg.count * a.C * a.n;
-  const dim3 grid_local(grid.x, grid.y, grid.z - 1);  // nothing enters from the last segment
-  ssm_scan_kernel<L, TIn, TOut, kLocal><<<grid_local, kThreads, 0, stream>>>(a, seg, ws_h, ws_dt);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_mode<L, 1, TIn, float, kLocal>(a, seg, seg.count - 1, ws_h, ws_dt, stream);  // nothing enters from the last
   if (e != cudaSuccess) return e;
   const int64_t states = a.B * a.C * a.n;
   ssm_combine_kernel<<<(unsigned)((states + 255) / 256), 256, 0, stream>>>(a, seg, ws_h, ws_dt);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  ssm_scan_kernel<L, TIn, TOut, kFinal><<<grid, kThreads, 0, stream>>>(a, seg, ws_h, ws_dt);
-  return cudaGetLastError();
+  return launch_mode<L, 1, TIn, TOut, kFinal>(a, seg, seg.count, ws_h, ws_dt, stream);
 }
 
 template <typename TIn, typename TOut>

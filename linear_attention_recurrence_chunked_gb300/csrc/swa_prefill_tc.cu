@@ -59,12 +59,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // 0 * x summed over the eight bf16 of a vector: NaN exactly where one of them is not finite
 __device__ __forceinline__ __nv_bfloat162 add_zero_times(uint4 u, __nv_bfloat162 acc) {
   const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
