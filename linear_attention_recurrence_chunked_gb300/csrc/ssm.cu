@@ -38,30 +38,6 @@ constexpr int block_threads(int ch) { return kScan + layout_threads(ch) + kOutpu
 constexpr int read_ahead(int ch) { return ch == 2 ? 4 : 2; }
 constexpr int kK = 4;              // states per lane
 
-// Paired fp32 operations: two independent lanes of a 64-bit register pair.
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(f32x2 x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f32x2 ex2_2(f32x2 x) {
-  float lo, hi;
-  unpack2(x, lo, hi);
-  return pack2(ex2(lo), ex2(hi));
-}
-
 // A log2(e), kept finite so that a step of dt = 0 changes nothing even for the lowest A
 __device__ __forceinline__ float log2_rate(float A) {
   const float x = A * kLog2e;

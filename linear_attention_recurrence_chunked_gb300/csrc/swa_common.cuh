@@ -11,17 +11,16 @@ struct KeySpan {
 
 // Query row i of sequence b, which has len tokens: its interval, clamped to the keys that exist.  Rows
 // behind the last query and padding see nothing.
-__device__ __forceinline__ KeySpan key_span(const SwaPrefillLaunch& a, int64_t b, int64_t i, int64_t len) {
-  const int64_t p = a.q_pos0 + i;
+__device__ __forceinline__ KeySpan key_span(const SwaPrefillLaunch& a, int b, int i, int len) {
+  const int p = (int)a.q_pos0 + i;
   KeySpan s{0, 0};
-  if (i >= a.Nq || p >= len) return s;
-  int64_t lo = a.key_lo ? max(a.key_lo[b * a.Nq + i], 0) : 0;
-  int64_t hi = a.key_hi ? (int64_t)a.key_hi[b * a.Nq + i] : p + 1;
-  if (a.window > 0) lo = max(lo, p - a.window + 1);
-  hi = min(hi, len);
-  if (lo >= hi) return s;
-  s.lo = (int)lo;
-  s.hi = (int)hi;
+  if (i >= (int)a.Nq || p >= len) return s;
+  const int64_t at = (int64_t)b * a.Nq + i;
+  const int w = (int)min(a.window, (int64_t)INT32_MAX);
+  int lo = a.key_lo ? max(a.key_lo[at], 0) : 0;
+  const int hi = min(a.key_hi ? a.key_hi[at] : p + 1, len);
+  if (w > 0) lo = max(lo, p - w + 1);
+  if (lo < hi) s = KeySpan{lo, hi};
   return s;
 }
 

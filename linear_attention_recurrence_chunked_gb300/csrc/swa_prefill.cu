@@ -45,7 +45,7 @@ swa_simt_kernel(const SwaPrefillLaunch a, int q_tiles) {
   }
   __syncthreads();
   if (tid < kBM) {
-    const KeySpan sp = key_span(a, b, i0 + tid, len);
+    const KeySpan sp = key_span(a, (int)b, (int)i0 + tid, (int)len);
     s_lo[tid] = sp.lo;
     s_hi[tid] = sp.hi;
     if (sp.lo < sp.hi) {

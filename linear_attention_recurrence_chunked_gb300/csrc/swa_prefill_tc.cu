@@ -6,19 +6,28 @@
 // All exponentials are base 2 (scores carry a factor log2 e).  The scale-up is put off while m grows by
 // less than 2^8: P then stays below 256, which fp32 sums and bf16 weights hold as exactly as values below 1.
 //
-// One CTA takes 256 queries of one head as two tiles of 128 rows that share the key and value blocks.  Per
-// block and tile: S = Q K^T into tensor memory (tcgen05, both operands from shared memory), one thread per
-// row turns S into P (bf16, over the first half of S's columns), O += P V (tcgen05, P from tensor memory).
-// While the threads of one tile work on its P, the tensor core works for the other tile: of a block of 128
-// keys at d = 128 the products take 1024 clocks a tile and the 16,384 exponentials as many.  K and V come by
-// TMA into two-stage rings.  Widths up to 64 use blocks of 64 keys, so that two CTAs fit an SM (256 columns
-// of tensor memory and 96 KB each) and one's prologue and epilogue hide behind the other's work.
+// Work is cut into items of 256 queries of one head: two tiles of 128 rows that share the key and value
+// blocks.  Per block and tile: S = Q K^T into tensor memory (tcgen05, both operands from shared memory), one
+// thread per row turns S into P (bf16, into shared memory), O += P V (tcgen05).  P does not take S's place in
+// tensor memory: as soon as the threads hold S in registers the product for the next block may run, so that
+// neither the products nor the hand-offs lie on the threads' way.  (With P over S the threads waited 1600 of
+// 3100 clocks a block of 128 keys.  Blocks of 64 keys with two buffers of S were slower too: a product with
+// N = 64 reads as much of Q from shared memory as one with N = 128 and takes as long.)  At d = 128 the products
+// of a block of 128 keys take 1024 clocks a tile, the 16,384 exponentials 512.  Key and value blocks come by
+// TMA through one ring, in the order in which the products take them: K0, K1, V0, K2, V1, ...  CTAs are
+// persistent: the copies and the first products of the next item run while the rows of the last one are
+// finished.  Widths up to 64 with narrow windows take blocks of 64 keys and two CTAs an SM: their blocks are
+// few, and a chain of product, softmax and product is mostly latency.
 //
-// Warps 0-3 and 4-7: rows of tile 0 and 1; warp 8: MMAs; warp 9: copies; warp 10: looks at each value block
-// before it is used.  A value that a row does not see enters its product as 0 * v, which a NaN or an
+// Warps 0-3 and 4-7: rows of tile 0 and 1; warps 8 and 11: their MMAs; warp 9: copies; warp 10: looks at each
+// value block before it is used.  A value that a row does not see enters its product as 0 * v, which a NaN or an
 // infinity would spoil: rows of padding are overwritten with zeros in shared memory, and where a block that
-// is not seen as a whole holds other values that are not finite, the CTA computes its rows again, key by
+// is not seen as a whole holds other values that are not finite, the item's rows are computed again, key by
 // key, on the CUDA cores (a rare path: only the keys in a row's interval are touched there).
+//
+// Every wait is bounded.  One that expires sets the status word and a flag in shared memory, after which no
+// wait of the CTA lasts, no copy or product is issued and nothing is stored; the loops still run to their end.
+#include <algorithm>
 #include <mutex>
 
 #include "layers.cuh"
@@ -30,20 +39,41 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;                    // queries per tile
-constexpr int kThreads = 352;                 // 11 warps
-constexpr uint32_t kStages = 2;
+constexpr int kThreads = 384;                 // three warpgroups: rows of tile 0, of tile 1, and the rest
 constexpr float kGrowth = 8.f;                // log2 of how far P may exceed 1 before the output is scaled
+constexpr int kSMs = 152;
+// Windows up to this are narrow: blocks of 64 keys, two CTAs an SM.
+#ifndef KNARROW
+#define KNARROW 512
+#endif
+constexpr int64_t kNarrow = KNARROW;
 
-template <int DP>
+// DP: width padded to whole 64-column blocks; KB: keys per block
+template <int DP, int KB>
 struct Shape {
-  static constexpr int KB = DP == 64 ? 64 : 128;             // keys per block
+  static constexpr int kCtas = KB == 64 ? 2 : 1;             // per SM
+  static constexpr uint32_t kSlots = DP == 128 ? 3 : KB == 128 ? 6 : 5;  // of the ring of key and value blocks
   static constexpr uint32_t kBlk = DP / 64;                  // 64-column blocks per row
   static constexpr uint32_t kQTile = kRows * DP * 2;         // bytes
+  static constexpr uint32_t kPTile = kRows * KB * 2;
   static constexpr uint32_t kKTile = KB * DP * 2;
-  static constexpr uint32_t kOffK = 2 * kQTile, kOffV = kOffK + kStages * kKTile;
-  static constexpr uint32_t kSmem = kOffV + kStages * kKTile + 1024;  // + alignment of the base
-  static constexpr uint32_t kColO = 2 * KB, kTmemCols = 2 * KB + 2 * DP;
+  static constexpr uint32_t kOffP = 2 * kQTile, kOffR = kOffP + 2 * kPTile;
+  static constexpr uint32_t kSmem = kOffR + kSlots * kKTile + 1024;  // + alignment of the base
+  static_assert(kCtas * (kSmem + 2048) <= 228 * 1024, "");
+  static constexpr uint32_t kColO = 2 * KB, kTmemCols = kCtas == 2 ? 256 : 512;
+  static_assert(kColO + 2 * DP <= kTmemCols, "");
+  // The row threads take more registers than the launch gives a thread; the third warpgroup gives them up first.
+  static constexpr int kRegs = kCtas == 2 ? 80 : 168, kRegsRows = kCtas == 2 ? 96 : 208, kRegsRest = kCtas == 2 ? 48 : 88;
+  static_assert(2 * kRegsRows + kRegsRest <= 3 * kRegs, "");
 };
+
+// tanh(z) / z in z^2 on [0, 1] through six Chebyshev nodes: tanh is off by 4.5e-7 at most
+__device__ constexpr float kTanh[6] = {0.9999994040f, -0.3332895041f, 0.1328072101f, -0.0515859872f, 0.0167208556f, -0.0030582291f};
+
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t r[32];
@@ -59,6 +89,53 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Bounded wait without a sleep (the hand-offs lie on one chain); over at once when `dead` is set.
+__device__ __forceinline__ void mbar_spin(uint64_t* bar, uint32_t parity, volatile uint32_t* dead, unsigned* status) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !mbar_try_wait(smem_u32(bar), parity & 1u); ++n) {
+    if (n % 64 == 0) {
+      if (*dead) return;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      else if (t - t0 > kWaitLimitNs) {
+        *dead = 1;
+        atomicOr(status, kStatusTimeout);
+        return;
+      }
+    }
+  }
+}
+
+// Products and completions for a warp that runs as one, with the instruction itself left to one lane: inside a
+// branch of one lane every operand would have to be moved to a uniform register first, about 100 clocks a
+// product.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// Shared-memory descriptors in halves: the lower one holds the address (in units of 16 bytes) and the distance
+// between 64-column blocks, the upper one is the same for all: 1024 bytes between 8-row groups, version 1,
+// 128-byte swizzle.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t blocks_apart) { return ((addr & 0x3FFFFu) >> 4) | (blocks_apart >> 4) << 16; }
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate, uint32_t mine) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 x, {%1, %6};\n\tmov.b64 y, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(mine), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t mine) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(mine)
+      : "memory");
+}
+
 // 0 * x summed over the eight bf16 of a vector: NaN exactly where one of them is not finite
 __device__ __forceinline__ __nv_bfloat162 add_zero_times(uint4 u, __nv_bfloat162 acc) {
   const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
@@ -70,7 +147,7 @@ __device__ __forceinline__ __nv_bfloat162 add_zero_times(uint4 u, __nv_bfloat162
 
 // One row by one warp on the CUDA cores, reading only the keys of its interval.  Score in log2 units.
 template <bool CAP, bool BIAS>
-__device__ void slow_row(const SwaPrefillLaunch& a, int64_t b, int64_t h, int64_t hk, int64_t i, KeySpan sp, float slope2) {
+__device__ __noinline__ void slow_row(const SwaPrefillLaunch& a, int64_t b, int64_t h, int64_t hk, int64_t i, KeySpan sp, float slope2) {
   const int lane = threadIdx.x & 31;
   const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q.ptr) + b * a.q.sb + h * a.q.sh + i * a.q.st;
   const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(a.k.ptr) + b * a.k.sb + hk * a.k.sh;
@@ -115,53 +192,118 @@ __device__ void slow_row(const SwaPrefillLaunch& a, int64_t b, int64_t h, int64_
   }
 }
 
-template <int DP, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
+// The keys of 128 rows from i0 on, found by one warp (every lane gets them): [lo, hi) that some row sees, and
+// [f_lo, f_hi) that every row sees that sees any.  (The loops here stay rolled: the kernel's four roles each
+// have a copy, and code that every launch has to fetch costs small problems most.)
+struct TileSpan {
+  int lo, hi, f_lo, f_hi;
+};
+__device__ __forceinline__ TileSpan tile_span(const SwaPrefillLaunch& a, int b, int i0, int len) {
+  TileSpan t{INT32_MAX, 0, 0, INT32_MAX};
+#pragma unroll 1
+  for (int i = i0 + (threadIdx.x & 31); i < i0 + kRows; i += 32) {
+    const KeySpan s = key_span(a, b, i, len);
+    if (s.lo < s.hi) t = TileSpan{min(t.lo, s.lo), max(t.hi, s.hi), max(t.f_lo, s.lo), min(t.f_hi, s.hi)};
+  }
+  t.lo = __reduce_min_sync(kFullMask, t.lo);
+  t.hi = __reduce_max_sync(kFullMask, t.hi);
+  t.f_lo = __reduce_max_sync(kFullMask, t.f_lo);
+  t.f_hi = __reduce_min_sync(kFullMask, t.f_hi);
+  return t;
+}
+
+// An item: 256 queries of one head.
+struct Item {
+  int b, h, i0, len;
+  // The last queries see the most keys under the causal mask: items go from the last tiles to the first, and
+  // every other round of CTAs takes its items in reverse.  False: there is none, or its sequence is skipped.
+  __device__ __forceinline__ bool place(const SwaPrefillLaunch& a, int round, int items, int q_tiles, bool report) {
+    const int64_t at = (int64_t)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (at >= items) return false;
+    const int heads = (int)(a.B * a.H), bh = (int)at % heads;
+    i0 = (q_tiles - 1 - (int)at / heads) * (2 * kRows);
+    b = bh / (int)a.H;
+    h = bh - b * (int)a.H;
+    len = (int)sequence_length(a.lens, b, a.Nk, a.status, report && h == 0 && i0 == 0);
+    return len >= 0;
+  }
+};
+
+// The blocks of keys that an item's two tiles see.
+template <int KB>
+struct Blocks {
+  int jb[2], je[2];      // blocks [jb, je) of each tile
+  int f_lo[2], f_hi[2];
+  int j0, j1;            // and of both
+
+  __device__ __forceinline__ Blocks(const SwaPrefillLaunch& a, const Item& it) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const TileSpan s = tile_span(a, it.b, it.i0 + t * kRows, it.len);
+      jb[t] = s.lo < s.hi ? s.lo / KB : 0;
+      je[t] = s.lo < s.hi ? (s.hi + KB - 1) / KB : 0;
+      f_lo[t] = s.f_lo;
+      f_hi[t] = s.f_hi;
+    }
+    const bool any0 = jb[0] < je[0], any1 = jb[1] < je[1];
+    j0 = any0 && any1 ? min(jb[0], jb[1]) : any0 ? jb[0] : jb[1];
+    j1 = max(je[0], je[1]);
+  }
+  __device__ __forceinline__ bool active(int t, int j) const { return j >= jb[t] && j < je[t]; }
+  __device__ __forceinline__ bool active(int j) const { return active(0, j) || active(1, j); }
+  __device__ __forceinline__ int next(int j) const {  // the next block that a tile is at work on, or j1
+    do ++j; while (j < j1 && !active(j));
+    return j;
+  }
+  // whether all rows of the tiles at work on block j see all of it
+  __device__ __forceinline__ bool whole(int j) const {
+    const int k0 = j * KB, k1 = k0 + KB;
+    return (!active(0, j) || (k0 >= f_lo[0] && k1 <= f_hi[0])) && (!active(1, j) || (k0 >= f_lo[1] && k1 <= f_hi[1]));
+  }
+};
+
+template <int DP, int KB, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, Shape<DP, KB>::kCtas)
 swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-              const __grid_constant__ CUtensorMap map_v, const SwaPrefillLaunch a, int q_tiles) {
-  using S = Shape<DP>;
-  constexpr int KB = S::KB;
+              const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SwaPrefillLaunch a, int items, int q_tiles) {
+  using S = Shape<DP, KB>;
+  constexpr uint32_t kSlots = S::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t bar_q, bar_k[kStages], bar_v[kStages], bar_kfree[kStages], bar_vfree[kStages];
-  __shared__ uint64_t bar_vok[kStages];  // warp 10: the block holds what the products may read
-  __shared__ uint64_t bar_s[2], bar_p[2], bar_o[2], bar_fin;
+  __shared__ uint64_t bar_q, bar_qfree;                           // queries of an item: here; used up
+  __shared__ uint64_t bar_full[kSlots], bar_free[kSlots];         // of the ring
+  __shared__ uint64_t bar_vok[kSlots];                            // warp 10: a value block holds what the products may read
+  // per tile: S here, S read, P here, P V done, O read
+  __shared__ uint64_t bar_s[2], bar_sfree[2], bar_p[2], bar_o[2], bar_ofree[2];
+  __shared__ uint64_t bar_fin;
   __shared__ uint32_t tmem_base_sh;
-  __shared__ int r_lo[2], r_hi[2];       // keys that a tile's rows see: lowest lo, highest hi
-  __shared__ int f_lo[2], f_hi[2];       // keys that every row sees that sees any: highest lo, lowest hi
-  __shared__ int bad;                    // a block that is not seen as a whole holds a value that is not finite
+  __shared__ volatile uint32_t dead;
+  // bad[n % 8] == n + 1: item n of this CTA has values that are not finite in a block that is not seen as a
+  // whole.  Warp 10 is at most kSlots + 1 < 8 items ahead of the rows: a product of item n + 1 waits for the
+  // rows to have read the output of item n, and the ring holds kSlots blocks.
+  __shared__ volatile uint32_t bad[8];
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t heads = a.B * a.H;
-  const int64_t bh = blockIdx.x % heads;
-  // the last queries see the most keys under the causal mask: they start first
-  const int64_t i0 = (int64_t)(q_tiles - 1 - blockIdx.x / heads) * (2 * kRows);
-  const int64_t b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hkv);
-  const int64_t len = sequence_length(a.lens, b, a.Nk, a.status, h == 0 && i0 == 0 && tid == 0);
-  if (len < 0) return;  // uniform over the CTA
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(sm);
-
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bar_q), 1);
-    for (uint32_t s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&bar_k[s]), 1);
-      mbar_init(smem_u32(&bar_v[s]), 1);
-      mbar_init(smem_u32(&bar_kfree[s]), 1);
-      mbar_init(smem_u32(&bar_vfree[s]), 1);
+    mbar_init(smem_u32(&bar_qfree), 2);  // what both tiles use up: an arrival of each one's products
+    for (uint32_t s = 0; s < kSlots; ++s) {
+      mbar_init(smem_u32(&bar_full[s]), 1);
+      mbar_init(smem_u32(&bar_free[s]), 2);
       mbar_init(smem_u32(&bar_vok[s]), 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&bar_s[t]), 1);
-      mbar_init(smem_u32(&bar_p[t]), 4);  // one arrival per warp of the tile
+      mbar_init(smem_u32(&bar_sfree[t]), 4);  // one arrival per warp of the tile
+      mbar_init(smem_u32(&bar_p[t]), 4);
       mbar_init(smem_u32(&bar_o[t]), 1);
-      r_lo[t] = INT32_MAX;
-      r_hi[t] = 0;
-      f_lo[t] = 0;
-      f_hi[t] = INT32_MAX;
+      mbar_init(smem_u32(&bar_ofree[t]), 4);
     }
-    mbar_init(smem_u32(&bar_fin), 1);
+    mbar_init(smem_u32(&bar_fin), 2);
+    dead = 0;
+    for (int n = 0; n < 8; ++n) bad[n] = 0;
     fence_mbar_init();
-    bad = 0;
   }
   if (warp == 8) {
     tmem_alloc(smem_u32(&tmem_base_sh), S::kTmemCols);
@@ -172,296 +314,395 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
-  __syncthreads();
-  // thread t < 256 owns row i0 + t
-  KeySpan span{0, 0};
-  if (warp < 8) {
-    span = key_span(a, b, i0 + tid, len);
-    const bool any = span.lo < span.hi;
-    const int t = warp >> 2;
-    const int lo = __reduce_min_sync(kFullMask, any ? span.lo : INT32_MAX), hi = __reduce_max_sync(kFullMask, any ? span.hi : 0);
-    const int flo = __reduce_max_sync(kFullMask, any ? span.lo : 0), fhi = __reduce_min_sync(kFullMask, any ? span.hi : INT32_MAX);
-    if (lane == 0 && lo < hi) {
-      atomicMin(&r_lo[t], lo);
-      atomicMax(&r_hi[t], hi);
-      atomicMax(&f_lo[t], flo);
-      atomicMin(&f_hi[t], fhi);
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
-  // blocks [jb, je) of each tile, and of both
-  int jb[2], je[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const bool any = r_lo[t] < r_hi[t];
-    jb[t] = any ? r_lo[t] / KB : 0;
-    je[t] = any ? (r_hi[t] + KB - 1) / KB : 0;
-  }
-  const bool any0 = jb[0] < je[0], any1 = jb[1] < je[1];
-  const int J0 = any0 && any1 ? min(jb[0], jb[1]) : any0 ? jb[0] : jb[1];
-  const int J1 = max(je[0], je[1]);
-  auto active = [&](int t, int j) { return j >= jb[t] && j < je[t]; };
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(smem_u32(bar), parity, a.status); };
-  // waits of a whole warp whose lanes leave together
-  auto wwait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFullMask, wait(bar, parity)); };
-  // stage and parity of the i-th block that passes through a ring
-  auto stage = [](uint32_t i) { return i % kStages; };
-  auto phase = [](uint32_t i) { return (i / kStages) & 1u; };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { mbar_spin(bar, parity, &dead, a.status); };
+  // slot and phase of the i-th block that passes through the ring
+  auto slot = [](uint32_t i) { return i % kSlots; };
+  auto phase = [](uint32_t i) { return i / kSlots; };
+  const int group = (int)(a.H / a.Hkv);
+  const int rounds = (items + (int)gridDim.x - 1) / (int)gridDim.x;
+  Item it;
 
-  if (warp == 9) {
-    // ================================================================ copies
-    uint32_t i = 0;
-    bool ok = true;
-    if (J0 < J1 && lane == 0) {
-      mbar_arrive_expect_tx(smem_u32(&bar_q), 2 * S::kQTile);
-      for (int t = 0; t < 2; ++t)
-        for (uint32_t c = 0; c < S::kBlk; ++c)
-          tma_load_4d(sbase + t * S::kQTile + c * (kRows * 128), &map_q, c * 64, (int)i0 + t * kRows, (int)h, (int)b, smem_u32(&bar_q));
-    }
-    for (int j = J0; j < J1 && ok; ++j) {
-      if (!active(0, j) && !active(1, j)) continue;
-      const uint32_t s = stage(i);
-      if (i >= kStages) ok = wwait(&bar_kfree[s], phase(i - kStages));
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(smem_u32(&bar_k[s]), S::kKTile);
-        for (uint32_t c = 0; c < S::kBlk; ++c)
-          tma_load_4d(sbase + S::kOffK + s * S::kKTile + c * (KB * 128), &map_k, c * 64, j * KB, (int)hk, (int)b, smem_u32(&bar_k[s]));
-      }
-      if (i >= kStages) ok = wwait(&bar_vfree[s], phase(i - kStages));
-      if (!ok) {
-        wwait(&bar_k[s], phase(i));  // the copy in flight lands before the CTA ends
-        break;
-      }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(smem_u32(&bar_v[s]), S::kKTile);
-        for (uint32_t c = 0; c < S::kBlk; ++c)
-          tma_load_4d(sbase + S::kOffV + s * S::kKTile + c * (KB * 128), &map_v, c * 64, j * KB, (int)hk, (int)b, smem_u32(&bar_v[s]));
-      }
-      __syncwarp();
-      ++i;
-    }
-    // nobody may be left to wait for the last blocks after an expired wait elsewhere: their copies land here
-    for (uint32_t k = i > kStages ? i - kStages : 0; k < i; ++k) {
-      wwait(&bar_k[stage(k)], phase(k));
-      wwait(&bar_v[stage(k)], phase(k));
-    }
-    if (J0 < J1) wwait(&bar_q, 0);
-  } else if (warp == 10) {
-    // ================================================================ a look at each value block
-    uint32_t i = 0;
-    bool ok = true;
-    for (int j = J0; j < J1 && ok; ++j) {
-      const bool on0 = active(0, j), on1 = active(1, j);
-      if (!on0 && !on1) continue;
-      const uint32_t s = stage(i);
-      ok = wwait(&bar_v[s], phase(i));
-      if (!ok) break;
-      uint8_t* v = sm + S::kOffV + s * S::kKTile;
-      const int k0 = j * KB, k1 = k0 + KB;
-      if (k1 > len) {  // rows of padding (TMA has zeroed those behind the last key only)
-        for (int e = lane; e < (int)(S::kBlk * KB * 8); e += 32) {
-          const int row = e / 8 % KB;
-          if (k0 + row >= len) *reinterpret_cast<uint4*>(v + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+  if (warp >= 8) {
+    regs_dec<S::kRegsRest>();
+    if (warp == 9) {
+      // ================================================================ copies: one thread
+      uint32_t i = 0, n = 0;
+      for (int r = 0; r < rounds; ++r) {
+        if (!it.place(a, r, items, q_tiles, false)) continue;
+        const Blocks<KB> bl(a, it);
+        if (bl.j0 >= bl.j1) continue;
+        if (lane == 0) {
+          if (n > 0) wait(&bar_qfree, n - 1);
+          if (!dead) {
+            mbar_arrive_expect_tx(smem_u32(&bar_q), 2 * S::kQTile);
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t)
+#pragma unroll 1
+              for (uint32_t c = 0; c < S::kBlk; ++c)
+                tma_load_4d(sbase + t * S::kQTile + c * (kRows * 128), &map_q, c * 64, it.i0 + t * kRows, it.h, it.b, smem_u32(&bar_q));
+            ++n;
+          }
+          auto load = [&](const CUtensorMap* map, int j) {
+            const uint32_t s = slot(i);
+            if (i >= kSlots) wait(&bar_free[s], phase(i - kSlots));
+            if (dead) return;
+            mbar_arrive_expect_tx(smem_u32(&bar_full[s]), S::kKTile);
+#pragma unroll 1
+            for (uint32_t c = 0; c < S::kBlk; ++c)
+              tma_load_4d(sbase + S::kOffR + s * S::kKTile + c * (KB * 128), map, c * 64, j * KB, it.h / group, it.b, smem_u32(&bar_full[s]));
+            ++i;
+          };
+          // keys a block ahead of values
+          for (int jk = bl.j0, jv = bl.j0; jv < bl.j1;) {
+            const bool keys = jk < bl.j1 && jk <= bl.next(jv);
+            load(keys ? &map_k : &map_v, keys ? jk : jv);
+            if (keys) jk = bl.next(jk);
+            else jv = bl.next(jv);
+          }
         }
-        fence_proxy_async_smem();
         __syncwarp();
       }
-      const bool whole = (!on0 || (k0 >= f_lo[0] && k1 <= f_hi[0])) && (!on1 || (k0 >= f_lo[1] && k1 <= f_hi[1]));
-      if (!whole) {
-        __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll 8
-        for (int e = lane; e < (int)(S::kBlk * KB * 8); e += 32) acc = add_zero_times(*reinterpret_cast<const uint4*>(v + e * 16), acc);
-        if (__any_sync(kFullMask, __hisnan(acc.x) || __hisnan(acc.y)) && lane == 0) bad = 1;
+      if (lane == 0) {  // the last copies land before the CTA ends, whatever became of those that use them
+        for (uint32_t k = i > kSlots ? i - kSlots : 0; k < i; ++k) mbar_wait(smem_u32(&bar_full[slot(k)]), phase(k) & 1u, a.status);
+        if (n > 0) mbar_wait(smem_u32(&bar_q), (n - 1) & 1u, a.status);
       }
-      warp_arrive(smem_u32(&bar_vok[s]));
-      ++i;
-    }
-  } else if (warp == 8) {
-    // ================================================================ products
-    // Order: per block, tile 0 then tile 1: O += P V of the block before, then S = Q K^T of this one over
-    // the same columns.  Products of one thread run in order, so S follows the reads of P, and the
-    // completion that announces S covers the products before it.
-    const uint32_t id_s = idesc_bf16(kRows, KB, 0, 0), id_o = idesc_bf16(kRows, DP, 0, 1);
-    bool ok = J0 >= J1 || wwait(&bar_q, 0);
-    bool issued = false;
-    uint32_t i = 0, np[2] = {0u, 0u};
-    bool have_prev = false;
-    for (int j = J0; j <= J1 && ok; ++j) {
-      const bool cur = j < J1 && (active(0, j) || active(1, j));
-      if (!cur && !have_prev) continue;
-      const uint32_t s = stage(i), sp = stage(i - 1);
-      if (cur) {
-        ok = wwait(&bar_k[s], phase(i));
-        if (!ok) break;
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (have_prev && active(t, j - 1)) {
-          ok = ok && wwait(&bar_p[t], np[t] & 1u) && wwait(&bar_vok[sp], phase(i - 1));
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t v = sbase + S::kOffV + sp * S::kKTile;
-#pragma unroll
-            for (int ks = 0; ks < KB / 16; ++ks)
-              mma_bf16_ts(tmem + S::kColO + t * DP, tmem + t * KB + 8 * ks, sw128_desc(v + ks * 2048, KB * 128, 1024), id_o,
-                          (np[t] > 0 || ks > 0) ? 1u : 0u);
-            if (j == je[t]) mma_commit(smem_u32(&bar_o[t]));
+      __syncwarp();
+    } else if (warp == 10) {
+      // ================================================================ a look at each value block
+      uint32_t i = 0, iv = 0, n = 0;
+      for (int r = 0; r < rounds; ++r) {
+        if (!it.place(a, r, items, q_tiles, lane == 0)) continue;
+        const Blocks<KB> bl(a, it);
+        ++n;
+        if (bl.j0 < bl.j1) ++i;  // the first block of keys
+        for (int j = bl.j0, after; j < bl.j1; j = after) {
+          after = bl.next(j);
+          if (after < bl.j1) ++i;  // the next block of keys
+          wait(&bar_full[slot(i)], phase(i));
+          __syncwarp();
+          uint8_t* v = sm + S::kOffR + slot(i) * S::kKTile;
+          if ((j + 1) * KB > it.len) {  // rows of padding (TMA has zeroed those behind the last key only)
+            for (int e = lane; e < (int)(S::kBlk * KB * 8); e += 32)
+              if (j * KB + e / 8 % KB >= it.len) *reinterpret_cast<uint4*>(v + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
           }
-          ++np[t];
-          issued = true;
+          if (!bl.whole(j)) {
+            __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll 4
+            for (int e = lane; e < (int)(S::kBlk * KB * 8); e += 32) acc = add_zero_times(*reinterpret_cast<const uint4*>(v + e * 16), acc);
+            if (__any_sync(kFullMask, __hisnan(acc.x) || __hisnan(acc.y)) && lane == 0) bad[(n - 1) % 8] = n;
+          }
+          warp_arrive(smem_u32(&bar_vok[slot(iv)]));
+          ++i;
+          ++iv;
         }
-        if (cur && active(t, j)) {
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t q = sbase + t * S::kQTile, k = sbase + S::kOffK + s * S::kKTile;
+      }
+    } else {
+      // ================================================================ products: warp 8 of tile 0, warp 11 of tile 1
+      // S = Q K^T a block ahead of O += P V.  Both warps pass through every block, also where only one has work,
+      // so that a block counts as used up once for each.
+      const int t = warp == 8 ? 0 : 1;
+      const uint32_t id_s = idesc_bf16(kRows, KB, 0, 0), id_o = idesc_bf16(kRows, DP, 0, 1);
+      const uint32_t mine = elect_one();
+      uint32_t i = 0, iv = 0, n = 0;         // blocks and value blocks used, items
+      uint32_t ns = 0, np = 0, no = 0;       // S issued, P used, outputs begun
+      const uint32_t q_lo = desc_lo(sbase + t * S::kQTile, 0), p_lo = desc_lo(sbase + S::kOffP + t * S::kPTile, 0);
+      const uint32_t s_col = tmem + t * KB, o_col = tmem + S::kColO + t * DP;
+      for (int r = 0; r < rounds; ++r) {
+        if (!it.place(a, r, items, q_tiles, false)) continue;
+        const Blocks<KB> bl(a, it);
+        if (bl.j0 >= bl.j1) continue;
+        const int jb = t ? bl.jb[1] : bl.jb[0], je = t ? bl.je[1] : bl.je[0];
+        wait(&bar_q, n);
+        auto step_s = [&](int j) {
+          wait(&bar_full[slot(i)], phase(i));
+          if (j >= jb && j < je) {
+            if (ns > 0) wait(&bar_sfree[t], ns - 1);  // the rows hold the last S in registers
+            tc_fence_after();
+            const uint32_t k_lo = desc_lo(sbase + S::kOffR + slot(i) * S::kKTile, 0);
 #pragma unroll
             for (int ks = 0; ks < DP / 16; ++ks) {
               const uint32_t blk = ks >> 2, in = (ks & 3) * 32;
-              mma_bf16(tmem + t * KB, sw128_desc(q + blk * (kRows * 128) + in, 0, 1024), sw128_desc(k + blk * (KB * 128) + in, 0, 1024),
-                       id_s, ks > 0);
+              mma_ss(s_col, q_lo + (blk * (kRows * 128) + in) / 16, k_lo + (blk * (KB * 128) + in) / 16, id_s, ks > 0, mine);
             }
-            mma_commit(smem_u32(&bar_s[t]));
+            commit(&bar_s[t], mine);
+            ++ns;
           }
-          issued = true;
+          commit(&bar_free[slot(i)], mine);
+          if (j == bl.j1 - 1) commit(&bar_qfree, mine);
+          ++i;
+        };
+        bool ahead = false;
+        for (int j = bl.j0, jq = bl.j0; j < bl.j1;) {
+          if (jq < bl.j1) {
+            step_s(jq);
+            jq = bl.next(jq);
+          }
+          if (!ahead) {  // the first S alone
+            ahead = true;
+            continue;
+          }
+          wait(&bar_vok[slot(iv)], phase(iv));
+          if (j >= jb && j < je) {
+            const bool begin = j == jb;
+            if (begin && no > 0) wait(&bar_ofree[t], no - 1);  // the rows have read the last item's output
+            wait(&bar_p[t], np);
+            tc_fence_after();
+            const uint32_t v_lo = desc_lo(sbase + S::kOffR + slot(i) * S::kKTile, KB * 128);
+#pragma unroll
+            for (int ks = 0; ks < KB / 16; ++ks) {
+              const uint32_t blk = ks >> 2, in = (ks & 3) * 32;
+              mma_ss(o_col, p_lo + (blk * (kRows * 128) + in) / 16, v_lo + ks * 2048 / 16, id_o, (!begin || ks > 0) ? 1u : 0u, mine);
+            }
+            commit(&bar_o[t], mine);
+            ++np;
+            if (j == je - 1) ++no;
+          }
+          commit(&bar_free[slot(i)], mine);
+          ++i;
+          ++iv;
+          j = bl.next(j);
         }
+        ++n;
       }
-      if (!ok) break;
-      if (lane == 0) {
-        if (have_prev) mma_commit(smem_u32(&bar_vfree[sp]));
-        if (cur) mma_commit(smem_u32(&bar_kfree[s]));
-      }
+      // every product has completed before tensor memory is given back
+      commit(&bar_fin, mine);
       __syncwarp();
-      if (cur) ++i;
-      have_prev = cur;
-    }
-    if (issued) {  // every product has completed before tensor memory is given back
-      if (lane == 0) mma_commit(smem_u32(&bar_fin));
+      mbar_wait(smem_u32(&bar_fin), 0, a.status);
       __syncwarp();
-      wwait(&bar_fin, 0);
     }
   } else {
     // ================================================================ one thread per row
+    regs_inc<S::kRegsRows>();
     const int t = warp >> 2;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t col_s = tl + t * KB, col_o = tl + S::kColO + t * DP;
-    const int64_t i = i0 + tid;
-    const int pos = (int)(a.q_pos0 + i);
+    uint8_t* p_tile = sm + S::kOffP + t * S::kPTile;
+    const uint32_t p_row = threadIdx.x % kRows;
+    const uint32_t cs = tl + t * KB, col_o = tl + S::kColO + t * DP;
     const float c1 = CAP ? a.scale / a.softcap * (2.f * kLog2e) : a.scale * kLog2e;
     const float capl = a.softcap * kLog2e;
-    const float slope2 = BIAS ? a.slopes[h] * kLog2e : 0.f;
-    float m = -INFINITY, l = 0.f;
-    uint32_t n = 0;
-    bool ok = true;
-    for (int j = jb[t]; j < je[t]; ++j, ++n) {
-      ok = ok && wait(&bar_s[t], n & 1u);
-      __syncwarp();
-      tc_fence_after();
-      float x[KB];
-#pragma unroll
-      for (int c = 0; c < KB; c += 32) tmem_ld32(col_s + c, x + c);
-      tmem_ld_wait();
-      const int k0 = j * KB;
-#pragma unroll
-      for (int c = 0; c < KB; ++c) {
-        if constexpr (CAP) x[c] = fmaf(-2.f * capl, rcp(1.f + ex2(x[c] * c1)), capl);  // cap tanh(y) = cap - 2 cap / (1 + e^2y)
-        else x[c] *= c1;
-      }
-      if constexpr (BIAS) {
-        const float dist = (float)(pos - k0);
-#pragma unroll
-        for (int c = 0; c < KB; ++c) x[c] = fmaf(-slope2, fabsf(dist - (float)c), x[c]);
-      }
-      const int va = span.lo - k0, vb = span.hi - k0;  // columns va <= c < vb are seen
-      if (!__all_sync(kFullMask, va <= 0 && vb >= KB)) {
-#pragma unroll
-        for (int c = 0; c < KB; ++c) x[c] = c >= va && c < vb ? x[c] : -INFINITY;
-      }
-      float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-      for (int c = 4; c < KB; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
-      const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      if (m == -INFINITY) {
-        m = mn;  // nothing seen before: the output holds zeros, or nothing yet
-      }
-      const bool grow = mn > m + kGrowth;
-      if (__any_sync(kFullMask, grow)) {
-        // S of this block was announced after P V of the block before: the output is at rest
-        const float f = grow ? ex2(m - mn) : 1.f;
-        if (grow) m = mn;
-        l *= f;
-        if (n > 0) {
-#pragma unroll
-          for (int c = 0; c < DP; c += 16) {
-            float o[16];
-            tmem_ld16(col_o + c, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= f;
-            tmem_st16(col_o + c, o);
-          }
-        }
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < KB; c += 32) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float p0 = ex2(x[c + e] - base), p1 = ex2(x[c + e + 1] - base);
-          sum[e & 3] += p0;
-          sum[(e & 3) + 1] += p1;
-          w[e / 2] = pack2_bf16(p0, p1);
-        }
-        tmem_st16u(col_s + c / 2, w);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st_wait();
-      tc_fence_before();
-      warp_arrive(smem_u32(&bar_p[t]));
-    }
-    if (n > 0) {
-      ok = ok && wait(&bar_o[t], 0);
-      __syncwarp();
-      tc_fence_after();
-    }
-    const bool stored = ok && i < a.Nq && a.q_pos0 + i < len;
-    const bool seen = l != 0.f;  // also a row whose sum is NaN
-    const float inv = seen ? 1.f / l : 0.f;
-    const int64_t at = b * a.o_sb + h * a.o_sh + i * a.o_st;
     const bool al32 = ((reinterpret_cast<uintptr_t>(a.o) | (uintptr_t)((a.o_sb | a.o_sh | a.o_st) * (a.out_bf16 ? 2 : 4))) & 31u) == 0;
+    uint32_t ns = 0, n = 0;  // blocks, items
+    for (int round = 0; round < rounds; ++round) {
+      if (!it.place(a, round, items, q_tiles, false)) continue;
+      ++n;
+      const int i = it.i0 + (int)threadIdx.x;
+      const KeySpan span = key_span(a, it.b, i, it.len);
+      const TileSpan ts = tile_span(a, it.b, it.i0 + t * kRows, it.len);
+      const int jb = ts.lo < ts.hi ? ts.lo / KB : 0, je = ts.lo < ts.hi ? (ts.hi + KB - 1) / KB : 0;
+      const int pos = (int)a.q_pos0 + i;
+      const float slope2 = BIAS && a.slopes ? a.slopes[it.h] * kLog2e : 0.f;
+      // The running maximum: of the raw products where a score grows with them (no bias), else of the scores.
+      float m = -INFINITY, l = 0.f;
+      for (int j = jb; j < je; ++j, ++ns) {
+        wait(&bar_s[t], ns);
+        __syncwarp();
+        tc_fence_after();
+        const int k0 = j * KB;
+        const int va = span.lo - k0, vb = span.hi - k0;  // columns va <= c < vb are seen
+        const bool all_seen = __all_sync(kFullMask, va <= 0 && vb >= KB);
+        // With two CTAs an SM the registers hold half a row at a time, read once for the maximum and once more
+        // for the weights.
+        constexpr int kHold = S::kCtas == 2 ? 32 : KB;
+        float x[kHold];
+        auto read = [&](int c0) {  // kHold columns: products, or scores where there is a bias
 #pragma unroll
-    for (int c = 0; c < DP; c += 16) {
-      float o[16];
-      if (n > 0) {
-        tmem_ld16(col_o + c, o);
-        tmem_ld_wait();
-      }
+          for (int c = 0; c < kHold; c += 32) tmem_ld32(cs + c0 + c, x + c);
+          tmem_ld_wait();
+          if constexpr (BIAS) {
+            const float dist = (float)(pos - k0 - c0);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] = seen ? o[e] * inv : 0.f;
-      if (stored && c < a.d) {
-        const bool two = c + 8 < a.d;  // d is a multiple of 8
-        if (a.out_bf16) {
-          __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.o) + at + c;
-          const uint4 lo8 = pack8_bf16(o), hi8 = pack8_bf16(o + 8);
-          if (two && al32) {
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(lo8.x), "r"(lo8.y), "r"(lo8.z),
-                         "r"(lo8.w), "r"(hi8.x), "r"(hi8.y), "r"(hi8.z), "r"(hi8.w)
-                         : "memory");
-          } else {
-            *reinterpret_cast<uint4*>(p) = lo8;
-            if (two) *reinterpret_cast<uint4*>(p + 8) = hi8;
+            for (int c = 0; c < kHold; ++c) {
+              if constexpr (CAP) x[c] = fmaf(-2.f * capl, rcp(1.f + ex2(x[c] * c1)), capl);
+              else x[c] *= c1;
+              x[c] = fmaf(-slope2, fabsf(dist - (float)c), x[c]);
+            }
           }
-        } else {
-          float* p = reinterpret_cast<float*>(a.o) + at + c;
+          if (!all_seen) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            if (e < 8 || two) *reinterpret_cast<float4*>(p + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int c = 0; c < kHold; ++c) x[c] = c0 + c >= va && c0 + c < vb ? x[c] : -INFINITY;
+          }
+        };
+        auto s_read = [&]() {  // the product for the next block may take S's place
+          tc_fence_before();
+          warp_arrive(smem_u32(&bar_sfree[t]));
+        };
+        float mn = -INFINITY;
+        [[maybe_unused]] float low = INFINITY;
+#pragma unroll
+        for (int c0 = 0; c0 < KB; c0 += kHold) {
+          read(c0);
+          if (kHold == KB) s_read();
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int c = 4; c < kHold; c += 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = c + 4 + e < kHold ? fmaxf(fmaxf(mx[e], x[c + e]), x[c + 4 + e]) : fmaxf(mx[e], x[c + e]);
+          }
+          mn = fmaxf(mn, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          if constexpr (CAP && !BIAS) {
+            float lo[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int c = 4; c < kHold; ++c) lo[c & 3] = fminf(lo[c & 3], x[c]);
+            low = fminf(low, fminf(fminf(lo[0], lo[1]), fminf(lo[2], lo[3])));
+          }
+        }
+        // the scores stay within the cap's straight part: no row of the warp has |scale q.k| > cap
+        [[maybe_unused]] const bool small = CAP && !BIAS && __all_sync(kFullMask, fmaxf(mn, -low) * c1 <= 2.f * kLog2e);
+        if constexpr (!BIAS) {  // to log2 units: the scale is positive here and tanh grows
+          if (mn != -INFINITY) mn = CAP ? fmaf(-2.f * capl, rcp(1.f + ex2(mn * c1)), capl) : mn * c1;
+        }
+        // The products of the block before: P's place is free and the output at rest behind them.
+        bool o_rests = j == jb;
+        auto wait_o = [&]() {
+          if (!o_rests) {
+            wait(&bar_o[t], ns - 1);
+            __syncwarp();
+            tc_fence_after();
+          }
+          o_rests = true;
+        };
+        if (m == -INFINITY) m = mn;  // nothing seen before: the output holds zeros, or nothing yet
+        const bool grow = mn > m + kGrowth;
+        if (__any_sync(kFullMask, grow)) {
+          const float f = grow ? ex2(m - mn) : 1.f;
+          if (grow) m = mn;
+          l *= f;
+          wait_o();
+          if (j > jb) {
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 16) {
+              float o[16];
+              tmem_ld16(col_o + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= f;
+              tmem_st16(col_o + c, o);
+            }
+          }
+        }
+        // ---- P in registers, and into its place once that is free
+        const float base = m == -INFINITY ? 0.f : m;
+        const f32x2 base2 = pack2(-base, -base), c2 = pack2(c1, c1);
+        f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+        uint32_t w[KB / 2];
+#pragma unroll
+        for (int c = 0; c < KB; c += 32) {
+          if (kHold < KB) {
+            read(c);
+            if (c + kHold == KB) s_read();
+          }
+          const float* xs = x + c % kHold;
+          f32x2 y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = pack2(xs[2 * e], xs[2 * e + 1]);
+          if constexpr (BIAS) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = add2(y[e], base2);
+          } else if constexpr (CAP) {
+            if (small) {
+              // tanh(z) = z P(z^2) for |z| <= 1 with the quintic P through the six Chebyshev nodes of [0, 1]
+              const f32x2 zc = pack2(0.5f * c1 / kLog2e, 0.5f * c1 / kLog2e), capz = pack2(capl * 0.5f * c1 / kLog2e, capl * 0.5f * c1 / kLog2e);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const f32x2 z = mul2(y[e], zc), u = mul2(z, z);
+                f32x2 q = fma2(pack2(kTanh[5], kTanh[5]), u, pack2(kTanh[4], kTanh[4]));
+#pragma unroll
+                for (int k = 3; k >= 0; --k) q = fma2(q, u, pack2(kTanh[k], kTanh[k]));
+                y[e] = fma2(mul2(y[e], capz), q, base2);
+              }
+            } else {  // cap tanh(z) = cap - 2 cap / (1 + e^2z); a masked product, -infinity, goes there again
+              const f32x2 cap2 = pack2(-2.f * capl, -2.f * capl), off2 = pack2(capl - base, capl - base), one2 = pack2(1.f, 1.f);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float z0, z1, p0, p1;
+                unpack2(mul2(y[e], c2), z0, z1);
+                unpack2(add2(pack2(ex2(z0), ex2(z1)), one2), z0, z1);
+                unpack2(fma2(pack2(rcp(z0), rcp(z1)), cap2, off2), p0, p1);
+                y[e] = pack2(xs[2 * e] == -INFINITY ? -INFINITY : p0, xs[2 * e + 1] == -INFINITY ? -INFINITY : p1);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = fma2(y[e], c2, base2);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const f32x2 p2 = ex2_2(y[e]);
+            sum[e & 1] = add2(sum[e & 1], p2);
+            float p0, p1;
+            unpack2(p2, p0, p1);
+            w[c / 2 + e] = pack2_bf16(p0, p1);
+          }
+        }
+        float s0, s1;
+        unpack2(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+        wait_o();
+#pragma unroll
+        for (int e = 0; e < KB / 8; ++e)
+          *reinterpret_cast<uint4*>(p_tile + sw128_off(p_row, 8 * e, kRows)) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        tmem_st_wait();  // of a scaled output
+        fence_proxy_async_smem();
+        tc_fence_before();
+        warp_arrive(smem_u32(&bar_p[t]));
+      }
+      bool again = false;
+      if (jb < je) {
+        wait(&bar_o[t], ns - 1);
+        __syncwarp();
+        tc_fence_after();
+        again = bad[(n - 1) % 8] == n;
+      }
+      const bool live = i < a.Nq && a.q_pos0 + i < it.len && !dead;
+      const bool seen = l != 0.f;  // also a row whose sum is NaN
+      const float inv = seen ? 1.f / l : 0.f;
+      const int64_t at = (int64_t)it.b * a.o_sb + (int64_t)it.h * a.o_sh + (int64_t)i * a.o_st;
+#pragma unroll 1
+      for (int c = 0; c < DP; c += 16) {
+        float o[16];
+        if (jb < je) {
+          tmem_ld16(col_o + c, o);
+          tmem_ld_wait();
+          if (c + 16 == DP) {  // the output is in registers: the next item's may be begun
+            tc_fence_before();
+            warp_arrive(smem_u32(&bar_ofree[t]));
+          }
+        }
+        if (live && !again && c < a.d) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = seen ? o[e] * inv : 0.f;
+          const bool two = c + 8 < a.d;  // d is a multiple of 8
+          if (a.out_bf16) {
+            __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.o) + at + c;
+            const uint4 u = pack8_bf16(o), v = pack8_bf16(o + 8);
+            if (two && al32) {
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u.x), "r"(u.y), "r"(u.z),
+                           "r"(u.w), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                           : "memory");
+            } else {
+              *reinterpret_cast<uint4*>(p) = u;
+              if (two) *reinterpret_cast<uint4*>(p + 8) = v;
+            }
+          } else {
+            float* p = reinterpret_cast<float*>(a.o) + at + c;
+#pragma unroll
+            for (int k = 0; k < 16; k += 4)
+              if (k < 8 || two) *reinterpret_cast<float4*>(p + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          }
+        }
+      }
+      if (again) {  // the rows of this warp once more, from their own keys only
+#pragma unroll 1
+        for (int r = 0; r < 32; ++r) {
+          const int row = it.i0 + warp * 32 + r;
+          const KeySpan sp{__shfl_sync(kFullMask, span.lo, r), __shfl_sync(kFullMask, span.hi, r)};
+          if (row < a.Nq && a.q_pos0 + row < it.len) slow_row<CAP, BIAS>(a, it.b, it.h, it.h / group, row, sp, slope2);
         }
       }
     }
@@ -469,15 +710,6 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   tc_fence_before();
   __syncthreads();
   if (warp == 8) tmem_dealloc(tmem, S::kTmemCols);
-  if (bad && warp < 8) {
-    // the rows again, a warp at a time, from their own keys only
-    const float slope2 = BIAS ? a.slopes[h] * kLog2e : 0.f;
-    for (int r = 0; r < 32; ++r) {
-      const int64_t i = i0 + warp * 32 + r;
-      const KeySpan sp{__shfl_sync(kFullMask, span.lo, r), __shfl_sync(kFullMask, span.hi, r)};
-      if (i < a.Nq && a.q_pos0 + i < len) slow_row<CAP, BIAS>(a, b, h, hk, i, sp, slope2);
-    }
-  }
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -513,36 +745,45 @@ bool encode(CUtensorMap* map, const View4& x, int64_t B, int64_t H, int64_t N, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DP, bool CAP, bool BIAS>
+template <int DP, int KB, bool CAP, bool BIAS>
 cudaError_t launch_typed(const SwaPrefillLaunch& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+  using S = Shape<DP, KB>;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(swa_tc_kernel<DP, CAP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<DP>::kSmem);
+    attr = cudaFuncSetAttribute(swa_tc_kernel<DP, KB, CAP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    // the row threads' registers come out of the launch's own: with fewer they would be waited for without end
+    cudaFuncAttributes f{};
+    if (attr == cudaSuccess) attr = cudaFuncGetAttributes(&f, swa_tc_kernel<DP, KB, CAP, BIAS>);
+    if (attr == cudaSuccess && f.numRegs < S::kRegs) attr = cudaErrorInvalidConfiguration;
   });
   if (attr != cudaSuccess) return attr;
   const int q_tiles = (int)((a.Nq + 2 * kRows - 1) / (2 * kRows));
-  swa_tc_kernel<DP, CAP, BIAS><<<(unsigned)(a.B * a.H * q_tiles), kThreads, Shape<DP>::kSmem, stream>>>(q, k, v, a, q_tiles);
+  const int64_t items = a.B * a.H * q_tiles;
+  const unsigned grid = (unsigned)std::min<int64_t>(items, S::kCtas * kSMs);
+  swa_tc_kernel<DP, KB, CAP, BIAS><<<grid, kThreads, S::kSmem, stream>>>(q, k, v, a, (int)items, q_tiles);
   return cudaGetLastError();
 }
 
-template <int DP>
+template <int DP, int KB>
 cudaError_t launch_width(const SwaPrefillLaunch& a, cudaStream_t stream) {
   CUtensorMap q, k, v;
-  if (!encode(&q, a.q, a.B, a.H, a.Nq, a.d, kRows) || !encode(&k, a.k, a.B, a.Hkv, a.Nk, a.d, Shape<DP>::KB) ||
-      !encode(&v, a.v, a.B, a.Hkv, a.Nk, a.d, Shape<DP>::KB))
+  if (!encode(&q, a.q, a.B, a.H, a.Nq, a.d, kRows) || !encode(&k, a.k, a.B, a.Hkv, a.Nk, a.d, KB) ||
+      !encode(&v, a.v, a.B, a.Hkv, a.Nk, a.d, KB))
     return cudaErrorNotSupported;  // strides that TMA cannot describe
-  const bool cap = a.softcap != 0.f, bias = a.slopes != nullptr;
-  if (cap && bias) return launch_typed<DP, true, true>(a, q, k, v, stream);
-  if (cap) return launch_typed<DP, true, false>(a, q, k, v, stream);
-  if (bias) return launch_typed<DP, false, true>(a, q, k, v, stream);
-  return launch_typed<DP, false, false>(a, q, k, v, stream);
+  // without a bias the running maximum is taken of the raw products, which the scale must not turn round
+  const bool cap = a.softcap != 0.f, bias = a.slopes != nullptr || !(a.scale > 0.f);
+  if (cap && bias) return launch_typed<DP, KB, true, true>(a, q, k, v, stream);
+  if (cap) return launch_typed<DP, KB, true, false>(a, q, k, v, stream);
+  if (bias) return launch_typed<DP, KB, false, true>(a, q, k, v, stream);
+  return launch_typed<DP, KB, false, false>(a, q, k, v, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_swa_prefill_tc(const SwaPrefillLaunch& a, cudaStream_t stream) {
-  return a.d <= 64 ? launch_width<64>(a, stream) : launch_width<128>(a, stream);
+  if (a.d > 64) return launch_width<128, 128>(a, stream);
+  return a.window > 0 && a.window <= kNarrow ? launch_width<64, 64>(a, stream) : launch_width<64, 128>(a, stream);
 }
 
 }  // namespace la
