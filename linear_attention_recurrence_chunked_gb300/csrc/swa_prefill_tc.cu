@@ -67,8 +67,9 @@ struct Shape {
   static_assert(2 * kRegsRows + kRegsRest <= 3 * kRegs, "");
 };
 
-// tanh(z) / z in z^2 on [0, 1] through six Chebyshev nodes: tanh is off by 4.5e-7 at most
-__device__ constexpr float kTanh[6] = {0.9999994040f, -0.3332895041f, 0.1328072101f, -0.0515859872f, 0.0167208556f, -0.0030582291f};
+// tanh(z) / z in z^2 on [0, 1/4] through four Chebyshev nodes: tanh is off by 3e-7 at most for |z| <= 1/2
+constexpr float kStraight = 0.5f;
+__device__ constexpr float kTanh[4] = {0.9999994636f, -0.3332628310f, 0.1318994015f, -0.0443927385f};
 
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -484,8 +485,28 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     uint8_t* p_tile = sm + S::kOffP + t * S::kPTile;
     const uint32_t p_row = threadIdx.x % kRows;
     const uint32_t cs = tl + t * KB, col_o = tl + S::kColO + t * DP;
-    const float c1 = CAP ? a.scale / a.softcap * (2.f * kLog2e) : a.scale * kLog2e;
-    const float capl = a.softcap * kLog2e;
+    const float c1 = a.scale * kLog2e;
+    // With a cap: tanh(z), z = zc x, is 1 - 2 / (1 + 2^(cz x)); and for |z| <= kStraight, cap tanh(z) = x Q(x^2) in
+    // log2 units (a zc far from 1 would take Q's coefficients out of the range of normal numbers, and a large cap
+    // the weights of scores near its negative).
+    const float zc = CAP ? a.scale / a.softcap : 0.f, cz = zc * (2.f * kLog2e), capl = a.softcap * kLog2e;
+    [[maybe_unused]] const bool straight = CAP && zc > 1e-4f && zc < 1e4f && capl <= 100.f;
+    float kq[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (CAP) {
+      const float z2 = zc * zc;
+      kq[0] = kTanh[0] * capl * zc;
+      kq[1] = kTanh[1] * capl * zc * z2;
+      kq[2] = kTanh[2] * capl * zc * z2 * z2;
+      kq[3] = kTanh[3] * capl * zc * z2 * z2 * z2;
+    }
+    [[maybe_unused]] auto straight_tanh = [&](float v) {
+      const float u = v * v;
+      return fmaf(fmaf(fmaf(kq[3], u, kq[2]), u, kq[1]), u, kq[0]);
+    };
+    [[maybe_unused]] auto straight_tanh2 = [&](f32x2 v) {
+      const f32x2 u = mul2(v, v);
+      return fma2(fma2(fma2(pack2(kq[3], kq[3]), u, pack2(kq[2], kq[2])), u, pack2(kq[1], kq[1])), u, pack2(kq[0], kq[0]));
+    };
     const bool al32 = ((reinterpret_cast<uintptr_t>(a.o) | (uintptr_t)((a.o_sb | a.o_sh | a.o_st) * (a.out_bf16 ? 2 : 4))) & 31u) == 0;
     uint32_t ns = 0, n = 0;  // blocks, items
     for (int round = 0; round < rounds; ++round) {
@@ -497,7 +518,6 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       const int jb = ts.lo < ts.hi ? ts.lo / KB : 0, je = ts.lo < ts.hi ? (ts.hi + KB - 1) / KB : 0;
       const int pos = (int)a.q_pos0 + i;
       const float slope2 = BIAS && a.slopes ? a.slopes[it.h] * kLog2e : 0.f;
-      // The running maximum: of the raw products where a score grows with them (no bias), else of the scores.
       float m = -INFINITY, l = 0.f;
       for (int j = jb; j < je; ++j, ++ns) {
         wait(&bar_s[t], ns);
@@ -505,58 +525,10 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         tc_fence_after();
         const int k0 = j * KB;
         const int va = span.lo - k0, vb = span.hi - k0;  // columns va <= c < vb are seen
-        const bool all_seen = __all_sync(kFullMask, va <= 0 && vb >= KB);
-        // With two CTAs an SM the registers hold half a row at a time, read once for the maximum and once more
-        // for the weights.
-        constexpr int kHold = S::kCtas == 2 ? 32 : KB;
-        float x[kHold];
-        auto read = [&](int c0) {  // kHold columns: products, or scores where there is a bias
-#pragma unroll
-          for (int c = 0; c < kHold; c += 32) tmem_ld32(cs + c0 + c, x + c);
-          tmem_ld_wait();
-          if constexpr (BIAS) {
-            const float dist = (float)(pos - k0 - c0);
-#pragma unroll
-            for (int c = 0; c < kHold; ++c) {
-              if constexpr (CAP) x[c] = fmaf(-2.f * capl, rcp(1.f + ex2(x[c] * c1)), capl);
-              else x[c] *= c1;
-              x[c] = fmaf(-slope2, fabsf(dist - (float)c), x[c]);
-            }
-          }
-          if (!all_seen) {
-#pragma unroll
-            for (int c = 0; c < kHold; ++c) x[c] = c0 + c >= va && c0 + c < vb ? x[c] : -INFINITY;
-          }
-        };
         auto s_read = [&]() {  // the product for the next block may take S's place
           tc_fence_before();
           warp_arrive(smem_u32(&bar_sfree[t]));
         };
-        float mn = -INFINITY;
-        [[maybe_unused]] float low = INFINITY;
-#pragma unroll
-        for (int c0 = 0; c0 < KB; c0 += kHold) {
-          read(c0);
-          if (kHold == KB) s_read();
-          float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-          for (int c = 4; c < kHold; c += 8) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = c + 4 + e < kHold ? fmaxf(fmaxf(mx[e], x[c + e]), x[c + 4 + e]) : fmaxf(mx[e], x[c + e]);
-          }
-          mn = fmaxf(mn, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-          if constexpr (CAP && !BIAS) {
-            float lo[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-            for (int c = 4; c < kHold; ++c) lo[c & 3] = fminf(lo[c & 3], x[c]);
-            low = fminf(low, fminf(fminf(lo[0], lo[1]), fminf(lo[2], lo[3])));
-          }
-        }
-        // the scores stay within the cap's straight part: no row of the warp has |scale q.k| > cap
-        [[maybe_unused]] const bool small = CAP && !BIAS && __all_sync(kFullMask, fmaxf(mn, -low) * c1 <= 2.f * kLog2e);
-        if constexpr (!BIAS) {  // to log2 units: the scale is positive here and tanh grows
-          if (mn != -INFINITY) mn = CAP ? fmaf(-2.f * capl, rcp(1.f + ex2(mn * c1)), capl) : mn * c1;
-        }
         // The products of the block before: P's place is free and the output at rest behind them.
         bool o_rests = j == jb;
         auto wait_o = [&]() {
@@ -567,86 +539,151 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           }
           o_rests = true;
         };
-        if (m == -INFINITY) m = mn;  // nothing seen before: the output holds zeros, or nothing yet
-        const bool grow = mn > m + kGrowth;
-        if (__any_sync(kFullMask, grow)) {
-          const float f = grow ? ex2(m - mn) : 1.f;
-          if (grow) m = mn;
-          l *= f;
-          wait_o();
-          if (j > jb) {
+        // The running maximum takes in this block's, mn (or a bound of it); returns what the exponentials subtract.
+        auto update = [&](float mn) {
+          if (m == -INFINITY) m = mn;  // nothing seen before: the output holds zeros, or nothing yet
+          const bool grow = mn > m + kGrowth;
+          if (__any_sync(kFullMask, grow)) {
+            const float f = grow ? ex2(m - mn) : 1.f;
+            if (grow) m = mn;
+            l *= f;
+            wait_o();
+            if (j > jb) {
 #pragma unroll 1
-            for (int c = 0; c < DP; c += 16) {
-              float o[16];
-              tmem_ld16(col_o + c, o);
-              tmem_ld_wait();
+              for (int c = 0; c < DP; c += 16) {
+                float o[16];
+                tmem_ld16(col_o + c, o);
+                tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] *= f;
-              tmem_st16(col_o + c, o);
+                for (int e = 0; e < 16; ++e) o[e] *= f;
+                tmem_st16(col_o + c, o);
+              }
             }
           }
-        }
-        // ---- P in registers, and into its place once that is free
-        const float base = m == -INFINITY ? 0.f : m;
-        const f32x2 base2 = pack2(-base, -base), c2 = pack2(c1, c1);
+          return m == -INFINITY ? 0.f : m;
+        };
         f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
-        uint32_t w[KB / 2];
+        auto weight = [&](f32x2 y, int e) {  // two columns' weights as bf16
+          const f32x2 p2 = ex2_2(y);
+          sum[e & 1] = add2(sum[e & 1], p2);
+          float p0, p1;
+          unpack2(p2, p0, p1);
+          return pack2_bf16(p0, p1);
+        };
+        // The whole row in registers; false, with nothing done, where products leave the cap's straight part.  For
+        // blocks that the whole warp sees, behind its rows where there is a bias; without cap and bias for any.
+        auto row_at_once = [&]() {
+          constexpr int kAll = KB == 128 ? KB : 2;
+          float x[kAll];
 #pragma unroll
-        for (int c = 0; c < KB; c += 32) {
-          if (kHold < KB) {
-            read(c);
-            if (c + kHold == KB) s_read();
-          }
-          const float* xs = x + c % kHold;
-          f32x2 y[16];
+          for (int c = 0; c + 32 <= kAll; c += 32) tmem_ld32(cs + c, x + c);
+          tmem_ld_wait();
+          f32x2 c2 = pack2(c1, c1);
+          if constexpr (CAP) {
+            float hi[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = pack2(xs[2 * e], xs[2 * e + 1]);
-          if constexpr (BIAS) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = add2(y[e], base2);
-          } else if constexpr (CAP) {
-            if (small) {
-              // tanh(z) = z P(z^2) for |z| <= 1 with the quintic P through the six Chebyshev nodes of [0, 1]
-              const f32x2 zc = pack2(0.5f * c1 / kLog2e, 0.5f * c1 / kLog2e), capz = pack2(capl * 0.5f * c1 / kLog2e, capl * 0.5f * c1 / kLog2e);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const f32x2 z = mul2(y[e], zc), u = mul2(z, z);
-                f32x2 q = fma2(pack2(kTanh[5], kTanh[5]), u, pack2(kTanh[4], kTanh[4]));
-#pragma unroll
-                for (int k = 3; k >= 0; --k) q = fma2(q, u, pack2(kTanh[k], kTanh[k]));
-                y[e] = fma2(mul2(y[e], capz), q, base2);
-              }
-            } else {  // cap tanh(z) = cap - 2 cap / (1 + e^2z); a masked product, -infinity, goes there again
-              const f32x2 cap2 = pack2(-2.f * capl, -2.f * capl), off2 = pack2(capl - base, capl - base), one2 = pack2(1.f, 1.f);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float z0, z1, p0, p1;
-                unpack2(mul2(y[e], c2), z0, z1);
-                unpack2(add2(pack2(ex2(z0), ex2(z1)), one2), z0, z1);
-                unpack2(fma2(pack2(rcp(z0), rcp(z1)), cap2, off2), p0, p1);
-                y[e] = pack2(xs[2 * e] == -INFINITY ? -INFINITY : p0, xs[2 * e + 1] == -INFINITY ? -INFINITY : p1);
-              }
+            for (int c = 0; c < kAll; ++c) hi[c & 3] = fmaxf(hi[c & 3], fabsf(x[c]));
+            const float h = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
+            if (!__all_sync(kFullMask, h * zc <= kStraight)) return false;
+            s_read();
+            // No score exceeds cap tanh(zc h), and none is below its negative: the bound serves as the maximum.
+            if constexpr (!BIAS) {
+              const float base = update(h * straight_tanh(h));
+              c2 = pack2(-base, -base);
             }
           } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = fma2(y[e], c2, base2);
+            s_read();
           }
+          if constexpr (BIAS) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const f32x2 p2 = ex2_2(y[e]);
-            sum[e & 1] = add2(sum[e & 1], p2);
-            float p0, p1;
-            unpack2(p2, p0, p1);
-            w[c / 2 + e] = pack2_bf16(p0, p1);
+            for (int c = 0; c < kAll; c += 32) {  // - slope (pos - k0 - c): two columns more add 2 slope
+              const float far = slope2 * (float)(k0 + c - pos);
+              f32x2 off = pack2(far, far + slope2);
+              const f32x2 step = pack2(2.f * slope2, 2.f * slope2);
+#pragma unroll
+              for (int e = 0; e < 32 && c + e < kAll; e += 2) {
+                const f32x2 v = pack2(x[c + e], x[c + e + 1]);
+                unpack2(fma2(v, CAP ? straight_tanh2(v) : c2, off), x[c + e], x[c + e + 1]);
+                off = add2(off, step);
+              }
+            }
+          } else if constexpr (!CAP) {
+            if (!__all_sync(kFullMask, va <= 0 && vb >= KB)) {
+#pragma unroll
+              for (int c = 0; c < kAll; ++c) x[c] = c >= va && c < vb ? x[c] : -INFINITY;
+            }
           }
+          f32x2 base2 = c2;
+          if constexpr (BIAS || !CAP) {
+            float mx[4] = {x[0], x[0], x[0], x[0]};
+#pragma unroll
+            for (int c = 0; c < kAll; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+            float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (!BIAS && mn != -INFINITY) mn *= c1;  // the scale is positive here
+            const float base = update(mn);
+            base2 = pack2(-base, -base);
+          }
+          uint32_t w[kAll / 2];
+#pragma unroll
+          for (int e = 0; e < kAll / 2; ++e) {
+            const f32x2 v = pack2(x[2 * e], x[2 * e + 1]);
+            w[e] = weight(BIAS ? add2(v, base2) : fma2(v, CAP ? straight_tanh2(v) : c2, base2), e);
+          }
+          wait_o();  // the products of the block before may have read P's place until here
+#pragma unroll
+          for (int e = 0; e < kAll / 8; ++e)
+            *reinterpret_cast<uint4*>(p_tile + sw128_off(p_row, 8 * e, kRows)) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          return true;
+        };
+        // 32 columns at a time, read once for the maximum and once more for the weights.
+        auto row_by_parts = [&]() {
+          auto read = [&](int c0, float (&v)[32]) {  // scores
+            tmem_ld32(cs + c0, v);
+            tmem_ld_wait();
+            const float dist = (float)(pos - k0 - c0);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              if constexpr (CAP) v[c] = fmaf(-2.f * capl, rcp(1.f + ex2(v[c] * cz)), capl);  // cap tanh(z) = cap - 2 cap / (1 + e^2z)
+              else v[c] *= c1;
+              if constexpr (BIAS) v[c] = fmaf(-slope2, fabsf(dist - (float)c), v[c]);
+              v[c] = c0 + c >= va && c0 + c < vb ? v[c] : -INFINITY;
+            }
+          };
+          float mn = -INFINITY;
+#pragma unroll 1
+          for (int c0 = 0; c0 < KB; c0 += 32) {
+            float v[32];
+            read(c0, v);
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) mn = fmaxf(fmaxf(mn, fmaxf(v[c], v[c + 1])), fmaxf(v[c + 2], v[c + 3]));
+          }
+          const float base = update(mn);
+          const f32x2 base2 = pack2(-base, -base);
+          wait_o();
+#pragma unroll 1
+          for (int c0 = 0; c0 < KB; c0 += 32) {
+            float v[32];
+            read(c0, v);
+            if (c0 + 32 == KB) s_read();
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = weight(add2(pack2(v[2 * e], v[2 * e + 1]), base2), e);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(p_tile + sw128_off(p_row, c0 + 8 * e, kRows)) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          }
+        };
+        if constexpr (KB == 64) {  // such blocks are few, and hardly ever seen as a whole
+          row_by_parts();
+        } else if constexpr (!CAP && !BIAS) {
+          row_at_once();
+        } else {
+          const bool whole = __all_sync(kFullMask, va <= 0 && vb >= KB && (!BIAS || pos - k0 >= KB - 1));
+          if (!whole || (CAP && !straight) || !row_at_once()) row_by_parts();
         }
         float s0, s1;
         unpack2(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
-        wait_o();
-#pragma unroll
-        for (int e = 0; e < KB / 8; ++e)
-          *reinterpret_cast<uint4*>(p_tile + sw128_off(p_row, 8 * e, kRows)) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
         tmem_st_wait();  // of a scaled output
         fence_proxy_async_smem();
         tc_fence_before();
@@ -771,7 +808,7 @@ cudaError_t launch_width(const SwaPrefillLaunch& a, cudaStream_t stream) {
   if (!encode(&q, a.q, a.B, a.H, a.Nq, a.d, kRows) || !encode(&k, a.k, a.B, a.Hkv, a.Nk, a.d, KB) ||
       !encode(&v, a.v, a.B, a.Hkv, a.Nk, a.d, KB))
     return cudaErrorNotSupported;  // strides that TMA cannot describe
-  // without a bias the running maximum is taken of the raw products, which the scale must not turn round
+  // without a bias the maximum is taken of the raw products, which the scale must not turn round
   const bool cap = a.softcap != 0.f, bias = a.slopes != nullptr || !(a.scale > 0.f);
   if (cap && bias) return launch_typed<DP, KB, true, true>(a, q, k, v, stream);
   if (cap) return launch_typed<DP, KB, true, false>(a, q, k, v, stream);
