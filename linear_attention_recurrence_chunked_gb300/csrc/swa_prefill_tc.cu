@@ -201,6 +201,14 @@ struct TileSpan {
 };
 __device__ __forceinline__ TileSpan tile_span(const SwaPrefillLaunch& a, int b, int i0, int len) {
   TileSpan t{INT32_MAX, 0, 0, INT32_MAX};
+  if (!a.key_lo && !a.key_hi) {  // intervals that move up with the rows: the first and the last row have them all
+    const int last = min(i0 + kRows, min((int)a.Nq, len - (int)a.q_pos0)) - 1;
+    if (last >= i0) {
+      const KeySpan s0 = key_span(a, b, i0, len), s1 = key_span(a, b, last, len);
+      t = TileSpan{s0.lo, s1.hi, s1.lo, s0.hi};
+    }
+    return t;
+  }
 #pragma unroll 1
   for (int i = i0 + (threadIdx.x & 31); i < i0 + kRows; i += 32) {
     const KeySpan s = key_span(a, b, i, len);
@@ -635,39 +643,59 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             *reinterpret_cast<uint4*>(p_tile + sw128_off(p_row, 8 * e, kRows)) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
           return true;
         };
-        // 32 columns at a time, read once for the maximum and once more for the weights.
+        // 32 columns at a time, read once for the maximum and once more for the weights.  Columns that no row of
+        // the warp sees are passed over (their weights are zeros), ones that all see are not masked.
         auto row_by_parts = [&]() {
-          auto read = [&](int c0, float (&v)[32]) {  // scores
+          constexpr bool raw = !CAP && !BIAS;  // products serve as scores until the exponential
+          auto none = [&](int c0) { return __all_sync(kFullMask, vb <= c0 || va >= c0 + 32 || va >= vb); };
+          auto read = [&](int c0, float (&v)[32]) {
             tmem_ld32(cs + c0, v);
             tmem_ld_wait();
             const float dist = (float)(pos - k0 - c0);
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
               if constexpr (CAP) v[c] = fmaf(-2.f * capl, rcp(1.f + ex2(v[c] * cz)), capl);  // cap tanh(z) = cap - 2 cap / (1 + e^2z)
-              else v[c] *= c1;
+              else if constexpr (BIAS) v[c] *= c1;
               if constexpr (BIAS) v[c] = fmaf(-slope2, fabsf(dist - (float)c), v[c]);
-              v[c] = c0 + c >= va && c0 + c < vb ? v[c] : -INFINITY;
+            }
+            if (!__all_sync(kFullMask, va <= c0 && vb >= c0 + 32)) {
+              const uint32_t from = va - c0 >= 32 ? 0u : ~0u << max(va - c0, 0), to = vb - c0 >= 32 ? ~0u : (1u << max(vb - c0, 0)) - 1u;
+              const uint32_t seen = from & to;
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] = seen & (1u << c) ? v[c] : -INFINITY;
             }
           };
           float mn = -INFINITY;
 #pragma unroll 1
           for (int c0 = 0; c0 < KB; c0 += 32) {
+            if (none(c0)) continue;
             float v[32];
             read(c0, v);
+            float mx[2] = {v[0], v[1]};
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) mn = fmaxf(fmaxf(mn, fmaxf(v[c], v[c + 1])), fmaxf(v[c + 2], v[c + 3]));
+            for (int c = 2; c < 32; ++c) mx[c & 1] = fmaxf(mx[c & 1], v[c]);
+            mn = fmaxf(mn, fmaxf(mx[0], mx[1]));
           }
+          if (raw && mn != -INFINITY) mn *= c1;  // the scale is positive here
           const float base = update(mn);
-          const f32x2 base2 = pack2(-base, -base);
+          const f32x2 base2 = pack2(-base, -base), c2 = pack2(c1, c1);
           wait_o();
 #pragma unroll 1
           for (int c0 = 0; c0 < KB; c0 += 32) {
-            float v[32];
-            read(c0, v);
-            if (c0 + 32 == KB) s_read();
             uint32_t w[16];
+            if (none(c0)) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = weight(add2(pack2(v[2 * e], v[2 * e + 1]), base2), e);
+              for (int e = 0; e < 16; ++e) w[e] = 0u;
+            } else {
+              float v[32];
+              read(c0, v);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const f32x2 y = pack2(v[2 * e], v[2 * e + 1]);
+                w[e] = weight(raw ? fma2(y, c2, base2) : add2(y, base2), e);
+              }
+            }
+            if (c0 + 32 == KB) s_read();
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               *reinterpret_cast<uint4*>(p_tile + sw128_off(p_row, c0 + 8 * e, kRows)) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
