@@ -2,12 +2,22 @@
 // distance bias, over the rings of swa_decode.cu (token p in slot p % window):
 //   s_j = cap tanh(scale q.k_j / cap) - slope (pos - j),   o = sum_j softmax_j(s_j) v_j.
 // The step reads each ring once and little else, so memory bounds it.  One CTA per (sequence, key head), one
-// warp per 32 slots of the ring: a warp scores its slots for up to four query heads of the group at a time
-// (rows read as 16-byte vectors, a row over LPR lanes, four loads a lane in flight; the sums over a row's
-// lanes are one reduce-scatter for four rows and four heads), takes the softmax of its own slots and adds up
-// its own value rows, so that no warp waits for another before the end, where the warps' parts meet in
-// shared memory.  The new token is used from the arguments; the warp of its slot writes it there.
+// warp per 32 slots of the ring: a warp scores its slots for all query heads of the group, takes the softmax
+// of its own slots and adds up its own value rows, so that no warp waits for another before the end, where
+// the warps' parts meet in shared memory.  The new token is used from the arguments; the warp of its slot
+// writes it there.
+//
+// bf16: a key row meets up to 16 query heads, too many operations for the CUDA cores beside the loads (58 us for
+// 256 x 16 heads over 4 key heads and 256 slots at d = 128, three times the time of its bytes) and too few rows
+// for tcgen05, so the products are mma.m16n8k16 with the heads as the 16 rows.  Keys go from memory to the
+// operand registers directly: a lane's 16 bytes are elements of one slot, and which elements of the sum they are
+// is the same for the queries.  Values come by asynchronous copies, all 32 rows of a warp at once, and are
+// transposed on the way from shared memory.  The weights are rounded to bf16 for their product, as over a prompt.
+// fp32: CUDA cores, four query heads at a time.
+#include <mutex>
+
 #include "layers.cuh"
+#include "tc.cuh"
 
 namespace la {
 namespace {
@@ -21,6 +31,193 @@ constexpr int kLoads = 4;      // row loads in flight
 template <typename T>
 __device__ __forceinline__ uint4 load_row(const T* p) { return *reinterpret_cast<const uint4*>(p); }
 
+// ---------------------------------------------------------------------------------------------- bf16
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// DP: width padded to 64 or 128
+template <typename TOut, int DP>
+__global__ void __launch_bounds__(32 * kMaxWarps, 2)
+swa_biased_decode_mma_kernel(const SwaBiasedDecodeLaunch a) {
+  using T = __nv_bfloat16;
+  constexpr int kGroups = DP / 32;               // of 32 columns: a load of eight slots each
+  constexpr int kPairs = DP / 16;                // of 8-column output tiles
+  constexpr int kRegion = kSlots * DP * 2;       // a warp's shared memory: its value rows, then its output
+  static_assert(kRegion >= 16 * DP * 4, "");
+  extern __shared__ __align__(128) uint8_t sw_smem[];
+  __shared__ float s_m[kMaxWarps][16], s_l[kMaxWarps][16];
+  const SwaDecodeLaunch& c = a.base;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int64_t sk = blockIdx.x, s = sk / a.Hkv, hk = sk - s * a.Hkv;
+  grid_dependents_trigger();
+  grid_dependency_wait();  // the rings, positions and inputs of this step are in memory
+  const int d = c.d, w = c.window, group = (int)(c.H / a.Hkv);
+  const int64_t pos = c.pos[s];
+  if (pos < 0) {  // uniform over the CTA
+    if (threadIdx.x == 0 && hk == 0) atomicOr(c.status, kStatusBadIndex);
+    return;
+  }
+  const int slot_new = (int)(pos % w);
+  const int n = pos + 1 < w ? (int)(pos + 1) : w;
+  const int first = warp * kSlots, h0 = (int)hk * group;
+  const T* kn = reinterpret_cast<const T*>(c.k) + sk * d;
+  const T* vn = reinterpret_cast<const T*>(c.v) + sk * d;
+  T* kc = reinterpret_cast<T*>(c.k_cache) + sk * (int64_t)w * d;
+  T* vc = reinterpret_cast<T*>(c.v_cache) + sk * (int64_t)w * d;
+  uint8_t* region = sw_smem + warp * kRegion;
+  const uint32_t rbase = tc::smem_u32(region);
+  const int chunks = d / 8;
+  // place of 16-byte chunk `ch` of value row r: eight neighbouring rows meet eight different banks
+  auto at = [](int r, int ch) { return (uint32_t)(r * (DP * 2) + ((ch ^ (r & 7)) << 4)); };
+
+  // ---- value rows on their way; slots that hold nothing become zeros
+#pragma unroll
+  for (int i = 0; i < kSlots * (DP / 8) / 32; ++i) {
+    const int e = lane + 32 * i, r = e / (DP / 8), ch = e % (DP / 8), slot = first + r;
+    const T* src = slot == slot_new ? vn : vc + (int64_t)slot * d;
+    const bool on = slot < n && ch < chunks;
+    tc::cp_async16(rbase + at(r, ch), on ? src + ch * 8 : vn, on ? 16u : 0u);
+  }
+  tc::cp_async_commit();
+
+  // ---- scores: rows = heads (lane / 4 and that + 8), columns = slots
+  const int hr = lane >> 2, q4 = lane & 3;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const T* q = reinterpret_cast<const T*>(c.q) + (s * c.H + h0) * d;
+  uint4 ql[kGroups], qh[kGroups];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const int col = g * 32 + q4 * 8;
+    ql[g] = hr < group && col < d ? *reinterpret_cast<const uint4*>(q + hr * d + col) : zero;
+    qh[g] = hr + 8 < group && col < d ? *reinterpret_cast<const uint4*>(q + (hr + 8) * d + col) : zero;
+  }
+  float x[4][4];
+  uint4 kr[2][2][kGroups];  // two tiles of eight slots now, two on their way
+  auto fetch = [&](int half) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int slot = first + (half * 2 + t) * 8 + hr;
+      const T* src = slot == slot_new ? kn : kc + (int64_t)slot * d;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int col = g * 32 + q4 * 8;
+        kr[half][t][g] = slot < n && col < d ? *reinterpret_cast<const uint4*>(src + col) : zero;
+      }
+    }
+  };
+  fetch(0);
+  fetch(1);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const uint4 k = kr[t / 2][t % 2][g];
+      mma16816(x[t], ql[g].x, qh[g].x, ql[g].y, qh[g].y, k.x, k.y);
+      mma16816(x[t], ql[g].z, qh[g].z, ql[g].w, qh[g].w, k.z, k.w);
+    }
+  }
+  // ---- softmax of this warp's slots
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int slot = first + t * 8 + q4 * 2 + (e & 1), h = hr + (e >> 1) * 8;
+      float y = x[t][e] * c.scale;
+      if (a.softcap != 0.f) y = fmaf(-2.f * a.softcap, rcp(1.f + ex2(y * (2.f * kLog2e / a.softcap))), a.softcap);
+      const float age = (float)(slot_new >= slot ? slot_new - slot : slot_new - slot + w);
+      if (a.slopes && h < group) y = fmaf(-a.slopes[h0 + h], age, y);
+      x[t][e] = slot < n ? y : -INFINITY;
+      m[e >> 1] = fmaxf(m[e >> 1], x[t][e]);
+    }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    m[r] = fmaxf(m[r], __shfl_xor_sync(kFullMask, m[r], 1));
+    m[r] = fmaxf(m[r], __shfl_xor_sync(kFullMask, m[r], 2));
+    const float base = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 2 * r; e < 2 * r + 2; ++e) {
+        x[t][e] = ex2((x[t][e] - base) * kLog2e);
+        l[r] += x[t][e];
+      }
+    l[r] += __shfl_xor_sync(kFullMask, l[r], 1);
+    l[r] += __shfl_xor_sync(kFullMask, l[r], 2);
+    if (q4 == 0) {
+      s_m[warp][hr + 8 * r] = m[r];
+      s_l[warp][hr + 8 * r] = l[r];
+    }
+  }
+  // ---- this warp's value rows
+  float o[2 * kPairs][4];
+#pragma unroll
+  for (int t = 0; t < 2 * kPairs; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+  tc::cp_async_wait_all();
+  __syncwarp();
+#pragma unroll
+  for (int kt = 0; kt < 2; ++kt) {
+    const uint32_t a0 = tc::pack2_bf16(x[2 * kt][0], x[2 * kt][1]), a1 = tc::pack2_bf16(x[2 * kt][2], x[2 * kt][3]);
+    const uint32_t a2 = tc::pack2_bf16(x[2 * kt + 1][0], x[2 * kt + 1][1]), a3 = tc::pack2_bf16(x[2 * kt + 1][2], x[2 * kt + 1][3]);
+    const int r = kt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+      uint32_t b[4];
+      ldmatrix_trans(b, rbase + at(r, 2 * p + (lane >> 4)));
+      mma16816(o[2 * p], a0, a1, a2, a3, b[0], b[1]);
+      mma16816(o[2 * p + 1], a0, a1, a2, a3, b[2], b[3]);
+    }
+  }
+  // the new token into its slot, by the warp that used it from the arguments
+  if (slot_new / kSlots == warp && lane < chunks) {
+    reinterpret_cast<uint4*>(kc + (int64_t)slot_new * d)[lane] = reinterpret_cast<const uint4*>(kn)[lane];
+    reinterpret_cast<uint4*>(vc + (int64_t)slot_new * d)[lane] = reinterpret_cast<const uint4*>(vn)[lane];
+  }
+  __syncwarp();  // the value rows are used up: their place takes the output
+  float* part = reinterpret_cast<float*>(region);
+#pragma unroll
+  for (int t = 0; t < 2 * kPairs; ++t) {
+    if (t * 8 < d) {
+      const int col = t * 8 + q4 * 2;
+      if (hr < group) *reinterpret_cast<float2*>(part + hr * d + col) = make_float2(o[t][0], o[t][1]);
+      if (hr + 8 < group) *reinterpret_cast<float2*>(part + (hr + 8) * d + col) = make_float2(o[t][2], o[t][3]);
+    }
+  }
+  __syncthreads();
+  // ---- the warps' parts together
+  for (int e = threadIdx.x * 2; e < group * d; e += blockDim.x * 2) {
+    const int g = e / d;
+    float hi = s_m[0][g];
+    for (int u = 1; u < warps; ++u) hi = fmaxf(hi, s_m[u][g]);
+    float2 sum = make_float2(0.f, 0.f);
+    float total = 0.f;
+    for (int u = 0; u < warps; ++u) {
+      const float f = ex2((s_m[u][g] - hi) * kLog2e);
+      const float2 y = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(sw_smem + u * kRegion) + e);
+      sum.x = fmaf(f, y.x, sum.x);
+      sum.y = fmaf(f, y.y, sum.y);
+      total = fmaf(f, s_l[u][g], total);
+    }
+    TOut* out = reinterpret_cast<TOut*>(c.out) + (s * c.H + h0) * d + e;
+    store1(out, sum.x / total);
+    store1(out + 1, sum.y / total);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------- fp32
 template <typename TIn, typename TOut, int LPR>
 __global__ void __launch_bounds__(32 * kMaxWarps, LPR >= 16 ? 2 : 1)
 swa_biased_decode_kernel(const SwaBiasedDecodeLaunch a) {
@@ -208,26 +405,39 @@ swa_biased_decode_kernel(const SwaBiasedDecodeLaunch a) {
   }
 }
 
-template <typename TIn, typename TOut>
-cudaError_t launch_typed(const SwaBiasedDecodeLaunch& a, cudaStream_t stream) {
+template <typename TOut, int DP>
+cudaError_t launch_mma(const SwaBiasedDecodeLaunch& a, cudaStream_t stream) {
+  constexpr int kRegion = kSlots * DP * 2;
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    attr = cudaFuncSetAttribute(swa_biased_decode_mma_kernel<TOut, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxWarps * kRegion);
+  });
+  if (attr != cudaSuccess) return attr;
+  const int warps = (a.base.window + kSlots - 1) / kSlots;
+  return launch_dependent(swa_biased_decode_mma_kernel<TOut, DP>, dim3((unsigned)(a.base.S * a.Hkv)), dim3((unsigned)(32 * warps)),
+                          (size_t)(warps * kRegion), stream, a);
+}
+
+template <typename TOut>
+cudaError_t launch_fp32(const SwaBiasedDecodeLaunch& a, cudaStream_t stream) {
   const dim3 grid((unsigned)(a.base.S * a.Hkv)), block((unsigned)(32 * ((a.base.window + kSlots - 1) / kSlots)));
-  const int vecs = a.base.d / kVec<TIn>;
-  if (vecs > 16) {
-    if constexpr (sizeof(TIn) == 4) return launch_dependent(swa_biased_decode_kernel<TIn, TOut, 32>, grid, block, 0, stream, a);
-  }
-  if (vecs > 8) return launch_dependent(swa_biased_decode_kernel<TIn, TOut, 16>, grid, block, 0, stream, a);
-  if (vecs > 4) return launch_dependent(swa_biased_decode_kernel<TIn, TOut, 8>, grid, block, 0, stream, a);
-  return launch_dependent(swa_biased_decode_kernel<TIn, TOut, 4>, grid, block, 0, stream, a);
+  const int vecs = a.base.d / kVec<float>;
+  if (vecs > 16) return launch_dependent(swa_biased_decode_kernel<float, TOut, 32>, grid, block, 0, stream, a);
+  if (vecs > 8) return launch_dependent(swa_biased_decode_kernel<float, TOut, 16>, grid, block, 0, stream, a);
+  return launch_dependent(swa_biased_decode_kernel<float, TOut, 8>, grid, block, 0, stream, a);
+}
+
+template <typename TOut>
+cudaError_t launch_out(const SwaBiasedDecodeLaunch& a, cudaStream_t stream) {
+  if (!a.base.in_bf16) return launch_fp32<TOut>(a, stream);
+  return a.base.d <= 64 ? launch_mma<TOut, 64>(a, stream) : launch_mma<TOut, 128>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_swa_biased_decode(const SwaBiasedDecodeLaunch& a, cudaStream_t stream) {
-  const bool in = a.base.in_bf16, out = a.base.out_bf16;
-  if (in && out) return launch_typed<__nv_bfloat16, __nv_bfloat16>(a, stream);
-  if (in) return launch_typed<__nv_bfloat16, float>(a, stream);
-  if (out) return launch_typed<float, __nv_bfloat16>(a, stream);
-  return launch_typed<float, float>(a, stream);
+  return a.base.out_bf16 ? launch_out<__nv_bfloat16>(a, stream) : launch_out<float>(a, stream);
 }
 
 }  // namespace la

@@ -300,6 +300,7 @@ def test_swa_masked_keys_and_values_reach_nothing(bad, dtype):
     v2 = v.clone()
     k2, _ = swa_case(1, 4, 2, N, N, 64, dtype, 9)[1].to(dev), None
     o2 = la.la_swa_prefill(q, k2, v2, window=window)
+    assert la.la_device_status() == la.LA_OK
     assert torch.isnan(o2[0, :, at:at + window, 5]).all() or torch.isinf(o2[0, :, at:at + window, 5]).all()
     assert torch.isfinite(o2[0, :, :, 6]).all()
 
@@ -340,8 +341,10 @@ def test_swa_biased_step_without_extras_meets_the_plain_step():
     a = la.la_swa_decode_step(q, k, v, k1, v1, pos, out_dtype=FP)
     b = la.la_swa_biased_decode_step(q, k, v, k2, v2, pos, out_dtype=FP)
     assert torch.equal(k1, k2) and torch.equal(v1, v2)
-    # both sum up to 64 fp32 terms in their own order
-    assert (a - b).abs().max() < 64 * 2 ** -23 * 8
+    # the biased step rounds each weight to bf16 for its product with v: off by at most 2^-8 of the weighted mean
+    # of |v|; beside that both sum up to 64 fp32 terms in their own order
+    largest = torch.cat([v2, v.unsqueeze(2)], 2).float().abs().max()
+    assert (a - b).abs().max() < (2 ** -8 + 64 * 2 ** -23) * largest
 
 
 # ------------------------------------------------------------------------------------------ errors, streams, graphs
