@@ -77,19 +77,35 @@ conv_prefill_kernel(const ConvLaunch a, int64_t vecs, int64_t runs, int run_len)
 #pragma unroll
   for (int i = 0; i < W - 1; ++i) row(t0 + i - (W - 1)).unpack(hist[i]);
 
+  // pairs of channels from here on
+  f32x2 w2[W][2], b2[2], h2[W - 1][2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    b2[p] = pack2(bs[2 * p], bs[2 * p + 1]);
+#pragma unroll
+    for (int i = 0; i < W; ++i) w2[i][p] = pack2(wt[i][2 * p], wt[i][2 * p + 1]);
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) h2[i][p] = pack2(hist[i][2 * p], hist[i][2 * p + 1]);
+  }
   auto token = [&](const Raw4<TIn>& raw, TOut* yp) {
     float cur[kV], o[kV];
     raw.unpack(cur);
 #pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      float acc = bs[j];
+    for (int p = 0; p < 2; ++p) {
+      f32x2 acc = b2[p];
 #pragma unroll
-      for (int i = 0; i < W - 1; ++i) acc = fmaf(wt[i][j], hist[i][j], acc);
-      acc = fmaf(wt[W - 1][j], cur[j], acc);
-      o[j] = a.silu ? silu(acc) : acc;
+      for (int i = 0; i < W - 1; ++i) acc = fma2(w2[i][p], h2[i][p], acc);
+      const f32x2 now = pack2(cur[2 * p], cur[2 * p + 1]);
+      acc = fma2(w2[W - 1][p], now, acc);
+      unpack2(acc, o[2 * p], o[2 * p + 1]);
+      if (a.silu) {
+        float e0, e1;
+        unpack2(add2(ex2_2(mul2(acc, pack2(-kLog2e, -kLog2e))), pack2(1.f, 1.f)), e0, e1);
+        unpack2(mul2(acc, pack2(rcp(e0), rcp(e1))), o[2 * p], o[2 * p + 1]);
+      }
 #pragma unroll
-      for (int i = 0; i + 1 < W - 1; ++i) hist[i][j] = hist[i + 1][j];
-      hist[W - 2][j] = cur[j];
+      for (int i = 0; i + 1 < W - 1; ++i) h2[i][p] = h2[i + 1][p];
+      h2[W - 2][p] = now;
     }
     store_floats(yp, o, valid, FULL);
   };

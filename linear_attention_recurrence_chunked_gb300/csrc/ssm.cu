@@ -416,79 +416,124 @@ ssm_combine_kernel(const SsmLaunch a, Segments seg, float* ws_h, const float* ws
 }
 
 // ---------------------------------------------------------------------------------------------- one token
+// The step reads and writes each state once, which bounds it.  L lanes share a channel, four states a lane, for
+// four sequences at a time: A, D and the bias are loaded once for them, the four states' loads are in flight
+// together, and of the channel's lanes each computes the step size and the gate of a sequence of its own.
 constexpr int kStepThreads = 256;
-constexpr int kStepSeqs = 4;  // sequences per thread: its A, D and bias loads serve all of them
+constexpr int kStepSeqs = 4;
+
+template <typename T>
+__device__ __forceinline__ void load_states(const T* p, int count, bool vec, float (&o)[kK]) {
+  if (vec) {
+    const float4 x = load4(p);
+    o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < kK; ++k) o[k] = k < count ? to_f(p[k]) : 0.f;
+  }
+}
 
 template <int L, typename TIn, typename TOut>
 __global__ void __launch_bounds__(kStepThreads)
-ssm_decode_kernel(const SsmLaunch a) {
+ssm_decode_kernel(const SsmLaunch a, bool bc_vec) {
+  constexpr int NQ = L >= kStepSeqs ? 1 : kStepSeqs / L;  // sequences whose gates this lane computes
   const int tid = threadIdx.x, l = tid % L;
   const int64_t c = (int64_t)blockIdx.x * (kStepThreads / L) + tid / L;
   const int64_t s0 = (int64_t)blockIdx.y * kStepSeqs;
   const bool live = c < a.C;
   const int64_t cc = live ? c : 0, g = cc / (a.C / a.G);
-  const bool vec = a.n % 4 == 0;
+  const int s_lo = l * kK, count = min(kK, a.n - s_lo);
+  const bool on = live && count > 0, vec = a.n % kK == 0;
+  const int q_own = L >= kStepSeqs ? l / (L >= kStepSeqs ? L / kStepSeqs : 1) : l * NQ;
   grid_dependents_trigger();
   grid_dependency_wait();  // the states and this step's inputs are in memory
-  float4 h[kStepSeqs];
-  float u[kStepSeqs], dt[kStepSeqs], z[kStepSeqs];
-  const int s_lo = l * kK;
+  float h[kStepSeqs][kK];
 #pragma unroll
   for (int q = 0; q < kStepSeqs; ++q) {
-    h[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int64_t s = s0 + q;
-    if (live && s < a.B) {
-      const float* p = a.h_in + (s * a.C + cc) * a.n + s_lo;
-      if (vec && s_lo < a.n) {
-        h[q] = __ldcs(reinterpret_cast<const float4*>(p));
+#pragma unroll
+    for (int k = 0; k < kK; ++k) h[q][k] = 0.f;
+    if (on && s0 + q < a.B) {
+      const float* p = a.h_in + ((s0 + q) * a.C + cc) * a.n + s_lo;
+      if (vec) {
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
+        h[q][0] = x.x; h[q][1] = x.y; h[q][2] = x.z; h[q][3] = x.w;
       } else {
-        if (s_lo + 0 < a.n) h[q].x = p[0];
-        if (s_lo + 1 < a.n) h[q].y = p[1];
-        if (s_lo + 2 < a.n) h[q].z = p[2];
-        if (s_lo + 3 < a.n) h[q].w = p[3];
+#pragma unroll
+        for (int k = 0; k < kK; ++k) h[q][k] = k < count ? p[k] : 0.f;
       }
     }
   }
   float A2[kK];
 #pragma unroll
-  for (int k = 0; k < kK; ++k) A2[k] = s_lo + k < a.n ? log2_rate(a.A[cc * a.n + s_lo + k]) : 0.f;
-  const float Dc = a.D ? a.D[cc] : 0.f, bias = a.delta_bias ? a.delta_bias[cc] : 0.f;
+  for (int k = 0; k < kK; ++k) A2[k] = k < count ? log2_rate(a.A[cc * a.n + s_lo + k]) : 0.f;
+  const float bias = a.delta_bias ? a.delta_bias[cc] : 0.f;
+  float u_own[NQ], dt_own[NQ];
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const int64_t s = min(s0 + q_own + i, a.B - 1);
+    u_own[i] = to_f(reinterpret_cast<const TIn*>(a.u)[s * a.u_sb + cc]);
+    const float x = to_f(reinterpret_cast<const TIn*>(a.delta)[s * a.d_sb + cc]) + bias;
+    dt_own[i] = a.softplus ? softplus(x) : x;
+  }
+  float acc[kStepSeqs];
+  const int group_lane = (tid & 31) - l;
 #pragma unroll
   for (int q = 0; q < kStepSeqs; ++q) {
     const int64_t s = min(s0 + q, a.B - 1);
-    u[q] = to_f(reinterpret_cast<const TIn*>(a.u)[s * a.u_sb + cc]);
-    const float x = to_f(reinterpret_cast<const TIn*>(a.delta)[s * a.d_sb + cc]) + bias;
-    dt[q] = a.softplus ? softplus(x) : x;
-    z[q] = a.z ? silu(to_f(reinterpret_cast<const TIn*>(a.z)[s * a.z_sb + cc])) : 1.f;
-  }
-#pragma unroll
-  for (int q = 0; q < kStepSeqs; ++q) {
-    const int64_t s = s0 + q;
-    if (s >= a.B) break;  // uniform over the block
-    const TIn* Bp = reinterpret_cast<const TIn*>(a.Bm.ptr) + s * a.Bm.sb + g * a.Bm.sh + s_lo;
-    const TIn* Cp = reinterpret_cast<const TIn*>(a.Cm.ptr) + s * a.Cm.sb + g * a.Cm.sh + s_lo;
-    float hk[kK] = {h[q].x, h[q].y, h[q].z, h[q].w};
-    float acc = 0.f;
-    const float dtu = dt[q] * u[q];
+    const int src = group_lane + (L >= kStepSeqs ? q * (L / kStepSeqs) : q / NQ);
+    const float dt = L == 1 ? dt_own[q % NQ] : __shfl_sync(kFullMask, dt_own[q % NQ], src);
+    const float u = L == 1 ? u_own[q % NQ] : __shfl_sync(kFullMask, u_own[q % NQ], src);
+    float Bk[kK], Ck[kK];
+    load_states(reinterpret_cast<const TIn*>(a.Bm.ptr) + s * a.Bm.sb + g * a.Bm.sh + s_lo, count, bc_vec && count > 0, Bk);
+    load_states(reinterpret_cast<const TIn*>(a.Cm.ptr) + s * a.Cm.sb + g * a.Cm.sh + s_lo, count, bc_vec && count > 0, Ck);
+    const float dtu = dt * u;
+    acc[q] = 0.f;
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
-      if (s_lo + k < a.n) {
-        hk[k] = fmaf(ex2(dt[q] * A2[k]), hk[k], dtu * to_f(Bp[k]));
-        acc = fmaf(to_f(Cp[k]), hk[k], acc);
-      }
+      h[q][k] = fmaf(ex2(dt * A2[k]), h[q][k], dtu * Bk[k]);
+      acc[q] = fmaf(Ck[k], h[q][k], acc[q]);
     }
-#pragma unroll
-    for (int off = L / 2; off >= 1; off >>= 1) acc += __shfl_xor_sync(kFullMask, acc, off);
-    if (live) {
-      float* p = a.h_out + (s * a.C + c) * a.n + s_lo;
-      if (vec && s_lo < a.n) {
-        __stcs(reinterpret_cast<float4*>(p), make_float4(hk[0], hk[1], hk[2], hk[3]));
+    if (on && s0 + q < a.B) {
+      float* p = a.h_out + ((s0 + q) * a.C + cc) * a.n + s_lo;
+      if (vec) {
+        __stcs(reinterpret_cast<float4*>(p), make_float4(h[q][0], h[q][1], h[q][2], h[q][3]));
       } else {
 #pragma unroll
         for (int k = 0; k < kK; ++k)
-          if (s_lo + k < a.n) p[k] = hk[k];
+          if (k < count) p[k] = h[q][k];
       }
-      if (l == 0) store1(reinterpret_cast<TOut*>(a.y) + s * a.y_sb + c, fmaf(Dc, u[q], acc) * z[q]);
+    }
+  }
+  // sums over the channel's lanes, each ending with its own sequences'
+  float y[NQ];
+  if constexpr (L == 1) {
+#pragma unroll
+    for (int q = 0; q < kStepSeqs; ++q) y[q % NQ] = acc[q];
+  } else {
+    const bool up = (l & (L / 2)) != 0;
+    float p0 = up ? acc[2] : acc[0], p1 = up ? acc[3] : acc[1];
+    p0 += __shfl_xor_sync(kFullMask, up ? acc[0] : acc[2], L / 2);
+    p1 += __shfl_xor_sync(kFullMask, up ? acc[1] : acc[3], L / 2);
+    if constexpr (L == 2) {
+      y[0] = p0;
+      y[NQ - 1] = p1;
+    } else {
+      const bool up2 = (l & (L / 4)) != 0;
+      y[0] = (up2 ? p1 : p0) + __shfl_xor_sync(kFullMask, up2 ? p0 : p1, L / 4);
+#pragma unroll
+      for (int off = L / 8; off >= 1; off >>= 1) y[0] += __shfl_xor_sync(kFullMask, y[0], off);
+    }
+  }
+  if (live && (L < kStepSeqs || l % (L >= kStepSeqs ? L / kStepSeqs : 1) == 0)) {
+    const float skip = a.D ? a.D[c] : 0.f;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int64_t s = s0 + q_own + i;
+      if (s < a.B) {
+        float o = fmaf(skip, u_own[i], y[i]);
+        if (a.z) o *= silu(to_f(reinterpret_cast<const TIn*>(a.z)[s * a.z_sb + c]));
+        store1(reinterpret_cast<TOut*>(a.y) + s * a.y_sb + c, o);
+      }
     }
   }
 }
@@ -541,10 +586,14 @@ cudaError_t launch_scan(const SsmLaunch& a, void* ws, const Segments& seg, cudaS
 
 template <typename TIn, typename TOut>
 cudaError_t launch_lanes(const SsmLaunch& a, void* ws, const Segments* seg, cudaStream_t stream) {
+  // four states of B and C in one load: rows of whole quadruples on their boundary
+  constexpr int64_t quad = 4 * (int64_t)sizeof(TIn);
+  const bool bc_vec = a.n % kK == 0 && ((reinterpret_cast<uintptr_t>(a.Bm.ptr) | reinterpret_cast<uintptr_t>(a.Cm.ptr) |
+                                         (uintptr_t)((a.Bm.sb | a.Bm.sh | a.Cm.sb | a.Cm.sh) * (int64_t)sizeof(TIn))) % quad) == 0;
   auto step = [&](auto kernel, int L) {
     const int64_t per = kStepThreads / L;
     const dim3 grid((unsigned)((a.C + per - 1) / per), (unsigned)((a.B + kStepSeqs - 1) / kStepSeqs));
-    return launch_dependent(kernel, grid, dim3(kStepThreads), 0, stream, a);
+    return launch_dependent(kernel, grid, dim3(kStepThreads), 0, stream, a, bc_vec);
   };
   switch (lanes_of(a.n)) {
     case 1: return seg ? launch_scan<1, TIn, TOut>(a, ws, *seg, stream) : step(ssm_decode_kernel<1, TIn, TOut>, 1);
