@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -609,41 +610,54 @@ def la_notebank_route(rho, u, R: int, positions=None, want_scores: bool = False,
 # the other layers of a hybrid model: convolution, selective scan, window attention
 
 
-def _same_device(first, **others):
-    """Index of the CUDA device that `first` and every other tensor given live on."""
-    index = first.get_device()
-    if index < 0:
-        raise ValueError("all tensors must live on a CUDA device")
-    for name, t in others.items():
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, the first argument on {first.device}")
-    return index
+_CODES = {torch.float32: LA_DTYPE_F32, torch.bfloat16: LA_DTYPE_BF16}
 
 
-def _expect(name, t, shape, dtype, contiguous=True):
-    if t is None:
-        return
+def _code(t: torch.dtype) -> int:
+    c = _CODES.get(t)
+    return _dtype_code(t) if c is None else c
+
+
+def _refuse(index, name, t, shape, dtype, whole):
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"all tensors must live on one CUDA device: {name} is on {t.device}")
     if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if contiguous:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    elif t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
-        raise ValueError(f"the last axis of {name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous" if whole else f"the last axis of {name} must be contiguous")
 
 
-def _axis_stride(t, i):
-    """Stride of axis i; 0 where the axis has one entry and its stride says nothing."""
-    return t.stride(i) if t.shape[i] > 1 else 0
+def _check(index, *expected):
+    """expected: (name, tensor or None, shape, dtype, whole): every tensor on CUDA device `index`, of that shape and
+    type, contiguous as a whole or along its last axis."""
+    for name, t, shape, dtype, whole in expected:
+        if t is None:
+            continue
+        if (index < 0 or t.get_device() != index or t.shape != shape or t.dtype is not dtype
+                or not (t.is_contiguous() if whole else shape[-1] <= 1 or t.stride(-1) == 1 or not t.numel())):
+            _refuse(index, name, t, shape, dtype, whole)
 
 
-def _rows3(t) -> LATensor:
-    """[B,N,C] tensor -> view (stride_h unused); None -> a null view."""
-    return LATensor(None, 0, 0, 0) if t is None else LATensor(t.data_ptr(), _axis_stride(t, 0), 0, _axis_stride(t, 1))
+def _rows(t):
+    """[B,N,C] tensor -> the words of a view (stride_h unused; the stride of an axis with one entry says nothing)."""
+    if t is None:
+        return 0, 0, 0, 0
+    (B, N, _), (sb, st, _) = t.shape, t.stride()
+    return t.data_ptr(), sb if B > 1 else 0, 0, st if N > 1 else 0
 
 
-def _heads4(t) -> LATensor:
-    return LATensor(t.data_ptr(), *(_axis_stride(t, i) for i in range(3)))
+def _row(t):
+    """[S,C] tensor -> the words of a view."""
+    return (0, 0, 0, 0) if t is None else (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, 0, 0)
+
+
+def _heads(t):
+    """[B,H,N,d] tensor -> the words of a view."""
+    (B, H, N, _), (sb, sh, st, _) = t.shape, t.stride()
+    return t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0, st if N > 1 else 0
+
+
+def _address(t):
+    return 0 if t is None else t.data_ptr()
 
 
 def _new_rows(shape, dtype, device, zero=False):
@@ -654,15 +668,32 @@ def _new_rows(shape, dtype, device, zero=False):
     return make((*shape[:-1], -(-shape[-1] // 8) * 8), dtype=dtype, device=device)[..., :shape[-1]]
 
 
-def _call(fn_name, index, stream, *args):
-    """Call an entry point with device `index` current, on `stream` or that device's current stream."""
-    fn = getattr(load_library(), fn_name)
+# The argument structs of include/la.h as words, for one pack() a call (the ctypes structures above describe the
+# same bytes).
+_CONV_PREFILL = struct.Struct("<4q3i4x8q5qi4x")
+_CONV_DECODE = struct.Struct("<3q3i4x8qi4x")
+_SSM_PREFILL = struct.Struct("<5q2i24q6qi4x")
+_SSM_DECODE = struct.Struct("<4q2i24q5qi4x")
+_SWA_PREFILL = struct.Struct("<7q2i16q2f3q1q3q")
+_SWA_BIASED_DECODE = struct.Struct("<4q2i7qf4xqf4xq")
+_packed = {}
+
+
+def _call(fn_name, index, stream, args, *more):
+    """Call an entry point with its packed arguments, device `index` current, on `stream` or that device's current
+    stream."""
+    fn = _packed.get(fn_name)
+    if fn is None or fn[0] is not _lib:
+        f = load_library()[fn_name]  # a function object of its own: it takes the packed bytes
+        f.restype = ctypes.c_int
+        f.argtypes = [ctypes.c_char_p, *([ctypes.c_void_p, ctypes.c_size_t] if more else []), ctypes.c_void_p]
+        fn = _packed[fn_name] = (_lib, f)
     handle = _stream_handle(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(index)
-    if torch.cuda.current_device() == index:
-        st = fn(*args, handle)
+    if torch._C._cuda_getDevice() == index:
+        st = fn[1](args, *more, handle)
     else:
         with torch.cuda.device(index):
-            st = fn(*args, handle)
+            st = fn[1](args, *more, handle)
     if st != LA_OK:
         raise LAError(st, fn_name)
 
@@ -676,27 +707,24 @@ def la_conv_prefill(x, w, bias=None, state_in=None, lens=None, silu: bool = True
     [B,W-1,C] in x's dtype, the last inputs, oldest first (None: zeros; state_out
     may be state_in).  lens: None or int64 [B] on the device: later tokens are
     padding, their rows of y stay as they were (zeros in a y made here)."""
-    index = _same_device(x, w=w, bias=bias, state_in=state_in, lens=lens, y=y, state_out=state_out)
     if x.dim() != 3 or w.dim() != 2:
         raise ValueError("x must be [B,N,C] and w [C,W]")
+    index, xt, wt = x.get_device(), x.dtype, w.dtype
     B, N, C = x.shape
     W = w.shape[1]
-    _expect("x", x, (B, N, C), x.dtype, contiguous=False)
-    _expect("w", w, (C, W), w.dtype)
-    _expect("bias", bias, (C,), w.dtype)
-    _expect("lens", lens, (B,), torch.int64)
-    for name, t in (("state_in", state_in), ("state_out", state_out)):
-        _expect(name, t, (B, W - 1, C), x.dtype)
     if y is None:
-        y = _new_rows((B, N, C), out_dtype or x.dtype, x.device, zero=lens is not None)
-    _expect("y", y, (B, N, C), y.dtype, contiguous=False)
+        y = _new_rows((B, N, C), out_dtype or xt, x.device, zero=lens is not None)
+    held = (B, W - 1, C)
+    _check(index, ("x", x, (B, N, C), xt, False), ("w", w, (C, W), wt, True), ("bias", bias, (C,), wt, True),
+           ("lens", lens, (B,), torch.int64, True), ("state_in", state_in, held, xt, True),
+           ("state_out", state_out, held, xt, True), ("y", y, (B, N, C), y.dtype, False))
     if state_out is None:
-        state_out = torch.empty((B, max(W - 1, 0), C), dtype=x.dtype, device=x.device)
+        state_out = torch.empty((B, max(W - 1, 0), C), dtype=xt, device=x.device)
         if lens is not None:  # a sequence whose length is out of range is left as it was
             state_out.copy_(state_in) if state_in is not None else state_out.zero_()
-    a = ConvPrefillArgs(B, N, C, W, _dtype_code(x.dtype), _dtype_code(y.dtype), _dtype_code(w.dtype), _rows3(x),
-                        _rows3(y), _ptr(w), _ptr(bias), _ptr(state_in), _ptr(state_out), _ptr(lens), int(bool(silu)))
-    _call("la_conv_prefill", index, stream, ctypes.byref(a))
+    _call("la_conv_prefill", index, stream,
+          _CONV_PREFILL.pack(B, N, C, W, _code(xt), _code(y.dtype), _code(wt), *_rows(x), *_rows(y), w.data_ptr(),
+                             _address(bias), _address(state_in), state_out.data_ptr(), _address(lens), bool(silu)))
     return y, state_out
 
 
@@ -705,37 +733,43 @@ def la_conv_decode_step(x, w, state, bias=None, silu: bool = True, out=None, sta
     """The convolution's step for one token of each sequence.  x: [S,C] (rows
     16-byte aligned); w, bias as in la_conv_prefill; state: [S,W-1,C], updated in
     place unless state_out is given.  Returns out [S,C]."""
-    index = _same_device(x, w=w, state=state, bias=bias, out=out, state_out=state_out)
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [S,C] and w [C,W]")
+    index, xt, wt = x.get_device(), x.dtype, w.dtype
     S, C = x.shape
     W = w.shape[1]
     state_out = state if state_out is None else state_out
-    _expect("x", x, (S, C), x.dtype, contiguous=False)
-    _expect("w", w, (C, W), w.dtype)
-    _expect("bias", bias, (C,), w.dtype)
-    _expect("state", state, (S, W - 1, C), x.dtype)
-    _expect("state_out", state_out, (S, W - 1, C), x.dtype)
     if out is None:
-        out = _new_rows((S, C), out_dtype or x.dtype, x.device)
-    _expect("out", out, (S, C), out.dtype, contiguous=False)
-    a = ConvDecodeArgs(S, C, W, _dtype_code(x.dtype), _dtype_code(out.dtype), _dtype_code(w.dtype), _ptr(x),
-                       _axis_stride(x, 0), _ptr(out), _axis_stride(out, 0), _ptr(w), _ptr(bias), _ptr(state),
-                       _ptr(state_out), int(bool(silu)))
-    _call("la_conv_decode_step", index, stream, ctypes.byref(a))
+        out = _new_rows((S, C), out_dtype or xt, x.device)
+    held = (S, W - 1, C)
+    _check(index, ("x", x, (S, C), xt, False), ("w", w, (C, W), wt, True), ("bias", bias, (C,), wt, True),
+           ("state", state, held, xt, True), ("state_out", state_out, held, xt, True),
+           ("out", out, (S, C), out.dtype, False))
+    _call("la_conv_decode_step", index, stream,
+          _CONV_DECODE.pack(S, C, W, _code(xt), _code(out.dtype), _code(wt), *_row(x)[:2], *_row(out)[:2],
+                            w.data_ptr(), _address(bias), state.data_ptr(), state_out.data_ptr(), bool(silu)))
     return out
 
 
 def _ssm_prefill_args(u, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus, h_in, lens, y, h_out):
     B, N, C = u.shape
-    return SsmPrefillArgs(B, N, C, A.shape[1], Bm.shape[1], _dtype_code(u.dtype), _dtype_code(y.dtype), _rows3(u),
-                          _rows3(delta), _rows3(z), _rows3(y), _heads4(Bm), _heads4(Cm), _ptr(A), _ptr(D),
-                          _ptr(delta_bias), _ptr(h_in), _ptr(h_out), _ptr(lens), int(bool(delta_softplus)))
+    return _SSM_PREFILL.pack(B, N, C, A.shape[1], Bm.shape[1], _code(u.dtype), _code(y.dtype), *_rows(u),
+                             *_rows(delta), *_rows(z), *_rows(y), *_heads(Bm), *_heads(Cm), A.data_ptr(), _address(D),
+                             _address(delta_bias), _address(h_in), _address(h_out), _address(lens),
+                             bool(delta_softplus))
+
+
+def _ssm_workspace_size(args) -> int:
+    f = _packed.get("la_ssm_prefill_workspace_size")
+    if f is None or f[0] is not _lib:
+        fn = load_library()["la_ssm_prefill_workspace_size"]
+        fn.restype, fn.argtypes = ctypes.c_size_t, [ctypes.c_char_p]
+        f = _packed["la_ssm_prefill_workspace_size"] = (_lib, fn)
+    return f[1](args)
 
 
 def la_ssm_prefill_workspace_size(u, delta, A, Bm, Cm) -> int:
-    a = _ssm_prefill_args(u, delta, A, Bm, Cm, None, None, None, True, None, None, u, None)
-    return int(load_library().la_ssm_prefill_workspace_size(ctypes.byref(a)))
+    return _ssm_workspace_size(_ssm_prefill_args(u, delta, A, Bm, Cm, None, None, None, True, None, None, u, None))
 
 
 def la_ssm_prefill(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, delta_softplus: bool = True, h_in=None,
@@ -750,34 +784,27 @@ def la_ssm_prefill(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, delta_s
     delta_bias: fp32 [C] or None; h: fp32 [B,C,n] (h_out may be h_in); lens as in
     la_conv_prefill; workspace: uint8 device tensor of at least
     la_ssm_prefill_workspace_size bytes, allocated here by default."""
-    index = _same_device(u, delta=delta, A=A, Bm=Bm, Cm=Cm, D=D, z=z, delta_bias=delta_bias, h_in=h_in, lens=lens, y=y,
-                 h_out=h_out, workspace=workspace)
     if u.dim() != 3 or A.dim() != 2 or Bm.dim() != 4:
         raise ValueError("u must be [B,N,C], A [C,n] and Bm, Cm [B,G,N,n]")
-    B, N, C = u.shape
+    index, ut, f32 = u.get_device(), u.dtype, torch.float32
+    B, N, C = rows = tuple(u.shape)
     n, G = A.shape[1], Bm.shape[1]
-    for name, t in (("u", u), ("delta", delta), ("z", z)):
-        _expect(name, t, (B, N, C), u.dtype, contiguous=False)
-    for name, t in (("Bm", Bm), ("Cm", Cm)):
-        _expect(name, t, (B, G, N, n), u.dtype, contiguous=False)
-    _expect("A", A, (C, n), torch.float32)
-    for name, t in (("D", D), ("delta_bias", delta_bias)):
-        _expect(name, t, (C,), torch.float32)
-    for name, t in (("h_in", h_in), ("h_out", h_out)):
-        _expect(name, t, (B, C, n), torch.float32)
-    _expect("lens", lens, (B,), torch.int64)
     if y is None:
-        y = _new_rows((B, N, C), out_dtype or u.dtype, u.device, zero=lens is not None)
-    _expect("y", y, (B, N, C), y.dtype, contiguous=False)
+        y = _new_rows(rows, out_dtype or ut, u.device, zero=lens is not None)
+    _check(index, ("u", u, rows, ut, False), ("delta", delta, rows, ut, False), ("z", z, rows, ut, False),
+           ("Bm", Bm, (B, G, N, n), ut, False), ("Cm", Cm, (B, G, N, n), ut, False), ("A", A, (C, n), f32, True),
+           ("D", D, (C,), f32, True), ("delta_bias", delta_bias, (C,), f32, True), ("h_in", h_in, (B, C, n), f32, True),
+           ("h_out", h_out, (B, C, n), f32, True), ("lens", lens, (B,), torch.int64, True),
+           ("y", y, rows, y.dtype, False))
     if h_out is None:
-        h_out = torch.empty((B, C, n), dtype=torch.float32, device=u.device)
+        h_out = torch.empty((B, C, n), dtype=f32, device=u.device)
         if lens is not None:
             h_out.copy_(h_in) if h_in is not None else h_out.zero_()
     a = _ssm_prefill_args(u, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus, h_in, lens, y, h_out)
-    need = int(load_library().la_ssm_prefill_workspace_size(ctypes.byref(a)))
-    ws, ws_bytes = _workspace(need, workspace, u.device)
-    _call("la_ssm_prefill", index, stream, ctypes.byref(a), _ptr(ws) if isinstance(ws, torch.Tensor) else ws,
-          ws_bytes)
+    ws, ws_bytes = _workspace(_ssm_workspace_size(a), workspace, u.device)
+    if workspace is not None and workspace.get_device() != index:
+        raise ValueError("workspace must live on the device of the inputs")
+    _call("la_ssm_prefill", index, stream, a, ws.data_ptr() if isinstance(ws, torch.Tensor) else ws, ws_bytes)
     return y, h_out
 
 
@@ -786,31 +813,25 @@ def la_ssm_decode_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=No
     """The scan's step for one token of each sequence.  u, delta, z: [S,C]; Bm,
     Cm: [S,G,n]; state: fp32 [S,C,n], updated in place unless state_out is given;
     the rest as in la_ssm_prefill.  Returns out [S,C]."""
-    index = _same_device(u, delta=delta, A=A, Bm=Bm, Cm=Cm, state=state, D=D, z=z, delta_bias=delta_bias, out=out,
-                 state_out=state_out)
     if u.dim() != 2 or A.dim() != 2 or Bm.dim() != 3:
         raise ValueError("u must be [S,C], A [C,n] and Bm, Cm [S,G,n]")
-    S, C = u.shape
+    index, ut, f32 = u.get_device(), u.dtype, torch.float32
+    S, C = rows = tuple(u.shape)
     n, G = A.shape[1], Bm.shape[1]
     state_out = state if state_out is None else state_out
-    for name, t in (("u", u), ("delta", delta), ("z", z)):
-        _expect(name, t, (S, C), u.dtype, contiguous=False)
-    for name, t in (("Bm", Bm), ("Cm", Cm)):
-        _expect(name, t, (S, G, n), u.dtype, contiguous=False)
-    _expect("A", A, (C, n), torch.float32)
-    for name, t in (("D", D), ("delta_bias", delta_bias)):
-        _expect(name, t, (C,), torch.float32)
-    for name, t in (("state", state), ("state_out", state_out)):
-        _expect(name, t, (S, C, n), torch.float32)
     if out is None:
-        out = torch.empty((S, C), dtype=out_dtype or u.dtype, device=u.device)
-    _expect("out", out, (S, C), out.dtype, contiguous=False)
-    row = lambda t: LATensor(None, 0, 0, 0) if t is None else LATensor(t.data_ptr(), _axis_stride(t, 0), 0, 0)  # noqa: E731
-    grp = lambda t: LATensor(t.data_ptr(), _axis_stride(t, 0), _axis_stride(t, 1), 0)  # noqa: E731
-    a = SsmDecodeArgs(S, C, n, G, _dtype_code(u.dtype), _dtype_code(out.dtype), row(u), row(delta), row(z), row(out),
-                      grp(Bm), grp(Cm), _ptr(A), _ptr(D), _ptr(delta_bias), _ptr(state), _ptr(state_out),
-                      int(bool(delta_softplus)))
-    _call("la_ssm_decode_step", index, stream, ctypes.byref(a))
+        out = torch.empty(rows, dtype=out_dtype or ut, device=u.device)
+    _check(index, ("u", u, rows, ut, False), ("delta", delta, rows, ut, False), ("z", z, rows, ut, False),
+           ("Bm", Bm, (S, G, n), ut, False), ("Cm", Cm, (S, G, n), ut, False), ("A", A, (C, n), f32, True),
+           ("D", D, (C,), f32, True), ("delta_bias", delta_bias, (C,), f32, True), ("state", state, (S, C, n), f32, True),
+           ("state_out", state_out, (S, C, n), f32, True), ("out", out, rows, out.dtype, False))
+    many, groups = S > 1, G > 1
+    _call("la_ssm_decode_step", index, stream,
+          _SSM_DECODE.pack(S, C, n, G, _code(ut), _code(out.dtype), *_row(u), *_row(delta), *_row(z), *_row(out),
+                           Bm.data_ptr(), Bm.stride(0) if many else 0, Bm.stride(1) if groups else 0, 0,
+                           Cm.data_ptr(), Cm.stride(0) if many else 0, Cm.stride(1) if groups else 0, 0,
+                           A.data_ptr(), _address(D), _address(delta_bias), state.data_ptr(), state_out.data_ptr(),
+                           bool(delta_softplus)))
     return out
 
 
@@ -828,29 +849,24 @@ def la_swa_prefill(q, k, v, window: int = 0, scale: float | None = None, softcap
     lens: None or int64 [B]: later keys are not seen and later queries' rows of o
     stay as they were.  k_cache, v_cache: [B,H_kv,window,d] rings to fill for
     la_swa_decode_step and la_swa_biased_decode_step (window <= 256)."""
-    index = _same_device(q, k=k, v=v, slopes=slopes, key_lo=key_lo, key_hi=key_hi, lens=lens, o=o, k_cache=k_cache,
-                 v_cache=v_cache)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B,H,Nq,d] and k, v [B,H_kv,Nk,d]")
-    B, H, Nq, d = q.shape
-    Hkv, Nk = k.shape[1], k.shape[2]
-    _expect("q", q, (B, H, Nq, d), q.dtype, contiguous=False)
-    for name, t in (("k", k), ("v", v)):
-        _expect(name, t, (B, Hkv, Nk, d), q.dtype, contiguous=False)
-    _expect("slopes", slopes, (H,), torch.float32)
-    for name, t in (("key_lo", key_lo), ("key_hi", key_hi)):
-        _expect(name, t, (B, Nq), torch.int32)
-    _expect("lens", lens, (B,), torch.int64)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _expect(name, t, (B, Hkv, window, d), q.dtype)
+    index, qt, i32 = q.get_device(), q.dtype, torch.int32
+    B, H, Nq, d = queries = tuple(q.shape)
+    keys = tuple(k.shape)
+    Hkv, Nk, window = keys[1], keys[2], int(window)
     if o is None:
-        o = (torch.zeros if lens is not None else torch.empty)((B, H, Nq, d), dtype=out_dtype or q.dtype, device=q.device)
-    _expect("o", o, (B, H, Nq, d), o.dtype, contiguous=False)
-    a = SwaPrefillArgs(B, H, Hkv, Nq, Nk, d, int(window), _dtype_code(q.dtype), _dtype_code(o.dtype), _heads4(q),
-                       _heads4(k), _heads4(v), _heads4(o), float(scale if scale is not None else d ** -0.5),
-                       float(softcap), _ptr(slopes), _ptr(key_lo), _ptr(key_hi),
-                       int(q_pos0 if q_pos0 is not None else Nk - Nq), _ptr(lens), _ptr(k_cache), _ptr(v_cache))
-    _call("la_swa_prefill", index, stream, ctypes.byref(a))
+        o = (torch.zeros if lens is not None else torch.empty)(queries, dtype=out_dtype or qt, device=q.device)
+    _check(index, ("q", q, queries, qt, False), ("k", k, (B, Hkv, Nk, d), qt, False), ("v", v, (B, Hkv, Nk, d), qt, False),
+           ("slopes", slopes, (H,), torch.float32, True), ("key_lo", key_lo, (B, Nq), i32, True),
+           ("key_hi", key_hi, (B, Nq), i32, True), ("lens", lens, (B,), torch.int64, True),
+           ("k_cache", k_cache, (B, Hkv, window, d), qt, True), ("v_cache", v_cache, (B, Hkv, window, d), qt, True),
+           ("o", o, queries, o.dtype, False))
+    _call("la_swa_prefill", index, stream,
+          _SWA_PREFILL.pack(B, H, Hkv, Nq, Nk, d, window, _code(qt), _code(o.dtype), *_heads(q), *_heads(k), *_heads(v),
+                            *_heads(o), scale if scale is not None else d ** -0.5, softcap, _address(slopes),
+                            _address(key_lo), _address(key_hi), q_pos0 if q_pos0 is not None else Nk - Nq,
+                            _address(lens), _address(k_cache), _address(v_cache)))
     return o
 
 
@@ -859,26 +875,21 @@ def la_swa_biased_decode_step(q, k, v, k_cache, v_cache, pos, softcap: float = 0
     """la_swa_decode_step with grouped heads, capped scores and a distance bias:
     q: [S,H,d]; k, v: [S,H_kv,d]; k_cache, v_cache: [S,H_kv,window,d]; pos: int64
     [S]; softcap and slopes as in la_swa_prefill.  Returns out [S,H,d]."""
-    index = _same_device(q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, pos=pos, slopes=slopes, out=out)
     if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [S,H,d], k, v [S,H_kv,d] and the caches [S,H_kv,window,d]")
-    S, H, d = q.shape
+    index, qt = q.get_device(), q.dtype
+    S, H, d = heads = tuple(q.shape)
     Hkv, window = k.shape[1], k_cache.shape[2]
-    _expect("q", q, (S, H, d), q.dtype)
-    for name, t in (("k", k), ("v", v)):
-        _expect(name, t, (S, Hkv, d), q.dtype)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _expect(name, t, (S, Hkv, window, d), q.dtype)
-    _expect("pos", pos, (S,), torch.int64)
-    _expect("slopes", slopes, (H,), torch.float32)
     if out is None:
-        out = torch.empty((S, H, d), dtype=out_dtype or q.dtype, device=q.device)
-    _expect("out", out, (S, H, d), out.dtype)
-    base = SwaDecodeArgs(S, H, d, window, _dtype_code(q.dtype), _dtype_code(out.dtype), _ptr(q), _ptr(k), _ptr(v),
-                         _ptr(k_cache), _ptr(v_cache), _ptr(pos), _ptr(out),
-                         float(scale if scale is not None else d ** -0.5))
-    a = SwaBiasedDecodeArgs(base, Hkv, float(softcap), _ptr(slopes))
-    _call("la_swa_biased_decode_step", index, stream, ctypes.byref(a))
+        out = torch.empty(heads, dtype=out_dtype or qt, device=q.device)
+    ring = (S, Hkv, window, d)
+    _check(index, ("q", q, heads, qt, True), ("k", k, (S, Hkv, d), qt, True), ("v", v, (S, Hkv, d), qt, True),
+           ("k_cache", k_cache, ring, qt, True), ("v_cache", v_cache, ring, qt, True), ("pos", pos, (S,), torch.int64, True),
+           ("slopes", slopes, (H,), torch.float32, True), ("out", out, heads, out.dtype, True))
+    _call("la_swa_biased_decode_step", index, stream,
+          _SWA_BIASED_DECODE.pack(S, H, d, window, _code(qt), _code(out.dtype), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                  k_cache.data_ptr(), v_cache.data_ptr(), pos.data_ptr(), out.data_ptr(),
+                                  scale if scale is not None else d ** -0.5, Hkv, softcap, _address(slopes)))
     return out
 
 

@@ -167,8 +167,33 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(lib):
         la.la_ssm_prefill(x, x, torch.zeros((8, 4)), torch.zeros((1, 1, 4, 4)), torch.zeros((1, 1, 4, 4)))
     with pytest.raises(ValueError):
         la.la_swa_prefill(torch.zeros((1, 2, 4, 8)), torch.zeros((1, 2, 4, 8)), torch.zeros((1, 2, 4, 8)))
-    for bad in (dict(shape=(1, 2), dtype=torch.float32), dict(shape=(2, 2), dtype=torch.bfloat16)):
+    t = torch.zeros((2, 4))
+    for bad in (("t", t, (1, 4), torch.float32, True), ("t", t, (2, 4), torch.bfloat16, True), ("t", t, (2, 4), torch.float32, True)):
         with pytest.raises(ValueError):
-            la._expect("t", torch.zeros((2, 2)), **bad)
+            la._check(t.get_device(), bad)  # a host tensor's index is -1: refused whatever its shape
     with pytest.raises(ValueError):
-        la._expect("t", torch.zeros((2, 4))[:, ::2], (2, 2), torch.float32, contiguous=False)
+        la._refuse(-1, *("t", t, (2, 4), torch.float32, True))
+
+
+def test_packed_arguments_are_the_structures_bytes():
+    """The binding packs each argument struct in one call: the same bytes as the ctypes structure of the header."""
+    T4 = lambda k: T(at(k), 1 + k, 2 + k, 3 + k)  # noqa: E731
+    W4 = lambda k: (at(k), 1 + k, 2 + k, 3 + k)  # noqa: E731
+    cases = [
+        (la._CONV_PREFILL, la.ConvPrefillArgs(1, 2, 3, 4, 1, 0, 1, T4(0), T4(1), at(2), at(3), at(4), at(5), at(6), 1),
+         (1, 2, 3, 4, 1, 0, 1, *W4(0), *W4(1), at(2), at(3), at(4), at(5), at(6), 1)),
+        (la._CONV_DECODE, la.ConvDecodeArgs(1, 2, 3, 1, 0, 1, at(0), 5, at(1), 6, at(2), at(3), at(4), at(5), 1),
+         (1, 2, 3, 1, 0, 1, at(0), 5, at(1), 6, at(2), at(3), at(4), at(5), 1)),
+        (la._SSM_PREFILL, la.SsmPrefillArgs(1, 2, 3, 4, 5, 1, 0, *(T4(k) for k in range(6)), *(at(k) for k in range(6, 12)), 1),
+         (1, 2, 3, 4, 5, 1, 0, *(w for k in range(6) for w in W4(k)), *(at(k) for k in range(6, 12)), 1)),
+        (la._SSM_DECODE, la.SsmDecodeArgs(1, 2, 3, 4, 1, 0, *(T4(k) for k in range(6)), *(at(k) for k in range(6, 11)), 1),
+         (1, 2, 3, 4, 1, 0, *(w for k in range(6) for w in W4(k)), *(at(k) for k in range(6, 11)), 1)),
+        (la._SWA_PREFILL, la.SwaPrefillArgs(1, 2, 3, 4, 5, 6, 7, 1, 0, *(T4(k) for k in range(4)), 0.5, 2.5, at(4), at(5), at(6), 9, at(7),
+                                            at(8), at(9)),
+         (1, 2, 3, 4, 5, 6, 7, 1, 0, *(w for k in range(4) for w in W4(k)), 0.5, 2.5, at(4), at(5), at(6), 9, at(7), at(8), at(9))),
+        (la._SWA_BIASED_DECODE, la.SwaBiasedDecodeArgs(la.SwaDecodeArgs(1, 2, 3, 4, 1, 0, *(at(k) for k in range(7)), 0.5), 8, 1.5, at(9)),
+         (1, 2, 3, 4, 1, 0, *(at(k) for k in range(7)), 0.5, 8, 1.5, at(9))),
+    ]
+    for packer, struct, words in cases:
+        assert packer.size == ctypes.sizeof(struct)
+        assert packer.pack(*words) == bytes(struct)
