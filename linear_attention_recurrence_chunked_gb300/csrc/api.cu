@@ -479,7 +479,7 @@ la_status la_conv_decode_step(const la_conv_decode_args* a, void* stream) {
 
 static bool ssm_shape(const la_ssm_prefill_args* a) {
   return a && a->B > 0 && a->C > 0 && a->G > 0 && a->B <= 65535 && a->C % a->G == 0 && valid_size(a->N) && a->n >= 1 && a->n <= 64 &&
-         a->C <= kMaxDim && within(kMaxElems, {a->B, a->C, a->n}) && within(kMaxElems, {a->B, a->N + 1, a->C});
+         a->C <= INT32_MAX / 64 && a->N <= INT32_MAX / 2 && within(kMaxElems, {a->B, a->C, a->n}) && within(kMaxElems, {a->B, a->N + 1, a->C});
 }
 
 size_t la_ssm_prefill_workspace_size(const la_ssm_prefill_args* a) {
@@ -525,7 +525,7 @@ la_status la_ssm_decode_step(const la_ssm_decode_args* a, void* stream) {
   if (!valid_dtype(a->in_dtype) || !valid_dtype(a->out_dtype)) return LA_ERR_INVALID_ARGUMENT;
   if (a->n < 1 || a->n > 64) return LA_ERR_UNSUPPORTED;
   if (a->S == 0 || a->C == 0) return LA_OK;
-  if (a->S > 4 * 65535 || !within(kMaxElems, {a->S, a->C, a->n})) return LA_ERR_UNSUPPORTED;
+  if (a->S > 4 * 65535 || a->C > INT32_MAX / 64 || !within(kMaxElems, {a->S, a->C, a->n})) return LA_ERR_UNSUPPORTED;
   for (const la_tensor* t : {&a->u, &a->delta, &a->Bm, &a->Cm})
     if (!valid_elem(t->ptr, a->in_dtype) || !valid_strides(*t)) return LA_ERR_INVALID_ARGUMENT;
   if (a->z.ptr && (!valid_elem(a->z.ptr, a->in_dtype) || !valid_strides(a->z))) return LA_ERR_INVALID_ARGUMENT;

@@ -422,28 +422,18 @@ ssm_combine_kernel(const SsmLaunch a, Segments seg, float* ws_h, const float* ws
 constexpr int kStepThreads = 256;
 constexpr int kStepSeqs = 4;
 
-template <typename T>
-__device__ __forceinline__ void load_states(const T* p, int count, bool vec, float (&o)[kK]) {
-  if (vec) {
-    const float4 x = load4(p);
-    o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
-  } else {
-#pragma unroll
-    for (int k = 0; k < kK; ++k) o[k] = k < count ? to_f(p[k]) : 0.f;
-  }
-}
-
 template <int L, typename TIn, typename TOut>
 __global__ void __launch_bounds__(kStepThreads)
-ssm_decode_kernel(const SsmLaunch a, bool bc_vec) {
+ssm_decode_kernel(const SsmLaunch a, bool a_vec, bool bc_vec) {
   constexpr int NQ = L >= kStepSeqs ? 1 : kStepSeqs / L;  // sequences whose gates this lane computes
   const int tid = threadIdx.x, l = tid % L;
   const int64_t c = (int64_t)blockIdx.x * (kStepThreads / L) + tid / L;
   const int64_t s0 = (int64_t)blockIdx.y * kStepSeqs;
   const bool live = c < a.C;
-  const int64_t cc = live ? c : 0, g = cc / (a.C / a.G);
-  const int s_lo = l * kK, count = min(kK, a.n - s_lo);
-  const bool on = live && count > 0, vec = a.n % kK == 0;
+  const int64_t cc = live ? c : 0;
+  const int g = a.G == 1 ? 0 : (int)cc / ((int)a.C / (int)a.G);  // channels are 32-bit here
+  const int s_lo = l * kK, count = max(0, min(kK, a.n - s_lo));
+  const bool on = live && count > 0, vec = a_vec;
   const int q_own = L >= kStepSeqs ? l / (L >= kStepSeqs ? L / kStepSeqs : 1) : l * NQ;
   grid_dependents_trigger();
   grid_dependency_wait();  // the states and this step's inputs are in memory
@@ -463,29 +453,53 @@ ssm_decode_kernel(const SsmLaunch a, bool bc_vec) {
       }
     }
   }
-  float A2[kK];
+  // everything else that the step reads, behind the states and before any of it is used
+  Raw4<TIn> Br[kStepSeqs], Cr[kStepSeqs];
 #pragma unroll
-  for (int k = 0; k < kK; ++k) A2[k] = k < count ? log2_rate(a.A[cc * a.n + s_lo + k]) : 0.f;
-  const float bias = a.delta_bias ? a.delta_bias[cc] : 0.f;
-  float u_own[NQ], dt_own[NQ];
+  for (int q = 0; q < kStepSeqs; ++q) {
+    const int64_t s = min(s0 + q, a.B - 1);
+    const TIn* Bp = reinterpret_cast<const TIn*>(a.Bm.ptr) + s * a.Bm.sb + g * a.Bm.sh + s_lo;
+    const TIn* Cp = reinterpret_cast<const TIn*>(a.Cm.ptr) + s * a.Cm.sb + g * a.Cm.sh + s_lo;
+    if (bc_vec && count > 0) {
+      Br[q].load(Bp);
+      Cr[q].load(Cp);
+    } else {
+      Br[q].load(Bp, count);
+      Cr[q].load(Cp, count);
+    }
+  }
+  float u_own[NQ], dt_own[NQ], z_own[NQ];
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
     const int64_t s = min(s0 + q_own + i, a.B - 1);
     u_own[i] = to_f(reinterpret_cast<const TIn*>(a.u)[s * a.u_sb + cc]);
-    const float x = to_f(reinterpret_cast<const TIn*>(a.delta)[s * a.d_sb + cc]) + bias;
+    dt_own[i] = to_f(reinterpret_cast<const TIn*>(a.delta)[s * a.d_sb + cc]);
+    z_own[i] = a.z ? to_f(reinterpret_cast<const TIn*>(a.z)[s * a.z_sb + cc]) : 0.f;
+  }
+  const float bias = a.delta_bias ? a.delta_bias[cc] : 0.f, skip = a.D ? a.D[cc] : 0.f;
+  float A2[kK];
+  if (vec && count > 0) {
+    const float4 x = *reinterpret_cast<const float4*>(a.A + cc * a.n + s_lo);
+    A2[0] = log2_rate(x.x); A2[1] = log2_rate(x.y); A2[2] = log2_rate(x.z); A2[3] = log2_rate(x.w);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kK; ++k) A2[k] = k < count ? log2_rate(a.A[cc * a.n + s_lo + k]) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const float x = dt_own[i] + bias;
     dt_own[i] = a.softplus ? softplus(x) : x;
   }
   float acc[kStepSeqs];
   const int group_lane = (tid & 31) - l;
 #pragma unroll
   for (int q = 0; q < kStepSeqs; ++q) {
-    const int64_t s = min(s0 + q, a.B - 1);
     const int src = group_lane + (L >= kStepSeqs ? q * (L / kStepSeqs) : q / NQ);
     const float dt = L == 1 ? dt_own[q % NQ] : __shfl_sync(kFullMask, dt_own[q % NQ], src);
     const float u = L == 1 ? u_own[q % NQ] : __shfl_sync(kFullMask, u_own[q % NQ], src);
     float Bk[kK], Ck[kK];
-    load_states(reinterpret_cast<const TIn*>(a.Bm.ptr) + s * a.Bm.sb + g * a.Bm.sh + s_lo, count, bc_vec && count > 0, Bk);
-    load_states(reinterpret_cast<const TIn*>(a.Cm.ptr) + s * a.Cm.sb + g * a.Cm.sh + s_lo, count, bc_vec && count > 0, Ck);
+    Br[q].unpack(Bk);
+    Cr[q].unpack(Ck);
     const float dtu = dt * u;
     acc[q] = 0.f;
 #pragma unroll
@@ -525,13 +539,12 @@ ssm_decode_kernel(const SsmLaunch a, bool bc_vec) {
     }
   }
   if (live && (L < kStepSeqs || l % (L >= kStepSeqs ? L / kStepSeqs : 1) == 0)) {
-    const float skip = a.D ? a.D[c] : 0.f;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const int64_t s = s0 + q_own + i;
       if (s < a.B) {
         float o = fmaf(skip, u_own[i], y[i]);
-        if (a.z) o *= silu(to_f(reinterpret_cast<const TIn*>(a.z)[s * a.z_sb + c]));
+        if (a.z) o *= silu(z_own[i]);
         store1(reinterpret_cast<TOut*>(a.y) + s * a.y_sb + c, o);
       }
     }
@@ -588,12 +601,13 @@ template <typename TIn, typename TOut>
 cudaError_t launch_lanes(const SsmLaunch& a, void* ws, const Segments* seg, cudaStream_t stream) {
   // four states of B and C in one load: rows of whole quadruples on their boundary
   constexpr int64_t quad = 4 * (int64_t)sizeof(TIn);
+  const bool a_vec = a.n % kK == 0 && (reinterpret_cast<uintptr_t>(a.A) & 15u) == 0;
   const bool bc_vec = a.n % kK == 0 && ((reinterpret_cast<uintptr_t>(a.Bm.ptr) | reinterpret_cast<uintptr_t>(a.Cm.ptr) |
                                          (uintptr_t)((a.Bm.sb | a.Bm.sh | a.Cm.sb | a.Cm.sh) * (int64_t)sizeof(TIn))) % quad) == 0;
   auto step = [&](auto kernel, int L) {
     const int64_t per = kStepThreads / L;
     const dim3 grid((unsigned)((a.C + per - 1) / per), (unsigned)((a.B + kStepSeqs - 1) / kStepSeqs));
-    return launch_dependent(kernel, grid, dim3(kStepThreads), 0, stream, a, bc_vec);
+    return launch_dependent(kernel, grid, dim3(kStepThreads), 0, stream, a, a_vec, bc_vec);
   };
   switch (lanes_of(a.n)) {
     case 1: return seg ? launch_scan<1, TIn, TOut>(a, ws, *seg, stream) : step(ssm_decode_kernel<1, TIn, TOut>, 1);
