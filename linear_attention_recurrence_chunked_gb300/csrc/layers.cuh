@@ -2,10 +2,26 @@
 // attention: 16-byte vectors of either element type, and the scalar functions of their epilogues.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 
 namespace la {
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device; `done` (one per kernel) remembers the
+// devices that know.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // elements of T in a 16-byte vector
 template <typename T>

@@ -17,7 +17,6 @@
 // of the readout are written: the compiler keeps that order (it cannot tell the two apart), and the other one
 // would put a shared-memory round trip, an exponential and four operations in a row for every token.
 #include <algorithm>
-#include <mutex>
 
 #include "layers.cuh"
 #include "tc.cuh"
@@ -571,10 +570,9 @@ template <int L, int kCh, typename TIn, typename TOut, int MODE>
 cudaError_t launch_mode(const SsmLaunch& a, const Segments& seg, int segments, float* ws_h, float* ws_dt, cudaStream_t stream) {
   using T = Tile<L, kCh, TIn>;
   const auto kernel = ssm_scan_kernel<L, kCh, TIn, TOut, MODE>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [&] { attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(T)); });
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kernel, (int)sizeof(T), done);
+  if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(a.G * ((a.C / a.G + T::CT - 1) / T::CT)), (unsigned)a.B, (unsigned)segments);
   kernel<<<grid, block_threads(kCh), sizeof(T), stream>>>(a, seg, ws_h, ws_dt);
   return cudaGetLastError();

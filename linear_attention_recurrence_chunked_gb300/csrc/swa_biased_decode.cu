@@ -14,8 +14,6 @@
 // is the same for the queries.  Values come by asynchronous copies, all 32 rows of a warp at once, and are
 // transposed on the way from shared memory.  The weights are rounded to bf16 for their product, as over a prompt.
 // fp32: CUDA cores, four query heads at a time.
-#include <mutex>
-
 #include "layers.cuh"
 #include "tc.cuh"
 
@@ -408,12 +406,9 @@ swa_biased_decode_kernel(const SwaBiasedDecodeLaunch a) {
 template <typename TOut, int DP>
 cudaError_t launch_mma(const SwaBiasedDecodeLaunch& a, cudaStream_t stream) {
   constexpr int kRegion = kSlots * DP * 2;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(swa_biased_decode_mma_kernel<TOut, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxWarps * kRegion);
-  });
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(swa_biased_decode_mma_kernel<TOut, DP>, kMaxWarps * kRegion, done);
+  if (e != cudaSuccess) return e;
   const int warps = (a.base.window + kSlots - 1) / kSlots;
   return launch_dependent(swa_biased_decode_mma_kernel<TOut, DP>, dim3((unsigned)(a.base.S * a.Hkv)), dim3((unsigned)(32 * warps)),
                           (size_t)(warps * kRegion), stream, a);

@@ -7,9 +7,6 @@
 // A CTA takes 64 queries of one head and walks the key tiles between its lowest lo and highest hi; each
 // of its 256 threads holds a 4 x 4 piece of the scores and 4 rows x d/16 columns of the output.  fp32
 // products run on the CUDA cores (bf16 operands would not keep fp32's accuracy), which bound it.
-#include <algorithm>
-#include <mutex>
-
 #include "layers.cuh"
 #include "swa_common.cuh"
 
@@ -207,12 +204,9 @@ swa_fill_rings_kernel(const SwaPrefillLaunch a) {
 template <typename TIn, typename TOut, int DP>
 cudaError_t launch_simt(const SwaPrefillLaunch& a, cudaStream_t stream) {
   constexpr int kSmem = (3 * 64 * (DP + 4) + kBM * (kBN + 4)) * (int)sizeof(float);
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(swa_simt_kernel<TIn, TOut, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  });
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(swa_simt_kernel<TIn, TOut, DP>, kSmem, done);
+  if (e != cudaSuccess) return e;
   const int q_tiles = (int)((a.Nq + kBM - 1) / kBM);
   swa_simt_kernel<TIn, TOut, DP><<<(unsigned)(a.B * a.H * q_tiles), kThreads, kSmem, stream>>>(a, q_tiles);
   return cudaGetLastError();

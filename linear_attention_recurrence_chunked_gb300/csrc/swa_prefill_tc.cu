@@ -796,6 +796,8 @@ EncodeTiledFn encode_fn() {
 bool encode(CUtensorMap* map, const View4& x, int64_t B, int64_t H, int64_t N, int d, int rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
+  // (an axis repeated with stride 0 is not for a map either)
+  if ((N > 1 && x.st == 0) || (H > 1 && x.sh == 0) || (B > 1 && x.sb == 0)) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)N, (cuuint64_t)H, (cuuint64_t)B};
   // the stride of an axis with one entry is never used, but has to be one that a map can hold
   const cuuint64_t row = (cuuint64_t)d * 2;
@@ -811,16 +813,18 @@ bool encode(CUtensorMap* map, const View4& x, int64_t B, int64_t H, int64_t N, i
 template <int DP, int KB, bool CAP, bool BIAS>
 cudaError_t launch_typed(const SwaPrefillLaunch& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
   using S = Shape<DP, KB>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(swa_tc_kernel<DP, KB, CAP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
-    // the row threads' registers come out of the launch's own: with fewer they would be waited for without end
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(swa_tc_kernel<DP, KB, CAP, BIAS>, (int)S::kSmem, done);
+  if (e != cudaSuccess) return e;
+  // the row threads' registers come out of the launch's own: with fewer they would be waited for without end
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
     cudaFuncAttributes f{};
-    if (attr == cudaSuccess) attr = cudaFuncGetAttributes(&f, swa_tc_kernel<DP, KB, CAP, BIAS>);
-    if (attr == cudaSuccess && f.numRegs < S::kRegs) attr = cudaErrorInvalidConfiguration;
-  });
-  if (attr != cudaSuccess) return attr;
+    e = cudaFuncGetAttributes(&f, swa_tc_kernel<DP, KB, CAP, BIAS>);
+    if (e != cudaSuccess) return e;
+    regs.store(f.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) < S::kRegs) return cudaErrorInvalidConfiguration;
   const int q_tiles = (int)((a.Nq + 2 * kRows - 1) / (2 * kRows));
   const int64_t items = a.B * a.H * q_tiles;
   const unsigned grid = (unsigned)std::min<int64_t>(items, S::kCtas * kSMs);

@@ -468,3 +468,102 @@ def test_steps_captured_and_replayed():
     assert torch.equal(out, want)
     for x, s in zip((conv, h, kc, vc), after):
         assert torch.equal(x, s)
+
+
+# ------------------------------------------------------------------------------------------ larger, repeated, shared
+@pytest.mark.parametrize("B,H,Hkv,N,d,window,softcap,slopes", [
+    (1, 4, 2, 3001, 128, 0, 0.0, False), (1, 4, 2, 2500, 64, 0, 0.0, False), (2, 4, 1, 2049, 128, 0, 30.0, False),
+    (1, 4, 4, 3000, 64, 100, 0.0, False), (1, 2, 2, 2600, 96, 700, 0.0, True), (1, 4, 4, 2300, 64, 0, 4.0, True)])
+def test_swa_long_prompts_sampled_and_repeated(B, H, Hkv, N, d, window, softcap, slopes):
+    """Many blocks a query tile: sampled rows against the definition in fp64, and the same bits every time."""
+    dev = cuda_device()
+    q, k, v = swa_case(B, H, Hkv, N, N, d, BF, N)
+    sl = slopes_of(H) if slopes else None
+    qd, kd, vd, sld = on(dev, q, k, v, sl)
+    o = la.la_swa_prefill(qd, kd, vd, window=window, softcap=softcap, slopes=sld)
+    for _ in range(10):
+        assert torch.equal(la.la_swa_prefill(qd, kd, vd, window=window, softcap=softcap, slopes=sld), o)
+    assert la.la_device_status() == la.LA_OK
+    sample = sorted(set(np.random.default_rng(N).choice(N, 24, replace=False).tolist()) | {0, 127, 128, 255, 256, N - 1})
+    rows = ref.spans(N, N, B, window, None, None, 0, None)
+    rows = [[r if i in sample else None for i, r in enumerate(rb)] for rb in rows]
+    o_ref, bound = ref.swa(q, k, v, d ** -0.5, softcap, sl, rows, 0, BF)
+    ref.check(o, o_ref, bound)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_swa_keys_shared_by_sequences_and_strided_views(dtype):
+    """Keys and values expanded over the batch (stride 0) and heads taken out of one wide projection."""
+    dev = cuda_device()
+    B, H, Hkv, N, d = 3, 4, 2, 200, 64
+    g = gen(2)
+    wide = randn(g, B, N, (H + 2 * Hkv) * d, dtype=dtype, scale=1.5).to(dev)
+    heads = wide.unflatten(-1, (H + 2 * Hkv, d)).transpose(1, 2)
+    q, k, v = heads[:, :H], heads[:, H:H + Hkv], heads[:, H + Hkv:]
+    o = la.la_swa_prefill(q, k, v, window=70)
+    want = la.la_swa_prefill(q.contiguous(), k.contiguous(), v.contiguous(), window=70)
+    assert torch.equal(o, want)
+    ks, vs = k[:1].expand(B, -1, -1, -1), v[:1].expand(B, -1, -1, -1)
+    o = la.la_swa_prefill(q, ks, vs, window=70)
+    rows = ref.spans(N, N, B, 70, None, None, 0, None)
+    o_ref, bound = ref.swa(q.cpu(), ks.cpu(), vs.cpu(), d ** -0.5, 0.0, None, rows, 0, dtype)
+    ref.check(o, o_ref, bound)
+
+
+def test_ssm_repeated_gives_the_same_bits():
+    """Two channels per lane (many blocks), one channel, and time segments."""
+    dev = cuda_device()
+    for B, N, C in ((4, 700, 2048), (1, 500, 512), (1, 4000, 96)):
+        t = ssm_inputs(B, N, C, 16, 1, BF, True, N)
+        u, delta, z, A, Bm, Cm, D, bias = on(dev, *(t[k] for k in ("u", "delta", "z", "A", "Bm", "Cm", "D", "bias")))
+        y, h = la.la_ssm_prefill(u, delta, A, Bm, Cm, D=D, z=z, delta_bias=bias)
+        for _ in range(5):
+            y2, h2 = la.la_ssm_prefill(u, delta, A, Bm, Cm, D=D, z=z, delta_bias=bias)
+            assert torch.equal(y, y2) and torch.equal(h, h2)
+        # a slice of the channels alone takes another schedule: the same recurrence
+        c = slice(0, 64)
+        ys, hs = la.la_ssm_prefill(u[..., c], delta[..., c], A[c].contiguous(), Bm, Cm, D=D[c].contiguous(), z=z[..., c],
+                                   delta_bias=bias[c].contiguous())
+        assert (hs - h[:, c]).abs().max() <= 2e-5 * h.abs().max()
+        assert (ys.float() - y[..., c].float()).abs().max() <= 2 * 2 ** -8 * y.float().abs().max()
+
+
+@pytest.mark.parametrize("n,G", [(16, 1), (8, 2), (4, 1), (24, 1), (64, 2)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_ssm_two_channels_per_lane_meets_the_definition(dtype, n, G):
+    """Enough channels and sequences for two channels a lane; a few of them against fp64."""
+    dev = cuda_device()
+    lanes = 1 if n <= 4 else 2 if n <= 8 else 4 if n <= 16 else 8 if n <= 32 else 16
+    B, N, C = 2, 67, 80 * (128 // lanes)
+    t = ssm_inputs(B, N, C, n, G, dtype, True, n)
+    lens = [N, 40]
+    u, delta, z, A, Bm, Cm, D, bias, h0 = on(dev, *(t[k] for k in ("u", "delta", "z", "A", "Bm", "Cm", "D", "bias", "h")))
+    y, h = la.la_ssm_prefill(u, delta, A, Bm, Cm, D=D, z=z, delta_bias=bias, h_in=h0, lens=torch.tensor(lens, device=dev))
+    pick = torch.tensor(sorted({0, 1, C // G - 1, C // G % C, C // 2, C - 2, C - 1}))
+    group = pick // (C // G)
+    sub = {k: t[k][..., pick] for k in ("u", "delta", "z")}
+    for i, c in enumerate(pick.tolist()):  # one channel at a time: its group's B and C
+        b1, c1 = t["Bm"][:, group[i]:group[i] + 1], t["Cm"][:, group[i]:group[i] + 1]
+        y_ref, bound, h_ref, h_bound = ref.ssm(sub["u"][..., i:i + 1], sub["delta"][..., i:i + 1], t["A"][c:c + 1], b1, c1, t["D"][c:c + 1],
+                                               sub["z"][..., i:i + 1], t["bias"][c:c + 1], True, t["h"][:, c:c + 1], lens, dtype)
+        ref.check(h[:, c:c + 1], h_ref, h_bound)
+        ref.check(y[..., c:c + 1], y_ref, bound)
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams without an order between them: each has its own workspace and flags."""
+    dev = cuda_device()
+    t = [hybrid(dev, 1, 1500, s) for s in (11, 12)]
+    want = [prompt_pass(x, 1500, 64) for x in t]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(dev) for _ in t]
+    for _ in range(4):
+        got = []
+        for s, x in zip(streams, t):
+            with torch.cuda.stream(s):
+                got.append(prompt_pass(x, 1500, 64))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            for a, b in zip(g, w):
+                assert torch.equal(a, b)
+    assert la.la_device_status() == la.LA_OK
