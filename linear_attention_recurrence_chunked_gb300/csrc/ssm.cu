@@ -43,6 +43,13 @@ __device__ __forceinline__ float log2_rate(float A) {
   return x < -3.402823466e38f ? -3.402823466e38f : x;
 }
 
+// Added to the exponent, which costs nothing in its multiplication.  The unit's 2^x came out low by 2.1e-8 to 5e-8
+// of the value on average for decays below 0.999 (2^20 arguments per range against fp64; exp2f likewise), and a
+// state takes one such factor per token, so the errors add up along its memory: 2.5e-8 log2(e) centres them.
+// States of 4 x 300 tokens came out off by 1.0e-6 without it, by less than 0.7e-6 with it.  It is below half a
+// rounding at 1: dt = 0 stays the identity.
+constexpr float kCentre = 3.6e-8f;
+
 // Time segments: segment g of a sequence takes tokens [g * len, (g + 1) * len).
 struct Segments {
   int count;
@@ -140,6 +147,7 @@ ssm_scan_kernel(const SsmLaunch a, Segments seg, float* ws_h, float* ws_dt) {
       float dt[kCh], dtu[kCh];
       LaneBC bc;
     };
+    const f32x2 centre = pack2(kCentre, kCentre);
     __syncthreads();  // tile 0 is laid out
     for (int i = 0; i < count; ++i) {
       typename T::Work& q = sm.work[i & 1];
@@ -175,8 +183,8 @@ ssm_scan_kernel(const SsmLaunch a, Segments seg, float* ws_h, float* ws_dt) {
           for (int e = 0; e < kCh; ++e) {
             const In& x = cur[k];
             const f32x2 dt2 = pack2(x.dt[e], x.dt[e]), dtu2 = pack2(x.dtu[e], x.dtu[e]);
-            h01[e] = fma2(ex2_2(mul2(dt2, A01[e])), h01[e], mul2(dtu2, x.bc.b.x));
-            h23[e] = fma2(ex2_2(mul2(dt2, A23[e])), h23[e], mul2(dtu2, x.bc.b.y));
+            h01[e] = fma2(ex2_2(fma2(dt2, A01[e], centre)), h01[e], mul2(dtu2, x.bc.b.x));
+            h23[e] = fma2(ex2_2(fma2(dt2, A23[e], centre)), h23[e], mul2(dtu2, x.bc.b.y));
             if constexpr (MODE == kLocal) {
               dt_sum[e] += x.dt[e];
             } else {

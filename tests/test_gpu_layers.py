@@ -567,3 +567,16 @@ def test_two_streams_at_once():
             for a, b in zip(g, w):
                 assert torch.equal(a, b)
     assert la.la_device_status() == la.LA_OK
+
+
+@pytest.mark.parametrize("C", [24, 5120])
+def test_ssm_step_of_zero_length_keeps_the_state(C):
+    """dt = 0 is the identity to the bit, for any decay rate: neither the exponential nor its argument may move it."""
+    dev = cuda_device()
+    B, N, n = 1, 70, 16
+    t = ssm_inputs(B, N, C, n, 1, FP, False, 3)
+    A = t["A"].clone()
+    A[:, 0], A[:, 1], A[:, 2] = 0.0, torch.finfo(torch.float32).min, -1e-30
+    u, z, Bm, Cm, h0 = on(dev, t["u"], t["z"], t["Bm"], t["Cm"], t["h"])
+    _, h = la.la_ssm_prefill(u, torch.zeros_like(u), A.to(dev), Bm, Cm, h_in=h0, delta_softplus=False)
+    assert torch.equal(h, h0)
