@@ -285,10 +285,11 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   __shared__ uint64_t bar_fin;
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile uint32_t dead;
-  // bad[n % 8] == n + 1: item n of this CTA has values that are not finite in a block that is not seen as a
-  // whole.  Warp 10 is at most kSlots + 1 < 8 items ahead of the rows: a product of item n + 1 waits for the
-  // rows to have read the output of item n, and the ring holds kSlots blocks.
-  __shared__ volatile uint32_t bad[8];
+  // bad[t][n % 8] == n + 1: the n-th item at whose keys tile t is at work has values that are not finite in a block
+  // that is not seen as a whole.  Warp 10 is at most kSlots + 1 < 8 such items ahead of the rows: a product of the
+  // next one waits for the rows to have read this one's output, and the ring holds kSlots blocks.  (Items that see
+  // nothing pass without a wait, any number of them, and do not count.)
+  __shared__ volatile uint32_t bad[2][8];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(sm);
@@ -309,7 +310,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     }
     mbar_init(smem_u32(&bar_fin), 2);
     dead = 0;
-    for (int n = 0; n < 8; ++n) bad[n] = 0;
+    for (int n = 0; n < 16; ++n) bad[n / 8][n % 8] = 0;
     fence_mbar_init();
   }
   if (warp == 8) {
@@ -380,11 +381,13 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       __syncwarp();
     } else if (warp == 10) {
       // ================================================================ a look at each value block
-      uint32_t i = 0, iv = 0, n = 0;
+      uint32_t i = 0, iv = 0, n0 = 0, n1 = 0;
       for (int r = 0; r < rounds; ++r) {
         if (!it.place(a, r, items, q_tiles, lane == 0)) continue;
         const Blocks<KB> bl(a, it);
-        ++n;
+        const bool any0 = bl.jb[0] < bl.je[0], any1 = bl.jb[1] < bl.je[1];
+        if (any0) ++n0;
+        if (any1) ++n1;
         if (bl.j0 < bl.j1) ++i;  // the first block of keys
         for (int j = bl.j0, after; j < bl.j1; j = after) {
           after = bl.next(j);
@@ -402,7 +405,10 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll 4
             for (int e = lane; e < (int)(S::kBlk * KB * 8); e += 32) acc = add_zero_times(*reinterpret_cast<const uint4*>(v + e * 16), acc);
-            if (__any_sync(kFullMask, __hisnan(acc.x) || __hisnan(acc.y)) && lane == 0) bad[(n - 1) % 8] = n;
+            if (__any_sync(kFullMask, __hisnan(acc.x) || __hisnan(acc.y)) && lane == 0) {
+              if (any0) bad[0][(n0 - 1) % 8] = n0;
+              if (any1) bad[1][(n1 - 1) % 8] = n1;
+            }
           }
           warp_arrive(smem_u32(&bar_vok[slot(iv)]));
           ++i;
@@ -514,10 +520,9 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       return fma2(fma2(fma2(pack2(kq[3], kq[3]), u, pack2(kq[2], kq[2])), u, pack2(kq[1], kq[1])), u, pack2(kq[0], kq[0]));
     };
     const bool al32 = ((reinterpret_cast<uintptr_t>(a.o) | (uintptr_t)((a.o_sb | a.o_sh | a.o_st) * (a.out_bf16 ? 2 : 4))) & 31u) == 0;
-    uint32_t ns = 0, n = 0;  // blocks, items
+    uint32_t ns = 0, n = 0;  // blocks, items at whose keys this tile is at work
     for (int round = 0; round < rounds; ++round) {
       if (!it.place(a, round, items, q_tiles, false)) continue;
-      ++n;
       const int i = it.i0 + (int)threadIdx.x;
       const KeySpan span = key_span(a, it.b, i, it.len);
       const TileSpan ts = tile_span(a, it.b, it.i0 + t * kRows, it.len);
@@ -720,7 +725,8 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         wait(&bar_o[t], ns - 1);
         __syncwarp();
         tc_fence_after();
-        again = bad[(n - 1) % 8] == n;
+        ++n;
+        again = bad[t][(n - 1) % 8] == n;
       }
       const bool live = i < a.Nq && a.q_pos0 + i < it.len && !dead;
       const bool seen = l != 0.f;  // also a row whose sum is NaN

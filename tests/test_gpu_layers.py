@@ -580,3 +580,22 @@ def test_ssm_step_of_zero_length_keeps_the_state(C):
     u, z, Bm, Cm, h0 = on(dev, t["u"], t["z"], t["Bm"], t["Cm"], t["h"])
     _, h = la.la_ssm_prefill(u, torch.zeros_like(u), A.to(dev), Bm, Cm, h_in=h0, delta_softplus=False)
     assert torch.equal(h, h0)
+
+
+def test_swa_bad_values_are_seen_by_their_own_queries_only():
+    """Nine query tiles per block of the grid, seven of which see nothing: the notes that the first and the last
+    one's masked values are not finite must not take each other's place."""
+    dev = cuda_device()
+    H, N, d = 152, 9 * 256, 16
+    q, k, v = swa_case(1, H, 2, N, N, d, BF, 77)
+    lo, hi = torch.zeros(1, N, dtype=torch.int32), torch.zeros(1, N, dtype=torch.int32)
+    lo[0, :256], hi[0, :256] = 10, 256
+    lo[0, -256:], hi[0, -256:] = N - 246, N
+    clean = la.la_swa_prefill(*on(dev, q, k, v), key_lo=lo.to(dev), key_hi=hi.to(dev))
+    v[:, :, 5], v[:, :, N - 251] = float("nan"), float("inf")
+    for _ in range(5):
+        o = la.la_swa_prefill(*on(dev, q, k, v), key_lo=lo.to(dev), key_hi=hi.to(dev))
+        assert torch.isfinite(o.float()).all()
+        assert (o.float() - clean.float()).abs().max() <= 2 ** -7 * clean.float().abs().max()
+    assert not o[:, :, 256:-256].any()
+    assert la.la_device_status() == la.LA_OK
