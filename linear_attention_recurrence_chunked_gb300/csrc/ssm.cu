@@ -511,7 +511,7 @@ ssm_decode_kernel(const SsmLaunch a, bool a_vec, bool bc_vec) {
     acc[q] = 0.f;
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
-      h[q][k] = fmaf(ex2(dt * A2[k]), h[q][k], dtu * Bk[k]);
+      h[q][k] = fmaf(ex2(fmaf(dt, A2[k], kCentre)), h[q][k], dtu * Bk[k]);
       acc[q] = fmaf(Ck[k], h[q][k], acc[q]);
     }
     if (on && s0 + q < a.B) {
