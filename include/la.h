@@ -404,7 +404,8 @@ la_status la_notebank_route(const la_notebank_route_args* args, void* stream);
  *     outside [0, N] skips the whole sequence (nothing of it is written) and
  *     sets the device status word (LA_ERR_INVALID_ARGUMENT).
  *   - outputs must not overlap inputs, except a state updated in place
- *     (state_out == state_in). */
+ *     (state_out == state_in), and an output's elements must not overlap one
+ *     another (sequences or heads repeated with stride 0 are for inputs). */
 
 /* Causal depthwise convolution over a prompt.
  *   y_t[c] = act(bias[c] + sum_{i<W} w[c,i] x_{t-W+1+i}[c]),   act = identity or SiLU
@@ -464,7 +465,8 @@ la_status la_conv_decode_step(const la_conv_decode_args* args, void* stream);
  * scanned in time segments, whose states need the workspace that
  * la_ssm_prefill_workspace_size returns (often 0; a function of the sizes
  * only; 16-byte aligned, dead when the call's work has finished).  A call
- * with a smaller workspace fails with LA_ERR_WORKSPACE. */
+ * with a smaller workspace fails with LA_ERR_WORKSPACE.
+ * Limits: B <= 65535, C < 2^25, N < 2^30 (LA_ERR_UNSUPPORTED). */
 typedef struct la_ssm_prefill_args {
   int64_t B, N, C, n, G;
   la_dtype in_dtype, out_dtype;
@@ -484,8 +486,8 @@ la_status la_ssm_prefill(const la_ssm_prefill_args* args, void* workspace, size_
 /* The same for one token of each of S sequences: u, delta, z, out are [S, C]
  * rows (stride_b elements apart, any element alignment; stride_h, stride_t
  * ignored), Bm, Cm [S, G, n] (stride_b, stride_h), states [S, C, n] fp32
- * contiguous (state_out may alias state_in).  Launched as a programmatic
- * dependent, as la_decode_step. */
+ * contiguous (state_out may alias state_in).  S <= 262140, C < 2^25.
+ * Launched as a programmatic dependent, as la_decode_step. */
 typedef struct la_ssm_decode_args {
   int64_t S, C, n, G;
   la_dtype in_dtype, out_dtype;
@@ -521,6 +523,7 @@ la_status la_ssm_decode_step(const la_ssm_decode_args* args, void* stream);
  *            (1 <= window <= 256): the last min(lens[b], window) tokens are
  *            stored for la_swa_decode_step / la_swa_biased_decode_step (token
  *            p in slot p % window; other slots are left as they were).
+ *   softcap : 0, or up to 1e37 with |scale| / softcap up to 1e37
  * bf16 inputs: products on the tensor cores with fp32 sums and statistics,
  * the softmax weights rounded to bf16 for their product with v.  fp32 inputs:
  * fp32 throughout. */

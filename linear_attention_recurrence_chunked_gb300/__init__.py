@@ -11,6 +11,7 @@ Names follow the C entry points: ``la_based_prefill``, ``la_gdn_prefill``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -679,16 +680,15 @@ _SWA_BIASED_DECODE = struct.Struct("<4q2i7qf4xqf4xq")
 _packed = {}
 
 
-def _call(fn_name, index, stream, args, *more):
-    """Call an entry point with its packed arguments, device `index` current, on `stream` or that device's current
-    stream."""
+def _call(fn_name, index, args, *more):
+    """Call an entry point with its packed arguments on the current stream of device `index`."""
     fn = _packed.get(fn_name)
     if fn is None or fn[0] is not _lib:
         f = load_library()[fn_name]  # a function object of its own: it takes the packed bytes
         f.restype = ctypes.c_int
         f.argtypes = [ctypes.c_char_p, *([ctypes.c_void_p, ctypes.c_size_t] if more else []), ctypes.c_void_p]
         fn = _packed[fn_name] = (_lib, f)
-    handle = _stream_handle(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    handle = torch._C._cuda_getCurrentRawStream(index)
     if torch._C._cuda_getDevice() == index:
         st = fn[1](args, *more, handle)
     else:
@@ -698,8 +698,30 @@ def _call(fn_name, index, stream, args, *more):
         raise LAError(st, fn_name)
 
 
+def _on_stream(fn):
+    """With `stream` (a torch stream or a cudaStream_t) the whole call runs on it: the kernels, and also the zeros and
+    copies that prepare outputs and the memory that outputs and workspaces take."""
+    first = fn.__code__.co_varnames[0]
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        x = args[0] if args else kwargs[first]
+        if not x.is_cuda:
+            return fn(*args, **kwargs)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream_handle(stream), device=x.device)
+        if stream.device != x.device:
+            raise ValueError(f"the stream is of {stream.device}, the tensors of {x.device}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return call
+
+
+@_on_stream
 def la_conv_prefill(x, w, bias=None, state_in=None, lens=None, silu: bool = True, y=None, state_out=None,
-                    out_dtype=None, stream=None):
+                    out_dtype=None, *, stream=None):
     """Short causal depthwise convolution of a prompt.  Returns (y, state_out).
 
     x: [B,N,C] (fp32 or bf16, channels contiguous, rows 16-byte aligned); w:
@@ -722,14 +744,15 @@ def la_conv_prefill(x, w, bias=None, state_in=None, lens=None, silu: bool = True
         state_out = torch.empty((B, max(W - 1, 0), C), dtype=xt, device=x.device)
         if lens is not None:  # a sequence whose length is out of range is left as it was
             state_out.copy_(state_in) if state_in is not None else state_out.zero_()
-    _call("la_conv_prefill", index, stream,
+    _call("la_conv_prefill", index,
           _CONV_PREFILL.pack(B, N, C, W, _code(xt), _code(y.dtype), _code(wt), *_rows(x), *_rows(y), w.data_ptr(),
                              _address(bias), _address(state_in), state_out.data_ptr(), _address(lens), bool(silu)))
     return y, state_out
 
 
+@_on_stream
 def la_conv_decode_step(x, w, state, bias=None, silu: bool = True, out=None, state_out=None, out_dtype=None,
-                        stream=None):
+                        *, stream=None):
     """The convolution's step for one token of each sequence.  x: [S,C] (rows
     16-byte aligned); w, bias as in la_conv_prefill; state: [S,W-1,C], updated in
     place unless state_out is given.  Returns out [S,C]."""
@@ -745,7 +768,7 @@ def la_conv_decode_step(x, w, state, bias=None, silu: bool = True, out=None, sta
     _check(index, ("x", x, (S, C), xt, False), ("w", w, (C, W), wt, True), ("bias", bias, (C,), wt, True),
            ("state", state, held, xt, True), ("state_out", state_out, held, xt, True),
            ("out", out, (S, C), out.dtype, False))
-    _call("la_conv_decode_step", index, stream,
+    _call("la_conv_decode_step", index,
           _CONV_DECODE.pack(S, C, W, _code(xt), _code(out.dtype), _code(wt), *_row(x)[:2], *_row(out)[:2],
                             w.data_ptr(), _address(bias), state.data_ptr(), state_out.data_ptr(), bool(silu)))
     return out
@@ -772,8 +795,9 @@ def la_ssm_prefill_workspace_size(u, delta, A, Bm, Cm) -> int:
     return _ssm_workspace_size(_ssm_prefill_args(u, delta, A, Bm, Cm, None, None, None, True, None, None, u, None))
 
 
+@_on_stream
 def la_ssm_prefill(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, delta_softplus: bool = True, h_in=None,
-                   lens=None, y=None, h_out=None, out_dtype=None, workspace=None, stream=None):
+                   lens=None, y=None, h_out=None, out_dtype=None, workspace=None, *, stream=None):
     """Selective state space scan of a prompt.  Returns (y, h_out).
 
         dt = softplus(delta + delta_bias)   (delta + delta_bias without delta_softplus)
@@ -804,12 +828,13 @@ def la_ssm_prefill(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, delta_s
     ws, ws_bytes = _workspace(_ssm_workspace_size(a), workspace, u.device)
     if workspace is not None and workspace.get_device() != index:
         raise ValueError("workspace must live on the device of the inputs")
-    _call("la_ssm_prefill", index, stream, a, ws.data_ptr() if isinstance(ws, torch.Tensor) else ws, ws_bytes)
+    _call("la_ssm_prefill", index, a, ws.data_ptr() if isinstance(ws, torch.Tensor) else ws, ws_bytes)
     return y, h_out
 
 
+@_on_stream
 def la_ssm_decode_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None, delta_softplus: bool = True,
-                       out=None, state_out=None, out_dtype=None, stream=None):
+                       out=None, state_out=None, out_dtype=None, *, stream=None):
     """The scan's step for one token of each sequence.  u, delta, z: [S,C]; Bm,
     Cm: [S,G,n]; state: fp32 [S,C,n], updated in place unless state_out is given;
     the rest as in la_ssm_prefill.  Returns out [S,C]."""
@@ -826,7 +851,7 @@ def la_ssm_decode_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=No
            ("D", D, (C,), f32, True), ("delta_bias", delta_bias, (C,), f32, True), ("state", state, (S, C, n), f32, True),
            ("state_out", state_out, (S, C, n), f32, True), ("out", out, rows, out.dtype, False))
     many, groups = S > 1, G > 1
-    _call("la_ssm_decode_step", index, stream,
+    _call("la_ssm_decode_step", index,
           _SSM_DECODE.pack(S, C, n, G, _code(ut), _code(out.dtype), *_row(u), *_row(delta), *_row(z), *_row(out),
                            Bm.data_ptr(), Bm.stride(0) if many else 0, Bm.stride(1) if groups else 0, 0,
                            Cm.data_ptr(), Cm.stride(0) if many else 0, Cm.stride(1) if groups else 0, 0,
@@ -835,9 +860,10 @@ def la_ssm_decode_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=No
     return out
 
 
+@_on_stream
 def la_swa_prefill(q, k, v, window: int = 0, scale: float | None = None, softcap: float = 0.0, slopes=None,
                    key_lo=None, key_hi=None, q_pos0: int | None = None, lens=None, o=None, k_cache=None, v_cache=None,
-                   out_dtype=None, stream=None):
+                   out_dtype=None, *, stream=None):
     """Softmax attention of a prompt's queries.  Returns o [B,H,Nq,d].
 
     q: [B,H,Nq,d], k, v: [B,H_kv,Nk,d] (fp32 or bf16; H a multiple of H_kv; d a
@@ -862,7 +888,7 @@ def la_swa_prefill(q, k, v, window: int = 0, scale: float | None = None, softcap
            ("key_hi", key_hi, (B, Nq), i32, True), ("lens", lens, (B,), torch.int64, True),
            ("k_cache", k_cache, (B, Hkv, window, d), qt, True), ("v_cache", v_cache, (B, Hkv, window, d), qt, True),
            ("o", o, queries, o.dtype, False))
-    _call("la_swa_prefill", index, stream,
+    _call("la_swa_prefill", index,
           _SWA_PREFILL.pack(B, H, Hkv, Nq, Nk, d, window, _code(qt), _code(o.dtype), *_heads(q), *_heads(k), *_heads(v),
                             *_heads(o), scale if scale is not None else d ** -0.5, softcap, _address(slopes),
                             _address(key_lo), _address(key_hi), q_pos0 if q_pos0 is not None else Nk - Nq,
@@ -870,8 +896,9 @@ def la_swa_prefill(q, k, v, window: int = 0, scale: float | None = None, softcap
     return o
 
 
+@_on_stream
 def la_swa_biased_decode_step(q, k, v, k_cache, v_cache, pos, softcap: float = 0.0, slopes=None, out=None,
-                              scale: float | None = None, out_dtype=None, stream=None):
+                              scale: float | None = None, out_dtype=None, *, stream=None):
     """la_swa_decode_step with grouped heads, capped scores and a distance bias:
     q: [S,H,d]; k, v: [S,H_kv,d]; k_cache, v_cache: [S,H_kv,window,d]; pos: int64
     [S]; softcap and slopes as in la_swa_prefill.  Returns out [S,H,d]."""
@@ -886,7 +913,7 @@ def la_swa_biased_decode_step(q, k, v, k_cache, v_cache, pos, softcap: float = 0
     _check(index, ("q", q, heads, qt, True), ("k", k, (S, Hkv, d), qt, True), ("v", v, (S, Hkv, d), qt, True),
            ("k_cache", k_cache, ring, qt, True), ("v_cache", v_cache, ring, qt, True), ("pos", pos, (S,), torch.int64, True),
            ("slopes", slopes, (H,), torch.float32, True), ("out", out, heads, out.dtype, True))
-    _call("la_swa_biased_decode_step", index, stream,
+    _call("la_swa_biased_decode_step", index,
           _SWA_BIASED_DECODE.pack(S, H, d, window, _code(qt), _code(out.dtype), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                   k_cache.data_ptr(), v_cache.data_ptr(), pos.data_ptr(), out.data_ptr(),
                                   scale if scale is not None else d ** -0.5, Hkv, softcap, _address(slopes)))

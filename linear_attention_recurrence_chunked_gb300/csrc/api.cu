@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <cmath>
 #include <initializer_list>
 
 #include "kernels.h"
@@ -417,10 +419,29 @@ bool within(int64_t limit, std::initializer_list<int64_t> sizes) {
 }
 bool valid_size(int64_t s) { return s >= 0 && s <= kMaxDim; }
 
-// [B, N, C] view: as a [B, 1, N, C] one; an output's sequences must not lie on one another
+// Whether no two elements of a [B, H, N, d] view lie on one another, for views whose axes nest in some order.
+bool distinct(const la_tensor& x, int64_t B, int64_t H, int64_t N, int64_t d) {
+  struct Axis { int64_t stride, size; } ax[3] = {{x.stride_b, B}, {x.stride_h, H}, {x.stride_t, N}};
+  std::sort(ax, ax + 3, [](const Axis& a, const Axis& b) { return a.stride < b.stride; });
+  int64_t extent = d;  // elements from the first to the last of what the smaller axes span
+  for (const Axis& a : ax) {
+    if (a.size == 0) return true;
+    if (a.size == 1) continue;
+    if (a.stride < extent || a.stride > (INT64_MAX - extent) / (a.size - 1)) return false;
+    extent += a.stride * (a.size - 1);
+  }
+  return true;
+}
+
+// [B, N, C] view: as a [B, 1, N, C] one
 bool valid_rows(la_tensor x, int64_t B, int64_t N, int64_t C, la_dtype dt, bool output) {
   x.stride_h = 0;
-  return valid_view(x, B, 1, N, C, dt) && !(output && B > 1 && N > 0 && x.stride_b < (N > 1 ? x.stride_t : C));
+  return valid_view(x, B, 1, N, C, dt) && !(output && !distinct(x, B, 1, N, C));
+}
+
+// 0, or a cap whose ratios to the scale and to log2(e) are far from fp32's ends
+bool valid_cap(float softcap, float scale) {
+  return softcap == 0.f || (softcap > 0.f && softcap <= 1e37f && std::fabs(scale / softcap) <= 1e37f);
 }
 bool valid_elem(const void* p, la_dtype dt) { return p && (reinterpret_cast<uintptr_t>(p) % elem_bytes(dt)) == 0; }
 bool valid_strides(const la_tensor& x) { return x.stride_b >= 0 && x.stride_h >= 0 && x.stride_t >= 0; }
@@ -553,18 +574,19 @@ la_status la_swa_prefill(const la_swa_prefill_args* a, void* stream) {
       a->H % a->H_kv != 0 || a->q_pos0 < 0 || a->q_pos0 > a->Nk || a->Nq > a->Nk - a->q_pos0)
     return LA_ERR_INVALID_ARGUMENT;
   if (!valid_dtype(a->in_dtype) || !valid_dtype(a->out_dtype)) return LA_ERR_INVALID_ARGUMENT;
-  if (!(a->softcap >= 0.f) || a->softcap > 3.402823466e38f || (a->k_cache == nullptr) != (a->v_cache == nullptr))
+  if (!valid_cap(a->softcap, a->scale) || (a->k_cache == nullptr) != (a->v_cache == nullptr))
     return LA_ERR_INVALID_ARGUMENT;
   if (a->d < 8 || a->d > 128 || a->d % 8 != 0) return LA_ERR_UNSUPPORTED;
   if (a->k_cache && (a->window < 1 || a->window > 256)) return LA_ERR_UNSUPPORTED;
   if (a->Nk > INT32_MAX - 512) return LA_ERR_UNSUPPORTED;  // key positions are 32-bit
   if (a->B == 0 || a->H == 0 || a->Nk == 0) return LA_OK;
-  if (!within((int64_t(1) << 31) - 1, {a->B, a->H, (a->Nq + 63) / 64}) || !within((int64_t(1) << 31) - 1, {a->B, a->H_kv, 256}))
+  if (!within((int64_t(1) << 31) - 1024, {a->B, a->H, (a->Nq + 63) / 64}) ||
+      (a->k_cache && !within((int64_t(1) << 34) - 8, {a->B, a->H_kv, a->window})))
     return LA_ERR_UNSUPPORTED;
   if (!valid_view(a->q, a->B, a->H, a->Nq, a->d, a->in_dtype) || !valid_view(a->k, a->B, a->H_kv, a->Nk, a->d, a->in_dtype) ||
       !valid_view(a->v, a->B, a->H_kv, a->Nk, a->d, a->in_dtype) || !valid_view(a->o, a->B, a->H, a->Nq, a->d, a->out_dtype))
     return LA_ERR_INVALID_ARGUMENT;
-  if (a->Nq > 0 && ((a->B > 1 && a->o.stride_b == 0) || (a->H > 1 && a->o.stride_h == 0))) return LA_ERR_INVALID_ARGUMENT;
+  if (!distinct(a->o, a->B, a->H, a->Nq, a->d)) return LA_ERR_INVALID_ARGUMENT;
   if (!aligned4(a->slopes) || !aligned4(a->key_lo) || !aligned4(a->key_hi) || !aligned8(a->lens) || !aligned16(a->k_cache) ||
       !aligned16(a->v_cache))
     return LA_ERR_INVALID_ARGUMENT;
@@ -592,7 +614,7 @@ la_status la_swa_biased_decode_step(const la_swa_biased_decode_args* args, void*
   const la_swa_decode_args* a = &args->base;
   if (a->S < 0 || a->H < 0 || a->S > kMaxDim || a->H > kMaxDim || args->H_kv < 1 || a->H % args->H_kv != 0) return LA_ERR_INVALID_ARGUMENT;
   if (!valid_dtype(a->in_dtype) || !valid_dtype(a->out_dtype)) return LA_ERR_INVALID_ARGUMENT;
-  if (!(args->softcap >= 0.f) || args->softcap > 3.402823466e38f) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_cap(args->softcap, a->scale)) return LA_ERR_INVALID_ARGUMENT;
   if (a->d < 8 || a->d > 128 || a->d % 8 != 0 || a->window < 1 || a->window > 256 || a->H / args->H_kv > 16) return LA_ERR_UNSUPPORTED;
   if (a->S == 0 || a->H == 0) return LA_OK;
   if (!within((int64_t(1) << 31) - 1, {a->S, a->H})) return LA_ERR_UNSUPPORTED;

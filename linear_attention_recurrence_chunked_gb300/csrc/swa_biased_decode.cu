@@ -15,6 +15,7 @@
 // transposed on the way from shared memory.  The weights are rounded to bf16 for their product, as over a prompt.
 // fp32: CUDA cores, four query heads at a time.
 #include "layers.cuh"
+#include "swa_common.cuh"
 #include "tc.cuh"
 
 namespace la {
@@ -126,6 +127,7 @@ swa_biased_decode_mma_kernel(const SwaBiasedDecodeLaunch a) {
     }
   }
   // ---- softmax of this warp's slots
+  const float inv_cap = 1.f / a.softcap;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
   for (int t = 0; t < 4; ++t)
@@ -133,7 +135,7 @@ swa_biased_decode_mma_kernel(const SwaBiasedDecodeLaunch a) {
     for (int e = 0; e < 4; ++e) {
       const int slot = first + t * 8 + q4 * 2 + (e & 1), h = hr + (e >> 1) * 8;
       float y = x[t][e] * c.scale;
-      if (a.softcap != 0.f) y = fmaf(-2.f * a.softcap, rcp(1.f + ex2(y * (2.f * kLog2e / a.softcap))), a.softcap);
+      if (a.softcap != 0.f) y = capped(y, a.softcap, inv_cap);
       const float age = (float)(slot_new >= slot ? slot_new - slot : slot_new - slot + w);
       if (a.slopes && h < group) y = fmaf(-a.slopes[h0 + h], age, y);
       x[t][e] = slot < n ? y : -INFINITY;
@@ -244,6 +246,7 @@ swa_biased_decode_kernel(const SwaBiasedDecodeLaunch a) {
   const TIn* vn = reinterpret_cast<const TIn*>(c.v) + sk * d + col;
   TIn* kc = reinterpret_cast<TIn*>(c.k_cache) + sk * (int64_t)w * d + col;
   TIn* vc = reinterpret_cast<TIn*>(c.v_cache) + sk * (int64_t)w * d + col;
+  const float inv_cap = 1.f / a.softcap;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   auto row = [&](const TIn* ring, const TIn* fresh, int slot) {
     return on && slot < n ? load_row(slot == slot_new ? fresh : ring + (int64_t)slot * d) : zero;
@@ -325,7 +328,7 @@ swa_biased_decode_kernel(const SwaBiasedDecodeLaunch a) {
       const float age = (float)(slot_new >= slot ? slot_new - slot : slot_new - slot + w);
 #pragma unroll
       for (int g = 0; g < kHeads; ++g) {
-        if (a.softcap != 0.f) x[g] = fmaf(-2.f * a.softcap, rcp(1.f + ex2(x[g] * (2.f * kLog2e / a.softcap))), a.softcap);
+        if (a.softcap != 0.f) x[g] = capped(x[g], a.softcap, inv_cap);
         if (a.slopes && g < heads) x[g] = fmaf(-a.slopes[h0 + g], age, x[g]);
         if (slot >= n) x[g] = -INFINITY;
         float m = x[g];

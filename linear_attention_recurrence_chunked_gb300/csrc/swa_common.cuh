@@ -24,6 +24,20 @@ __device__ __forceinline__ KeySpan key_span(const SwaPrefillLaunch& a, int b, in
   return s;
 }
 
+// tanh(z) / z in z^2 on [0, 1/4] through four Chebyshev nodes, off by 6e-7 of the value at most.  A capped score is
+// cap tanh(z) = x Q(z^2) with z = x / cap up to kStraight, and cap - 2 cap / (1 + e^2z) beyond, where the difference
+// loses nothing that the value itself would hold: as the only form it would leave an error of 1e-7 cap in scores
+// that are far below a large cap.
+constexpr float kStraight = 0.5f;
+__device__ constexpr float kTanh[4] = {0.9999994636f, -0.3332628310f, 0.1318994015f, -0.0443927385f};
+
+__device__ __forceinline__ float capped(float x, float cap, float inv_cap) {
+  const float z = x * inv_cap, u = z * z;
+  const float near = x * fmaf(fmaf(fmaf(kTanh[3], u, kTanh[2]), u, kTanh[1]), u, kTanh[0]);
+  const float far = fmaf(-2.f * cap, rcp(1.f + ex2(z * (2.f * kLog2e))), cap);
+  return fabsf(z) <= kStraight ? near : far;
+}
+
 __device__ __forceinline__ bool finite1(float x) { return fabsf(x) <= 3.402823466e38f; }
 __device__ __forceinline__ bool finite4(float4 x) { return finite1(x.x) && finite1(x.y) && finite1(x.z) && finite1(x.w); }
 

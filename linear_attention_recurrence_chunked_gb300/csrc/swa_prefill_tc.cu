@@ -65,10 +65,6 @@ struct Shape {
   static_assert(2 * kRegsRows + kRegsRest <= 3 * kRegs, "");
 };
 
-// tanh(z) / z in z^2 on [0, 1/4] through four Chebyshev nodes: tanh is off by 3e-7 at most for |z| <= 1/2
-constexpr float kStraight = 0.5f;
-__device__ constexpr float kTanh[4] = {0.9999994636f, -0.3332628310f, 0.1318994015f, -0.0443927385f};
-
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -498,9 +494,9 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const uint32_t p_row = threadIdx.x % kRows;
     const uint32_t cs = tl + t * KB, col_o = tl + S::kColO + t * DP;
     const float c1 = a.scale * kLog2e;
-    // With a cap: tanh(z), z = zc x, is 1 - 2 / (1 + 2^(cz x)); and for |z| <= kStraight, cap tanh(z) = x Q(x^2) in
-    // log2 units (a zc far from 1 would take Q's coefficients out of the range of normal numbers, and a large cap
-    // the weights of scores near its negative).
+    // With a cap: z = zc x for a product x.  Where whole rows are `straight` the factors are drawn into Q's
+    // coefficients, cap tanh(z) = x Q(x^2) in log2 units (a zc far from 1 would take them out of the range of normal
+    // numbers, and a large cap the weights of scores near its negative).
     const float zc = CAP ? a.scale / a.softcap : 0.f, cz = zc * (2.f * kLog2e), capl = a.softcap * kLog2e;
     [[maybe_unused]] const bool straight = CAP && zc > 1e-4f && zc < 1e4f && capl <= 100.f;
     float kq[4] = {0.f, 0.f, 0.f, 0.f};
@@ -655,11 +651,30 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             tmem_ld32(cs + c0, v);
             tmem_ld_wait();
             const float dist = (float)(pos - k0 - c0);
+            if constexpr (CAP) {
+              float hi[2] = {0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if constexpr (CAP) v[c] = fmaf(-2.f * capl, rcp(1.f + ex2(v[c] * cz)), capl);  // cap tanh(z) = cap - 2 cap / (1 + e^2z)
-              else if constexpr (BIAS) v[c] *= c1;
-              if constexpr (BIAS) v[c] = fmaf(-slope2, fabsf(dist - (float)c), v[c]);
+              for (int c = 0; c < 32; ++c) hi[c & 1] = fmaxf(hi[c & 1], fabsf(v[c]));
+              if (fmaxf(hi[0], hi[1]) * fabsf(zc) <= kStraight) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                  const f32x2 x = pack2(v[c], v[c + 1]), z = mul2(x, pack2(zc, zc)), u = mul2(z, z);
+                  f32x2 q = pack2(kTanh[3], kTanh[3]);
+#pragma unroll
+                  for (int e = 2; e >= 0; --e) q = fma2(q, u, pack2(kTanh[e], kTanh[e]));
+                  unpack2(mul2(mul2(x, pack2(c1, c1)), q), v[c], v[c + 1]);
+                }
+              } else {  // beside a score of half the cap an error of 1e-7 cap is one of the score's own rounding
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = fmaf(-2.f * capl, rcp(1.f + ex2(v[c] * cz)), capl);
+              }
+            } else if constexpr (BIAS) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] *= c1;
+            }
+            if constexpr (BIAS) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] = fmaf(-slope2, fabsf(dist - (float)c), v[c]);
             }
             if (!__all_sync(kFullMask, va <= c0 && vb >= c0 + 32)) {
               const uint32_t from = va - c0 >= 32 ? 0u : ~0u << max(va - c0, 0), to = vb - c0 >= 32 ? ~0u : (1u << max(vb - c0, 0)) - 1u;

@@ -141,7 +141,10 @@ def swa(q, k, v, scale, softcap, slopes, rows, q_pos0, out_dtype):
                 es = (2 * d + 4) * U * abs(scale) * np.abs(terms).sum(1)
                 if softcap:
                     s = softcap * np.tanh(s / softcap)
-                    es = es + 16 * U * softcap  # two quotients, an exponential and a sum, of values up to 1
+                    # beyond half the cap: two quotients, an exponential and a sum, of values up to the cap, and the
+                    # largest score is then above cap / 2.2; up to there a polynomial, off by 10 U of the score,
+                    # and its six roundings
+                    es = es + 16 * U * min(softcap, 2.2 * np.abs(s).max())
                 dist = slopes[h] * np.abs(q_pos0 + i - np.arange(lo, hi))
                 s = s - dist
                 es = es + 2 * U * (dist + np.abs(s))

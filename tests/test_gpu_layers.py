@@ -599,3 +599,76 @@ def test_swa_bad_values_are_seen_by_their_own_queries_only():
         assert (o.float() - clean.float()).abs().max() <= 2 ** -7 * clean.float().abs().max()
     assert not o[:, :, 256:-256].any()
     assert la.la_device_status() == la.LA_OK
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("scale,softcap,slope", [(-0.3, 0.0, 0.0), (0.0, 0.0, 0.0), (-0.3, 3.0, 0.0), (0.2, 1e6, 0.0), (0.2, 1e-3, 0.0),
+                                                 (0.2, 2e3, 0.01), (0.2, 0.0, -0.02), (2.0, 1.5, -0.5)])
+def test_swa_unusual_scales_caps_and_slopes(dtype, scale, softcap, slope):
+    """Negative and zero scales, caps far above and below the scores, biases that grow with the distance."""
+    dev = cuda_device()
+    B, H, Hkv, N, d = 1, 2, 1, 300, 64
+    q, k, v = swa_case(B, H, Hkv, N, N, d, dtype, 55)
+    sl = torch.full((H,), slope) if slope else None
+    for window in (0, 90):  # wide and narrow blocks
+        o = la.la_swa_prefill(*on(dev, q, k, v), scale=scale, softcap=softcap, slopes=None if sl is None else sl.to(dev), window=window)
+        rows = ref.spans(N, N, B, window, None, None, 0, None)
+        o_ref, bound = ref.swa(q, k, v, scale, softcap, sl, rows, 0, dtype)
+        ref.check(o, o_ref, bound)
+    # the step at the last position, over a ring of the last 90 tokens
+    w = 90
+    kc, vc = (torch.zeros(B, Hkv, w, d, dtype=dtype) for _ in range(2))
+    for p in range(N - w, N - 1):
+        kc[:, :, p % w], vc[:, :, p % w] = k[:, :, p], v[:, :, p]
+    last = [x[:, :, -1].contiguous() for x in (q, k, v)]
+    out = la.la_swa_biased_decode_step(*on(dev, *last, kc, vc), torch.tensor([N - 1], device=dev), softcap=softcap,
+                                       slopes=None if sl is None else sl.to(dev), scale=scale)
+    ref.check(out, o_ref[:, :, -1], bound[:, :, -1])
+
+
+def test_time_major_activations():
+    """[N, B, C] activations as [B, N, C] views, outputs too: sequences lie within a token's row."""
+    dev = cuda_device()
+    B, N, C, n = 3, 150, 64, 8
+    t = ssm_inputs(B, N, C, n, 1, BF, True, 5)
+    u, delta, z, A, Bm, Cm = on(dev, *(t[k] for k in ("u", "delta", "z", "A", "Bm", "Cm")))
+    w = randn(gen(1), C, 4, dtype=BF).to(dev)
+    major = lambda x: x.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+    empty = lambda: torch.empty(N, B, C, dtype=BF, device=dev).transpose(0, 1)  # noqa: E731
+    y, s = la.la_conv_prefill(u, w)
+    y2, s2 = la.la_conv_prefill(major(u), w, y=empty())
+    assert torch.equal(y, y2) and torch.equal(s, s2)
+    y, h = la.la_ssm_prefill(u, delta, A, Bm, Cm, z=z)
+    y2, h2 = la.la_ssm_prefill(major(u), major(delta), A, Bm, Cm, z=major(z), y=empty())
+    assert torch.equal(y, y2) and torch.equal(h, h2)
+
+
+def test_stream_argument_orders_the_whole_call():
+    """Outputs with zeros for padding, copies of states, workspaces: all of a call's work is on the stream it is given."""
+    dev = cuda_device()
+    B, N, C, n = 1, 4000, 64, 16
+    t = ssm_inputs(B, N, C, n, 1, FP, False, 6)
+    u, delta, A, Bm, Cm, h0 = on(dev, *(t[k] for k in ("u", "delta", "A", "Bm", "Cm", "h")))
+    lens = torch.tensor([N - 100], device=dev)
+    w = randn(gen(1), C, 4, dtype=FP).to(dev)
+    s0 = randn(gen(2), B, 3, C, dtype=FP).to(dev)
+    q, k, v = on(dev, *swa_case(1, 2, 1, N, N, 64, BF, 9))
+    calls = (lambda s: la.la_conv_prefill(u, w, state_in=s0, lens=lens, stream=s),
+             lambda s: la.la_ssm_prefill(u, delta, A, Bm, Cm, h_in=h0, lens=lens, stream=s),
+             lambda s: (la.la_swa_prefill(q=q, k=k, v=v, lens=lens, window=300, stream=s),))
+    want = [c(None) for c in calls]
+    side = torch.cuda.Stream(dev)
+    side.wait_stream(torch.cuda.current_stream())
+    big = torch.randn(8192, 8192, device=dev)
+    for handle in (side, side.cuda_stream):
+        busy = big
+        for _ in range(6):
+            busy = busy @ big  # the current stream is behind: what a call put on it would come too late
+        got = [c(handle) for c in calls]
+        side.synchronize()
+        for g, x in zip(got, want):
+            for a, b in zip(g, x):
+                assert torch.equal(a.cpu(), b.cpu())
+    torch.cuda.synchronize()
+    with pytest.raises(TypeError):
+        la.la_conv_prefill(u, w, None, None, None, True, None, None, None, side)  # by name only

@@ -153,6 +153,29 @@ def test_swa_step_refusals(lib, base, kw, status):
     assert lib.la_swa_biased_decode_step(ctypes.byref(swa_step_args(base, **kw)), None) == status
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(y=T(at(1), 100, 0, 64)), INV), (dict(y=T(at(1), 64, 0, 64)), INV), (dict(y=T(at(1), 64, 0, 96)), INV),
+    # time-major output: the sequences lie within a token's row; no pointer for the taps is the next thing to refuse
+    (dict(y=T(at(1), 64, 0, 128), w=None), INV)])
+def test_conv_output_must_not_overlap_itself(lib, kw, status):
+    assert lib.la_conv_prefill(ctypes.byref(conv_args(**kw)), None) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(o=T(at(3), 5120, 640, 64)), INV), (dict(o=T(at(3), 64, 1280, 64)), INV), (dict(softcap=2e37), INV), (dict(softcap=1e-39), INV),
+    (dict(softcap=30.0, scale=float("inf")), INV), (dict(softcap=30.0, scale=float("nan")), INV),
+    # one query of each of 2^31 heads: more rows than a launch's grid counts
+    (dict(B=1 << 20, H=1 << 11, H_kv=1, Nq=1, Nk=1, k_cache=None, v_cache=None), UNS),
+    (dict(B=1 << 20, H_kv=4, H=4, window=256 * 16, k_cache=None, v_cache=None, o=T(at(3), 0, 1280, 64)), INV)])
+def test_swa_prefill_refuses_overlapping_outputs_extreme_caps_and_counts(lib, kw, status):
+    assert lib.la_swa_prefill(ctypes.byref(swa_args(**kw)), None) == status
+
+
+def test_swa_step_refuses_extreme_caps(lib):
+    assert lib.la_swa_biased_decode_step(ctypes.byref(swa_step_args(softcap=1e-39)), None) == INV
+    assert lib.la_swa_biased_decode_step(ctypes.byref(swa_step_args(softcap=1e38)), None) == INV
+
+
 def test_null_arguments(lib):
     for fn in (lib.la_conv_prefill, lib.la_conv_decode_step, lib.la_ssm_decode_step, lib.la_swa_prefill, lib.la_swa_biased_decode_step):
         assert fn(None, None) == INV
