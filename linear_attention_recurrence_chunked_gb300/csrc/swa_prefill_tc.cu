@@ -29,6 +29,7 @@
 // wait of the CTA lasts, no copy or product is issued and nothing is stored; the loops still run to their end.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "layers.cuh"
 #include "swa_common.cuh"
@@ -494,11 +495,12 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const uint32_t p_row = threadIdx.x % kRows;
     const uint32_t cs = tl + t * KB, col_o = tl + S::kColO + t * DP;
     const float c1 = a.scale * kLog2e;
-    // With a cap: z = zc x for a product x.  Where whole rows are `straight` the factors are drawn into Q's
-    // coefficients, cap tanh(z) = x Q(x^2) in log2 units (a zc far from 1 would take them out of the range of normal
-    // numbers, and a large cap the weights of scores near its negative).
+    // With a cap: z = zc x for a product x.  Where whole rows are straight the factors are drawn into the polynomial's
+    // coefficients, cap tanh(z) = x Q(x^2) in log2 units (as long as they stay normal numbers).
     const float zc = CAP ? a.scale / a.softcap : 0.f, cz = zc * (2.f * kLog2e), capl = a.softcap * kLog2e;
-    [[maybe_unused]] const bool straight = CAP && zc > 1e-4f && zc < 1e4f && capl <= 100.f;
+    [[maybe_unused]] const bool drawn = zc > 2e-5f && zc < 1e3f;
+    // the difference's error of 1e-7 cap stays below a hundredth of the weights' rounding: any row may take it
+    [[maybe_unused]] const bool small_cap = capl <= 400.f;
     float kq[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (CAP) {
       const float z2 = zc * zc;
@@ -577,29 +579,39 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           unpack2(p2, p0, p1);
           return pack2_bf16(p0, p1);
         };
-        // The whole row in registers; false, with nothing done, where products leave the cap's straight part.  For
-        // blocks that the whole warp sees, behind its rows where there is a bias; without cap and bias for any.
-        auto row_at_once = [&]() {
+        // The whole row in registers, for blocks that the whole warp sees (and that lie behind its rows where there is
+        // a bias; without cap and bias for any block).  A cap comes from the polynomial as the scores are used
+        // (straight; false, with nothing done, where products leave the part that it is good for or scores spread too
+        // far for the bound below), or else from the difference, in place.  4 x 16 x 4096 at d = 128 takes 386 us without
+        // a cap, 551 with the one and 816 with the other, against 1340 where a row is read in parts.
+        auto row_at_once = [&](auto straight) {
+          constexpr bool kPoly = CAP && decltype(straight)::value, kFar = CAP && !kPoly;
           constexpr int kAll = KB == 128 ? KB : 2;
           float x[kAll];
 #pragma unroll
           for (int c = 0; c + 32 <= kAll; c += 32) tmem_ld32(cs + c, x + c);
           tmem_ld_wait();
-          f32x2 c2 = pack2(c1, c1);
-          if constexpr (CAP) {
+          const float unit = kFar ? 1.f : c1;
+          f32x2 c2 = pack2(unit, unit);
+          if constexpr (kPoly) {
             float hi[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < kAll; ++c) hi[c & 3] = fmaxf(hi[c & 3], fabsf(x[c]));
             const float h = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
-            if (!__all_sync(kFullMask, h * zc <= kStraight)) return false;
+            if (!__all_sync(kFullMask, h * zc <= kStraight && h * c1 <= 60.f)) return false;
             s_read();
-            // No score exceeds cap tanh(zc h), and none is below its negative: the bound serves as the maximum.
+            // No score exceeds cap tanh(zc h), and none is below its negative: the bound serves as the maximum.  The
+            // weights stay above 2^-120, normal numbers also in bf16.
             if constexpr (!BIAS) {
               const float base = update(h * straight_tanh(h));
               c2 = pack2(-base, -base);
             }
           } else {
             s_read();
+          }
+          if constexpr (kFar) {
+#pragma unroll
+            for (int c = 0; c < kAll; ++c) x[c] = fmaf(-2.f * capl, rcp(1.f + ex2(x[c] * cz)), capl);
           }
           if constexpr (BIAS) {
 #pragma unroll
@@ -610,23 +622,23 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 #pragma unroll
               for (int e = 0; e < 32 && c + e < kAll; e += 2) {
                 const f32x2 v = pack2(x[c + e], x[c + e + 1]);
-                unpack2(fma2(v, CAP ? straight_tanh2(v) : c2, off), x[c + e], x[c + e + 1]);
+                unpack2(fma2(v, kPoly ? straight_tanh2(v) : c2, off), x[c + e], x[c + e + 1]);
                 off = add2(off, step);
               }
             }
-          } else if constexpr (!CAP) {
+          } else if constexpr (!kPoly) {
             if (!__all_sync(kFullMask, va <= 0 && vb >= KB)) {
 #pragma unroll
               for (int c = 0; c < kAll; ++c) x[c] = c >= va && c < vb ? x[c] : -INFINITY;
             }
           }
           f32x2 base2 = c2;
-          if constexpr (BIAS || !CAP) {
+          if constexpr (BIAS || !kPoly) {
             float mx[4] = {x[0], x[0], x[0], x[0]};
 #pragma unroll
             for (int c = 0; c < kAll; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
             float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (!BIAS && mn != -INFINITY) mn *= c1;  // the scale is positive here
+            if (!BIAS && mn != -INFINITY) mn *= unit;  // the scale is positive here
             const float base = update(mn);
             base2 = pack2(-base, -base);
           }
@@ -634,7 +646,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 #pragma unroll
           for (int e = 0; e < kAll / 2; ++e) {
             const f32x2 v = pack2(x[2 * e], x[2 * e + 1]);
-            w[e] = weight(BIAS ? add2(v, base2) : fma2(v, CAP ? straight_tanh2(v) : c2, base2), e);
+            w[e] = weight(BIAS ? add2(v, base2) : fma2(v, kPoly ? straight_tanh2(v) : c2, base2), e);
           }
           wait_o();  // the products of the block before may have read P's place until here
 #pragma unroll
@@ -655,7 +667,10 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
               float hi[2] = {0.f, 0.f};
 #pragma unroll
               for (int c = 0; c < 32; ++c) hi[c & 1] = fmaxf(hi[c & 1], fabsf(v[c]));
-              if (fmaxf(hi[0], hi[1]) * fabsf(zc) <= kStraight) {
+              // half a warp each way would cost both
+              bool near = fmaxf(hi[0], hi[1]) * fabsf(zc) <= kStraight;
+              if (small_cap) near = __all_sync(kFullMask, near);
+              if (near) {
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
                   const f32x2 x = pack2(v[c], v[c + 1]), z = mul2(x, pack2(zc, zc)), u = mul2(z, z);
@@ -722,10 +737,16 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         if constexpr (KB == 64) {  // such blocks are few, and hardly ever seen as a whole
           row_by_parts();
         } else if constexpr (!CAP && !BIAS) {
-          row_at_once();
+          row_at_once(std::false_type{});
         } else {
           const bool whole = __all_sync(kFullMask, va <= 0 && vb >= KB && (!BIAS || pos - k0 >= KB - 1));
-          if (!whole || (CAP && !straight) || !row_at_once()) row_by_parts();
+          bool done = false;
+          if constexpr (CAP) {
+            done = whole && ((drawn && row_at_once(std::true_type{})) || (small_cap && row_at_once(std::false_type{})));
+          } else if (whole) {
+            done = row_at_once(std::false_type{});
+          }
+          if (!done) row_by_parts();
         }
         float s0, s1;
         unpack2(add2(sum[0], sum[1]), s0, s1);
