@@ -7,17 +7,23 @@
 // A CTA takes 64 queries of one head and walks the key tiles between its lowest lo and highest hi; each
 // of its 256 threads holds a 4 x 4 piece of the scores and 4 rows x d/16 columns of the output.  fp32
 // products run on the CUDA cores (bf16 operands would not keep fp32's accuracy), which bound it.
+// Where the query tiles leave SMs idle, the CTAs of a cluster share a tile's keys; their maxima, sums and outputs
+// meet in distributed shared memory, so that no workspace is needed.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
 #include "layers.cuh"
 #include "swa_common.cuh"
 
 namespace la {
 namespace {
 
-constexpr int kBM = 64, kBN = 64, kThreads = 256;
+constexpr int kBM = 64, kBN = 64, kThreads = 256, kSMs = 152;
 
 template <typename TIn, typename TOut, int DP>
 __global__ void __launch_bounds__(kThreads)
-swa_simt_kernel(const SwaPrefillLaunch a, int q_tiles) {
+swa_simt_kernel(const SwaPrefillLaunch a, int q_tiles, int parts) {
   constexpr int LD = DP + 4;       // row pitch of Q, K, V in floats: rows start 4 banks apart
   constexpr int LP = kBN + 4;
   constexpr int NC = DP / 16;      // output columns per thread: tx + 16 j
@@ -28,13 +34,15 @@ swa_simt_kernel(const SwaPrefillLaunch a, int q_tiles) {
   float* Ps = Vs + kBN * LD;       // [64][LP]
   __shared__ int s_lo[kBM], s_hi[kBM];
   __shared__ int s_range[2];
+  __shared__ float s_m[kBM], s_l[kBM];  // of this CTA's share of the keys
 
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int64_t bh = blockIdx.x / q_tiles;
-  const int qt = (int)(blockIdx.x % q_tiles);
+  const int part = (int)(blockIdx.x % parts);  // the cluster's rank
+  const int64_t tile = blockIdx.x / parts, bh = tile / q_tiles;
+  const int qt = (int)(tile % q_tiles);
   const int64_t b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hkv);
-  const int64_t len = sequence_length(a.lens, b, a.Nk, a.status, h == 0 && qt == 0 && tid == 0);
-  if (len < 0) return;
+  const int64_t len = sequence_length(a.lens, b, a.Nk, a.status, h == 0 && qt == 0 && part == 0 && tid == 0);
+  if (len < 0) return;  // the whole cluster
   const int64_t i0 = (int64_t)qt * kBM;
   if (tid == 0) {
     s_range[0] = INT32_MAX;
@@ -75,7 +83,7 @@ swa_simt_kernel(const SwaPrefillLaunch a, int q_tiles) {
   }
   const float slope = a.slopes ? a.slopes[h] : 0.f;
 
-  for (int j0 = first; j0 < last; j0 += kBN) {
+  for (int j0 = last > 0 ? first + part * kBN : 0; j0 < last; j0 += parts * kBN) {  // none seen: last = 0
     __syncthreads();  // the previous tile is used up
     bool bad = false;
     for (int e = tid; e < kBN * (DP / 4); e += kThreads) {
@@ -166,6 +174,47 @@ swa_simt_kernel(const SwaPrefillLaunch a, int q_tiles) {
     }
   }
   TOut* out = reinterpret_cast<TOut*>(a.o) + b * a.o_sb + h * a.o_sh;
+  if (parts > 1) {
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    __syncthreads();  // the last tile is used up: its place takes the output
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) Ks[r * LD + tx + 16 * c] = o[i][c];
+      if (tx == 0) {
+        s_m[r] = m[i];
+        s_l[r] = l[i];
+      }
+    }
+    cluster.sync();
+    // rows part, part + parts, ...: a half warp a row
+    for (int r = part + (tid >> 4) * parts; r < kBM; r += (kThreads / 16) * parts) {
+      const int64_t row = i0 + r;
+      if (row < a.Nq && a.q_pos0 + row < len) {
+        float top = -INFINITY, total = 0.f, sum[NC];
+        for (int u = 0; u < parts; ++u) top = fmaxf(top, *cluster.map_shared_rank(&s_m[r], u));
+#pragma unroll
+        for (int c = 0; c < NC; ++c) sum[c] = 0.f;
+        for (int u = 0; u < parts; ++u) {
+          const float mu = *cluster.map_shared_rank(&s_m[r], u), lu = *cluster.map_shared_rank(&s_l[r], u);
+          if (lu == 0.f) continue;  // this share holds none of the row's keys
+          const float f = __expf(mu - (top == -INFINITY ? 0.f : top));
+          const float* x = cluster.map_shared_rank(Ks + r * LD, u);
+          total = fmaf(f, lu, total);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) sum[c] = fmaf(f, x[tx + 16 * c], sum[c]);
+        }
+        const float inv = total == 0.f ? 0.f : 1.f / total;  // a row that sees nothing gives zeros
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          if (tx + 16 * c < a.d) store1(out + row * a.o_st + tx + 16 * c, sum[c] * inv);
+      }
+    }
+    cluster.sync();  // the parts are read before a CTA ends
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t row = i0 + ty * 4 + i;
@@ -208,8 +257,23 @@ cudaError_t launch_simt(const SwaPrefillLaunch& a, cudaStream_t stream) {
   const cudaError_t e = allow_smem(swa_simt_kernel<TIn, TOut, DP>, kSmem, done);
   if (e != cudaSuccess) return e;
   const int q_tiles = (int)((a.Nq + kBM - 1) / kBM);
-  swa_simt_kernel<TIn, TOut, DP><<<(unsigned)(a.B * a.H * q_tiles), kThreads, kSmem, stream>>>(a, q_tiles);
-  return cudaGetLastError();
+  const int64_t tiles = a.B * a.H * q_tiles;
+  // key tiles of a query tile at most
+  const int64_t keys = std::min<int64_t>((a.Nk + kBN - 1) / kBN, a.window > 0 ? (a.window + kBM + 2 * kBN - 2) / kBN : INT32_MAX);
+  int parts = 1;
+  while (parts < 8 && tiles * parts < kSMs && parts < keys) parts *= 2;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = (unsigned)parts;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(tiles * parts));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, swa_simt_kernel<TIn, TOut, DP>, a, q_tiles, parts);
 }
 
 template <typename TIn, typename TOut>

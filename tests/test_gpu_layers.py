@@ -672,3 +672,35 @@ def test_stream_argument_orders_the_whole_call():
     torch.cuda.synchronize()
     with pytest.raises(TypeError):
         la.la_conv_prefill(u, w, None, None, None, True, None, None, None, side)  # by name only
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("Nq,Nk,d,window,softcap,slopes,lens", [
+    (1, 1, 64, 0, 0.0, False, None), (1, 2000, 128, 0, 0.0, False, None), (7, 1501, 40, 0, 0.0, True, None), (133, 1333, 64, 0, 5.0, False, None),
+    (300, 2300, 96, 900, 0.0, True, None), (65, 700, 128, 0, 0.0, False, [640, 700]), (40, 4000, 8, 2000, 3.0, True, [3990, 1000])])
+def test_swa_few_queries_share_their_keys(dtype, Nq, Nk, d, window, softcap, slopes, lens):
+    """Few query tiles over long caches: clusters of blocks share a tile's keys."""
+    dev = cuda_device()
+    B, H, Hkv = (len(lens) if lens else 1), 2, 1
+    q, k, v = swa_case(B, H, Hkv, Nq, Nk, d, dtype, Nq + Nk)
+    sl = slopes_of(H) if slopes else None
+    dlens = None if lens is None else torch.tensor(lens, device=dev)
+    rows = ref.spans(Nq, Nk, B, window, None, None, Nk - Nq, lens)
+    o_ref, bound = ref.swa(q, k, v, d ** -0.5, softcap, sl, rows, Nk - Nq, dtype)
+    qd, kd, vd, sld = on(dev, q, k, v, sl)
+    o = la.la_swa_prefill(qd, kd, vd, window=window, softcap=softcap, slopes=sld, lens=dlens)
+    ref.check(o, o_ref, bound)
+    for _ in range(3):
+        assert torch.equal(la.la_swa_prefill(qd, kd, vd, window=window, softcap=softcap, slopes=sld, lens=dlens), o)
+    # values that no query sees, and rows that see nothing but one share's keys
+    lo = torch.full((B, Nq), max(0, Nk // 2 - 3), dtype=torch.int32)
+    hi = torch.minimum(lo + 1 + torch.arange(Nq, dtype=torch.int32) % 5, torch.tensor(Nk, dtype=torch.int32))
+    hi[:, ::3] = lo[:, ::3]
+    seen = torch.zeros(Nk, dtype=torch.bool)
+    seen[int(lo[0, 0]):int(lo[0, 0]) + 5] = True
+    k[:, :, ~seen], v[:, :, ~seen] = float("nan"), float("inf")
+    rows = ref.spans(Nq, Nk, B, 0, lo.numpy(), hi.numpy(), Nk - Nq, lens)
+    o_ref, bound = ref.swa(q, k, v, d ** -0.5, softcap, sl, rows, Nk - Nq, dtype)
+    o = la.la_swa_prefill(*on(dev, q, k, v), softcap=softcap, slopes=sld, lens=dlens, key_lo=lo.to(dev), key_hi=hi.to(dev))
+    ref.check(o, o_ref, bound)
+    assert la.la_device_status() == la.LA_OK
