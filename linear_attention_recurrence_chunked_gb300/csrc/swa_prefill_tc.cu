@@ -19,6 +19,9 @@
 // finished.  Widths up to 64 with narrow windows take blocks of 64 keys and two CTAs an SM: their blocks are
 // few, and a chain of product, softmax and product is mostly latency.
 //
+// Where items leave SMs idle and see many blocks, the CTAs of a cluster share an item's blocks; each leaves its
+// rows' outputs, divided by their sums, and m + log2 l in its shared memory, where the cluster joins them.
+//
 // Warps 0-3 and 4-7: rows of tile 0 and 1; warps 8 and 11: their MMAs; warp 9: copies; warp 10: looks at each
 // value block before it is used.  A value that a row does not see enters its product as 0 * v, which a NaN or an
 // infinity would spoil: rows of padding are overwritten with zeros in shared memory, and where a block that
@@ -27,6 +30,8 @@
 //
 // Every wait is bounded.  One that expires sets the status word and a flag in shared memory, after which no
 // wait of the CTA lasts, no copy or product is issued and nothing is stored; the loops still run to their end.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -46,6 +51,10 @@ constexpr int kSMs = 152;
 // Windows up to this are narrow: blocks of 64 keys, two CTAs an SM.  8 x 16 x 4096 at d = 64: 88 us against 118
 // with blocks of 128 for a window of 64, 124 against 132 for 256, 168 against 170 for 512.
 constexpr int64_t kNarrow = 512;
+// Blocks of keys that a CTA of a cluster gets at least (128 keys each).  8 heads of 16 queries over 65536 keys: 118 us
+// with clusters of 8 against 853 without; 64 over 1024 (a share of 2): 16 against 21; 1024 over 1024 under the
+// causal mask: 24 against 22; with shares of 3 or more the second and the third take 20 and 30 us.
+constexpr int64_t kShare = 2;
 
 // DP: width padded to whole 64-column blocks; KB: keys per block
 template <int DP, int KB>
@@ -221,8 +230,10 @@ struct Item {
   int b, h, i0, len;
   // The last queries see the most keys under the causal mask: items go from the last tiles to the first, and
   // every other round of CTAs takes its items in reverse.  False: there is none, or its sequence is skipped.
-  __device__ __forceinline__ bool place(const SwaPrefillLaunch& a, int round, int items, int q_tiles, bool report) {
-    const int64_t at = (int64_t)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  // (Parts of an item are neighbouring CTAs, and then there is one round.)
+  __device__ __forceinline__ bool place(const SwaPrefillLaunch& a, int round, int items, int q_tiles, int parts, bool report) {
+    const int64_t at = parts > 1 ? blockIdx.x / parts
+                                 : (int64_t)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     if (at >= items) return false;
     const int heads = (int)(a.B * a.H), bh = (int)at % heads;
     i0 = (q_tiles - 1 - (int)at / heads) * (2 * kRows);
@@ -240,7 +251,7 @@ struct Blocks {
   int f_lo[2], f_hi[2];
   int j0, j1;            // and of both
 
-  __device__ __forceinline__ Blocks(const SwaPrefillLaunch& a, const Item& it) {
+  __device__ __forceinline__ Blocks(const SwaPrefillLaunch& a, const Item& it, int parts) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const TileSpan s = tile_span(a, it.b, it.i0 + t * kRows, it.len);
@@ -249,6 +260,19 @@ struct Blocks {
       f_lo[t] = s.f_lo;
       f_hi[t] = s.f_hi;
     }
+    bounds();
+    if (parts > 1) {  // this CTA's share
+      const int share = (j1 - j0 + parts - 1) / parts, from = j0 + (int)(blockIdx.x % parts) * share, to = from + share;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        jb[t] = max(jb[t], from);
+        je[t] = min(je[t], to);
+        if (jb[t] >= je[t]) jb[t] = je[t] = 0;
+      }
+      bounds();
+    }
+  }
+  __device__ __forceinline__ void bounds() {
     const bool any0 = jb[0] < je[0], any1 = jb[1] < je[1];
     j0 = any0 && any1 ? min(jb[0], jb[1]) : any0 ? jb[0] : jb[1];
     j1 = max(je[0], je[1]);
@@ -266,10 +290,75 @@ struct Blocks {
   }
 };
 
+// Where a part's output has four columns of a row of tile t: the lower half of the columns in the place of the
+// queries, the upper one in that of the weights.
+template <int DP, int KB>
+__device__ __forceinline__ float4* part_at(uint8_t* sm, int t, int row, int c4) {
+  using S = Shape<DP, KB>;
+  constexpr int kHalf = DP / 8;  // float4 per half row
+  const uint32_t base = c4 < kHalf ? t * S::kQTile : S::kOffP + t * S::kPTile;
+  return reinterpret_cast<float4*>(sm + base) + row * kHalf + ((c4 % kHalf) ^ (row & 7));
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The item's rows out of the cluster's parts; every CTA takes rows of its own, a warp a row.
 template <int DP, int KB, bool CAP, bool BIAS>
+__device__ __noinline__ void join_parts(const SwaPrefillLaunch& a, const Item& it, uint8_t* sm, float* lse, uint32_t* redo, int parts,
+                                        volatile uint32_t* dead) {
+  namespace cg = cooperative_groups;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t again[2] = {0, 0};
+  for (int u = 0; u < parts; ++u)
+    for (int t = 0; t < 2; ++t) again[t] |= *cluster.map_shared_rank(redo + t, u);
+  if (*dead) return;
+#pragma unroll 1
+  for (int r = (int)(blockIdx.x % parts) + warp * parts; r < 2 * kRows; r += 8 * parts) {
+    const int row = it.i0 + r;
+    if (row >= a.Nq || a.q_pos0 + row >= it.len) continue;
+    if (r < kRows ? again[0] : again[1]) {
+      slow_row<CAP, BIAS>(a, it.b, it.h, it.h / (a.H / a.Hkv), row, key_span(a, it.b, row, it.len),
+                          BIAS && a.slopes ? a.slopes[it.h] * kLog2e : 0.f);
+      continue;
+    }
+    float e[8], top = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      e[u] = u < parts ? *cluster.map_shared_rank(lse + r, u) : -INFINITY;
+      top = fmaxf(top, e[u]);
+    }
+    if (top == -INFINITY) top = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (e[u] == -INFINITY) continue;  // no keys of this row there, and no output
+      const float f = ex2(e[u] - top);
+      total += f;
+      if (lane * 4 < a.d) {
+        const float4 x = *cluster.map_shared_rank(part_at<DP, KB>(sm, r / kRows, r % kRows, lane), u);
+        o.x = fmaf(f, x.x, o.x); o.y = fmaf(f, x.y, o.y); o.z = fmaf(f, x.z, o.z); o.w = fmaf(f, x.w, o.w);
+      }
+    }
+    if (lane * 4 < a.d) {
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+      const int64_t at = (int64_t)it.b * a.o_sb + (int64_t)it.h * a.o_sh + (int64_t)row * a.o_st + lane * 4;
+      if (a.out_bf16) store_floats(reinterpret_cast<__nv_bfloat16*>(a.o) + at, v, 4, true);
+      else store_floats(reinterpret_cast<float*>(a.o) + at, v, 4, true);
+    }
+  }
+}
+
+// JOIN: an item belongs to a cluster of `clusters` CTAs
+template <int DP, int KB, bool CAP, bool BIAS, bool JOIN>
 __global__ void __launch_bounds__(kThreads, Shape<DP, KB>::kCtas)
 swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-              const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SwaPrefillLaunch a, int items, int q_tiles) {
+              const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SwaPrefillLaunch a, int items, int q_tiles, int clusters) {
+  const int parts = JOIN ? clusters : 1;
   using S = Shape<DP, KB>;
   constexpr uint32_t kSlots = S::kSlots;
   extern __shared__ uint8_t smem_raw[];
@@ -287,6 +376,9 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   // next one waits for the rows to have read this one's output, and the ring holds kSlots blocks.  (Items that see
   // nothing pass without a wait, any number of them, and do not count.)
   __shared__ volatile uint32_t bad[2][8];
+  // with parts: a row's m + log2 l (no keys: -infinity), and whether a tile's rows have to be computed again
+  __shared__ float lse[JOIN ? 2 * kRows : 1];
+  __shared__ uint32_t redo[2];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(sm);
@@ -307,6 +399,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     }
     mbar_init(smem_u32(&bar_fin), 2);
     dead = 0;
+    redo[0] = redo[1] = 0;
     for (int n = 0; n < 16; ++n) bad[n / 8][n % 8] = 0;
     fence_mbar_init();
   }
@@ -328,7 +421,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   auto slot = [](uint32_t i) { return i % kSlots; };
   auto phase = [](uint32_t i) { return i / kSlots; };
   const int group = (int)(a.H / a.Hkv);
-  const int rounds = (items + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int rounds = JOIN ? 1 : (items + (int)gridDim.x - 1) / (int)gridDim.x;
   Item it;
 
   if (warp >= 8) {
@@ -337,8 +430,8 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       // ================================================================ copies: one thread
       uint32_t i = 0, n = 0;
       for (int r = 0; r < rounds; ++r) {
-        if (!it.place(a, r, items, q_tiles, false)) continue;
-        const Blocks<KB> bl(a, it);
+        if (!it.place(a, r, items, q_tiles, parts, false)) continue;
+        const Blocks<KB> bl(a, it, parts);
         if (bl.j0 >= bl.j1) continue;
         if (lane == 0) {
           if (n > 0) wait(&bar_qfree, n - 1);
@@ -380,8 +473,8 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       // ================================================================ a look at each value block
       uint32_t i = 0, iv = 0, n0 = 0, n1 = 0;
       for (int r = 0; r < rounds; ++r) {
-        if (!it.place(a, r, items, q_tiles, lane == 0)) continue;
-        const Blocks<KB> bl(a, it);
+        if (!it.place(a, r, items, q_tiles, parts, lane == 0 && (parts == 1 || blockIdx.x % parts == 0))) continue;
+        const Blocks<KB> bl(a, it, parts);
         const bool any0 = bl.jb[0] < bl.je[0], any1 = bl.jb[1] < bl.je[1];
         if (any0) ++n0;
         if (any1) ++n1;
@@ -424,8 +517,8 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       const uint32_t q_lo = desc_lo(sbase + t * S::kQTile, 0), p_lo = desc_lo(sbase + S::kOffP + t * S::kPTile, 0);
       const uint32_t s_col = tmem + t * KB, o_col = tmem + S::kColO + t * DP;
       for (int r = 0; r < rounds; ++r) {
-        if (!it.place(a, r, items, q_tiles, false)) continue;
-        const Blocks<KB> bl(a, it);
+        if (!it.place(a, r, items, q_tiles, parts, false)) continue;
+        const Blocks<KB> bl(a, it, parts);
         if (bl.j0 >= bl.j1) continue;
         const int jb = t ? bl.jb[1] : bl.jb[0], je = t ? bl.je[1] : bl.je[0];
         wait(&bar_q, n);
@@ -486,6 +579,10 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       mbar_wait(smem_u32(&bar_fin), 0, a.status);
       __syncwarp();
     }
+    if constexpr (JOIN) {  // the rows join their parts
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     // ================================================================ one thread per row
     regs_inc<S::kRegsRows>();
@@ -520,11 +617,16 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const bool al32 = ((reinterpret_cast<uintptr_t>(a.o) | (uintptr_t)((a.o_sb | a.o_sh | a.o_st) * (a.out_bf16 ? 2 : 4))) & 31u) == 0;
     uint32_t ns = 0, n = 0;  // blocks, items at whose keys this tile is at work
     for (int round = 0; round < rounds; ++round) {
-      if (!it.place(a, round, items, q_tiles, false)) continue;
+      if (!it.place(a, round, items, q_tiles, parts, false)) continue;
       const int i = it.i0 + (int)threadIdx.x;
       const KeySpan span = key_span(a, it.b, i, it.len);
       const TileSpan ts = tile_span(a, it.b, it.i0 + t * kRows, it.len);
-      const int jb = ts.lo < ts.hi ? ts.lo / KB : 0, je = ts.lo < ts.hi ? (ts.hi + KB - 1) / KB : 0;
+      int jb = ts.lo < ts.hi ? ts.lo / KB : 0, je = ts.lo < ts.hi ? (ts.hi + KB - 1) / KB : 0;
+      if (JOIN) {
+        const Blocks<KB> bl(a, it, parts);
+        jb = t ? bl.jb[1] : bl.jb[0];
+        je = t ? bl.je[1] : bl.je[0];
+      }
       const int pos = (int)a.q_pos0 + i;
       const float slope2 = BIAS && a.slopes ? a.slopes[it.h] * kLog2e : 0.f;
       float m = -INFINITY, l = 0.f;
@@ -764,6 +866,25 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         ++n;
         again = bad[t][(n - 1) % 8] == n;
       }
+      if (JOIN) {
+        // The tile's own queries and weights are used up: their places take its outputs.  (Queries may still be on
+        // their way to a tile that is not at work, which leaves nothing.)
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        if (jb < je) {
+#pragma unroll 1
+          for (int c = 0; c < DP; c += 16) {
+            float o[16];
+            tmem_ld16(col_o + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *part_at<DP, KB>(sm, t, (int)p_row, (c + e) / 4) = make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+          }
+        }
+        lse[threadIdx.x] = l != 0.f ? m + __log2f(l) : -INFINITY;
+        if (again && lane == 0) redo[t] = 1;
+        break;
+      }
       const bool live = i < a.Nq && a.q_pos0 + i < it.len && !dead;
       const bool seen = l != 0.f;  // also a row whose sum is NaN
       const float inv = seen ? 1.f / l : 0.f;
@@ -811,6 +932,11 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         }
       }
     }
+    if (JOIN) {
+      cluster_sync();
+      if (it.place(a, 0, items, q_tiles, parts, false)) join_parts<DP, KB, CAP, BIAS>(a, it, sm, lse, redo, parts, &dead);
+      cluster_sync();  // the parts are read before a CTA ends
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -852,26 +978,67 @@ bool encode(CUtensorMap* map, const View4& x, int64_t B, int64_t H, int64_t N, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DP, int KB, bool CAP, bool BIAS>
+// blocks of keys that an item may see
+int64_t key_blocks(const SwaPrefillLaunch& a, int KB) { return (a.window > 0 ? std::min(a.Nk, a.window + 2 * kRows) : a.Nk) / KB; }
+
+template <int DP, int KB, bool CAP, bool BIAS, bool JOIN>
 cudaError_t launch_typed(const SwaPrefillLaunch& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
   using S = Shape<DP, KB>;
+  const auto kernel = swa_tc_kernel<DP, KB, CAP, BIAS, JOIN>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(swa_tc_kernel<DP, KB, CAP, BIAS>, (int)S::kSmem, done);
+  cudaError_t e = allow_smem(kernel, (int)S::kSmem, done);
   if (e != cudaSuccess) return e;
   // the row threads' registers come out of the launch's own: with fewer they would be waited for without end
   static std::atomic<int> regs{0};
   if (regs.load(std::memory_order_relaxed) == 0) {
     cudaFuncAttributes f{};
-    e = cudaFuncGetAttributes(&f, swa_tc_kernel<DP, KB, CAP, BIAS>);
+    e = cudaFuncGetAttributes(&f, kernel);
     if (e != cudaSuccess) return e;
     regs.store(f.numRegs, std::memory_order_relaxed);
   }
   if (regs.load(std::memory_order_relaxed) < S::kRegs) return cudaErrorInvalidConfiguration;
   const int q_tiles = (int)((a.Nq + 2 * kRows - 1) / (2 * kRows));
   const int64_t items = a.B * a.H * q_tiles;
-  const unsigned grid = (unsigned)std::min<int64_t>(items, S::kCtas * kSMs);
-  swa_tc_kernel<DP, KB, CAP, BIAS><<<grid, kThreads, S::kSmem, stream>>>(q, k, v, a, (int)items, q_tiles);
-  return cudaGetLastError();
+  cudaLaunchAttribute cluster;
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = &cluster;
+  int parts = 1;
+  if constexpr (JOIN) {
+    static std::atomic<int> room[4] = {};  // clusters of 2, 4 and 8 that the GPU holds at once (its SMs come in groups), + 1
+    for (int log = 3; log >= 1 && parts == 1; --log) {
+      if (key_blocks(a, KB) < (kShare << log) || items > (kSMs >> log)) continue;
+      cluster.id = cudaLaunchAttributeClusterDimension;
+      cluster.val.clusterDim.x = 1u << log;
+      cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+      cfg.numAttrs = 1;
+      cfg.gridDim = dim3((unsigned)(items << log));
+      int n = room[log].load(std::memory_order_relaxed);
+      if (n == 0) {
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (e != cudaSuccess) return e;
+        room[log].store(++n, std::memory_order_relaxed);
+      }
+      if (items < n) parts = 1 << log;
+    }
+    if (parts == 1) return cudaErrorNotReady;  // for the kernel without
+  } else {
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, S::kCtas * kSMs));
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, q, k, v, a, (int)items, q_tiles, parts);
+}
+
+template <int DP, int KB, bool CAP, bool BIAS>
+cudaError_t launch_parts(const SwaPrefillLaunch& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+  if constexpr (KB == 128) {
+    if (a.B * a.H * ((a.Nq + 2 * kRows - 1) / (2 * kRows)) <= kSMs / 2 && key_blocks(a, KB) >= 2 * kShare) {
+      const cudaError_t e = launch_typed<DP, KB, CAP, BIAS, true>(a, q, k, v, stream);
+      if (e != cudaErrorNotReady) return e;
+    }
+  }
+  return launch_typed<DP, KB, CAP, BIAS, false>(a, q, k, v, stream);
 }
 
 template <int DP, int KB>
@@ -882,10 +1049,10 @@ cudaError_t launch_width(const SwaPrefillLaunch& a, cudaStream_t stream) {
     return cudaErrorNotSupported;  // strides that TMA cannot describe
   // without a bias the maximum is taken of the raw products, which the scale must not turn round
   const bool cap = a.softcap != 0.f, bias = a.slopes != nullptr || !(a.scale > 0.f);
-  if (cap && bias) return launch_typed<DP, KB, true, true>(a, q, k, v, stream);
-  if (cap) return launch_typed<DP, KB, true, false>(a, q, k, v, stream);
-  if (bias) return launch_typed<DP, KB, false, true>(a, q, k, v, stream);
-  return launch_typed<DP, KB, false, false>(a, q, k, v, stream);
+  if (cap && bias) return launch_parts<DP, KB, true, true>(a, q, k, v, stream);
+  if (cap) return launch_parts<DP, KB, true, false>(a, q, k, v, stream);
+  if (bias) return launch_parts<DP, KB, false, true>(a, q, k, v, stream);
+  return launch_parts<DP, KB, false, false>(a, q, k, v, stream);
 }
 
 }  // namespace
