@@ -7,6 +7,9 @@
 // four 2-byte elements of memory: with 16 states the special-function unit (16 results per SM and clock)
 // bounds it at three times the memory time.  The decay differs per (channel, state), so no chunk form on
 // the tensor cores exists: the tokens are walked in order, with the channels and states in parallel.
+// 4 x 16384 x 2048 channels with 16 states, bf16: 804 us.  The bytes alone take 161 us and the exponentials 220 us (32 of
+// them an SM and clock, at the 2.0 GHz it ran at); the four scan warps' issue slots bound it at about 500 us, and
+// shared memory (LSU pipe 70 % busy) and the barrier a tile make up the rest.
 //
 // A block has four scan warps, four layout warps and four output warps, which work on tiles of tokens in turn
 // through shared memory, one barrier a tile.  While the scan warps walk tile i, the layout warps prepare tile
@@ -423,7 +426,8 @@ ssm_combine_kernel(const SsmLaunch a, Segments seg, float* ws_h, const float* ws
 }
 
 // ---------------------------------------------------------------------------------------------- one token
-// The step reads and writes each state once, which bounds it.  L lanes share a channel, four states a lane, for
+// The step reads and writes each state once, which bounds it: 256 x 4096 x 16 takes 25 us, 5.7 TB/s, 85 % of the
+// measured copy rate (33 us with the loads behind the arithmetic that uses them).  L lanes share a channel, four states a lane, for
 // four sequences at a time: A, D and the bias are loaded once for them, the four states' loads are in flight
 // together, and of the channel's lanes each computes the step size and the gate of a sequence of its own.
 constexpr int kStepThreads = 256;

@@ -8,7 +8,9 @@
 // of its 256 threads holds a 4 x 4 piece of the scores and 4 rows x d/16 columns of the output.  fp32
 // products run on the CUDA cores (bf16 operands would not keep fp32's accuracy), which bound it.
 // Where the query tiles leave SMs idle, the CTAs of a cluster share a tile's keys; their maxima, sums and outputs
-// meet in distributed shared memory, so that no workspace is needed.
+// meet in distributed shared memory, so that no workspace is needed (6 heads of 133 queries over 333 keys at d = 40:
+// 47 -> 25 us).  16 heads of 512 queries over 16384 keys at d = 64: 1260 us, 27 TFLOP/s of 80: each float4 read from
+// shared memory feeds eight multiply-adds, half of what the cores could take.
 #include <cooperative_groups.h>
 
 #include <algorithm>
