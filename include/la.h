@@ -403,9 +403,15 @@ la_status la_notebank_route(const la_notebank_route_args* args, void* stream);
  *     they were, and the state is the one after token lens[b] - 1.  A length
  *     outside [0, N] skips the whole sequence (nothing of it is written) and
  *     sets the device status word (LA_ERR_INVALID_ARGUMENT).
+ *   - fill: LA_FILL_ROWS writes zeros into the output rows of padding (and of
+ *     skipped sequences), LA_FILL_STATE writes the incoming state (zeros
+ *     without one) into the state of skipped sequences; 0 leaves them.
  *   - outputs must not overlap inputs, except a state updated in place
  *     (state_out == state_in), and an output's elements must not overlap one
  *     another (sequences or heads repeated with stride 0 are for inputs). */
+
+#define LA_FILL_ROWS 1
+#define LA_FILL_STATE 2
 
 /* Causal depthwise convolution over a prompt.
  *   y_t[c] = act(bias[c] + sum_{i<W} w[c,i] x_{t-W+1+i}[c]),   act = identity or SiLU
@@ -425,6 +431,7 @@ typedef struct la_conv_prefill_args {
   void* state_out;
   const int64_t* lens;
   int32_t silu;
+  int32_t fill;
 } la_conv_prefill_args;
 la_status la_conv_prefill(const la_conv_prefill_args* args, void* stream);
 
@@ -479,6 +486,7 @@ typedef struct la_ssm_prefill_args {
   float* h_out;
   const int64_t* lens;
   int32_t delta_softplus;
+  int32_t fill;
 } la_ssm_prefill_args;
 size_t la_ssm_prefill_workspace_size(const la_ssm_prefill_args* args);
 la_status la_ssm_prefill(const la_ssm_prefill_args* args, void* workspace, size_t workspace_bytes, void* stream);
@@ -539,6 +547,7 @@ typedef struct la_swa_prefill_args {
   const int64_t* lens;
   void* k_cache;
   void* v_cache;
+  int32_t fill;  /* LA_FILL_ROWS or 0 */
 } la_swa_prefill_args;
 la_status la_swa_prefill(const la_swa_prefill_args* args, void* stream);
 

@@ -111,7 +111,7 @@ class ConvPrefillArgs(ctypes.Structure):
                 ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
                 ("x", LATensor), ("y", LATensor), ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p),
                 ("state_in", ctypes.c_void_p), ("state_out", ctypes.c_void_p), ("lens", ctypes.c_void_p),
-                ("silu", ctypes.c_int32)]
+                ("silu", ctypes.c_int32), ("fill", ctypes.c_int32)]
 
 
 class ConvDecodeArgs(ctypes.Structure):
@@ -129,7 +129,7 @@ class SsmPrefillArgs(ctypes.Structure):
                 ("Bm", LATensor), ("Cm", LATensor),
                 ("A", ctypes.c_void_p), ("D", ctypes.c_void_p), ("delta_bias", ctypes.c_void_p),
                 ("h_in", ctypes.c_void_p), ("h_out", ctypes.c_void_p), ("lens", ctypes.c_void_p),
-                ("delta_softplus", ctypes.c_int32)]
+                ("delta_softplus", ctypes.c_int32), ("fill", ctypes.c_int32)]
 
 
 class SsmDecodeArgs(ctypes.Structure):
@@ -147,7 +147,7 @@ class SwaPrefillArgs(ctypes.Structure):
                 ("q", LATensor), ("k", LATensor), ("v", LATensor), ("o", LATensor),
                 ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
                 ("key_lo", ctypes.c_void_p), ("key_hi", ctypes.c_void_p), ("q_pos0", _i64), ("lens", ctypes.c_void_p),
-                ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p)]
+                ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("fill", ctypes.c_int32)]
 
 
 class SwaBiasedDecodeArgs(ctypes.Structure):
@@ -661,21 +661,24 @@ def _address(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _new_rows(shape, dtype, device, zero=False):
-    """An output whose rows start on 16-byte boundaries whatever the last size is."""
-    make = torch.zeros if zero else torch.empty
+def _new_rows(x, shape, dtype):
+    """An output beside x whose rows start on 16-byte boundaries whatever the last size is."""
     if shape[-1] % 8 == 0:
-        return make(shape, dtype=dtype, device=device)
-    return make((*shape[:-1], -(-shape[-1] // 8) * 8), dtype=dtype, device=device)[..., :shape[-1]]
+        return x.new_empty(shape, dtype=dtype)
+    return x.new_empty((*shape[:-1], -(-shape[-1] // 8) * 8), dtype=dtype)[..., :shape[-1]]
+
+
+# what a call with lens writes into outputs that were made for it (include/la.h)
+_FILL_ROWS, _FILL_STATE = 1, 2
 
 
 # The argument structs of include/la.h as words, for one pack() a call (the ctypes structures above describe the
 # same bytes).
-_CONV_PREFILL = struct.Struct("<4q3i4x8q5qi4x")
+_CONV_PREFILL = struct.Struct("<4q3i4x8q5q2i")
 _CONV_DECODE = struct.Struct("<3q3i4x8qi4x")
-_SSM_PREFILL = struct.Struct("<5q2i24q6qi4x")
+_SSM_PREFILL = struct.Struct("<5q2i24q6q2i")
 _SSM_DECODE = struct.Struct("<4q2i24q5qi4x")
-_SWA_PREFILL = struct.Struct("<7q2i16q2f3q1q3q")
+_SWA_PREFILL = struct.Struct("<7q2i16q2f3q1q3qi4x")
 _SWA_BIASED_DECODE = struct.Struct("<4q2i7qf4xqf4xq")
 _packed = {}
 
@@ -699,8 +702,8 @@ def _call(fn_name, index, args, *more):
 
 
 def _on_stream(fn):
-    """With `stream` (a torch stream or a cudaStream_t) the whole call runs on it: the kernels, and also the zeros and
-    copies that prepare outputs and the memory that outputs and workspaces take."""
+    """With `stream` (a torch stream or a cudaStream_t) the whole call runs on it: the kernels, and the memory that
+    outputs and workspaces take."""
     first = fn.__code__.co_varnames[0]
 
     @functools.wraps(fn)
@@ -734,19 +737,20 @@ def la_conv_prefill(x, w, bias=None, state_in=None, lens=None, silu: bool = True
     index, xt, wt = x.get_device(), x.dtype, w.dtype
     B, N, C = x.shape
     W = w.shape[1]
+    fill = 0
     if y is None:
-        y = _new_rows((B, N, C), out_dtype or xt, x.device, zero=lens is not None)
+        y = _new_rows(x, (B, N, C), out_dtype or xt)
+        fill = _FILL_ROWS
     held = (B, W - 1, C)
     _check(index, ("x", x, (B, N, C), xt, False), ("w", w, (C, W), wt, True), ("bias", bias, (C,), wt, True),
            ("lens", lens, (B,), torch.int64, True), ("state_in", state_in, held, xt, True),
            ("state_out", state_out, held, xt, True), ("y", y, (B, N, C), y.dtype, False))
     if state_out is None:
-        state_out = torch.empty((B, max(W - 1, 0), C), dtype=xt, device=x.device)
-        if lens is not None:  # a sequence whose length is out of range is left as it was
-            state_out.copy_(state_in) if state_in is not None else state_out.zero_()
+        state_out = x.new_empty((B, max(W - 1, 0), C))
+        fill |= _FILL_STATE
     _call("la_conv_prefill", index,
           _CONV_PREFILL.pack(B, N, C, W, _code(xt), _code(y.dtype), _code(wt), *_rows(x), *_rows(y), w.data_ptr(),
-                             _address(bias), _address(state_in), state_out.data_ptr(), _address(lens), bool(silu)))
+                             _address(bias), _address(state_in), state_out.data_ptr(), _address(lens), bool(silu), fill))
     return y, state_out
 
 
@@ -763,7 +767,7 @@ def la_conv_decode_step(x, w, state, bias=None, silu: bool = True, out=None, sta
     W = w.shape[1]
     state_out = state if state_out is None else state_out
     if out is None:
-        out = _new_rows((S, C), out_dtype or xt, x.device)
+        out = _new_rows(x, (S, C), out_dtype or xt)
     held = (S, W - 1, C)
     _check(index, ("x", x, (S, C), xt, False), ("w", w, (C, W), wt, True), ("bias", bias, (C,), wt, True),
            ("state", state, held, xt, True), ("state_out", state_out, held, xt, True),
@@ -774,12 +778,12 @@ def la_conv_decode_step(x, w, state, bias=None, silu: bool = True, out=None, sta
     return out
 
 
-def _ssm_prefill_args(u, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus, h_in, lens, y, h_out):
+def _ssm_prefill_args(u, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus, h_in, lens, y, h_out, fill=0):
     B, N, C = u.shape
     return _SSM_PREFILL.pack(B, N, C, A.shape[1], Bm.shape[1], _code(u.dtype), _code(y.dtype), *_rows(u),
                              *_rows(delta), *_rows(z), *_rows(y), *_heads(Bm), *_heads(Cm), A.data_ptr(), _address(D),
                              _address(delta_bias), _address(h_in), _address(h_out), _address(lens),
-                             bool(delta_softplus))
+                             bool(delta_softplus), fill)
 
 
 def _ssm_workspace_size(args) -> int:
@@ -813,18 +817,19 @@ def la_ssm_prefill(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, delta_s
     index, ut, f32 = u.get_device(), u.dtype, torch.float32
     B, N, C = rows = tuple(u.shape)
     n, G = A.shape[1], Bm.shape[1]
+    fill = 0
     if y is None:
-        y = _new_rows(rows, out_dtype or ut, u.device, zero=lens is not None)
+        y = _new_rows(u, rows, out_dtype or ut)
+        fill = _FILL_ROWS
     _check(index, ("u", u, rows, ut, False), ("delta", delta, rows, ut, False), ("z", z, rows, ut, False),
            ("Bm", Bm, (B, G, N, n), ut, False), ("Cm", Cm, (B, G, N, n), ut, False), ("A", A, (C, n), f32, True),
            ("D", D, (C,), f32, True), ("delta_bias", delta_bias, (C,), f32, True), ("h_in", h_in, (B, C, n), f32, True),
            ("h_out", h_out, (B, C, n), f32, True), ("lens", lens, (B,), torch.int64, True),
            ("y", y, rows, y.dtype, False))
     if h_out is None:
-        h_out = torch.empty((B, C, n), dtype=f32, device=u.device)
-        if lens is not None:
-            h_out.copy_(h_in) if h_in is not None else h_out.zero_()
-    a = _ssm_prefill_args(u, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus, h_in, lens, y, h_out)
+        h_out = u.new_empty((B, C, n), dtype=f32)
+        fill |= _FILL_STATE
+    a = _ssm_prefill_args(u, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus, h_in, lens, y, h_out, fill)
     ws, ws_bytes = _workspace(_ssm_workspace_size(a), workspace, u.device)
     if workspace is not None and workspace.get_device() != index:
         raise ValueError("workspace must live on the device of the inputs")
@@ -845,7 +850,7 @@ def la_ssm_decode_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=No
     n, G = A.shape[1], Bm.shape[1]
     state_out = state if state_out is None else state_out
     if out is None:
-        out = torch.empty(rows, dtype=out_dtype or ut, device=u.device)
+        out = u.new_empty(rows, dtype=out_dtype or ut)
     _check(index, ("u", u, rows, ut, False), ("delta", delta, rows, ut, False), ("z", z, rows, ut, False),
            ("Bm", Bm, (S, G, n), ut, False), ("Cm", Cm, (S, G, n), ut, False), ("A", A, (C, n), f32, True),
            ("D", D, (C,), f32, True), ("delta_bias", delta_bias, (C,), f32, True), ("state", state, (S, C, n), f32, True),
@@ -881,8 +886,10 @@ def la_swa_prefill(q, k, v, window: int = 0, scale: float | None = None, softcap
     B, H, Nq, d = queries = tuple(q.shape)
     keys = tuple(k.shape)
     Hkv, Nk, window = keys[1], keys[2], int(window)
+    fill = 0
     if o is None:
-        o = (torch.zeros if lens is not None else torch.empty)(queries, dtype=out_dtype or qt, device=q.device)
+        o = q.new_empty(queries, dtype=out_dtype or qt)
+        fill = _FILL_ROWS
     _check(index, ("q", q, queries, qt, False), ("k", k, (B, Hkv, Nk, d), qt, False), ("v", v, (B, Hkv, Nk, d), qt, False),
            ("slopes", slopes, (H,), torch.float32, True), ("key_lo", key_lo, (B, Nq), i32, True),
            ("key_hi", key_hi, (B, Nq), i32, True), ("lens", lens, (B,), torch.int64, True),
@@ -892,7 +899,7 @@ def la_swa_prefill(q, k, v, window: int = 0, scale: float | None = None, softcap
           _SWA_PREFILL.pack(B, H, Hkv, Nq, Nk, d, window, _code(qt), _code(o.dtype), *_heads(q), *_heads(k), *_heads(v),
                             *_heads(o), scale if scale is not None else d ** -0.5, softcap, _address(slopes),
                             _address(key_lo), _address(key_hi), q_pos0 if q_pos0 is not None else Nk - Nq,
-                            _address(lens), _address(k_cache), _address(v_cache)))
+                            _address(lens), _address(k_cache), _address(v_cache), fill))
     return o
 
 
@@ -908,7 +915,7 @@ def la_swa_biased_decode_step(q, k, v, k_cache, v_cache, pos, softcap: float = 0
     S, H, d = heads = tuple(q.shape)
     Hkv, window = k.shape[1], k_cache.shape[2]
     if out is None:
-        out = torch.empty(heads, dtype=out_dtype or qt, device=q.device)
+        out = q.new_empty(heads, dtype=out_dtype or qt)
     ring = (S, Hkv, window, d)
     _check(index, ("q", q, heads, qt, True), ("k", k, (S, Hkv, d), qt, True), ("v", v, (S, Hkv, d), qt, True),
            ("k_cache", k_cache, ring, qt, True), ("v_cache", v_cache, ring, qt, True), ("pos", pos, (S,), torch.int64, True),

@@ -439,6 +439,19 @@ bool valid_rows(la_tensor x, int64_t B, int64_t N, int64_t C, la_dtype dt, bool 
   return valid_view(x, B, 1, N, C, dt) && !(output && !distinct(x, B, 1, N, C));
 }
 
+// Zeros and incoming states for what a call with lens leaves out, as its `fill` asks for.
+la_status fill_padding(int32_t fill, int64_t B, int64_t H, int64_t N, int64_t max_len, int64_t offset, const int64_t* lens, const la_tensor& y,
+                       int64_t row, la_dtype dt, const void* state_in, void* state_out, int64_t state_bytes, cudaStream_t stream) {
+  if (!lens || !(fill & (LA_FILL_ROWS | LA_FILL_STATE))) return LA_OK;
+  const int64_t e = elem_bytes(dt);
+  la::PaddingLaunch p{};
+  p.B = B; p.H = H; p.N = N; p.max_len = max_len; p.offset = offset; p.lens = lens;
+  p.rows = fill & LA_FILL_ROWS ? y.ptr : nullptr;
+  p.sb = y.stride_b * e; p.sh = y.stride_h * e; p.st = y.stride_t * e; p.row_bytes = row * e;
+  p.state_in = state_in; p.state_out = fill & LA_FILL_STATE ? state_out : nullptr; p.state_bytes = state_bytes;
+  return from_cuda(la::launch_fill_padding(p, stream));
+}
+
 // 0, or a cap whose ratios to the scale and to log2(e) are far from fp32's ends
 bool valid_cap(float softcap, float scale) {
   return softcap == 0.f || (softcap > 0.f && softcap <= 1e37f && std::fabs(scale / softcap) <= 1e37f);
@@ -471,7 +484,12 @@ la_status la_conv_prefill(const la_conv_prefill_args* a, void* stream) {
   L.y = a->y.ptr; L.y_sb = a->y.stride_b; L.y_st = a->y.stride_t;
   L.w = a->w; L.bias = a->bias; L.state_in = a->state_in; L.state_out = a->state_out;
   L.lens = a->lens; L.silu = a->silu; L.status = status;
-  return from_cuda(la::launch_conv_prefill(L, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  la_tensor y = a->y;
+  y.stride_h = 0;
+  const la_status st = fill_padding(a->fill, a->B, 1, a->N, a->N, 0, a->lens, y, a->C, a->out_dtype, a->state_in, a->state_out,
+                                    (a->W - 1) * a->C * elem_bytes(a->in_dtype), s);
+  return st != LA_OK ? st : from_cuda(la::launch_conv_prefill(L, s));
 }
 
 la_status la_conv_decode_step(const la_conv_decode_args* a, void* stream) {
@@ -537,7 +555,11 @@ la_status la_ssm_prefill(const la_ssm_prefill_args* a, void* ws, size_t ws_bytes
   L.Bm = view(a->Bm); L.Cm = view(a->Cm);
   L.A = a->A; L.D = a->D; L.delta_bias = a->delta_bias; L.h_in = a->h_in; L.h_out = a->h_out;
   L.lens = a->lens; L.softplus = a->delta_softplus; L.status = status;
-  return from_cuda(la::launch_ssm_prefill(L, ws, ws_bytes, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  la_tensor y = a->y;
+  y.stride_h = 0;
+  const la_status st = fill_padding(a->fill, B, 1, N, N, 0, a->lens, y, C, a->out_dtype, a->h_in, a->h_out, C * a->n * (int64_t)sizeof(float), s);
+  return st != LA_OK ? st : from_cuda(la::launch_ssm_prefill(L, ws, ws_bytes, s));
 }
 
 la_status la_ssm_decode_step(const la_ssm_decode_args* a, void* stream) {
@@ -602,6 +624,9 @@ la_status la_swa_prefill(const la_swa_prefill_args* a, void* stream) {
   L.lens = a->lens; L.k_cache = a->k_cache; L.v_cache = a->v_cache; L.status = status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a->Nq > 0) {
+    const la_status st = fill_padding(a->fill & LA_FILL_ROWS, a->B, a->H, a->Nq, a->Nk, a->q_pos0, a->lens, a->o, a->d, a->out_dtype, nullptr,
+                                      nullptr, 0, s);
+    if (st != LA_OK) return st;
     cudaError_t e = L.in_bf16 ? la::launch_swa_prefill_tc(L, s) : cudaErrorNotSupported;
     if (e == cudaErrorNotSupported) e = la::launch_swa_prefill_simt(L, s);
     if (e != cudaSuccess) return from_cuda(e);

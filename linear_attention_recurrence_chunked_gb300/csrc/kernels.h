@@ -143,6 +143,20 @@ cudaError_t launch_notebank_scores(const NotebankScoresLaunch& a, cudaStream_t s
 cudaError_t launch_notebank_address(const NotebankAddressLaunch& a, unsigned* status, cudaStream_t stream);
 cudaError_t launch_notebank_route(const NotebankRouteLaunch& a, cudaStream_t stream);
 
+// What a call with lens leaves out (padding.cu): rows [B, H, N] of row_bytes (strides in bytes, 16-byte aligned; null:
+// none) from lens[b] - offset on become zeros, and where lens[b] is outside [0, max_len] all of the sequence's rows
+// and its state_out (null: none) becomes state_in (null: zeros).
+struct PaddingLaunch {
+  int64_t B, H, N, max_len, offset;
+  const int64_t* lens;
+  void* rows;
+  int64_t sb, sh, st, row_bytes;
+  const void* state_in;
+  void* state_out;
+  int64_t state_bytes;  // of one sequence
+};
+cudaError_t launch_fill_padding(const PaddingLaunch& a, cudaStream_t stream);
+
 // Short causal convolution (conv.cu).  The step is the prompt form's data with one token per sequence.
 struct ConvLaunch {
   int64_t B, N, C;

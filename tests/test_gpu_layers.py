@@ -704,3 +704,34 @@ def test_swa_few_queries_share_their_keys(dtype, Nq, Nk, d, window, softcap, slo
     o = la.la_swa_prefill(*on(dev, q, k, v), softcap=softcap, slopes=sld, lens=dlens, key_lo=lo.to(dev), key_hi=hi.to(dev))
     ref.check(o, o_ref, bound)
     assert la.la_device_status() == la.LA_OK
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("C", [13, 64])
+def test_new_outputs_have_zeros_for_padding_and_the_incoming_state_of_skipped_sequences(dtype, C):
+    dev = cuda_device()
+    B, N, n = 4, 150, 5
+    lens = torch.tensor([0, 70, N + 1, N], device=dev)
+    t = ssm_inputs(B, N, C, n, 1, dtype, True, C)
+    u, delta, z = (pad_rows(t[k], dev) for k in ("u", "delta", "z"))
+    A, Bm, Cm, h0 = on(dev, *(t[k] for k in ("A", "Bm", "Cm", "h")))
+    w, s0 = randn(gen(1), C, 4, dtype=dtype).to(dev), randn(gen(2), B, 3, C, dtype=dtype).to(dev)
+    q, k, v = on(dev, *swa_case(B, 2, 1, N - 20, N, 16, dtype, 3))
+
+    def poison():  # what the next outputs are made of
+        for shape in ((B, N, 16), (B, N, 64), (B, 3, C), (B, C, n), (B, 2, N - 20, 16)):
+            for dt in (dtype, FP):
+                torch.full(shape, float("nan"), dtype=dt, device=dev)
+    for state in (False, True):
+        poison()
+        y, s = la.la_conv_prefill(u, w, state_in=s0 if state else None, lens=lens)
+        assert not y[0].any() and not y[1, 70:].any() and not y[2].any() and torch.isfinite(y.float()).all() and y[1, :70].any()
+        assert torch.equal(s[2], s0[2] if state else torch.zeros_like(s0[2])) and torch.equal(s[0], s[2] if not state else s0[0])
+        poison()
+        y, h = la.la_ssm_prefill(u, delta, A, Bm, Cm, z=z, h_in=h0 if state else None, lens=lens)
+        assert not y[0].any() and not y[1, 70:].any() and not y[2].any() and torch.isfinite(y.float()).all() and y[3, N - 1].any()
+        assert torch.equal(h[2], h0[2] if state else torch.zeros_like(h0[2])) and torch.isfinite(h).all()
+    poison()
+    o = la.la_swa_prefill(q, k, v, lens=lens)  # queries stand at 20..149
+    assert not o[0].any() and not o[1, :, 50:].any() and not o[2].any() and torch.isfinite(o.float()).all() and o[1, :, :50].any()
+    assert la.la_device_status() == la.LA_ERR_INVALID_ARGUMENT

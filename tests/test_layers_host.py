@@ -203,17 +203,17 @@ def test_packed_arguments_are_the_structures_bytes():
     T4 = lambda k: T(at(k), 1 + k, 2 + k, 3 + k)  # noqa: E731
     W4 = lambda k: (at(k), 1 + k, 2 + k, 3 + k)  # noqa: E731
     cases = [
-        (la._CONV_PREFILL, la.ConvPrefillArgs(1, 2, 3, 4, 1, 0, 1, T4(0), T4(1), at(2), at(3), at(4), at(5), at(6), 1),
-         (1, 2, 3, 4, 1, 0, 1, *W4(0), *W4(1), at(2), at(3), at(4), at(5), at(6), 1)),
+        (la._CONV_PREFILL, la.ConvPrefillArgs(1, 2, 3, 4, 1, 0, 1, T4(0), T4(1), at(2), at(3), at(4), at(5), at(6), 1, 3),
+         (1, 2, 3, 4, 1, 0, 1, *W4(0), *W4(1), at(2), at(3), at(4), at(5), at(6), 1, 3)),
         (la._CONV_DECODE, la.ConvDecodeArgs(1, 2, 3, 1, 0, 1, at(0), 5, at(1), 6, at(2), at(3), at(4), at(5), 1),
          (1, 2, 3, 1, 0, 1, at(0), 5, at(1), 6, at(2), at(3), at(4), at(5), 1)),
-        (la._SSM_PREFILL, la.SsmPrefillArgs(1, 2, 3, 4, 5, 1, 0, *(T4(k) for k in range(6)), *(at(k) for k in range(6, 12)), 1),
-         (1, 2, 3, 4, 5, 1, 0, *(w for k in range(6) for w in W4(k)), *(at(k) for k in range(6, 12)), 1)),
+        (la._SSM_PREFILL, la.SsmPrefillArgs(1, 2, 3, 4, 5, 1, 0, *(T4(k) for k in range(6)), *(at(k) for k in range(6, 12)), 1, 2),
+         (1, 2, 3, 4, 5, 1, 0, *(w for k in range(6) for w in W4(k)), *(at(k) for k in range(6, 12)), 1, 2)),
         (la._SSM_DECODE, la.SsmDecodeArgs(1, 2, 3, 4, 1, 0, *(T4(k) for k in range(6)), *(at(k) for k in range(6, 11)), 1),
          (1, 2, 3, 4, 1, 0, *(w for k in range(6) for w in W4(k)), *(at(k) for k in range(6, 11)), 1)),
         (la._SWA_PREFILL, la.SwaPrefillArgs(1, 2, 3, 4, 5, 6, 7, 1, 0, *(T4(k) for k in range(4)), 0.5, 2.5, at(4), at(5), at(6), 9, at(7),
-                                            at(8), at(9)),
-         (1, 2, 3, 4, 5, 6, 7, 1, 0, *(w for k in range(4) for w in W4(k)), 0.5, 2.5, at(4), at(5), at(6), 9, at(7), at(8), at(9))),
+                                            at(8), at(9), 1),
+         (1, 2, 3, 4, 5, 6, 7, 1, 0, *(w for k in range(4) for w in W4(k)), 0.5, 2.5, at(4), at(5), at(6), 9, at(7), at(8), at(9), 1)),
         (la._SWA_BIASED_DECODE, la.SwaBiasedDecodeArgs(la.SwaDecodeArgs(1, 2, 3, 4, 1, 0, *(at(k) for k in range(7)), 0.5), 8, 1.5, at(9)),
          (1, 2, 3, 4, 1, 0, *(at(k) for k in range(7)), 0.5, 8, 1.5, at(9))),
     ]
