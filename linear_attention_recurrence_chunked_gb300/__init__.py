@@ -664,8 +664,8 @@ def _address(t):
 def _new_rows(x, shape, dtype):
     """An output beside x whose rows start on 16-byte boundaries whatever the last size is."""
     if shape[-1] % 8 == 0:
-        return x.new_empty(shape, dtype=dtype)
-    return x.new_empty((*shape[:-1], -(-shape[-1] // 8) * 8), dtype=dtype)[..., :shape[-1]]
+        return torch.empty(shape, dtype=dtype, device=x.device)
+    return torch.empty((*shape[:-1], -(-shape[-1] // 8) * 8), dtype=dtype, device=x.device)[..., :shape[-1]]
 
 
 # what a call with lens writes into outputs that were made for it (include/la.h)
@@ -746,7 +746,7 @@ def la_conv_prefill(x, w, bias=None, state_in=None, lens=None, silu: bool = True
            ("lens", lens, (B,), torch.int64, True), ("state_in", state_in, held, xt, True),
            ("state_out", state_out, held, xt, True), ("y", y, (B, N, C), y.dtype, False))
     if state_out is None:
-        state_out = x.new_empty((B, max(W - 1, 0), C))
+        state_out = torch.empty((B, max(W - 1, 0), C), dtype=xt, device=x.device)
         fill |= _FILL_STATE
     _call("la_conv_prefill", index,
           _CONV_PREFILL.pack(B, N, C, W, _code(xt), _code(y.dtype), _code(wt), *_rows(x), *_rows(y), w.data_ptr(),
@@ -827,7 +827,7 @@ def la_ssm_prefill(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, delta_s
            ("h_out", h_out, (B, C, n), f32, True), ("lens", lens, (B,), torch.int64, True),
            ("y", y, rows, y.dtype, False))
     if h_out is None:
-        h_out = u.new_empty((B, C, n), dtype=f32)
+        h_out = torch.empty((B, C, n), dtype=f32, device=u.device)
         fill |= _FILL_STATE
     a = _ssm_prefill_args(u, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus, h_in, lens, y, h_out, fill)
     ws, ws_bytes = _workspace(_ssm_workspace_size(a), workspace, u.device)
@@ -850,7 +850,7 @@ def la_ssm_decode_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=No
     n, G = A.shape[1], Bm.shape[1]
     state_out = state if state_out is None else state_out
     if out is None:
-        out = u.new_empty(rows, dtype=out_dtype or ut)
+        out = torch.empty(rows, dtype=out_dtype or ut, device=u.device)
     _check(index, ("u", u, rows, ut, False), ("delta", delta, rows, ut, False), ("z", z, rows, ut, False),
            ("Bm", Bm, (S, G, n), ut, False), ("Cm", Cm, (S, G, n), ut, False), ("A", A, (C, n), f32, True),
            ("D", D, (C,), f32, True), ("delta_bias", delta_bias, (C,), f32, True), ("state", state, (S, C, n), f32, True),
@@ -888,7 +888,7 @@ def la_swa_prefill(q, k, v, window: int = 0, scale: float | None = None, softcap
     Hkv, Nk, window = keys[1], keys[2], int(window)
     fill = 0
     if o is None:
-        o = q.new_empty(queries, dtype=out_dtype or qt)
+        o = torch.empty(queries, dtype=out_dtype or qt, device=q.device)
         fill = _FILL_ROWS
     _check(index, ("q", q, queries, qt, False), ("k", k, (B, Hkv, Nk, d), qt, False), ("v", v, (B, Hkv, Nk, d), qt, False),
            ("slopes", slopes, (H,), torch.float32, True), ("key_lo", key_lo, (B, Nq), i32, True),
@@ -915,7 +915,7 @@ def la_swa_biased_decode_step(q, k, v, k_cache, v_cache, pos, softcap: float = 0
     S, H, d = heads = tuple(q.shape)
     Hkv, window = k.shape[1], k_cache.shape[2]
     if out is None:
-        out = q.new_empty(heads, dtype=out_dtype or qt)
+        out = torch.empty(heads, dtype=out_dtype or qt, device=q.device)
     ring = (S, Hkv, window, d)
     _check(index, ("q", q, heads, qt, True), ("k", k, (S, Hkv, d), qt, True), ("v", v, (S, Hkv, d), qt, True),
            ("k_cache", k_cache, ring, qt, True), ("v_cache", v_cache, ring, qt, True), ("pos", pos, (S,), torch.int64, True),
