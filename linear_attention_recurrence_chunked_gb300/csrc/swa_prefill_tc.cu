@@ -687,8 +687,8 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           unpack2(p2, p0, p1);
           return pack2_bf16(p0, p1);
         };
-        // The whole row in registers, for blocks that the whole warp sees (and that lie behind its rows where there is
-        // a bias; without cap and bias for any block).  A cap comes from the polynomial as the scores are used
+        // The whole row in registers: with a cap for blocks that the whole warp sees, with a bias for blocks of which
+        // its rows see what lies behind them, and with neither for any.  A cap comes from the polynomial as the scores are used
         // (straight; false, with nothing done, where products leave the part that it is good for or scores spread too
         // far for the bound below), or else from the difference, in place.  4 x 16 x 4096 at d = 128 takes 386 us without
         // a cap, 551 with the one and 816 with the other, against 1340 where a row is read in parts.
@@ -734,7 +734,8 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 off = add2(off, step);
               }
             }
-          } else if constexpr (!kPoly) {
+          }
+          if constexpr (!kPoly) {
             if (!__all_sync(kFullMask, va <= 0 && vb >= KB)) {
 #pragma unroll
               for (int c = 0; c < kAll; ++c) x[c] = c >= va && c < vb ? x[c] : -INFINITY;
@@ -847,7 +848,9 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         } else if constexpr (!CAP && !BIAS) {
           row_at_once(std::false_type{});
         } else {
-          const bool whole = __all_sync(kFullMask, va <= 0 && vb >= KB && (!BIAS || pos - k0 >= KB - 1));
+          // what a row sees lies behind it: |pos - key| is linear there
+          const bool behind = !BIAS || va >= vb || pos - k0 >= min(vb, KB) - 1;
+          const bool whole = __all_sync(kFullMask, behind && (!CAP || (va <= 0 && vb >= KB)));
           bool done = false;
           if constexpr (CAP) {
             done = whole && ((drawn && row_at_once(std::true_type{})) || (small_cap && row_at_once(std::false_type{})));
