@@ -735,3 +735,58 @@ def test_new_outputs_have_zeros_for_padding_and_the_incoming_state_of_skipped_se
     o = la.la_swa_prefill(q, k, v, lens=lens)  # queries stand at 20..149
     assert not o[0].any() and not o[1, :, 50:].any() and not o[2].any() and torch.isfinite(o.float()).all() and o[1, :, :50].any()
     assert la.la_device_status() == la.LA_ERR_INVALID_ARGUMENT
+
+
+def test_offsets_beyond_32_bits():
+    """Sequences, heads and states more than 2^31 elements apart give what they give side by side."""
+    dev = cuda_device()
+    far = (1 << 31) + (1 << 12)
+    N, C, n, H, d = 70, 64, 16, 2, 64
+    t = ssm_inputs(2, N, C, n, 1, BF, True, 8)
+    u, delta, z, A, Bm, Cm = on(dev, *(t[k] for k in ("u", "delta", "z", "A", "Bm", "Cm")))
+    w = randn(gen(1), C, 4, dtype=BF).to(dev)
+    q, k, v = on(dev, *swa_case(2, H, H, N, N, d, BF, 4))
+    room = torch.empty(far + (1 << 22), dtype=BF, device=dev)
+    at = 0
+
+    def apart(x, make=True):  # the same values, the sequences `far` elements apart
+        nonlocal at
+        y = room.as_strided(x.shape, (far, *x[0].contiguous().stride()), at)
+        at += -(-x[0].numel() // 64) * 64
+        if make:
+            y.copy_(x)
+        return y
+    assert all(torch.equal(a, b) for a, b in zip(la.la_conv_prefill(apart(u), w, y=apart(u, False)), la.la_conv_prefill(u, w)))
+    got = la.la_ssm_prefill(apart(u), apart(delta), A, apart(Bm), apart(Cm), z=apart(z), y=apart(u, False))
+    assert all(torch.equal(a, b) for a, b in zip(got, la.la_ssm_prefill(u, delta, A, Bm, Cm, z=z)))
+    for x in (BF, FP):
+        if x is FP:
+            q, k, v = (i.float() for i in (q, k, v))
+            room, at = torch.empty(far + (1 << 22), dtype=FP, device=dev), 0
+        assert torch.equal(la.la_swa_prefill(apart(q), apart(k), apart(v), window=40, o=apart(q, False)), la.la_swa_prefill(q, k, v, window=40))
+        # heads and tokens apart: one sequence, the far axis inside it
+        side = apart(k.transpose(0, 1)).transpose(0, 1)
+        assert torch.equal(la.la_swa_prefill(q, side, v, window=40), la.la_swa_prefill(q, k, v, window=40))
+    del room
+    # rings and states of so many sequences that the last one lies beyond 2^31 elements
+    S, ring = (1 << 31) // (256 * 128) + 3, (256, 128)
+    kc, vc = (torch.zeros((S, 1, *ring), dtype=BF, device=dev) for _ in range(2))
+    qs, ks, vs = (randn(gen(i), S, 1, 128, dtype=BF).to(dev) for i in (5, 6, 7))
+    kc[-1], vc[-1] = randn(gen(8), 1, *ring, dtype=BF).to(dev), randn(gen(9), 1, *ring, dtype=BF).to(dev)
+    last = [i[-1:].clone() for i in (qs, ks, vs, kc, vc)]
+    pos = torch.full((S,), 300, device=dev)
+    out = la.la_swa_biased_decode_step(qs, ks, vs, kc, vc, pos)
+    assert torch.equal(out[-1:], la.la_swa_biased_decode_step(*last, pos[:1]))
+    assert torch.equal(kc[-1:], last[3]) and torch.equal(vc[-1, 0, 300 % 256], vs[-1, 0])
+    del kc, vc
+    S, C, n = 8200, 4096, 64
+    h = torch.zeros((S, C, n), device=dev)
+    h[-1] = randn(gen(3), C, n).to(dev)
+    us, ds = (randn(gen(i), S, C, dtype=BF).to(dev) for i in (1, 2))
+    bc = randn(gen(4), S, 1, n, dtype=BF).to(dev)
+    A = -torch.rand((C, n), device=dev)
+    h_last = h[-1:].clone()
+    y = la.la_ssm_decode_step(us, ds, A, bc, bc, h)
+    y_last = la.la_ssm_decode_step(us[-1:], ds[-1:], A, bc[-1:], bc[-1:], h_last)
+    assert torch.equal(y[-1:], y_last) and torch.equal(h[-1:], h_last)
+    assert la.la_device_status() == la.LA_OK
