@@ -1,7 +1,7 @@
 // padding.cu -- what a prompt call with sequence lengths leaves out of outputs that were made for it: zeros into the
 // rows of padding, and the incoming state (or zeros) into the state of a sequence whose length is out of range.
 // One launch that touches those rows only, in place of a fill of the whole output and a copy of the whole state
-// in front of the call (5 x 1001 x 520 fp32 with a state: 2.5 us of the host's time against 18).
+// in front of the call (5 ragged sequences of up to 1001 x 520 fp32 with a state: 19 us a call against 27).
 #include "layers.cuh"
 
 namespace la {

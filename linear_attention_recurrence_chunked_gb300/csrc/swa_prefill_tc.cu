@@ -23,7 +23,8 @@
 // with a cap of 30 540-565 us, bound by the rows' instructions (a polynomial, an exponential and a rounding per
 // score).  8 x 16 x 4096 at d = 64 with a window of 64: 91 us with the rings, of which its bytes take 40; a block's
 // chain of product, softmax and product bounds it.  Documents of 700 tokens with prefixes, a window of 1024 and a bias
-// at d = 96 (2 x 8 x 4099): 74 us, 48 us without the bias, whose columns are computed twice in partial blocks.
+// at d = 96 (2 x 8 x 4099): 68 us, 48 us without the bias; where a prefix reaches ahead of its rows the bias takes the
+// distance column by column (a form of that in registers too made it 70 us).
 //
 // Where items leave SMs idle and see several blocks, the CTAs of a cluster share an item's blocks; each leaves its
 // rows' outputs, divided by their sums, and m + log2 l in its shared memory, where the cluster joins them.
