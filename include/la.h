@@ -555,9 +555,9 @@ la_status la_swa_prefill(const la_swa_prefill_args* args, void* stream);
  * Arguments as in la_swa_decode_args (base.q, base.out: [S, H, d]; base.k,
  * base.v: [S, H_kv, d]; base.k_cache, base.v_cache: [S, H_kv, window, d]);
  * slopes [H] fp32 or NULL, softcap 0 = no cap.  H % H_kv == 0, H / H_kv <= 16.
- * bf16 inputs: as over a prompt, the softmax weights are rounded to bf16 for
- * their product with v; fp32 inputs: fp32 throughout.  A negative position
- * skips that sequence and sets the device status word. */
+ * bf16 inputs: the softmax weights meet v in two bf16 parts, off by 2^-17 of a
+ * weight; fp32 inputs: fp32 throughout.  A negative position skips that
+ * sequence and sets the device status word. */
 typedef struct la_swa_biased_decode_args {
   la_swa_decode_args base;
   int64_t H_kv;

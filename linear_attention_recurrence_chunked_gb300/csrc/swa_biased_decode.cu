@@ -13,7 +13,7 @@
 // for tcgen05, so the products are mma.m16n8k16 with the heads as the 16 rows.  Keys go from memory to the
 // operand registers directly: a lane's 16 bytes are elements of one slot, and which elements of the sum they are
 // is the same for the queries.  Values come by asynchronous copies, all 32 rows of a warp at once, and are
-// transposed on the way from shared memory.  The weights are rounded to bf16 for their product, as over a prompt.
+// transposed on the way from shared memory.  The weights meet them in two bf16 parts.
 // fp32: CUDA cores, four query heads at a time.
 #include "layers.cuh"
 #include "swa_common.cuh"
@@ -128,12 +128,14 @@ swa_biased_decode_mma_kernel(const SwaBiasedDecodeLaunch a) {
     }
   }
   // ---- softmax of this warp's slots
+  const bool spare = group <= 8;  // rows 8 to 15 have no head
   const float inv_cap = 1.f / a.softcap;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
   for (int t = 0; t < 4; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+      if (e >= 2 && spare) continue;
       const int slot = first + t * 8 + q4 * 2 + (e & 1), h = hr + (e >> 1) * 8;
       float y = x[t][e] * c.scale;
       if (a.softcap != 0.f) y = capped(y, a.softcap, inv_cap);
@@ -144,6 +146,7 @@ swa_biased_decode_mma_kernel(const SwaBiasedDecodeLaunch a) {
     }
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
+    if (r == 1 && spare) continue;
     m[r] = fmaxf(m[r], __shfl_xor_sync(kFullMask, m[r], 1));
     m[r] = fmaxf(m[r], __shfl_xor_sync(kFullMask, m[r], 2));
     const float base = m[r] == -INFINITY ? 0.f : m[r];
@@ -169,17 +172,45 @@ swa_biased_decode_mma_kernel(const SwaBiasedDecodeLaunch a) {
     for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
   tc::cp_async_wait_all();
   __syncwarp();
+  // Weights in two bf16 parts, the second one what the first leaves: a weight is off by 2^-17 of itself, where one part
+  // would leave 2^-9, more than an fp32 output can hide.  Up to eight heads the second parts take the rows that have no
+  // head, and
+  // no product is added; beyond, they are products of their own (256 x 64 heads over 4: 42.8 us, 41.3 with one part).
 #pragma unroll
   for (int kt = 0; kt < 2; ++kt) {
-    const uint32_t a0 = tc::pack2_bf16(x[2 * kt][0], x[2 * kt][1]), a1 = tc::pack2_bf16(x[2 * kt][2], x[2 * kt][3]);
-    const uint32_t a2 = tc::pack2_bf16(x[2 * kt + 1][0], x[2 * kt + 1][1]), a3 = tc::pack2_bf16(x[2 * kt + 1][2], x[2 * kt + 1][3]);
     const int r = kt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+    uint32_t w[4], rest[4];  // rows lane / 4 and that + 8 of the first eight slots, then of the others
+    auto split = [&](int i) {
+      const float w0 = x[2 * kt + i / 2][i % 2 * 2], w1 = x[2 * kt + i / 2][i % 2 * 2 + 1];
+      w[i] = tc::pack2_bf16(w0, w1);
+      rest[i] = tc::pack2_bf16(w0 - __uint_as_float(w[i] << 16), w1 - __uint_as_float(w[i] & 0xffff0000u));
+    };
+    split(0);
+    split(2);
+    if (spare) {
+      w[1] = rest[0];
+      w[3] = rest[2];
+    } else {
+      split(1);
+      split(3);
+    }
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
       uint32_t b[4];
       ldmatrix_trans(b, rbase + at(r, 2 * p + (lane >> 4)));
-      mma16816(o[2 * p], a0, a1, a2, a3, b[0], b[1]);
-      mma16816(o[2 * p + 1], a0, a1, a2, a3, b[2], b[3]);
+      mma16816(o[2 * p], w[0], w[1], w[2], w[3], b[0], b[1]);
+      mma16816(o[2 * p + 1], w[0], w[1], w[2], w[3], b[2], b[3]);
+      if (!spare) {
+        mma16816(o[2 * p], rest[0], rest[1], rest[2], rest[3], b[0], b[1]);
+        mma16816(o[2 * p + 1], rest[0], rest[1], rest[2], rest[3], b[2], b[3]);
+      }
+    }
+  }
+  if (spare) {
+#pragma unroll
+    for (int t = 0; t < 2 * kPairs; ++t) {
+      o[t][0] += o[t][2];
+      o[t][1] += o[t][3];
     }
   }
   // the new token into its slot, by the warp that used it from the arguments

@@ -1,0 +1,50 @@
+"""The layers' calls at the ends of what their documentation allows: ranges of scores, far keys, shared keys, growing
+states, counts and streams, against fp64 definitions."""
+import numpy as np
+import pytest
+import torch
+
+import linear_attention_recurrence_chunked_gb300 as la
+from tests import layers_oracle as ref
+from tests.helpers import cuda_device
+from tests.test_gpu_layers import gen, on, randn, slopes_of
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("H,Hkv,d,window,softcap,slopes", [
+    (4, 4, 64, 64, 0.0, False), (16, 4, 128, 256, 30.0, True), (16, 1, 72, 100, 0.0, True), (3, 3, 8, 33, 5.0, False)])
+def test_swa_step_weights_hold_more_than_bf16(H, Hkv, d, window, softcap, slopes):
+    """bf16 rings, fp32 outputs: the weights meet their values in two bf16 parts, off by 2^-17 of a weight."""
+    dev = cuda_device()
+    S = 5
+    g = gen(H + d)
+    q, k, v = randn(g, S, H, d, dtype=BF, scale=1.5), randn(g, S, Hkv, d, dtype=BF, scale=1.5), randn(g, S, Hkv, d, dtype=BF)
+    kc, vc = randn(g, S, Hkv, window, d, dtype=BF, scale=1.5), randn(g, S, Hkv, window, d, dtype=BF)
+    sl = slopes_of(H) if slopes else None
+    pos = torch.tensor([0, 7, window - 1, window, 1000 * window + 5])
+    out = la.la_swa_biased_decode_step(*on(dev, q, k, v, kc, vc, pos), softcap=softcap, slopes=None if sl is None else sl.to(dev), out_dtype=FP)
+    for s in range(S):
+        p = int(pos[s])
+        n = min(p + 1, window)
+        order = [(p - i) % window for i in range(n - 1, 0, -1)]  # oldest first, the new token behind them
+        keys = torch.cat([kc[s][:, order], k[s][:, None]], 1)[None].float()
+        values = torch.cat([vc[s][:, order], v[s][:, None]], 1)[None].float()
+        # fp32 copies: the definition's bound then has no term for weights in bf16
+        want, bound = ref.swa(q[s][None, :, None].float(), keys, values, d ** -0.5, softcap, sl, [[(0, n)]], n - 1, FP)
+        ref.check(out[s][None, :, None], want, bound + 2 ** -17 * values.abs().max().item())
+
+
+def test_swa_biased_step_and_plain_step_agree_beyond_bf16():
+    dev = cuda_device()
+    S, H, d, w = 7, 4, 64, 64
+    g = gen(1)
+    q, k, v = (randn(g, S, H, d, dtype=BF).to(dev) for _ in range(3))
+    kc, vc = (randn(g, S, H, w, d, dtype=BF).to(dev) for _ in range(2))
+    pos = torch.tensor([0, 1, 63, 64, 65, 1000, 1 << 40], dtype=torch.int64, device=dev)
+    a = la.la_swa_decode_step(q, k, v, kc.clone(), vc.clone(), pos, out_dtype=FP)
+    b = la.la_swa_biased_decode_step(q, k, v, kc.clone(), vc.clone(), pos, out_dtype=FP)
+    # two-part weights: 2^-17 of the weighted mean of |v|; beside that both sum up to 64 fp32 terms in their own order
+    largest = max(vc.float().abs().max(), v.float().abs().max())
+    assert (a - b).abs().max() < (2 ** -17 + 64 * 2 ** -23) * largest
