@@ -55,6 +55,12 @@ constexpr int kRows = 128;                    // queries per tile
 constexpr int kThreads = 384;                 // three warpgroups: rows of tile 0, of tile 1, and the rest
 constexpr float kGrowth = 8.f;                // log2 of how far P may exceed 1 before the output is scaled
 constexpr int kSMs = 152;
+// Capped scores may take a bound on their size, up to this in log2 units, for their maximum.  A row's running maximum is
+// never lowered, and its true one lies 2 kBound below it at most; the exponential drops what lies 126 below the running
+// one.  What is lost then lies 46 or more below the row's largest score: 2^24 such keys add 2^-22 to its sum.  (With a
+// limit of 60 a key six binades below the largest was lost.)  The polynomial's part ends at half the cap, 0.72 cap in
+// these units: caps up to 55 never meet the limit.
+constexpr float kBound = 40.f;
 // Windows up to this are narrow: blocks of 64 keys, two CTAs an SM.  8 x 16 x 4096 at d = 64: 88 us against 118
 // with blocks of 128 for a window of 64, 124 against 132 for 256, 168 against 170 for 512.
 constexpr int64_t kNarrow = 512;
@@ -707,10 +713,9 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 #pragma unroll
             for (int c = 0; c < kAll; ++c) hi[c & 3] = fmaxf(hi[c & 3], fabsf(x[c]));
             const float h = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
-            if (!__all_sync(kFullMask, h * zc <= kStraight && h * c1 <= 60.f)) return false;
+            if (!__all_sync(kFullMask, h * zc <= kStraight && h * c1 <= kBound)) return false;
             s_read();
-            // No score exceeds cap tanh(zc h), and none is below its negative: the bound serves as the maximum.  The
-            // weights stay above 2^-120, normal numbers also in bf16.
+            // No score exceeds cap tanh(zc h): the bound serves as the maximum.
             if constexpr (!BIAS) {
               const float base = update(h * straight_tanh(h));
               c2 = pack2(-base, -base);

@@ -48,3 +48,21 @@ def test_swa_biased_step_and_plain_step_agree_beyond_bf16():
     # two-part weights: 2^-17 of the weighted mean of |v|; beside that both sum up to 64 fp32 terms in their own order
     largest = max(vc.float().abs().max(), v.float().abs().max())
     assert (a - b).abs().max() < (2 ** -17 + 64 * 2 ** -23) * largest
+
+
+@pytest.mark.parametrize("d,first,later", [(64, 41, 46.5), (128, 41, 46.5), (64, 27.5, 35), (128, 27.5, 35), (64, 20, 36)])
+def test_swa_capped_scores_far_below_zero(d, first, later):
+    """Scores that are all far below zero, under a cap far above them: a block's bound on its maximum lies as far above
+    zero, and what later blocks hold must still count beside it."""
+    dev = cuda_device()
+    H, N = 4, 8192
+    q = torch.ones((1, H, N, d), dtype=BF)
+    per = torch.full((N,), -later / d)
+    per[:128] = -first / d  # exact in bf16
+    k = per.to(BF)[None, None, :, None].expand(1, 1, N, d).contiguous()
+    v = randn(gen(d), 1, 1, N, d, dtype=BF) + 1
+    v[:, :, :128] -= 2
+    o = la.la_swa_prefill(*on(dev, q, k, v), scale=1.0, softcap=1000.0)
+    rows = [[(0, i + 1) if i in (5, 127, 128, 500, 4000, N - 1) else None for i in range(N)]]
+    o_ref, bound = ref.swa(q, k, v, 1.0, 1000.0, None, rows, 0, BF)
+    ref.check(o, o_ref, bound)
