@@ -518,30 +518,9 @@ cudaError_t launch_typed(const GdnPrefillLaunch& a, void* ws, unsigned* status, 
 
 }  // namespace
 
-namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
-}  // namespace
-
 // bf16 [B, H, N, 128] view -> 4-D tensor map with a (64 features x 64 tokens) box, 128-byte swizzle.
 bool gdn_make_map(CUtensorMap* m, const View4& x, int64_t B, int64_t H, int64_t N) {
-  EncodeTiledFn fn = encode_fn();
+  const tc::EncodeTiledFn fn = tc::encode_tiled();
   if (!fn) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)N, (cuuint64_t)H, (cuuint64_t)B};
   const cuuint64_t strides[3] = {(cuuint64_t)(x.st * 2), (cuuint64_t)(x.sh * 2), (cuuint64_t)(x.sb * 2)};

@@ -40,7 +40,6 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 
 #include "layers.cuh"
@@ -958,26 +957,9 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   if (warp == 8) tmem_dealloc(tmem, S::kTmemCols);
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
 // [B, H, N, d] bf16 view as boxes of `rows` x 64 columns, columns and rows behind the ends filled with zeros
 bool encode(CUtensorMap* map, const View4& x, int64_t B, int64_t H, int64_t N, int d, int rows) {
-  EncodeTiledFn fn = encode_fn();
+  const tc::EncodeTiledFn fn = tc::encode_tiled();
   if (!fn) return false;
   // (an axis repeated with stride 0 is not for a map either)
   if ((N > 1 && x.st == 0) || (H > 1 && x.sh == 0) || (B > 1 && x.sb == 0)) return false;

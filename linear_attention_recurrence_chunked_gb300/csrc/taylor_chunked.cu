@@ -784,26 +784,9 @@ taylor_chunked_kernel(const __grid_constant__ CUtensorMap tmap_v, const TaylorPr
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
 template <typename TOut, bool DECAY>
 cudaError_t launch_typed(const TaylorPrefillLaunch& a, unsigned* status, cudaStream_t stream) {
-  EncodeTiledFn fn = encode_fn();
+  const tc::EncodeTiledFn fn = tc::encode_tiled();
   if (!fn) return cudaErrorInvalidValue;
   CUtensorMap mv;
   const cuuint64_t dims[4] = {(cuuint64_t)kDv, (cuuint64_t)a.N, (cuuint64_t)a.H, (cuuint64_t)a.B};
