@@ -532,6 +532,7 @@ la_status la_ssm_decode_step(const la_ssm_decode_args* args, void* stream);
  *            stored for la_swa_decode_step / la_swa_biased_decode_step (token
  *            p in slot p % window; other slots are left as they were).
  *   softcap : 0, or up to 1e37 with |scale| / softcap up to 1e37
+ *   bf16 q, k, v: strides below 2^40 bytes (LA_ERR_UNSUPPORTED)
  * bf16 inputs: products on the tensor cores with fp32 sums and statistics,
  * the softmax weights rounded to bf16 for their product with v.  fp32 inputs:
  * fp32 throughout. */

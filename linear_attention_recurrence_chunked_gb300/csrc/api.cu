@@ -457,6 +457,11 @@ bool valid_cap(float softcap, float scale) {
   return softcap == 0.f || (softcap > 0.f && softcap <= 1e37f && std::fabs(scale / softcap) <= 1e37f);
 }
 bool valid_elem(const void* p, la_dtype dt) { return p && (reinterpret_cast<uintptr_t>(p) % elem_bytes(dt)) == 0; }
+// strides of a bf16 view that a tensor map can hold: below 2^40 bytes
+bool mappable(const la_tensor& x, int64_t B, int64_t H, int64_t N) {
+  constexpr int64_t kEnd = int64_t(1) << 39;
+  return (B <= 1 || x.stride_b < kEnd) && (H <= 1 || x.stride_h < kEnd) && (N <= 1 || x.stride_t < kEnd);
+}
 bool valid_strides(const la_tensor& x) { return x.stride_b >= 0 && x.stride_h >= 0 && x.stride_t >= 0; }
 
 }  // namespace
@@ -609,6 +614,8 @@ la_status la_swa_prefill(const la_swa_prefill_args* a, void* stream) {
       !valid_view(a->v, a->B, a->H_kv, a->Nk, a->d, a->in_dtype) || !valid_view(a->o, a->B, a->H, a->Nq, a->d, a->out_dtype))
     return LA_ERR_INVALID_ARGUMENT;
   if (!distinct(a->o, a->B, a->H, a->Nq, a->d)) return LA_ERR_INVALID_ARGUMENT;
+  if (a->in_dtype == LA_DTYPE_BF16 && !(mappable(a->q, a->B, a->H, a->Nq) && mappable(a->k, a->B, a->H_kv, a->Nk) && mappable(a->v, a->B, a->H_kv, a->Nk)))
+    return LA_ERR_UNSUPPORTED;
   if (!aligned4(a->slopes) || !aligned4(a->key_lo) || !aligned4(a->key_hi) || !aligned8(a->lens) || !aligned16(a->k_cache) ||
       !aligned16(a->v_cache))
     return LA_ERR_INVALID_ARGUMENT;
@@ -627,8 +634,7 @@ la_status la_swa_prefill(const la_swa_prefill_args* a, void* stream) {
     const la_status st = fill_padding(a->fill & LA_FILL_ROWS, a->B, a->H, a->Nq, a->Nk, a->q_pos0, a->lens, a->o, a->d, a->out_dtype, nullptr,
                                       nullptr, 0, s);
     if (st != LA_OK) return st;
-    cudaError_t e = L.in_bf16 ? la::launch_swa_prefill_tc(L, s) : cudaErrorNotSupported;
-    if (e == cudaErrorNotSupported) e = la::launch_swa_prefill_simt(L, s);
+    const cudaError_t e = L.in_bf16 ? la::launch_swa_prefill_tc(L, s) : la::launch_swa_prefill_simt(L, s);
     if (e != cudaSuccess) return from_cuda(e);
   }
   return a->k_cache ? from_cuda(la::launch_swa_fill_rings(L, s)) : LA_OK;

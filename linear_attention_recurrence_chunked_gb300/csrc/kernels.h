@@ -211,9 +211,8 @@ struct SwaPrefillLaunch {
   void *k_cache, *v_cache;
   unsigned* status;
 };
-// bf16 inputs; cudaErrorNotSupported (nothing launched) where TMA cannot describe the strides
-cudaError_t launch_swa_prefill_tc(const SwaPrefillLaunch& a, cudaStream_t stream);
-cudaError_t launch_swa_prefill_simt(const SwaPrefillLaunch& a, cudaStream_t stream);
+cudaError_t launch_swa_prefill_tc(const SwaPrefillLaunch& a, cudaStream_t stream);    // bf16 inputs, strides below 2^40 bytes
+cudaError_t launch_swa_prefill_simt(const SwaPrefillLaunch& a, cudaStream_t stream);  // fp32 inputs
 cudaError_t launch_swa_fill_rings(const SwaPrefillLaunch& a, cudaStream_t stream);
 
 struct SwaBiasedDecodeLaunch {

@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kBM = 64, kBN = 64, kThreads = 256, kSMs = 152;
 
-template <typename TIn, typename TOut, int DP>
+template <typename TOut, int DP>
 __global__ void __launch_bounds__(kThreads)
 swa_simt_kernel(const SwaPrefillLaunch a, int q_tiles, int parts) {
   constexpr int LD = DP + 4;       // row pitch of Q, K, V in floats: rows start 4 banks apart
@@ -60,9 +60,9 @@ swa_simt_kernel(const SwaPrefillLaunch a, int q_tiles, int parts) {
       atomicMax(&s_range[1], sp.hi);
     }
   }
-  const TIn* q = reinterpret_cast<const TIn*>(a.q.ptr) + b * a.q.sb + h * a.q.sh;
-  const TIn* k = reinterpret_cast<const TIn*>(a.k.ptr) + b * a.k.sb + hk * a.k.sh;
-  const TIn* v = reinterpret_cast<const TIn*>(a.v.ptr) + b * a.v.sb + hk * a.v.sh;
+  const float* q = reinterpret_cast<const float*>(a.q.ptr) + b * a.q.sb + h * a.q.sh;
+  const float* k = reinterpret_cast<const float*>(a.k.ptr) + b * a.k.sb + hk * a.k.sh;
+  const float* v = reinterpret_cast<const float*>(a.v.ptr) + b * a.v.sb + hk * a.v.sh;
   for (int e = tid; e < kBM * (DP / 4); e += kThreads) {
     const int r = e / (DP / 4), c = e % (DP / 4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -252,11 +252,11 @@ swa_fill_rings_kernel(const SwaPrefillLaunch a) {
   }
 }
 
-template <typename TIn, typename TOut, int DP>
+template <typename TOut, int DP>
 cudaError_t launch_simt(const SwaPrefillLaunch& a, cudaStream_t stream) {
   constexpr int kSmem = (3 * 64 * (DP + 4) + kBM * (kBN + 4)) * (int)sizeof(float);
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(swa_simt_kernel<TIn, TOut, DP>, kSmem, done);
+  const cudaError_t e = allow_smem(swa_simt_kernel<TOut, DP>, kSmem, done);
   if (e != cudaSuccess) return e;
   const int q_tiles = (int)((a.Nq + kBM - 1) / kBM);
   const int64_t tiles = a.B * a.H * q_tiles;
@@ -275,23 +275,20 @@ cudaError_t launch_simt(const SwaPrefillLaunch& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &cluster;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, swa_simt_kernel<TIn, TOut, DP>, a, q_tiles, parts);
+  return cudaLaunchKernelEx(&cfg, swa_simt_kernel<TOut, DP>, a, q_tiles, parts);
 }
 
-template <typename TIn, typename TOut>
+template <typename TOut>
 cudaError_t launch_width(const SwaPrefillLaunch& a, cudaStream_t stream) {
-  if (a.d <= 32) return launch_simt<TIn, TOut, 32>(a, stream);
-  if (a.d <= 64) return launch_simt<TIn, TOut, 64>(a, stream);
-  return launch_simt<TIn, TOut, 128>(a, stream);
+  if (a.d <= 32) return launch_simt<TOut, 32>(a, stream);
+  if (a.d <= 64) return launch_simt<TOut, 64>(a, stream);
+  return launch_simt<TOut, 128>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_swa_prefill_simt(const SwaPrefillLaunch& a, cudaStream_t stream) {
-  if (a.in_bf16 && a.out_bf16) return launch_width<__nv_bfloat16, __nv_bfloat16>(a, stream);
-  if (a.in_bf16) return launch_width<__nv_bfloat16, float>(a, stream);
-  if (a.out_bf16) return launch_width<float, __nv_bfloat16>(a, stream);
-  return launch_width<float, float>(a, stream);
+  return a.out_bf16 ? launch_width<__nv_bfloat16>(a, stream) : launch_width<float>(a, stream);
 }
 
 cudaError_t launch_swa_fill_rings(const SwaPrefillLaunch& a, cudaStream_t stream) {

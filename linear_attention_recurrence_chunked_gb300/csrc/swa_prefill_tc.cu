@@ -446,6 +446,8 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         const Blocks<KB> bl(a, it, parts);
         if (bl.j0 >= bl.j1) continue;
         if (lane == 0) {
+          // an axis repeated with stride 0 has one entry in its map
+          const int q_b = a.q.sb ? it.b : 0, q_h = a.q.sh ? it.h : 0;
           if (n > 0) wait(&bar_qfree, n - 1);
           if (!dead) {
             mbar_arrive_expect_tx(smem_u32(&bar_q), 2 * S::kQTile);
@@ -453,23 +455,23 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             for (int t = 0; t < 2; ++t)
 #pragma unroll 1
               for (uint32_t c = 0; c < S::kBlk; ++c)
-                tma_load_4d(sbase + t * S::kQTile + c * (kRows * 128), &map_q, c * 64, it.i0 + t * kRows, it.h, it.b, smem_u32(&bar_q));
+                tma_load_4d(sbase + t * S::kQTile + c * (kRows * 128), &map_q, c * 64, it.i0 + t * kRows, q_h, q_b, smem_u32(&bar_q));
             ++n;
           }
-          auto load = [&](const CUtensorMap* map, int j) {
+          auto load = [&](const CUtensorMap* map, const View4& x, int j) {
             const uint32_t s = slot(i);
             if (i >= kSlots) wait(&bar_free[s], phase(i - kSlots));
             if (dead) return;
             mbar_arrive_expect_tx(smem_u32(&bar_full[s]), S::kKTile);
 #pragma unroll 1
             for (uint32_t c = 0; c < S::kBlk; ++c)
-              tma_load_4d(sbase + S::kOffR + s * S::kKTile + c * (KB * 128), map, c * 64, j * KB, it.h / group, it.b, smem_u32(&bar_full[s]));
+              tma_load_4d(sbase + S::kOffR + s * S::kKTile + c * (KB * 128), map, c * 64, j * KB, x.sh ? it.h / group : 0, x.sb ? it.b : 0, smem_u32(&bar_full[s]));
             ++i;
           };
           // keys a block ahead of values
           for (int jk = bl.j0, jv = bl.j0; jv < bl.j1;) {
             const bool keys = jk < bl.j1 && jk <= bl.next(jv);
-            load(keys ? &map_k : &map_v, keys ? jk : jv);
+            load(keys ? &map_k : &map_v, keys ? a.k : a.v, keys ? jk : jv);
             if (keys) jk = bl.next(jk);
             else jv = bl.next(jv);
           }
@@ -957,12 +959,13 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   if (warp == 8) tmem_dealloc(tmem, S::kTmemCols);
 }
 
-// [B, H, N, d] bf16 view as boxes of `rows` x 64 columns, columns and rows behind the ends filled with zeros
+// [B, H, N, d] bf16 view as boxes of `rows` x 64 columns, columns and rows behind the ends filled with zeros.  Sequences
+// or heads repeated with stride 0 are an axis with one entry.
 bool encode(CUtensorMap* map, const View4& x, int64_t B, int64_t H, int64_t N, int d, int rows) {
   const tc::EncodeTiledFn fn = tc::encode_tiled();
   if (!fn) return false;
-  // (an axis repeated with stride 0 is not for a map either)
-  if ((N > 1 && x.st == 0) || (H > 1 && x.sh == 0) || (B > 1 && x.sb == 0)) return false;
+  if (x.sh == 0) H = 1;
+  if (x.sb == 0) B = 1;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)N, (cuuint64_t)H, (cuuint64_t)B};
   // the stride of an axis with one entry is never used, but has to be one that a map can hold
   const cuuint64_t row = (cuuint64_t)d * 2;
@@ -1043,7 +1046,7 @@ cudaError_t launch_width(const SwaPrefillLaunch& a, cudaStream_t stream) {
   CUtensorMap q, k, v;
   if (!encode(&q, a.q, a.B, a.H, a.Nq, a.d, kRows) || !encode(&k, a.k, a.B, a.Hkv, a.Nk, a.d, KB) ||
       !encode(&v, a.v, a.B, a.Hkv, a.Nk, a.d, KB))
-    return cudaErrorNotSupported;  // strides that TMA cannot describe
+    return cudaErrorInvalidValue;
   // without a bias the maximum is taken of the raw products, which the scale must not turn round
   const bool cap = a.softcap != 0.f, bias = a.slopes != nullptr || !(a.scale > 0.f);
   if (cap && bias) return launch_parts<DP, KB, true, true>(a, q, k, v, stream);

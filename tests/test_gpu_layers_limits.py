@@ -7,7 +7,7 @@ import torch
 import linear_attention_recurrence_chunked_gb300 as la
 from tests import layers_oracle as ref
 from tests.helpers import cuda_device
-from tests.test_gpu_layers import gen, on, randn, slopes_of
+from tests.test_gpu_layers import gen, on, randn, slopes_of, swa_case
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float32
@@ -66,3 +66,18 @@ def test_swa_capped_scores_far_below_zero(d, first, later):
     rows = [[(0, i + 1) if i in (5, 127, 128, 500, 4000, N - 1) else None for i in range(N)]]
     o_ref, bound = ref.swa(q, k, v, 1.0, 1000.0, None, rows, 0, BF)
     ref.check(o, o_ref, bound)
+
+
+@pytest.mark.parametrize("B,H,Hkv,Nq,N,d,window,softcap", [
+    (3, 4, 2, 200, 200, 64, 70, 0.0), (2, 8, 4, 300, 300, 128, 0, 20.0), (4, 40, 4, 260, 260, 72, 0, 0.0), (2, 4, 2, 10, 1500, 64, 0, 0.0)])
+def test_swa_repeated_axes_give_what_copies_give(B, H, Hkv, Nq, N, d, window, softcap):
+    """Keys, values and queries expanded over sequences or heads (stride 0): the same kernel, to the bit."""
+    dev = cuda_device()
+    q, k, v = (t.to(dev) for t in swa_case(B, H, Hkv, Nq, N, d, BF, N + d))
+    kw = dict(window=window, softcap=softcap)
+    for ks, vs in ((k[:1].expand(B, -1, -1, -1), v[:1].expand(B, -1, -1, -1)), (k[:, :1].expand(-1, Hkv, -1, -1), v),
+                   (k[:1, :1].expand(B, Hkv, -1, -1), v[:, :1].expand(-1, Hkv, -1, -1))):
+        assert torch.equal(la.la_swa_prefill(q, ks, vs, **kw), la.la_swa_prefill(q, ks.contiguous(), vs.contiguous(), **kw))
+    qs = q[:1, :1].expand(B, H, -1, -1)
+    assert torch.equal(la.la_swa_prefill(qs, k, v, **kw), la.la_swa_prefill(qs.contiguous(), k, v, **kw))
+    assert la.la_device_status() == la.LA_OK

@@ -176,6 +176,15 @@ def test_swa_step_refuses_extreme_caps(lib):
     assert lib.la_swa_biased_decode_step(ctypes.byref(swa_step_args(softcap=1e38)), None) == INV
 
 
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+def test_swa_prefill_refuses_bf16_strides_that_no_tensor_map_holds(lib, name):
+    far = T(at(1), 1 << 39, 1280, 64)
+    assert lib.la_swa_prefill(ctypes.byref(swa_args(**{name: far})), None) == UNS
+    # fp32 inputs take any stride: their misaligned slopes are the next thing to refuse
+    fp32 = dict(in_dtype=la.LA_DTYPE_F32, slopes=at(4) + 1)
+    assert lib.la_swa_prefill(ctypes.byref(swa_args(**{name: far}, **fp32)), None) == INV
+
+
 def test_null_arguments(lib):
     for fn in (lib.la_conv_prefill, lib.la_conv_decode_step, lib.la_ssm_decode_step, lib.la_swa_prefill, lib.la_swa_biased_decode_step):
         assert fn(None, None) == INV
