@@ -35,8 +35,9 @@
 // is not seen as a whole holds other values that are not finite, the item's rows are computed again, key by
 // key, on the CUDA cores (a rare path: only the keys in a row's interval are touched there).
 //
-// Every wait is bounded.  One that expires sets the status word and a flag in shared memory, after which no
-// wait of the CTA lasts, no copy or product is issued and nothing is stored; the loops still run to their end.
+// Every wait is bounded.  One that expires sets the status word and a flag in shared memory, after which no wait of the
+// CTA lasts, no copy is issued and no row is stored, nor by the other CTAs of its cluster.  The loops still run to their
+// end, with products of whatever shared memory holds, which only such rows would see.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -110,7 +111,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 __device__ __forceinline__ void mbar_spin(uint64_t* bar, uint32_t parity, volatile uint32_t* dead, unsigned* status) {
   uint64_t t0 = 0;
   for (uint32_t n = 1; !mbar_try_wait(smem_u32(bar), parity & 1u); ++n) {
-    if (n % 64 == 0) {
+    if (n % 8 == 0) {  // a try that fails takes 1.4 us
       if (*dead) return;
       const uint64_t t = globaltimer_ns();
       if (t0 == 0) t0 = t;
@@ -320,14 +321,16 @@ __device__ __forceinline__ void cluster_sync() {
 // The item's rows out of the cluster's parts; every CTA takes rows of its own, a warp a row.
 template <int DP, int KB, bool CAP, bool BIAS>
 __device__ __noinline__ void join_parts(const SwaPrefillLaunch& a, const Item& it, uint8_t* sm, float* lse, uint32_t* redo, int parts,
-                                        volatile uint32_t* dead) {
+                                        uint32_t* dead) {
   namespace cg = cooperative_groups;
   const cg::cluster_group cluster = cg::this_cluster();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t again[2] = {0, 0};
-  for (int u = 0; u < parts; ++u)
+  uint32_t again[2] = {0, 0}, given_up = 0;
+  for (int u = 0; u < parts; ++u) {
     for (int t = 0; t < 2; ++t) again[t] |= *cluster.map_shared_rank(redo + t, u);
-  if (*dead) return;
+    given_up |= *cluster.map_shared_rank(dead, u);  // a part that is not whole spoils the rows of all
+  }
+  if (given_up) return;
 #pragma unroll 1
   for (int r = (int)(blockIdx.x % parts) + warp * parts; r < 2 * kRows; r += 8 * parts) {
     const int row = it.i0 + r;
@@ -880,7 +883,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         __syncwarp();
         tc_fence_after();
         ++n;
-        again = bad[t][(n - 1) % 8] == n;
+        again = __all_sync(kFullMask, bad[t][(n - 1) % 8] == n && !dead);
       }
       if (JOIN) {
         // The tile's own queries and weights are used up: their places take its outputs.  (Queries may still be on
@@ -950,7 +953,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     }
     if (JOIN) {
       cluster_sync();
-      if (it.place(a, 0, items, q_tiles, parts, false)) join_parts<DP, KB, CAP, BIAS>(a, it, sm, lse, redo, parts, &dead);
+      if (it.place(a, 0, items, q_tiles, parts, false)) join_parts<DP, KB, CAP, BIAS>(a, it, sm, lse, redo, parts, const_cast<uint32_t*>(&dead));
       cluster_sync();  // the parts are read before a CTA ends
     }
   }
