@@ -210,6 +210,7 @@ struct SwaPrefillLaunch {
   const int64_t* lens;
   void *k_cache, *v_cache;
   unsigned* status;
+  uint64_t wait_ns;  // limit of a wait (bf16)
 };
 cudaError_t launch_swa_prefill_tc(const SwaPrefillLaunch& a, cudaStream_t stream);    // bf16 inputs, strides below 2^40 bytes
 cudaError_t launch_swa_prefill_simt(const SwaPrefillLaunch& a, cudaStream_t stream);  // fp32 inputs

@@ -55,6 +55,10 @@ constexpr int kRows = 128;                    // queries per tile
 constexpr int kThreads = 384;                 // three warpgroups: rows of tile 0, of tile 1, and the rest
 constexpr float kGrowth = 8.f;                // log2 of how far P may exceed 1 before the output is scaled
 constexpr int kSMs = 152;
+// What a wait's limit grows by for each key.  One tile may be at work on all keys, or its rows may be computed again over
+// them, while warps wait for what comes behind; the latter took 2.9 us a key (32 rows a warp, d = 8, 1.2 million keys) and
+// takes a few times that at d = 128.
+constexpr uint64_t kWaitPerKeyNs = 50000;
 // Capped scores may take a bound on their size, up to this in log2 units, for their maximum.  A row's running maximum is
 // never lowered, and its true one lies 2 kBound below it at most; the exponential drops what lies 126 below the running
 // one.  What is lost then lies 46 or more below the row's largest score: 2^24 such keys add 2^-22 to its sum.  (With a
@@ -108,16 +112,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 }
 
 // Bounded wait without a sleep (the hand-offs lie on one chain); over at once when `dead` is set.
-__device__ __forceinline__ void mbar_spin(uint64_t* bar, uint32_t parity, volatile uint32_t* dead, unsigned* status) {
+__device__ __forceinline__ void mbar_spin(uint64_t* bar, uint32_t parity, volatile uint32_t* dead, const SwaPrefillLaunch& a) {
   uint64_t t0 = 0;
   for (uint32_t n = 1; !mbar_try_wait(smem_u32(bar), parity & 1u); ++n) {
     if (n % 8 == 0) {  // a try that fails takes 1.4 us
       if (*dead) return;
       const uint64_t t = globaltimer_ns();
       if (t0 == 0) t0 = t;
-      else if (t - t0 > kWaitLimitNs) {
+      else if (t - t0 > a.wait_ns) {
         *dead = 1;
-        atomicOr(status, kStatusTimeout);
+        atomicOr(a.status, kStatusTimeout);
         return;
       }
     }
@@ -431,7 +435,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { mbar_spin(bar, parity, &dead, a.status); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { mbar_spin(bar, parity, &dead, a); };
   // slot and phase of the i-th block that passes through the ring
   auto slot = [](uint32_t i) { return i % kSlots; };
   auto phase = [](uint32_t i) { return i / kSlots; };
@@ -1060,7 +1064,9 @@ cudaError_t launch_width(const SwaPrefillLaunch& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_swa_prefill_tc(const SwaPrefillLaunch& a, cudaStream_t stream) {
+cudaError_t launch_swa_prefill_tc(const SwaPrefillLaunch& args, cudaStream_t stream) {
+  SwaPrefillLaunch a = args;
+  a.wait_ns = kWaitLimitNs + kWaitPerKeyNs * (uint64_t)a.Nk;
   if (a.d > 64) return launch_width<128, 128>(a, stream);
   return a.window > 0 && a.window <= kNarrow ? launch_width<64, 64>(a, stream) : launch_width<64, 128>(a, stream);
 }

@@ -81,3 +81,26 @@ def test_swa_repeated_axes_give_what_copies_give(B, H, Hkv, Nq, N, d, window, so
     qs = q[:1, :1].expand(B, H, -1, -1)
     assert torch.equal(la.la_swa_prefill(qs, k, v, **kw), la.la_swa_prefill(qs.contiguous(), k, v, **kw))
     assert la.la_device_status() == la.LA_OK
+
+
+def test_swa_rows_computed_again_over_long_prompts_time_nothing_out():
+    """A value that is not finite in a partly seen block has its item's rows computed again key by key, here for seconds,
+    while the products of the block's next item wait: work that goes on is not a wait that has expired."""
+    dev = cuda_device()
+    B, H, Nq, Nk, d = 20, 8, 256, 1_200_000, 8  # 160 items on 152 SMs: those of sequence 19 come behind sequence 18's
+    g = gen(6)
+    q = randn(g, B, H, Nq, d, dtype=BF).to(dev)
+    k, v = (torch.randn((B, 1, Nk, d), device=dev, generator=torch.Generator(dev).manual_seed(s)).to(BF) for s in (1, 2))
+    lens = torch.full((B,), Nk - Nq, device=dev)  # every query is padding
+    lens[18:] = Nk
+    clean = la.la_swa_prefill(q, k, v, lens=lens)
+    v[18, 0, -1, 3] = float("nan")
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    o = la.la_swa_prefill(q, k, v, lens=lens)
+    end.record()
+    assert la.la_device_status() == la.LA_OK
+    print(f"computed again in {start.elapsed_time(end):.0f} ms")
+    assert torch.equal(o[19], clean[19]) and not o[:18].any()
+    assert (o[18, :, :-1].float() - clean[18, :, :-1].float()).abs().max() <= 2 ** -7 * clean[18].float().abs().max() + 1e-4
+    assert torch.isnan(o[18, :, -1, 3]).all() and torch.isfinite(o[18, :, -1, 4]).all()
