@@ -24,6 +24,12 @@ __device__ __forceinline__ KeySpan key_span(const SwaPrefillLaunch& a, int b, in
   return s;
 }
 
+// Where a bias counts a row's distances from.  A softmax is the same for scores that all have moved by as much, so what
+// the row's keys have in common of slope |p - j| is left out: the distance from the row to its interval, which in fp32
+// would cost the scores their lower bits (a row 70000 tokens from its 300 keys at a slope of 0.7 was off by 2e-3).  For a
+// key j of the interval |p - j| less that distance is |c - j| with c, the row moved to its interval's end.
+__device__ __forceinline__ int bias_origin(KeySpan s, int p) { return s.lo < s.hi ? max(s.lo, min(p, s.hi - 1)) : p; }
+
 // tanh(z) / z in z^2 on [0, 1/4] through four Chebyshev nodes, off by 6e-7 of the value at most.  A capped score is
 // cap tanh(z) = x Q(z^2) with z = x / cap up to kStraight, and cap - 2 cap / (1 + e^2z) beyond, where the difference
 // loses nothing that the value itself would hold: as the only form it would leave an error of 1e-7 cap in scores

@@ -119,7 +119,7 @@ swa_simt_kernel(const SwaPrefillLaunch a, int q_tiles, int parts) {
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int pos = (int)(a.q_pos0 + i0) + ty * 4 + i;
+      const int pos = bias_origin(KeySpan{lo[i], hi[i]}, (int)(a.q_pos0 + i0) + ty * 4 + i);
       float mt = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {

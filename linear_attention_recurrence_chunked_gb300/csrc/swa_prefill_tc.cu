@@ -174,7 +174,7 @@ __device__ __noinline__ void slow_row(const SwaPrefillLaunch& a, int64_t b, int6
   const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q.ptr) + b * a.q.sb + h * a.q.sh + i * a.q.st;
   const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(a.k.ptr) + b * a.k.sb + hk * a.k.sh;
   const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.v.ptr) + b * a.v.sb + hk * a.v.sh;
-  const int pos = (int)(a.q_pos0 + i);
+  const int pos = bias_origin(sp, (int)(a.q_pos0 + i));
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j0 = sp.lo; j0 < sp.hi; j0 += 32) {
@@ -648,7 +648,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         jb = t ? bl.jb[1] : bl.jb[0];
         je = t ? bl.je[1] : bl.je[0];
       }
-      const int pos = (int)a.q_pos0 + i;
+      const int pos = bias_origin(span, (int)a.q_pos0 + i);
       const float slope2 = BIAS && a.slopes ? a.slopes[it.h] * kLog2e : 0.f;
       float m = -INFINITY, l = 0.f;
       for (int j = jb; j < je; ++j, ++ns) {

@@ -104,3 +104,36 @@ def test_swa_rows_computed_again_over_long_prompts_time_nothing_out():
     assert torch.equal(o[19], clean[19]) and not o[:18].any()
     assert (o[18, :, :-1].float() - clean[18, :, :-1].float()).abs().max() <= 2 ** -7 * clean[18].float().abs().max() + 1e-4
     assert torch.isnan(o[18, :, -1, 3]).all() and torch.isfinite(o[18, :, -1, 4]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("H,Nq", [(2, 3), (160, 200)])
+def test_swa_biased_rows_far_from_all_their_keys(dtype, H, Nq):
+    """Rows whose keys all lie far behind or far ahead of them: the bias is the same for all of a row's keys but for
+    their distance from the nearest one, and what they share must not cost the scores their accuracy."""
+    dev = cuda_device()
+    Nk, d, seen = 70000, 64, 300
+    q, k, v = swa_case(1, H, 1, Nq, Nk, d, dtype, H)
+    sl = torch.full((H,), 0.7)
+    for q_pos0, lo, hi, nearest in ((Nk - Nq, 40, 40 + seen, seen - 1), (0, Nk - seen, Nk, 0)):
+        key_lo, key_hi = (torch.full((1, Nq), x, dtype=torch.int32, device=dev) for x in (lo, hi))
+        o = la.la_swa_prefill(*on(dev, q, k, v), slopes=sl.to(dev), key_lo=key_lo, key_hi=key_hi, q_pos0=q_pos0)
+        for h, i in ((0, 0), (H - 1, 1), (H // 2, Nq - 1)):
+            want, bound = ref.swa(q[:, h:h + 1, i:i + 1], k[:, :, lo:hi], v[:, :, lo:hi], d ** -0.5, 0.0, sl[:1], [[(0, seen)]], nearest, dtype)
+            ref.check(o[:, h:h + 1, i:i + 1], want, bound)
+    assert la.la_device_status() == la.LA_OK
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_swa_biased_rows_far_from_their_keys_computed_again(bad):
+    """The same where a masked value of a partly seen block is not finite."""
+    dev = cuda_device()
+    Nk, d, Nq = 70000, 64, 5
+    q, k, v = swa_case(1, 2, 1, Nq, Nk, d, BF, 3)
+    v[:, :, 39] = bad
+    sl = torch.full((2,), 0.7)
+    key_lo, key_hi = (torch.full((1, Nq), x, dtype=torch.int32, device=dev) for x in (40, 340))
+    o = la.la_swa_prefill(*on(dev, q, k, v), slopes=sl.to(dev), key_lo=key_lo, key_hi=key_hi)
+    for i in (0, 4):
+        want, bound = ref.swa(q[:, :, i:i + 1], k[:, :, 40:340], v[:, :, 40:340], d ** -0.5, 0.0, sl, [[(0, 300)]], 299, BF)
+        ref.check(o[:, :, i:i + 1], want, bound)
