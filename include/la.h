@@ -420,7 +420,8 @@ la_status la_notebank_route(const la_notebank_route_args* args, void* stream);
  *   bias  : [C] w_dtype or NULL; w and bias 16-byte aligned
  *   state : [B, W-1, C] in_dtype contiguous, the last W-1 inputs, oldest first;
  *           state_in NULL = zeros; state_out required, may alias state_in.
- * fp32 arithmetic. */
+ * fp32 arithmetic.  Limits: B ceil(N / 64) < 2^31, B (N + 1) C <= 2^39 - 256
+ * (LA_ERR_UNSUPPORTED). */
 typedef struct la_conv_prefill_args {
   int64_t B, N, C, W;
   la_dtype in_dtype, out_dtype, w_dtype;
@@ -437,8 +438,8 @@ la_status la_conv_prefill(const la_conv_prefill_args* args, void* stream);
 
 /* The same for one token of each of S sequences (x, out: [S, C] rows,
  * x_stride / out_stride elements apart, rows 16-byte aligned; state [S, W-1, C]
- * contiguous; state_out may alias state_in).  Launched as a programmatic
- * dependent, as la_decode_step. */
+ * contiguous; state_out may alias state_in).  S C <= 2^39 - 256.  Launched as a
+ * programmatic dependent, as la_decode_step. */
 typedef struct la_conv_decode_args {
   int64_t S, C, W;
   la_dtype in_dtype, out_dtype, w_dtype;
@@ -473,7 +474,8 @@ la_status la_conv_decode_step(const la_conv_decode_args* args, void* stream);
  * la_ssm_prefill_workspace_size returns (often 0; a function of the sizes
  * only; 16-byte aligned, dead when the call's work has finished).  A call
  * with a smaller workspace fails with LA_ERR_WORKSPACE.
- * Limits: B <= 65535, C < 2^25, N < 2^30 (LA_ERR_UNSUPPORTED). */
+ * Limits: B <= 65535, C < 2^25, N < 2^30, B ceil(N / 64) < 2^31
+ * (LA_ERR_UNSUPPORTED). */
 typedef struct la_ssm_prefill_args {
   int64_t B, N, C, n, G;
   la_dtype in_dtype, out_dtype;

@@ -419,6 +419,10 @@ bool within(int64_t limit, std::initializer_list<int64_t> sizes) {
 }
 bool valid_size(int64_t s) { return s >= 0 && s <= kMaxDim; }
 
+constexpr int64_t kMaxBlocks = (int64_t(1) << 31) - 1;  // of a launch's grid
+// Whether the padding of [B, H, N] rows fits one launch (64 rows a block).
+bool paddable(int64_t B, int64_t H, int64_t N) { return within(kMaxBlocks, {B, H, (N + 63) / 64}); }
+
 // Whether no two elements of a [B, H, N, d] view lie on one another, for views whose axes nest in some order.
 bool distinct(const la_tensor& x, int64_t B, int64_t H, int64_t N, int64_t d) {
   struct Axis { int64_t stride, size; } ax[3] = {{x.stride_b, B}, {x.stride_h, H}, {x.stride_t, N}};
@@ -472,7 +476,7 @@ la_status la_conv_prefill(const la_conv_prefill_args* a, void* stream) {
   if (!valid_dtype(a->in_dtype) || !valid_dtype(a->out_dtype) || !valid_dtype(a->w_dtype)) return LA_ERR_INVALID_ARGUMENT;
   if (a->W < 2 || a->W > 4) return LA_ERR_UNSUPPORTED;
   if (a->B == 0 || a->C == 0) return LA_OK;
-  if (!within(int64_t(1) << 40, {a->B, a->N + 1, a->C})) return LA_ERR_UNSUPPORTED;
+  if (!within(kMaxBlocks * 256, {a->B, a->N + 1, a->C}) || !paddable(a->B, 1, a->N)) return LA_ERR_UNSUPPORTED;
   if (!valid_rows(a->x, a->B, a->N, a->C, a->in_dtype, false) || !valid_rows(a->y, a->B, a->N, a->C, a->out_dtype, true))
     return LA_ERR_INVALID_ARGUMENT;
   if (a->N > 0 && a->x.ptr == a->y.ptr) return LA_ERR_INVALID_ARGUMENT;  // a run's history may be overwritten
@@ -503,7 +507,7 @@ la_status la_conv_decode_step(const la_conv_decode_args* a, void* stream) {
   if (!valid_dtype(a->in_dtype) || !valid_dtype(a->out_dtype) || !valid_dtype(a->w_dtype)) return LA_ERR_INVALID_ARGUMENT;
   if (a->W < 2 || a->W > 4) return LA_ERR_UNSUPPORTED;
   if (a->S == 0 || a->C == 0) return LA_OK;
-  if (!within(int64_t(1) << 40, {a->S, a->C})) return LA_ERR_UNSUPPORTED;
+  if (!within(kMaxBlocks * 256, {a->S, a->C})) return LA_ERR_UNSUPPORTED;
   const la_tensor x{const_cast<void*>(a->x), 0, 0, a->x_stride}, y{a->out, 0, 0, a->out_stride};
   if (!valid_rows(x, 1, a->S, a->C, a->in_dtype, false) || !valid_rows(y, 1, a->S, a->C, a->out_dtype, true))
     return LA_ERR_INVALID_ARGUMENT;
@@ -536,7 +540,7 @@ la_status la_ssm_prefill(const la_ssm_prefill_args* a, void* ws, size_t ws_bytes
   if (!valid_dtype(a->in_dtype) || !valid_dtype(a->out_dtype)) return LA_ERR_INVALID_ARGUMENT;
   if (a->n < 1 || a->n > 64) return LA_ERR_UNSUPPORTED;
   if (a->B == 0 || a->C == 0) return LA_OK;
-  if (!ssm_shape(a)) return LA_ERR_UNSUPPORTED;
+  if (!ssm_shape(a) || !paddable(a->B, 1, a->N)) return LA_ERR_UNSUPPORTED;
   const int64_t B = a->B, N = a->N, C = a->C;
   if (!valid_rows(a->u, B, N, C, a->in_dtype, false) || !valid_rows(a->delta, B, N, C, a->in_dtype, false) ||
       (a->z.ptr && !valid_rows(a->z, B, N, C, a->in_dtype, false)) || !valid_rows(a->y, B, N, C, a->out_dtype, true))

@@ -185,6 +185,22 @@ def test_swa_prefill_refuses_bf16_strides_that_no_tensor_map_holds(lib, name):
     assert lib.la_swa_prefill(ctypes.byref(swa_args(**{name: far}, **fp32)), None) == INV
 
 
+def test_counts_beyond_a_launchs_grid_are_refused(lib):
+    """One short sequence too many for the launch that fills the padding, or for the convolution's own."""
+    for B, N, status in ((1 << 31, 1, UNS), ((1 << 32) + 5, 1, UNS), (1 << 31, 0, UNS), ((1 << 32) + 5, 64, UNS), ((1 << 31) - 1, 1, INV)):
+        wide = lambda k: T(at(k), 8 * max(N, 1), 0, 8)  # noqa: E731
+        kw = dict(B=B, N=N, C=1, x=wide(0), y=wide(1), lens=at(6), fill=3)
+        # within the limits the missing taps are the next thing to refuse
+        assert lib.la_conv_prefill(ctypes.byref(conv_args(w=None, **kw)), None) == status
+    assert lib.la_conv_prefill(ctypes.byref(conv_args(B=1 << 20, N=1 << 19, C=1, x=T(at(0), 1 << 22, 0, 8), y=T(at(1), 1 << 22, 0, 8))), None) == UNS
+    for S, status in ((1 << 39, UNS), ((1 << 39) - 256, INV)):
+        assert lib.la_conv_decode_step(ctypes.byref(conv_step_args(S=S, C=1, x_stride=8, out_stride=8, w=None)), None) == status
+    B, N = 65535, 1 << 29
+    big = dict(B=B, N=N, C=1, G=1, u=T(at(0), 0, 0, 8), delta=T(at(1), 0, 0, 8), z=T(None, 0, 0, 0), y=T(at(3), 8 * N, 0, 8),
+               Bm=T(at(4), 0, 0, 16), Cm=T(at(5), 0, 0, 16), A=None)
+    assert lib.la_ssm_prefill(ctypes.byref(ssm_args(**big)), None, 0, None) == UNS
+
+
 def test_null_arguments(lib):
     for fn in (lib.la_conv_prefill, lib.la_conv_decode_step, lib.la_ssm_decode_step, lib.la_swa_prefill, lib.la_swa_biased_decode_step):
         assert fn(None, None) == INV
