@@ -405,7 +405,8 @@ ssm_scan_kernel(const SsmLaunch a, Segments seg, float* ws_h, float* ws_dt) {
 }
 
 // The state that enters each segment, in place of the segment's local state: over a segment a state
-// decays by exp(A * sum of dt).
+// decays by exp(A * sum of dt).  A state may grow too, and over a segment by more than fp32 holds: the factor comes in two
+// halves, and a state of zero, which a token's finite factors leave at zero, takes none.
 __global__ void __launch_bounds__(256)
 ssm_combine_kernel(const SsmLaunch a, Segments seg, float* ws_h, const float* ws_dt) {
   const int64_t per = a.C * a.n;
@@ -420,7 +421,8 @@ ssm_combine_kernel(const SsmLaunch a, Segments seg, float* ws_h, const float* ws
   for (int g = 0; g + 1 < seg.count; ++g) {
     const float local = p[g * per];
     p[g * per] = h;
-    h = fmaf(ex2(A2 * d[(int64_t)g * a.C]), h, local);
+    const float half = ex2(0.5f * (A2 * d[(int64_t)g * a.C]));
+    h = h == 0.f ? local : fmaf(half * h, half, local);
   }
   p[(seg.count - 1) * per] = h;
 }

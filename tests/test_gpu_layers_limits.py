@@ -137,3 +137,22 @@ def test_swa_biased_rows_far_from_their_keys_computed_again(bad):
     for i in (0, 4):
         want, bound = ref.swa(q[:, :, i:i + 1], k[:, :, 40:340], v[:, :, 40:340], d ** -0.5, 0.0, sl, [[(0, 300)]], 299, BF)
         ref.check(o[:, :, i:i + 1], want, bound)
+
+
+@pytest.mark.parametrize("h0,lens", [(0.0, None), (1e-30, [170])])
+def test_ssm_segments_of_growing_states(h0, lens):
+    """Time segments over which exp(A sum dt) leaves fp32's range: a state of zero stays zero, a small one grows."""
+    dev = cuda_device()
+    B, N, C, n = 1, 2000, 48, 16
+    g = gen(4)
+    A = 0.8 + 0.2 * torch.rand((C, n), generator=g)
+    delta = 0.6 + 0.1 * torch.rand((B, N, C), generator=g)
+    u, Bm, Cm = randn(g, B, N, C), randn(g, B, 1, N, n), randn(g, B, 1, N, n)
+    u[:, :N - 40] = 0  # what enters grows by 2^40 at most
+    h_in = torch.full((B, C, n), h0)
+    ln = None if lens is None else torch.tensor(lens, device=dev)
+    assert la.la_ssm_prefill_workspace_size(*on(dev, u, delta, A, Bm, Cm)) > 0
+    y, h = la.la_ssm_prefill(*on(dev, u, delta, A, Bm, Cm), h_in=h_in.to(dev), delta_softplus=False, lens=ln)
+    y_ref, bound, h_ref, h_bound = ref.ssm(u, delta, A, Bm, Cm, None, None, None, False, h_in, lens, FP, segment=160)
+    ref.check(h, h_ref, h_bound)
+    ref.check(y, y_ref, bound)
