@@ -714,7 +714,9 @@ def _on_stream(fn):
         if not x.is_cuda:
             return fn(*args, **kwargs)
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(_stream_handle(stream), device=x.device)
+            handle = _stream_handle(stream)
+            # NULL and cudaStreamLegacy are the default stream; as an external stream torch takes neither for it
+            stream = torch.cuda.default_stream(x.device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=x.device)
         if stream.device != x.device:
             raise ValueError(f"the stream is of {stream.device}, the tensors of {x.device}")
         with torch.cuda.stream(stream):

@@ -156,3 +156,20 @@ def test_ssm_segments_of_growing_states(h0, lens):
     y_ref, bound, h_ref, h_bound = ref.ssm(u, delta, A, Bm, Cm, None, None, None, False, h_in, lens, FP, segment=160)
     ref.check(h, h_ref, h_bound)
     ref.check(y, y_ref, bound)
+
+
+@pytest.mark.parametrize("handle,runs_on", [(0, 0), (1, 0), (2, 2)])
+def test_stream_handles_of_the_default_streams(monkeypatch, handle, runs_on):
+    """0 and cudaStreamLegacy (1) are the legacy default stream, cudaStreamPerThread (2) is the thread's own."""
+    dev = cuda_device()
+    x, w = torch.randn((1, 9, 16), device=dev), torch.randn((16, 4), device=dev)
+    want = la.la_conv_prefill(x, w)
+    torch.cuda.synchronize()
+    used = []
+    call = la._call
+    monkeypatch.setattr(la, "_call", lambda name, index, *a: (used.append(torch.cuda.current_stream(dev).cuda_stream), call(name, index, *a)))
+    with torch.cuda.stream(torch.cuda.Stream(dev)):
+        got = la.la_conv_prefill(x, w, stream=handle)
+        torch.cuda.synchronize()
+    assert used == [runs_on]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
