@@ -67,7 +67,7 @@ swa_biased_decode_mma_kernel(const SwaBiasedDecodeLaunch a) {
     return;
   }
   const int slot_new = (int)(pos % w);
-  const int n = pos + 1 < w ? (int)(pos + 1) : w;
+  const int n = pos < w ? (int)pos + 1 : w;
   const int first = warp * kSlots, h0 = (int)hk * group;
   const T* kn = reinterpret_cast<const T*>(c.k) + sk * d;
   const T* vn = reinterpret_cast<const T*>(c.v) + sk * d;
@@ -271,7 +271,7 @@ swa_biased_decode_kernel(const SwaBiasedDecodeLaunch a) {
     return;
   }
   const int slot_new = (int)(pos % w);
-  const int n = pos + 1 < w ? (int)(pos + 1) : w;
+  const int n = pos < w ? (int)pos + 1 : w;
   const int col = lane % LPR * V, sub = lane / LPR, first = warp * kSlots;
   const bool on = col < d;
   const TIn* kn = reinterpret_cast<const TIn*>(c.k) + sk * d + col;

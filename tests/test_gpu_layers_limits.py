@@ -173,3 +173,16 @@ def test_stream_handles_of_the_default_streams(monkeypatch, handle, runs_on):
         torch.cuda.synchronize()
     assert used == [runs_on]
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_swa_step_at_the_last_position(dtype):
+    dev = cuda_device()
+    g = gen(3)
+    q, k, v = (randn(g, 2, 4, 64, dtype=dtype).to(dev) for _ in range(3))
+    kc, vc = (randn(g, 2, 4, 40, 64, dtype=dtype).to(dev) for _ in range(2))
+    far = torch.tensor([(1 << 63) - 1, (1 << 63) - 2], device=dev)
+    near = 40 + far % 40  # the same slots of a full ring
+    a = la.la_swa_biased_decode_step(q, k, v, kc.clone(), vc.clone(), far)
+    b = la.la_swa_biased_decode_step(q, k, v, kc.clone(), vc.clone(), near)
+    assert torch.isfinite(a.float()).all() and torch.equal(a, b)
