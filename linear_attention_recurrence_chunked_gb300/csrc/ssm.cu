@@ -46,12 +46,14 @@ __device__ __forceinline__ float log2_rate(float A) {
   return x < -3.402823466e38f ? -3.402823466e38f : x;
 }
 
-// Added to the exponent, which costs nothing in its multiplication.  The unit's 2^x came out low by 2.1e-8 to 5e-8
-// of the value on average for decays below 0.999 (2^20 arguments per range against fp64; exp2f likewise), and a
-// state takes one such factor per token, so the errors add up along its memory: 2.5e-8 log2(e) centres them.
-// States of 4 x 300 tokens came out off by 1.0e-6 without it, by less than 0.7e-6 with it.  It is below half a
-// rounding at 1: dt = 0 stays the identity.
-constexpr float kCentre = 3.6e-8f;
+// Added to the exponent x, which costs nothing in its multiplication: the unit's 2^x comes out low on average, and a state
+// takes one such factor per token, so that the errors add up along its memory.  Against fp64 over 2^20 arguments per
+// factor of two, the mean is -1.6e-8 to -2.7e-8 of the value for 2^-8 < |x| < 1 and -5e-9 to -1e-8 for 2^-19 < |x| < 2^-8,
+// where results are so close to 1 that they are nearly rounded to nearest.  Each range has a centre of its own; below 9e-9
+// is left for 2^-8 < |x| < 1/2, and below 4e-9 from there down to 2^-19, where memories are long.  (3.6e-8 for all left
+// 2e-8 there: a memory of 6000 tokens was off by 5e-5 in one pass, now by less than 2e-5, and 2000 tokens of 4096
+// channels by 5.2e-7, now 1.9e-7.)  Both are below half a rounding at 1: dt = 0 stays the identity.
+__device__ __forceinline__ float centre_of(float x) { return fabsf(x) > 0.00390625f ? 3.6e-8f : 9e-9f; }
 
 // Time segments: segment g of a sequence takes tokens [g * len, (g + 1) * len).
 struct Segments {
@@ -121,7 +123,7 @@ ssm_scan_kernel(const SsmLaunch a, Segments seg, float* ws_h, float* ws_dt) {
     const int l = tid % L, p = tid / L;
     const int64_t c = c_base + p * kCh;
     f32x2 A01[kCh], A23[kCh], h01[kCh], h23[kCh];
-    float dt_sum[kCh];
+    float dt_sum[kCh], slowest = INFINITY;  // of the lane's states
 #pragma unroll
     for (int e = 0; e < kCh; ++e) {
       float A2[kK], h[kK];
@@ -130,6 +132,7 @@ ssm_scan_kernel(const SsmLaunch a, Segments seg, float* ws_h, float* ws_dt) {
         const int s = l * kK + k;
         const bool on = c + e < c_end && s < a.n;
         A2[k] = on ? log2_rate(a.A[(c + e) * a.n + s]) : 0.f;
+        if (on) slowest = fminf(slowest, fabsf(A2[k]));
         h[k] = 0.f;
         if (MODE == kFull && on && a.h_in) h[k] = a.h_in[(b * a.C + c + e) * a.n + s];
         if (MODE == kFinal && on) h[k] = ws_h[((b * seg.count + sid) * a.C + c + e) * a.n + s];
@@ -150,8 +153,21 @@ ssm_scan_kernel(const SsmLaunch a, Segments seg, float* ws_h, float* ws_dt) {
       float dt[kCh], dtu[kCh];
       LaneBC bc;
     };
-    const f32x2 centre = pack2(kCentre, kCentre);
+    // A lane's states share a centre, that of the slowest: a pair of registers for each state
+    // took 848 us for the prompt above, one for all states and tokens 809, this 818.
+    // A tile's goes by the last step of the tile before, the first tile's by its own first step.
+    f32x2 centre;
+    auto centre_by = [&](const float (&dt)[kCh]) {
+      const float m = centre_of(slowest * fminf(fabsf(dt[0]), fabsf(dt[kCh - 1])));
+      centre = pack2(m, m);
+    };
     __syncthreads();  // tile 0 is laid out
+    {
+      float dt[kCh];
+#pragma unroll
+      for (int e = 0; e < kCh; ++e) dt[e] = sm.work[0].dt[0][dt_at[0] + e].x;
+      centre_by(dt);
+    }
     for (int i = 0; i < count; ++i) {
       typename T::Work& q = sm.work[i & 1];
       auto read = [&](int r) {
@@ -202,9 +218,12 @@ ssm_scan_kernel(const SsmLaunch a, Segments seg, float* ws_h, float* ws_dt) {
 #pragma unroll
             for (int e = 0; e < kCh; ++e) q.y[e][r + k][y_at[(r + k) % T::kPeriod]] = y[k][e];
         }
+        if (r + kAhead < TT) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) cur[k] = next[k];
+          for (int k = 0; k < kAhead; ++k) cur[k] = next[k];
+        }
       }
+      centre_by(cur[kAhead - 1].dt);
       __syncthreads();
     }
 #pragma unroll
@@ -517,7 +536,7 @@ ssm_decode_kernel(const SsmLaunch a, bool a_vec, bool bc_vec) {
     acc[q] = 0.f;
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
-      h[q][k] = fmaf(ex2(fmaf(dt, A2[k], kCentre)), h[q][k], dtu * Bk[k]);
+      h[q][k] = fmaf(ex2(fmaf(dt, A2[k], centre_of(dt * A2[k]))), h[q][k], dtu * Bk[k]);
       acc[q] = fmaf(Ck[k], h[q][k], acc[q]);
     }
     if (on && s0 + q < a.B) {

@@ -186,3 +186,23 @@ def test_swa_step_at_the_last_position(dtype):
     a = la.la_swa_biased_decode_step(q, k, v, kc.clone(), vc.clone(), far)
     b = la.la_swa_biased_decode_step(q, k, v, kc.clone(), vc.clone(), near)
     assert torch.isfinite(a.float()).all() and torch.equal(a, b)
+
+
+def test_ssm_slow_decays_add_up_to_no_bias():
+    """One pass over 20000 tokens with memories of about 800 to 6000: a state takes one rounded factor per token, and the
+    mean of their errors must stay near zero where factors are close to 1 too."""
+    dev = cuda_device()
+    B, N, C, n = 1, 20000, 3328, 16
+    g = torch.Generator(dev).manual_seed(5)
+    draw = lambda *shape: torch.randn(shape, device=dev, generator=g)  # noqa: E731
+    u, delta, Bm, Cm = (draw(*s).to(BF) for s in ((B, N, C), (B, N, C), (B, 1, N, n), (B, 1, N, n)))
+    A = -torch.linspace(0.2, 1.5, n, device=dev).expand(C, n).contiguous()
+    bias = torch.full((C,), -7.6, device=dev)  # steps near 5e-4
+    assert la.la_ssm_prefill_workspace_size(u, delta, A, Bm, Cm) == 0
+    _, h = la.la_ssm_prefill(u, delta, A, Bm, Cm, delta_bias=bias, out_dtype=FP)
+    pick = torch.tensor([0, 1, 1700, C - 1], device=dev)
+    h_ref = ref.ssm(u[..., pick], delta[..., pick], A[pick], Bm, Cm, None, None, bias[pick], True, None, None, FP)[2]
+    err = np.linalg.norm(h[:, pick].double().cpu().numpy() - h_ref) / np.linalg.norm(h_ref)
+    # a mean of 2.5e-9 a token over 6000 tokens of memory, 0.7 of which weigh: 1.1e-5; a factor's and a state's rounding of
+    # 2^-24 enter at random: 2.5e-6
+    assert err < 2e-5
