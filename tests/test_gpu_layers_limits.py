@@ -7,7 +7,7 @@ import torch
 import linear_attention_recurrence_chunked_gb300 as la
 from tests import layers_oracle as ref
 from tests.helpers import cuda_device
-from tests.test_gpu_layers import gen, on, randn, slopes_of, swa_case
+from tests.test_gpu_layers import gen, on, pad_rows, randn, slopes_of, ssm_inputs, swa_case
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float32
@@ -206,3 +206,53 @@ def test_ssm_slow_decays_add_up_to_no_bias():
     # a mean of 2.5e-9 a token over 6000 tokens of memory, 0.7 of which weigh: 1.1e-5; a factor's and a state's rounding of
     # 2^-24 enter at random: 2.5e-6
     assert err < 2e-5
+
+
+@pytest.mark.parametrize("B,N,C,n,G,dtype,out,z,softplus", [
+    (2, 37, 40, 16, 2, BF, BF, True, True), (2, 70, 33, 4, 1, FP, FP, False, True), (3, 129, 24, 24, 3, FP, FP, True, True),
+    (1, 100, 10, 64, 2, BF, FP, False, True), (2, 31, 7, 1, 1, FP, FP, True, True), (1, 40, 21, 7, 3, BF, FP, True, False),
+    (1, 300, 16, 16, 1, FP, FP, True, True)])
+def test_ssm_prefill_in_one_segment_within_single_roundings(B, N, C, n, G, dtype, out, z, softplus):
+    """No time segments: a token's decay has the errors of its own product and exponential alone."""
+    dev = cuda_device()
+    t = ssm_inputs(B, N, C, n, G, dtype, z, 2 * N + C)
+    if not softplus:
+        t["delta"], t["bias"] = t["delta"].abs() * 0.2, t["bias"].abs() * 0.1
+    names = ("u", "delta", "A", "Bm", "Cm", "D", "z", "bias", "h")
+    args = [t[k] for k in names]
+    y_ref, bound, h_ref, h_bound = ref.ssm(*args[:8], softplus, t["h"], None, out)
+    u, delta, A, Bm, Cm, D, zd, bias, h0 = on(dev, *args)
+    u, delta, zd = (None if x is None else pad_rows(x, dev) for x in (u, delta, zd))
+    assert la.la_ssm_prefill_workspace_size(u, delta, A, Bm, Cm) == 0
+    y, h = la.la_ssm_prefill(u, delta, A, Bm, Cm, D=D, z=zd, delta_bias=bias, delta_softplus=softplus, h_in=h0, out_dtype=out)
+    ref.check(h, h_ref, h_bound)
+    ref.check(y, y_ref, bound)
+
+
+@pytest.mark.parametrize("B,N,C,n,dtype,length", [(1, 2000, 48, 16, BF, 160), (2, 1500, 24, 8, FP, 160), (1, 4000, 96, 16, FP, 160)])
+def test_ssm_prefill_in_segments_joins_them_within_a_segments_roundings(B, N, C, n, dtype, length):
+    """Time segments: a state that enters one decays by exp(A sum dt), whose sum has a rounding per token of the segment.
+    That error enters once per segment, on top of the single pass's."""
+    dev = cuda_device()
+    t = ssm_inputs(B, N, C, n, 1, dtype, False, N)
+    args = [t[k] for k in ("u", "delta", "A", "Bm", "Cm", "D", "z", "bias")]
+    y_ref, bound, h_ref, h_bound = ref.ssm(*args, True, t["h"], None, FP)
+    # what a segment's end holds of the states that entered it, times the error of the decay that carried it there
+    dt = np.logaddexp(ref.f64(t["delta"]) + ref.f64(t["bias"]), 0)
+    A, e, states = ref.f64(t["A"]), 0.0, ref.f64(t["h"])
+    for s in range(0, N, length):
+        total = dt[:, s:s + length].sum(1)[..., None] * A  # [B, C, n]
+        a = np.exp(total)
+        e = a * e + a * np.abs(states) * (np.abs(total) * (length + 4) * ref.U + 2.0 ** -21)
+        cut = [x[:, s:s + length] for x in (t["u"], t["delta"])]
+        bc = [x[:, :, s:s + length] for x in (t["Bm"], t["Cm"])]
+        states = ref.ssm(*cut, t["A"], *bc, t["D"], None, t["bias"], True, torch.from_numpy(states), None, FP)[2]
+    u, delta, Ad, Bm, Cm, D, _, bias, h0 = on(dev, *args, t["h"])
+    assert la.la_ssm_prefill_workspace_size(u, delta, Ad, Bm, Cm) > 0
+    y, h = la.la_ssm_prefill(u, delta, Ad, Bm, Cm, D=D, delta_bias=bias, h_in=h0, out_dtype=FP)
+    ref.check(h, h_ref, h_bound + e)
+    # the first segment enters without a join
+    assert N > 2 * length
+    first = np.full_like(y_ref, np.nan)
+    first[:, :length] = y_ref[:, :length]
+    ref.check(y, first, bound)
