@@ -4,15 +4,16 @@
 // per token, channel c of group g and state s (NoteBank Sec. 2 Eq. (1) with a diagonal A_t).
 //
 // Per (token, channel, state) the scan needs one exponential and four fp32 operations, per (token, channel)
-// four 2-byte elements of memory: with 16 states the special-function unit (16 results per SM and clock)
-// bounds it at three times the memory time.  The decay differs per (channel, state), so no chunk form on
+// four 2-byte elements of memory: with 16 states the special-function unit (32 results an SM and clock) needs
+// 1.4 times what memory does.  The decay differs per (channel, state), so no chunk form on
 // the tensor cores exists: the tokens are walked in order, with the channels and states in parallel.
-// 4 x 16384 x 2048 channels with 16 states, bf16: 804 us.  The bytes alone take 161 us and the exponentials 220 us (32 of
-// them an SM and clock, at the 2.0 GHz it ran at); the four scan warps' issue slots bound it at about 500 us, and
-// shared memory (LSU pipe 70 % busy) and the barrier a tile make up the rest.
+// 4 x 16384 x 2048 channels with 16 states, bf16: 818 us.  The bytes alone take 161 us and the exponentials 220 us, at the
+// 2.0 GHz it ran at, on all SMs; 128 blocks leave 24 of 152 without one.  A (token, channel) costs 126 instructions, about
+// 70 of them the recurrence's own with its loads and stores; nothing is near its limit (the special-function pipe at 31 %,
+// fp32 at 25 %, shared memory at 24 % of elapsed), and the warps wait most for the barrier of a tile, on one another.
 //
-// A block has four scan warps, four layout warps and four output warps, which work on tiles of tokens in turn
-// through shared memory, one barrier a tile.  While the scan warps walk tile i, the layout warps prepare tile
+// A block has four scan warps, four layout warps for each channel of a lane, and four output warps, which work on
+// tiles of tokens in turn through shared memory, one barrier a tile.  While the scan warps walk tile i, the layout warps prepare tile
 // i + 1 (the step sizes with their softplus, once per (token, channel), and B_t, C_t in fp32), with the raw
 // inputs of the tiles behind it on their way, and the output warps add up the readout of tile i - 1, apply
 // the skip term and the gate and store it.  In the scan L lanes share kCh channels; a lane holds four states
@@ -31,7 +32,7 @@ constexpr int kScan = 128;    // threads of the four scan warps
 constexpr int kOutput = 128;  // and of the output warps
 // Channels per scan lane.  Two halve a state's share of the reads of B and C (a lane's bytes count there, 128
 // a clock and SM, also where lanes read the same), which bound the scan with one, but leave half the blocks.
-// 4 x 16384 x 2048 channels, 16 states: 807 us with two, 928 us with one; with at most one block of one channel
+// 4 x 16384 x 2048 channels, 16 states: 818 us with two, 928 us with one; with at most one block of one channel
 // per lane on each SM, one channel is faster.
 constexpr int layout_threads(int ch) { return ch * kScan; }
 constexpr int block_threads(int ch) { return kScan + layout_threads(ch) + kOutput; }
@@ -153,9 +154,9 @@ ssm_scan_kernel(const SsmLaunch a, Segments seg, float* ws_h, float* ws_dt) {
       float dt[kCh], dtu[kCh];
       LaneBC bc;
     };
-    // A lane's states share a centre, that of the slowest: a pair of registers for each state
-    // took 848 us for the prompt above, one for all states and tokens 809, this 818.
-    // A tile's goes by the last step of the tile before, the first tile's by its own first step.
+    // A lane's states share a centre, that of the slowest: a pair of registers for each state took 848 us for the prompt
+    // above, one centre for all states and tokens 809, this 818.  A tile's goes by the last step of the tile before, the
+    // first tile's by its own first step.
     f32x2 centre;
     auto centre_by = [&](const float (&dt)[kCh]) {
       const float m = centre_of(slowest * fminf(fabsf(dt[0]), fabsf(dt[kCh - 1])));

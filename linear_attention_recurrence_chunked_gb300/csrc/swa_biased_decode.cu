@@ -173,7 +173,7 @@ swa_biased_decode_mma_kernel(const SwaBiasedDecodeLaunch a) {
   tc::cp_async_wait_all();
   __syncwarp();
   // Weights in two bf16 parts, the second one what the first leaves: a weight is off by 2^-17 of itself, where one part
-  // would leave 2^-9, more than an fp32 output can hide.  Up to eight heads the second parts take the rows that have no
+  // would leave 2^-8, more than an fp32 output can hide.  Up to eight heads the second parts take the rows that have no
   // head and no product is added; beyond, they are products of their own (256 x 64 heads over 4: 42.8 us, 41.3 with one
   // part).
 #pragma unroll

@@ -19,12 +19,13 @@
 // finished.  Widths up to 64 with narrow windows take blocks of 64 keys and two CTAs an SM: their blocks are
 // few, and a chain of product, softmax and product is mostly latency.
 //
-// 2 x 16 heads of 8192 tokens over 4 key heads at d = 128, causal: 386 us, 1430 TFLOP/s, 74 % of the measured bf16 rate;
-// with a cap of 30 540-565 us, bound by the rows' instructions (a polynomial, an exponential and a rounding per
-// score).  8 x 16 x 4096 at d = 64 with a window of 64: 91 us with the rings, of which its bytes take 40; a block's
+// 2 x 16 heads of 8192 tokens over 4 key heads at d = 128, causal: 387 us, 1420 TFLOP/s, 74 % of the measured bf16 rate;
+// with a cap of 30 535-575 us from box to box.  There neither the tensor pipe (35 %) nor the exponential unit (17 %) nor
+// the issue slots (38 %) are near their limit: two row warps a scheduler wait for tensor-memory reads and for
+// instructions.  8 x 16 x 4096 at d = 64 with a window of 64: 94 us with the rings, of which its bytes take 40; a block's
 // chain of product, softmax and product bounds it.  Documents of 700 tokens with prefixes, a window of 1024 and a bias
-// at d = 96 (2 x 8 x 4099): 68 us, 48 us without the bias; where a prefix reaches ahead of its rows the bias takes the
-// distance column by column (a form of that in registers too made it 70 us).
+// at d = 96 (2 x 8 x 4099): 69 us, 48 us without the bias, on 272 items for 152 SMs; where a prefix reaches ahead of its
+// rows the bias takes the distance column by column (a form of that in registers too made it 70 us).
 //
 // Where items leave SMs idle and see several blocks, the CTAs of a cluster share an item's blocks; each leaves its
 // rows' outputs, divided by their sums, and m + log2 l in its shared memory, where the cluster joins them.
@@ -695,7 +696,11 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           return m == -INFINITY ? 0.f : m;
         };
         f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
-        auto weight = [&](f32x2 y, int e) {  // two columns' weights as bf16
+        // Two columns' weights as bf16, which is what a product with bf16 values takes.  Their roundings, up to 2^-8 of a
+        // weight each and without a common sign, left the outputs of the measured prompts off by 1.4e-3 of their norm, less than
+        // the 1.7e-3 of a bf16 output's own rounding; l sums the weights before it.  A second bf16 part of each weight
+        // would take half as much again of the tensor pipe and 32 KB that the ring of keys and values fills.
+        auto weight = [&](f32x2 y, int e) {
           const f32x2 p2 = ex2_2(y);
           sum[e & 1] = add2(sum[e & 1], p2);
           float p0, p1;
@@ -705,8 +710,8 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         // The whole row in registers: with a cap for blocks that the whole warp sees, with a bias for blocks of which
         // its rows see what lies behind them, and with neither for any.  A cap comes from the polynomial as the scores are used
         // (straight; false, with nothing done, where products leave the part that it is good for or scores spread too
-        // far for the bound below), or else from the difference, in place.  4 x 16 x 4096 at d = 128 takes 386 us without
-        // a cap, 551 with the one and 816 with the other, against 1340 where a row is read in parts.
+        // far for the bound below), or else from the difference, in place.  2 x 16 x 8192 at d = 128 takes 387 us without
+        // a cap, 535 with the one and 826 with the other, against 1340 where a row is read in parts.
         auto row_at_once = [&](auto straight) {
           constexpr bool kPoly = CAP && decltype(straight)::value, kFar = CAP && !kPoly;
           constexpr int kAll = KB == 128 ? KB : 2;
