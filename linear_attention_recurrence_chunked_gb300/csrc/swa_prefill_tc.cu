@@ -301,11 +301,8 @@ struct Blocks {
     do ++j; while (j < j1 && !active(j));
     return j;
   }
-  // whether all rows of the tiles at work on block j see all of it
-  __device__ __forceinline__ bool whole(int j) const {
-    const int k0 = j * KB, k1 = k0 + KB;
-    return (!active(0, j) || (k0 >= f_lo[0] && k1 <= f_hi[0])) && (!active(1, j) || (k0 >= f_lo[1] && k1 <= f_hi[1]));
-  }
+  // whether tile t is at work on block j and some of its rows do not see all of it
+  __device__ __forceinline__ bool partial(int t, int j) const { return active(t, j) && (j * KB < f_lo[t] || j * KB + KB > f_hi[t]); }
 };
 
 // Where a part's output has four columns of a row of tile t: the lower half of the columns in the place of the
@@ -392,7 +389,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile uint32_t dead;
   // bad[t][n % 8] == n + 1: the n-th item at whose keys tile t is at work has values that are not finite in a block
-  // that is not seen as a whole.  Warp 10 is at most kSlots + 1 < 8 such items ahead of the rows: a product of the
+  // that the tile's rows do not all see as a whole.  Warp 10 is at most kSlots + 1 < 8 such items ahead of the rows: a product of the
   // next one waits for the rows to have read this one's output, and the ring holds kSlots blocks.  (Items that see
   // nothing pass without a wait, any number of them, and do not count.)
   __shared__ volatile uint32_t bad[2][8];
@@ -513,13 +510,15 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (!bl.whole(j)) {
+          const bool part0 = bl.partial(0, j), part1 = bl.partial(1, j);
+          if (part0 || part1) {
             __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll 4
             for (int e = lane; e < (int)(S::kBlk * KB * 8); e += 32) acc = add_zero_times(*reinterpret_cast<const uint4*>(v + e * 16), acc);
             if (__any_sync(kFullMask, __hisnan(acc.x) || __hisnan(acc.y)) && lane == 0) {
-              if (any0) bad[0][(n0 - 1) % 8] = n0;
-              if (any1) bad[1][(n1 - 1) % 8] = n1;
+              // (only of a tile that has yet to use the block: the other one's rows may or may not have looked by now)
+              if (part0) bad[0][(n0 - 1) % 8] = n0;
+              if (part1) bad[1][(n1 - 1) % 8] = n1;
             }
           }
           warp_arrive(smem_u32(&bar_vok[slot(iv)]));

@@ -256,3 +256,23 @@ def test_ssm_prefill_in_segments_joins_them_within_a_segments_roundings(B, N, C,
     first = np.full_like(y_ref, np.nan)
     first[:, :length] = y_ref[:, :length]
     ref.check(y, first, bound)
+
+
+@pytest.mark.parametrize("B,H,Hkv,Nq,Nk,d,window,q_pos0", [
+    (2, 4, 1, 253, 561, 72, 0, 272), (3, 10, 2, 237, 283, 24, 345, 25), (2, 15, 3, 246, 257, 24, 59, 2), (3, 3, 3, 1242, 1976, 72, 620, 109)])
+def test_swa_values_that_are_not_finite_give_the_same_bits_every_time(B, H, Hkv, Nq, Nk, d, window, q_pos0):
+    """Values behind the last query are not finite: they have the rows of the last queries' tile computed again, and no
+    other tile's, however far along those are when the values are found."""
+    dev = cuda_device()
+    q, k, v = swa_case(B, H, Hkv, Nq, Nk, d, BF, Nq)
+    k[:, :, q_pos0 + Nq:], v[:, :, q_pos0 + Nq:] = float("nan"), float("inf")
+    q, k, v = on(dev, q, k, v)
+    first = la.la_swa_prefill(q, k, v, window=window, q_pos0=q_pos0)
+    assert torch.isfinite(first.float()).all()
+    for _ in range(200):
+        assert torch.equal(la.la_swa_prefill(q, k, v, window=window, q_pos0=q_pos0), first)
+    # values that are finite change the last tile's rows by their weights' roundings alone, and no other row
+    clean = la.la_swa_prefill(q, k, torch.nan_to_num(v, 0, 0, 0), window=window, q_pos0=q_pos0)
+    kept = (Nq - 1) // 128 * 128
+    assert torch.equal(clean[:, :, :kept], first[:, :, :kept])
+    assert la.la_device_status() == la.LA_OK
