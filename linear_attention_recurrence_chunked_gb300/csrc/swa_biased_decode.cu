@@ -174,44 +174,43 @@ swa_biased_decode_mma_kernel(const SwaBiasedDecodeLaunch a) {
   __syncwarp();
   // Weights in two bf16 parts, the second one what the first leaves: a weight is off by 2^-17 of itself, where one part
   // would leave 2^-8, more than an fp32 output can hide.  Up to eight heads the second parts take the rows that have no
-  // head and no product is added; beyond, they are products of their own (256 x 64 heads over 4: 42.8 us, 41.3 with one
-  // part).
+  // head and no product is added; beyond, they are products of their own (256 x 64 heads over 4: 44 us, 41.3 with one
+  // part).  What second parts make of a value that is not finite is left out: the first ones' result stands.
+  auto products = [&](auto a) {  // a(kt): the weights of sixteen slots as an operand
 #pragma unroll
-  for (int kt = 0; kt < 2; ++kt) {
-    const int r = kt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
-    uint32_t w[4], rest[4];  // rows lane / 4 and that + 8 of the first eight slots, then of the others
-    auto split = [&](int i) {
-      const float w0 = x[2 * kt + i / 2][i % 2 * 2], w1 = x[2 * kt + i / 2][i % 2 * 2 + 1];
-      w[i] = tc::pack2_bf16(w0, w1);
-      rest[i] = tc::pack2_bf16(w0 - __uint_as_float(w[i] << 16), w1 - __uint_as_float(w[i] & 0xffff0000u));
-    };
-    split(0);
-    split(2);
-    if (spare) {
-      w[1] = rest[0];
-      w[3] = rest[2];
-    } else {
-      split(1);
-      split(3);
-    }
+    for (int kt = 0; kt < 2; ++kt) {
+      const int r = kt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+      const uint4 w = a(kt);
 #pragma unroll
-    for (int p = 0; p < kPairs; ++p) {
-      uint32_t b[4];
-      ldmatrix_trans(b, rbase + at(r, 2 * p + (lane >> 4)));
-      mma16816(o[2 * p], w[0], w[1], w[2], w[3], b[0], b[1]);
-      mma16816(o[2 * p + 1], w[0], w[1], w[2], w[3], b[2], b[3]);
-      if (!spare) {
-        mma16816(o[2 * p], rest[0], rest[1], rest[2], rest[3], b[0], b[1]);
-        mma16816(o[2 * p + 1], rest[0], rest[1], rest[2], rest[3], b[2], b[3]);
+      for (int p = 0; p < kPairs; ++p) {
+        uint32_t b[4];
+        ldmatrix_trans(b, rbase + at(r, 2 * p + (lane >> 4)));
+        mma16816(o[2 * p], w.x, w.y, w.z, w.w, b[0], b[1]);
+        mma16816(o[2 * p + 1], w.x, w.y, w.z, w.w, b[2], b[3]);
       }
     }
-  }
+  };
+  // rows of half h (0: lane / 4, 1: that + 8) of tile t: two slots' first parts, and what they leave
+  auto major = [&](int t, int h) { return tc::pack2_bf16(x[t][2 * h], x[t][2 * h + 1]); };
+  auto minor = [&](int t, int h) {
+    const uint32_t w = major(t, h);
+    return tc::pack2_bf16(x[t][2 * h] - __uint_as_float(w << 16), x[t][2 * h + 1] - __uint_as_float(w & 0xffff0000u));
+  };
   if (spare) {
+    products([&](int kt) { return make_uint4(major(2 * kt, 0), minor(2 * kt, 0), major(2 * kt + 1, 0), minor(2 * kt + 1, 0)); });
 #pragma unroll
-    for (int t = 0; t < 2 * kPairs; ++t) {
-      o[t][0] += o[t][2];
-      o[t][1] += o[t][3];
-    }
+    for (int t = 0; t < 2 * kPairs; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) o[t][e] += finite1(o[t][2 + e]) ? o[t][2 + e] : 0.f;
+  } else {
+    products([&](int kt) { return make_uint4(major(2 * kt, 0), major(2 * kt, 1), major(2 * kt + 1, 0), major(2 * kt + 1, 1)); });
+    float sum = 0.f;
+#pragma unroll
+    for (int t = 0; t < 2 * kPairs; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum = fmaf(0.f, o[t][e], sum);
+    if (__all_sync(kFullMask, sum == 0.f))
+      products([&](int kt) { return make_uint4(minor(2 * kt, 0), minor(2 * kt, 1), minor(2 * kt + 1, 0), minor(2 * kt + 1, 1)); });
   }
   // the new token into its slot, by the warp that used it from the arguments
   if (slot_new / kSlots == warp && lane < chunks) {

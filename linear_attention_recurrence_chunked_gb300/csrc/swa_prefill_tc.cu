@@ -389,9 +389,9 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile uint32_t dead;
   // bad[t][n % 8] == n + 1: the n-th item at whose keys tile t is at work has values that are not finite in a block
-  // that the tile's rows do not all see as a whole.  Warp 10 is at most kSlots + 1 < 8 such items ahead of the rows: a product of the
-  // next one waits for the rows to have read this one's output, and the ring holds kSlots blocks.  (Items that see
-  // nothing pass without a wait, any number of them, and do not count.)
+  // that the tile's rows do not all see as a whole.  Warp 10 is at most kSlots + 1 < 8 such items ahead of the rows: a
+  // product of the next one waits for the rows to have read this one's output, and the ring holds kSlots blocks.  (Items
+  // that see nothing pass without a wait, any number of them, and do not count.)
   __shared__ volatile uint32_t bad[2][8];
   // with parts: a row's m + log2 l (no keys: -infinity), and whether a tile's rows have to be computed again
   __shared__ float lse[JOIN ? 2 * kRows : 1];

@@ -276,3 +276,19 @@ def test_swa_values_that_are_not_finite_give_the_same_bits_every_time(B, H, Hkv,
     kept = (Nq - 1) // 128 * 128
     assert torch.equal(clean[:, :, :kept], first[:, :, :kept])
     assert la.la_device_status() == la.LA_OK
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("H,Hkv", [(4, 4), (16, 2), (12, 1)])
+def test_swa_step_of_infinite_values(H, Hkv, dtype):
+    """A seen value of infinity with the only weight is the output, as in the plain step; its neighbours stay finite."""
+    dev = cuda_device()
+    g = gen(H)
+    q, k, v = (randn(g, 2, n, 64, dtype=dtype).to(dev) for n in (H, Hkv, Hkv))
+    kc, vc = (randn(g, 2, Hkv, 40, 64, dtype=dtype).to(dev) for _ in range(2))
+    v[0, :, 5], v[1, :, 7] = float("inf"), -float("inf")
+    pos = torch.tensor([0, 100], device=dev)  # alone, and beside a full ring
+    out = la.la_swa_biased_decode_step(q, k, v, kc, vc, pos, out_dtype=FP)
+    assert (out[0, :, 5] == float("inf")).all() and (out[1, :, 7] == -float("inf")).all()
+    out[0, :, 5], out[1, :, 7] = 0, 0
+    assert torch.isfinite(out).all()
