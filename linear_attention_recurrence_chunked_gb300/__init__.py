@@ -703,7 +703,8 @@ def _call(fn_name, index, args, *more):
 
 def _on_stream(fn):
     """With `stream` (a torch stream or a cudaStream_t) the whole call runs on it: the kernels, and the memory that
-    outputs and workspaces take."""
+    outputs and workspaces take.  Tensors of the caller's stream stay allocated until that work is done, outputs until
+    the caller's stream has used them."""
     first = fn.__code__.co_varnames[0]
 
     @functools.wraps(fn)
@@ -719,8 +720,17 @@ def _on_stream(fn):
             stream = torch.cuda.default_stream(x.device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=x.device)
         if stream.device != x.device:
             raise ValueError(f"the stream is of {stream.device}, the tensors of {x.device}")
+        own = torch.cuda.current_stream(x.device)
         with torch.cuda.stream(stream):
-            return fn(*args, **kwargs)
+            out = fn(*args, **kwargs)
+        if own != stream:
+            taken = [t for t in (*args, *kwargs.values()) if isinstance(t, torch.Tensor)]
+            for t in taken:
+                t.record_stream(stream)
+            for t in out if isinstance(out, tuple) else (out,):
+                if not any(t is i for i in taken):
+                    t.record_stream(own)
+        return out
     return call
 
 

@@ -292,3 +292,38 @@ def test_swa_step_of_infinite_values(H, Hkv, dtype):
     assert (out[0, :, 5] == float("inf")).all() and (out[1, :, 7] == -float("inf")).all()
     out[0, :, 5], out[1, :, 7] = 0, 0
     assert torch.isfinite(out).all()
+
+
+def test_tensors_freed_behind_a_call_on_another_stream():
+    """Inputs that are gone when a call on another stream gets to them, and outputs that are while their reader has not:
+    neither's memory goes to the next tensor before that."""
+    dev = cuda_device()
+    N, C = 700, 256
+    x, w = randn(gen(1), 2, N, C).to(dev), randn(gen(2), C, 4).to(dev)
+    q, k, v = on(dev, *swa_case(1, 2, 1, 300, 300, 64, BF, 9))
+    want = la.la_conv_prefill(x, w)[0], la.la_swa_prefill(q, k, v)
+    side, big = torch.cuda.Stream(dev), torch.randn(8192, 8192, device=dev)
+    torch.cuda.synchronize()
+
+    def keep_busy():
+        busy = big
+        for _ in range(6):
+            busy = busy @ big
+
+    with torch.cuda.stream(side):
+        keep_busy()
+    got = [la.la_conv_prefill(x.clone(), w.clone(), stream=side)[0], la.la_swa_prefill(q.clone(), k=k.clone(), v=v.clone(), stream=side)]
+    spoil = [torch.full_like(t, float("nan")) for t in (x, w, q, k, v)]  # where the copies were, were they free
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(spoil) == 5
+    # outputs: read on this stream, behind long work, and dropped
+    side.wait_stream(torch.cuda.current_stream())
+    y = la.la_conv_prefill(x, w, stream=side)[0]
+    torch.cuda.current_stream().wait_stream(side)
+    keep_busy()
+    copy = y * 1
+    del y
+    with torch.cuda.stream(side):
+        spoil = [torch.full_like(x, float("nan")) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want[0])
