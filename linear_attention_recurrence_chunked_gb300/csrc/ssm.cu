@@ -518,6 +518,9 @@ ssm_decode_kernel(const SsmLaunch a, bool a_vec, bool bc_vec) {
 #pragma unroll
     for (int k = 0; k < kK; ++k) A2[k] = k < count ? log2_rate(a.A[cc * a.n + s_lo + k]) : 0.f;
   }
+  float slowest = INFINITY;  // of the lane's states, which share a centre
+#pragma unroll
+  for (int k = 0; k < kK; ++k) slowest = k < count ? fminf(slowest, fabsf(A2[k])) : slowest;
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
     const float x = dt_own[i] + bias;
@@ -533,11 +536,11 @@ ssm_decode_kernel(const SsmLaunch a, bool a_vec, bool bc_vec) {
     float Bk[kK], Ck[kK];
     Br[q].unpack(Bk);
     Cr[q].unpack(Ck);
-    const float dtu = dt * u;
+    const float dtu = dt * u, centre = centre_of(dt * slowest);
     acc[q] = 0.f;
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
-      h[q][k] = fmaf(ex2(fmaf(dt, A2[k], centre_of(dt * A2[k]))), h[q][k], dtu * Bk[k]);
+      h[q][k] = fmaf(ex2(fmaf(dt, A2[k], centre)), h[q][k], dtu * Bk[k]);
       acc[q] = fmaf(Ck[k], h[q][k], acc[q]);
     }
     if (on && s0 + q < a.B) {
