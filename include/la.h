@@ -569,13 +569,137 @@ typedef struct la_swa_biased_decode_args {
 } la_swa_biased_decode_args;
 la_status la_swa_biased_decode_step(const la_swa_biased_decode_args* args, void* stream);
 
+/* Norms and position rotation of queries and keys, for each head, in one pass over them:
+ *   x <- w x / sqrt(mean_i x_i^2 + eps)    LA_NORM_RMS
+ *   x <- w x / sqrt(sum_i x_i^2 + eps)     LA_NORM_L2 (unit length: what la_gdn_prefill asks of its keys)
+ *   x <- x                                 LA_NORM_NONE (no weights)
+ * then each pair (a, b) of the first `rot` elements becomes (a c - b s, b c + a s), with
+ * c, s = cos[p, i], sin[p, i] of the token's position p; pair i is (i, i + rot / 2), or
+ * (2 i, 2 i + 1) where `interleaved`.
+ *   q, q_out : [B, H, N, d] views;  k, k_out : [B, H_kv, N, d] views (H_kv = 0: none).  A step's
+ *            tokens are B sequences with N = 1.  An output may be its input (same address and
+ *            strides, one type), and must not overlap it otherwise.  d a multiple of 8 in [8, 256].
+ *   q_weight, k_weight : [d] w_dtype, 16-byte aligned, or NULL (ones)
+ *   eps    : > 0 with a norm
+ *   rot    : a multiple of 16 in [0, d]; 0: no rotation
+ *   cos, sin : [positions, rot / 2] fp32 contiguous, 16-byte aligned
+ *   pos    : NULL (token n stands at n), [B] int64 (token n at pos[b] + n), or with `pos_each`
+ *            [B, N] int64.  A token that stands outside the tables is skipped as padding is, and
+ *            sets the device status word (LA_ERR_INVALID_ARGUMENT).
+ *   lens, fill : as above (LA_FILL_ROWS)
+ * fp32 arithmetic, one rounding to out_dtype. */
+#define LA_NORM_NONE 0
+#define LA_NORM_RMS 1
+#define LA_NORM_L2 2
+typedef struct la_qk_norm_rope_args {
+  int64_t B, H, H_kv, N, d, rot, positions;
+  la_dtype in_dtype, out_dtype, w_dtype;
+  int32_t norm;
+  la_tensor q, k, q_out, k_out;
+  const void* q_weight;
+  const void* k_weight;
+  const float* cos;
+  const float* sin;
+  const int64_t* pos;
+  const int64_t* lens;
+  float eps;
+  int32_t interleaved, pos_each, fill;
+} la_qk_norm_rope_args;
+la_status la_qk_norm_rope(const la_qk_norm_rope_args* args, void* stream);
+
+/* Paged caches of keys and values, for attention layers without a window or with one beyond the
+ * rings' 256 tokens.  A pool holds `pages` pages of `page` tokens of every key head; the table
+ * [B, width] int32 names the page of tokens i page .. (i + 1) page - 1 of a sequence in column i.
+ * Columns that no token of a call needs are not read.  A needed entry outside [0, pages) sets the
+ * device status word (LA_ERR_INVALID_ARGUMENT): its tokens are not stored, not read and not seen.
+ *   page   : a multiple of 16 in [16, 4096];  width page < 2^31 - 8192
+ *   bits 0 : k_pages, v_pages [pages, H_kv, page, d] in the inputs' type, d a multiple of 8 in [8, 128]
+ *   bits 4 : bf16 inputs, d 64 or 128: [pages, H_kv, page, 9 d / 16] bytes.  64 neighbouring elements
+ *            of a row share a bf16 offset, the least of them, and a bf16 scale, a fifteenth of their
+ *            spread ((max - min) / 15 rounded); an element is offset + scale code with
+ *            code = (element - offset) / scale rounded to even, at most 15.  A group whose spread
+ *            is not finite reads back as NaN.  A page of one head holds the codes of its tokens
+ *            (d / 2 bytes each), then their scales and offsets (4 bytes a group, the scale in the
+ *            lower half).  A token's 32-bit words take eight elements each, least first, of its
+ *            groups in turn: with d = 128 word 2 e + g holds elements 64 g + 8 e .. 64 g + 8 e + 7.
+ * Pools contiguous and 16-byte aligned, table 4-byte aligned.
+ *
+ * la_paged_append stores tokens i < N (lens[b]) of k, v [B, H_kv, N, d] views as tokens seen[b] + i
+ * of their sequences.  Keys are rotated on the way as la_qk_norm_rope does at those positions (rot 0:
+ * stored as they are): in fp32 with one rounding, in front of 4 bits so closely that the key is the
+ * exact rotation rounded to fp32 and then bf16.  seen: [B] int64, not advanced.  Tokens
+ * behind the table's last column or outside cos and sin are skipped and set the device status word.  Two
+ * tokens of a call must not go to one place. */
+typedef struct la_paged_append_args {
+  int64_t B, H_kv, N, d, rot, positions, page, pages, width;
+  la_dtype in_dtype;
+  int32_t bits;
+  la_tensor k, v;
+  void* k_pages;
+  void* v_pages;
+  const int32_t* table;
+  const int64_t* seen;
+  const float* cos;
+  const float* sin;
+  const int64_t* lens;
+  int32_t interleaved;
+} la_paged_append_args;
+la_status la_paged_append(const la_paged_append_args* args, void* stream);
+
+/* The first lens[b] tokens (0 <= lens[b] <= N; NULL: N) of each sequence of a paged cache as rows of
+ * k, v [B, H_kv, N, d] views of out_dtype, as la_swa_prefill reads them where a prompt goes on from
+ * earlier calls.  in_dtype is the type of the pages (bf16 for bits 4).  4-bit elements are rounded to
+ * fp32 and then to out_dtype.  Rows behind lens[b], and of tokens whose page is out of range or behind the
+ * table, are left as they were (zeros with LA_FILL_ROWS). */
+typedef struct la_paged_read_args {
+  int64_t B, H_kv, N, d, page, pages, width;
+  la_dtype in_dtype, out_dtype;
+  int32_t bits, fill;
+  la_tensor k, v;
+  const void* k_pages;
+  const void* v_pages;
+  const int32_t* table;
+  const int64_t* lens;
+} la_paged_read_args;
+la_status la_paged_read(const la_paged_read_args* args, void* stream);
+
+/* Softmax attention of one token of each of S sequences over a paged cache that holds it already:
+ * with n = lens[s] tokens the query stands at n - 1 and
+ *   s_j = cap tanh(scale q.k_j / cap) - slope_h (n - 1 - j),   o = sum_j softmax_j(s_j) v_j,
+ *   max(0, n - window) <= j < n   (window 0: every token)
+ *   q, out : [S, H, d] views of in_dtype and out_dtype (stride_t ignored); query head h reads key
+ *            head h / (H / H_kv); H % H_kv == 0, H / H_kv <= 16
+ *   lens   : [S] int64; 0 gives zeros; a length below 0 or beyond the table leaves the sequence's
+ *            rows as they were and sets the device status word
+ *   slopes, softcap, scale : as in la_swa_prefill
+ * bf16 (bits 0 and 4): products on the tensor cores with fp32 sums and statistics, the softmax
+ * weights in two bf16 parts (2^-17 of a weight).  fp32: fp32 throughout.  Few or long sequences are
+ * split along their tokens; the parts meet in the workspace, which
+ * la_paged_decode_workspace_size sizes from the other arguments (0 where nothing is split; 16-byte
+ * aligned, dead when the call's work has finished).  A smaller one fails with LA_ERR_WORKSPACE.
+ * Launched as a programmatic dependent, as la_decode_step. */
+typedef struct la_paged_decode_args {
+  int64_t S, H, H_kv, d, window, page, pages, width;
+  la_dtype in_dtype, out_dtype;
+  int32_t bits;
+  float scale, softcap;
+  la_tensor q, out;
+  const void* k_pages;
+  const void* v_pages;
+  const int32_t* table;
+  const int64_t* lens;
+  const float* slopes;
+} la_paged_decode_args;
+size_t la_paged_decode_workspace_size(const la_paged_decode_args* args);
+la_status la_paged_decode_step(const la_paged_decode_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then reports (and clears when `clear` != 0) the
  * device-side status word: LA_ERR_TIMEOUT when a bounded wait expired,
  * LA_ERR_INVALID_ARGUMENT when la_state_gather skipped an out-of-range
  * index, la_swa_decode_step or la_swa_biased_decode_step met a negative
- * position, a prefill a sequence length out of range or la_notebank_address
- * a bad span or coordinate, else LA_OK; LA_ERR_CUDA if the synchronisation
- * failed. */
+ * position, a prefill a sequence length out of range, la_notebank_address
+ * a bad span or coordinate or a paged cache's call a bad page, length or
+ * position, else LA_OK; LA_ERR_CUDA if the synchronisation failed. */
 la_status la_device_status(void* stream, int clear);
 
 /* Self-test of the bounded-wait error path (infrastructure; the pages have no

@@ -75,7 +75,8 @@ EXPORTED = ("la_based_prefill", "la_gdn_prefill", "la_gated_prefill", "la_decode
             "la_gdn_prefill_workspace_size", "la_gdn_prefill_workspace_size_min", "la_gdn_prefill_noalloc", "la_device_status",
             "la_state_rescale", "la_state_gather", "la_swa_decode_step", "la_notebank_scores", "la_notebank_address",
             "la_notebank_route", "la_conv_prefill", "la_conv_decode_step", "la_ssm_prefill_workspace_size", "la_ssm_prefill",
-            "la_ssm_decode_step", "la_swa_prefill", "la_swa_biased_decode_step", "la_selftest_bounded_wait", "la_status_string", "la_abi_version",
+            "la_ssm_decode_step", "la_swa_prefill", "la_swa_biased_decode_step", "la_qk_norm_rope", "la_paged_append",
+            "la_paged_read", "la_paged_decode_workspace_size", "la_paged_decode_step", "la_selftest_bounded_wait", "la_status_string", "la_abi_version",
             "la_last_cuda_error", "la_cuda_error_name")
 
 
@@ -154,6 +155,38 @@ class SwaBiasedDecodeArgs(ctypes.Structure):
     _fields_ = [("base", SwaDecodeArgs), ("H_kv", _i64), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p)]
 
 
+class QkNormRopeArgs(ctypes.Structure):
+    _fields_ = [("B", _i64), ("H", _i64), ("H_kv", _i64), ("N", _i64), ("d", _i64), ("rot", _i64), ("positions", _i64),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int), ("norm", ctypes.c_int32),
+                ("q", LATensor), ("k", LATensor), ("q_out", LATensor), ("k_out", LATensor),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("eps", ctypes.c_float), ("interleaved", ctypes.c_int32),
+                ("pos_each", ctypes.c_int32), ("fill", ctypes.c_int32)]
+
+
+class PagedAppendArgs(ctypes.Structure):
+    _fields_ = [("B", _i64), ("H_kv", _i64), ("N", _i64), ("d", _i64), ("rot", _i64), ("positions", _i64), ("page", _i64),
+                ("pages", _i64), ("width", _i64), ("in_dtype", ctypes.c_int), ("bits", ctypes.c_int32),
+                ("k", LATensor), ("v", LATensor), ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("seen", ctypes.c_void_p), ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("interleaved", ctypes.c_int32)]
+
+
+class PagedReadArgs(ctypes.Structure):
+    _fields_ = [("B", _i64), ("H_kv", _i64), ("N", _i64), ("d", _i64), ("page", _i64), ("pages", _i64), ("width", _i64),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("bits", ctypes.c_int32), ("fill", ctypes.c_int32),
+                ("k", LATensor), ("v", LATensor), ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
+
+
+class PagedDecodeArgs(ctypes.Structure):
+    _fields_ = [("S", _i64), ("H", _i64), ("H_kv", _i64), ("d", _i64), ("window", _i64), ("page", _i64), ("pages", _i64),
+                ("width", _i64), ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("bits", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("q", LATensor), ("out", LATensor),
+                ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("slopes", ctypes.c_void_p)]
+
+
 class LAError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -220,6 +253,16 @@ def load_library(path: str | None = None):
     lib.la_swa_prefill.argtypes = [ctypes.POINTER(SwaPrefillArgs), vp]
     lib.la_swa_biased_decode_step.restype = ctypes.c_int
     lib.la_swa_biased_decode_step.argtypes = [ctypes.POINTER(SwaBiasedDecodeArgs), vp]
+    lib.la_qk_norm_rope.restype = ctypes.c_int
+    lib.la_qk_norm_rope.argtypes = [ctypes.POINTER(QkNormRopeArgs), vp]
+    lib.la_paged_append.restype = ctypes.c_int
+    lib.la_paged_append.argtypes = [ctypes.POINTER(PagedAppendArgs), vp]
+    lib.la_paged_read.restype = ctypes.c_int
+    lib.la_paged_read.argtypes = [ctypes.POINTER(PagedReadArgs), vp]
+    lib.la_paged_decode_workspace_size.restype = ctypes.c_size_t
+    lib.la_paged_decode_workspace_size.argtypes = [ctypes.POINTER(PagedDecodeArgs)]
+    lib.la_paged_decode_step.restype = ctypes.c_int
+    lib.la_paged_decode_step.argtypes = [ctypes.POINTER(PagedDecodeArgs), vp, ctypes.c_size_t, vp]
     lib.la_state_rescale.restype = ctypes.c_int
     lib.la_state_rescale.argtypes = [vp, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_float, vp]
     lib.la_state_gather.restype = ctypes.c_int
@@ -680,6 +723,10 @@ _SSM_PREFILL = struct.Struct("<5q2i24q6q2i")
 _SSM_DECODE = struct.Struct("<4q2i24q5qi4x")
 _SWA_PREFILL = struct.Struct("<7q2i16q2f3q1q3qi4x")
 _SWA_BIASED_DECODE = struct.Struct("<4q2i7qf4xqf4xq")
+_QK_NORM_ROPE = struct.Struct("<7q4i16q6qf3i")
+_PAGED_APPEND = struct.Struct("<9q2i8q7qi4x")
+_PAGED_READ = struct.Struct("<7q4i8q4q")
+_PAGED_DECODE = struct.Struct("<8q3i2f4x8q5q")
 _packed = {}
 
 
@@ -728,7 +775,7 @@ def _on_stream(fn):
             for t in taken:
                 t.record_stream(stream)
             for t in out if isinstance(out, tuple) else (out,):
-                if not any(t is i for i in taken):
+                if t is not None and not any(t is i for i in taken):
                     t.record_stream(own)
         return out
     return call
@@ -798,13 +845,18 @@ def _ssm_prefill_args(u, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus, h_i
                              bool(delta_softplus), fill)
 
 
-def _ssm_workspace_size(args) -> int:
-    f = _packed.get("la_ssm_prefill_workspace_size")
+def _size(fn_name, args) -> int:
+    """A workspace query of packed arguments."""
+    f = _packed.get(fn_name)
     if f is None or f[0] is not _lib:
-        fn = load_library()["la_ssm_prefill_workspace_size"]
+        fn = load_library()[fn_name]
         fn.restype, fn.argtypes = ctypes.c_size_t, [ctypes.c_char_p]
-        f = _packed["la_ssm_prefill_workspace_size"] = (_lib, fn)
+        f = _packed[fn_name] = (_lib, fn)
     return f[1](args)
+
+
+def _ssm_workspace_size(args) -> int:
+    return _size("la_ssm_prefill_workspace_size", args)
 
 
 def la_ssm_prefill_workspace_size(u, delta, A, Bm, Cm) -> int:
@@ -936,6 +988,182 @@ def la_swa_biased_decode_step(q, k, v, k_cache, v_cache, pos, softcap: float = 0
           _SWA_BIASED_DECODE.pack(S, H, d, window, _code(qt), _code(out.dtype), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                   k_cache.data_ptr(), v_cache.data_ptr(), pos.data_ptr(), out.data_ptr(),
                                   scale if scale is not None else d ** -0.5, Hkv, softcap, _address(slopes)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# full attention layers: queries' and keys' norms with the position rotation, paged caches
+
+
+_NORMS = {None: 0, "rms": 1, "l2": 2}
+
+
+def _tokens(t):
+    """[B,H,N,d] tensor, or a step's [S,H,d] -> the words of a view."""
+    if t is None:
+        return 0, 0, 0, 0
+    if t.dim() == 4:
+        return _heads(t)
+    (S, H, _), (sb, sh, _) = t.shape, t.stride()
+    return t.data_ptr(), sb if S > 1 else 0, sh if H > 1 else 0, 0
+
+
+def _tables(index, cos, sin, d):
+    """Rotation tables: (rotated elements, rows)."""
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    if cos is None:
+        return 0, 0
+    if cos.dim() != 2 or 2 * cos.shape[1] > d:
+        raise ValueError(f"cos and sin must be [positions, rot / 2] with rot up to {d}")
+    _check(index, ("cos", cos, cos.shape, torch.float32, True), ("sin", sin, cos.shape, torch.float32, True))
+    return 2 * cos.shape[1], cos.shape[0]
+
+
+@_on_stream
+def la_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, norm: str | None = "rms", eps: float = 1e-6, cos=None,
+                    sin=None, pos=None, interleaved: bool = False, lens=None, q_out=None, k_out=None, out_dtype=None,
+                    *, stream=None):
+    """Norms of queries and keys for each head, and the position rotation, in one pass.  Returns (q_out, k_out).
+
+        x <- w x / sqrt(mean(x^2) + eps)   (norm "rms";  "l2": the sum in the mean's place;  None: x)
+        pairs of the first rot elements <- (a c - b s, b c + a s) of the token's row of cos and sin
+
+    q: [B,H,N,d], k: [B,H_kv,N,d] or None, or a step's [S,H,d], [S,H_kv,d] (fp32 or bf16, d a multiple of 8 up to 256);
+    q_weight, k_weight: [d] or None, both fp32 or both bf16; cos, sin: fp32 [positions, rot / 2] or None, rot a multiple
+    of 16; pairs are (i, i + rot / 2), or neighbours if interleaved; pos: int64 [B], the first token's position (None: 0),
+    or [B,N]; lens as in la_conv_prefill.  An output may be its input."""
+    step = q.dim() == 3
+    if q.dim() not in (3, 4) or (k is not None and k.dim() != q.dim()):
+        raise ValueError("q and k must be [B,H,N,d], or [S,H,d] of single tokens")
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be 'rms', 'l2' or None, got {norm!r}")
+    index, qt = q.get_device(), q.dtype
+    B, H, d = q.shape[0], q.shape[1], q.shape[-1]
+    N, Hkv = 1 if step else q.shape[2], 0 if k is None else k.shape[1]
+    keys = None if k is None else ((B, Hkv, d) if step else (B, Hkv, N, d))
+    rot, positions = _tables(index, cos, sin, d)
+    each = pos is not None and pos.dim() == 2
+    made = [q_out is None, k is not None and k_out is None]
+    if made[0]:
+        q_out = torch.empty_like(q, dtype=out_dtype or qt, memory_format=torch.contiguous_format)
+    if made[1]:
+        k_out = torch.empty_like(k, dtype=q_out.dtype, memory_format=torch.contiguous_format)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    if lens is not None and made[0] != made[1] and k is not None:
+        raise ValueError("with lens, q_out and k_out are both given or both made here")
+    wt = q_weight.dtype if q_weight is not None else k_weight.dtype if k_weight is not None else torch.float32
+    _check(index, ("q", q, q.shape, qt, False), ("k", k, keys, qt, False), ("q_out", q_out, q.shape, q_out.dtype, False),
+           ("k_out", k_out, keys, q_out.dtype, False), ("q_weight", q_weight, (d,), wt, True),
+           ("k_weight", k_weight, (d,), wt, True), ("pos", pos, (B, N) if each else (B,), torch.int64, True),
+           ("lens", lens, (B,), torch.int64, True))
+    _call("la_qk_norm_rope", index,
+          _QK_NORM_ROPE.pack(B, H, Hkv, N, d, rot, positions, _code(qt), _code(q_out.dtype), _code(wt), _NORMS[norm],
+                             *_tokens(q), *_tokens(k), *_tokens(q_out), *_tokens(k_out), _address(q_weight),
+                             _address(k_weight), _address(cos), _address(sin), _address(pos), _address(lens), eps,
+                             bool(interleaved), each, _FILL_ROWS if made[0] else 0))
+    return q_out, k_out
+
+
+def _pool(index, k_pages, v_pages, table, B, dtype):
+    """A paged cache's sizes: (H_kv, d, page, pages, width, bits)."""
+    if k_pages.dim() != 4 or table.dim() != 2:
+        raise ValueError("k_pages and v_pages must be [pages,H_kv,page,d] (4 bits: uint8 [pages,H_kv,page,9 d / 16]) and table [B,width]")
+    pages, Hkv, page, row = shape = tuple(k_pages.shape)
+    four = k_pages.dtype is torch.uint8
+    if four and row not in (36, 72):
+        raise ValueError(f"4-bit rows take 36 bytes (d = 64) or 72 (d = 128), got {row}")
+    kind = torch.uint8 if four else dtype
+    _check(index, ("k_pages", k_pages, shape, kind, True), ("v_pages", v_pages, shape, kind, True),
+           ("table", table, (B, table.shape[1]), torch.int32, True))
+    return Hkv, row * 16 // 9 if four else row, page, pages, table.shape[1], 4 if four else 0
+
+
+@_on_stream
+def la_paged_append(k, v, k_pages, v_pages, table, seen, cos=None, sin=None, interleaved: bool = False, lens=None,
+                    *, stream=None):
+    """Keys and values of new tokens into a paged cache, the keys rotated on the way.  Returns (k_pages, v_pages).
+
+    k, v: [B,H_kv,N,d], or a step's [S,H_kv,d] (fp32 or bf16); k_pages, v_pages: [pages,H_kv,page,d] in their type, or
+    for 4 bits (bf16 k, v; d 64 or 128) uint8 [pages,H_kv,page,9 d / 16]; table: int32 [B,width], the page of tokens i page
+    .. (i + 1) page - 1 of a sequence in column i; seen: int64 [B], tokens in the cache before (not advanced here): token n
+    becomes token seen[b] + n; cos, sin, interleaved as in la_qk_norm_rope; lens: None or int64 [B], new tokens of each
+    sequence of a padded batch."""
+    if k.dim() not in (3, 4) or v.dim() != k.dim():
+        raise ValueError("k and v must be [B,H_kv,N,d], or [S,H_kv,d] of single tokens")
+    index, kt = k.get_device(), k.dtype
+    B, N = k.shape[0], 1 if k.dim() == 3 else k.shape[2]
+    Hkv, d, page, pages, width, bits = _pool(index, k_pages, v_pages, table, B, kt)
+    rows = (B, Hkv, d) if k.dim() == 3 else (B, Hkv, N, d)
+    rot, positions = _tables(index, cos, sin, d)
+    _check(index, ("k", k, rows, kt, False), ("v", v, rows, kt, False), ("seen", seen, (B,), torch.int64, True),
+           ("lens", lens, (B,), torch.int64, True))
+    _call("la_paged_append", index,
+          _PAGED_APPEND.pack(B, Hkv, N, d, rot, positions, page, pages, width, _code(kt), bits, *_tokens(k), *_tokens(v),
+                             k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), seen.data_ptr(), _address(cos),
+                             _address(sin), _address(lens), bool(interleaved)))
+    return k_pages, v_pages
+
+
+@_on_stream
+def la_paged_read(k_pages, v_pages, table, lens, N: int, k=None, v=None, out_dtype=None, *, stream=None):
+    """The first lens[b] tokens of each sequence of a paged cache as rows: k, v [B,H_kv,N,d], what la_swa_prefill takes
+    where a prompt goes on from earlier calls.  lens: int64 [B] up to N, or None (N); rows behind it stay as they were
+    (zeros in k, v made here).  4-bit caches give bf16 by default.  Returns (k, v)."""
+    if (k is None) != (v is None):
+        raise ValueError("k and v are both given or both made here")
+    index, four = k_pages.get_device(), k_pages.dtype is torch.uint8
+    kt, B = torch.bfloat16 if four else k_pages.dtype, table.shape[0]
+    Hkv, d, page, pages, width, bits = _pool(index, k_pages, v_pages, table, B, kt)
+    rows = (B, Hkv, int(N), d)
+    fill = _FILL_ROWS if k is None else 0
+    if k is None:
+        k, v = (torch.empty(rows, dtype=out_dtype or kt, device=k_pages.device) for _ in range(2))
+    _check(index, ("k", k, rows, k.dtype, False), ("v", v, rows, k.dtype, False), ("lens", lens, (B,), torch.int64, True))
+    _call("la_paged_read", index,
+          _PAGED_READ.pack(B, Hkv, int(N), d, page, pages, width, _code(kt), _code(k.dtype), bits, fill, *_heads(k), *_heads(v),
+                           k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), _address(lens)))
+    return k, v
+
+
+def _paged_decode_args(q, k_pages, v_pages, table, lens, window, scale, softcap, slopes, out):
+    S, H, d = q.shape
+    Hkv, dk, page, pages, width, bits = _pool(q.get_device(), k_pages, v_pages, table, S, q.dtype)
+    if dk != d:
+        raise ValueError(f"the pages hold rows of {dk} elements, q of {d}")
+    return _PAGED_DECODE.pack(S, H, Hkv, d, int(window), page, pages, width, _code(q.dtype), _code(out.dtype), bits,
+                              scale if scale is not None else d ** -0.5, softcap, *_tokens(q), *_tokens(out),
+                              k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), _address(lens), _address(slopes))
+
+
+def la_paged_decode_workspace_size(q, k_pages, v_pages, table, window: int = 0) -> int:
+    """Bytes of workspace la_paged_decode_step takes for tensors of these shapes (it does not depend on the lengths)."""
+    return _size("la_paged_decode_workspace_size", _paged_decode_args(q, k_pages, v_pages, table, None, window, None, 0.0, None, q))
+
+
+@_on_stream
+def la_paged_decode_step(q, k_pages, v_pages, table, lens, window: int = 0, scale: float | None = None,
+                         softcap: float = 0.0, slopes=None, out=None, out_dtype=None, workspace=None, *, stream=None):
+    """Softmax attention of one token of each sequence over a paged cache that holds it already.  Returns out [S,H,d].
+
+    q: [S,H,d] (fp32 or bf16, H a multiple of H_kv up to 16 H_kv); k_pages, v_pages, table as in la_paged_append; lens:
+    int64 [S], tokens in the cache (0: zeros); the query stands at lens - 1 and sees the last `window` tokens (0: all);
+    scale, softcap, slopes as in la_swa_prefill; workspace: uint8 device tensor of at least
+    la_paged_decode_workspace_size bytes, allocated here by default."""
+    if q.dim() != 3:
+        raise ValueError("q must be [S,H,d]")
+    index, qt = q.get_device(), q.dtype
+    S, H, d = heads = tuple(q.shape)
+    if out is None:
+        out = torch.empty(heads, dtype=out_dtype or qt, device=q.device)
+    _check(index, ("q", q, heads, qt, False), ("lens", lens, (S,), torch.int64, True), ("slopes", slopes, (H,), torch.float32, True),
+           ("out", out, heads, out.dtype, False))
+    a = _paged_decode_args(q, k_pages, v_pages, table, lens, window, scale, softcap, slopes, out)
+    ws, ws_bytes = _workspace(_size("la_paged_decode_workspace_size", a), workspace, q.device)
+    if workspace is not None and workspace.get_device() != index:
+        raise ValueError("workspace must live on the device of the inputs")
+    _call("la_paged_decode_step", index, a, ws.data_ptr() if isinstance(ws, torch.Tensor) else ws, ws_bytes)
     return out
 
 

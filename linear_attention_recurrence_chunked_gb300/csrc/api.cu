@@ -669,6 +669,177 @@ la_status la_swa_biased_decode_step(const la_swa_biased_decode_args* args, void*
   return from_cuda(la::launch_swa_biased_decode(L, static_cast<cudaStream_t>(stream)));
 }
 
+// ---- queries' and keys' norms, paged caches
+
+extern "C++" {
+namespace {
+
+// Rotation tables of `positions` rows for the first `rot` of d elements
+bool valid_tables(const float* cos, const float* sin, int64_t rot, int64_t positions) {
+  return rot == 0 || (cos && sin && aligned16(cos) && aligned16(sin) && positions >= 0 && positions <= kMaxDim);
+}
+
+template <typename Args>
+la_status check_pages(const Args* a, int64_t B) {
+  if (!valid_size(a->H_kv) || !valid_size(a->pages) || !valid_size(a->width) || !valid_dtype(a->in_dtype) || (a->bits != 0 && a->bits != 4))
+    return LA_ERR_INVALID_ARGUMENT;
+  if (a->bits == 4 ? a->in_dtype != LA_DTYPE_BF16 || (a->d != 64 && a->d != 128) : a->d < 8 || a->d > 128 || a->d % 8 != 0) return LA_ERR_UNSUPPORTED;
+  if (a->page < 16 || a->page > 4096 || a->page % 16 != 0 || a->pages > INT32_MAX) return LA_ERR_UNSUPPORTED;
+  if (!within(INT32_MAX - 8192, {a->width, a->page}) || !within(kMaxElems, {a->pages, a->H_kv, a->page, a->d}) ||
+      !within(kMaxElems, {B, a->width}))
+    return LA_ERR_UNSUPPORTED;
+  return LA_OK;
+}
+
+template <typename Args>
+bool valid_pools(const Args* a, int64_t B) {
+  if (a->pages > 0 && a->H_kv > 0 && (!a->k_pages || !a->v_pages)) return false;
+  return aligned16(a->k_pages) && aligned16(a->v_pages) && aligned4(a->table) && (a->table || B == 0 || a->width == 0);
+}
+
+template <typename Args>
+la::PagedCache cache_of(const Args* a, unsigned* status) {
+  la::PagedCache c{};
+  c.Hkv = a->H_kv; c.pages = a->pages; c.width = a->width; c.d = (int)a->d; c.page = (int)a->page;
+  c.bf16 = a->in_dtype == LA_DTYPE_BF16; c.four = a->bits == 4;
+  c.k = const_cast<void*>(static_cast<const void*>(a->k_pages)); c.v = const_cast<void*>(static_cast<const void*>(a->v_pages));
+  c.table = a->table; c.status = status;
+  return c;
+}
+
+bool same_rows(const la_tensor& x, const la_tensor& y) {
+  return x.stride_b == y.stride_b && x.stride_h == y.stride_h && x.stride_t == y.stride_t;
+}
+
+}  // namespace
+}  // extern "C++"
+
+la_status la_qk_norm_rope(const la_qk_norm_rope_args* a, void* stream) {
+  if (!a) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_size(a->B) || !valid_size(a->H) || !valid_size(a->H_kv) || !valid_size(a->N)) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_dtype(a->in_dtype) || !valid_dtype(a->out_dtype) || !valid_dtype(a->w_dtype)) return LA_ERR_INVALID_ARGUMENT;
+  if (a->norm < LA_NORM_NONE || a->norm > LA_NORM_L2 || (a->norm != LA_NORM_NONE && !(a->eps > 0.f && a->eps <= 1e37f)) ||
+      (a->norm == LA_NORM_NONE && (a->q_weight || a->k_weight)))
+    return LA_ERR_INVALID_ARGUMENT;
+  if (a->d < 8 || a->d > 256 || a->d % 8 != 0) return LA_ERR_UNSUPPORTED;
+  if (a->rot < 0 || a->rot > a->d) return LA_ERR_INVALID_ARGUMENT;
+  if (a->rot % 16 != 0) return LA_ERR_UNSUPPORTED;
+  if (a->B == 0 || a->N == 0 || (a->H == 0 && a->H_kv == 0)) return LA_OK;
+  if (!within(kMaxElems, {a->B, a->N, a->H + a->H_kv}) || la::qk_norm_rope_blocks(a->B, a->H, a->H_kv, a->N, (int)a->d) > kMaxBlocks)
+    return LA_ERR_UNSUPPORTED;
+  if (!valid_view(a->q, a->B, a->H, a->N, a->d, a->in_dtype) || !valid_view(a->q_out, a->B, a->H, a->N, a->d, a->out_dtype) ||
+      !valid_view(a->k, a->B, a->H_kv, a->N, a->d, a->in_dtype) || !valid_view(a->k_out, a->B, a->H_kv, a->N, a->d, a->out_dtype) ||
+      (a->H > 0 && !distinct(a->q_out, a->B, a->H, a->N, a->d)) || (a->H_kv > 0 && !distinct(a->k_out, a->B, a->H_kv, a->N, a->d)))
+    return LA_ERR_INVALID_ARGUMENT;
+  if ((a->H > 0 && a->q.ptr == a->q_out.ptr && (a->in_dtype != a->out_dtype || !same_rows(a->q, a->q_out))) ||
+      (a->H_kv > 0 && a->k.ptr == a->k_out.ptr && (a->in_dtype != a->out_dtype || !same_rows(a->k, a->k_out))))
+    return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_tables(a->cos, a->sin, a->rot, a->positions) || !aligned16(a->q_weight) || !aligned16(a->k_weight) || !aligned8(a->pos) ||
+      !aligned8(a->lens))
+    return LA_ERR_INVALID_ARGUMENT;
+  unsigned* status = device_status_ptr();
+  if (!status) return LA_ERR_CUDA;
+  la::QkNormRopeLaunch L{};
+  L.B = a->B; L.H = a->H; L.Hkv = a->H_kv; L.N = a->N; L.positions = a->positions;
+  L.d = (int)a->d; L.rot = (int)a->rot; L.norm = a->norm;
+  L.in_bf16 = a->in_dtype == LA_DTYPE_BF16; L.out_bf16 = a->out_dtype == LA_DTYPE_BF16; L.w_bf16 = a->w_dtype == LA_DTYPE_BF16;
+  L.q = view(a->q); L.k = view(a->k); L.q_out = a->q_out.ptr; L.k_out = a->k_out.ptr;
+  L.q_sb = a->q_out.stride_b; L.q_sh = a->q_out.stride_h; L.q_st = a->q_out.stride_t;
+  L.k_sb = a->k_out.stride_b; L.k_sh = a->k_out.stride_h; L.k_st = a->k_out.stride_t;
+  L.q_weight = a->q_weight; L.k_weight = a->k_weight; L.cos = a->cos; L.sin = a->sin; L.pos = a->pos; L.lens = a->lens;
+  L.eps = a->eps; L.interleaved = a->interleaved != 0; L.pos_each = a->pos_each != 0; L.fill = (a->fill & LA_FILL_ROWS) != 0;
+  L.status = status;
+  return from_cuda(la::launch_qk_norm_rope(L, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_paged_append(const la_paged_append_args* a, void* stream) {
+  if (!a) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_size(a->B) || !valid_size(a->N)) return LA_ERR_INVALID_ARGUMENT;
+  const la_status st = check_pages(a, a->B);
+  if (st != LA_OK) return st;
+  if (a->rot < 0 || a->rot > a->d) return LA_ERR_INVALID_ARGUMENT;
+  if (a->rot % 16 != 0) return LA_ERR_UNSUPPORTED;
+  if (a->B == 0 || a->N == 0 || a->H_kv == 0) return LA_OK;
+  if (!within((int64_t(1) << 31) - 8, {a->B, a->N, a->H_kv})) return LA_ERR_UNSUPPORTED;
+  if (!valid_view(a->k, a->B, a->H_kv, a->N, a->d, a->in_dtype) || !valid_view(a->v, a->B, a->H_kv, a->N, a->d, a->in_dtype) ||
+      !valid_pools(a, a->B) || !valid_tables(a->cos, a->sin, a->rot, a->positions) || !a->seen || !aligned8(a->seen) || !aligned8(a->lens))
+    return LA_ERR_INVALID_ARGUMENT;
+  unsigned* status = device_status_ptr();
+  if (!status) return LA_ERR_CUDA;
+  la::PagedAppendLaunch L{};
+  L.c = cache_of(a, status);
+  L.B = a->B; L.N = a->N; L.positions = a->positions; L.rot = (int)a->rot;
+  L.k = view(a->k); L.v = view(a->v); L.cos = a->cos; L.sin = a->sin; L.seen = a->seen; L.lens = a->lens;
+  L.interleaved = a->interleaved != 0;
+  return from_cuda(la::launch_paged_append(L, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_paged_read(const la_paged_read_args* a, void* stream) {
+  if (!a) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_size(a->B) || !valid_size(a->N) || !valid_dtype(a->out_dtype)) return LA_ERR_INVALID_ARGUMENT;
+  const la_status st = check_pages(a, a->B);
+  if (st != LA_OK) return st;
+  if (a->B == 0 || a->N == 0 || a->H_kv == 0) return LA_OK;
+  if (a->N > INT32_MAX - 8192 || !within((int64_t(1) << 31) - 8, {a->B, (a->N + 15) / 16, a->H_kv, 2})) return LA_ERR_UNSUPPORTED;
+  if (!valid_view(a->k, a->B, a->H_kv, a->N, a->d, a->out_dtype) || !valid_view(a->v, a->B, a->H_kv, a->N, a->d, a->out_dtype) ||
+      !distinct(a->k, a->B, a->H_kv, a->N, a->d) || !distinct(a->v, a->B, a->H_kv, a->N, a->d) || !valid_pools(a, a->B) || !aligned8(a->lens))
+    return LA_ERR_INVALID_ARGUMENT;
+  unsigned* status = device_status_ptr();
+  if (!status) return LA_ERR_CUDA;
+  la::PagedReadLaunch L{};
+  L.c = cache_of(a, status);
+  L.B = a->B; L.N = a->N; L.out_bf16 = a->out_dtype == LA_DTYPE_BF16; L.fill = (a->fill & LA_FILL_ROWS) != 0;
+  L.k = a->k.ptr; L.k_sb = a->k.stride_b; L.k_sh = a->k.stride_h; L.k_st = a->k.stride_t;
+  L.v = a->v.ptr; L.v_sb = a->v.stride_b; L.v_sh = a->v.stride_h; L.v_st = a->v.stride_t;
+  L.lens = a->lens;
+  return from_cuda(la::launch_paged_read(L, static_cast<cudaStream_t>(stream)));
+}
+
+// LA_OK where the sizes say how often a sequence is split
+static la_status paged_decode_shape(const la_paged_decode_args* a) {
+  if (!a) return LA_ERR_INVALID_ARGUMENT;
+  if (!valid_size(a->S) || !valid_size(a->H) || !valid_size(a->window) || a->H_kv < 1 || a->H % a->H_kv != 0) return LA_ERR_INVALID_ARGUMENT;
+  const la_status st = check_pages(a, a->S);
+  if (st != LA_OK) return st;
+  if (a->H / a->H_kv > 16 || !within((int64_t(1) << 24) - 1, {a->S, a->H})) return LA_ERR_UNSUPPORTED;
+  return LA_OK;
+}
+
+static int paged_decode_plan(const la_paged_decode_args* a) {
+  const int64_t tokens = a->width * a->page;
+  return la::paged_decode_splits(a->S, a->H_kv, (int)(a->H / a->H_kv), a->window > 0 ? std::min(tokens, a->window + 16) : tokens,
+                                 a->in_dtype == LA_DTYPE_BF16, a->bits == 4);
+}
+
+size_t la_paged_decode_workspace_size(const la_paged_decode_args* a) {
+  if (paged_decode_shape(a) != LA_OK || a->S == 0 || a->H == 0) return 0;
+  const int splits = paged_decode_plan(a);
+  return splits > 1 ? (size_t)a->S * a->H * splits * (a->d + 2) * sizeof(float) : 0;
+}
+
+la_status la_paged_decode_step(const la_paged_decode_args* a, void* ws, size_t ws_bytes, void* stream) {
+  la_status st = paged_decode_shape(a);
+  if (st != LA_OK) return st;
+  if (!valid_dtype(a->out_dtype) || !valid_cap(a->softcap, a->scale)) return LA_ERR_INVALID_ARGUMENT;
+  if (a->S == 0 || a->H == 0) return LA_OK;
+  la_tensor q = a->q, o = a->out;
+  q.stride_t = o.stride_t = a->d;
+  if (!valid_view(q, a->S, a->H, 1, a->d, a->in_dtype) || !valid_view(o, a->S, a->H, 1, a->d, a->out_dtype) ||
+      !distinct(o, a->S, a->H, 1, a->d) || !valid_pools(a, a->S) || !a->lens || !aligned8(a->lens) || !aligned4(a->slopes))
+    return LA_ERR_INVALID_ARGUMENT;
+  const size_t need = la_paged_decode_workspace_size(a);
+  if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need)) return LA_ERR_WORKSPACE;
+  unsigned* status = device_status_ptr();
+  if (!status) return LA_ERR_CUDA;
+  la::PagedDecodeLaunch L{};
+  L.c = cache_of(a, status);
+  L.S = a->S; L.H = a->H; L.window = a->window; L.out_bf16 = a->out_dtype == LA_DTYPE_BF16;
+  L.scale = a->scale; L.softcap = a->softcap; L.q = view(q); L.out = o.ptr; L.o_sb = o.stride_b; L.o_sh = o.stride_h;
+  L.lens = a->lens; L.slopes = a->slopes;
+  L.splits = paged_decode_plan(a); L.parts = static_cast<float*>(ws);
+  return from_cuda(la::launch_paged_decode(L, static_cast<cudaStream_t>(stream)));
+}
+
 la_status la_selftest_bounded_wait(int arrive, int64_t limit_ns, void* stream) {
   if (limit_ns < 1000000 || limit_ns > 2000000000) return LA_ERR_INVALID_ARGUMENT;
   unsigned* status = device_status_ptr();

@@ -224,4 +224,68 @@ struct SwaBiasedDecodeLaunch {
 };
 cudaError_t launch_swa_biased_decode(const SwaBiasedDecodeLaunch& a, cudaStream_t stream);
 
+// Norms and position rotation of queries and keys (heads.cu).
+struct QkNormRopeLaunch {
+  int64_t B, H, Hkv, N, positions;
+  int d, rot, norm;
+  bool in_bf16, out_bf16, w_bf16;
+  View4 q, k;
+  void *q_out, *k_out;
+  int64_t q_sb, q_sh, q_st, k_sb, k_sh, k_st;  // of the outputs
+  const void *q_weight, *k_weight;
+  const float *cos, *sin;
+  const int64_t *pos, *lens;
+  float eps;
+  bool interleaved, pos_each, fill;
+  unsigned* status;
+};
+int64_t qk_norm_rope_blocks(int64_t B, int64_t H, int64_t Hkv, int64_t N, int d);  // of the launch's grid
+cudaError_t launch_qk_norm_rope(const QkNormRopeLaunch& a, cudaStream_t stream);
+
+// Paged caches (paged.cu): what a token's place follows from.
+struct PagedCache {
+  int64_t Hkv, pages, width;
+  int d, page;
+  bool bf16, four;       // type of the rows; four: 4 bits of bf16 rows
+  void *k, *v;
+  const int32_t* table;  // [B, width]
+  unsigned* status;
+};
+struct PagedAppendLaunch {
+  PagedCache c;
+  int64_t B, N, positions;
+  int rot;
+  View4 k, v;
+  const float *cos, *sin;
+  const int64_t *seen, *lens;
+  bool interleaved;
+};
+struct PagedReadLaunch {
+  PagedCache c;
+  int64_t B, N;
+  bool out_bf16, fill;
+  void *k, *v;
+  int64_t k_sb, k_sh, k_st, v_sb, v_sh, v_st;
+  const int64_t* lens;
+};
+cudaError_t launch_paged_append(const PagedAppendLaunch& a, cudaStream_t stream);
+cudaError_t launch_paged_read(const PagedReadLaunch& a, cudaStream_t stream);
+
+// One token's attention over a paged cache (paged_decode.cu).
+struct PagedDecodeLaunch {
+  PagedCache c;
+  int64_t S, H, window;
+  bool out_bf16;
+  float scale, softcap;
+  View4 q;
+  void* out;
+  int64_t o_sb, o_sh;
+  const int64_t* lens;
+  const float* slopes;
+  int splits;    // of a sequence's tokens; more than one: the parts meet in `parts`
+  float* parts;  // [S, H, splits, d + 2]: sums of weighted values, their greatest score, the sum of weights
+};
+int paged_decode_splits(int64_t S, int64_t Hkv, int group, int64_t tokens, bool bf16, bool four);
+cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream);
+
 }  // namespace la

@@ -1,0 +1,299 @@
+// paged_decode.cu -- attention of one token of each sequence over a paged cache:
+//   s_j = cap tanh(scale q.k_j / cap) - slope (n - 1 - j),   o = sum_j softmax_j(s_j) v_j,   max(0, n - window) <= j < n.
+// This file: the join of a split sequence's parts, the choice of the split, and the CUDA-core kernel.
+//
+// A warp takes tiles of 32 tokens of its block's part in turn.  It scores them for a few query heads of the group, four
+// elements a lane and d / 4 lanes a row, takes their softmax a token a lane with the running maximum and sum of its
+// tokens so far, and adds up its value rows; warps do not wait for one another before the end, where their sums meet in
+// shared memory.
+#include <algorithm>
+#include <type_traits>
+
+#include "paged_decode.cuh"
+
+namespace la {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kTokens = 32;  // of a warp's tile: two of 16
+constexpr int kLoads = 4;    // row loads in flight
+constexpr int kMaxD = 128;
+
+enum Rows { kRowsF32, kRowsBf16, kRowsFour };
+
+// Four elements of a cached row from element `col` on.
+template <Rows kind>
+__device__ __forceinline__ void load_row4(const uint8_t* head, int page, int slot, int d, int col, float (&o)[4]) {
+  if constexpr (kind == kRowsF32) {
+    Raw4<float> r;
+    r.load(reinterpret_cast<const float*>(head) + (int64_t)slot * d + col);
+    r.unpack(o);
+  } else if constexpr (kind == kRowsBf16) {
+    Raw4<__nv_bfloat16> r;
+    r.load(reinterpret_cast<const __nv_bfloat16*>(head) + (int64_t)slot * d + col);
+    r.unpack(o);
+  } else {
+    const int groups = d / kGroup, g = col / kGroup;
+    const uint32_t w = reinterpret_cast<const uint32_t*>(head + (int64_t)slot * (d / 2))[code_word(g, col % kGroup / 8, groups)];
+    const uint32_t meta = reinterpret_cast<const uint32_t*>(head + (int64_t)page * (d / 2))[slot * groups + g];
+    const float scale = __uint_as_float(meta << 16), offset = __uint_as_float(meta & 0xffff0000u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = fmaf((float)(w >> (col % 8 + e) * 4 & 15u), scale, offset);
+  }
+}
+
+// LPR lanes a row, HG query heads a pass
+template <Rows kind, typename TOut, int LPR, int HG>
+__global__ void __launch_bounds__(32 * kWarps)
+paged_decode_kernel(const PagedDecodeLaunch a, const int passes) {
+  using TIn = std::conditional_t<kind == kRowsF32, float, __nv_bfloat16>;
+  constexpr int R = 32 / LPR, kBatch = kLoads * R, kBatches = kTokens / kBatch, NV = kLoads * HG;
+  __shared__ float s_p[kWarps][kTokens][HG];  // scores, then weights
+  __shared__ float s_o[kWarps][HG][kMaxD];
+  __shared__ float s_m[kWarps][HG], s_l[kWarps][HG];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dependents_trigger();
+  grid_dependency_wait();
+  const int part = (int)(blockIdx.x % a.splits);
+  int64_t rest = blockIdx.x / a.splits;
+  const int pass = (int)(rest % passes);
+  rest /= passes;
+  const int64_t s = rest / a.c.Hkv, hk = rest - s * a.c.Hkv;
+  const int d = a.c.d, group = (int)(a.H / a.c.Hkv), heads = min(HG, group - pass * HG);
+  const int64_t h0 = hk * group + pass * HG;
+  const SeenTokens t = seen_tokens(a, s);
+  const bool report = part == 0 && pass == 0 && hk == 0 && threadIdx.x == 0;
+  if (t.hi < 0) {
+    if (report) atomicOr(a.c.status, kStatusBadIndex);
+    return;
+  }
+  if (part >= max(t.parts, 1)) return;
+  const int first = (t.lo / kTile + part * t.tiles) * kTile, last = min(t.hi, first + t.tiles * kTile);  // this part's tokens
+  const int lane_col = lane % LPR * 4, sub = lane / LPR;
+  const bool on = lane_col < d;
+  const int col = on ? lane_col : 0;
+  const int64_t size = page_bytes(a.c);
+  const float inv_cap = 1.f / a.softcap;
+
+  float q[HG][4], o[HG][4], m[HG], l[HG];
+#pragma unroll
+  for (int g = 0; g < HG; ++g) {
+    Raw4<TIn> r;
+    r.zero();
+    if (on && g < heads) r.load(static_cast<const TIn*>(a.q.ptr) + s * a.q.sb + (h0 + g) * a.q.sh + col);
+    r.unpack(q[g]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[g][e] = 0.f;
+    m[g] = -INFINITY;
+    l[g] = 0.f;
+  }
+
+  for (int t0 = first + warp * kTokens; t0 < last; t0 += kWarps * kTokens) {
+    // the tile's two pages; tokens of a page that is not there are not seen
+    int page[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = t0 + i * kTile;
+      page[i] = at < last ? table_page(a.c, s, at / a.c.page) : -1;
+      if (at < last && page[i] < 0 && hk == 0 && pass == 0 && lane == 0) atomicOr(a.c.status, kStatusBadIndex);
+    }
+    auto seen = [&](int r) { return t0 + r >= t.lo && t0 + r < last && (r < kTile ? page[0] : page[1]) >= 0; };
+    auto row = [&](const void* pool, int r, float (&x)[4]) {
+      if (on && seen(r)) {
+        load_row4<kind>(static_cast<const uint8_t*>(pool) + ((r < kTile ? page[0] : page[1]) * a.c.Hkv + hk) * size, a.c.page,
+                        (t0 + r) % a.c.page, d, col, x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = 0.f;
+      }
+    };
+    // ---- scores
+#pragma unroll
+    for (int bt = 0; bt < kBatches; ++bt) {
+      float k[kLoads][4], sum[NV];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) row(a.c.k, bt * kBatch + i * R + sub, k[i]);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+        for (int g = 0; g < HG; ++g)
+          sum[i * HG + g] = fmaf(q[g][3], k[i][3], fmaf(q[g][2], k[i][2], fmaf(q[g][1], k[i][1], q[g][0] * k[i][0])));
+      // sums over the row's lanes: halve the values while there are lanes to share them with
+      int at = 0, left = NV;
+#pragma unroll
+      for (int off = LPR / 2; off >= 1; off /= 2) {
+        if (left > 1) {
+          const int half = left / 2;
+          const bool up = (lane & off) != 0;
+#pragma unroll
+          for (int e = 0; e < NV / 2; ++e) {
+            if (e < half) {
+              const float send = up ? sum[e] : sum[e + half];
+              sum[e] = (up ? sum[e + half] : sum[e]) + __shfl_xor_sync(kFullMask, send, off);
+            }
+          }
+          at += up ? half : 0;
+          left = half;
+        } else {
+          sum[0] += __shfl_xor_sync(kFullMask, sum[0], off);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < NV; ++e)
+        if (e < left) s_p[warp][bt * kBatch + (at + e) / HG * R + sub][(at + e) % HG] = sum[e];
+    }
+    __syncwarp();
+    // ---- softmax with what came before, a token a lane
+    const bool mine = seen(lane);
+    float f[HG];
+#pragma unroll
+    for (int g = 0; g < HG; ++g) {
+      float x = score(s_p[warp][lane][g], a.scale, a.softcap, inv_cap);
+      if (a.slopes && g < heads) x = fmaf(-a.slopes[h0 + g] * kLog2e, (float)(t.hi - 1 - t0 - lane), x);
+      if (!mine) x = -INFINITY;
+      float top = x;
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, off));
+      top = fmaxf(top, m[g]);
+      const float base = top == -INFINITY ? 0.f : top;
+      f[g] = ex2(m[g] - base);
+      x = ex2(x - base);
+      l[g] = fmaf(l[g], f[g], warp_sum(x));
+      m[g] = top;
+      s_p[warp][lane][g] = x;
+    }
+    __syncwarp();
+    // ---- values
+#pragma unroll
+    for (int g = 0; g < HG; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[g][e] *= f[g];
+#pragma unroll
+    for (int bt = 0; bt < kBatches; ++bt) {
+      float v[kLoads][4];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) row(a.c.v, bt * kBatch + i * R + sub, v[i]);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+        for (int g = 0; g < HG; ++g) {
+          const float p = s_p[warp][bt * kBatch + i * R + sub][g];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[g][e] = fmaf(p, v[i][e], o[g][e]);
+        }
+    }
+    __syncwarp();  // the weights are used up
+  }
+
+  // ---- the warps' sums together
+#pragma unroll
+  for (int g = 0; g < HG; ++g) {
+#pragma unroll
+    for (int off = LPR; off < 32; off *= 2)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[g][e] += __shfl_xor_sync(kFullMask, o[g][e], off);
+    if (sub == 0 && on) *reinterpret_cast<float4*>(&s_o[warp][g][col]) = make_float4(o[g][0], o[g][1], o[g][2], o[g][3]);
+    if (lane == 0) {
+      s_m[warp][g] = m[g];
+      s_l[warp][g] = l[g];
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < heads * d; e += blockDim.x) {
+    const int g = e / d, c = e - g * d;
+    float top = s_m[0][g];
+#pragma unroll
+    for (int u = 1; u < kWarps; ++u) top = fmaxf(top, s_m[u][g]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, total = 0.f;
+#pragma unroll
+    for (int u = 0; u < kWarps; ++u) {
+      const float w = ex2(s_m[u][g] - base);
+      sum = fmaf(w, s_o[u][g][c], sum);
+      total = fmaf(w, s_l[u][g], total);
+    }
+    if (a.splits > 1) {
+      part_values(a, s, h0 + g, part)[c] = sum;
+      if (c == 0) *part_sums(a, s, h0 + g, part) = make_float2(top, total);
+    } else {
+      store1(static_cast<TOut*>(a.out) + s * a.o_sb + (h0 + g) * a.o_sh + c, t.hi > 0 ? sum / total : 0.f);
+    }
+  }
+}
+
+// The parts of a split sequence together: a warp a query head.
+template <typename TOut>
+__global__ void __launch_bounds__(128)
+paged_join_kernel(const PagedDecodeLaunch a) {
+  grid_dependents_trigger();
+  grid_dependency_wait();
+  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int64_t s = unit / a.H, h = unit - s * a.H;
+  if (s >= a.S) return;
+  const int lane = threadIdx.x & 31, d = a.c.d;
+  const SeenTokens t = seen_tokens(a, s);
+  if (t.hi < 0) return;
+  const float2* sums = part_sums(a, s, h, 0);
+  float top = -INFINITY;
+  for (int i = lane; i < t.parts; i += 32) top = fmaxf(top, sums[i].x);
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, off));
+  const float base = top == -INFINITY ? 0.f : top;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float total = 0.f;
+  const bool on = lane * 4 < d;
+  const float* values = part_values(a, s, h, 0) + lane * 4;
+#pragma unroll 4
+  for (int i = 0; i < t.parts; ++i) {
+    const float2 ml = sums[i];
+    const float w = ex2(ml.x - base);
+    total = fmaf(w, ml.y, total);
+    if (on) {
+      const float4 v = *reinterpret_cast<const float4*>(values + (int64_t)i * d);
+      o.x = fmaf(w, v.x, o.x); o.y = fmaf(w, v.y, o.y); o.z = fmaf(w, v.z, o.z); o.w = fmaf(w, v.w, o.w);
+    }
+  }
+  if (!on) return;
+  const bool empty = t.hi == 0;
+  const float y[4] = {empty ? 0.f : o.x / total, empty ? 0.f : o.y / total, empty ? 0.f : o.z / total, empty ? 0.f : o.w / total};
+  store_floats(static_cast<TOut*>(a.out) + s * a.o_sb + h * a.o_sh + lane * 4, y, 4, true);
+}
+
+template <Rows kind, typename TOut, int LPR, int HG>
+cudaError_t launch(const PagedDecodeLaunch& a, cudaStream_t stream) {
+  const int group = (int)(a.H / a.c.Hkv), passes = (group + HG - 1) / HG;
+  return launch_dependent(paged_decode_kernel<kind, TOut, LPR, HG>, dim3((unsigned)(a.S * a.c.Hkv * passes * a.splits)), 32 * kWarps, 0, stream, a, passes);
+}
+template <Rows kind, typename TOut, int LPR>
+cudaError_t by_group(const PagedDecodeLaunch& a, cudaStream_t stream) {
+  const int group = (int)(a.H / a.c.Hkv);
+  return group == 1 ? launch<kind, TOut, LPR, 1>(a, stream) : group == 2 ? launch<kind, TOut, LPR, 2>(a, stream)
+       : group <= 4 ? launch<kind, TOut, LPR, 4>(a, stream) : launch<kind, TOut, LPR, 8>(a, stream);
+}
+template <Rows kind, typename TOut>
+cudaError_t by_width(const PagedDecodeLaunch& a, cudaStream_t stream) {
+  return a.c.d <= 32 ? by_group<kind, TOut, 8>(a, stream) : a.c.d <= 64 ? by_group<kind, TOut, 16>(a, stream) : by_group<kind, TOut, 32>(a, stream);
+}
+
+}  // namespace
+
+// Blocks of one part each would leave SMs idle or end one long sequence after the others: as many parts as make 16 blocks an
+// SM, each of at least kPartTokens tokens.
+int paged_decode_splits(int64_t S, int64_t Hkv, int group, int64_t tokens, bool bf16, bool four) {
+  const int64_t blocks = S * Hkv, most = (tokens + kPartTokens - 1) / kPartTokens;
+  const int64_t want = (152 * 16 + blocks - 1) / blocks;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 256));
+}
+
+cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream) {
+  cudaError_t e;
+  if (a.c.four) e = a.out_bf16 ? by_width<kRowsFour, __nv_bfloat16>(a, stream) : by_width<kRowsFour, float>(a, stream);
+  else if (a.c.bf16) e = a.out_bf16 ? by_width<kRowsBf16, __nv_bfloat16>(a, stream) : by_width<kRowsBf16, float>(a, stream);
+  else e = a.out_bf16 ? by_width<kRowsF32, __nv_bfloat16>(a, stream) : by_width<kRowsF32, float>(a, stream);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  const dim3 grid((unsigned)((a.S * a.H + 3) / 4));
+  return a.out_bf16 ? launch_dependent(paged_join_kernel<__nv_bfloat16>, grid, 128, 0, stream, a)
+                    : launch_dependent(paged_join_kernel<float>, grid, 128, 0, stream, a);
+}
+
+}  // namespace la

@@ -1,0 +1,45 @@
+// paged_decode.cuh -- what the kernels of a step over a paged cache share: the tokens a block takes, the scores, and where a
+// block's result goes.
+#pragma once
+
+#include "paged.cuh"
+#include "swa_common.cuh"
+
+namespace la {
+
+constexpr int kTile = 16;          // tokens that lie in one page: a page holds a multiple
+constexpr int kPartTokens = 256;   // a part of a split sequence takes no fewer, but for the last one
+
+// The tokens of a sequence that its query sees, [lo, hi), and how many parts they make of at most `splits`.  hi < 0: the
+// length is out of range, and nothing of the sequence is written.
+struct SeenTokens {
+  int lo, hi, parts, tiles;  // tiles a part takes, counted from lo's tile
+};
+__device__ __forceinline__ SeenTokens seen_tokens(const PagedDecodeLaunch& a, int64_t s) {
+  const int64_t n = a.lens[s];
+  SeenTokens t{0, -1, 0, 0};
+  if (n < 0 || n > a.c.width * a.c.page) return t;
+  t.hi = (int)n;
+  t.lo = a.window > 0 && a.window < n ? (int)(n - a.window) : 0;
+  const int tiles = t.hi > t.lo ? (t.hi - 1) / kTile - t.lo / kTile + 1 : 0;
+  t.tiles = max((tiles + a.splits - 1) / a.splits, kPartTokens / kTile);
+  t.parts = (tiles + t.tiles - 1) / t.tiles;
+  return t;
+}
+
+// The score of a product, before the bias, in units of log2.
+__device__ __forceinline__ float score(float product, float scale, float softcap, float inv_cap) {
+  float y = product * scale;
+  if (softcap != 0.f) y = capped(y, softcap, inv_cap);
+  return y * kLog2e;
+}
+
+// Places of a part's sums, greatest score and sum of weights in the workspace.
+__device__ __forceinline__ float* part_values(const PagedDecodeLaunch& a, int64_t s, int64_t h, int part) {
+  return a.parts + ((s * a.H + h) * a.splits + part) * a.c.d;
+}
+__device__ __forceinline__ float2* part_sums(const PagedDecodeLaunch& a, int64_t s, int64_t h, int part) {
+  return reinterpret_cast<float2*>(a.parts + a.S * a.H * a.splits * a.c.d) + (s * a.H + h) * a.splits + part;
+}
+
+}  // namespace la
