@@ -1,13 +1,12 @@
 // paged_decode.cu -- attention of one token of each sequence over a paged cache:
 //   s_j = cap tanh(scale q.k_j / cap) - slope (n - 1 - j),   o = sum_j softmax_j(s_j) v_j,   max(0, n - window) <= j < n.
-// This file: the join of a split sequence's parts, the choice of the split, and the CUDA-core kernel.
+// This file: the join of a split sequence's parts, the choice of the split, and the kernel of fp32 pages, on the CUDA cores.
 //
 // A warp takes tiles of 32 tokens of its block's part in turn.  It scores them for a few query heads of the group, four
 // elements a lane and d / 4 lanes a row, takes their softmax a token a lane with the running maximum and sum of its
 // tokens so far, and adds up its value rows; warps do not wait for one another before the end, where their sums meet in
 // shared memory.
 #include <algorithm>
-#include <type_traits>
 
 #include "paged_decode.cuh"
 
@@ -19,34 +18,10 @@ constexpr int kTokens = 32;  // of a warp's tile: two of 16
 constexpr int kLoads = 4;    // row loads in flight
 constexpr int kMaxD = 128;
 
-enum Rows { kRowsF32, kRowsBf16, kRowsFour };
-
-// Four elements of a cached row from element `col` on.
-template <Rows kind>
-__device__ __forceinline__ void load_row4(const uint8_t* head, int page, int slot, int d, int col, float (&o)[4]) {
-  if constexpr (kind == kRowsF32) {
-    Raw4<float> r;
-    r.load(reinterpret_cast<const float*>(head) + (int64_t)slot * d + col);
-    r.unpack(o);
-  } else if constexpr (kind == kRowsBf16) {
-    Raw4<__nv_bfloat16> r;
-    r.load(reinterpret_cast<const __nv_bfloat16*>(head) + (int64_t)slot * d + col);
-    r.unpack(o);
-  } else {
-    const int groups = d / kGroup, g = col / kGroup;
-    const uint32_t w = reinterpret_cast<const uint32_t*>(head + (int64_t)slot * (d / 2))[code_word(g, col % kGroup / 8, groups)];
-    const uint32_t meta = reinterpret_cast<const uint32_t*>(head + (int64_t)page * (d / 2))[slot * groups + g];
-    const float scale = __uint_as_float(meta << 16), offset = __uint_as_float(meta & 0xffff0000u);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = fmaf((float)(w >> (col % 8 + e) * 4 & 15u), scale, offset);
-  }
-}
-
 // LPR lanes a row, HG query heads a pass
-template <Rows kind, typename TOut, int LPR, int HG>
+template <typename TOut, int LPR, int HG>
 __global__ void __launch_bounds__(32 * kWarps)
-paged_decode_kernel(const PagedDecodeLaunch a, const int passes) {
-  using TIn = std::conditional_t<kind == kRowsF32, float, __nv_bfloat16>;
+paged_decode_f32_kernel(const PagedDecodeLaunch a, const int passes) {
   constexpr int R = 32 / LPR, kBatch = kLoads * R, kBatches = kTokens / kBatch, NV = kLoads * HG;
   __shared__ float s_p[kWarps][kTokens][HG];  // scores, then weights
   __shared__ float s_o[kWarps][HG][kMaxD];
@@ -72,15 +47,13 @@ paged_decode_kernel(const PagedDecodeLaunch a, const int passes) {
   const int lane_col = lane % LPR * 4, sub = lane / LPR;
   const bool on = lane_col < d;
   const int col = on ? lane_col : 0;
-  const int64_t size = page_bytes(a.c);
-  const float inv_cap = 1.f / a.softcap;
 
   float q[HG][4], o[HG][4], m[HG], l[HG];
 #pragma unroll
   for (int g = 0; g < HG; ++g) {
-    Raw4<TIn> r;
+    Raw4<float> r;
     r.zero();
-    if (on && g < heads) r.load(static_cast<const TIn*>(a.q.ptr) + s * a.q.sb + (h0 + g) * a.q.sh + col);
+    if (on && g < heads) r.load(static_cast<const float*>(a.q.ptr) + s * a.q.sb + (h0 + g) * a.q.sh + col);
     r.unpack(q[g]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[g][e] = 0.f;
@@ -98,14 +71,15 @@ paged_decode_kernel(const PagedDecodeLaunch a, const int passes) {
       if (at < last && page[i] < 0 && hk == 0 && pass == 0 && lane == 0) atomicOr(a.c.status, kStatusBadIndex);
     }
     auto seen = [&](int r) { return t0 + r >= t.lo && t0 + r < last && (r < kTile ? page[0] : page[1]) >= 0; };
+    const int slot[2] = {t0 % a.c.page, (t0 + kTile) % a.c.page};
     auto row = [&](const void* pool, int r, float (&x)[4]) {
+      Raw4<float> raw;
+      raw.zero();
       if (on && seen(r)) {
-        load_row4<kind>(static_cast<const uint8_t*>(pool) + ((r < kTile ? page[0] : page[1]) * a.c.Hkv + hk) * size, a.c.page,
-                        (t0 + r) % a.c.page, d, col, x);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = 0.f;
+        const int64_t at = ((r < kTile ? page[0] : page[1]) * a.c.Hkv + hk) * a.c.page + (r < kTile ? slot[0] + r : slot[1] + r - kTile);
+        raw.load(static_cast<const float*>(pool) + at * d + col);
       }
+      raw.unpack(x);
     };
     // ---- scores
 #pragma unroll
@@ -148,7 +122,9 @@ paged_decode_kernel(const PagedDecodeLaunch a, const int passes) {
     float f[HG];
 #pragma unroll
     for (int g = 0; g < HG; ++g) {
-      float x = score(s_p[warp][lane][g], a.scale, a.softcap, inv_cap);
+      float x = s_p[warp][lane][g] * a.scale;
+      if (a.softcap != 0.f) x = a.softcap * tanhf(x / a.softcap);  // fp32 throughout: the polynomial of `capped` is off by 10 half steps
+      x *= kLog2e;
       if (a.slopes && g < heads) x = fmaf(-a.slopes[h0 + g] * kLog2e, (float)(t.hi - 1 - t0 - lane), x);
       if (!mine) x = -INFINITY;
       float top = x;
@@ -259,20 +235,20 @@ paged_join_kernel(const PagedDecodeLaunch a) {
   store_floats(static_cast<TOut*>(a.out) + s * a.o_sb + h * a.o_sh + lane * 4, y, 4, true);
 }
 
-template <Rows kind, typename TOut, int LPR, int HG>
+template <typename TOut, int LPR, int HG>
 cudaError_t launch(const PagedDecodeLaunch& a, cudaStream_t stream) {
   const int group = (int)(a.H / a.c.Hkv), passes = (group + HG - 1) / HG;
-  return launch_dependent(paged_decode_kernel<kind, TOut, LPR, HG>, dim3((unsigned)(a.S * a.c.Hkv * passes * a.splits)), 32 * kWarps, 0, stream, a, passes);
+  return launch_dependent(paged_decode_f32_kernel<TOut, LPR, HG>, dim3((unsigned)(a.S * a.c.Hkv * passes * a.splits)), 32 * kWarps, 0, stream, a, passes);
 }
-template <Rows kind, typename TOut, int LPR>
+template <typename TOut, int LPR>
 cudaError_t by_group(const PagedDecodeLaunch& a, cudaStream_t stream) {
   const int group = (int)(a.H / a.c.Hkv);
-  return group == 1 ? launch<kind, TOut, LPR, 1>(a, stream) : group == 2 ? launch<kind, TOut, LPR, 2>(a, stream)
-       : group <= 4 ? launch<kind, TOut, LPR, 4>(a, stream) : launch<kind, TOut, LPR, 8>(a, stream);
+  return group == 1 ? launch<TOut, LPR, 1>(a, stream) : group == 2 ? launch<TOut, LPR, 2>(a, stream)
+       : group <= 4 ? launch<TOut, LPR, 4>(a, stream) : launch<TOut, LPR, 8>(a, stream);
 }
-template <Rows kind, typename TOut>
+template <typename TOut>
 cudaError_t by_width(const PagedDecodeLaunch& a, cudaStream_t stream) {
-  return a.c.d <= 32 ? by_group<kind, TOut, 8>(a, stream) : a.c.d <= 64 ? by_group<kind, TOut, 16>(a, stream) : by_group<kind, TOut, 32>(a, stream);
+  return a.c.d <= 32 ? by_group<TOut, 8>(a, stream) : a.c.d <= 64 ? by_group<TOut, 16>(a, stream) : by_group<TOut, 32>(a, stream);
 }
 
 }  // namespace
@@ -286,10 +262,7 @@ int paged_decode_splits(int64_t S, int64_t Hkv, int group, int64_t tokens, bool 
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream) {
-  cudaError_t e;
-  if (a.c.four) e = a.out_bf16 ? by_width<kRowsFour, __nv_bfloat16>(a, stream) : by_width<kRowsFour, float>(a, stream);
-  else if (a.c.bf16) e = a.out_bf16 ? by_width<kRowsBf16, __nv_bfloat16>(a, stream) : by_width<kRowsBf16, float>(a, stream);
-  else e = a.out_bf16 ? by_width<kRowsF32, __nv_bfloat16>(a, stream) : by_width<kRowsF32, float>(a, stream);
+  const cudaError_t e = a.c.bf16 ? launch_paged_decode_mma(a, stream) : a.out_bf16 ? by_width<__nv_bfloat16>(a, stream) : by_width<float>(a, stream);
   if (e != cudaSuccess || a.splits == 1) return e;
   const dim3 grid((unsigned)((a.S * a.H + 3) / 4));
   return a.out_bf16 ? launch_dependent(paged_join_kernel<__nv_bfloat16>, grid, 128, 0, stream, a)

@@ -27,13 +27,6 @@ __device__ __forceinline__ SeenTokens seen_tokens(const PagedDecodeLaunch& a, in
   return t;
 }
 
-// The score of a product, before the bias, in units of log2.
-__device__ __forceinline__ float score(float product, float scale, float softcap, float inv_cap) {
-  float y = product * scale;
-  if (softcap != 0.f) y = capped(y, softcap, inv_cap);
-  return y * kLog2e;
-}
-
 // Places of a part's sums, greatest score and sum of weights in the workspace.
 __device__ __forceinline__ float* part_values(const PagedDecodeLaunch& a, int64_t s, int64_t h, int part) {
   return a.parts + ((s * a.H + h) * a.splits + part) * a.c.d;
@@ -41,5 +34,7 @@ __device__ __forceinline__ float* part_values(const PagedDecodeLaunch& a, int64_
 __device__ __forceinline__ float2* part_sums(const PagedDecodeLaunch& a, int64_t s, int64_t h, int part) {
   return reinterpret_cast<float2*>(a.parts + a.S * a.H * a.splits * a.c.d) + (s * a.H + h) * a.splits + part;
 }
+
+cudaError_t launch_paged_decode_mma(const PagedDecodeLaunch& a, cudaStream_t stream);  // bf16 and 4-bit pages, without the join
 
 }  // namespace la

@@ -1,0 +1,699 @@
+// paged_decode_mma.cu -- a step over bf16 pages and over 4-bit pages.
+//
+// A key row meets up to 16 query heads, too many operations for the CUDA cores beside the loads and too few rows for
+// tcgen05, so the products are mma.m16n8k16 with the heads as the 16 rows, as in swa_biased_decode.cu.  Each warp takes
+// tiles of its block's part in turn, through a ring of its own in shared memory that asynchronous copies fill, with the
+// running maximum and sum of its tokens; no warp waits for another before the end, where their sums meet.  A tile's pages
+// are looked up one tile ahead of its copies.
+//
+// The running maximum moves only where a score is more than 2^kSlack times beyond it: until then weights are up to 2^kSlack,
+// which costs fp32 sums nothing, and the sums of values need not be scaled.
+//
+// 4 bits: a code is put into the mantissa of a bf16 one, 1 + code / 16, exactly, and the products run on those:
+//   k = offset + scale code = (offset - 16 scale) + 16 scale (1 + code / 16)
+//   q.k = sum over groups of 16 scale (q.(1 + code / 16)) + (offset - 16 scale) sum q
+//   sum_j p_j v_j = sum_j (16 scale_j p_j) (1 + code_j / 16) + sum_j p_j (offset_j - 16 scale_j)
+// so that scales and offsets meet whole sums in fp32, and weights once per group.
+#include <algorithm>
+
+#include "paged_decode.cuh"
+#include "tc.cuh"
+
+namespace la {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr float kSlack = 8.f;
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Two values as bf16, and what that leaves of them as bf16: together off by 2^-17 of a value.
+__device__ __forceinline__ void two_parts(float lo, float hi, uint32_t& major, uint32_t& minor) {
+  major = tc::pack2_bf16(lo, hi);
+  minor = tc::pack2_bf16(lo - __uint_as_float(major << 16), hi - __uint_as_float(major & 0xffff0000u));
+}
+
+// Two bf16 values, zero in the place of what is not finite.
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+
+// What every warp of a block knows.
+struct Part {
+  int64_t s, hk, h0;
+  int group, part, first, last;  // tokens [first, last), first a multiple of kTile
+  SeenTokens seen;
+};
+// False: nothing to do.
+__device__ __forceinline__ bool part_of(const PagedDecodeLaunch& a, Part& p) {
+  p.part = (int)(blockIdx.x % a.splits);
+  const int64_t rest = blockIdx.x / a.splits;
+  p.s = rest / a.c.Hkv;
+  p.hk = rest - p.s * a.c.Hkv;
+  p.group = (int)(a.H / a.c.Hkv);
+  p.h0 = p.hk * p.group;
+  p.seen = seen_tokens(a, p.s);
+  if (p.seen.hi < 0 && p.part == 0 && p.hk == 0 && threadIdx.x == 0) atomicOr(a.c.status, kStatusBadIndex);
+  p.first = (p.seen.lo / kTile + p.part * p.seen.tiles) * kTile;
+  p.last = min(p.seen.hi, p.first + p.seen.tiles * kTile);
+  return p.seen.hi >= 0 && p.part < max(p.seen.parts, 1);
+}
+
+// The running softmax of a warp: rows lane / 4 (0) and that + 8 (1), a quad's lanes with the same maximum and sums of their own.
+struct Running {
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+};
+
+// Scores of T tiles of eight tokens into weights; f: the factors of the sums so far, and whether they are not one.
+template <int T, int kRowsUsed>
+__device__ __forceinline__ bool weigh(Running& r, float (&x)[T][4], float (&f)[2]) {
+  bool moves = false;
+  float top[2];
+#pragma unroll
+  for (int i = 0; i < kRowsUsed; ++i) {
+    float y = x[0][2 * i];
+#pragma unroll
+    for (int t = 0; t < T; ++t) y = fmaxf(y, fmaxf(x[t][2 * i], x[t][2 * i + 1]));
+    y = fmaxf(y, __shfl_xor_sync(kFullMask, y, 1));
+    top[i] = fmaxf(y, __shfl_xor_sync(kFullMask, y, 2));
+    moves |= top[i] > r.m[i] + kSlack;  // from -infinity too
+  }
+  moves = __any_sync(kFullMask, moves);
+  if (moves) {
+#pragma unroll
+    for (int i = 0; i < kRowsUsed; ++i) {
+      const float m = fmaxf(r.m[i], top[i]);
+      f[i] = ex2(r.m[i] - (m == -INFINITY ? 0.f : m));
+      r.m[i] = m;
+      r.l[i] *= f[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsUsed; ++i) {
+    const float base = r.m[i] == -INFINITY ? 0.f : r.m[i];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int e = 2 * i; e < 2 * i + 2; ++e) {
+        x[t][e] = ex2(x[t][e] - base);
+        r.l[i] += x[t][e];
+      }
+  }
+  return moves;
+}
+
+// The warps' sums together and out: s_m, s_l [warp][16], `values` warp w's sums of row g at w * stride + g * d.
+__device__ __forceinline__ void finish(const PagedDecodeLaunch& a, const Part& p, const float (*s_m)[16], const float (*s_l)[16],
+                                       const float* values, int stride) {
+  const int d = a.c.d;
+  for (int e = threadIdx.x * 2; e < p.group * d; e += 32 * kWarps * 2) {
+    const int g = e / d, c = e - g * d;
+    float top = s_m[0][g];
+#pragma unroll
+    for (int u = 1; u < kWarps; ++u) top = fmaxf(top, s_m[u][g]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float2 sum = make_float2(0.f, 0.f);
+    float total = 0.f;
+#pragma unroll
+    for (int u = 0; u < kWarps; ++u) {
+      const float w = ex2(s_m[u][g] - base);
+      const float2 y = *reinterpret_cast<const float2*>(values + u * stride + e);
+      sum.x = fmaf(w, y.x, sum.x);
+      sum.y = fmaf(w, y.y, sum.y);
+      total = fmaf(w, s_l[u][g], total);
+    }
+    const int64_t h = p.h0 + g;
+    if (a.splits > 1) {
+      *reinterpret_cast<float2*>(part_values(a, p.s, h, p.part) + c) = sum;
+      if (c == 0) *part_sums(a, p.s, h, p.part) = make_float2(top, total);
+      continue;
+    }
+    if (p.seen.hi > 0) sum = make_float2(sum.x / total, sum.y / total);
+    const int64_t at = p.s * a.o_sb + h * a.o_sh + c;
+    if (a.out_bf16) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at) = tc::pack2_bf16(sum.x, sum.y);
+    else *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = sum;
+  }
+}
+
+// A warp's rows of scores: caps, biases and what is not seen.  tokens(t, e): of tile t, entry e's token's distance from the
+// warp tile's first one.
+template <int T, int kRowsUsed, typename Tokens>
+__device__ __forceinline__ void bias_and_mask(const PagedDecodeLaunch& a, float (&x)[T][4], const float (&slope)[2], float scale, float inv_cap,
+                                              int age0, uint32_t seen, uint32_t whole, Tokens tokens) {
+#pragma unroll
+  for (int i = 0; i < kRowsUsed; ++i)
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int e = 2 * i; e < 2 * i + 2; ++e) {
+        float y = x[t][e];
+        if (a.softcap != 0.f) y = capped(y * a.scale, a.softcap, inv_cap) * kLog2e;
+        else y *= scale;
+        if (a.slopes) y = fmaf(-slope[i], (float)(age0 - tokens(t, e & 1)), y);
+        x[t][e] = y;
+      }
+  if (seen != whole) {
+#pragma unroll
+    for (int i = 0; i < kRowsUsed; ++i)
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int e = 2 * i; e < 2 * i + 2; ++e)
+          if (!(seen >> tokens(t, e & 1) & 1u)) x[t][e] = -INFINITY;
+  }
+}
+
+// Bits of the tokens [t0, t0 + n) that lie in [lo, hi).
+__device__ __forceinline__ uint32_t token_bits(int t0, int n, int lo, int hi) {
+  const int from = min(max(lo - t0, 0), n), to = min(max(hi - t0, 0), n);
+  if (from >= to) return 0u;
+  return (to == 32 ? 0xffffffffu : (1u << to) - 1u) & ~((1u << from) - 1u);
+}
+
+// ---------------------------------------------------------------------------------------------- bf16
+// DP: width padded to 64 or 128.  kSpare: at most eight heads a group; the weights' second parts take rows 8 to 15.
+template <int DP>
+constexpr int kStages = DP == 128 ? 3 : 5;
+template <int DP>
+constexpr int kTileBytes = 2 * kTile * DP * 2;  // keys, then values
+template <int DP>
+constexpr int kSmem = kWarps * kStages<DP> * kTileBytes<DP>;
+
+template <int DP, bool kSpare>
+__global__ void __launch_bounds__(32 * kWarps)
+paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
+  using T = __nv_bfloat16;
+  constexpr int kRows = kSpare ? 1 : 2, kSteps = DP / 16, kChunks = DP / 8, kS = kStages<DP>;
+  extern __shared__ __align__(128) uint8_t pd_smem[];
+  __shared__ float s_m[kWarps][16], s_l[kWarps][16];
+  __shared__ uint32_t s_seen[kWarps][kS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, q4 = lane & 3;
+  grid_dependents_trigger();
+  grid_dependency_wait();
+  Part p;
+  if (!part_of(a, p)) return;
+  const int d = a.c.d, page = a.c.page;
+  uint8_t* region = pd_smem + warp * kS * kTileBytes<DP>;
+  const uint32_t base = tc::smem_u32(region);
+  // place of 16-byte chunk `ch` of row r: eight neighbouring rows meet eight different banks
+  auto at = [](int r, int ch) { return (uint32_t)(r * (DP * 2) + ((ch ^ (r & 7)) << 4)); };
+
+  const int tiles = p.last > p.first ? (p.last - p.first + kTile - 1) / kTile : 0;
+  auto lookup = [&](int i) {  // the page of this warp's i-th tile, -1 behind the last one or where there is none
+    const int t = warp + i * kWarps;
+    if (t >= tiles) return -1;
+    const int pg = table_page(a.c, p.s, (p.first + t * kTile) / page);
+    if (pg < 0 && p.hk == 0 && lane == 0) atomicOr(a.c.status, kStatusBadIndex);
+    return pg;
+  };
+  auto fetch = [&](int i, int pg) {  // this warp's i-th tile into its stage
+    const int t0 = p.first + (warp + i * kWarps) * kTile, stage = i % kS;
+    const uint32_t seen = pg < 0 ? 0u : token_bits(t0, kTile, p.seen.lo, p.last);
+    if (lane == 0) s_seen[warp][stage] = seen;
+    if (pg < 0) return;
+    const int64_t from = ((pg * a.c.Hkv + p.hk) * page + t0 % page) * d;
+    const uint32_t to = base + stage * kTileBytes<DP>;
+#pragma unroll
+    for (int j = 0; j < kTile * kChunks / 32; ++j) {
+      const int e = lane + 32 * j, r = e / kChunks, ch = e % kChunks;
+      const bool on = (seen >> r & 1u) && ch * 8 < d;  // what is not seen becomes zeros: a weight of zero times NaN is NaN
+      const int64_t off = from + r * d + (ch * 8 < d ? ch * 8 : 0);
+      tc::cp_async16(to + at(r, ch), static_cast<const T*>(a.c.k) + off, on ? 16u : 0u);
+      tc::cp_async16(to + kTileBytes<DP> / 2 + at(r, ch), static_cast<const T*>(a.c.v) + off, on ? 16u : 0u);
+    }
+  };
+
+  // ---- queries as operands
+  uint32_t qa[kSteps][2 * kRows];
+  float slope[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int g = row + 8 * i;
+    const T* q = static_cast<const T*>(a.q.ptr) + p.s * a.q.sb + (p.h0 + (g < p.group ? g : 0)) * a.q.sh;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int col = 16 * k + 8 * u + 2 * q4;
+        qa[k][i * 2 + u] = g < p.group && col < d ? *reinterpret_cast<const uint32_t*>(q + col) : 0u;
+      }
+    if (a.slopes && g < p.group) slope[i] = a.slopes[p.h0 + g] * kLog2e;
+  }
+  const float scale = a.scale * kLog2e, inv_cap = 1.f / a.softcap;
+
+  float o[2 * kSteps][4];
+  Running run;
+  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+  for (bool guarded = false;; guarded = true) {
+#pragma unroll
+    for (int t = 0; t < 2 * kSteps; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+    int next = lookup(0);
+#pragma unroll
+    for (int i = 0; i < kS - 1; ++i) {
+      if (i < mine) fetch(i, next);
+      tc::cp_async_commit();
+      next = lookup(i + 1);
+    }
+    for (int i = 0; i < mine; ++i) {
+      cp_async_wait<kS - 2>();
+      __syncwarp();  // every lane's copies of this tile are in, and its reads of the stage that is filled next are done
+      if (i + kS - 1 < mine) fetch(i + kS - 1, next);
+      tc::cp_async_commit();
+      next = lookup(i + kS);
+      const int stage = i % kS;
+      const uint32_t keys = base + stage * kTileBytes<DP>, vals = keys + kTileBytes<DP> / 2;
+      const uint32_t seen = s_seen[warp][stage];
+      if (seen == 0u) continue;
+      float x[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        uint32_t b[4];
+        ldmatrix(b, keys + at((lane >> 4) * 8 + (lane & 7), 2 * k + ((lane >> 3) & 1)));
+        mma16816(x[0], qa[k][0], kSpare ? 0u : qa[k][2 * kRows - 2], qa[k][1], kSpare ? 0u : qa[k][2 * kRows - 1], b[0], b[1]);
+        mma16816(x[1], qa[k][0], kSpare ? 0u : qa[k][2 * kRows - 2], qa[k][1], kSpare ? 0u : qa[k][2 * kRows - 1], b[2], b[3]);
+      }
+      const int t0 = p.first + (warp + i * kWarps) * kTile;
+      bias_and_mask<2, kRows>(a, x, slope, scale, inv_cap, p.seen.hi - 1 - t0, seen, 0xffffu, [&](int t, int e) { return t * 8 + q4 * 2 + e; });
+      float f[2];
+      if (weigh<2, kRows>(run, x, f)) {
+#pragma unroll
+        for (int t = 0; t < 2 * kSteps; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][e] *= f[kSpare ? 0 : e >> 1];
+      }
+      uint32_t w[4], z[4];  // first and second parts: rows row and row + 8 of tile 0, then of tile 1
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) two_parts(x[t][2 * u], x[t][2 * u + 1], w[2 * t + u], z[2 * t + u]);
+      if constexpr (kSpare) {
+        w[1] = z[0];
+        w[3] = z[2];
+      }
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        uint32_t b[4];
+        ldmatrix_trans(b, vals + at(((lane >> 3) & 1) * 8 + (lane & 7), 2 * k + (lane >> 4)));
+        mma16816(o[2 * k], w[0], w[1], w[2], w[3], b[0], b[1]);
+        mma16816(o[2 * k + 1], w[0], w[1], w[2], w[3], b[2], b[3]);
+        if constexpr (!kSpare) {
+          if (guarded) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[e] = finite_or_zero(b[e]);
+          }
+          mma16816(o[2 * k], z[0], z[1], z[2], z[3], b[0], b[1]);
+          mma16816(o[2 * k + 1], z[0], z[1], z[2], z[3], b[2], b[3]);
+        }
+      }
+    }
+    tc::cp_async_wait_all();
+    __syncwarp();
+    // What second parts make of a value that is not finite is left out: the first ones' result stands.  With rows of their
+    // own they are added here; otherwise the warp's tiles are gone through again with zeros for such values in their product.
+    if constexpr (kSpare) {
+#pragma unroll
+      for (int t = 0; t < 2 * kSteps; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) o[t][e] += finite1(o[t][2 + e]) ? o[t][2 + e] : 0.f;
+      break;
+    } else {
+      float sum = 0.f;
+#pragma unroll
+      for (int t = 0; t < 2 * kSteps; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum = fmaf(0.f, o[t][e], sum);
+      if (guarded || __all_sync(kFullMask, sum == 0.f)) break;
+      run = Running();
+    }
+  }
+  // ---- this warp's sums into its place
+  float* part = reinterpret_cast<float*>(region);
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    float l = run.l[u];
+    l += __shfl_xor_sync(kFullMask, l, 1);
+    l += __shfl_xor_sync(kFullMask, l, 2);
+    if (q4 == 0) {
+      s_m[warp][row + 8 * u] = run.m[u];
+      s_l[warp][row + 8 * u] = l;
+    }
+    if (row + 8 * u < p.group) {
+#pragma unroll
+      for (int t = 0; t < 2 * kSteps; ++t)
+        if (t * 8 < d) *reinterpret_cast<float2*>(part + (row + 8 * u) * d + t * 8 + q4 * 2) = make_float2(o[t][2 * u], o[t][2 * u + 1]);
+    }
+  }
+  __syncthreads();
+  finish(a, p, s_m, s_l, reinterpret_cast<const float*>(pd_smem), kS * kTileBytes<DP> / 4);
+}
+
+// ---------------------------------------------------------------------------------------------- 4 bits
+constexpr int kPair = 2 * kTile;  // tokens of a warp's tile: two of a page's sixteenths
+constexpr int kStages4 = 3;
+template <int D>
+constexpr int kCodes = kPair * D / 2;
+template <int D>
+constexpr int kMeta = kPair * (D / kGroup) * 4;
+template <int D>
+constexpr int kTileBytes4 = 2 * (kCodes<D> + kMeta<D>);  // codes of keys and values, then their scales and offsets
+template <int D>
+constexpr int kRing4 = kStages4 * kTileBytes4<D>;
+// ... and each token's 16 scale and offset - 16 scale, of its keys' groups and of its values'
+template <int D>
+constexpr int kSmem4 = kWarps * (kRing4<D> + 2 * kPair * (D / kGroup) * 8);
+
+// (1 + code / 16) of nibbles m and m + 4 of a word, as bf16
+template <int m>
+__device__ __forceinline__ uint32_t ones(uint32_t w) {
+  const uint32_t x = m == 0 ? w << 3 : w >> (4 * m - 3);
+  return (x & 0x00780078u) | 0x3f803f80u;
+}
+
+// Place of a row's 16-byte chunk: the rows that a product's lanes read together lie in different banks.
+template <int D>
+__device__ __forceinline__ uint32_t place4(int r, int ch) {
+  if constexpr (D == 128) return (uint32_t)((r >> 1) * 128 + ((r ^ (r >> 2)) & 1) * 64 + (ch ^ (r & 2)) * 16);
+  else return (uint32_t)((r >> 2) * 128 + ((r & 3) ^ ((r >> 1) & 2)) * 32 + ch * 16);
+}
+
+template <int D, bool kSpare>
+__global__ void __launch_bounds__(32 * kWarps, 3)
+paged_decode_four_kernel(const PagedDecodeLaunch a) {
+  using T = __nv_bfloat16;
+  constexpr int kRows = kSpare ? 1 : 2, kGroups = D / kGroup, kS = kStages4;
+  constexpr int kHalf = kTile * D / 2 / 16;            // chunks of codes of 16 tokens
+  constexpr int kHalfMeta = kTile * kGroups * 4 / 16;  // and of their scales and offsets
+  extern __shared__ __align__(128) uint8_t pd_smem[];
+  __shared__ float s_m[kWarps][16], s_l[kWarps][16];
+  __shared__ uint32_t s_seen[kWarps][kS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, q4 = lane & 3;
+  grid_dependents_trigger();
+  grid_dependency_wait();
+  Part p;
+  if (!part_of(a, p)) return;
+  const int page = a.c.page;
+  uint8_t* region = pd_smem + warp * kRing4<D>;
+  const uint32_t base = tc::smem_u32(region);
+  float2* factors = reinterpret_cast<float2*>(pd_smem + kWarps * kRing4<D>) + warp * 2 * kPair * kGroups;
+  const int64_t size = page_bytes(a.c);
+
+  const int tiles = p.last > p.first ? (p.last - p.first + kPair - 1) / kPair : 0;
+  struct Pages { int a, b; };
+  auto lookup = [&](int i) {  // the pages of this warp's i-th tile
+    Pages g{-1, -1};
+    const int t = warp + i * kWarps, t0 = p.first + t * kPair;
+    if (t >= tiles) return g;
+    g.a = table_page(a.c, p.s, t0 / page);
+    if (t0 + kTile < p.last) g.b = table_page(a.c, p.s, (t0 + kTile) / page);
+    if ((g.a < 0 || (g.b < 0 && t0 + kTile < p.last)) && p.hk == 0 && lane == 0) atomicOr(a.c.status, kStatusBadIndex);
+    return g;
+  };
+  auto fetch = [&](int i, Pages g) {
+    const int t0 = p.first + (warp + i * kWarps) * kPair, stage = i % kS;
+    uint32_t seen = token_bits(t0, kPair, p.seen.lo, p.last);
+    if (g.a < 0) seen &= 0xffff0000u;
+    if (g.b < 0) seen &= 0x0000ffffu;
+    if (lane == 0) s_seen[warp][stage] = seen;
+    const uint32_t to = base + stage * kTileBytes4<D>;
+    const int slot[2] = {t0 % page, (t0 + kTile) % page};
+    const int64_t at[2] = {(max(g.a, 0) * a.c.Hkv + p.hk) * size, (max(g.b, 0) * a.c.Hkv + p.hk) * size};
+    const bool there[2] = {g.a >= 0, g.b >= 0};  // otherwise codes of anything, whose tokens have no scale and no weight
+    const uint8_t* kp = static_cast<const uint8_t*>(a.c.k);
+    const uint8_t* vp = static_cast<const uint8_t*>(a.c.v);
+#pragma unroll
+    for (int j = 0; j < 2 * kHalf / 32; ++j) {
+      const int h = 32 * j / kHalf, c = 32 * j % kHalf + lane;
+      if (!there[h]) continue;
+      const int64_t from = at[h] + slot[h] * (D / 2) + c * 16;
+      const uint32_t place = place4<D>(h * kTile + c / (D / 32), c % (D / 32));
+      tc::cp_async16(to + place, kp + from, 16u);
+      tc::cp_async16(to + kCodes<D> + place, vp + from, 16u);
+    }
+    if (lane < 4 * kHalfMeta) {
+      const int c = lane % kHalfMeta, h = lane / kHalfMeta & 1, v = lane / (2 * kHalfMeta);
+      const int64_t from = (h ? at[1] : at[0]) + page * (D / 2) + (h ? slot[1] : slot[0]) * (kGroups * 4) + c * 16;
+      if (h ? there[1] : there[0]) tc::cp_async16(to + 2 * kCodes<D> + v * kMeta<D> + h * (kMeta<D> / 2) + c * 16, (v ? vp : kp) + from, 16u);
+    }
+  };
+
+  // ---- queries as operands: word e = 2 q4 + u of group g holds elements 64 g + 8 e + (0..7), whose pairs (m, m + 4) are a
+  // product's neighbours; and the groups' sums of them
+  uint32_t qa[kGroups][2][4][kRows];  // [group][word][m][row]
+  float qs[kGroups][2] = {}, slope[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int h = row + 8 * i;
+    const T* q = static_cast<const T*>(a.q.ptr) + p.s * a.q.sb + (p.h0 + (h < p.group ? h : 0)) * a.q.sh;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      float sum = 0.f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        Raw8<T> r;
+        r.zero();
+        if (h < p.group) r.load(q + kGroup * g + 8 * (2 * q4 + u));
+        float v[8];
+        r.unpack(v);
+        const uint32_t x[4] = {r.w.x, r.w.y, r.w.z, r.w.w};  // pairs (0, 1) (2, 3) (4, 5) (6, 7)
+        qa[g][u][0][i] = __byte_perm(x[0], x[2], 0x5410);
+        qa[g][u][1][i] = __byte_perm(x[0], x[2], 0x7632);
+        qa[g][u][2][i] = __byte_perm(x[1], x[3], 0x5410);
+        qa[g][u][3][i] = __byte_perm(x[1], x[3], 0x7632);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += v[e];
+      }
+      sum += __shfl_xor_sync(kFullMask, sum, 1);
+      qs[g][i] = sum + __shfl_xor_sync(kFullMask, sum, 2);
+    }
+    if (a.slopes && h < p.group) slope[i] = a.slopes[p.h0 + h] * kLog2e;
+  }
+  const float scale = a.scale * kLog2e, inv_cap = 1.f / a.softcap;
+  // tile t's column c is this token of the warp's 32, so that a lane's four weights of a 16-token product are tokens
+  // q4, q4 + 4, q4 + 8, q4 + 12 of it
+  auto token = [](int t, int c) { return (t >> 1) * kTile + (c >> 1) + 4 * (2 * (t & 1) + (c & 1)); };
+
+  float o[8 * kGroups][4], bias[kGroups][2] = {};  // sums of products; of offsets, a lane's tokens'
+#pragma unroll
+  for (int t = 0; t < 8 * kGroups; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+  Running run;
+  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+  Pages next = lookup(0);
+#pragma unroll
+  for (int i = 0; i < kS - 1; ++i) {
+    if (i < mine) fetch(i, next);
+    tc::cp_async_commit();
+    next = lookup(i + 1);
+  }
+  for (int i = 0; i < mine; ++i) {
+    cp_async_wait<kS - 2>();
+    __syncwarp();  // every lane's copies of this tile are in, and its reads of the stage that is filled next are done
+    if (i + kS - 1 < mine) fetch(i + kS - 1, next);
+    tc::cp_async_commit();
+    next = lookup(i + kS);
+    const int stage = i % kS;
+    const uint8_t* keys = region + stage * kTileBytes4<D>;
+    const uint8_t* vals = keys + kCodes<D>;
+    const uint32_t* meta = reinterpret_cast<const uint32_t*>(vals + kCodes<D>);
+    const uint32_t seen = s_seen[warp][stage];
+    // ---- a token a lane: 16 scale and offset - 16 scale
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const uint32_t w = meta[(v * kPair + lane) * kGroups + g];
+        const float s = 16.f * __uint_as_float(w << 16);
+        const bool on = seen >> lane & 1u;
+        factors[(v * kPair + lane) * kGroups + g] = on ? make_float2(s, __uint_as_float(w & 0xffff0000u) - s) : make_float2(0.f, 0.f);
+      }
+    __syncwarp();
+    // ---- scores
+    float x[4][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint8_t* at = keys + place4<D>(token(t, row), D == 128 ? q4 : q4 >> 1) + (D == 128 ? 0 : (q4 & 1) * 8);
+      uint32_t w[kGroups][2];  // [group][word]
+      if constexpr (D == 128) {
+        const uint4 c = *reinterpret_cast<const uint4*>(at);
+        w[0][0] = c.x; w[1][0] = c.y; w[0][1] = c.z; w[1][1] = c.w;
+      } else {
+        const uint2 c = *reinterpret_cast<const uint2*>(at);
+        w[0][0] = c.x; w[0][1] = c.y;
+      }
+      float y[kGroups][4];
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[g][e] = 0.f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          mma16816(y[g], qa[g][u][0][0], kSpare ? 0u : qa[g][u][0][kRows - 1], qa[g][u][1][0], kSpare ? 0u : qa[g][u][1][kRows - 1], ones<0>(w[g][u]),
+                   ones<1>(w[g][u]));
+          mma16816(y[g], qa[g][u][2][0], kSpare ? 0u : qa[g][u][2][kRows - 1], qa[g][u][3][0], kSpare ? 0u : qa[g][u][3][kRows - 1], ones<2>(w[g][u]),
+                   ones<3>(w[g][u]));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float2* f = factors + token(t, 2 * q4 + c) * kGroups;
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          float sum = 0.f;
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) sum = fmaf(f[g].x, y[g][2 * u + c], fmaf(f[g].y, qs[g][u], sum));
+          x[t][2 * u + c] = sum;
+        }
+      }
+    }
+    const int t0 = p.first + (warp + i * kWarps) * kPair;
+    bias_and_mask<4, kRows>(a, x, slope, scale, inv_cap, p.seen.hi - 1 - t0, seen, 0xffffffffu, [&](int t, int e) { return token(t, 2 * q4 + e); });
+    float f[2];
+    if (weigh<4, kRows>(run, x, f)) {
+#pragma unroll
+      for (int t = 0; t < 8 * kGroups; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][e] *= f[kSpare ? 0 : e >> 1];
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) bias[g][u] *= f[u];
+    }
+    // ---- values, 16 tokens a product
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      uint32_t w[4][kGroups];  // the word e = row of each group, of tokens q4 + 4 j
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = ks * kTile + q4 + 4 * j;
+        if constexpr (D == 128) {
+          const uint2 c = *reinterpret_cast<const uint2*>(vals + place4<D>(r, row >> 1) + (row & 1) * 8);
+          w[j][0] = c.x; w[j][1] = c.y;
+        } else {
+          w[j][0] = *reinterpret_cast<const uint32_t*>(vals + place4<D>(r, row >> 2) + (row & 3) * 4);
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        uint32_t major[4], minor[4];  // [j / 2][row]
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float2 fa = factors[(kPair + ks * kTile + q4 + 8 * t) * kGroups + g], fb = factors[(kPair + ks * kTile + q4 + 8 * t + 4) * kGroups + g];
+#pragma unroll
+          for (int u = 0; u < kRows; ++u) {
+            const float pa = x[2 * ks + t][2 * u], pb = x[2 * ks + t][2 * u + 1];
+            bias[g][u] = fmaf(pa, fa.y, fmaf(pb, fb.y, bias[g][u]));
+            two_parts(pa * fa.x, pb * fb.x, major[2 * t + u], minor[2 * t + u]);
+          }
+        }
+        if constexpr (kSpare) {
+          major[1] = minor[0];
+          major[3] = minor[2];
+        }
+        const uint32_t lo0 = __byte_perm(w[0][g], w[1][g], 0x5410), hi0 = __byte_perm(w[0][g], w[1][g], 0x7632);
+        const uint32_t lo1 = __byte_perm(w[2][g], w[3][g], 0x5410), hi1 = __byte_perm(w[2][g], w[3][g], 0x7632);
+        auto product = [&](int n, uint32_t b0, uint32_t b1) {  // elements 8 e + n of the group
+          mma16816(o[8 * g + n], major[0], major[1], major[2], major[3], b0, b1);
+          if constexpr (!kSpare) mma16816(o[8 * g + n], minor[0], minor[1], minor[2], minor[3], b0, b1);
+        };
+        product(0, ones<0>(lo0), ones<0>(lo1));
+        product(1, ones<1>(lo0), ones<1>(lo1));
+        product(2, ones<2>(lo0), ones<2>(lo1));
+        product(3, ones<3>(lo0), ones<3>(lo1));
+        product(4, ones<0>(hi0), ones<0>(hi1));
+        product(5, ones<1>(hi0), ones<1>(hi1));
+        product(6, ones<2>(hi0), ones<2>(hi1));
+        product(7, ones<3>(hi0), ones<3>(hi1));
+      }
+    }
+    __syncwarp();  // the factors are used up
+  }
+  tc::cp_async_wait_all();
+  __syncwarp();
+  // ---- this warp's sums into its place
+  float* part = reinterpret_cast<float*>(region);
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    float l = run.l[u];
+    l += __shfl_xor_sync(kFullMask, l, 1);
+    l += __shfl_xor_sync(kFullMask, l, 2);
+    if (q4 == 0) {
+      s_m[warp][row + 8 * u] = run.m[u];
+      s_l[warp][row + 8 * u] = l;
+    }
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      float off = bias[g][u];
+      off += __shfl_xor_sync(kFullMask, off, 1);
+      off += __shfl_xor_sync(kFullMask, off, 2);
+      if (row + 8 * u >= p.group) continue;
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float y = o[8 * g + n][2 * u + c] + (kSpare ? o[8 * g + n][2 + c] : 0.f);
+          part[(row + 8 * u) * D + kGroup * g + 8 * (2 * q4 + c) + n] = y + off;
+        }
+    }
+  }
+  __syncthreads();
+  finish(a, p, s_m, s_l, reinterpret_cast<const float*>(pd_smem), kRing4<D> / 4);
+}
+
+template <typename K>
+cudaError_t launch(K kernel, int smem, std::atomic<uint64_t>& done, const PagedDecodeLaunch& a, cudaStream_t stream) {
+  const cudaError_t e = allow_smem(kernel, smem, done);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kernel, dim3((unsigned)(a.S * a.c.Hkv * a.splits)), 32 * kWarps, smem, stream, a);
+}
+
+template <int DP, bool kSpare>
+cudaError_t launch_bf16(const PagedDecodeLaunch& a, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  static_assert(kStages<DP> * kTileBytes<DP> >= 16 * DP * 4, "a warp's sums take the place of its ring");
+  return launch(paged_decode_bf16_kernel<DP, kSpare>, kSmem<DP>, done, a, stream);
+}
+template <int D, bool kSpare>
+cudaError_t launch_four(const PagedDecodeLaunch& a, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  static_assert(kRing4<D> >= 16 * D * 4, "a warp's sums take the place of its ring");
+  return launch(paged_decode_four_kernel<D, kSpare>, kSmem4<D>, done, a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode_mma(const PagedDecodeLaunch& a, cudaStream_t stream) {
+  const bool spare = a.H / a.c.Hkv <= 8;
+  if (a.c.four && a.c.d == 64) return spare ? launch_four<64, true>(a, stream) : launch_four<64, false>(a, stream);
+  if (a.c.four) return spare ? launch_four<128, true>(a, stream) : launch_four<128, false>(a, stream);
+  if (a.c.d <= 64) return spare ? launch_bf16<64, true>(a, stream) : launch_bf16<64, false>(a, stream);
+  return spare ? launch_bf16<128, true>(a, stream) : launch_bf16<128, false>(a, stream);
+}
+
+}  // namespace la
