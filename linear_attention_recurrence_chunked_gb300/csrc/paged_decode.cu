@@ -197,16 +197,15 @@ paged_decode_f32_kernel(const PagedDecodeLaunch a, const int passes) {
   }
 }
 
-// The parts of a split sequence together: a warp a query head.
+// The parts of a split sequence together: a block a query head, each warp a quarter of the parts, four elements a lane.
 template <typename TOut>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(32 * kWarps)
 paged_join_kernel(const PagedDecodeLaunch a) {
+  __shared__ float s_o[kWarps][kMaxD], s_l[kWarps];
   grid_dependents_trigger();
   grid_dependency_wait();
-  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int64_t s = unit / a.H, h = unit - s * a.H;
-  if (s >= a.S) return;
-  const int lane = threadIdx.x & 31, d = a.c.d;
+  const int64_t s = blockIdx.x / a.H, h = blockIdx.x - s * a.H;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = a.c.d;
   const SeenTokens t = seen_tokens(a, s);
   if (t.hi < 0) return;
   const float2* sums = part_sums(a, s, h, 0);
@@ -215,24 +214,30 @@ paged_join_kernel(const PagedDecodeLaunch a) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, off));
   const float base = top == -INFINITY ? 0.f : top;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float total = 0.f;
+  float o[4] = {0.f, 0.f, 0.f, 0.f}, total = 0.f;
   const bool on = lane * 4 < d;
-  const float* values = part_values(a, s, h, 0) + lane * 4;
-#pragma unroll 4
-  for (int i = 0; i < t.parts; ++i) {
+  const float* values = part_values(a, s, h, 0) + (on ? lane * 4 : 0);
+#pragma unroll 8
+  for (int i = warp; i < t.parts; i += kWarps) {
     const float2 ml = sums[i];
+    const float4 v = *reinterpret_cast<const float4*>(values + (int64_t)i * d);
     const float w = ex2(ml.x - base);
     total = fmaf(w, ml.y, total);
-    if (on) {
-      const float4 v = *reinterpret_cast<const float4*>(values + (int64_t)i * d);
-      o.x = fmaf(w, v.x, o.x); o.y = fmaf(w, v.y, o.y); o.z = fmaf(w, v.z, o.z); o.w = fmaf(w, v.w, o.w);
-    }
+    o[0] = fmaf(w, v.x, o[0]); o[1] = fmaf(w, v.y, o[1]); o[2] = fmaf(w, v.z, o[2]); o[3] = fmaf(w, v.w, o[3]);
   }
-  if (!on) return;
-  const bool empty = t.hi == 0;
-  const float y[4] = {empty ? 0.f : o.x / total, empty ? 0.f : o.y / total, empty ? 0.f : o.z / total, empty ? 0.f : o.w / total};
-  store_floats(static_cast<TOut*>(a.out) + s * a.o_sb + h * a.o_sh + lane * 4, y, 4, true);
+  if (on) *reinterpret_cast<float4*>(&s_o[warp][lane * 4]) = make_float4(o[0], o[1], o[2], o[3]);
+  if (lane == 0) s_l[warp] = total;
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c >= d) return;
+  float sum = 0.f;
+  total = 0.f;
+#pragma unroll
+  for (int u = 0; u < kWarps; ++u) {
+    sum += s_o[u][c];
+    total += s_l[u];
+  }
+  store1(static_cast<TOut*>(a.out) + s * a.o_sb + h * a.o_sh + c, t.hi > 0 ? sum / total : 0.f);
 }
 
 template <typename TOut, int LPR, int HG>
@@ -258,15 +263,15 @@ cudaError_t by_width(const PagedDecodeLaunch& a, cudaStream_t stream) {
 int paged_decode_splits(int64_t S, int64_t Hkv, int group, int64_t tokens, bool bf16, bool four) {
   const int64_t blocks = S * Hkv, most = (tokens + kPartTokens - 1) / kPartTokens;
   const int64_t want = (152 * 16 + blocks - 1) / blocks;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 256));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 128));
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream) {
   const cudaError_t e = a.c.bf16 ? launch_paged_decode_mma(a, stream) : a.out_bf16 ? by_width<__nv_bfloat16>(a, stream) : by_width<float>(a, stream);
   if (e != cudaSuccess || a.splits == 1) return e;
-  const dim3 grid((unsigned)((a.S * a.H + 3) / 4));
-  return a.out_bf16 ? launch_dependent(paged_join_kernel<__nv_bfloat16>, grid, 128, 0, stream, a)
-                    : launch_dependent(paged_join_kernel<float>, grid, 128, 0, stream, a);
+  const dim3 grid((unsigned)(a.S * a.H));
+  return a.out_bf16 ? launch_dependent(paged_join_kernel<__nv_bfloat16>, grid, 32 * kWarps, 0, stream, a)
+                    : launch_dependent(paged_join_kernel<float>, grid, 32 * kWarps, 0, stream, a);
 }
 
 }  // namespace la

@@ -26,9 +26,14 @@ constexpr int kWarps = 4;
 constexpr float kSlack = 8.f;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -160,28 +165,39 @@ __device__ __forceinline__ void finish(const PagedDecodeLaunch& a, const Part& p
 template <int T, int kRowsUsed, typename Tokens>
 __device__ __forceinline__ void bias_and_mask(const PagedDecodeLaunch& a, float (&x)[T][4], const float (&slope)[2], float scale, float inv_cap,
                                               int age0, uint32_t seen, uint32_t whole, Tokens tokens) {
-#pragma unroll
-  for (int i = 0; i < kRowsUsed; ++i)
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-#pragma unroll
-      for (int e = 2 * i; e < 2 * i + 2; ++e) {
-        float y = x[t][e];
-        if (a.softcap != 0.f) y = capped(y * a.scale, a.softcap, inv_cap) * kLog2e;
-        else y *= scale;
-        if (a.slopes) y = fmaf(-slope[i], (float)(age0 - tokens(t, e & 1)), y);
-        x[t][e] = y;
-      }
-  if (seen != whole) {
+  auto each = [&](auto fn) {
 #pragma unroll
     for (int i = 0; i < kRowsUsed; ++i)
 #pragma unroll
       for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int e = 2 * i; e < 2 * i + 2; ++e)
-          if (!(seen >> tokens(t, e & 1) & 1u)) x[t][e] = -INFINITY;
-  }
+        for (int e = 2 * i; e < 2 * i + 2; ++e) x[t][e] = fn(x[t][e], i, t, e & 1);
+  };
+  if (a.softcap != 0.f) each([&](float y, int, int, int) { return capped(y * a.scale, a.softcap, inv_cap) * kLog2e; });
+  else each([&](float y, int, int, int) { return y * scale; });
+  if (a.slopes) each([&](float y, int i, int t, int e) { return fmaf(-slope[i], (float)(age0 - tokens(t, e)), y); });
+  if (seen != whole) each([&](float y, int, int t, int e) { return seen >> tokens(t, e) & 1u ? y : -INFINITY; });
 }
+
+// Where a warp's tiles lie in the table: the tiles are `step` tokens apart, and a division at every one would cost as much as
+// a product.
+struct Place {
+  int column, slot, step_columns, step_slots, page;
+  __device__ __forceinline__ Place(int token, int step, int page_) : page(page_) {
+    column = token / page;
+    slot = token - column * page;
+    step_columns = step / page;
+    step_slots = step - step_columns * page;
+  }
+  __device__ __forceinline__ void advance() {
+    column += step_columns;
+    slot += step_slots;
+    if (slot >= page) {
+      slot -= page;
+      ++column;
+    }
+  }
+};
 
 // Bits of the tokens [t0, t0 + n) that lie in [lo, hi).
 __device__ __forceinline__ uint32_t token_bits(int t0, int n, int lo, int hi) {
@@ -219,19 +235,22 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
   auto at = [](int r, int ch) { return (uint32_t)(r * (DP * 2) + ((ch ^ (r & 7)) << 4)); };
 
   const int tiles = p.last > p.first ? (p.last - p.first + kTile - 1) / kTile : 0;
-  auto lookup = [&](int i) {  // the page of this warp's i-th tile, -1 behind the last one or where there is none
-    const int t = warp + i * kWarps;
-    if (t >= tiles) return -1;
-    const int pg = table_page(a.c, p.s, (p.first + t * kTile) / page);
-    if (pg < 0 && p.hk == 0 && lane == 0) atomicOr(a.c.status, kStatusBadIndex);
-    return pg;
+  struct Next { int page, slot; };
+  auto lookup = [&](Place& at, int i) {  // where this warp's i-th tile lies: page -1 behind the last one or where there is none
+    Next n{-1, at.slot};
+    if (warp + i * kWarps < tiles) {
+      n.page = table_page(a.c, p.s, at.column);
+      if (n.page < 0 && p.hk == 0 && lane == 0) atomicOr(a.c.status, kStatusBadIndex);
+    }
+    at.advance();
+    return n;
   };
-  auto fetch = [&](int i, int pg) {  // this warp's i-th tile into its stage
-    const int t0 = p.first + (warp + i * kWarps) * kTile, stage = i % kS;
-    const uint32_t seen = pg < 0 ? 0u : token_bits(t0, kTile, p.seen.lo, p.last);
+  auto fetch = [&](int i, int stage, Next n) {  // this warp's i-th tile into its stage
+    const int t0 = p.first + (warp + i * kWarps) * kTile;
+    const uint32_t seen = n.page < 0 ? 0u : token_bits(t0, kTile, p.seen.lo, p.last);
     if (lane == 0) s_seen[warp][stage] = seen;
-    if (pg < 0) return;
-    const int64_t from = ((pg * a.c.Hkv + p.hk) * page + t0 % page) * d;
+    if (n.page < 0) return;
+    const int64_t from = ((n.page * a.c.Hkv + p.hk) * page + n.slot) * d;
     const uint32_t to = base + stage * kTileBytes<DP>;
 #pragma unroll
     for (int j = 0; j < kTile * kChunks / 32; ++j) {
@@ -269,34 +288,36 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
     for (int t = 0; t < 2 * kSteps; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
-    int next = lookup(0);
+    Place place(p.first + warp * kTile, kWarps * kTile, page);
+    Next next = lookup(place, 0);
 #pragma unroll
     for (int i = 0; i < kS - 1; ++i) {
-      if (i < mine) fetch(i, next);
+      if (i < mine) fetch(i, i, next);
       tc::cp_async_commit();
-      next = lookup(i + 1);
+      next = lookup(place, i + 1);
     }
-    for (int i = 0; i < mine; ++i) {
+    for (int i = 0, stage = 0, into = kS - 1; i < mine; ++i, stage = stage + 1 == kS ? 0 : stage + 1, into = into + 1 == kS ? 0 : into + 1) {
       cp_async_wait<kS - 2>();
       __syncwarp();  // every lane's copies of this tile are in, and its reads of the stage that is filled next are done
-      if (i + kS - 1 < mine) fetch(i + kS - 1, next);
+      if (i + kS - 1 < mine) fetch(i + kS - 1, into, next);
       tc::cp_async_commit();
-      next = lookup(i + kS);
-      const int stage = i % kS;
+      next = lookup(place, i + kS);
       const uint32_t keys = base + stage * kTileBytes<DP>, vals = keys + kTileBytes<DP> / 2;
       const uint32_t seen = s_seen[warp][stage];
       if (seen == 0u) continue;
       float x[2][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
-#pragma unroll
       for (int k = 0; k < kSteps; ++k) {
         uint32_t b[4];
         ldmatrix(b, keys + at((lane >> 4) * 8 + (lane & 7), 2 * k + ((lane >> 3) & 1)));
-        mma16816(x[0], qa[k][0], kSpare ? 0u : qa[k][2 * kRows - 2], qa[k][1], kSpare ? 0u : qa[k][2 * kRows - 1], b[0], b[1]);
-        mma16816(x[1], qa[k][0], kSpare ? 0u : qa[k][2 * kRows - 2], qa[k][1], kSpare ? 0u : qa[k][2 * kRows - 1], b[2], b[3]);
+        const uint32_t a0 = qa[k][0], a1 = kSpare ? 0u : qa[k][2 * kRows - 2], a2 = qa[k][1], a3 = kSpare ? 0u : qa[k][2 * kRows - 1];
+        if (k == 0) {
+          mma16816_first(x[0], a0, a1, a2, a3, b[0], b[1]);
+          mma16816_first(x[1], a0, a1, a2, a3, b[2], b[3]);
+        } else {
+          mma16816(x[0], a0, a1, a2, a3, b[0], b[1]);
+          mma16816(x[1], a0, a1, a2, a3, b[2], b[3]);
+        }
       }
       const int t0 = p.first + (warp + i * kWarps) * kTile;
       bias_and_mask<2, kRows>(a, x, slope, scale, inv_cap, p.seen.hi - 1 - t0, seen, 0xffffu, [&](int t, int e) { return t * 8 + q4 * 2 + e; });
@@ -388,11 +409,12 @@ constexpr int kRing4 = kStages4 * kTileBytes4<D>;
 template <int D>
 constexpr int kSmem4 = kWarps * (kRing4<D> + 2 * kPair * (D / kGroup) * 8);
 
-// (1 + code / 16) of nibbles m and m + 4 of a word, as bf16
+// (1 + code / 16) of nibbles m and m + 4 of a word, as bf16.  `one`: two bf16 ones in a register that the compiler takes
+// for unknown, so that mask and or are one instruction.
 template <int m>
-__device__ __forceinline__ uint32_t ones(uint32_t w) {
+__device__ __forceinline__ uint32_t ones(uint32_t w, uint32_t one) {
   const uint32_t x = m == 0 ? w << 3 : w >> (4 * m - 3);
-  return (x & 0x00780078u) | 0x3f803f80u;
+  return (x & 0x00780078u) | one;
 }
 
 // Place of a row's 16-byte chunk: the rows that a product's lanes read together lie in different banks.
@@ -420,51 +442,56 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
   const int page = a.c.page;
   uint8_t* region = pd_smem + warp * kRing4<D>;
   const uint32_t base = tc::smem_u32(region);
-  float2* factors = reinterpret_cast<float2*>(pd_smem + kWarps * kRing4<D>) + warp * 2 * kPair * kGroups;
+  float* factors = reinterpret_cast<float*>(pd_smem + kWarps * kRing4<D>) + warp * 2 * kPair * 2 * kGroups;
   const int64_t size = page_bytes(a.c);
 
   const int tiles = p.last > p.first ? (p.last - p.first + kPair - 1) / kPair : 0;
-  struct Pages { int a, b; };
-  auto lookup = [&](int i) {  // the pages of this warp's i-th tile
-    Pages g{-1, -1};
-    const int t = warp + i * kWarps, t0 = p.first + t * kPair;
-    if (t >= tiles) return g;
-    g.a = table_page(a.c, p.s, t0 / page);
-    if (t0 + kTile < p.last) g.b = table_page(a.c, p.s, (t0 + kTile) / page);
-    if ((g.a < 0 || (g.b < 0 && t0 + kTile < p.last)) && p.hk == 0 && lane == 0) atomicOr(a.c.status, kStatusBadIndex);
-    return g;
+  struct Next { int page[2], slot[2]; };  // of the tile's two sixteenths
+  auto lookup = [&](Place& at, int i) {    // page -1 behind the last token or where there is none
+    const bool wraps = at.slot + kTile >= page;
+    Next n{{-1, -1}, {at.slot, wraps ? 0 : at.slot + kTile}};
+    const int t0 = p.first + (warp + i * kWarps) * kPair;
+    if (t0 < p.last) {
+      n.page[0] = table_page(a.c, p.s, at.column);
+      if (t0 + kTile < p.last) n.page[1] = table_page(a.c, p.s, wraps ? at.column + 1 : at.column);
+      if ((n.page[0] < 0 || (n.page[1] < 0 && t0 + kTile < p.last)) && p.hk == 0 && lane == 0) atomicOr(a.c.status, kStatusBadIndex);
+    }
+    at.advance();
+    return n;
   };
-  auto fetch = [&](int i, Pages g) {
-    const int t0 = p.first + (warp + i * kWarps) * kPair, stage = i % kS;
+  const uint8_t* kp = static_cast<const uint8_t*>(a.c.k) + p.hk * size;
+  const uint8_t* vp = static_cast<const uint8_t*>(a.c.v) + p.hk * size;
+  const int64_t page_size = a.c.Hkv * size;
+  // a lane's places in a tile: of the codes' chunk `lane` (later ones lie 32 chunks on), and of the scales'
+  const int meta_half = lane / kHalfMeta & 1;
+  const uint8_t* meta_pool = lane < 2 * kHalfMeta ? kp : vp;
+  const int meta_to = 2 * kCodes<D> + lane / (2 * kHalfMeta) * kMeta<D> + meta_half * (kMeta<D> / 2) + lane % kHalfMeta * 16;
+  const int meta_from = page * (D / 2) + lane % kHalfMeta * 16;
+  auto fetch = [&](int i, int stage, const Next& n) {
+    const int t0 = p.first + (warp + i * kWarps) * kPair;
     uint32_t seen = token_bits(t0, kPair, p.seen.lo, p.last);
-    if (g.a < 0) seen &= 0xffff0000u;
-    if (g.b < 0) seen &= 0x0000ffffu;
+    if (n.page[0] < 0) seen &= 0xffff0000u;
+    if (n.page[1] < 0) seen &= 0x0000ffffu;
     if (lane == 0) s_seen[warp][stage] = seen;
     const uint32_t to = base + stage * kTileBytes4<D>;
-    const int slot[2] = {t0 % page, (t0 + kTile) % page};
-    const int64_t at[2] = {(max(g.a, 0) * a.c.Hkv + p.hk) * size, (max(g.b, 0) * a.c.Hkv + p.hk) * size};
-    const bool there[2] = {g.a >= 0, g.b >= 0};  // otherwise codes of anything, whose tokens have no scale and no weight
-    const uint8_t* kp = static_cast<const uint8_t*>(a.c.k);
-    const uint8_t* vp = static_cast<const uint8_t*>(a.c.v);
 #pragma unroll
-    for (int j = 0; j < 2 * kHalf / 32; ++j) {
-      const int h = 32 * j / kHalf, c = 32 * j % kHalf + lane;
-      if (!there[h]) continue;
-      const int64_t from = at[h] + slot[h] * (D / 2) + c * 16;
-      const uint32_t place = place4<D>(h * kTile + c / (D / 32), c % (D / 32));
-      tc::cp_async16(to + place, kp + from, 16u);
-      tc::cp_async16(to + kCodes<D> + place, vp + from, 16u);
+    for (int h = 0; h < 2; ++h) {
+      if (n.page[h] < 0) continue;  // codes of anything, whose tokens get no scale and no weight
+      const int64_t from = n.page[h] * page_size + n.slot[h] * (D / 2) + lane * 16;
+#pragma unroll
+      for (int j = 0; j < kHalf / 32; ++j) {
+        const uint32_t place = place4<D>(h * kTile + (lane + 32 * j) / (D / 32), (lane + 32 * j) % (D / 32));
+        tc::cp_async16(to + place, kp + from + j * 512, 16u);
+        tc::cp_async16(to + kCodes<D> + place, vp + from + j * 512, 16u);
+      }
     }
-    if (lane < 4 * kHalfMeta) {
-      const int c = lane % kHalfMeta, h = lane / kHalfMeta & 1, v = lane / (2 * kHalfMeta);
-      const int64_t from = (h ? at[1] : at[0]) + page * (D / 2) + (h ? slot[1] : slot[0]) * (kGroups * 4) + c * 16;
-      if (h ? there[1] : there[0]) tc::cp_async16(to + 2 * kCodes<D> + v * kMeta<D> + h * (kMeta<D> / 2) + c * 16, (v ? vp : kp) + from, 16u);
-    }
+    const int pg = meta_half ? n.page[1] : n.page[0], slot = meta_half ? n.slot[1] : n.slot[0];
+    if (lane < 4 * kHalfMeta && pg >= 0) tc::cp_async16(to + meta_to, meta_pool + pg * page_size + meta_from + slot * (kGroups * 4), 16u);
   };
 
   // ---- queries as operands: word e = 2 q4 + u of group g holds elements 64 g + 8 e + (0..7), whose pairs (m, m + 4) are a
   // product's neighbours; and the groups' sums of them
-  uint32_t qa[kGroups][2][4][kRows];  // [group][word][m][row]
+  uint32_t qa[kGroups][2][4 * kRows];  // [group][word][m, row]
   float qs[kGroups][2] = {}, slope[2] = {0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
@@ -481,10 +508,8 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
         float v[8];
         r.unpack(v);
         const uint32_t x[4] = {r.w.x, r.w.y, r.w.z, r.w.w};  // pairs (0, 1) (2, 3) (4, 5) (6, 7)
-        qa[g][u][0][i] = __byte_perm(x[0], x[2], 0x5410);
-        qa[g][u][1][i] = __byte_perm(x[0], x[2], 0x7632);
-        qa[g][u][2][i] = __byte_perm(x[1], x[3], 0x5410);
-        qa[g][u][3][i] = __byte_perm(x[1], x[3], 0x7632);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) qa[g][u][m * kRows + i] = __byte_perm(x[m / 2], x[2 + m / 2], m & 1 ? 0x7632 : 0x5410);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum += v[e];
       }
@@ -493,52 +518,87 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
     }
     if (a.slopes && h < p.group) slope[i] = a.slopes[p.h0 + h] * kLog2e;
   }
+  uint32_t one = 0x3f803f80u;
+  asm volatile("" : "+r"(one));
   const float scale = a.scale * kLog2e, inv_cap = 1.f / a.softcap;
   // tile t's column c is this token of the warp's 32, so that a lane's four weights of a 16-token product are tokens
   // q4, q4 + 4, q4 + 8, q4 + 12 of it
   auto token = [](int t, int c) { return (t >> 1) * kTile + (c >> 1) + 4 * (2 * (t & 1) + (c & 1)); };
 
-  float o[8 * kGroups][4], bias[kGroups][2] = {};  // sums of products; of offsets, a lane's tokens'
+  // Sums of products, elements as rows and heads as columns: [heads 0-7, 8-15][group, m], elements 8 row + m (and that + 4) of
+  // the group, heads 2 q4 and 2 q4 + 1.  The scores' layout is that of such a product's second operand.
+  float o[kRows][4 * kGroups][4], bias[kGroups][2] = {};  // bias: sums of offsets, of head `row` and a lane's tokens
 #pragma unroll
-  for (int t = 0; t < 8 * kGroups; ++t)
+  for (int u = 0; u < kRows; ++u)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+    for (int t = 0; t < 4 * kGroups; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[u][t][e] = 0.f;
   Running run;
   const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-  Pages next = lookup(0);
+  // where a lane's words lie: of keys, of values of tokens q4 and q4 + 4; eight tokens on are 8 rows on, whatever the place
+  const int key_at = place4<D>(token(0, row), D == 128 ? q4 : q4 >> 1) + (D == 128 ? 0 : (q4 & 1) * 8);
+  int val_at[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    val_at[j] = kCodes<D> + (D == 128 ? place4<D>(q4 + 4 * j, row >> 1) + (row & 1) * 8 : place4<D>(q4 + 4 * j, row >> 2) + (row & 3) * 4);
+  Place place(p.first + warp * kPair, kWarps * kPair, page);
+  Next next = lookup(place, 0);
 #pragma unroll
   for (int i = 0; i < kS - 1; ++i) {
-    if (i < mine) fetch(i, next);
+    if (i < mine) fetch(i, i, next);
     tc::cp_async_commit();
-    next = lookup(i + 1);
+    next = lookup(place, i + 1);
   }
-  for (int i = 0; i < mine; ++i) {
+  for (int i = 0, stage = 0, into = kS - 1; i < mine; ++i, stage = stage + 1 == kS ? 0 : stage + 1, into = into + 1 == kS ? 0 : into + 1) {
     cp_async_wait<kS - 2>();
     __syncwarp();  // every lane's copies of this tile are in, and its reads of the stage that is filled next are done
-    if (i + kS - 1 < mine) fetch(i + kS - 1, next);
+    if (i + kS - 1 < mine) fetch(i + kS - 1, into, next);
     tc::cp_async_commit();
-    next = lookup(i + kS);
-    const int stage = i % kS;
-    const uint8_t* keys = region + stage * kTileBytes4<D>;
-    const uint8_t* vals = keys + kCodes<D>;
-    const uint32_t* meta = reinterpret_cast<const uint32_t*>(vals + kCodes<D>);
+    next = lookup(place, i + kS);
+    const uint8_t* tile = region + stage * kTileBytes4<D>;
+    const uint32_t* meta = reinterpret_cast<const uint32_t*>(tile + 2 * kCodes<D>);
     const uint32_t seen = s_seen[warp][stage];
     // ---- a token a lane: 16 scale and offset - 16 scale
 #pragma unroll
-    for (int v = 0; v < 2; ++v)
+    for (int v = 0; v < 2; ++v) {
+      uint32_t w[kGroups];
+      float f[2 * kGroups];
+      if constexpr (D == 128) {
+        const uint2 x = *reinterpret_cast<const uint2*>(meta + (v * kPair + lane) * kGroups);
+        w[0] = x.x; w[1] = x.y;
+      } else {
+        w[0] = meta[v * kPair + lane];
+      }
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        const uint32_t w = meta[(v * kPair + lane) * kGroups + g];
-        const float s = 16.f * __uint_as_float(w << 16);
-        const bool on = seen >> lane & 1u;
-        factors[(v * kPair + lane) * kGroups + g] = on ? make_float2(s, __uint_as_float(w & 0xffff0000u) - s) : make_float2(0.f, 0.f);
+        f[2 * g] = 16.f * __uint_as_float(w[g] << 16);
+        f[2 * g + 1] = __uint_as_float(w[g] & 0xffff0000u) - f[2 * g];
       }
+      if (!(seen >> lane & 1u)) {
+#pragma unroll
+        for (int e = 0; e < 2 * kGroups; ++e) f[e] = 0.f;
+      }
+      float* to = factors + (v * kPair + lane) * 2 * kGroups;
+      if constexpr (D == 128) *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
+      else *reinterpret_cast<float2*>(to) = make_float2(f[0], f[1]);
+    }
     __syncwarp();
+    auto factors_of = [&](int v, int token, float (&f)[2 * kGroups]) {
+      const float* from = factors + (v * kPair + token) * 2 * kGroups;
+      if constexpr (D == 128) {
+        const float4 x = *reinterpret_cast<const float4*>(from);
+        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(from);
+        f[0] = x.x; f[1] = x.y;
+      }
+    };
     // ---- scores
     float x[4][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const uint8_t* at = keys + place4<D>(token(t, row), D == 128 ? q4 : q4 >> 1) + (D == 128 ? 0 : (q4 & 1) * 8);
+      const uint8_t* at = tile + key_at + t * 8 * (D / 2);
       uint32_t w[kGroups][2];  // [group][word]
       if constexpr (D == 128) {
         const uint4 c = *reinterpret_cast<const uint4*>(at);
@@ -547,27 +607,42 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
         const uint2 c = *reinterpret_cast<const uint2*>(at);
         w[0][0] = c.x; w[0][1] = c.y;
       }
-      float y[kGroups][4];
+      float y[kGroups][4], z[kGroups][4];
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[g][e] = 0.f;
+      for (int g = 0; g < kGroups; ++g)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          mma16816(y[g], qa[g][u][0][0], kSpare ? 0u : qa[g][u][0][kRows - 1], qa[g][u][1][0], kSpare ? 0u : qa[g][u][1][kRows - 1], ones<0>(w[g][u]),
-                   ones<1>(w[g][u]));
-          mma16816(y[g], qa[g][u][2][0], kSpare ? 0u : qa[g][u][2][kRows - 1], qa[g][u][3][0], kSpare ? 0u : qa[g][u][3][kRows - 1], ones<2>(w[g][u]),
-                   ones<3>(w[g][u]));
+          const uint32_t(&q)[4 * kRows] = qa[g][u];
+          const uint32_t b0 = ones<0>(w[g][u], one), b1 = ones<1>(w[g][u], one), b2 = ones<2>(w[g][u], one), b3 = ones<3>(w[g][u], one);
+          if constexpr (kSpare) {
+            // Four registers of one head's elements as one operand, m = 0 and 2 in its rows 0 to 7, 1 and 3 in the others: the
+            // rows that do not match a product's second operand are not used (zeros for them would take registers, or moves).
+            if (u == 0) {
+              mma16816_first(y[g], q[0], q[1], q[2], q[3], b0, b2);
+              mma16816_first(z[g], q[0], q[1], q[2], q[3], b1, b3);
+            } else {
+              mma16816(y[g], q[0], q[1], q[2], q[3], b0, b2);
+              mma16816(z[g], q[0], q[1], q[2], q[3], b1, b3);
+            }
+          } else {
+            if (u == 0) mma16816_first(y[g], q[0], q[1], q[2], q[3], b0, b1);
+            else mma16816(y[g], q[0], q[1], q[2], q[3], b0, b1);
+            mma16816(y[g], q[4 * kRows - 4], q[4 * kRows - 3], q[4 * kRows - 2], q[4 * kRows - 1], b2, b3);
+          }
         }
-      }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float2* f = factors + token(t, 2 * q4 + c) * kGroups;
+        float f[2 * kGroups];
+        factors_of(0, token(t, 2 * q4 + c), f);
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
           float sum = 0.f;
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g) sum = fmaf(f[g].x, y[g][2 * u + c], fmaf(f[g].y, qs[g][u], sum));
+          for (int g = 0; g < kGroups; ++g) {
+            const float product = kSpare ? y[g][c] + z[g][2 + c] : y[g][2 * u + c];
+            sum = g == 0 ? f[1] * qs[0][u] : fmaf(f[2 * g + 1], qs[g][u], sum);
+            sum = fmaf(f[2 * g], product, sum);
+          }
           x[t][2 * u + c] = sum;
         }
       }
@@ -577,59 +652,57 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
     float f[2];
     if (weigh<4, kRows>(run, x, f)) {
 #pragma unroll
-      for (int t = 0; t < 8 * kGroups; ++t)
+      for (int u = 0; u < kRows; ++u) {
+        const float f0 = __shfl_sync(kFullMask, f[u], 8 * q4), f1 = __shfl_sync(kFullMask, f[u], 8 * q4 + 4);  // of heads 2 q4, 2 q4 + 1
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[t][e] *= f[kSpare ? 0 : e >> 1];
+        for (int t = 0; t < 4 * kGroups; ++t) {
+          o[u][t][0] *= f0; o[u][t][1] *= f1; o[u][t][2] *= f0; o[u][t][3] *= f1;
+        }
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) bias[g][u] *= f[u];
+        for (int g = 0; g < kGroups; ++g) bias[g][u] *= f[u];
+      }
     }
     // ---- values, 16 tokens a product
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       uint32_t w[4][kGroups];  // the word e = row of each group, of tokens q4 + 4 j
+      float f[4][2 * kGroups];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = ks * kTile + q4 + 4 * j;
+        const uint8_t* at = tile + val_at[j & 1] + (2 * ks + (j >> 1)) * 8 * (D / 2);
         if constexpr (D == 128) {
-          const uint2 c = *reinterpret_cast<const uint2*>(vals + place4<D>(r, row >> 1) + (row & 1) * 8);
+          const uint2 c = *reinterpret_cast<const uint2*>(at);
           w[j][0] = c.x; w[j][1] = c.y;
         } else {
-          w[j][0] = *reinterpret_cast<const uint32_t*>(vals + place4<D>(r, row >> 2) + (row & 3) * 4);
+          w[j][0] = *reinterpret_cast<const uint32_t*>(at);
         }
+        factors_of(1, ks * kTile + q4 + 4 * j, f[j]);
       }
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        uint32_t major[4], minor[4];  // [j / 2][row]
+        uint32_t major[kRows][2], minor[kRows][2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float2 fa = factors[(kPair + ks * kTile + q4 + 8 * t) * kGroups + g], fb = factors[(kPair + ks * kTile + q4 + 8 * t + 4) * kGroups + g];
+        for (int u = 0; u < kRows; ++u)
 #pragma unroll
-          for (int u = 0; u < kRows; ++u) {
+          for (int t = 0; t < 2; ++t) {
             const float pa = x[2 * ks + t][2 * u], pb = x[2 * ks + t][2 * u + 1];
-            bias[g][u] = fmaf(pa, fa.y, fmaf(pb, fb.y, bias[g][u]));
-            two_parts(pa * fa.x, pb * fb.x, major[2 * t + u], minor[2 * t + u]);
+            bias[g][u] = fmaf(pa, f[2 * t][2 * g + 1], fmaf(pb, f[2 * t + 1][2 * g + 1], bias[g][u]));
+            two_parts(pa * f[2 * t][2 * g], pb * f[2 * t + 1][2 * g], major[u][t], minor[u][t]);
           }
-        }
-        if constexpr (kSpare) {
-          major[1] = minor[0];
-          major[3] = minor[2];
-        }
+        // words of two tokens side by side: elements 0 to 3 in `lo`, 4 to 7 in `hi`
         const uint32_t lo0 = __byte_perm(w[0][g], w[1][g], 0x5410), hi0 = __byte_perm(w[0][g], w[1][g], 0x7632);
         const uint32_t lo1 = __byte_perm(w[2][g], w[3][g], 0x5410), hi1 = __byte_perm(w[2][g], w[3][g], 0x7632);
-        auto product = [&](int n, uint32_t b0, uint32_t b1) {  // elements 8 e + n of the group
-          mma16816(o[8 * g + n], major[0], major[1], major[2], major[3], b0, b1);
-          if constexpr (!kSpare) mma16816(o[8 * g + n], minor[0], minor[1], minor[2], minor[3], b0, b1);
+        auto product = [&](int m, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+          for (int u = 0; u < kRows; ++u) {
+            mma16816(o[u][4 * g + m], a0, a1, a2, a3, major[u][0], major[u][1]);
+            mma16816(o[u][4 * g + m], a0, a1, a2, a3, minor[u][0], minor[u][1]);
+          }
         };
-        product(0, ones<0>(lo0), ones<0>(lo1));
-        product(1, ones<1>(lo0), ones<1>(lo1));
-        product(2, ones<2>(lo0), ones<2>(lo1));
-        product(3, ones<3>(lo0), ones<3>(lo1));
-        product(4, ones<0>(hi0), ones<0>(hi1));
-        product(5, ones<1>(hi0), ones<1>(hi1));
-        product(6, ones<2>(hi0), ones<2>(hi1));
-        product(7, ones<3>(hi0), ones<3>(hi1));
+        product(0, ones<0>(lo0, one), ones<0>(hi0, one), ones<0>(lo1, one), ones<0>(hi1, one));
+        product(1, ones<1>(lo0, one), ones<1>(hi0, one), ones<1>(lo1, one), ones<1>(hi1, one));
+        product(2, ones<2>(lo0, one), ones<2>(hi0, one), ones<2>(lo1, one), ones<2>(hi1, one));
+        product(3, ones<3>(lo0, one), ones<3>(hi0, one), ones<3>(lo1, one), ones<3>(hi1, one));
       }
     }
     __syncwarp();  // the factors are used up
@@ -652,14 +725,15 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
       float off = bias[g][u];
       off += __shfl_xor_sync(kFullMask, off, 1);
       off += __shfl_xor_sync(kFullMask, off, 2);
-      if (row + 8 * u >= p.group) continue;
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float y = o[8 * g + n][2 * u + c] + (kSpare ? o[8 * g + n][2 + c] : 0.f);
-          part[(row + 8 * u) * D + kGroup * g + 8 * (2 * q4 + c) + n] = y + off;
-        }
+      for (int c = 0; c < 2; ++c) {
+        const int h = 2 * q4 + c + 8 * u;
+        const float y = __shfl_sync(kFullMask, off, 4 * (2 * q4 + c));
+        if (h >= p.group) continue;
+        float4* to = reinterpret_cast<float4*>(part + h * D + kGroup * g + 8 * row);
+        to[0] = make_float4(o[u][4 * g][c] + y, o[u][4 * g + 1][c] + y, o[u][4 * g + 2][c] + y, o[u][4 * g + 3][c] + y);
+        to[1] = make_float4(o[u][4 * g][2 + c] + y, o[u][4 * g + 1][2 + c] + y, o[u][4 * g + 2][2 + c] + y, o[u][4 * g + 3][2 + c] + y);
+      }
     }
   }
   __syncthreads();
