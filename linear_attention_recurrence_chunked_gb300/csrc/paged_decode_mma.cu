@@ -85,8 +85,9 @@ __device__ __forceinline__ bool part_of(const PagedDecodeLaunch& a, Part& p) {
 }
 
 // The running softmax of a warp: rows lane / 4 (0) and that + 8 (1), a quad's lanes with the same maximum and sums of their own.
+// No score is below the first maximum but -infinity, whose weight is zero beside any.
 struct Running {
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m[2] = {-3.402823466e38f, -3.402823466e38f}, l[2] = {0.f, 0.f};
 };
 
 // Scores of T tiles of eight tokens into weights; f: the factors of the sums so far, and whether they are not one.
@@ -101,26 +102,25 @@ __device__ __forceinline__ bool weigh(Running& r, float (&x)[T][4], float (&f)[2
     for (int t = 0; t < T; ++t) y = fmaxf(y, fmaxf(x[t][2 * i], x[t][2 * i + 1]));
     y = fmaxf(y, __shfl_xor_sync(kFullMask, y, 1));
     top[i] = fmaxf(y, __shfl_xor_sync(kFullMask, y, 2));
-    moves |= top[i] > r.m[i] + kSlack;  // from -infinity too
+    moves |= top[i] > r.m[i] + kSlack;
   }
   moves = __any_sync(kFullMask, moves);
   if (moves) {
 #pragma unroll
     for (int i = 0; i < kRowsUsed; ++i) {
       const float m = fmaxf(r.m[i], top[i]);
-      f[i] = ex2(r.m[i] - (m == -INFINITY ? 0.f : m));
+      f[i] = ex2(r.m[i] - m);
       r.m[i] = m;
       r.l[i] *= f[i];
     }
   }
 #pragma unroll
   for (int i = 0; i < kRowsUsed; ++i) {
-    const float base = r.m[i] == -INFINITY ? 0.f : r.m[i];
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
       for (int e = 2 * i; e < 2 * i + 2; ++e) {
-        x[t][e] = ex2(x[t][e] - base);
+        x[t][e] = ex2(x[t][e] - r.m[i]);
         r.l[i] += x[t][e];
       }
   }
@@ -136,12 +136,11 @@ __device__ __forceinline__ void finish(const PagedDecodeLaunch& a, const Part& p
     float top = s_m[0][g];
 #pragma unroll
     for (int u = 1; u < kWarps; ++u) top = fmaxf(top, s_m[u][g]);
-    const float base = top == -INFINITY ? 0.f : top;
     float2 sum = make_float2(0.f, 0.f);
     float total = 0.f;
 #pragma unroll
     for (int u = 0; u < kWarps; ++u) {
-      const float w = ex2(s_m[u][g] - base);
+      const float w = ex2(s_m[u][g] - top);
       const float2 y = *reinterpret_cast<const float2*>(values + u * stride + e);
       sum.x = fmaf(w, y.x, sum.x);
       sum.y = fmaf(w, y.y, sum.y);
@@ -160,11 +159,14 @@ __device__ __forceinline__ void finish(const PagedDecodeLaunch& a, const Part& p
   }
 }
 
+// What a product is multiplied by: scores are in units of log2, but in front of a cap.
+__device__ __forceinline__ float score_scale(const PagedDecodeLaunch& a) { return a.softcap != 0.f ? a.scale : a.scale * kLog2e; }
+
 // A warp's rows of scores: caps, biases and what is not seen.  tokens(t, e): of tile t, entry e's token's distance from the
 // warp tile's first one.
 template <int T, int kRowsUsed, typename Tokens>
-__device__ __forceinline__ void bias_and_mask(const PagedDecodeLaunch& a, float (&x)[T][4], const float (&slope)[2], float scale, float inv_cap,
-                                              int age0, uint32_t seen, uint32_t whole, Tokens tokens) {
+__device__ __forceinline__ void bias_and_mask(const PagedDecodeLaunch& a, float (&x)[T][4], const float (&slope)[2], float inv_cap, int age0,
+                                              uint32_t seen, uint32_t whole, Tokens tokens) {
   auto each = [&](auto fn) {
 #pragma unroll
     for (int i = 0; i < kRowsUsed; ++i)
@@ -173,8 +175,7 @@ __device__ __forceinline__ void bias_and_mask(const PagedDecodeLaunch& a, float 
 #pragma unroll
         for (int e = 2 * i; e < 2 * i + 2; ++e) x[t][e] = fn(x[t][e], i, t, e & 1);
   };
-  if (a.softcap != 0.f) each([&](float y, int, int, int) { return capped(y * a.scale, a.softcap, inv_cap) * kLog2e; });
-  else each([&](float y, int, int, int) { return y * scale; });
+  if (a.softcap != 0.f) each([&](float y, int, int, int) { return capped(y, a.softcap, inv_cap) * kLog2e; });
   if (a.slopes) each([&](float y, int i, int t, int e) { return fmaf(-slope[i], (float)(age0 - tokens(t, e)), y); });
   if (seen != whole) each([&](float y, int, int t, int e) { return seen >> tokens(t, e) & 1u ? y : -INFINITY; });
 }
@@ -278,7 +279,7 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
       }
     if (a.slopes && g < p.group) slope[i] = a.slopes[p.h0 + g] * kLog2e;
   }
-  const float scale = a.scale * kLog2e, inv_cap = 1.f / a.softcap;
+  const float scale = score_scale(a), inv_cap = 1.f / a.softcap;
 
   float o[2 * kSteps][4];
   Running run;
@@ -320,7 +321,11 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
         }
       }
       const int t0 = p.first + (warp + i * kWarps) * kTile;
-      bias_and_mask<2, kRows>(a, x, slope, scale, inv_cap, p.seen.hi - 1 - t0, seen, 0xffffu, [&](int t, int e) { return t * 8 + q4 * 2 + e; });
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2 * kRows; ++e) x[t][e] *= scale;
+      bias_and_mask<2, kRows>(a, x, slope, inv_cap, p.seen.hi - 1 - t0, seen, 0xffffu, [&](int t, int e) { return t * 8 + q4 * 2 + e; });
       float f[2];
       if (weigh<2, kRows>(run, x, f)) {
 #pragma unroll
@@ -405,16 +410,27 @@ template <int D>
 constexpr int kTileBytes4 = 2 * (kCodes<D> + kMeta<D>);  // codes of keys and values, then their scales and offsets
 template <int D>
 constexpr int kRing4 = kStages4 * kTileBytes4<D>;
-// ... and each token's 16 scale and offset - 16 scale, of its keys' groups and of its values'
+// Where sixteen tokens lie in the pools, and which of them the query sees.
+struct __align__(16) Spot {
+  int64_t codes;  // byte of the first one's codes, or -1: no page
+  int meta;       // from there to its scales and offsets
+  uint32_t seen;
+};
+constexpr int kBatch = 16;  // tiles that a warp looks up at once; the spots of two batches are kept
+// ... and each token's 16 scale and offset - 16 scale, of its keys' groups and of its values', and the spots
 template <int D>
-constexpr int kSmem4 = kWarps * (kRing4<D> + 2 * kPair * (D / kGroup) * 8);
+constexpr int kFactors = 2 * kPair * (D / kGroup) * 8;
+template <int D>
+constexpr int kSmem4 = kWarps * (kRing4<D> + kFactors<D> + 4 * kBatch * (int)sizeof(Spot));
 
-// (1 + code / 16) of nibbles m and m + 4 of a word, as bf16.  `one`: two bf16 ones in a register that the compiler takes
-// for unknown, so that mask and or are one instruction.
+// (1 + code / 16) of nibbles m and m + 4 of a word, as bf16.  `one`: two bf16 ones, in a register so that mask and or are
+// one instruction (from C the compiler made two, 1.3 times the whole kernel's).
 template <int m>
 __device__ __forceinline__ uint32_t ones(uint32_t w, uint32_t one) {
   const uint32_t x = m == 0 ? w << 3 : w >> (4 * m - 3);
-  return (x & 0x00780078u) | one;
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x00780078, %2, 0xea;" : "=r"(r) : "r"(x), "r"(one));  // (x & mask) | one
+  return r;
 }
 
 // Place of a row's 16-byte chunk: the rows that a product's lanes read together lie in different banks.
@@ -433,7 +449,6 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
   constexpr int kHalfMeta = kTile * kGroups * 4 / 16;  // and of their scales and offsets
   extern __shared__ __align__(128) uint8_t pd_smem[];
   __shared__ float s_m[kWarps][16], s_l[kWarps][16];
-  __shared__ uint32_t s_seen[kWarps][kS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, q4 = lane & 3;
   grid_dependents_trigger();
   grid_dependency_wait();
@@ -442,51 +457,53 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
   const int page = a.c.page;
   uint8_t* region = pd_smem + warp * kRing4<D>;
   const uint32_t base = tc::smem_u32(region);
-  float* factors = reinterpret_cast<float*>(pd_smem + kWarps * kRing4<D>) + warp * 2 * kPair * 2 * kGroups;
+  float* factors = reinterpret_cast<float*>(pd_smem + kWarps * kRing4<D> + warp * kFactors<D>);
+  Spot* spots = reinterpret_cast<Spot*>(pd_smem + kWarps * (kRing4<D> + kFactors<D>)) + warp * 4 * kBatch;
   const int64_t size = page_bytes(a.c);
 
   const int tiles = p.last > p.first ? (p.last - p.first + kPair - 1) / kPair : 0;
-  struct Next { int page[2], slot[2]; };  // of the tile's two sixteenths
-  auto lookup = [&](Place& at, int i) {    // page -1 behind the last token or where there is none
-    const bool wraps = at.slot + kTile >= page;
-    Next n{{-1, -1}, {at.slot, wraps ? 0 : at.slot + kTile}};
-    const int t0 = p.first + (warp + i * kWarps) * kPair;
-    if (t0 < p.last) {
-      n.page[0] = table_page(a.c, p.s, at.column);
-      if (t0 + kTile < p.last) n.page[1] = table_page(a.c, p.s, wraps ? at.column + 1 : at.column);
-      if ((n.page[0] < 0 || (n.page[1] < 0 && t0 + kTile < p.last)) && p.hk == 0 && lane == 0) atomicOr(a.c.status, kStatusBadIndex);
-    }
-    at.advance();
-    return n;
+  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+  // ---- where the tiles lie: sixteen tiles at a time, a sixteenth of a page a lane, their pages looked up sixteen tiles ahead
+  auto first_token = [&](int batch) { return p.first + (warp + (batch * kBatch + (lane >> 1)) * kWarps) * kPair + (lane & 1) * kTile; };
+  auto lookup = [&](int batch) {  // -1 behind the last token or where there is no page
+    const int t0 = first_token(batch);
+    if (t0 >= p.last) return -1;
+    const int pg = table_page(a.c, p.s, t0 / page);
+    if (pg < 0 && p.hk == 0) atomicOr(a.c.status, kStatusBadIndex);
+    return pg;
   };
-  const uint8_t* kp = static_cast<const uint8_t*>(a.c.k) + p.hk * size;
-  const uint8_t* vp = static_cast<const uint8_t*>(a.c.v) + p.hk * size;
-  const int64_t page_size = a.c.Hkv * size;
+  auto place = [&](int batch, int pg) {
+    const int t0 = first_token(batch), slot = t0 % page;
+    Spot n{-1, 0, 0u};
+    if (pg >= 0) {
+      n.codes = (pg * a.c.Hkv + p.hk) * size + slot * (D / 2);
+      n.meta = page * (D / 2) + slot * (kGroups * 4 - D / 2);
+      n.seen = token_bits(t0, kTile, p.seen.lo, p.last);
+    }
+    spots[batch % 2 * 32 + lane] = n;
+  };
   // a lane's places in a tile: of the codes' chunk `lane` (later ones lie 32 chunks on), and of the scales'
+  const uint8_t* kp = static_cast<const uint8_t*>(a.c.k) + lane * 16;
+  const uint8_t* vp = static_cast<const uint8_t*>(a.c.v) + lane * 16;
   const int meta_half = lane / kHalfMeta & 1;
-  const uint8_t* meta_pool = lane < 2 * kHalfMeta ? kp : vp;
+  const uint8_t* meta_pool = static_cast<const uint8_t*>(lane < 2 * kHalfMeta ? a.c.k : a.c.v) + lane % kHalfMeta * 16;
   const int meta_to = 2 * kCodes<D> + lane / (2 * kHalfMeta) * kMeta<D> + meta_half * (kMeta<D> / 2) + lane % kHalfMeta * 16;
-  const int meta_from = page * (D / 2) + lane % kHalfMeta * 16;
-  auto fetch = [&](int i, int stage, const Next& n) {
-    const int t0 = p.first + (warp + i * kWarps) * kPair;
-    uint32_t seen = token_bits(t0, kPair, p.seen.lo, p.last);
-    if (n.page[0] < 0) seen &= 0xffff0000u;
-    if (n.page[1] < 0) seen &= 0x0000ffffu;
-    if (lane == 0) s_seen[warp][stage] = seen;
+  auto fetch = [&](int i, int stage) {
+    const Spot* spot = spots + i % (2 * kBatch) * 2;
     const uint32_t to = base + stage * kTileBytes4<D>;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (n.page[h] < 0) continue;  // codes of anything, whose tokens get no scale and no weight
-      const int64_t from = n.page[h] * page_size + n.slot[h] * (D / 2) + lane * 16;
+      const int64_t from = spot[h].codes;
+      if (from < 0) continue;  // codes of anything, whose tokens get no scale and no weight
 #pragma unroll
       for (int j = 0; j < kHalf / 32; ++j) {
-        const uint32_t place = place4<D>(h * kTile + (lane + 32 * j) / (D / 32), (lane + 32 * j) % (D / 32));
-        tc::cp_async16(to + place, kp + from + j * 512, 16u);
-        tc::cp_async16(to + kCodes<D> + place, vp + from + j * 512, 16u);
+        const uint32_t at = place4<D>(h * kTile + (lane + 32 * j) / (D / 32), (lane + 32 * j) % (D / 32));
+        tc::cp_async16(to + at, kp + from + j * 512, 16u);
+        tc::cp_async16(to + kCodes<D> + at, vp + from + j * 512, 16u);
       }
     }
-    const int pg = meta_half ? n.page[1] : n.page[0], slot = meta_half ? n.slot[1] : n.slot[0];
-    if (lane < 4 * kHalfMeta && pg >= 0) tc::cp_async16(to + meta_to, meta_pool + pg * page_size + meta_from + slot * (kGroups * 4), 16u);
+    const Spot m = spot[meta_half];
+    if (lane < 4 * kHalfMeta && m.codes >= 0) tc::cp_async16(to + meta_to, meta_pool + m.codes + m.meta, 16u);
   };
 
   // ---- queries as operands: word e = 2 q4 + u of group g holds elements 64 g + 8 e + (0..7), whose pairs (m, m + 4) are a
@@ -520,7 +537,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
   }
   uint32_t one = 0x3f803f80u;
   asm volatile("" : "+r"(one));
-  const float scale = a.scale * kLog2e, inv_cap = 1.f / a.softcap;
+  const float scale = score_scale(a), inv_cap = 1.f / a.softcap;
   // tile t's column c is this token of the warp's 32, so that a lane's four weights of a 16-token product are tokens
   // q4, q4 + 4, q4 + 8, q4 + 12 of it
   auto token = [](int t, int c) { return (t >> 1) * kTile + (c >> 1) + 4 * (2 * (t & 1) + (c & 1)); };
@@ -535,31 +552,35 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[u][t][e] = 0.f;
   Running run;
-  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
   // where a lane's words lie: of keys, of values of tokens q4 and q4 + 4; eight tokens on are 8 rows on, whatever the place
   const int key_at = place4<D>(token(0, row), D == 128 ? q4 : q4 >> 1) + (D == 128 ? 0 : (q4 & 1) * 8);
   int val_at[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j)
     val_at[j] = kCodes<D> + (D == 128 ? place4<D>(q4 + 4 * j, row >> 1) + (row & 1) * 8 : place4<D>(q4 + 4 * j, row >> 2) + (row & 3) * 4);
-  Place place(p.first + warp * kPair, kWarps * kPair, page);
-  Next next = lookup(place, 0);
+  int next = lookup(0);
+  place(0, next);
+  next = lookup(1);
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < kS - 1; ++i) {
-    if (i < mine) fetch(i, i, next);
+    if (i < mine) fetch(i, i);
     tc::cp_async_commit();
-    next = lookup(place, i + 1);
   }
   for (int i = 0, stage = 0, into = kS - 1; i < mine; ++i, stage = stage + 1 == kS ? 0 : stage + 1, into = into + 1 == kS ? 0 : into + 1) {
     cp_async_wait<kS - 2>();
+    const int ahead = i + kS - 1;
+    if (ahead % kBatch == 0) {
+      place(ahead / kBatch, next);
+      next = lookup(ahead / kBatch + 1);
+    }
     __syncwarp();  // every lane's copies of this tile are in, and its reads of the stage that is filled next are done
-    if (i + kS - 1 < mine) fetch(i + kS - 1, into, next);
+    if (ahead < mine) fetch(ahead, into);
     tc::cp_async_commit();
-    next = lookup(place, i + kS);
     const uint8_t* tile = region + stage * kTileBytes4<D>;
     const uint32_t* meta = reinterpret_cast<const uint32_t*>(tile + 2 * kCodes<D>);
-    const uint32_t seen = s_seen[warp][stage];
-    // ---- a token a lane: 16 scale and offset - 16 scale
+    const uint32_t seen = spots[i % (2 * kBatch) * 2].seen | spots[i % (2 * kBatch) * 2 + 1].seen << 16;
+    // ---- a token a lane: 16 scale and offset - 16 scale, the keys' times what scores are multiplied by
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       uint32_t w[kGroups];
@@ -574,6 +595,10 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
       for (int g = 0; g < kGroups; ++g) {
         f[2 * g] = 16.f * __uint_as_float(w[g] << 16);
         f[2 * g + 1] = __uint_as_float(w[g] & 0xffff0000u) - f[2 * g];
+        if (v == 0) {
+          f[2 * g] *= scale;
+          f[2 * g + 1] *= scale;
+        }
       }
       if (!(seen >> lane & 1u)) {
 #pragma unroll
@@ -648,7 +673,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
       }
     }
     const int t0 = p.first + (warp + i * kWarps) * kPair;
-    bias_and_mask<4, kRows>(a, x, slope, scale, inv_cap, p.seen.hi - 1 - t0, seen, 0xffffffffu, [&](int t, int e) { return token(t, 2 * q4 + e); });
+    bias_and_mask<4, kRows>(a, x, slope, inv_cap, p.seen.hi - 1 - t0, seen, 0xffffffffu, [&](int t, int e) { return token(t, 2 * q4 + e); });
     float f[2];
     if (weigh<4, kRows>(run, x, f)) {
 #pragma unroll
