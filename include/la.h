@@ -618,7 +618,7 @@ la_status la_qk_norm_rope(const la_qk_norm_rope_args* args, void* stream);
  *            of a row share a bf16 offset, the least of them, and a bf16 scale, a fifteenth of their
  *            spread ((max - min) / 15 rounded); an element is offset + scale code with
  *            code = (element - offset) / scale rounded to even, at most 15.  A group whose spread
- *            is not finite reads back as NaN.  A page of one head holds the codes of its tokens
+ *            is not below 2^119 (or not a number) reads back as NaN.  A page of one head holds the codes of its tokens
  *            (d / 2 bytes each), then their scales and offsets (4 bytes a group, the scale in the
  *            lower half).  A token's 32-bit words take eight elements each, least first, of its
  *            groups in turn: with d = 128 word 2 e + g holds elements 64 g + 8 e .. 64 g + 8 e + 7.

@@ -1,9 +1,9 @@
 // heads.cu -- norms of queries and keys for each head with the position rotation in the same pass:
 //   x <- w x / sqrt(mean x^2 + eps) (or the sum in the mean's place), then pairs of the first elements turned by their
 //   token's angle.
-// Every element is read and written once, so memory bounds it.  A warp takes a token's query heads or its key heads, a part
-// of them where there are few tokens: eight elements a lane and d / 8 lanes a row, so that the weights and the angles of a
-// lane's elements stay in registers from head to head.  Sums of squares meet by shuffles, and so do the pairs.
+// Every element is read and written once, so memory bounds it.  A warp takes a token's heads, a part of them where there are
+// few tokens: eight elements a lane and d / 8 lanes a row, so that the angles of a lane's elements stay in registers from
+// head to head.  Sums of squares meet by shuffles, those of four rows at a time.
 #include "la.h"
 #include "rows.cuh"
 
@@ -15,8 +15,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 4;  // rows of a lane on their way at once
 
 struct Plan {
-  int per;                 // heads a warp takes
-  int64_t q_parts, parts;  // warps for a token's queries, for its queries and keys
+  int per;        // heads a warp takes, of the queries' and then the keys'
+  int64_t parts;  // warps for a token
   int64_t blocks;
 };
 
@@ -26,138 +26,173 @@ int lanes_of(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 Plan plan_of(int64_t B, int64_t H, int64_t Hkv, int64_t N, int d) {
   const int rows = 32 / lanes_of(d);
   Plan p{};
-  for (int m = 8; m >= 1; m /= 2) {
+  for (int m = 8 * kRows; m >= 1; m /= 2) {
     p.per = rows * m;
-    p.q_parts = (H + p.per - 1) / p.per;
-    p.parts = p.q_parts + (Hkv + p.per - 1) / p.per;
+    p.parts = (H + Hkv + p.per - 1) / p.per;
     if (B * N * p.parts >= 152 * 32) break;
   }
   p.blocks = (B * N * p.parts + kWarps - 1) / kWarps;
   return p;
 }
 
-template <typename TIn, typename TOut, int LPR>
-__global__ void __launch_bounds__(kThreads)
+template <typename TIn, typename TOut, int LPR, TurnKind kTurn, bool kNorm>
+__global__ void __launch_bounds__(kThreads, sizeof(TIn) == 2 ? 3 : 2)
 qk_norm_rope_kernel(const QkNormRopeLaunch a, const Plan p) {
   constexpr int R = 32 / LPR;
+  constexpr bool kWhole = kTurn != kTurnHalves;
   const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR;
   grid_dependents_trigger();
   grid_dependency_wait();
   const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t token = unit / p.parts, b = token / a.N, n = token - b * a.N;
+  const int64_t token = divide(unit, p.parts), b = divide(token, a.N), n = token - b * a.N;
   if (b >= a.B) return;  // whole warps
-  const int64_t part = unit - token * p.parts;
-  const bool keys = part >= p.q_parts;
-  const int64_t h0 = (keys ? part - p.q_parts : part) * p.per, heads = keys ? a.Hkv : a.H, h1 = min(h0 + p.per, heads);
+  const int part = (int)(unit - token * p.parts);
   const bool on = col * 8 < a.d;
-
-  const TIn* x = static_cast<const TIn*>(keys ? a.k.ptr : a.q.ptr) + b * (keys ? a.k.sb : a.q.sb) + n * (keys ? a.k.st : a.q.st) + col * 8;
-  TOut* y = static_cast<TOut*>(keys ? a.k_out : a.q_out) + b * (keys ? a.k_sb : a.q_sb) + n * (keys ? a.k_st : a.q_st) + col * 8;
-  const int64_t xh = keys ? a.k.sh : a.q.sh, yh = keys ? a.k_sh : a.q_sh;
+  const int2 at = runs_of<kTurn>(on ? col : 0, a.rot);
 
   // ---- the token: padding and positions outside the tables are left alone or become zeros
   const int64_t len = sequence_length(a.lens, b, a.N, a.status, lane == 0 && part == 0 && n == 0);
   int64_t row = 0;
   bool alive = n < len;
-  if (alive && a.rot > 0) {
+  if (kTurn != kTurnNone && alive) {
     row = table_row(a.pos ? a.pos[a.pos_each ? token : b] : 0, a.pos && a.pos_each ? 0 : n, a.positions);
     alive = row >= 0;
     if (!alive && lane == 0 && part == 0) atomicOr(a.status, kStatusBadIndex);
   }
-  if (!alive) {
-    if (!a.fill) return;
-    Raw8<TOut> zero;
-    zero.zero();
-    for (int64_t h = h0 + sub; h < h1; h += R)
-      if (on) zero.store(y + h * yh);
-    return;
-  }
-
-  float w[8];
-  const void* weight = keys ? a.k_weight : a.q_weight;
-  if (weight && on) {
-    if (a.w_bf16) {
-      Raw8<__nv_bfloat16> r;
-      r.load(static_cast<const __nv_bfloat16*>(weight) + col * 8);
-      r.unpack(w);
-    } else {
-      Raw8<float> r;
-      r.load(static_cast<const float*>(weight) + col * 8);
-      r.unpack(w);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.f;
-  }
-  Turn turn;
+  if (!alive && !a.fill) return;
+  Turn<kTurn> turn;
   turn.on = false;
-  if (a.rot > 0) turn.init(a.cos + row * (a.rot / 2), a.sin + row * (a.rot / 2), a.rot, a.interleaved, lane, col);
+  if (kTurn != kTurnNone && alive && on) turn.init(a.cos + row * (a.rot / 2), a.sin + row * (a.rot / 2), a.rot, col);
   const float share = a.norm == LA_NORM_RMS ? 1.f / (float)a.d : 1.f;
 
-  for (int64_t h = h0; h < h1; h += kRows * R) {
-    Raw8<TIn> raw[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      raw[i].zero();
-      const int64_t at = h + i * R + sub;
-      if (on && at < h1) raw[i].load(x + at * xh);
+#pragma unroll 1
+  for (int keys = 0; keys < 2; ++keys) {
+    // this warp's heads of the queries, or of the keys
+    const int64_t before = keys ? a.H : 0, heads = keys ? a.Hkv : a.H;
+    const int64_t h0 = max((int64_t)part * p.per - before, (int64_t)0), h1 = min((int64_t)(part + 1) * p.per - before, heads);
+    if (h0 >= h1) continue;
+    const TIn* x = static_cast<const TIn*>(keys ? a.k.ptr : a.q.ptr) + b * (keys ? a.k.sb : a.q.sb) + n * (keys ? a.k.st : a.q.st);
+    TOut* y = static_cast<TOut*>(keys ? a.k_out : a.q_out) + b * (keys ? a.k_sb : a.q_sb) + n * (keys ? a.k_st : a.q_st);
+    const int64_t xh = keys ? a.k.sh : a.q.sh, yh = keys ? a.k_sh : a.q_sh;
+    if (!alive) {
+      Raw8<TOut> zero;
+      zero.zero();
+      for (int64_t h = h0 + sub; h < h1; h += R)
+        if (on) zero.template store<kWhole>(y + h * yh, at);
+      continue;
     }
+    const void* weight = keys ? a.k_weight : a.q_weight;
+    f32x2 w[4];
+    if (kNorm && weight) {
+      if (a.w_bf16) {
+        Raw8<__nv_bfloat16> r;
+        r.template load<kWhole>(static_cast<const __nv_bfloat16*>(weight), at);
+        r.unpack(w);
+      } else {
+        Raw8<float> r;
+        r.template load<kWhole>(static_cast<const float*>(weight), at);
+        r.unpack(w);
+      }
+    }
+
+    x += (h0 + sub) * xh;
+    y += (h0 + sub) * yh;
+    int left = on ? (int)(h1 - h0) - sub : 0;  // this lane's rows: every R-th while it is positive
+#pragma unroll 1
+    for (int more = (int)(h1 - h0); more > 0; more -= kRows * R, left -= kRows * R) {
+      Raw8<TIn> raw[kRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (h + i * R >= h1) break;  // the same for the whole warp
-      float v[8];
-      raw[i].unpack(v);
-      float scale = 1.f;
-      if (a.norm != LA_NORM_NONE) {
-        float sum = 0.f;
+      for (int i = 0; i < kRows; ++i) {
+        raw[i].zero();
+        if (left > i * R) raw[i].template load<kWhole>(x, at);
+        x += R * xh;
+      }
+      float scale[kRows];
+      if constexpr (kNorm) {
+        float sum[kRows];
+        bool beyond = false;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
+        for (int i = 0; i < kRows; ++i) {
+          f32x2 v[4];
+          raw[i].unpack(v);
+          f32x2 t = mul2(v[0], v[0]);
 #pragma unroll
-        for (int off = LPR / 2; off >= 1; off /= 2) sum += __shfl_xor_sync(kFullMask, sum, off);
-        scale = rsqrtf(fmaf(sum, share, a.eps));
-        if (__any_sync(kFullMask, !(sum <= 3.402823466e38f))) {
+          for (int e = 1; e < 4; ++e) t = fma2(v[e], v[e], t);
+          float lo, hi;
+          unpack2(t, lo, hi);
+          sum[i] = lo + hi;
+        }
+#pragma unroll
+        for (int off = LPR / 2; off >= 1; off /= 2)
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) sum[i] += __shfl_xor_sync(kFullMask, sum[i], off);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          scale[i] = rsqrtf(fmaf(sum[i], share, a.eps));
+          beyond |= !(sum[i] <= 3.402823466e38f);
+        }
+        if (__any_sync(kFullMask, beyond)) {
           // Squares beyond fp32 (elements above 1e18): the same of the row's 2^-80th, whose squares stay below 2^96, so
           // that eps no longer counts.  NaN and infinities stay what they are.
-          float small = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) small = fmaf(v[e] * 0x1p-80f, v[e] * 0x1p-80f, small);
+          for (int i = 0; i < kRows; ++i) {
+            f32x2 v[4], t = pack2(0.f, 0.f);
+            raw[i].unpack(v);
 #pragma unroll
-          for (int off = LPR / 2; off >= 1; off /= 2) small += __shfl_xor_sync(kFullMask, small, off);
-          if (!(sum <= 3.402823466e38f)) scale = rsqrtf(small * share) * 0x1p-80f;
+            for (int e = 0; e < 4; ++e) {
+              v[e] = mul2(v[e], pack2(0x1p-80f, 0x1p-80f));
+              t = fma2(v[e], v[e], t);
+            }
+            float lo, hi;
+            unpack2(t, lo, hi);
+            float small = lo + hi;
+#pragma unroll
+            for (int off = LPR / 2; off >= 1; off /= 2) small += __shfl_xor_sync(kFullMask, small, off);
+            if (!(sum[i] <= 3.402823466e38f)) scale[i] = rsqrtf(small * share) * 0x1p-80f;
+          }
         }
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * scale * w[e];
-      if (a.rot > 0) {
-        float u[8];
-        if (a.interleaved) {
+      for (int i = 0; i < kRows; ++i) {
+        if (left <= i * R) break;
+        f32x2 v[4];
+        raw[i].unpack(v);
+        if constexpr (kNorm) {
+          const f32x2 both = pack2(scale[i], scale[i]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] = v[e ^ 1];
-        } else {
+          for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], both);
+          if (weight) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] = __shfl_sync(kFullMask, v[e], turn.partner);
+            for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], w[e]);
+          }
         }
-        if (turn.on) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], turn.c[e], u[e] * turn.s[e]);
-        }
+        if (turn.on) turn.apply(v, turn_rounded);
+        Raw8<TOut> out;
+        out.pack(v);
+        out.template store<kWhole>(y, at);
+        y += R * yh;
       }
-      const int64_t at = h + i * R + sub;
-      if (on && at < h1) store_floats(y + at * yh, v, 8, true);
     }
   }
 }
 
-template <typename TIn, typename TOut>
-cudaError_t launch(const QkNormRopeLaunch& a, cudaStream_t stream) {
+template <typename TIn, typename TOut, int LPR, TurnKind kTurn>
+cudaError_t launch_turn(const QkNormRopeLaunch& a, cudaStream_t stream) {
   const Plan p = plan_of(a.B, a.H, a.Hkv, a.N, a.d);
   const dim3 grid((unsigned)p.blocks);
-  switch (lanes_of(a.d)) {
-    case 4: return launch_dependent(qk_norm_rope_kernel<TIn, TOut, 4>, grid, kThreads, 0, stream, a, p);
-    case 8: return launch_dependent(qk_norm_rope_kernel<TIn, TOut, 8>, grid, kThreads, 0, stream, a, p);
-    case 16: return launch_dependent(qk_norm_rope_kernel<TIn, TOut, 16>, grid, kThreads, 0, stream, a, p);
-    default: return launch_dependent(qk_norm_rope_kernel<TIn, TOut, 32>, grid, kThreads, 0, stream, a, p);
-  }
+  if (a.norm == LA_NORM_NONE) return launch_dependent(qk_norm_rope_kernel<TIn, TOut, LPR, kTurn, false>, grid, kThreads, 0, stream, a, p);
+  return launch_dependent(qk_norm_rope_kernel<TIn, TOut, LPR, kTurn, true>, grid, kThreads, 0, stream, a, p);
+}
+template <typename TIn, typename TOut, int LPR>
+cudaError_t launch_row(const QkNormRopeLaunch& a, cudaStream_t stream) {
+  return a.rot == 0 ? launch_turn<TIn, TOut, LPR, kTurnNone>(a, stream) : a.interleaved ? launch_turn<TIn, TOut, LPR, kTurnNeighbours>(a, stream)
+                                                                        : launch_turn<TIn, TOut, LPR, kTurnHalves>(a, stream);
+}
+template <typename TIn, typename TOut>
+cudaError_t launch(const QkNormRopeLaunch& a, cudaStream_t stream) {
+  const int lanes = lanes_of(a.d);
+  return lanes == 4 ? launch_row<TIn, TOut, 4>(a, stream) : lanes == 8 ? launch_row<TIn, TOut, 8>(a, stream)
+       : lanes == 16 ? launch_row<TIn, TOut, 16>(a, stream) : launch_row<TIn, TOut, 32>(a, stream);
 }
 
 }  // namespace

@@ -1,6 +1,8 @@
 // paged.cu -- keys and values of new tokens into a paged cache, the keys rotated on the way, and a cache's tokens back into
-// rows.  Both read and write every element once, so memory bounds them.  As in heads.cu a lane has eight elements of a row:
-// one 32-bit word of 4-bit codes, whose group of 64 elements is eight neighbouring lanes.
+// rows.  Both read and write every element once, so memory bounds them.  As in heads.cu a lane has eight elements of a row,
+// for 4 bits always consecutive ones: one 32-bit word of codes, whose group of 64 elements is eight neighbouring lanes.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace la {
@@ -12,177 +14,278 @@ constexpr int kRows = 4;  // rows of a lane on their way at once
 
 int lanes_of(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : 16; }
 
-// x c + y s, the exact value rounded to fp32 but for a 2^-20th of an ulp: the products' errors and the sum's are added last.
-// (Next to a border of the 4-bit codes an fp32 rounding more could be a whole code.)
-__device__ __forceinline__ float turn_exact(float x, float c, float y, float s) {
-  const float p = __fmul_rn(x, c), ep = __fmaf_rn(x, c, -p);
-  const float q = __fmul_rn(y, s), eq = __fmaf_rn(y, s, -q);
-  const float sum = __fadd_rn(p, q), t = __fsub_rn(sum, p);
-  const float es = __fadd_rn(__fsub_rn(p, __fsub_rn(sum, t)), __fsub_rn(q, t));
-  const float r = __fadd_rn(sum, __fadd_rn(es, __fadd_rn(ep, eq)));
-  return fabsf(sum) <= 3.402823466e38f ? r : sum;  // the parts of an infinity are NaN
+// x c + y s, the exact value rounded to fp32 but for a 2^-20th of an ulp: the products' errors and the sum's (Knuth's two-sum)
+// are added last.  Next to a border of the 4-bit codes an fp32 rounding more could be a whole code.
+__device__ __forceinline__ f32x2 turn_exact(f32x2 x, f32x2 c, f32x2 y, f32x2 s) {
+  const f32x2 minus = pack2(-1.f, -1.f);
+  auto sub = [&](f32x2 a, f32x2 b) { return fma2(b, minus, a); };
+  const f32x2 p = mul2(x, c), ep = fma2(x, c, mul2(p, minus));
+  const f32x2 q = mul2(y, s), eq = fma2(y, s, mul2(q, minus));
+  const f32x2 sum = add2(p, q), t = sub(sum, p);
+  const f32x2 es = add2(sub(p, sub(sum, t)), sub(q, t));
+  const f32x2 r = add2(sum, add2(es, add2(ep, eq)));
+  float s0, s1, r0, r1;
+  unpack2(sum, s0, s1);
+  unpack2(r, r0, r1);
+  return pack2(fabsf(s0) <= 3.402823466e38f ? r0 : s0, fabsf(s1) <= 3.402823466e38f ? r1 : s1);  // the parts of an infinity are NaN
 }
 
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// Eight bf16 elements of a lane, whose group is eight neighbouring lanes: their codes and the group's scale (lower half) and offset.
-__device__ __forceinline__ void quantise(const float (&v)[8], uint32_t& codes, uint32_t& meta) {
-  float lo = v[0], hi = v[0];
+// A lane's angles for eight consecutive elements, whose partners at rot / 2 are those of lane +- rot / 16.
+template <TurnKind kTurn>
+struct TurnWide {
+  bool on;
+  int partner;
+  f32x2 c[4], s[4];  // s negative for a pair's first element
+  __device__ __forceinline__ void init(const float* cos, const float* sin, int rot, int lane, int col) {
+    on = col * 8 < rot;
+    partner = lane;
+    if (!on) return;
+    if constexpr (kTurn == kTurnNeighbours) {
+      Turn<kTurnNeighbours> t;
+      t.init(cos, sin, rot, col);
 #pragma unroll
-  for (int e = 1; e < 8; ++e) {
-    lo = min_nan(lo, v[e]);
-    hi = max_nan(hi, v[e]);
+      for (int i = 0; i < 4; ++i) { c[i] = t.c[i]; s[i] = t.s[i]; }
+    } else {
+      const int half = rot / 16;  // lanes of the pairs' first elements
+      const bool second = col >= half;
+      partner = second ? lane - half : lane + half;
+      const int at = 8 * (second ? col - half : col);
+      Raw8<float> r;
+      r.load<true>(cos, make_int2(at, at + 4));
+      r.unpack(c);
+      r.load<true>(sin, make_int2(at, at + 4));
+      r.unpack(s);
+      if (!second) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = mul2(s[i], pack2(-1.f, -1.f));
+      }
+    }
   }
+  __device__ __forceinline__ void apply(Raw8<__nv_bfloat16>& raw) const {
+    f32x2 v[4], u[4];
+    raw.unpack(v);
+    if constexpr (kTurn == kTurnNeighbours) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpack2(v[i], lo, hi);
+        u[i] = pack2(hi, lo);
+      }
+    } else {
+      Raw8<__nv_bfloat16> other;
+      other.a.x = __shfl_sync(kFullMask, raw.a.x, partner); other.a.y = __shfl_sync(kFullMask, raw.a.y, partner);
+      other.b.x = __shfl_sync(kFullMask, raw.b.x, partner); other.b.y = __shfl_sync(kFullMask, raw.b.y, partner);
+      other.unpack(u);
+    }
+    if (!on) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = turn_exact(v[i], c[i], u[i], s[i]);
+    raw.pack(v);
+  }
+};
+
+__device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+constexpr float kLargestSpread = 0x1p119f;  // 16 scale times a weight of 2^8 stays within fp32
+
+// Eight elements of a lane, whose group is eight neighbouring lanes: their codes and the group's scale (lower half) and offset.
+__device__ __forceinline__ void quantise(const Raw8<__nv_bfloat16>& raw, uint32_t& codes, uint32_t& meta) {
+  uint32_t lo2 = min_nan2(min_nan2(raw.a.x, raw.a.y), min_nan2(raw.b.x, raw.b.y));
+  uint32_t hi2 = max_nan2(max_nan2(raw.a.x, raw.a.y), max_nan2(raw.b.x, raw.b.y));
+  lo2 = min_nan2(lo2, __byte_perm(lo2, lo2, 0x1032));  // the least of the lane in both halves
+  hi2 = max_nan2(hi2, __byte_perm(hi2, hi2, 0x1032));
+  uint32_t ends = __byte_perm(lo2, hi2, 0x5410);  // least, greatest
 #pragma unroll
   for (int off = 4; off >= 1; off /= 2) {
-    lo = min_nan(lo, __shfl_xor_sync(kFullMask, lo, off));
-    hi = max_nan(hi, __shfl_xor_sync(kFullMask, hi, off));
+    const uint32_t other = __shfl_xor_sync(kFullMask, ends, off);
+    ends = __byte_perm(min_nan2(ends, other), max_nan2(ends, other), 0x7610);
   }
-  const float spread = __fsub_rn(hi, lo);
+  const float lo = __uint_as_float(ends << 16), spread = __uint_as_float(ends & 0xffff0000u) - lo;
   codes = 0;
-  if (!(spread <= 3.402823466e38f)) {
+  if (!(spread < kLargestSpread)) {  // NaN too
     meta = 0x7fc07fc0u;
     return;
   }
-  const __nv_bfloat16 step = __float2bfloat16_rn(__fdiv_rn(spread, 15.f));
+  // spread / 15 correctly rounded: a quotient with the rounded reciprocal, corrected by its remainder (Markstein 1990); all
+  // 2^24 significands of two binades were compared with the division.
+  constexpr float kFifteenth = 1.f / 15.f;
+  const float q = spread * kFifteenth;
+  const bool small = spread < 0x1p-100f;  // where remainders lose bits
+  const __nv_bfloat16 step = __float2bfloat16_rn(small ? __fdiv_rn(spread, 15.f) : fmaf(fmaf(-15.f, q, spread), kFifteenth, q));
   const float scale = __bfloat162float(step);
-  meta = (uint32_t)__bfloat16_as_ushort(step) | (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(lo)) << 16;
-  if (!(scale > 0.f)) return;
+  meta = (uint32_t)__bfloat16_as_ushort(step) | ends << 16;
   // A product with the reciprocal is within 3e-6 of the quotient, which decides where it could lie on the other side of a border.
-  const float inv = __fdiv_rn(1.f, scale);
-  const bool tiny = !(inv <= 3.402823466e38f);
+  const float inv = rcp(scale);
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: the sum's last bits are the rounded value
+  f32x2 v[4], y[4];
+  raw.unpack(v);
+  float r[8], far = small ? 1.f : 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float x = __fsub_rn(v[e], lo);
-    const float y = x * inv;
-    float r = rintf(y);
-    if (tiny || fabsf(y - r) > 0.4999f) r = rintf(__fdiv_rn(x, scale));
-    codes |= (uint32_t)(int)fminf(r, 15.f) << (4 * e);
+  for (int i = 0; i < 4; ++i) {
+    v[i] = add2(v[i], pack2(-lo, -lo));
+    y[i] = mul2(v[i], pack2(inv, inv));
+    const f32x2 z = add2(y[i], pack2(kRound, kRound)), back = add2(z, pack2(-kRound, -kRound));
+    float t0, t1;
+    unpack2(fma2(back, pack2(-1.f, -1.f), y[i]), t0, t1);
+    far = fmaxf(far, fmaxf(fabsf(t0), fabsf(t1)));
+    unpack2(z, r[2 * i], r[2 * i + 1]);
+  }
+  if (far <= 0.4999f) {
+    // the sums' bits are 0x4b400000 + code
+#pragma unroll
+    for (int e = 0; e < 8; ++e) codes += __float_as_uint(r[e]) << (4 * e);
+    codes -= 0x4b400000u * 0x11111111u;
+    return;
+  }
+  if (!(scale > 0.f)) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x0, x1;
+    unpack2(v[i], x0, x1);
+    codes |= (uint32_t)(int)fminf(rintf(__fdiv_rn(x0, scale)), 15.f) << (8 * i);
+    codes |= (uint32_t)(int)fminf(rintf(__fdiv_rn(x1, scale)), 15.f) << (8 * i + 4);
   }
 }
 
-// A warp stores a token's keys or its values, `per` heads of them.
-template <typename T, bool kFour, int LPR>
-__global__ void __launch_bounds__(kThreads)
-paged_append_kernel(const PagedAppendLaunch a, const int per, const int64_t parts) {
-  constexpr int R = 32 / LPR;
-  const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR;
-  grid_dependents_trigger();
-  grid_dependency_wait();
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t token = unit / (2 * parts), b = token / a.N, n = token - b * a.N;
-  if (b >= a.B) return;  // whole warps
-  const int64_t part = unit - token * 2 * parts;
-  const bool values = part >= parts;
-  const bool report = lane == 0 && part == 0;
-  if (n >= sequence_length(a.lens, b, a.N, a.c.status, report && n == 0)) return;
-  const int64_t p = table_row(a.seen[b], n, a.c.width * a.c.page);
-  const int page = p < 0 || (a.rot > 0 && p >= a.positions) ? -1 : table_page(a.c, b, p / a.c.page);
-  if (page < 0) {
-    if (report) atomicOr(a.c.status, kStatusBadIndex);
-    return;
-  }
-  const int slot = (int)(p % a.c.page), d = a.c.d;
-  const bool on = col * 8 < d, turned = a.rot > 0 && !values;
-  const int64_t h0 = (values ? part - parts : part) * per, h1 = min(h0 + per, a.c.Hkv);
-  const View4& view = values ? a.v : a.k;
-  const T* x = static_cast<const T*>(view.ptr) + b * view.sb + n * view.st + col * 8;
-  const int64_t size = page_bytes(a.c);
-  uint8_t* y = static_cast<uint8_t*>(values ? a.c.v : a.c.k) + page * a.c.Hkv * size;  // this token's page, head 0
-  Turn turn;
-  turn.on = false;
-  if (turned) turn.init(a.cos + p * (a.rot / 2), a.sin + p * (a.rot / 2), a.rot, a.interleaved, lane, col);
+// One token's rows of some heads, from x (step `xh` from head to head) into the page at y (`size` bytes a head).
+struct Heads {
+  const void* x;
+  uint8_t* y;
+  int64_t xh, size;
+  int heads, slot;
+};
 
-  for (int64_t h = h0; h < h1; h += kRows * R) {
+template <typename T, bool kFour, int LPR, TurnKind kTurn>
+__device__ __forceinline__ void append_heads(const PagedAppendLaunch& a, const Heads& h, int64_t position) {
+  constexpr int R = 32 / LPR;
+  constexpr bool kWhole = kFour || kTurn != kTurnHalves;
+  const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR, d = a.c.d;
+  const bool on = col * 8 < d;
+  const int2 at = runs_of<kFour ? kTurnNone : kTurn>(on ? col : 0, a.rot);
+  const float *cos = a.cos + position * (a.rot / 2), *sin = a.sin + position * (a.rot / 2);
+  std::conditional_t<kFour, TurnWide<kTurn>, Turn<kTurn>> turn;
+  turn.on = false;
+  if constexpr (kTurn != kTurnNone) {
+    if constexpr (kFour) turn.init(cos, sin, a.rot, lane, col);
+    else if (on) turn.init(cos, sin, a.rot, col);
+  }
+  const T* x = static_cast<const T*>(h.x) + sub * h.xh;
+  uint8_t* y = h.y + sub * h.size;
+  int left = on ? h.heads - sub : 0;  // this lane's rows: every R-th while it is positive
+#pragma unroll 1
+  for (int more = h.heads; more > 0; more -= kRows * R, left -= kRows * R) {
     Raw8<T> raw[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       raw[i].zero();
-      const int64_t at = h + i * R + sub;
-      if (on && at < h1) raw[i].load(x + at * view.sh);
+      if (left > i * R) raw[i].template load<kWhole>(x, at);
+      x += R * h.xh;
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      if (h + i * R >= h1) break;  // the same for the whole warp
-      const int64_t at = h + i * R + sub;
-      const bool store = on && at < h1;
-      float v[8];
-      raw[i].unpack(v);
-      if (turned) {
-        float u[8];
-        if (a.interleaved) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] = v[e ^ 1];
-        } else {
-          raw[i].from_lane(turn.partner).unpack(u);
-        }
-        if (turn.on) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if constexpr (kFour) v[e] = __bfloat162float(__float2bfloat16_rn(turn_exact(v[e], turn.c[e], u[e], turn.s[e])));
-            else v[e] = fmaf(v[e], turn.c[e], u[e] * turn.s[e]);
-          }
-        }
-      }
+      if (more <= i * R) break;  // the same for the whole warp
       if constexpr (kFour) {
+        if constexpr (kTurn != kTurnNone) turn.apply(raw[i]);
         uint32_t codes, meta;
-        quantise(v, codes, meta);
+        quantise(raw[i], codes, meta);
         const int groups = d / kGroup, g = col / 8, e = col % 8;
-        uint8_t* head = y + at * size;
-        if (store) {
-          reinterpret_cast<uint32_t*>(head + (int64_t)slot * (d / 2))[code_word(g, e, groups)] = codes;
-          if (e == 0) reinterpret_cast<uint32_t*>(head + (int64_t)a.c.page * (d / 2))[slot * groups + g] = meta;
+        if (left > i * R) {
+          reinterpret_cast<uint32_t*>(y + h.slot * (d / 2))[code_word(g, e, groups)] = codes;
+          if (e == 0) reinterpret_cast<uint32_t*>(y + a.c.page * (d / 2))[h.slot * groups + g] = meta;
         }
-      } else if (store) {
-        T* row = reinterpret_cast<T*>(y + at * size) + (int64_t)slot * d + col * 8;
-        if (turned) store_floats(row, v, 8, true);
-        else raw[i].store(row);  // as they are, whatever they hold
+      } else if (left > i * R) {
+        if (kTurn != kTurnNone && turn.on) {  // other rows and elements go as they are, whatever they hold
+          f32x2 v[4];
+          raw[i].unpack(v);
+          turn.apply(v, turn_rounded);
+          raw[i].pack(v);
+        }
+        raw[i].template store<kWhole>(reinterpret_cast<T*>(y) + (int64_t)h.slot * d, at);
       }
+      y += R * h.size;
     }
   }
+}
+
+// A warp stores a token's keys or its values, `per` heads of them.
+template <typename T, bool kFour, int LPR, TurnKind kTurn>
+__global__ void __launch_bounds__(kThreads, 3)
+paged_append_kernel(const PagedAppendLaunch a, const int per, const int parts) {
+  grid_dependents_trigger();
+  grid_dependency_wait();
+  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t token = divide(unit, 2 * parts), b = divide(token, a.N), n = token - b * a.N;
+  if (b >= a.B) return;  // whole warps
+  const int part = (int)(unit - token * 2 * parts);
+  const bool values = part >= parts, report = part == 0 && (threadIdx.x & 31) == 0;
+  if (n >= sequence_length(a.lens, b, a.N, a.c.status, report && n == 0)) return;
+  const int64_t p = table_row(a.seen[b], n, a.c.width * a.c.page);  // below 2^31
+  const int column = (int)((unsigned)p / (unsigned)a.c.page);
+  const int page = p < 0 || (kTurn != kTurnNone && p >= a.positions) ? -1 : table_page(a.c, b, column);
+  if (page < 0) {
+    if (report) atomicOr(a.c.status, kStatusBadIndex);
+    return;
+  }
+  const int h0 = (values ? part - parts : part) * per;
+  const View4& view = values ? a.v : a.k;
+  Heads h;
+  h.size = page_bytes(a.c);
+  h.x = static_cast<const T*>(view.ptr) + b * view.sb + n * view.st + h0 * view.sh;
+  h.y = static_cast<uint8_t*>(values ? a.c.v : a.c.k) + (page * a.c.Hkv + h0) * h.size;
+  h.xh = view.sh;
+  h.heads = min(per, (int)a.c.Hkv - h0);
+  h.slot = (int)p - column * a.c.page;
+  if (kTurn == kTurnNone || values) append_heads<T, kFour, LPR, kTurnNone>(a, h, 0);
+  else append_heads<T, kFour, LPR, kTurn>(a, h, p);
 }
 
 // A warp reads 16 tokens of one head, keys or values.
 template <typename T, typename TOut, bool kFour, int LPR>
 __global__ void __launch_bounds__(kThreads)
-paged_read_kernel(const PagedReadLaunch a, const int64_t tiles) {
+paged_read_kernel(const PagedReadLaunch a, const int tiles) {
   constexpr int R = 32 / LPR;
   const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR;
   grid_dependents_trigger();
   grid_dependency_wait();
   const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  int64_t rest = unit / tiles;
-  const int64_t n0 = (unit - rest * tiles) * 16;
-  const bool values = rest & 1;
-  rest >>= 1;
-  const int64_t b = rest / a.c.Hkv, h = rest - b * a.c.Hkv;
+  const int64_t bhv = divide(unit, tiles), b = divide(bhv, 2 * a.c.Hkv);
   if (b >= a.B) return;  // whole warps
-  const int d = a.c.d;
+  const int n0 = (int)(unit - bhv * tiles) * 16;
+  const bool values = bhv & 1;
+  const int h = (int)(bhv - b * 2 * a.c.Hkv) >> 1, d = a.c.d;
   const bool on = col * 8 < d, report = lane == 0 && h == 0 && !values;
-  const int64_t len = sequence_length(a.lens, b, a.N, a.c.status, report && n0 == 0);
-  int64_t have = min(len, n0 + 16);  // tokens below are in the cache
-  int page = -1;
+  const int len = (int)sequence_length(a.lens, b, a.N, a.c.status, report && n0 == 0), end = min(n0 + 16, (int)a.N);
+  int have = max(n0, min(len, end));  // tokens below are in the cache
+  int page = -1, slot = 0;
   if (n0 < have) {
-    page = n0 < a.c.width * a.c.page ? table_page(a.c, b, n0 / a.c.page) : -1;
+    const int column = (int)((unsigned)n0 / (unsigned)a.c.page);
+    slot = n0 - column * a.c.page;
+    page = column < a.c.width ? table_page(a.c, b, column) : -1;
     if (page < 0) {
       if (report) atomicOr(a.c.status, kStatusBadIndex);
       have = n0;
     }
   }
-  const int64_t end = min(n0 + 16, a.N), size = page_bytes(a.c);
-  const int slot0 = (int)(n0 % a.c.page);
-  const uint8_t* x = static_cast<const uint8_t*>(values ? a.c.v : a.c.k) + (page * a.c.Hkv + h) * size;
-  TOut* y = static_cast<TOut*>(values ? a.v : a.k) + b * (values ? a.v_sb : a.k_sb) + h * (values ? a.v_sh : a.k_sh) + col * 8;
+  if (have == n0 && !a.fill) return;
+  if (!on) return;  // no lane waits for another from here on
+  const uint8_t* x = static_cast<const uint8_t*>(values ? a.c.v : a.c.k) + (max(page, 0) * a.c.Hkv + h) * page_bytes(a.c);
   const int64_t yt = values ? a.v_st : a.k_st;
+  TOut* y = static_cast<TOut*>(values ? a.v : a.k) + b * (values ? a.v_sb : a.k_sb) + h * (values ? a.v_sh : a.k_sh) + (n0 + sub) * yt;
+  const int2 at = make_int2(8 * col, 8 * col + 4);
+  const int there = have - n0 - sub, wanted = (a.fill ? end : have) - n0 - sub;  // this lane's rows: every R-th below
+  const int groups = d / kGroup;
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(x) + (slot + sub) * (d / 8) + code_word(col / 8, col % 8, groups);
+  const uint32_t* metas = reinterpret_cast<const uint32_t*>(x + a.c.page * (d / 2)) + (slot + sub) * groups + col / 8;
+  const T* rows = reinterpret_cast<const T*>(x) + (int64_t)(slot + sub) * d;
 
 #pragma unroll
   for (int i0 = 0; i0 < 16 / R; i0 += kRows) {
@@ -190,55 +293,63 @@ paged_read_kernel(const PagedReadLaunch a, const int64_t tiles) {
     uint32_t codes[kRows], meta[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int r = (i0 + i) * R + sub;
-      if (!on || n0 + r >= have) continue;
+      if (there <= (i0 + i) * R) continue;
       if constexpr (kFour) {
-        const int groups = d / kGroup, g = col / 8, e = col % 8;
-        codes[i] = reinterpret_cast<const uint32_t*>(x + (int64_t)(slot0 + r) * (d / 2))[code_word(g, e, groups)];
-        meta[i] = reinterpret_cast<const uint32_t*>(x + (int64_t)a.c.page * (d / 2))[(slot0 + r) * groups + g];
+        codes[i] = words[(i0 + i) * R * (d / 8)];
+        meta[i] = metas[(i0 + i) * R * groups];
       } else {
-        raw[i].load(reinterpret_cast<const T*>(x) + (int64_t)(slot0 + r) * d + col * 8);
+        raw[i].template load<true>(rows + (i0 + i) * R * d, at);
       }
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int64_t n = n0 + (i0 + i) * R + sub;
-      if (!on || n >= end) continue;
-      float v[8];
-      if (n >= have) {
-        if (!a.fill) continue;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.f;
-      } else if constexpr (kFour) {
-        const float scale = __uint_as_float(meta[i] << 16), offset = __uint_as_float(meta[i] & 0xffff0000u);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf((float)(codes[i] >> (4 * e) & 15u), scale, offset);
+      if (wanted <= (i0 + i) * R) continue;
+      f32x2 v[4];
+      Raw8<TOut> out;
+      if (there <= (i0 + i) * R) {
+        out.zero();
       } else {
-        raw[i].unpack(v);
+        if constexpr (kFour) {
+          const float scale = __uint_as_float(meta[i] << 16), offset = __uint_as_float(meta[i] & 0xffff0000u);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // a code in the last bits of 2^23 is a float: no conversion, of which an SM makes 16 a clock
+            const f32x2 c = pack2(__uint_as_float((codes[i] >> (8 * e) & 15u) | 0x4b000000u), __uint_as_float((codes[i] >> (8 * e + 4) & 15u) | 0x4b000000u));
+            v[e] = fma2(add2(c, pack2(-0x1p23f, -0x1p23f)), pack2(scale, scale), pack2(offset, offset));
+          }
+        } else {
+          raw[i].unpack(v);
+        }
+        out.pack(v);
       }
-      store_floats(y + n * yt, v, 8, true);
+      out.template store<true>(y + (i0 + i) * R * yt, at);
     }
   }
 }
 
-template <typename T, bool kFour, int LPR>
-cudaError_t append(const PagedAppendLaunch& a, cudaStream_t stream) {
+template <typename T, bool kFour, int LPR, TurnKind kTurn>
+cudaError_t append_turn(const PagedAppendLaunch& a, cudaStream_t stream) {
   constexpr int R = 32 / LPR;
   int per = R;
   int64_t parts = 0;
-  for (int m = kRows; m >= 1; m /= 2) {  // as many heads a warp as leave 32 warps to each of 152 SMs
+  for (int m = 2 * kRows; m >= 1; m /= 2) {  // as many heads a warp as leave 32 warps to each of 152 SMs
     per = R * m;
     parts = (a.c.Hkv + per - 1) / per;
     if (2 * a.B * a.N * parts >= 152 * 32) break;
   }
   const int64_t blocks = (2 * a.B * a.N * parts + kWarps - 1) / kWarps;
-  return launch_dependent(paged_append_kernel<T, kFour, LPR>, dim3((unsigned)blocks), kThreads, 0, stream, a, per, parts);
+  return launch_dependent(paged_append_kernel<T, kFour, LPR, kTurn>, dim3((unsigned)blocks), kThreads, 0, stream, a, per, (int)parts);
+}
+template <typename T, bool kFour, int LPR>
+cudaError_t append(const PagedAppendLaunch& a, cudaStream_t stream) {
+  return a.rot == 0 ? append_turn<T, kFour, LPR, kTurnNone>(a, stream) : a.interleaved ? append_turn<T, kFour, LPR, kTurnNeighbours>(a, stream)
+                                                                       : append_turn<T, kFour, LPR, kTurnHalves>(a, stream);
 }
 
 template <typename T, typename TOut, bool kFour, int LPR>
 cudaError_t read(const PagedReadLaunch& a, cudaStream_t stream) {
   const int64_t tiles = (a.N + 15) / 16, blocks = (2 * a.B * a.c.Hkv * tiles + kWarps - 1) / kWarps;
-  return launch_dependent(paged_read_kernel<T, TOut, kFour, LPR>, dim3((unsigned)blocks), kThreads, 0, stream, a, tiles);
+  return launch_dependent(paged_read_kernel<T, TOut, kFour, LPR>, dim3((unsigned)blocks), kThreads, 0, stream, a, (int)tiles);
 }
 
 template <typename T, typename TOut>

@@ -519,12 +519,11 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
       float sum = 0.f;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        Raw8<T> r;
-        r.zero();
-        if (h < p.group) r.load(q + kGroup * g + 8 * (2 * q4 + u));
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (h < p.group) w = *reinterpret_cast<const uint4*>(q + kGroup * g + 8 * (2 * q4 + u));
         float v[8];
-        r.unpack(v);
-        const uint32_t x[4] = {r.w.x, r.w.y, r.w.z, r.w.w};  // pairs (0, 1) (2, 3) (4, 5) (6, 7)
+        unpack_vec(w, v);
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};  // pairs (0, 1) (2, 3) (4, 5) (6, 7)
 #pragma unroll
         for (int m = 0; m < 4; ++m) qa[g][u][m * kRows + i] = __byte_perm(x[m / 2], x[2 + m / 2], m & 1 ? 0x7632 : 0x5410);
 #pragma unroll
