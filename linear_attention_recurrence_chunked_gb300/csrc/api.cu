@@ -725,7 +725,7 @@ la_status la_qk_norm_rope(const la_qk_norm_rope_args* a, void* stream) {
   if (a->rot < 0 || a->rot > a->d) return LA_ERR_INVALID_ARGUMENT;
   if (a->rot % 16 != 0) return LA_ERR_UNSUPPORTED;
   if (a->B == 0 || a->N == 0 || (a->H == 0 && a->H_kv == 0)) return LA_OK;
-  if (!within(kMaxElems, {a->B, a->N, a->H + a->H_kv}) || la::qk_norm_rope_blocks(a->B, a->H, a->H_kv, a->N, (int)a->d) > kMaxBlocks)
+  if (!within(kMaxElems, {a->B, a->N, a->H + a->H_kv}) || la::qk_norm_rope_blocks(a->B, a->H, a->H_kv, a->N, (int)a->d) > kMaxBlocks / 4)
     return LA_ERR_UNSUPPORTED;
   if (!valid_view(a->q, a->B, a->H, a->N, a->d, a->in_dtype) || !valid_view(a->q_out, a->B, a->H, a->N, a->d, a->out_dtype) ||
       !valid_view(a->k, a->B, a->H_kv, a->N, a->d, a->in_dtype) || !valid_view(a->k_out, a->B, a->H_kv, a->N, a->d, a->out_dtype) ||

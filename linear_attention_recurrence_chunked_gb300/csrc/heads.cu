@@ -15,9 +15,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 4;  // rows of a lane on their way at once
 
 struct Plan {
-  int per;        // heads a warp takes, of the queries' and then the keys'
-  int64_t parts;  // warps for a token
+  int per;  // heads a warp takes, of the queries' and then the keys'
   int64_t blocks;
+  Divisor parts, tokens;  // warps for a token; tokens of a sequence
 };
 
 int lanes_of(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
@@ -26,27 +26,29 @@ int lanes_of(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 Plan plan_of(int64_t B, int64_t H, int64_t Hkv, int64_t N, int d) {
   const int rows = 32 / lanes_of(d);
   Plan p{};
+  int64_t parts = 0;
   for (int m = 8 * kRows; m >= 1; m /= 2) {
     p.per = rows * m;
-    p.parts = (H + Hkv + p.per - 1) / p.per;
-    if (B * N * p.parts >= 152 * 32) break;
+    parts = (H + Hkv + p.per - 1) / p.per;
+    if (B * N * parts >= 152 * 32) break;
   }
-  p.blocks = (B * N * p.parts + kWarps - 1) / kWarps;
+  p.blocks = (B * N * parts + kWarps - 1) / kWarps;
+  p.parts = Divisor(parts);
+  p.tokens = Divisor(N);
   return p;
 }
 
 template <typename TIn, typename TOut, int LPR, TurnKind kTurn, bool kNorm>
-__global__ void __launch_bounds__(kThreads, sizeof(TIn) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 3)
 qk_norm_rope_kernel(const QkNormRopeLaunch a, const Plan p) {
   constexpr int R = 32 / LPR;
   constexpr bool kWhole = kTurn != kTurnHalves;
   const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR;
   grid_dependents_trigger();
   grid_dependency_wait();
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t token = divide(unit, p.parts), b = divide(token, a.N), n = token - b * a.N;
+  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), token = p.parts(unit), b = p.tokens(token), n = token - b * p.tokens.d;
   if (b >= a.B) return;  // whole warps
-  const int part = (int)(unit - token * p.parts);
+  const int part = (int)(unit - token * p.parts.d);
   const bool on = col * 8 < a.d;
   const int2 at = runs_of<kTurn>(on ? col : 0, a.rot);
 

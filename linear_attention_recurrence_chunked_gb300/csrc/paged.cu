@@ -219,17 +219,16 @@ __device__ __forceinline__ void append_heads(const PagedAppendLaunch& a, const H
 // A warp stores a token's keys or its values, `per` heads of them.
 template <typename T, bool kFour, int LPR, TurnKind kTurn>
 __global__ void __launch_bounds__(kThreads, 3)
-paged_append_kernel(const PagedAppendLaunch a, const int per, const int parts) {
+paged_append_kernel(const PagedAppendLaunch a, const int per, const Divisor parts2, const Divisor tokens, const Divisor pages) {
   grid_dependents_trigger();
   grid_dependency_wait();
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t token = divide(unit, 2 * parts), b = divide(token, a.N), n = token - b * a.N;
+  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), token = parts2(unit), b = tokens(token), n = token - b * tokens.d;
   if (b >= a.B) return;  // whole warps
-  const int part = (int)(unit - token * 2 * parts);
+  const int part = (int)(unit - token * parts2.d), parts = (int)(parts2.d / 2);
   const bool values = part >= parts, report = part == 0 && (threadIdx.x & 31) == 0;
   if (n >= sequence_length(a.lens, b, a.N, a.c.status, report && n == 0)) return;
   const int64_t p = table_row(a.seen[b], n, a.c.width * a.c.page);  // below 2^31
-  const int column = (int)((unsigned)p / (unsigned)a.c.page);
+  const int column = (int)pages((uint32_t)p);
   const int page = p < 0 || (kTurn != kTurnNone && p >= a.positions) ? -1 : table_page(a.c, b, column);
   if (page < 0) {
     if (report) atomicOr(a.c.status, kStatusBadIndex);
@@ -251,23 +250,22 @@ paged_append_kernel(const PagedAppendLaunch a, const int per, const int parts) {
 // A warp reads 16 tokens of one head, keys or values.
 template <typename T, typename TOut, bool kFour, int LPR>
 __global__ void __launch_bounds__(kThreads)
-paged_read_kernel(const PagedReadLaunch a, const int tiles) {
+paged_read_kernel(const PagedReadLaunch a, const Divisor tiles, const Divisor heads2, const Divisor pages) {
   constexpr int R = 32 / LPR;
   const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR;
   grid_dependents_trigger();
   grid_dependency_wait();
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t bhv = divide(unit, tiles), b = divide(bhv, 2 * a.c.Hkv);
+  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), bhv = tiles(unit), b = heads2(bhv);
   if (b >= a.B) return;  // whole warps
-  const int n0 = (int)(unit - bhv * tiles) * 16;
+  const int n0 = (int)(unit - bhv * tiles.d) * 16;
   const bool values = bhv & 1;
-  const int h = (int)(bhv - b * 2 * a.c.Hkv) >> 1, d = a.c.d;
+  const int h = (int)(bhv - b * heads2.d) >> 1, d = a.c.d;
   const bool on = col * 8 < d, report = lane == 0 && h == 0 && !values;
   const int len = (int)sequence_length(a.lens, b, a.N, a.c.status, report && n0 == 0), end = min(n0 + 16, (int)a.N);
   int have = max(n0, min(len, end));  // tokens below are in the cache
   int page = -1, slot = 0;
   if (n0 < have) {
-    const int column = (int)((unsigned)n0 / (unsigned)a.c.page);
+    const int column = (int)pages((uint32_t)n0);
     slot = n0 - column * a.c.page;
     page = column < a.c.width ? table_page(a.c, b, column) : -1;
     if (page < 0) {
@@ -338,7 +336,7 @@ cudaError_t append_turn(const PagedAppendLaunch& a, cudaStream_t stream) {
     if (2 * a.B * a.N * parts >= 152 * 32) break;
   }
   const int64_t blocks = (2 * a.B * a.N * parts + kWarps - 1) / kWarps;
-  return launch_dependent(paged_append_kernel<T, kFour, LPR, kTurn>, dim3((unsigned)blocks), kThreads, 0, stream, a, per, (int)parts);
+  return launch_dependent(paged_append_kernel<T, kFour, LPR, kTurn>, dim3((unsigned)blocks), kThreads, 0, stream, a, per, Divisor(2 * parts), Divisor(a.N), Divisor(a.c.page));
 }
 template <typename T, bool kFour, int LPR>
 cudaError_t append(const PagedAppendLaunch& a, cudaStream_t stream) {
@@ -349,7 +347,7 @@ cudaError_t append(const PagedAppendLaunch& a, cudaStream_t stream) {
 template <typename T, typename TOut, bool kFour, int LPR>
 cudaError_t read(const PagedReadLaunch& a, cudaStream_t stream) {
   const int64_t tiles = (a.N + 15) / 16, blocks = (2 * a.B * a.c.Hkv * tiles + kWarps - 1) / kWarps;
-  return launch_dependent(paged_read_kernel<T, TOut, kFour, LPR>, dim3((unsigned)blocks), kThreads, 0, stream, a, (int)tiles);
+  return launch_dependent(paged_read_kernel<T, TOut, kFour, LPR>, dim3((unsigned)blocks), kThreads, 0, stream, a, Divisor(tiles), Divisor(2 * a.c.Hkv), Divisor(a.c.page));
 }
 
 template <typename T, typename TOut>

@@ -129,9 +129,20 @@ __device__ __forceinline__ int64_t table_row(int64_t first, int64_t n, int64_t p
   return p < (uint64_t)positions ? (int64_t)p : -1;
 }
 
-// Quotient where the operands mostly fit in 32 bits: a 64-bit division takes a few hundred clocks.
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-  return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
+// Division by a number that the host knows: a product and two shifts (Granlund and Montgomery 1994), where the instruction
+// sequence of a division takes thirty.
+struct Divisor {
+  uint32_t d, factor, shift;
+  Divisor() = default;
+  explicit Divisor(int64_t by) : d((uint32_t)by), factor(0), shift(0) {
+    while (shift < 32 && (uint64_t(1) << shift) < d) ++shift;
+    factor = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - d)) / d + 1);
+  }
+  // n / d for every 32-bit n
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    const uint32_t t = __umulhi(n, factor);
+    return shift == 0 ? n : (t + ((n - t) >> 1)) >> (shift - 1);
+  }
+};
 
 }  // namespace la
