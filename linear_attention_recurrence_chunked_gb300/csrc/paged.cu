@@ -121,22 +121,28 @@ __device__ __forceinline__ void quantise(const Raw8<__nv_bfloat16>& raw, uint32_
   const float q = spread * kFifteenth;
   const bool small = spread < 0x1p-100f;  // where remainders lose bits
   const __nv_bfloat16 step = __float2bfloat16_rn(small ? __fdiv_rn(spread, 15.f) : fmaf(fmaf(-15.f, q, spread), kFifteenth, q));
-  const float scale = __bfloat162float(step);
+  float scale = __bfloat162float(step);
   meta = (uint32_t)__bfloat16_as_ushort(step) | ends << 16;
+  f32x2 v[4], y[4], back[4];
+  raw.unpack(v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = add2(v[i], pack2(-lo, -lo));
+  if (small) {  // the same quotients of larger numbers
+    scale *= 0x1p100f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], pack2(0x1p100f, 0x1p100f));
+  }
   // A product with the reciprocal is within 3e-6 of the quotient, which decides where it could lie on the other side of a border.
   const float inv = rcp(scale);
   constexpr float kRound = 12582912.f;  // 1.5 * 2^23: the sum's last bits are the rounded value
-  f32x2 v[4], y[4];
-  raw.unpack(v);
-  float r[8], far = small ? 1.f : 0.f;
+  float r[8], t[8], far = small ? 1.f : 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[i] = add2(v[i], pack2(-lo, -lo));
     y[i] = mul2(v[i], pack2(inv, inv));
-    const f32x2 z = add2(y[i], pack2(kRound, kRound)), back = add2(z, pack2(-kRound, -kRound));
-    float t0, t1;
-    unpack2(fma2(back, pack2(-1.f, -1.f), y[i]), t0, t1);
-    far = fmaxf(far, fmaxf(fabsf(t0), fabsf(t1)));
+    const f32x2 z = add2(y[i], pack2(kRound, kRound));
+    back[i] = add2(z, pack2(-kRound, -kRound));
+    unpack2(fma2(back[i], pack2(-1.f, -1.f), y[i]), t[2 * i], t[2 * i + 1]);
+    far = fmaxf(far, fmaxf(fabsf(t[2 * i]), fabsf(t[2 * i + 1])));
     unpack2(z, r[2 * i], r[2 * i + 1]);
   }
   if (far <= 0.4999f) {
@@ -147,30 +153,62 @@ __device__ __forceinline__ void quantise(const Raw8<__nv_bfloat16>& raw, uint32_
     return;
   }
   if (!(scale > 0.f)) return;
+  // Bf16 elements often lie on a border.  m: the one between two codes that y is next to; m scale has 13 bits and is exact, and
+  // so is the sign of what it leaves of the element (two fp32 numbers that differ do so by more than a quotient's rounding).
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float x0, x1;
-    unpack2(v[i], x0, x1);
-    codes |= (uint32_t)(int)fminf(rintf(__fdiv_rn(x0, scale)), 15.f) << (8 * i);
-    codes |= (uint32_t)(int)fminf(rintf(__fdiv_rn(x1, scale)), 15.f) << (8 * i + 4);
+    float x[2], n[2];
+    unpack2(v[i], x[0], x[1]);
+    unpack2(back[i], n[0], n[1]);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float m = n[u] + (t[2 * i + u] > 0.f ? 0.5f : -0.5f), rest = fmaf(-m, scale, x[u]);
+      const float up = m + 0.5f, down = m - 0.5f;
+      const float even = rintf(m);  // ties to even
+      const float code = fabsf(t[2 * i + u]) <= 0.4999f ? n[u] : rest > 0.f ? up : rest < 0.f ? down : even;
+      codes |= (uint32_t)(int)fminf(code, 15.f) << (8 * i + 4 * u);
+    }
   }
 }
 
-// One token's rows of some heads, from x (step `xh` from head to head) into the page at y (`size` bytes a head).
-struct Heads {
-  const void* x;
-  uint8_t* y;
-  int64_t xh, size;
-  int heads, slot;
+// A token of a call: where it stands and goes.
+struct Token {
+  uint32_t b, n;
+  bool report;  // of the warps with parts of it, this one tells of errors
 };
 
+// One token's keys or values of `heads` heads from h0 on.  Their rows are on their way before the token's place is known.
 template <typename T, bool kFour, int LPR, TurnKind kTurn>
-__device__ __forceinline__ void append_heads(const PagedAppendLaunch& a, const Heads& h, int64_t position) {
+__device__ __forceinline__ void append_heads(const PagedAppendLaunch& a, const Token& token, const View4& view, void* pool, int h0, int heads,
+                                             const Divisor& pages) {
   constexpr int R = 32 / LPR;
   constexpr bool kWhole = kFour || kTurn != kTurnHalves;
-  const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR, d = a.c.d;
+  const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR, d = kFour ? 8 * LPR : a.c.d;
   const bool on = col * 8 < d;
   const int2 at = runs_of<kFour ? kTurnNone : kTurn>(on ? col : 0, a.rot);
+  const T* x = static_cast<const T*>(view.ptr) + token.b * view.sb + token.n * view.st + (h0 + sub) * view.sh;
+  const int64_t xr = R * view.sh;
+  int left = on ? heads - sub : 0;  // this lane's rows: every R-th while it is positive
+  Raw8<T> raw[kRows];
+  auto load = [&] {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      raw[i].zero();
+      if (left > i * R) raw[i].template load<kWhole>(x, at);
+      x += xr;
+    }
+  };
+  load();
+  if (token.n >= sequence_length(a.lens, token.b, a.N, a.c.status, token.report && token.n == 0)) return;
+  const int64_t position = table_row(a.seen[token.b], token.n, a.c.width * a.c.page);  // below 2^31
+  const int column = (int)pages((uint32_t)position);
+  const int page = position < 0 || (a.rot > 0 && position >= a.positions) ? -1 : table_page(a.c, token.b, column);
+  if (page < 0) {
+    if (token.report) atomicOr(a.c.status, kStatusBadIndex);
+    return;
+  }
+  const int64_t size = page_bytes(a.c);
+  const int slot = (int)position - column * a.c.page;
   const float *cos = a.cos + position * (a.rot / 2), *sin = a.sin + position * (a.rot / 2);
   std::conditional_t<kFour, TurnWide<kTurn>, Turn<kTurn>> turn;
   turn.on = false;
@@ -178,18 +216,9 @@ __device__ __forceinline__ void append_heads(const PagedAppendLaunch& a, const H
     if constexpr (kFour) turn.init(cos, sin, a.rot, lane, col);
     else if (on) turn.init(cos, sin, a.rot, col);
   }
-  const T* x = static_cast<const T*>(h.x) + sub * h.xh;
-  uint8_t* y = h.y + sub * h.size;
-  int left = on ? h.heads - sub : 0;  // this lane's rows: every R-th while it is positive
+  uint8_t* y = static_cast<uint8_t*>(pool) + (page * a.c.Hkv + h0 + sub) * size;
 #pragma unroll 1
-  for (int more = h.heads; more > 0; more -= kRows * R, left -= kRows * R) {
-    Raw8<T> raw[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      raw[i].zero();
-      if (left > i * R) raw[i].template load<kWhole>(x, at);
-      x += R * h.xh;
-    }
+  for (int more = heads;;) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       if (more <= i * R) break;  // the same for the whole warp
@@ -197,10 +226,10 @@ __device__ __forceinline__ void append_heads(const PagedAppendLaunch& a, const H
         if constexpr (kTurn != kTurnNone) turn.apply(raw[i]);
         uint32_t codes, meta;
         quantise(raw[i], codes, meta);
-        const int groups = d / kGroup, g = col / 8, e = col % 8;
+        constexpr int kGroups = LPR / 8;
         if (left > i * R) {
-          reinterpret_cast<uint32_t*>(y + h.slot * (d / 2))[code_word(g, e, groups)] = codes;
-          if (e == 0) reinterpret_cast<uint32_t*>(y + a.c.page * (d / 2))[h.slot * groups + g] = meta;
+          reinterpret_cast<uint32_t*>(y + slot * (d / 2))[code_word(col / 8, col % 8, kGroups)] = codes;
+          if (col % 8 == 0) reinterpret_cast<uint32_t*>(y + a.c.page * (d / 2))[slot * kGroups + col / 8] = meta;
         }
       } else if (left > i * R) {
         if (kTurn != kTurnNone && turn.on) {  // other rows and elements go as they are, whatever they hold
@@ -209,42 +238,31 @@ __device__ __forceinline__ void append_heads(const PagedAppendLaunch& a, const H
           turn.apply(v, turn_rounded);
           raw[i].pack(v);
         }
-        raw[i].template store<kWhole>(reinterpret_cast<T*>(y) + (int64_t)h.slot * d, at);
+        raw[i].template store<kWhole>(reinterpret_cast<T*>(y) + (int64_t)slot * d, at);
       }
-      y += R * h.size;
+      y += R * size;
     }
+    more -= kRows * R;
+    if (more <= 0) return;
+    left -= kRows * R;
+    load();
   }
 }
 
 // A warp stores a token's keys or its values, `per` heads of them.
 template <typename T, bool kFour, int LPR, TurnKind kTurn>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kFour || sizeof(T) == 4 ? 3 : 4)
 paged_append_kernel(const PagedAppendLaunch a, const int per, const Divisor parts2, const Divisor tokens, const Divisor pages) {
   grid_dependents_trigger();
   grid_dependency_wait();
-  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), token = parts2(unit), b = tokens(token), n = token - b * tokens.d;
+  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), at = parts2(unit), b = tokens(at), n = at - b * tokens.d;
   if (b >= a.B) return;  // whole warps
-  const int part = (int)(unit - token * parts2.d), parts = (int)(parts2.d / 2);
-  const bool values = part >= parts, report = part == 0 && (threadIdx.x & 31) == 0;
-  if (n >= sequence_length(a.lens, b, a.N, a.c.status, report && n == 0)) return;
-  const int64_t p = table_row(a.seen[b], n, a.c.width * a.c.page);  // below 2^31
-  const int column = (int)pages((uint32_t)p);
-  const int page = p < 0 || (kTurn != kTurnNone && p >= a.positions) ? -1 : table_page(a.c, b, column);
-  if (page < 0) {
-    if (report) atomicOr(a.c.status, kStatusBadIndex);
-    return;
-  }
-  const int h0 = (values ? part - parts : part) * per;
-  const View4& view = values ? a.v : a.k;
-  Heads h;
-  h.size = page_bytes(a.c);
-  h.x = static_cast<const T*>(view.ptr) + b * view.sb + n * view.st + h0 * view.sh;
-  h.y = static_cast<uint8_t*>(values ? a.c.v : a.c.k) + (page * a.c.Hkv + h0) * h.size;
-  h.xh = view.sh;
-  h.heads = min(per, (int)a.c.Hkv - h0);
-  h.slot = (int)p - column * a.c.page;
-  if (kTurn == kTurnNone || values) append_heads<T, kFour, LPR, kTurnNone>(a, h, 0);
-  else append_heads<T, kFour, LPR, kTurn>(a, h, p);
+  const int part = (int)(unit - at * parts2.d), parts = (int)(parts2.d / 2);
+  const Token token{b, n, part == 0 && (threadIdx.x & 31) == 0};
+  const bool values = part >= parts;
+  const int h0 = (values ? part - parts : part) * per, heads = min(per, (int)a.c.Hkv - h0);
+  if (values) append_heads<T, kFour, LPR, kTurnNone>(a, token, a.v, a.c.v, h0, heads, pages);
+  else append_heads<T, kFour, LPR, kTurn>(a, token, a.k, a.c.k, h0, heads, pages);
 }
 
 // A warp reads 16 tokens of one head, keys or values.
@@ -280,48 +298,65 @@ paged_read_kernel(const PagedReadLaunch a, const Divisor tiles, const Divisor he
   TOut* y = static_cast<TOut*>(values ? a.v : a.k) + b * (values ? a.v_sb : a.k_sb) + h * (values ? a.v_sh : a.k_sh) + (n0 + sub) * yt;
   const int2 at = make_int2(8 * col, 8 * col + 4);
   const int there = have - n0 - sub, wanted = (a.fill ? end : have) - n0 - sub;  // this lane's rows: every R-th below
-  const int groups = d / kGroup;
-  const uint32_t* words = reinterpret_cast<const uint32_t*>(x) + (slot + sub) * (d / 8) + code_word(col / 8, col % 8, groups);
-  const uint32_t* metas = reinterpret_cast<const uint32_t*>(x + a.c.page * (d / 2)) + (slot + sub) * groups + col / 8;
+  constexpr int kGroups = LPR / 8, kWords = LPR;  // of a 4-bit row
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(x) + (slot + sub) * kWords + code_word(col / 8, col % 8, kGroups);
+  const uint32_t* metas = reinterpret_cast<const uint32_t*>(x + a.c.page * (kWords * 4)) + (slot + sub) * kGroups + col / 8;
   const T* rows = reinterpret_cast<const T*>(x) + (int64_t)(slot + sub) * d;
+  const int64_t yr = R * yt;
+  uint32_t magic = 0x43004300u;  // two bf16 128
+  asm volatile("" : "+r"(magic));
 
-#pragma unroll
-  for (int i0 = 0; i0 < 16 / R; i0 += kRows) {
-    Raw8<T> raw[kRows];
-    uint32_t codes[kRows], meta[kRows];
+  auto batch = [&](auto all, int i0) {  // all: every row is there
+    [[maybe_unused]] Raw8<T> raw[kRows];
+    [[maybe_unused]] uint32_t codes[kRows], meta[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      if (there <= (i0 + i) * R) continue;
+      if (!decltype(all)::value && there <= (i0 + i) * R) continue;
       if constexpr (kFour) {
-        codes[i] = words[(i0 + i) * R * (d / 8)];
-        meta[i] = metas[(i0 + i) * R * groups];
+        codes[i] = words[i * R * kWords];
+        meta[i] = metas[i * R * kGroups];
       } else {
-        raw[i].template load<true>(rows + (i0 + i) * R * d, at);
+        raw[i].template load<true>(rows + i * R * d, at);
       }
     }
+    words += kRows * R * kWords;
+    metas += kRows * R * kGroups;
+    rows += kRows * R * d;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (wanted <= (i0 + i) * R) continue;
+    for (int i = 0; i < kRows; ++i, y += yr) {
+      if (!decltype(all)::value && wanted <= (i0 + i) * R) continue;
       f32x2 v[4];
       Raw8<TOut> out;
-      if (there <= (i0 + i) * R) {
+      if (!decltype(all)::value && there <= (i0 + i) * R) {
         out.zero();
       } else {
         if constexpr (kFour) {
-          const float scale = __uint_as_float(meta[i] << 16), offset = __uint_as_float(meta[i] & 0xffff0000u);
+          const f32x2 scale = Raw8<__nv_bfloat16>::wide(__byte_perm(meta[i], 0u, 0x1010)), offset = Raw8<__nv_bfloat16>::wide(__byte_perm(meta[i], 0u, 0x3232));
+          float c[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // a code in the last bits of 2^23 is a float: no conversion, of which an SM makes 16 a clock
-            const f32x2 c = pack2(__uint_as_float((codes[i] >> (8 * e) & 15u) | 0x4b000000u), __uint_as_float((codes[i] >> (8 * e + 4) & 15u) | 0x4b000000u));
-            v[e] = fma2(add2(c, pack2(-0x1p23f, -0x1p23f)), pack2(scale, scale), pack2(offset, offset));
+          for (int m = 0; m < 4; ++m) {
+            // codes m and m + 4 as bf16 128 + code, exact, and no conversion, of which an SM makes 16 a clock
+            uint32_t w;
+            asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(w) : "r"(codes[i] >> (4 * m)), "r"(magic));
+            const f32x2 code = add2(Raw8<__nv_bfloat16>::wide(w), pack2(-128.f, -128.f));
+            unpack2(fma2(code, scale, offset), c[m], c[4 + m]);
           }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = pack2(c[2 * e], c[2 * e + 1]);
         } else {
           raw[i].unpack(v);
         }
         out.pack(v);
       }
-      out.template store<true>(y + (i0 + i) * R * yt, at);
+      out.template store<true>(y, at);
     }
+  };
+  if (have == n0 + 16) {
+#pragma unroll
+    for (int i0 = 0; i0 < 16 / R; i0 += kRows) batch(std::true_type{}, i0);
+  } else {
+#pragma unroll 1
+    for (int i0 = 0; i0 < 16 / R; i0 += kRows) batch(std::false_type{}, i0);
   }
 }
 
