@@ -587,7 +587,8 @@ la_status la_swa_biased_decode_step(const la_swa_biased_decode_args* args, void*
  *            [B, N] int64.  A token that stands outside the tables is skipped as padding is, and
  *            sets the device status word (LA_ERR_INVALID_ARGUMENT).
  *   lens, fill : as above (LA_FILL_ROWS)
- * fp32 arithmetic, one rounding to out_dtype. */
+ * fp32 arithmetic, one rounding to out_dtype.  Strides below 2^36 bytes (LA_ERR_UNSUPPORTED), here
+ * and of la_paged_append and la_paged_read. */
 #define LA_NORM_NONE 0
 #define LA_NORM_RMS 1
 #define LA_NORM_L2 2

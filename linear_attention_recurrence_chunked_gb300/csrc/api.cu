@@ -707,6 +707,16 @@ la::PagedCache cache_of(const Args* a, unsigned* status) {
   return c;
 }
 
+// Strides that 16 bytes times 32 bits hold
+bool spannable(const la_tensor& x, int64_t B, int64_t H, int64_t N, la_dtype dt) {
+  const int64_t end = (int64_t(1) << 36) / elem_bytes(dt);
+  return (B <= 1 || x.stride_b < end) && (H <= 1 || x.stride_h < end) && (N <= 1 || x.stride_t < end);
+}
+la::Span4 span(const la_tensor& x, int64_t B, int64_t H, int64_t N, la_dtype dt) {  // a spannable one; strides of single entries do not count
+  const int e = elem_bytes(dt);
+  return la::Span4{x.ptr, (uint32_t)(B > 1 ? x.stride_b * e / 16 : 0), (uint32_t)(H > 1 ? x.stride_h * e / 16 : 0), (uint32_t)(N > 1 ? x.stride_t * e / 16 : 0)};
+}
+
 bool same_rows(const la_tensor& x, const la_tensor& y) {
   return x.stride_b == y.stride_b && x.stride_h == y.stride_h && x.stride_t == y.stride_t;
 }
@@ -725,7 +735,7 @@ la_status la_qk_norm_rope(const la_qk_norm_rope_args* a, void* stream) {
   if (a->rot < 0 || a->rot > a->d) return LA_ERR_INVALID_ARGUMENT;
   if (a->rot % 16 != 0) return LA_ERR_UNSUPPORTED;
   if (a->B == 0 || a->N == 0 || (a->H == 0 && a->H_kv == 0)) return LA_OK;
-  if (!within(kMaxElems, {a->B, a->N, a->H + a->H_kv}) || la::qk_norm_rope_blocks(a->B, a->H, a->H_kv, a->N, (int)a->d) > kMaxBlocks / 4)
+  if (a->H + a->H_kv > (int64_t(1) << 30) || !within(kMaxElems, {a->B, a->N, a->H + a->H_kv}) || la::qk_norm_rope_blocks(a->B, a->H, a->H_kv, a->N, (int)a->d) > kMaxBlocks / 4)
     return LA_ERR_UNSUPPORTED;
   if (!valid_view(a->q, a->B, a->H, a->N, a->d, a->in_dtype) || !valid_view(a->q_out, a->B, a->H, a->N, a->d, a->out_dtype) ||
       !valid_view(a->k, a->B, a->H_kv, a->N, a->d, a->in_dtype) || !valid_view(a->k_out, a->B, a->H_kv, a->N, a->d, a->out_dtype) ||
@@ -734,6 +744,9 @@ la_status la_qk_norm_rope(const la_qk_norm_rope_args* a, void* stream) {
   if ((a->H > 0 && a->q.ptr == a->q_out.ptr && (a->in_dtype != a->out_dtype || !same_rows(a->q, a->q_out))) ||
       (a->H_kv > 0 && a->k.ptr == a->k_out.ptr && (a->in_dtype != a->out_dtype || !same_rows(a->k, a->k_out))))
     return LA_ERR_INVALID_ARGUMENT;
+  if (!spannable(a->q, a->B, a->H, a->N, a->in_dtype) || !spannable(a->k, a->B, a->H_kv, a->N, a->in_dtype) ||
+      !spannable(a->q_out, a->B, a->H, a->N, a->out_dtype) || !spannable(a->k_out, a->B, a->H_kv, a->N, a->out_dtype))
+    return LA_ERR_UNSUPPORTED;
   if (!valid_tables(a->cos, a->sin, a->rot, a->positions) || !aligned16(a->q_weight) || !aligned16(a->k_weight) || !aligned8(a->pos) ||
       !aligned8(a->lens))
     return LA_ERR_INVALID_ARGUMENT;
@@ -743,9 +756,8 @@ la_status la_qk_norm_rope(const la_qk_norm_rope_args* a, void* stream) {
   L.B = a->B; L.H = a->H; L.Hkv = a->H_kv; L.N = a->N; L.positions = a->positions;
   L.d = (int)a->d; L.rot = (int)a->rot; L.norm = a->norm;
   L.in_bf16 = a->in_dtype == LA_DTYPE_BF16; L.out_bf16 = a->out_dtype == LA_DTYPE_BF16; L.w_bf16 = a->w_dtype == LA_DTYPE_BF16;
-  L.q = view(a->q); L.k = view(a->k); L.q_out = a->q_out.ptr; L.k_out = a->k_out.ptr;
-  L.q_sb = a->q_out.stride_b; L.q_sh = a->q_out.stride_h; L.q_st = a->q_out.stride_t;
-  L.k_sb = a->k_out.stride_b; L.k_sh = a->k_out.stride_h; L.k_st = a->k_out.stride_t;
+  L.q = span(a->q, a->B, a->H, a->N, a->in_dtype); L.k = span(a->k, a->B, a->H_kv, a->N, a->in_dtype);
+  L.q_out = span(a->q_out, a->B, a->H, a->N, a->out_dtype); L.k_out = span(a->k_out, a->B, a->H_kv, a->N, a->out_dtype);
   L.q_weight = a->q_weight; L.k_weight = a->k_weight; L.cos = a->cos; L.sin = a->sin; L.pos = a->pos; L.lens = a->lens;
   L.eps = a->eps; L.interleaved = a->interleaved != 0; L.pos_each = a->pos_each != 0; L.fill = (a->fill & LA_FILL_ROWS) != 0;
   L.status = status;
@@ -764,12 +776,13 @@ la_status la_paged_append(const la_paged_append_args* a, void* stream) {
   if (!valid_view(a->k, a->B, a->H_kv, a->N, a->d, a->in_dtype) || !valid_view(a->v, a->B, a->H_kv, a->N, a->d, a->in_dtype) ||
       !valid_pools(a, a->B) || !valid_tables(a->cos, a->sin, a->rot, a->positions) || !a->seen || !aligned8(a->seen) || !aligned8(a->lens))
     return LA_ERR_INVALID_ARGUMENT;
+  if (!spannable(a->k, a->B, a->H_kv, a->N, a->in_dtype) || !spannable(a->v, a->B, a->H_kv, a->N, a->in_dtype)) return LA_ERR_UNSUPPORTED;
   unsigned* status = device_status_ptr();
   if (!status) return LA_ERR_CUDA;
   la::PagedAppendLaunch L{};
   L.c = cache_of(a, status);
   L.B = a->B; L.N = a->N; L.positions = a->positions; L.rot = (int)a->rot;
-  L.k = view(a->k); L.v = view(a->v); L.cos = a->cos; L.sin = a->sin; L.seen = a->seen; L.lens = a->lens;
+  L.k = span(a->k, a->B, a->H_kv, a->N, a->in_dtype); L.v = span(a->v, a->B, a->H_kv, a->N, a->in_dtype); L.cos = a->cos; L.sin = a->sin; L.seen = a->seen; L.lens = a->lens;
   L.interleaved = a->interleaved != 0;
   return from_cuda(la::launch_paged_append(L, static_cast<cudaStream_t>(stream)));
 }
@@ -784,13 +797,13 @@ la_status la_paged_read(const la_paged_read_args* a, void* stream) {
   if (!valid_view(a->k, a->B, a->H_kv, a->N, a->d, a->out_dtype) || !valid_view(a->v, a->B, a->H_kv, a->N, a->d, a->out_dtype) ||
       !distinct(a->k, a->B, a->H_kv, a->N, a->d) || !distinct(a->v, a->B, a->H_kv, a->N, a->d) || !valid_pools(a, a->B) || !aligned8(a->lens))
     return LA_ERR_INVALID_ARGUMENT;
+  if (!spannable(a->k, a->B, a->H_kv, a->N, a->out_dtype) || !spannable(a->v, a->B, a->H_kv, a->N, a->out_dtype)) return LA_ERR_UNSUPPORTED;
   unsigned* status = device_status_ptr();
   if (!status) return LA_ERR_CUDA;
   la::PagedReadLaunch L{};
   L.c = cache_of(a, status);
   L.B = a->B; L.N = a->N; L.out_bf16 = a->out_dtype == LA_DTYPE_BF16; L.fill = (a->fill & LA_FILL_ROWS) != 0;
-  L.k = a->k.ptr; L.k_sb = a->k.stride_b; L.k_sh = a->k.stride_h; L.k_st = a->k.stride_t;
-  L.v = a->v.ptr; L.v_sb = a->v.stride_b; L.v_sh = a->v.stride_h; L.v_st = a->v.stride_t;
+  L.k = span(a->k, a->B, a->H_kv, a->N, a->out_dtype); L.v = span(a->v, a->B, a->H_kv, a->N, a->out_dtype);
   L.lens = a->lens;
   return from_cuda(la::launch_paged_read(L, static_cast<cudaStream_t>(stream)));
 }

@@ -70,17 +70,19 @@ qk_norm_rope_kernel(const QkNormRopeLaunch a, const Plan p) {
 #pragma unroll 1
   for (int keys = 0; keys < 2; ++keys) {
     // this warp's heads of the queries, or of the keys
-    const int64_t before = keys ? a.H : 0, heads = keys ? a.Hkv : a.H;
-    const int64_t h0 = max((int64_t)part * p.per - before, (int64_t)0), h1 = min((int64_t)(part + 1) * p.per - before, heads);
+    const int before = keys ? (int)a.H : 0, heads = keys ? (int)a.Hkv : (int)a.H;
+    const int h0 = max(part * p.per - before, 0), h1 = min((part + 1) * p.per - before, heads);
     if (h0 >= h1) continue;
-    const TIn* x = static_cast<const TIn*>(keys ? a.k.ptr : a.q.ptr) + b * (keys ? a.k.sb : a.q.sb) + n * (keys ? a.k.st : a.q.st);
-    TOut* y = static_cast<TOut*>(keys ? a.k_out : a.q_out) + b * (keys ? a.k_sb : a.q_sb) + n * (keys ? a.k_st : a.q_st);
-    const int64_t xh = keys ? a.k.sh : a.q.sh, yh = keys ? a.k_sh : a.q_sh;
+    const TIn* x = keys ? a.k.at<const TIn>(b, h0 + sub, n) : a.q.at<const TIn>(b, h0 + sub, n);
+    TOut* y = keys ? a.k_out.at<TOut>(b, h0 + sub, n) : a.q_out.at<TOut>(b, h0 + sub, n);
+    const int64_t xr = R * (keys ? a.k.step<TIn>() : a.q.step<TIn>()), yr = R * (keys ? a.k_out.step<TOut>() : a.q_out.step<TOut>());
     if (!alive) {
       Raw8<TOut> zero;
       zero.zero();
-      for (int64_t h = h0 + sub; h < h1; h += R)
-        if (on) zero.template store<kWhole>(y + h * yh, at);
+      for (int h = h0 + sub; h < h1; h += R) {
+        if (on) zero.template store<kWhole>(y, at);
+        y += yr;
+      }
       continue;
     }
     const void* weight = keys ? a.k_weight : a.q_weight;
@@ -97,17 +99,15 @@ qk_norm_rope_kernel(const QkNormRopeLaunch a, const Plan p) {
       }
     }
 
-    x += (h0 + sub) * xh;
-    y += (h0 + sub) * yh;
-    int left = on ? (int)(h1 - h0) - sub : 0;  // this lane's rows: every R-th while it is positive
+    int left = on ? h1 - h0 - sub : 0;  // this lane's rows: every R-th while it is positive
 #pragma unroll 1
-    for (int more = (int)(h1 - h0); more > 0; more -= kRows * R, left -= kRows * R) {
+    for (int more = h1 - h0; more > 0; more -= kRows * R, left -= kRows * R) {
       Raw8<TIn> raw[kRows];
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         raw[i].zero();
         if (left > i * R) raw[i].template load<kWhole>(x, at);
-        x += R * xh;
+        x += xr;
       }
       float scale[kRows];
       if constexpr (kNorm) {
@@ -172,7 +172,7 @@ qk_norm_rope_kernel(const QkNormRopeLaunch a, const Plan p) {
         Raw8<TOut> out;
         out.pack(v);
         out.template store<kWhole>(y, at);
-        y += R * yh;
+        y += yr;
       }
     }
   }

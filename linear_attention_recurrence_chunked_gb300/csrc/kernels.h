@@ -224,14 +224,26 @@ struct SwaBiasedDecodeLaunch {
 };
 cudaError_t launch_swa_biased_decode(const SwaBiasedDecodeLaunch& a, cudaStream_t stream);
 
+// A [B, H, N, d] view whose strides are counted in 16 bytes: an element's place takes 32-bit products.
+struct Span4 {
+  void* ptr;
+  uint32_t sb, sh, st;
+#ifdef __CUDACC__
+  template <typename T>
+  __device__ __forceinline__ T* at(uint32_t b, uint32_t h, uint32_t n) const {
+    return reinterpret_cast<T*>(static_cast<uint4*>(ptr) + ((uint64_t)b * sb + (uint64_t)h * sh + (uint64_t)n * st));
+  }
+  template <typename T>
+  __device__ __forceinline__ int64_t step() const { return (int64_t)sh * (16 / (int)sizeof(T)); }  // elements from head to head
+#endif
+};
+
 // Norms and position rotation of queries and keys (heads.cu).
 struct QkNormRopeLaunch {
   int64_t B, H, Hkv, N, positions;
   int d, rot, norm;
   bool in_bf16, out_bf16, w_bf16;
-  View4 q, k;
-  void *q_out, *k_out;
-  int64_t q_sb, q_sh, q_st, k_sb, k_sh, k_st;  // of the outputs
+  Span4 q, k, q_out, k_out;
   const void *q_weight, *k_weight;
   const float *cos, *sin;
   const int64_t *pos, *lens;
@@ -255,7 +267,7 @@ struct PagedAppendLaunch {
   PagedCache c;
   int64_t B, N, positions;
   int rot;
-  View4 k, v;
+  Span4 k, v;
   const float *cos, *sin;
   const int64_t *seen, *lens;
   bool interleaved;
@@ -264,8 +276,7 @@ struct PagedReadLaunch {
   PagedCache c;
   int64_t B, N;
   bool out_bf16, fill;
-  void *k, *v;
-  int64_t k_sb, k_sh, k_st, v_sb, v_sh, v_st;
+  Span4 k, v;
   const int64_t* lens;
 };
 cudaError_t launch_paged_append(const PagedAppendLaunch& a, cudaStream_t stream);

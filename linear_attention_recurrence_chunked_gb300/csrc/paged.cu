@@ -23,11 +23,7 @@ __device__ __forceinline__ f32x2 turn_exact(f32x2 x, f32x2 c, f32x2 y, f32x2 s) 
   const f32x2 q = mul2(y, s), eq = fma2(y, s, mul2(q, minus));
   const f32x2 sum = add2(p, q), t = sub(sum, p);
   const f32x2 es = add2(sub(p, sub(sum, t)), sub(q, t));
-  const f32x2 r = add2(sum, add2(es, add2(ep, eq)));
-  float s0, s1, r0, r1;
-  unpack2(sum, s0, s1);
-  unpack2(r, r0, r1);
-  return pack2(fabsf(s0) <= 3.402823466e38f ? r0 : s0, fabsf(s1) <= 3.402823466e38f ? r1 : s1);  // the parts of an infinity are NaN
+  return add2(sum, add2(es, add2(ep, eq)));  // of an infinity NaN, as the whole group then is
 }
 
 // A lane's angles for eight consecutive elements, whose partners at rot / 2 are those of lane +- rot / 16.
@@ -123,7 +119,7 @@ __device__ __forceinline__ void quantise(const Raw8<__nv_bfloat16>& raw, uint32_
   const __nv_bfloat16 step = __float2bfloat16_rn(small ? __fdiv_rn(spread, 15.f) : fmaf(fmaf(-15.f, q, spread), kFifteenth, q));
   float scale = __bfloat162float(step);
   meta = (uint32_t)__bfloat16_as_ushort(step) | ends << 16;
-  f32x2 v[4], y[4], back[4];
+  f32x2 v[4];
   raw.unpack(v);
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = add2(v[i], pack2(-lo, -lo));
@@ -132,43 +128,24 @@ __device__ __forceinline__ void quantise(const Raw8<__nv_bfloat16>& raw, uint32_
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], pack2(0x1p100f, 0x1p100f));
   }
-  // A product with the reciprocal is within 3e-6 of the quotient, which decides where it could lie on the other side of a border.
-  const float inv = rcp(scale);
-  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: the sum's last bits are the rounded value
-  float r[8], t[8], far = small ? 1.f : 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    y[i] = mul2(v[i], pack2(inv, inv));
-    const f32x2 z = add2(y[i], pack2(kRound, kRound));
-    back[i] = add2(z, pack2(-kRound, -kRound));
-    unpack2(fma2(back[i], pack2(-1.f, -1.f), y[i]), t[2 * i], t[2 * i + 1]);
-    far = fmaxf(far, fmaxf(fabsf(t[2 * i]), fabsf(t[2 * i + 1])));
-    unpack2(z, r[2 * i], r[2 * i + 1]);
-  }
-  if (far <= 0.4999f) {
-    // the sums' bits are 0x4b400000 + code
-#pragma unroll
-    for (int e = 0; e < 8; ++e) codes += __float_as_uint(r[e]) << (4 * e);
-    codes -= 0x4b400000u * 0x11111111u;
-    return;
-  }
   if (!(scale > 0.f)) return;
-  // Bf16 elements often lie on a border.  m: the one between two codes that y is next to; m scale has 13 bits and is exact, and
-  // so is the sign of what it leaves of the element (two fp32 numbers that differ do so by more than a quotient's rounding).
+  // Bf16 elements often lie on a border, so the quotient has to be the rounded one (the remainder again): a border, which fp32
+  // holds, then comes out as it is, and what is next to one does not.  The sum with 1.5 * 2^23 rounds it to even.
+  const float inv = rcp(scale);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float x[2], n[2];
-    unpack2(v[i], x[0], x[1]);
-    unpack2(back[i], n[0], n[1]);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float m = n[u] + (t[2 * i + u] > 0.f ? 0.5f : -0.5f), rest = fmaf(-m, scale, x[u]);
-      const float up = m + 0.5f, down = m - 0.5f;
-      const float even = rintf(m);  // ties to even
-      const float code = fabsf(t[2 * i + u]) <= 0.4999f ? n[u] : rest > 0.f ? up : rest < 0.f ? down : even;
-      codes |= (uint32_t)(int)fminf(code, 15.f) << (8 * i + 4 * u);
+    const f32x2 y = mul2(v[i], pack2(inv, inv));
+    f32x2 quotient = fma2(fma2(y, pack2(-scale, -scale), v[i]), pack2(inv, inv), y);
+    float z[2];
+    if (small) {  // where a scale has few bits, quotients can pass 15
+      unpack2(quotient, z[0], z[1]);
+      quotient = pack2(fminf(z[0], 15.f), fminf(z[1], 15.f));
     }
+    unpack2(add2(quotient, pack2(12582912.f, 12582912.f)), z[0], z[1]);
+    codes += __float_as_uint(z[0]) << (8 * i);
+    codes += __float_as_uint(z[1]) << (8 * i + 4);
   }
+  codes -= 0x4b400000u * 0x11111111u;  // the sums' bits are 0x4b400000 + code
 }
 
 // A token of a call: where it stands and goes.
@@ -179,15 +156,15 @@ struct Token {
 
 // One token's keys or values of `heads` heads from h0 on.  Their rows are on their way before the token's place is known.
 template <typename T, bool kFour, int LPR, TurnKind kTurn>
-__device__ __forceinline__ void append_heads(const PagedAppendLaunch& a, const Token& token, const View4& view, void* pool, int h0, int heads,
+__device__ __forceinline__ void append_heads(const PagedAppendLaunch& a, const Token& token, const Span4& view, void* pool, int h0, int heads,
                                              const Divisor& pages) {
   constexpr int R = 32 / LPR;
   constexpr bool kWhole = kFour || kTurn != kTurnHalves;
   const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR, d = kFour ? 8 * LPR : a.c.d;
   const bool on = col * 8 < d;
   const int2 at = runs_of<kFour ? kTurnNone : kTurn>(on ? col : 0, a.rot);
-  const T* x = static_cast<const T*>(view.ptr) + token.b * view.sb + token.n * view.st + (h0 + sub) * view.sh;
-  const int64_t xr = R * view.sh;
+  const T* x = view.at<const T>(token.b, h0 + sub, token.n);
+  const int64_t xr = R * view.step<T>();
   int left = on ? heads - sub : 0;  // this lane's rows: every R-th while it is positive
   Raw8<T> raw[kRows];
   auto load = [&] {
@@ -207,16 +184,16 @@ __device__ __forceinline__ void append_heads(const PagedAppendLaunch& a, const T
     if (token.report) atomicOr(a.c.status, kStatusBadIndex);
     return;
   }
-  const int64_t size = page_bytes(a.c);
+  const int size = page_bytes(a.c);
   const int slot = (int)position - column * a.c.page;
-  const float *cos = a.cos + position * (a.rot / 2), *sin = a.sin + position * (a.rot / 2);
+  const float *cos = a.cos + (uint64_t)(uint32_t)position * (uint32_t)(a.rot / 2), *sin = a.sin + (uint64_t)(uint32_t)position * (uint32_t)(a.rot / 2);
   std::conditional_t<kFour, TurnWide<kTurn>, Turn<kTurn>> turn;
   turn.on = false;
   if constexpr (kTurn != kTurnNone) {
     if constexpr (kFour) turn.init(cos, sin, a.rot, lane, col);
     else if (on) turn.init(cos, sin, a.rot, col);
   }
-  uint8_t* y = static_cast<uint8_t*>(pool) + (page * a.c.Hkv + h0 + sub) * size;
+  uint8_t* y = static_cast<uint8_t*>(pool) + ((uint64_t)(uint32_t)page * (uint32_t)a.c.Hkv + (uint32_t)(h0 + sub)) * (uint32_t)size;
 #pragma unroll 1
   for (int more = heads;;) {
 #pragma unroll
@@ -238,9 +215,9 @@ __device__ __forceinline__ void append_heads(const PagedAppendLaunch& a, const T
           turn.apply(v, turn_rounded);
           raw[i].pack(v);
         }
-        raw[i].template store<kWhole>(reinterpret_cast<T*>(y) + (int64_t)slot * d, at);
+        raw[i].template store<kWhole>(reinterpret_cast<T*>(y) + slot * d, at);
       }
-      y += R * size;
+      y += (int64_t)R * size;
     }
     more -= kRows * R;
     if (more <= 0) return;
@@ -293,16 +270,16 @@ paged_read_kernel(const PagedReadLaunch a, const Divisor tiles, const Divisor he
   }
   if (have == n0 && !a.fill) return;
   if (!on) return;  // no lane waits for another from here on
-  const uint8_t* x = static_cast<const uint8_t*>(values ? a.c.v : a.c.k) + (max(page, 0) * a.c.Hkv + h) * page_bytes(a.c);
-  const int64_t yt = values ? a.v_st : a.k_st;
-  TOut* y = static_cast<TOut*>(values ? a.v : a.k) + b * (values ? a.v_sb : a.k_sb) + h * (values ? a.v_sh : a.k_sh) + (n0 + sub) * yt;
+  const uint8_t* x = static_cast<const uint8_t*>(values ? a.c.v : a.c.k) + ((uint64_t)max(page, 0) * (uint32_t)a.c.Hkv + h) * (uint32_t)page_bytes(a.c);
+  const Span4& out = values ? a.v : a.k;
+  TOut* y = out.at<TOut>(b, h, n0 + sub);
   const int2 at = make_int2(8 * col, 8 * col + 4);
   const int there = have - n0 - sub, wanted = (a.fill ? end : have) - n0 - sub;  // this lane's rows: every R-th below
   constexpr int kGroups = LPR / 8, kWords = LPR;  // of a 4-bit row
   const uint32_t* words = reinterpret_cast<const uint32_t*>(x) + (slot + sub) * kWords + code_word(col / 8, col % 8, kGroups);
   const uint32_t* metas = reinterpret_cast<const uint32_t*>(x + a.c.page * (kWords * 4)) + (slot + sub) * kGroups + col / 8;
   const T* rows = reinterpret_cast<const T*>(x) + (int64_t)(slot + sub) * d;
-  const int64_t yr = R * yt;
+  const int64_t yr = (int64_t)R * out.st * (16 / sizeof(TOut));
   uint32_t magic = 0x43004300u;  // two bf16 128
   asm volatile("" : "+r"(magic));
 
@@ -326,9 +303,9 @@ paged_read_kernel(const PagedReadLaunch a, const Divisor tiles, const Divisor he
     for (int i = 0; i < kRows; ++i, y += yr) {
       if (!decltype(all)::value && wanted <= (i0 + i) * R) continue;
       f32x2 v[4];
-      Raw8<TOut> out;
+      Raw8<TOut> packed;
       if (!decltype(all)::value && there <= (i0 + i) * R) {
-        out.zero();
+        packed.zero();
       } else {
         if constexpr (kFour) {
           const f32x2 scale = Raw8<__nv_bfloat16>::wide(__byte_perm(meta[i], 0u, 0x1010)), offset = Raw8<__nv_bfloat16>::wide(__byte_perm(meta[i], 0u, 0x3232));
@@ -346,9 +323,9 @@ paged_read_kernel(const PagedReadLaunch a, const Divisor tiles, const Divisor he
         } else {
           raw[i].unpack(v);
         }
-        out.pack(v);
+        packed.pack(v);
       }
-      out.template store<true>(y, at);
+      packed.template store<true>(y, at);
     }
   };
   if (have == n0 + 16) {

@@ -8,8 +8,8 @@ namespace la {
 constexpr int kGroup = 64;  // elements that share a scale and an offset
 
 // Bytes of a page's tokens of one head.
-__host__ __device__ __forceinline__ int64_t page_bytes(const PagedCache& c) {
-  return (int64_t)c.page * (c.four ? c.d * 9 / 16 : c.d * (c.bf16 ? 2 : 4));
+__host__ __device__ __forceinline__ int page_bytes(const PagedCache& c) {
+  return c.page * (c.four ? c.d * 9 / 16 : c.d * (c.bf16 ? 2 : 4));
 }
 
 // Page of column `at` of a sequence's table, or -1 where it is none of the pool's.

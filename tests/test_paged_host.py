@@ -66,7 +66,8 @@ def step_args(**kw):
     (dict(k=T(at(1), 1280, 640, 63)), INV), (dict(q_out=T(at(2), 0, 640, 64)), INV), (dict(k_out=T(at(3), 1280, 0, 64)), INV),
     (dict(q_out=T(at(0), 5120, 1280, 128)), INV), (dict(q_out=T(at(0), 2560, 640, 64), out_dtype=FP), INV), (dict(q_weight=at(4) + 8), INV),
     (dict(pos=at(8) + 4), INV), (dict(lens=at(9) + 4), INV),
-    (dict(B=1 << 30, N=1 << 20), UNS), (dict(B=0), la.LA_OK), (dict(N=0), la.LA_OK), (dict(H=0, H_kv=0), la.LA_OK)])
+    (dict(B=1 << 30, N=1 << 20), UNS), (dict(k=T(at(1), 1 << 35, 640, 64)), UNS), (dict(q_out=T(at(2), 2560, 1 << 35, 64)), UNS),
+    (dict(H=1 << 31), UNS), (dict(B=0), la.LA_OK), (dict(N=0), la.LA_OK), (dict(H=0, H_kv=0), la.LA_OK)])
 def test_qk_norm_rope_refusals(lib, kw, status):
     assert lib.la_qk_norm_rope(ctypes.byref(qk_args(**kw)), None) == status
 
@@ -81,8 +82,8 @@ PAGES = [
 @pytest.mark.parametrize("kw,status", PAGES + [
     (dict(B=-1), INV), (dict(N=1 << 41), INV), (dict(rot=8), UNS), (dict(rot=-16), INV), (dict(rot=80), INV), (dict(cos=None), INV),
     (dict(seen=None), INV), (dict(seen=at(5) + 4), INV), (dict(lens=at(8) + 4), INV), (dict(k=T(None, 1280, 640, 64)), INV),
-    (dict(v=T(at(1), 1280, 640, 32)), INV), (dict(B=1 << 20, N=1 << 12, width=1), UNS), (dict(B=0), la.LA_OK), (dict(N=0), la.LA_OK),
-    (dict(H_kv=0), la.LA_OK)])
+    (dict(v=T(at(1), 1280, 640, 32)), INV), (dict(B=1 << 20, N=1 << 12, width=1), UNS), (dict(v=T(at(1), 1 << 35, 640, 64)), UNS),
+    (dict(B=0), la.LA_OK), (dict(N=0), la.LA_OK), (dict(H_kv=0), la.LA_OK)])
 def test_paged_append_refusals(lib, kw, status):
     assert lib.la_paged_append(ctypes.byref(append_args(**kw)), None) == status
 
