@@ -1046,9 +1046,9 @@ def la_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, norm: str | None = 
     each = pos is not None and pos.dim() == 2
     made = [q_out is None, k is not None and k_out is None]
     if made[0]:
-        q_out = torch.empty_like(q, dtype=out_dtype or qt, memory_format=torch.contiguous_format)
+        q_out = torch.empty(q.shape, dtype=out_dtype or qt, device=q.device)
     if made[1]:
-        k_out = torch.empty_like(k, dtype=q_out.dtype, memory_format=torch.contiguous_format)
+        k_out = torch.empty(k.shape, dtype=q_out.dtype, device=q.device)
     if k is None and k_out is not None:
         raise ValueError("k_out without k")
     if lens is not None and made[0] != made[1] and k is not None:

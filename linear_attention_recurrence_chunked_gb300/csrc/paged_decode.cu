@@ -4,7 +4,7 @@
 //
 // A warp takes tiles of 32 tokens of its block's part in turn.  It scores them for a few query heads of the group, four
 // elements a lane and d / 4 lanes a row, takes their softmax a token a lane with the running maximum and sum of its
-// tokens so far, and adds up its value rows; warps do not wait for one another before the end, where their sums meet in
+// tokens so far, and adds up its value rows, the next few rows always on their way; warps do not wait for one another before the end, where their sums meet in
 // shared memory.
 #include <algorithm>
 
@@ -61,37 +61,54 @@ paged_decode_f32_kernel(const PagedDecodeLaunch a, const int passes) {
     l[g] = 0.f;
   }
 
-  for (int t0 = first + warp * kTokens; t0 < last; t0 += kWarps * kTokens) {
-    // the tile's two pages; tokens of a page that is not there are not seen
-    int page[2];
+  // A tile's place: its tokens' two pages; tokens of a page that is not there are not seen.
+  struct Tile { int t0, page[2], slot[2]; };
+  auto lookup = [&](int t0) {
+    Tile n{t0, {-1, -1}, {0, 0}};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int at = t0 + i * kTile;
-      page[i] = at < last ? table_page(a.c, s, at / a.c.page) : -1;
-      if (at < last && page[i] < 0 && hk == 0 && pass == 0 && lane == 0) atomicOr(a.c.status, kStatusBadIndex);
+      if (at >= last) continue;
+      n.page[i] = table_page(a.c, s, at / a.c.page);
+      n.slot[i] = at % a.c.page;
+      if (n.page[i] < 0 && hk == 0 && pass == 0 && lane == 0) atomicOr(a.c.status, kStatusBadIndex);
     }
-    auto seen = [&](int r) { return t0 + r >= t.lo && t0 + r < last && (r < kTile ? page[0] : page[1]) >= 0; };
-    const int slot[2] = {t0 % a.c.page, (t0 + kTile) % a.c.page};
-    auto row = [&](const void* pool, int r, float (&x)[4]) {
-      Raw4<float> raw;
-      raw.zero();
-      if (on && seen(r)) {
-        const int64_t at = ((r < kTile ? page[0] : page[1]) * a.c.Hkv + hk) * a.c.page + (r < kTile ? slot[0] + r : slot[1] + r - kTile);
-        raw.load(static_cast<const float*>(pool) + at * d + col);
+    return n;
+  };
+  auto seen = [&](const Tile& n, int r) { return n.t0 + r >= t.lo && n.t0 + r < last && (r < kTile ? n.page[0] : n.page[1]) >= 0; };
+  // batch bt of a tile: its keys, then its values; zeros where nothing is seen
+  auto fetch = [&](const Tile& n, int bt, Raw4<float> (&raw)[kLoads]) {
+    const float* pool = static_cast<const float*>(bt < kBatches ? a.c.k : a.c.v) + col;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = bt % kBatches * kBatch + i * R + sub;
+      raw[i].zero();
+      if (on && seen(n, r)) {
+        const int64_t at = ((r < kTile ? n.page[0] : n.page[1]) * a.c.Hkv + hk) * a.c.page + (r < kTile ? n.slot[0] + r : n.slot[1] + r - kTile);
+        raw[i].load(pool + at * d);
       }
-      raw.unpack(x);
-    };
+    }
+  };
+  constexpr int kStep = kWarps * kTokens;
+  Tile now = lookup(first + warp * kTokens), next = lookup(first + warp * kTokens + kStep);
+  Raw4<float> raw[kLoads], ahead[kLoads];
+  fetch(now, 0, ahead);
+#pragma unroll 1
+  for (; now.t0 < last; now = next, next = lookup(now.t0 + kStep)) {
     // ---- scores
 #pragma unroll
     for (int bt = 0; bt < kBatches; ++bt) {
-      float k[kLoads][4], sum[NV];
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) row(a.c.k, bt * kBatch + i * R + sub, k[i]);
+      for (int i = 0; i < kLoads; ++i) raw[i] = ahead[i];
+      fetch(now, bt + 1, ahead);  // the first values behind the last keys
+      float sum[NV];
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i)
+      for (int i = 0; i < kLoads; ++i) {
+        float k[4];
+        raw[i].unpack(k);
 #pragma unroll
-        for (int g = 0; g < HG; ++g)
-          sum[i * HG + g] = fmaf(q[g][3], k[i][3], fmaf(q[g][2], k[i][2], fmaf(q[g][1], k[i][1], q[g][0] * k[i][0])));
+        for (int g = 0; g < HG; ++g) sum[i * HG + g] = fmaf(q[g][3], k[3], fmaf(q[g][2], k[2], fmaf(q[g][1], k[1], q[g][0] * k[0])));
+      }
       // sums over the row's lanes: halve the values while there are lanes to share them with
       int at = 0, left = NV;
 #pragma unroll
@@ -118,14 +135,14 @@ paged_decode_f32_kernel(const PagedDecodeLaunch a, const int passes) {
     }
     __syncwarp();
     // ---- softmax with what came before, a token a lane
-    const bool mine = seen(lane);
+    const bool mine = seen(now, lane);
     float f[HG];
 #pragma unroll
     for (int g = 0; g < HG; ++g) {
       float x = s_p[warp][lane][g] * a.scale;
       if (a.softcap != 0.f) x = a.softcap * tanhf(x / a.softcap);  // fp32 throughout: the polynomial of `capped` is off by 10 half steps
       x *= kLog2e;
-      if (a.slopes && g < heads) x = fmaf(-a.slopes[h0 + g] * kLog2e, (float)(t.hi - 1 - t0 - lane), x);
+      if (a.slopes && g < heads) x = fmaf(-a.slopes[h0 + g] * kLog2e, (float)(t.hi - 1 - now.t0 - lane), x);
       if (!mine) x = -INFINITY;
       float top = x;
 #pragma unroll
@@ -146,17 +163,21 @@ paged_decode_f32_kernel(const PagedDecodeLaunch a, const int passes) {
       for (int e = 0; e < 4; ++e) o[g][e] *= f[g];
 #pragma unroll
     for (int bt = 0; bt < kBatches; ++bt) {
-      float v[kLoads][4];
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) row(a.c.v, bt * kBatch + i * R + sub, v[i]);
+      for (int i = 0; i < kLoads; ++i) raw[i] = ahead[i];
+      if (bt + 1 < kBatches) fetch(now, kBatches + bt + 1, ahead);
+      else fetch(next, 0, ahead);
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i)
+      for (int i = 0; i < kLoads; ++i) {
+        float v[4];
+        raw[i].unpack(v);
 #pragma unroll
         for (int g = 0; g < HG; ++g) {
           const float p = s_p[warp][bt * kBatch + i * R + sub][g];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[g][e] = fmaf(p, v[i][e], o[g][e]);
+          for (int e = 0; e < 4; ++e) o[g][e] = fmaf(p, v[e], o[g][e]);
         }
+      }
     }
     __syncwarp();  // the weights are used up
   }
