@@ -820,8 +820,7 @@ static la_status paged_decode_shape(const la_paged_decode_args* a) {
 
 static int paged_decode_plan(const la_paged_decode_args* a) {
   const int64_t tokens = a->width * a->page;
-  return la::paged_decode_splits(a->S, a->H_kv, (int)(a->H / a->H_kv), a->window > 0 ? std::min(tokens, a->window + 16) : tokens,
-                                 a->in_dtype == LA_DTYPE_BF16, a->bits == 4);
+  return la::paged_decode_splits(a->S, a->H_kv, a->window > 0 ? std::min(tokens, a->window + 16) : tokens);
 }
 
 size_t la_paged_decode_workspace_size(const la_paged_decode_args* a) {

@@ -296,7 +296,7 @@ struct PagedDecodeLaunch {
   int splits;    // of a sequence's tokens; more than one: the parts meet in `parts`
   float* parts;  // [S, H, splits, d + 2]: sums of weighted values, their greatest score, the sum of weights
 };
-int paged_decode_splits(int64_t S, int64_t Hkv, int group, int64_t tokens, bool bf16, bool four);
+int paged_decode_splits(int64_t S, int64_t Hkv, int64_t tokens);
 cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream);
 
 }  // namespace la

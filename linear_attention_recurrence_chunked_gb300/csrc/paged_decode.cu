@@ -218,15 +218,18 @@ paged_decode_f32_kernel(const PagedDecodeLaunch a, const int passes) {
   }
 }
 
-// The parts of a split sequence together: a block a query head, each warp a quarter of the parts, four elements a lane.
+constexpr int kJoinWarps = 8;
+
+// The parts of a split sequence together: a block a query head, its warps (one for a few parts, or kJoinWarps) in turn a part,
+// four elements a lane.
 template <typename TOut>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kJoinWarps)
 paged_join_kernel(const PagedDecodeLaunch a) {
-  __shared__ float s_o[kWarps][kMaxD], s_l[kWarps];
+  __shared__ float s_o[kJoinWarps][kMaxD], s_l[kJoinWarps];
   grid_dependents_trigger();
   grid_dependency_wait();
   const int64_t s = blockIdx.x / a.H, h = blockIdx.x - s * a.H;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = a.c.d;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, d = a.c.d;
   const SeenTokens t = seen_tokens(a, s);
   if (t.hi < 0) return;
   const float2* sums = part_sums(a, s, h, 0);
@@ -239,7 +242,7 @@ paged_join_kernel(const PagedDecodeLaunch a) {
   const bool on = lane * 4 < d;
   const float* values = part_values(a, s, h, 0) + (on ? lane * 4 : 0);
 #pragma unroll 8
-  for (int i = warp; i < t.parts; i += kWarps) {
+  for (int i = warp; i < t.parts; i += warps) {
     const float2 ml = sums[i];
     const float4 v = *reinterpret_cast<const float4*>(values + (int64_t)i * d);
     const float w = ex2(ml.x - base);
@@ -249,16 +252,14 @@ paged_join_kernel(const PagedDecodeLaunch a) {
   if (on) *reinterpret_cast<float4*>(&s_o[warp][lane * 4]) = make_float4(o[0], o[1], o[2], o[3]);
   if (lane == 0) s_l[warp] = total;
   __syncthreads();
-  const int c = threadIdx.x;
-  if (c >= d) return;
-  float sum = 0.f;
-  total = 0.f;
-#pragma unroll
-  for (int u = 0; u < kWarps; ++u) {
-    sum += s_o[u][c];
-    total += s_l[u];
+  for (int c = threadIdx.x; c < d; c += blockDim.x) {
+    float sum = 0.f, all = 0.f;
+    for (int u = 0; u < warps; ++u) {
+      sum += s_o[u][c];
+      all += s_l[u];
+    }
+    store1(static_cast<TOut*>(a.out) + s * a.o_sb + h * a.o_sh + c, t.hi > 0 ? sum / all : 0.f);
   }
-  store1(static_cast<TOut*>(a.out) + s * a.o_sb + h * a.o_sh + c, t.hi > 0 ? sum / total : 0.f);
 }
 
 template <typename TOut, int LPR, int HG>
@@ -279,20 +280,22 @@ cudaError_t by_width(const PagedDecodeLaunch& a, cudaStream_t stream) {
 
 }  // namespace
 
-// Blocks of one part each would leave SMs idle or end one long sequence after the others: as many parts as make 16 blocks an
-// SM, each of at least kPartTokens tokens.
-int paged_decode_splits(int64_t S, int64_t Hkv, int group, int64_t tokens, bool bf16, bool four) {
+// Blocks of one part each would leave SMs idle, or end one long sequence after the others.  Parts of at least kPartTokens
+// tokens, as many as make 16 blocks an SM, so that sequences of unequal lengths even out (256 sequences of 4 key heads, bf16,
+// 402 us; 8 blocks 405, 1 more); of few sequences 5, since every part is written and read again (2 sequences of up to 262144
+// tokens: 137 us with 5, 145 with 16).
+int paged_decode_splits(int64_t S, int64_t Hkv, int64_t tokens) {
   const int64_t blocks = S * Hkv, most = (tokens + kPartTokens - 1) / kPartTokens;
-  const int64_t want = (152 * 16 + blocks - 1) / blocks;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 128));
+  const int64_t want = (152 * (blocks < 152 ? 5 : 16) + blocks - 1) / blocks;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 256));
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream) {
   const cudaError_t e = a.c.bf16 ? launch_paged_decode_mma(a, stream) : a.out_bf16 ? by_width<__nv_bfloat16>(a, stream) : by_width<float>(a, stream);
   if (e != cudaSuccess || a.splits == 1) return e;
-  const dim3 grid((unsigned)(a.S * a.H));
-  return a.out_bf16 ? launch_dependent(paged_join_kernel<__nv_bfloat16>, grid, 32 * kWarps, 0, stream, a)
-                    : launch_dependent(paged_join_kernel<float>, grid, 32 * kWarps, 0, stream, a);
+  const dim3 grid((unsigned)(a.S * a.H)), block(a.splits <= 8 ? 32 : 32 * kJoinWarps);
+  return a.out_bf16 ? launch_dependent(paged_join_kernel<__nv_bfloat16>, grid, block, 0, stream, a)
+                    : launch_dependent(paged_join_kernel<float>, grid, block, 0, stream, a);
 }
 
 }  // namespace la
