@@ -998,26 +998,43 @@ def la_swa_biased_decode_step(q, k, v, k_cache, v_cache, pos, softcap: float = 0
 _NORMS = {None: 0, "rms": 1, "l2": 2}
 
 
-def _tokens(t):
-    """[B,H,N,d] tensor, or a step's [S,H,d] -> the words of a view."""
+def _view(index, name, t, shape, dtype):
+    """A [B,H,N,d] tensor, or a step's [S,H,d], checked as _check does -> the words of a view."""
+    st = t.stride()
+    if (index < 0 or t.get_device() != index or t.shape != shape or t.dtype is not dtype
+            or (st[-1] != 1 and shape[-1] > 1 and t.numel())):
+        _refuse(index, name, t, shape, dtype, False)
+    return (t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0,
+            st[2] if len(shape) == 4 and shape[2] > 1 else 0)
+
+
+def _whole(index, name, t, shape, dtype):
+    """A contiguous tensor or None, checked as _check does -> its address."""
     if t is None:
-        return 0, 0, 0, 0
-    if t.dim() == 4:
-        return _heads(t)
-    (S, H, _), (sb, sh, _) = t.shape, t.stride()
-    return t.data_ptr(), sb if S > 1 else 0, sh if H > 1 else 0, 0
+        return 0
+    if index < 0 or t.get_device() != index or t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(index, name, t, shape, dtype, True)
+    return t.data_ptr()
+
+
+def _made(shape, dtype, device):
+    """A new tensor and the words of its view."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    d, n = shape[-1], shape[2] if len(shape) == 4 else 1
+    return t, (t.data_ptr(), shape[1] * n * d, n * d, d)
 
 
 def _tables(index, cos, sin, d):
-    """Rotation tables: (rotated elements, rows)."""
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin come together")
-    if cos is None:
-        return 0, 0
-    if cos.dim() != 2 or 2 * cos.shape[1] > d:
+    """Rotation tables: (their addresses, rotated elements, rows)."""
+    if cos is None or sin is None:
+        if cos is not sin:
+            raise ValueError("cos and sin come together")
+        return 0, 0, 0, 0
+    shape = cos.shape
+    if len(shape) != 2 or 2 * shape[1] > d:
         raise ValueError(f"cos and sin must be [positions, rot / 2] with rot up to {d}")
-    _check(index, ("cos", cos, cos.shape, torch.float32, True), ("sin", sin, cos.shape, torch.float32, True))
-    return 2 * cos.shape[1], cos.shape[0]
+    return (_whole(index, "cos", cos, shape, torch.float32), _whole(index, "sin", sin, shape, torch.float32),
+            2 * shape[1], shape[0])
 
 
 @_on_stream
@@ -1033,51 +1050,60 @@ def la_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, norm: str | None = 
     q_weight, k_weight: [d] or None, both fp32 or both bf16; cos, sin: fp32 [positions, rot / 2] or None, rot a multiple
     of 16; pairs are (i, i + rot / 2), or neighbours if interleaved; pos: int64 [B], the first token's position (None: 0),
     or [B,N]; lens as in la_conv_prefill.  An output may be its input."""
-    step = q.dim() == 3
-    if q.dim() not in (3, 4) or (k is not None and k.dim() != q.dim()):
+    queries = tuple(q.shape)
+    dims = len(queries)
+    if dims not in (3, 4) or (k is not None and k.dim() != dims):
         raise ValueError("q and k must be [B,H,N,d], or [S,H,d] of single tokens")
     if norm not in _NORMS:
         raise ValueError(f"norm must be 'rms', 'l2' or None, got {norm!r}")
-    index, qt = q.get_device(), q.dtype
-    B, H, d = q.shape[0], q.shape[1], q.shape[-1]
-    N, Hkv = 1 if step else q.shape[2], 0 if k is None else k.shape[1]
-    keys = None if k is None else ((B, Hkv, d) if step else (B, Hkv, N, d))
-    rot, positions = _tables(index, cos, sin, d)
-    each = pos is not None and pos.dim() == 2
-    made = [q_out is None, k is not None and k_out is None]
-    if made[0]:
-        q_out = torch.empty(q.shape, dtype=out_dtype or qt, device=q.device)
-    if made[1]:
-        k_out = torch.empty(k.shape, dtype=q_out.dtype, device=q.device)
-    if k is None and k_out is not None:
-        raise ValueError("k_out without k")
-    if lens is not None and made[0] != made[1] and k is not None:
-        raise ValueError("with lens, q_out and k_out are both given or both made here")
+    index, qt, i64 = q.get_device(), q.dtype, torch.int64
+    B, H, d = queries[0], queries[1], queries[-1]
+    N = queries[2] if dims == 4 else 1
+    qv = _view(index, "q", q, queries, qt)
+    cosp, sinp, rot, positions = _tables(index, cos, sin, d)
+    fill = _FILL_ROWS if q_out is None else 0
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        Hkv, kv, kov = 0, (0, 0, 0, 0), (0, 0, 0, 0)
+    else:
+        if (q_out is None) != (k_out is None) and lens is not None:
+            raise ValueError("with lens, q_out and k_out are both given or both made here")
+        Hkv = k.shape[1]
+        keys = (B, Hkv, N, d) if dims == 4 else (B, Hkv, d)
+        kv = _view(index, "k", k, keys, qt)
+    if q_out is None:
+        q_out, qov = _made(queries, out_dtype or qt, q.device)
+    else:
+        qov = _view(index, "q_out", q_out, queries, q_out.dtype)
+    if k is not None:
+        if k_out is None:
+            k_out, kov = _made(keys, q_out.dtype, q.device)
+        else:
+            kov = _view(index, "k_out", k_out, keys, q_out.dtype)
     wt = q_weight.dtype if q_weight is not None else k_weight.dtype if k_weight is not None else torch.float32
-    _check(index, ("q", q, q.shape, qt, False), ("k", k, keys, qt, False), ("q_out", q_out, q.shape, q_out.dtype, False),
-           ("k_out", k_out, keys, q_out.dtype, False), ("q_weight", q_weight, (d,), wt, True),
-           ("k_weight", k_weight, (d,), wt, True), ("pos", pos, (B, N) if each else (B,), torch.int64, True),
-           ("lens", lens, (B,), torch.int64, True))
+    each = pos is not None and pos.dim() == 2
     _call("la_qk_norm_rope", index,
-          _QK_NORM_ROPE.pack(B, H, Hkv, N, d, rot, positions, _code(qt), _code(q_out.dtype), _code(wt), _NORMS[norm],
-                             *_tokens(q), *_tokens(k), *_tokens(q_out), *_tokens(k_out), _address(q_weight),
-                             _address(k_weight), _address(cos), _address(sin), _address(pos), _address(lens), eps,
-                             bool(interleaved), each, _FILL_ROWS if made[0] else 0))
+          _QK_NORM_ROPE.pack(B, H, Hkv, N, d, rot, positions, _code(qt), _code(q_out.dtype), _code(wt), _NORMS[norm], *qv, *kv,
+                             *qov, *kov, _whole(index, "q_weight", q_weight, (d,), wt), _whole(index, "k_weight", k_weight, (d,), wt),
+                             cosp, sinp, _whole(index, "pos", pos, (B, N) if each else (B,), i64),
+                             _whole(index, "lens", lens, (B,), i64), eps, bool(interleaved), each, fill))
     return q_out, k_out
 
 
 def _pool(index, k_pages, v_pages, table, B, dtype):
-    """A paged cache's sizes: (H_kv, d, page, pages, width, bits)."""
-    if k_pages.dim() != 4 or table.dim() != 2:
+    """A paged cache's sizes and addresses: (H_kv, d, page, pages, width, bits), (k_pages, v_pages, table)."""
+    shape, columns = tuple(k_pages.shape), tuple(table.shape)
+    if len(shape) != 4 or len(columns) != 2:
         raise ValueError("k_pages and v_pages must be [pages,H_kv,page,d] (4 bits: uint8 [pages,H_kv,page,9 d / 16]) and table [B,width]")
-    pages, Hkv, page, row = shape = tuple(k_pages.shape)
+    pages, Hkv, page, row = shape
     four = k_pages.dtype is torch.uint8
     if four and row not in (36, 72):
         raise ValueError(f"4-bit rows take 36 bytes (d = 64) or 72 (d = 128), got {row}")
     kind = torch.uint8 if four else dtype
-    _check(index, ("k_pages", k_pages, shape, kind, True), ("v_pages", v_pages, shape, kind, True),
-           ("table", table, (B, table.shape[1]), torch.int32, True))
-    return Hkv, row * 16 // 9 if four else row, page, pages, table.shape[1], 4 if four else 0
+    return ((Hkv, row * 16 // 9 if four else row, page, pages, columns[1], 4 if four else 0),
+            (_whole(index, "k_pages", k_pages, shape, kind), _whole(index, "v_pages", v_pages, shape, kind),
+             _whole(index, "table", table, (B, columns[1]), torch.int32)))
 
 
 @_on_stream
@@ -1090,19 +1116,20 @@ def la_paged_append(k, v, k_pages, v_pages, table, seen, cos=None, sin=None, int
     .. (i + 1) page - 1 of a sequence in column i; seen: int64 [B], tokens in the cache before (not advanced here): token n
     becomes token seen[b] + n; cos, sin, interleaved as in la_qk_norm_rope; lens: None or int64 [B], new tokens of each
     sequence of a padded batch."""
-    if k.dim() not in (3, 4) or v.dim() != k.dim():
+    rows = tuple(k.shape)
+    if len(rows) not in (3, 4) or v.dim() != len(rows):
         raise ValueError("k and v must be [B,H_kv,N,d], or [S,H_kv,d] of single tokens")
-    index, kt = k.get_device(), k.dtype
-    B, N = k.shape[0], 1 if k.dim() == 3 else k.shape[2]
-    Hkv, d, page, pages, width, bits = _pool(index, k_pages, v_pages, table, B, kt)
-    rows = (B, Hkv, d) if k.dim() == 3 else (B, Hkv, N, d)
-    rot, positions = _tables(index, cos, sin, d)
-    _check(index, ("k", k, rows, kt, False), ("v", v, rows, kt, False), ("seen", seen, (B,), torch.int64, True),
-           ("lens", lens, (B,), torch.int64, True))
+    index, kt, i64 = k.get_device(), k.dtype, torch.int64
+    B, N = rows[0], rows[2] if len(rows) == 4 else 1
+    (Hkv, d, page, pages, width, bits), pool = _pool(index, k_pages, v_pages, table, B, kt)
+    rows = (B, Hkv, N, d) if len(rows) == 4 else (B, Hkv, d)
+    cosp, sinp, rot, positions = _tables(index, cos, sin, d)
+    if seen is None:
+        raise ValueError("seen must be an int64 tensor")
     _call("la_paged_append", index,
-          _PAGED_APPEND.pack(B, Hkv, N, d, rot, positions, page, pages, width, _code(kt), bits, *_tokens(k), *_tokens(v),
-                             k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), seen.data_ptr(), _address(cos),
-                             _address(sin), _address(lens), bool(interleaved)))
+          _PAGED_APPEND.pack(B, Hkv, N, d, rot, positions, page, pages, width, _code(kt), bits, *_view(index, "k", k, rows, kt),
+                             *_view(index, "v", v, rows, kt), *pool, _whole(index, "seen", seen, (B,), i64), cosp, sinp,
+                             _whole(index, "lens", lens, (B,), i64), bool(interleaved)))
     return k_pages, v_pages
 
 
@@ -1113,33 +1140,35 @@ def la_paged_read(k_pages, v_pages, table, lens, N: int, k=None, v=None, out_dty
     (zeros in k, v made here).  4-bit caches give bf16 by default.  Returns (k, v)."""
     if (k is None) != (v is None):
         raise ValueError("k and v are both given or both made here")
-    index, four = k_pages.get_device(), k_pages.dtype is torch.uint8
+    index, four, N = k_pages.get_device(), k_pages.dtype is torch.uint8, int(N)
     kt, B = torch.bfloat16 if four else k_pages.dtype, table.shape[0]
-    Hkv, d, page, pages, width, bits = _pool(index, k_pages, v_pages, table, B, kt)
-    rows = (B, Hkv, int(N), d)
-    fill = _FILL_ROWS if k is None else 0
+    (Hkv, d, page, pages, width, bits), pool = _pool(index, k_pages, v_pages, table, B, kt)
+    rows, fill = (B, Hkv, N, d), 0
     if k is None:
-        k, v = (torch.empty(rows, dtype=out_dtype or kt, device=k_pages.device) for _ in range(2))
-    _check(index, ("k", k, rows, k.dtype, False), ("v", v, rows, k.dtype, False), ("lens", lens, (B,), torch.int64, True))
+        fill = _FILL_ROWS
+        (k, kv), (v, vv) = (_made(rows, out_dtype or kt, k_pages.device) for _ in range(2))
+    else:
+        kv, vv = _view(index, "k", k, rows, k.dtype), _view(index, "v", v, rows, k.dtype)
     _call("la_paged_read", index,
-          _PAGED_READ.pack(B, Hkv, int(N), d, page, pages, width, _code(kt), _code(k.dtype), bits, fill, *_heads(k), *_heads(v),
-                           k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), _address(lens)))
+          _PAGED_READ.pack(B, Hkv, N, d, page, pages, width, _code(kt), _code(k.dtype), bits, fill, *kv, *vv, *pool,
+                           _whole(index, "lens", lens, (B,), torch.int64)))
     return k, v
 
 
-def _paged_decode_args(q, k_pages, v_pages, table, lens, window, scale, softcap, slopes, out):
-    S, H, d = q.shape
-    Hkv, dk, page, pages, width, bits = _pool(q.get_device(), k_pages, v_pages, table, S, q.dtype)
+def _paged_decode_args(index, q, heads, k_pages, v_pages, table, lens, window, scale, softcap, slopes, out_type, out_view):
+    S, H, d = heads
+    (Hkv, dk, page, pages, width, bits), pool = _pool(index, k_pages, v_pages, table, S, q.dtype)
     if dk != d:
         raise ValueError(f"the pages hold rows of {dk} elements, q of {d}")
-    return _PAGED_DECODE.pack(S, H, Hkv, d, int(window), page, pages, width, _code(q.dtype), _code(out.dtype), bits,
-                              scale if scale is not None else d ** -0.5, softcap, *_tokens(q), *_tokens(out),
-                              k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), _address(lens), _address(slopes))
+    return _PAGED_DECODE.pack(S, H, Hkv, d, int(window), page, pages, width, _code(q.dtype), _code(out_type), bits,
+                              scale if scale is not None else d ** -0.5, softcap, *_view(index, "q", q, heads, q.dtype), *out_view, *pool,
+                              _whole(index, "lens", lens, (S,), torch.int64), _whole(index, "slopes", slopes, (H,), torch.float32))
 
 
 def la_paged_decode_workspace_size(q, k_pages, v_pages, table, window: int = 0) -> int:
     """Bytes of workspace la_paged_decode_step takes for tensors of these shapes (it does not depend on the lengths)."""
-    return _size("la_paged_decode_workspace_size", _paged_decode_args(q, k_pages, v_pages, table, None, window, None, 0.0, None, q))
+    return _size("la_paged_decode_workspace_size", _paged_decode_args(q.get_device(), q, tuple(q.shape), k_pages, v_pages, table, None,
+                                                                      window, None, 0.0, None, q.dtype, (0, 0, 0, 0)))
 
 
 @_on_stream
@@ -1151,15 +1180,17 @@ def la_paged_decode_step(q, k_pages, v_pages, table, lens, window: int = 0, scal
     int64 [S], tokens in the cache (0: zeros); the query stands at lens - 1 and sees the last `window` tokens (0: all);
     scale, softcap, slopes as in la_swa_prefill; workspace: uint8 device tensor of at least
     la_paged_decode_workspace_size bytes, allocated here by default."""
-    if q.dim() != 3:
+    heads = tuple(q.shape)
+    if len(heads) != 3:
         raise ValueError("q must be [S,H,d]")
-    index, qt = q.get_device(), q.dtype
-    S, H, d = heads = tuple(q.shape)
+    if lens is None:
+        raise ValueError("lens must be an int64 tensor")
+    index = q.get_device()
     if out is None:
-        out = torch.empty(heads, dtype=out_dtype or qt, device=q.device)
-    _check(index, ("q", q, heads, qt, False), ("lens", lens, (S,), torch.int64, True), ("slopes", slopes, (H,), torch.float32, True),
-           ("out", out, heads, out.dtype, False))
-    a = _paged_decode_args(q, k_pages, v_pages, table, lens, window, scale, softcap, slopes, out)
+        out, ov = _made(heads, out_dtype or q.dtype, q.device)
+    else:
+        ov = _view(index, "out", out, heads, out.dtype)
+    a = _paged_decode_args(index, q, heads, k_pages, v_pages, table, lens, window, scale, softcap, slopes, out.dtype, ov)
     ws, ws_bytes = _workspace(_size("la_paged_decode_workspace_size", a), workspace, q.device)
     if workspace is not None and workspace.get_device() != index:
         raise ValueError("workspace must live on the device of the inputs")
