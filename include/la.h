@@ -670,8 +670,9 @@ la_status la_paged_read(const la_paged_read_args* args, void* stream);
  *   max(0, n - window) <= j < n   (window 0: every token)
  *   q, out : [S, H, d] views of in_dtype and out_dtype (stride_t ignored); query head h reads key
  *            head h / (H / H_kv); H % H_kv == 0, H / H_kv <= 16
- *   lens   : [S] int64; 0 gives zeros; a length below 0 or beyond the table leaves the sequence's
- *            rows as they were and sets the device status word
+ *   lens   : [S] int64; a length below 0 or beyond the table leaves the sequence's rows as they
+ *            were and sets the device status word.  Where no token has a weight (a length of 0,
+ *            pages that are not there, scores of -infinity alone) the result is zero.
  *   slopes, softcap, scale : as in la_swa_prefill
  * bf16 (bits 0 and 4): products on the tensor cores with fp32 sums and statistics, the softmax
  * weights in two bf16 parts (2^-17 of a weight).  fp32: fp32 throughout.  Few or long sequences are

@@ -213,7 +213,7 @@ paged_decode_f32_kernel(const PagedDecodeLaunch a, const int passes) {
       part_values(a, s, h0 + g, part)[c] = sum;
       if (c == 0) *part_sums(a, s, h0 + g, part) = make_float2(top, total);
     } else {
-      store1(static_cast<TOut*>(a.out) + s * a.o_sb + (h0 + g) * a.o_sh + c, t.hi > 0 ? sum / total : 0.f);
+      store1(static_cast<TOut*>(a.out) + s * a.o_sb + (h0 + g) * a.o_sh + c, mean_of(sum, total));
     }
   }
 }
@@ -258,7 +258,7 @@ paged_join_kernel(const PagedDecodeLaunch a) {
       sum += s_o[u][c];
       all += s_l[u];
     }
-    store1(static_cast<TOut*>(a.out) + s * a.o_sb + h * a.o_sh + c, t.hi > 0 ? sum / all : 0.f);
+    store1(static_cast<TOut*>(a.out) + s * a.o_sb + h * a.o_sh + c, mean_of(sum, all));
   }
 }
 

@@ -27,6 +27,9 @@ __device__ __forceinline__ SeenTokens seen_tokens(const PagedDecodeLaunch& a, in
   return t;
 }
 
+// The weighted mean; zero where no token has a weight: an empty sequence, pages that are not there, scores of -infinity alone.
+__device__ __forceinline__ float mean_of(float sum, float total) { return total == 0.f ? 0.f : sum / total; }
+
 // Places of a part's sums, greatest score and sum of weights in the workspace.
 __device__ __forceinline__ float* part_values(const PagedDecodeLaunch& a, int64_t s, int64_t h, int part) {
   return a.parts + ((s * a.H + h) * a.splits + part) * a.c.d;

@@ -152,7 +152,7 @@ __device__ __forceinline__ void finish(const PagedDecodeLaunch& a, const Part& p
       if (c == 0) *part_sums(a, p.s, h, p.part) = make_float2(top, total);
       continue;
     }
-    if (p.seen.hi > 0) sum = make_float2(sum.x / total, sum.y / total);
+    sum = make_float2(mean_of(sum.x, total), mean_of(sum.y, total));
     const int64_t at = p.s * a.o_sb + h * a.o_sh + c;
     if (a.out_bf16) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at) = tc::pack2_bf16(sum.x, sum.y);
     else *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = sum;

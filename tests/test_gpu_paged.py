@@ -428,6 +428,25 @@ def test_steps_report_bad_lengths_and_pages(dtype, bits):
 
 
 @pytest.mark.parametrize("dtype,bits", [(FP, 0), (BF, 0), (BF, 4)])
+@pytest.mark.parametrize("width", [2, 100])
+def test_no_weight_gives_zeros(dtype, bits, width):
+    """Sequences none of whose pages is there, empty ones, and scores of -infinity alone."""
+    dev = cuda_device()
+    g = gen(17)
+    pools, table = cache(g, [32, 32, 32], 16, 1, 64, dtype, bits)
+    wide = torch.full((3, width), -1, dtype=torch.int32)
+    wide[:, :2] = table[:, :2]
+    wide[0, :2] = -1
+    q = torch.ones((3, 4, 64), dtype=dtype)
+    if not bits:
+        pools[0][table[2, :2].long()] = -float("inf")
+    qd, kd, vd, td = on(dev, q, *pools, wide)
+    got = la.la_paged_decode_step(qd, kd, vd, td, longs(dev, [32, 0, 32]), out_dtype=FP)
+    assert la.la_device_status() == la.LA_ERR_INVALID_ARGUMENT
+    assert torch.all(got[:2] == 0) and (bits or torch.all(got[2] == 0))
+
+
+@pytest.mark.parametrize("dtype,bits", [(FP, 0), (BF, 0), (BF, 4)])
 def test_scores_far_apart(dtype, bits):
     """One key that takes all the weight, first or last, and scores beyond what exp holds."""
     dev = cuda_device()
@@ -600,6 +619,29 @@ def test_calls_on_a_given_stream():
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(out, want) and torch.equal(alone, qn)
         assert torch.equal(kr[0, :, 700], kn[0]) and torch.equal(vr[2, :, 1000], v[2])
+
+
+def test_calls_at_once_on_two_streams():
+    """Calls share nothing but the status word: each with its own workspace, on streams of their own."""
+    dev = cuda_device()
+    g = gen(43)
+    H, Hkv, d, page, lens = 8, 2, 128, 32, [3000, 2500]
+    jobs = []
+    for bits in (0, 4, 0, 4):
+        pools, table = cache(g, lens, page, Hkv, d, BF, bits)
+        q = randn(g, 2, H, d, dtype=BF)
+        jobs.append(on(dev, q, *pools, table))
+    n = longs(dev, lens)
+    want = [la.la_paged_decode_step(*j, n) for j in jobs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for i, j in enumerate(jobs):
+            got.append((i, la.la_paged_decode_step(*j, n, stream=streams[i % 2])))
+    torch.cuda.synchronize()
+    for i, o in got:
+        assert torch.equal(o, want[i])
 
 
 @pytest.mark.parametrize("dtype,bits,page", [(BF, 0, 64), (BF, 4, 4096), (FP, 0, 16)])
