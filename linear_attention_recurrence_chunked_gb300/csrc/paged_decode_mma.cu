@@ -12,8 +12,10 @@
 // 4 bits: a code is put into the mantissa of a bf16 one, 1 + code / 16, exactly, and the products run on those:
 //   k = offset + scale code = (offset - 16 scale) + 16 scale (1 + code / 16)
 //   q.k = sum over groups of 16 scale (q.(1 + code / 16)) + (offset - 16 scale) sum q
-//   sum_j p_j v_j = sum_j (16 scale_j p_j) (1 + code_j / 16) + sum_j p_j (offset_j - 16 scale_j)
-// so that scales and offsets meet whole sums in fp32, and weights once per group.
+//   sum_j p_j v_j = sum_j (16 scale_j p_j) (code_j - 8) / 16 + sum_j p_j (offset_j + 8 scale_j)
+// so that scales and offsets meet whole sums in fp32, and weights once per group.  Values have the ones taken off (one packed
+// subtraction): their sums run over thousands of tokens and come out near zero, while sums of ones would not (off by 6e-4 of
+// an output's norm over 131071 tokens, where tensor cores cut sums off).
 #include <algorithm>
 
 #include "paged_decode.cuh"
@@ -433,6 +435,14 @@ __device__ __forceinline__ uint32_t ones(uint32_t w, uint32_t one) {
   return r;
 }
 
+// The same less 3/2, exact: (code - 8) / 16.
+template <int m>
+__device__ __forceinline__ uint32_t centred(uint32_t w, uint32_t one) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(ones<m>(w, one)), "r"(0x3fc03fc0u));
+  return r;
+}
+
 // Place of a row's 16-byte chunk: the rows that a product's lanes read together lie in different banks.
 template <int D>
 __device__ __forceinline__ uint32_t place4(int r, int ch) {
@@ -579,7 +589,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
     const uint8_t* tile = region + stage * kTileBytes4<D>;
     const uint32_t* meta = reinterpret_cast<const uint32_t*>(tile + 2 * kCodes<D>);
     const uint32_t seen = spots[i % (2 * kBatch) * 2].seen | spots[i % (2 * kBatch) * 2 + 1].seen << 16;
-    // ---- a token a lane: 16 scale and offset - 16 scale, the keys' times what scores are multiplied by
+    // ---- a token a lane: 16 scale and offset - 16 scale of keys, times what scores are multiplied by, and offset + 8 scale of values
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       uint32_t w[kGroups];
@@ -593,7 +603,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         f[2 * g] = 16.f * __uint_as_float(w[g] << 16);
-        f[2 * g + 1] = __uint_as_float(w[g] & 0xffff0000u) - f[2 * g];
+        f[2 * g + 1] = fmaf(v == 0 ? -1.f : 0.5f, f[2 * g], __uint_as_float(w[g] & 0xffff0000u));
         if (v == 0) {
           f[2 * g] *= scale;
           f[2 * g + 1] *= scale;
@@ -723,10 +733,10 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
             mma16816(o[u][4 * g + m], a0, a1, a2, a3, minor[u][0], minor[u][1]);
           }
         };
-        product(0, ones<0>(lo0, one), ones<0>(hi0, one), ones<0>(lo1, one), ones<0>(hi1, one));
-        product(1, ones<1>(lo0, one), ones<1>(hi0, one), ones<1>(lo1, one), ones<1>(hi1, one));
-        product(2, ones<2>(lo0, one), ones<2>(hi0, one), ones<2>(lo1, one), ones<2>(hi1, one));
-        product(3, ones<3>(lo0, one), ones<3>(hi0, one), ones<3>(lo1, one), ones<3>(hi1, one));
+        product(0, centred<0>(lo0, one), centred<0>(hi0, one), centred<0>(lo1, one), centred<0>(hi1, one));
+        product(1, centred<1>(lo0, one), centred<1>(hi0, one), centred<1>(lo1, one), centred<1>(hi1, one));
+        product(2, centred<2>(lo0, one), centred<2>(hi0, one), centred<2>(lo1, one), centred<2>(hi1, one));
+        product(3, centred<3>(lo0, one), centred<3>(hi0, one), centred<3>(lo1, one), centred<3>(hi1, one));
       }
     }
     __syncwarp();  // the factors are used up

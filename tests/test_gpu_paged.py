@@ -403,6 +403,29 @@ def test_split_sequences(dtype, bits, H, Hkv, d, window, softcap):
         la.la_paged_decode_step(qd, kd, vd, td, longs(dev, lens), window=window, workspace=ws[:size - 16])
 
 
+@pytest.mark.parametrize("bits,d,H", [(0, 128, 4), (4, 64, 4), (4, 128, 16)])
+def test_means_of_many_values_keep_their_bits(bits, d, H):
+    """A flat softmax over 40000 tokens gives means of 1 / sqrt(n) of a value's size, which sums that drift would drown.  Each
+    weight is off by up to 2^-17 of itself, independently, and adds 2^-17 / sqrt(n) of a value, 2^-17 of the mean's size; fp32
+    sums of n / 1000 terms a warp and their join stay below that.  Four times as much is allowed."""
+    dev = cuda_device()
+    g = torch.Generator(device=dev).manual_seed(d + H)
+    n, page = 40000, 64
+    P = n // page
+    x = [torch.randn((P, 1, page, d), generator=g, device=dev).to(BF) for _ in range(2)]
+    table = torch.randperm(P, generator=g, device=dev).to(torch.int32)[None]
+    q = (0.05 * torch.randn((1, H, d), generator=g, device=dev)).to(BF)
+    pools = [torch.zeros((P, 1, page, d * 9 // 16), dtype=torch.uint8, device=dev) for _ in range(2)] if bits else x
+    rows = [t[table[0].long()].permute(1, 0, 2, 3).reshape(1, 1, n, d) for t in x]
+    if bits:
+        la.la_paged_append(*rows, *pools, table, longs(dev, [0]))
+        rows = la.la_paged_read(*pools, table, None, n, out_dtype=FP)
+    out = la.la_paged_decode_step(q, *pools, table, longs(dev, [n]), out_dtype=FP).double()
+    k, v = (t[0, 0].double() for t in rows)
+    want = torch.softmax(q[0].double() @ k.T * d ** -0.5, -1) @ v
+    assert (out[0] - want).norm() <= 2.0 ** -15 * want.norm()
+
+
 @pytest.mark.parametrize("dtype,bits", [(FP, 0), (BF, 0), (BF, 4)])
 def test_steps_report_bad_lengths_and_pages(dtype, bits):
     dev = cuda_device()
