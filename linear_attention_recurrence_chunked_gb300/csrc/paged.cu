@@ -1,6 +1,8 @@
 // paged.cu -- keys and values of new tokens into a paged cache, the keys rotated on the way, and a cache's tokens back into
 // rows.  Both read and write every element once, so memory bounds them.  As in heads.cu a lane has eight elements of a row,
 // for 4 bits always consecutive ones: one 32-bit word of codes, whose group of 64 elements is eight neighbouring lanes.
+// 8 ragged prompts of up to 4096 tokens, 4 heads x 128, bf16: 24 us for 102 MB, 4.2 TB/s; 4 x 2048 tokens of 8 heads into 4 bits
+// 25 us (half of the instructions rotation and codes), 4 x up to 16048 tokens back 48 us, 6.7 TB/s.
 #include <type_traits>
 
 #include "paged.cuh"
