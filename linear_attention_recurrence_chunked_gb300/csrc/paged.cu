@@ -1,8 +1,9 @@
 // paged.cu -- keys and values of new tokens into a paged cache, the keys rotated on the way, and a cache's tokens back into
 // rows.  Both read and write every element once, so memory bounds them.  As in heads.cu a lane has eight elements of a row,
 // for 4 bits always consecutive ones: one 32-bit word of codes, whose group of 64 elements is eight neighbouring lanes.
-// 8 ragged prompts of up to 4096 tokens, 4 heads x 128, bf16: 24 us for 102 MB, 4.2 TB/s; 4 x 2048 tokens of 8 heads into 4 bits
-// 25 us (half of the instructions rotation and codes), 4 x up to 16048 tokens back 48 us, 6.7 TB/s.
+// 8 ragged prompts of up to 4096 tokens, 4 heads x 128, bf16: 19.6 us for 102 MB, 5.2 TB/s (24 with a warp for the keys and one for
+// the values, 22 with four rows of each at once); 4 x 2048 tokens of 8 heads into 4 bits 24 us (half of the instructions
+// rotation and codes), 4 x up to 16048 tokens back 48 us, 6.7 TB/s.
 #include <type_traits>
 
 #include "paged.cuh"
@@ -12,7 +13,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 4;  // rows of a lane on their way at once
+constexpr int kRows = 2;   // rows of a lane on their way at once, of the keys and of the values, in an append
+constexpr int kReads = 4;  // and in a read
 
 int lanes_of(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : 16; }
 
@@ -150,98 +152,110 @@ __device__ __forceinline__ void quantise(const Raw8<__nv_bfloat16>& raw, uint32_
   codes -= 0x4b400000u * 0x11111111u;  // the sums' bits are 0x4b400000 + code
 }
 
-// A token of a call: where it stands and goes.
-struct Token {
-  uint32_t b, n;
-  bool report;  // of the warps with parts of it, this one tells of errors
+// Where a token goes.
+struct Place {
+  int page, slot;
 };
 
-// One token's keys or values of `heads` heads from h0 on.  Their rows are on their way before the token's place is known.
+// A token's keys or values of some heads, kRows rows of each lane at a time: on their way from `load` on, stored by `store`.
 template <typename T, bool kFour, int LPR, TurnKind kTurn>
-__device__ __forceinline__ void append_heads(const PagedAppendLaunch& a, const Token& token, const Span4& view, void* pool, int h0, int heads,
-                                             const Divisor& pages) {
-  constexpr int R = 32 / LPR;
-  constexpr bool kWhole = kFour || kTurn != kTurnHalves;
-  const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR, d = kFour ? 8 * LPR : a.c.d;
-  const bool on = col * 8 < d;
-  const int2 at = runs_of<kFour ? kTurnNone : kTurn>(on ? col : 0, a.rot);
-  const T* x = view.at<const T>(token.b, h0 + sub, token.n);
-  const int64_t xr = R * view.step<T>();
-  int left = on ? heads - sub : 0;  // this lane's rows: every R-th while it is positive
+struct HeadRows {
+  static constexpr int R = 32 / LPR;
+  static constexpr bool kWhole = kFour || kTurn != kTurnHalves;
+  const T* x;
+  int64_t step;
+  int2 at;
+  int left;  // this lane's rows: every R-th while it is positive
   Raw8<T> raw[kRows];
-  auto load = [&] {
+
+  __device__ __forceinline__ HeadRows(const PagedAppendLaunch& a, const Span4& view, uint32_t b, uint32_t n, int h0, int heads) {
+    const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR;
+    const bool on = col * 8 < (kFour ? 8 * LPR : a.c.d);
+    at = runs_of<kFour ? kTurnNone : kTurn>(on ? col : 0, a.rot);
+    x = view.at<const T>(b, h0 + sub, n);
+    step = R * view.step<T>();
+    left = on ? heads - sub : 0;
+    load();
+  }
+  __device__ __forceinline__ void load() {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       raw[i].zero();
       if (left > i * R) raw[i].template load<kWhole>(x, at);
-      x += xr;
+      x += step;
     }
-  };
-  load();
-  if (token.n >= sequence_length(a.lens, token.b, a.N, a.c.status, token.report && token.n == 0)) return;
-  const int64_t position = table_row(a.seen[token.b], token.n, a.c.width * a.c.page);  // below 2^31
-  const int column = (int)pages((uint32_t)position);
-  const int page = position < 0 || (a.rot > 0 && position >= a.positions) ? -1 : table_page(a.c, token.b, column);
-  if (page < 0) {
-    if (token.report) atomicOr(a.c.status, kStatusBadIndex);
-    return;
   }
-  const int size = page_bytes(a.c);
-  const int slot = (int)position - column * a.c.page;
-  const float *cos = a.cos + (uint64_t)(uint32_t)position * (uint32_t)(a.rot / 2), *sin = a.sin + (uint64_t)(uint32_t)position * (uint32_t)(a.rot / 2);
-  std::conditional_t<kFour, TurnWide<kTurn>, Turn<kTurn>> turn;
-  turn.on = false;
-  if constexpr (kTurn != kTurnNone) {
-    if constexpr (kFour) turn.init(cos, sin, a.rot, lane, col);
-    else if (on) turn.init(cos, sin, a.rot, col);
-  }
-  uint8_t* y = static_cast<uint8_t*>(pool) + ((uint64_t)(uint32_t)page * (uint32_t)a.c.Hkv + (uint32_t)(h0 + sub)) * (uint32_t)size;
+  template <typename Angles>
+  __device__ __forceinline__ void store(const PagedAppendLaunch& a, void* pool, const Place& place, int h0, int heads, const Angles& turn) {
+    const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR, d = kFour ? 8 * LPR : a.c.d, size = page_bytes(a.c);
+    uint8_t* y = static_cast<uint8_t*>(pool) + ((uint64_t)(uint32_t)place.page * (uint32_t)a.c.Hkv + (uint32_t)(h0 + sub)) * (uint32_t)size;
 #pragma unroll 1
-  for (int more = heads;;) {
+    for (int more = heads;;) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (more <= i * R) break;  // the same for the whole warp
-      if constexpr (kFour) {
-        if constexpr (kTurn != kTurnNone) turn.apply(raw[i]);
-        uint32_t codes, meta;
-        quantise(raw[i], codes, meta);
-        constexpr int kGroups = LPR / 8;
-        if (left > i * R) {
-          reinterpret_cast<uint32_t*>(y + slot * (d / 2))[code_word(col / 8, col % 8, kGroups)] = codes;
-          if (col % 8 == 0) reinterpret_cast<uint32_t*>(y + a.c.page * (d / 2))[slot * kGroups + col / 8] = meta;
+      for (int i = 0; i < kRows; ++i) {
+        if (more <= i * R) break;  // the same for the whole warp
+        if constexpr (kFour) {
+          if constexpr (kTurn != kTurnNone) turn.apply(raw[i]);
+          uint32_t codes, meta;
+          quantise(raw[i], codes, meta);
+          constexpr int kGroups = LPR / 8;
+          if (left > i * R) {
+            reinterpret_cast<uint32_t*>(y + place.slot * (d / 2))[code_word(col / 8, col % 8, kGroups)] = codes;
+            if (col % 8 == 0) reinterpret_cast<uint32_t*>(y + a.c.page * (d / 2))[place.slot * kGroups + col / 8] = meta;
+          }
+        } else if (left > i * R) {
+          if (kTurn != kTurnNone && turn.on) {  // other rows and elements go as they are, whatever they hold
+            f32x2 v[4];
+            raw[i].unpack(v);
+            turn.apply(v, turn_rounded);
+            raw[i].pack(v);
+          }
+          raw[i].template store<kWhole>(reinterpret_cast<T*>(y) + place.slot * d, at);
         }
-      } else if (left > i * R) {
-        if (kTurn != kTurnNone && turn.on) {  // other rows and elements go as they are, whatever they hold
-          f32x2 v[4];
-          raw[i].unpack(v);
-          turn.apply(v, turn_rounded);
-          raw[i].pack(v);
-        }
-        raw[i].template store<kWhole>(reinterpret_cast<T*>(y) + slot * d, at);
+        y += (int64_t)R * size;
       }
-      y += (int64_t)R * size;
+      more -= kRows * R;
+      if (more <= 0) return;
+      left -= kRows * R;
+      load();
     }
-    more -= kRows * R;
-    if (more <= 0) return;
-    left -= kRows * R;
-    load();
   }
-}
+};
 
-// A warp stores a token's keys or its values, `per` heads of them.
+// A warp stores a token's keys and values, `per` heads of them: one look at where it goes, while its first rows are on their way.
 template <typename T, bool kFour, int LPR, TurnKind kTurn>
-__global__ void __launch_bounds__(kThreads, kFour || sizeof(T) == 4 ? 3 : 4)
-paged_append_kernel(const PagedAppendLaunch a, const int per, const Divisor parts2, const Divisor tokens, const Divisor pages) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4)
+paged_append_kernel(const PagedAppendLaunch a, const int per, const Divisor parts, const Divisor tokens, const Divisor pages) {
+  using Angles = std::conditional_t<kFour, TurnWide<kTurn>, Turn<kTurn>>;
   grid_dependents_trigger();
   grid_dependency_wait();
-  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), at = parts2(unit), b = tokens(at), n = at - b * tokens.d;
+  const int lane = threadIdx.x & 31, col = lane % LPR;
+  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), token = parts(unit), b = tokens(token), n = token - b * tokens.d;
   if (b >= a.B) return;  // whole warps
-  const int part = (int)(unit - at * parts2.d), parts = (int)(parts2.d / 2);
-  const Token token{b, n, part == 0 && (threadIdx.x & 31) == 0};
-  const bool values = part >= parts;
-  const int h0 = (values ? part - parts : part) * per, heads = min(per, (int)a.c.Hkv - h0);
-  if (values) append_heads<T, kFour, LPR, kTurnNone>(a, token, a.v, a.c.v, h0, heads, pages);
-  else append_heads<T, kFour, LPR, kTurn>(a, token, a.k, a.c.k, h0, heads, pages);
+  const int part = (int)(unit - token * parts.d), h0 = part * per, heads = min(per, (int)a.c.Hkv - h0);
+  const bool report = part == 0 && lane == 0;
+  HeadRows<T, kFour, LPR, kTurn> keys(a, a.k, b, n, h0, heads);
+  HeadRows<T, kFour, LPR, kTurnNone> values(a, a.v, b, n, h0, heads);
+
+  if (n >= sequence_length(a.lens, b, a.N, a.c.status, report && n == 0)) return;
+  const int64_t position = table_row(a.seen[b], n, a.c.width * a.c.page);  // below 2^31
+  const int column = (int)pages((uint32_t)position);
+  Place place;
+  place.page = position < 0 || (kTurn != kTurnNone && position >= a.positions) ? -1 : table_page(a.c, b, column);
+  place.slot = (int)position - column * a.c.page;
+  if (place.page < 0) {
+    if (report) atomicOr(a.c.status, kStatusBadIndex);
+    return;
+  }
+  Angles turn;
+  turn.on = false;
+  if constexpr (kTurn != kTurnNone) {
+    const uint64_t row = (uint64_t)(uint32_t)position * (uint32_t)(a.rot / 2);
+    if constexpr (kFour) turn.init(a.cos + row, a.sin + row, a.rot, lane, col);
+    else if (col * 8 < a.c.d) turn.init(a.cos + row, a.sin + row, a.rot, col);
+  }
+  keys.store(a, a.c.k, place, h0, heads, turn);
+  values.store(a, a.c.v, place, h0, heads, turn);
 }
 
 // A warp reads 16 tokens of one head, keys or values.
@@ -286,10 +300,10 @@ paged_read_kernel(const PagedReadLaunch a, const Divisor tiles, const Divisor he
   asm volatile("" : "+r"(magic));
 
   auto batch = [&](auto all, int i0) {  // all: every row is there
-    [[maybe_unused]] Raw8<T> raw[kRows];
-    [[maybe_unused]] uint32_t codes[kRows], meta[kRows];
+    [[maybe_unused]] Raw8<T> raw[kReads];
+    [[maybe_unused]] uint32_t codes[kReads], meta[kReads];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < kReads; ++i) {
       if (!decltype(all)::value && there <= (i0 + i) * R) continue;
       if constexpr (kFour) {
         codes[i] = words[i * R * kWords];
@@ -298,11 +312,11 @@ paged_read_kernel(const PagedReadLaunch a, const Divisor tiles, const Divisor he
         raw[i].template load<true>(rows + i * R * d, at);
       }
     }
-    words += kRows * R * kWords;
-    metas += kRows * R * kGroups;
-    rows += kRows * R * d;
+    words += kReads * R * kWords;
+    metas += kReads * R * kGroups;
+    rows += kReads * R * d;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i, y += yr) {
+    for (int i = 0; i < kReads; ++i, y += yr) {
       if (!decltype(all)::value && wanted <= (i0 + i) * R) continue;
       f32x2 v[4];
       Raw8<TOut> packed;
@@ -332,10 +346,10 @@ paged_read_kernel(const PagedReadLaunch a, const Divisor tiles, const Divisor he
   };
   if (have == n0 + 16) {
 #pragma unroll
-    for (int i0 = 0; i0 < 16 / R; i0 += kRows) batch(std::true_type{}, i0);
+    for (int i0 = 0; i0 < 16 / R; i0 += kReads) batch(std::true_type{}, i0);
   } else {
 #pragma unroll 1
-    for (int i0 = 0; i0 < 16 / R; i0 += kRows) batch(std::false_type{}, i0);
+    for (int i0 = 0; i0 < 16 / R; i0 += kReads) batch(std::false_type{}, i0);
   }
 }
 
@@ -344,13 +358,13 @@ cudaError_t append_turn(const PagedAppendLaunch& a, cudaStream_t stream) {
   constexpr int R = 32 / LPR;
   int per = R;
   int64_t parts = 0;
-  for (int m = 2 * kRows; m >= 1; m /= 2) {  // as many heads a warp as leave 32 warps to each of 152 SMs
+  for (int m = 8; m >= 1; m /= 2) {  // as many heads a warp as leave 32 warps to each of 152 SMs
     per = R * m;
     parts = (a.c.Hkv + per - 1) / per;
-    if (2 * a.B * a.N * parts >= 152 * 32) break;
+    if (a.B * a.N * parts >= 152 * 32) break;
   }
-  const int64_t blocks = (2 * a.B * a.N * parts + kWarps - 1) / kWarps;
-  return launch_dependent(paged_append_kernel<T, kFour, LPR, kTurn>, dim3((unsigned)blocks), kThreads, 0, stream, a, per, Divisor(2 * parts), Divisor(a.N), Divisor(a.c.page));
+  const int64_t blocks = (a.B * a.N * parts + kWarps - 1) / kWarps;
+  return launch_dependent(paged_append_kernel<T, kFour, LPR, kTurn>, dim3((unsigned)blocks), kThreads, 0, stream, a, per, Divisor(parts), Divisor(a.N), Divisor(a.c.page));
 }
 template <typename T, bool kFour, int LPR>
 cudaError_t append(const PagedAppendLaunch& a, cudaStream_t stream) {
