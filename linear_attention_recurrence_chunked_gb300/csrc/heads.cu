@@ -4,17 +4,17 @@
 // Every element is read and written once, so memory bounds it.  A warp takes a token's heads, a part of them where there are
 // few tokens: eight elements a lane and d / 8 lanes a row, so that the angles of a lane's elements stay in registers from
 // head to head.  Sums of squares meet by shuffles, those of four rows at a time.  4 x 16384 tokens of 32 heads x 128 to unit
-// length in bf16 take 161 us, 98 % of the measured copy rate; 3 x 8191 tokens of 36 heads with weights and rotation 80 us, 85 %.
+// length in bf16 take 159 us, the measured copy rate; 3 x 8191 tokens of 36 heads with weights and rotation 78 us, 87 % of it.
 #include "la.h"
 #include "rows.cuh"
 
 namespace la {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-// Rows of a lane on their way at once, and three blocks an SM beside them: with rotation 80 us; 2 rows and four blocks 97, 6 rows
-// and two blocks 92.
+// Rows of a lane on their way at once, with 24 warps an SM beside them: with rotation 80 us; 2 rows and 32 warps 97, 6 rows and 16
+// warps 92.  (Blocks of eight warps, as those were; of four 78.)
 constexpr int kRows = 4;
 
 struct Plan {
@@ -42,7 +42,7 @@ Plan plan_of(int64_t B, int64_t H, int64_t Hkv, int64_t N, int d) {
 }
 
 template <typename TIn, typename TOut, int LPR, TurnKind kTurn, bool kNorm>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 6)
 qk_norm_rope_kernel(const QkNormRopeLaunch a, const Plan p) {
   constexpr int R = 32 / LPR;
   constexpr bool kWhole = kTurn != kTurnHalves;

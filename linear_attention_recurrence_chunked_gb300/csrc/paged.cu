@@ -1,7 +1,7 @@
 // paged.cu -- keys and values of new tokens into a paged cache, the keys rotated on the way, and a cache's tokens back into
 // rows.  Both read and write every element once, so memory bounds them.  As in heads.cu a lane has eight elements of a row,
 // for 4 bits always consecutive ones: one 32-bit word of codes, whose group of 64 elements is eight neighbouring lanes.
-// 8 ragged prompts of up to 4096 tokens, 4 heads x 128, bf16: 19.6 us for 102 MB, 5.2 TB/s (24 with a warp for the keys and one for
+// 8 ragged prompts of up to 4096 tokens, 4 heads x 128, bf16: 19 us for 102 MB, 5.3 TB/s (24 with a warp for the keys and one for
 // the values, 22 with four rows of each at once); 4 x 2048 tokens of 8 heads into 4 bits 24 us (half of the instructions
 // rotation and codes), 4 x up to 16048 tokens back 48 us, 6.7 TB/s.
 #include <type_traits>
@@ -11,7 +11,7 @@
 namespace la {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 2;   // rows of a lane on their way at once, of the keys and of the values, in an append
 constexpr int kReads = 4;  // and in a read
@@ -224,7 +224,7 @@ struct HeadRows {
 
 // A warp stores a token's keys and values, `per` heads of them: one look at where it goes, while its first rows are on their way.
 template <typename T, bool kFour, int LPR, TurnKind kTurn>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 8)
 paged_append_kernel(const PagedAppendLaunch a, const int per, const Divisor parts, const Divisor tokens, const Divisor pages) {
   using Angles = std::conditional_t<kFour, TurnWide<kTurn>, Turn<kTurn>>;
   grid_dependents_trigger();
