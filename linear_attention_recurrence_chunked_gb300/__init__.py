@@ -1049,7 +1049,7 @@ def la_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, norm: str | None = 
     q: [B,H,N,d], k: [B,H_kv,N,d] or None, or a step's [S,H,d], [S,H_kv,d] (fp32 or bf16, d a multiple of 8 up to 256);
     q_weight, k_weight: [d] or None, both fp32 or both bf16; cos, sin: fp32 [positions, rot / 2] or None, rot a multiple
     of 16; pairs are (i, i + rot / 2), or neighbours if interleaved; pos: int64 [B], the first token's position (None: 0),
-    or [B,N]; lens as in la_conv_prefill.  An output may be its input."""
+    or [B,N]; lens as in la_conv_prefill.  An output may be its input; both are given or both made here."""
     queries = tuple(q.shape)
     dims = len(queries)
     if dims not in (3, 4) or (k is not None and k.dim() != dims):
@@ -1067,8 +1067,8 @@ def la_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, norm: str | None = 
             raise ValueError("k_out without k")
         Hkv, kv, kov = 0, (0, 0, 0, 0), (0, 0, 0, 0)
     else:
-        if (q_out is None) != (k_out is None) and lens is not None:
-            raise ValueError("with lens, q_out and k_out are both given or both made here")
+        if (q_out is None) != (k_out is None):  # what is made here has zeros for skipped tokens, what is given stays
+            raise ValueError("q_out and k_out are both given or both made here")
         Hkv = k.shape[1]
         keys = (B, Hkv, N, d) if dims == 4 else (B, Hkv, d)
         kv = _view(index, "k", k, keys, qt)

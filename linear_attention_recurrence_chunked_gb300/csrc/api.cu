@@ -717,8 +717,10 @@ la::Span4 span(const la_tensor& x, int64_t B, int64_t H, int64_t N, la_dtype dt)
   return la::Span4{x.ptr, (uint32_t)(B > 1 ? x.stride_b * e / 16 : 0), (uint32_t)(H > 1 ? x.stride_h * e / 16 : 0), (uint32_t)(N > 1 ? x.stride_t * e / 16 : 0)};
 }
 
-bool same_rows(const la_tensor& x, const la_tensor& y) {
-  return x.stride_b == y.stride_b && x.stride_h == y.stride_h && x.stride_t == y.stride_t;
+// Whether an output at its input's address may be it: rows in the same places, or other places altogether
+bool in_place(const la_tensor& x, const la_tensor& y, int64_t B, int64_t H, int64_t N, la_dtype in, la_dtype out) {
+  if (H == 0 || x.ptr != y.ptr) return true;
+  return in == out && (B <= 1 || x.stride_b == y.stride_b) && (H <= 1 || x.stride_h == y.stride_h) && (N <= 1 || x.stride_t == y.stride_t);
 }
 
 }  // namespace
@@ -741,8 +743,8 @@ la_status la_qk_norm_rope(const la_qk_norm_rope_args* a, void* stream) {
       !valid_view(a->k, a->B, a->H_kv, a->N, a->d, a->in_dtype) || !valid_view(a->k_out, a->B, a->H_kv, a->N, a->d, a->out_dtype) ||
       (a->H > 0 && !distinct(a->q_out, a->B, a->H, a->N, a->d)) || (a->H_kv > 0 && !distinct(a->k_out, a->B, a->H_kv, a->N, a->d)))
     return LA_ERR_INVALID_ARGUMENT;
-  if ((a->H > 0 && a->q.ptr == a->q_out.ptr && (a->in_dtype != a->out_dtype || !same_rows(a->q, a->q_out))) ||
-      (a->H_kv > 0 && a->k.ptr == a->k_out.ptr && (a->in_dtype != a->out_dtype || !same_rows(a->k, a->k_out))))
+  if (!in_place(a->q, a->q_out, a->B, a->H, a->N, a->in_dtype, a->out_dtype) ||
+      !in_place(a->k, a->k_out, a->B, a->H_kv, a->N, a->in_dtype, a->out_dtype))
     return LA_ERR_INVALID_ARGUMENT;
   if (!spannable(a->q, a->B, a->H, a->N, a->in_dtype) || !spannable(a->k, a->B, a->H_kv, a->N, a->in_dtype) ||
       !spannable(a->q_out, a->B, a->H, a->N, a->out_dtype) || !spannable(a->k_out, a->B, a->H_kv, a->N, a->out_dtype))

@@ -83,9 +83,10 @@ __device__ __forceinline__ bool part_of(const PagedDecodeLaunch& a, Part& p) {
   p.h0 = p.hk * p.group;
   p.seen = seen_tokens(a, p.s);
   if (p.seen.hi < 0 && p.part == 0 && p.hk == 0 && threadIdx.x == 0) atomicOr(a.c.status, kStatusBadIndex);
+  if (p.seen.hi < 0 || p.part >= max(p.seen.parts, 1)) return false;
   p.first = (p.seen.lo / kTile + p.part * p.seen.tiles) * kTile;
   p.last = min(p.seen.hi, p.first + p.seen.tiles * kTile);
-  return p.seen.hi >= 0 && p.part < max(p.seen.parts, 1);
+  return true;
 }
 
 // The running softmax of a warp: rows lane / 4 (0) and that + 8 (1), a quad's lanes with the same maximum and sums of their own.

@@ -178,6 +178,8 @@ def test_positions_outside_the_tables_are_skipped_and_reported():
         for b in range(3):
             for n in range(4):
                 assert bool(torch.all(out[b, :, n] == 7.0)) == ((b, n) in dead)
+    with pytest.raises(ValueError):
+        la.la_qk_norm_rope(q, q, cos=cos, sin=sin, k_out=torch.full_like(q, 7.0))
     out = torch.full_like(q, 7.0)
     la.la_qk_norm_rope(q, lens=longs(dev, [5, 4, -1]), q_out=out)
     assert la.la_device_status() == la.LA_ERR_INVALID_ARGUMENT
