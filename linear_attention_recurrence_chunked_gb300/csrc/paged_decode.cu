@@ -282,12 +282,13 @@ cudaError_t by_width(const PagedDecodeLaunch& a, cudaStream_t stream) {
 
 }  // namespace
 
-// Blocks of one part each would leave SMs idle, or end one long sequence after the others.  Parts of at least kPartTokens
-// tokens, as many as make 16 blocks an SM, so that sequences of unequal lengths even out (256 sequences of 4 key heads, bf16,
-// 402 us; 8 blocks 405, 1 more); of few sequences 5, since every part is written and read again (2 sequences of up to 262144
-// tokens: 137 us with 5, 145 with 16).
+// Blocks of one part each would leave SMs idle, or end one long sequence after the others.  As many parts as make 16 blocks an SM,
+// so that sequences of unequal lengths even out (256 sequences of 4 key heads, bf16, 402 us; 405 with 8), of at least twice
+// kPartTokens tokens (64 sequences of up to 300 tokens over 8 key heads: 15 us, 21 with kPartTokens); of few sequences 5 blocks an
+// SM, since every part is written and read again (2 sequences of up to 262144 tokens: 137 us with 5, 145 with 16), of kPartTokens
+// or more (1 sequence of 2000 tokens: 9 us, 13 with twice as many).
 int paged_decode_splits(int64_t S, int64_t Hkv, int64_t tokens) {
-  const int64_t blocks = S * Hkv, most = (tokens + kPartTokens - 1) / kPartTokens;
+  const int64_t blocks = S * Hkv, part = blocks < 152 ? kPartTokens : 2 * kPartTokens, most = (tokens + part - 1) / part;
   const int64_t want = (152 * (blocks < 152 ? 5 : 16) + blocks - 1) / blocks;
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 256));
 }

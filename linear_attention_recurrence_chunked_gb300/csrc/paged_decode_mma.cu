@@ -26,7 +26,7 @@
 namespace la {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kMostWarps = 4;  // of a block: this many, or one
 constexpr float kSlack = 8.f;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -133,6 +133,7 @@ __device__ __forceinline__ bool weigh(Running& r, float (&x)[T][4], float (&f)[2
 }
 
 // The warps' sums together and out: s_m, s_l [warp][16], `values` warp w's sums of row g at w * stride + g * d.
+template <int kWarps>
 __device__ __forceinline__ void finish(const PagedDecodeLaunch& a, const Part& p, const float (*s_m)[16], const float (*s_l)[16],
                                        const float* values, int stride) {
   const int d = a.c.d;
@@ -219,9 +220,9 @@ constexpr int kStages = DP == 128 ? 3 : 5;
 template <int DP>
 constexpr int kTileBytes = 2 * kTile * DP * 2;  // keys, then values
 template <int DP>
-constexpr int kSmem = kWarps * kStages<DP> * kTileBytes<DP>;
+constexpr int kSmem = kStages<DP> * kTileBytes<DP>;  // of a warp
 
-template <int DP, bool kSpare>
+template <int DP, bool kSpare, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps)
 paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
   using T = __nv_bfloat16;
@@ -229,7 +230,7 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
   extern __shared__ __align__(128) uint8_t pd_smem[];
   __shared__ float s_m[kWarps][16], s_l[kWarps][16];
   __shared__ uint32_t s_seen[kWarps][kS];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, q4 = lane & 3;
+  const int warp = kWarps > 1 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31, row = lane >> 2, q4 = lane & 3;
   grid_dependents_trigger();
   grid_dependency_wait();
   Part p;
@@ -401,7 +402,7 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
     }
   }
   __syncthreads();
-  finish(a, p, s_m, s_l, reinterpret_cast<const float*>(pd_smem), kS * kTileBytes<DP> / 4);
+  finish<kWarps>(a, p, s_m, s_l, reinterpret_cast<const float*>(pd_smem), kS * kTileBytes<DP> / 4);
 }
 
 // ---------------------------------------------------------------------------------------------- 4 bits
@@ -426,7 +427,7 @@ constexpr int kBatch = 16;  // tiles that a warp looks up at once; the spots of 
 template <int D>
 constexpr int kFactors = 2 * kPair * (D / kGroup) * 8;
 template <int D>
-constexpr int kSmem4 = kWarps * (kRing4<D> + kFactors<D> + 4 * kBatch * (int)sizeof(Spot));
+constexpr int kSmem4 = kRing4<D> + kFactors<D> + 4 * kBatch * (int)sizeof(Spot);  // of a warp
 
 // (1 + code / 16) of nibbles m and m + 4 of a word, as bf16.  `one`: two bf16 ones, in a register so that mask and or are
 // one instruction (from C the compiler made two, 1.3 times the whole kernel's).
@@ -453,8 +454,8 @@ __device__ __forceinline__ uint32_t place4(int r, int ch) {
   else return (uint32_t)((r >> 2) * 128 + ((r & 3) ^ ((r >> 1) & 2)) * 32 + ch * 16);
 }
 
-template <int D, bool kSpare>
-__global__ void __launch_bounds__(32 * kWarps, 3)
+template <int D, bool kSpare, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 12 / kWarps)
 paged_decode_four_kernel(const PagedDecodeLaunch a) {
   using T = __nv_bfloat16;
   constexpr int kRows = kSpare ? 1 : 2, kGroups = D / kGroup, kS = kStages4;
@@ -462,7 +463,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
   constexpr int kHalfMeta = kTile * kGroups * 4 / 16;  // and of their scales and offsets
   extern __shared__ __align__(128) uint8_t pd_smem[];
   __shared__ float s_m[kWarps][16], s_l[kWarps][16];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, q4 = lane & 3;
+  const int warp = kWarps > 1 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31, row = lane >> 2, q4 = lane & 3;
   grid_dependents_trigger();
   grid_dependency_wait();
   Part p;
@@ -774,27 +775,33 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
     }
   }
   __syncthreads();
-  finish(a, p, s_m, s_l, reinterpret_cast<const float*>(pd_smem), kRing4<D> / 4);
+  finish<kWarps>(a, p, s_m, s_l, reinterpret_cast<const float*>(pd_smem), kRing4<D> / 4);
 }
 
 template <typename K>
-cudaError_t launch(K kernel, int smem, std::atomic<uint64_t>& done, const PagedDecodeLaunch& a, cudaStream_t stream) {
-  const cudaError_t e = allow_smem(kernel, smem, done);
+cudaError_t launch(K kernel, int warps, int smem, std::atomic<uint64_t>& done, const PagedDecodeLaunch& a, cudaStream_t stream) {
+  const cudaError_t e = allow_smem(kernel, warps * smem, done);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kernel, dim3((unsigned)(a.S * a.c.Hkv * a.splits)), 32 * kWarps, smem, stream, a);
+  return launch_dependent(kernel, dim3((unsigned)(a.S * a.c.Hkv * a.splits)), 32 * warps, warps * smem, stream, a);
 }
+
+// Many blocks of few tokens: blocks of one warp, so that more sequences are in their chain of length, page and rows at once (512
+// sequences of up to 20 tokens over 8 key heads, bf16: 28 us, 57 with four warps a block).
+bool one_warp(const PagedDecodeLaunch& a) { return a.S * a.c.Hkv * a.splits >= 152 * 16 && a.c.width * a.c.page / a.splits <= 512; }
 
 template <int DP, bool kSpare>
 cudaError_t launch_bf16(const PagedDecodeLaunch& a, cudaStream_t stream) {
-  static std::atomic<uint64_t> done{0};
+  static std::atomic<uint64_t> done[2];
   static_assert(kStages<DP> * kTileBytes<DP> >= 16 * DP * 4, "a warp's sums take the place of its ring");
-  return launch(paged_decode_bf16_kernel<DP, kSpare>, kSmem<DP>, done, a, stream);
+  return one_warp(a) ? launch(paged_decode_bf16_kernel<DP, kSpare, 1>, 1, kSmem<DP>, done[0], a, stream)
+                     : launch(paged_decode_bf16_kernel<DP, kSpare, kMostWarps>, kMostWarps, kSmem<DP>, done[1], a, stream);
 }
 template <int D, bool kSpare>
 cudaError_t launch_four(const PagedDecodeLaunch& a, cudaStream_t stream) {
-  static std::atomic<uint64_t> done{0};
+  static std::atomic<uint64_t> done[2];
   static_assert(kRing4<D> >= 16 * D * 4, "a warp's sums take the place of its ring");
-  return launch(paged_decode_four_kernel<D, kSpare>, kSmem4<D>, done, a, stream);
+  return one_warp(a) ? launch(paged_decode_four_kernel<D, kSpare, 1>, 1, kSmem4<D>, done[0], a, stream)
+                     : launch(paged_decode_four_kernel<D, kSpare, kMostWarps>, kMostWarps, kSmem4<D>, done[1], a, stream);
 }
 
 }  // namespace

@@ -405,6 +405,25 @@ def test_split_sequences(dtype, bits, H, Hkv, d, window, softcap):
         la.la_paged_decode_step(qd, kd, vd, td, longs(dev, lens), window=window, workspace=ws[:size - 16])
 
 
+@pytest.mark.parametrize("bits,d,H,Hkv", [(0, 128, 8, 4), (0, 40, 40, 4), (4, 64, 4, 4), (4, 128, 16, 4), (4, 128, 64, 4)])
+def test_many_short_sequences(bits, d, H, Hkv):
+    """Enough of them for blocks of one warp."""
+    dev = cuda_device()
+    g = gen(d + H)
+    S, page = 640, 16
+    lens = [(7 * s) % 61 for s in range(S)]
+    pools, table = cache(g, lens, page, Hkv, d, BF, bits, 1.2)
+    q = randn(g, S, H, d, dtype=BF, scale=1.2)
+    sl = torch.exp2(-8.0 * torch.arange(1, H + 1) / H)
+    for window in (0, 19):
+        got = la.la_paged_decode_step(*on(dev, q, *pools, table), longs(dev, lens), window=window, slopes=sl.to(dev), out_dtype=FP)
+        some = list(range(0, S, 23)) + [S - 1]
+        o, bound = ref.step(q[some], *pools, table[some], [lens[s] for s in some], window, d ** -0.5, 0.0, sl, FP)
+        ref.check(got[some], o, bound)
+        assert torch.isfinite(got).all() and torch.all(got[[s for s in range(S) if lens[s] == 0]] == 0)
+    assert la.la_device_status() == la.LA_OK
+
+
 @pytest.mark.parametrize("bits,d,H", [(0, 128, 4), (4, 64, 4), (4, 128, 16)])
 def test_means_of_many_values_keep_their_bits(bits, d, H):
     """A flat softmax over 40000 tokens gives means of 1 / sqrt(n) of a value's size, which sums that drift would drown.  Each
