@@ -221,46 +221,60 @@ paged_decode_f32_kernel(const PagedDecodeLaunch a, const int passes) {
 }
 
 constexpr int kJoinWarps = 8;
+constexpr int kMostParts = 32 * kJoinWarps;
 
-// The parts of a split sequence together: a block a query head, its warps (one for a few parts, or kJoinWarps) in turn a part,
-// four elements a lane.
+// The parts of a split sequence together: a block a query head, with a thread for every part.  A warp adds up every kJoinWarps-th
+// part (every one, of few), four elements a lane; the first of them are on their way while the parts' weights are made.
 template <typename TOut>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 paged_join_kernel(const PagedDecodeLaunch a) {
-  __shared__ float s_o[kJoinWarps][kMaxD], s_l[kJoinWarps];
+  constexpr int kAhead = 8;
+  __shared__ float s_o[kJoinWarps][kMaxD], s_w[kMostParts], s_top[kJoinWarps], s_l[kJoinWarps];
   grid_dependents_trigger();
   grid_dependency_wait();
   const int64_t s = blockIdx.x / a.H, h = blockIdx.x - s * a.H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, d = a.c.d;
   const SeenTokens t = seen_tokens(a, s);
   if (t.hi < 0) return;
-  const float2* sums = part_sums(a, s, h, 0);
-  float top = -INFINITY;
-  for (int i = lane; i < t.parts; i += 32) top = fmaxf(top, sums[i].x);
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, off));
-  const float base = top == -INFINITY ? 0.f : top;
-  float o[4] = {0.f, 0.f, 0.f, 0.f}, total = 0.f;
+  const float2 mine = (int)threadIdx.x < t.parts ? part_sums(a, s, h, 0)[threadIdx.x] : make_float2(-INFINITY, 0.f);
   const bool on = lane * 4 < d;
   const float* values = part_values(a, s, h, 0) + (on ? lane * 4 : 0);
-#pragma unroll 8
-  for (int i = warp; i < t.parts; i += warps) {
-    const float2 ml = sums[i];
-    const float4 v = *reinterpret_cast<const float4*>(values + (int64_t)i * d);
-    const float w = ex2(ml.x - base);
-    total = fmaf(w, ml.y, total);
-    o[0] = fmaf(w, v.x, o[0]); o[1] = fmaf(w, v.y, o[1]); o[2] = fmaf(w, v.z, o[2]); o[3] = fmaf(w, v.w, o[3]);
+  float4 ahead[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const int i = warp + j * warps;
+    ahead[j] = i < t.parts ? *reinterpret_cast<const float4*>(values + (int64_t)i * d) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  float top = mine.x;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, off));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+  for (int u = 0; u < warps; ++u) top = fmaxf(top, s_top[u]);
+  const float weight = ex2(mine.x - (top == -INFINITY ? 0.f : top));
+  s_w[threadIdx.x] = weight;
+  const float l = warp_sum((int)threadIdx.x < t.parts ? weight * mine.y : 0.f);
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+  auto add = [&](int i, float4 v) {
+    const float w = s_w[i];
+    o[0] = fmaf(w, v.x, o[0]); o[1] = fmaf(w, v.y, o[1]); o[2] = fmaf(w, v.z, o[2]); o[3] = fmaf(w, v.w, o[3]);
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j)
+    if (warp + j * warps < t.parts) add(warp + j * warps, ahead[j]);
+#pragma unroll 8
+  for (int i = warp + kAhead * warps; i < t.parts; i += warps) add(i, *reinterpret_cast<const float4*>(values + (int64_t)i * d));
   if (on) *reinterpret_cast<float4*>(&s_o[warp][lane * 4]) = make_float4(o[0], o[1], o[2], o[3]);
-  if (lane == 0) s_l[warp] = total;
   __syncthreads();
   for (int c = threadIdx.x; c < d; c += blockDim.x) {
-    float sum = 0.f, all = 0.f;
+    float sum = 0.f, total = 0.f;
     for (int u = 0; u < warps; ++u) {
       sum += s_o[u][c];
-      all += s_l[u];
+      total += s_l[u];
     }
-    store1(static_cast<TOut*>(a.out) + s * a.o_sb + h * a.o_sh + c, mean_of(sum, all));
+    store1(static_cast<TOut*>(a.out) + s * a.o_sb + h * a.o_sh + c, mean_of(sum, total));
   }
 }
 
@@ -290,7 +304,7 @@ cudaError_t by_width(const PagedDecodeLaunch& a, cudaStream_t stream) {
 int paged_decode_splits(int64_t S, int64_t Hkv, int64_t tokens) {
   const int64_t blocks = S * Hkv, part = blocks < 152 ? kPartTokens : 2 * kPartTokens, most = (tokens + part - 1) / part;
   const int64_t want = (152 * (blocks < 152 ? 5 : 16) + blocks - 1) / blocks;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 256));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), kMostParts));
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeLaunch& a, cudaStream_t stream) {
