@@ -528,6 +528,34 @@ def test_values_that_are_not_finite(dtype, H):
     assert torch.isfinite(got[0][:, rest]).all() and torch.equal(got[0][:, rest], clean[0][:, rest])
 
 
+@pytest.mark.parametrize("dtype,bits", [(FP, 0), (BF, 0), (BF, 4)])
+def test_repeated_axes_full_tables_and_single_tokens(dtype, bits):
+    """Heads or sequences repeated with stride 0, sequences that fill their table to the last slot, windows of one token."""
+    dev = cuda_device()
+    g = gen(61 + bits)
+    B, H, Hkv, N, d, page = 3, 6, 2, 32, 64, 16
+    cos, sin = ref.tables(N, 64)
+    x = randn(g, 1, 1, N, d, dtype=dtype)
+    y, bound = ref.norm_rope(x, None, "l2", 1e-6, cos, sin, np.arange(N)[None], False, None, dtype)
+    cd, sd = on(dev, cos, sin)
+    got, alone = la.la_qk_norm_rope(x.to(dev).expand(B, H, N, d), x.to(dev).expand(B, Hkv, N, d), norm="l2", cos=cd, sin=sd)
+    ref.check(got, np.broadcast_to(y, got.shape), np.broadcast_to(bound, got.shape))
+    assert torch.equal(got[:, :Hkv], alone)
+    table, count = table_of(g, [N] * B, page, spare_columns=0, spare_pages=0)
+    assert table.shape[1] * page == N
+    pools = [torch.zeros((count, Hkv, page, d * 9 // 16 if bits else d), dtype=torch.uint8 if bits else dtype, device=dev) for _ in range(2)]
+    v = randn(g, B, 1, N, d, dtype=dtype).to(dev).expand(B, Hkv, N, d)
+    la.la_paged_append(alone[:1].expand(B, Hkv, N, d), v, *pools, table.to(dev), longs(dev, [0] * B))
+    q = randn(g, 1, H, d, dtype=dtype)
+    for window in (0, 1):
+        o, bound = ref.step(q.expand(B, H, d), *pools, table, [N, N, N - 1], window, d ** -0.5, 0.0, None, FP)
+        got = la.la_paged_decode_step(q.to(dev).expand(B, H, d), *pools, table.to(dev), longs(dev, [N, N, N - 1]), window=window, out_dtype=FP)
+        ref.check(got, o, bound)
+    if not bits:
+        assert torch.equal(got[0, 0], v[0, 0, N - 1].float()) and torch.equal(got[2, 5], v[2, 1, N - 2].float())
+    assert la.la_device_status() == la.LA_OK
+
+
 # ------------------------------------------------------------------------------------------ together, streams, graphs
 @pytest.mark.parametrize("bits,window,interleaved", [(0, 0, False), (4, 0, False), (0, 40, True)])
 def test_a_layer_over_a_prompt_and_steps(bits, window, interleaved):
