@@ -447,6 +447,13 @@ __device__ __forceinline__ uint32_t centred(uint32_t w, uint32_t one) {
   return r;
 }
 
+// Nibbles m and m + 4 of a word as two bf16 numbers code * step<m>.  The last eight bits of a bf16 are a whole number of 2^-133
+// (subnormals and the first binade have the same step), so that a mask is all it takes, and a shift for two.
+template <int m>
+__device__ __forceinline__ uint32_t whole(uint32_t w, uint32_t w8) {  // w8: w >> 8
+  return (m < 2 ? w : w8) & (m & 1 ? 0x00f000f0u : 0x000f000fu);
+}
+
 // Place of a row's 16-byte chunk: the rows that a product's lanes read together lie in different banks.
 template <int D>
 __device__ __forceinline__ uint32_t place4(int r, int ch) {
@@ -522,6 +529,19 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
 
   // ---- queries as operands: word e = 2 q4 + u of group g holds elements 64 g + 8 e + (0..7), whose pairs (m, m + 4) are a
   // product's neighbours; and the groups' sums of them
+  // The largest element of the group's heads becomes 2^120 to 2^121, so that products with 2^-133 stay in fp32's range.
+  int top = 0;
+  for (int e = lane; e < p.group * (D / 8); e += 32) {
+    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q.ptr) + p.s * a.q.sb + (p.h0 + e / (D / 8)) * a.q.sh + e % (D / 8) * 8);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max((int)(x[i] & 0x7f80u) >> 7, (int)(x[i] >> 23 & 0xffu)));
+  }
+  top = min((int)__reduce_max_sync(kFullMask, (unsigned)top), 254);  // a biased exponent; of an infinity the largest finite one
+  const int up = min(374 - top, 254);  // 2^120 over the largest, as a biased exponent
+  const float q_up = __uint_as_float((uint32_t)up << 23);
+  // 2^133 / q_up in two factors, times what scores are multiplied by
+  const float q_down = __uint_as_float((uint32_t)((260 - up) / 2 + 127) << 23), q_down2 = __uint_as_float((uint32_t)(260 - up - (260 - up) / 2 + 127) << 23);
   uint32_t qa[kGroups][2][4 * kRows];  // [group][word][m, row]
   float qs[kGroups][2] = {}, slope[2] = {0.f, 0.f};
 #pragma unroll
@@ -537,7 +557,10 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
         if (h < p.group) w = *reinterpret_cast<const uint4*>(q + kGroup * g + 8 * (2 * q4 + u));
         float v[8];
         unpack_vec(w, v);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};  // pairs (0, 1) (2, 3) (4, 5) (6, 7)
+        // times q_up, and a sixteenth where the code is the upper one of its byte; powers of two, exact
+        uint32_t x[4];  // pairs (0, 1) (2, 3) (4, 5) (6, 7)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = tc::pack2_bf16(v[2 * e] * q_up, v[2 * e + 1] * (q_up * 0.0625f));
 #pragma unroll
         for (int m = 0; m < 4; ++m) qa[g][u][m * kRows + i] = __byte_perm(x[m / 2], x[2 + m / 2], m & 1 ? 0x7632 : 0x5410);
 #pragma unroll
@@ -606,12 +629,9 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
       }
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        f[2 * g] = 16.f * __uint_as_float(w[g] << 16);
-        f[2 * g + 1] = fmaf(v == 0 ? -1.f : 0.5f, f[2 * g], __uint_as_float(w[g] & 0xffff0000u));
-        if (v == 0) {
-          f[2 * g] *= scale;
-          f[2 * g + 1] *= scale;
-        }
+        const float step = __uint_as_float(w[g] << 16), offset = __uint_as_float(w[g] & 0xffff0000u);
+        f[2 * g] = v == 0 ? step * (q_down * scale) * q_down2 : 16.f * step;
+        f[2 * g + 1] = v == 0 ? offset * scale : fmaf(8.f, step, offset);
       }
       if (!(seen >> lane & 1u)) {
 #pragma unroll
@@ -651,7 +671,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const uint32_t(&q)[4 * kRows] = qa[g][u];
-          const uint32_t b0 = ones<0>(w[g][u], one), b1 = ones<1>(w[g][u], one), b2 = ones<2>(w[g][u], one), b3 = ones<3>(w[g][u], one);
+          const uint32_t w8 = w[g][u] >> 8, b0 = whole<0>(w[g][u], w8), b1 = whole<1>(w[g][u], w8), b2 = whole<2>(w[g][u], w8), b3 = whole<3>(w[g][u], w8);
           if constexpr (kSpare) {
             // Four registers of one head's elements as one operand, m = 0 and 2 in its rows 0 to 7, 1 and 3 in the others: the
             // rows that do not match a product's second operand are not used (zeros for them would take registers, or moves).
