@@ -5,19 +5,20 @@
 // tiles of its block's part in turn, through a ring of its own in shared memory that asynchronous copies fill, with the
 // running maximum and sum of its tokens; no warp waits for another before the end, where their sums meet.  A tile's pages
 // are looked up one tile (4 bits: sixteen tiles) ahead of its copies.  256 sequences of up to 8192 tokens, 32 heads over 4 and
-// d = 128 in bf16 take 398 us, the measured copy rate; of up to 16384 tokens in 4 bits 416 us, 54 % of it: 940 warp
+// d = 128 in bf16 take 398 us, the measured copy rate; of up to 16384 tokens in 4 bits 398 us, 56 % of it: 940 warp
 // instructions for 32 tokens, of which 300 turn codes into bf16, at 2.1 a clock.
 //
 // The running maximum moves only where a score is more than 2^kSlack times beyond it: until then weights are up to 2^kSlack,
 // which costs fp32 sums nothing, and the sums of values need not be scaled.
 //
-// 4 bits: a code is put into the mantissa of a bf16 one, 1 + code / 16, exactly, and the products run on those:
-//   k = offset + scale code = (offset - 16 scale) + 16 scale (1 + code / 16)
-//   q.k = sum over groups of 16 scale (q.(1 + code / 16)) + (offset - 16 scale) sum q
+// 4 bits: scales and offsets meet whole sums of codes in fp32 (keys), and weights once per group (values):
+//   q.k = sum over groups of scale (q.code) + offset sum q
 //   sum_j p_j v_j = sum_j (16 scale_j p_j) (code_j - 8) / 16 + sum_j p_j (offset_j + 8 scale_j)
-// so that scales and offsets meet whole sums in fp32, and weights once per group.  Values have the ones taken off (one packed
-// subtraction): their sums run over thousands of tokens and come out near zero, while sums of ones would not (off by 6e-4 of
-// an output's norm over 131071 tokens, where tensor cores cut sums off).
+// A key's code is the last bits of a bf16 number, a whole number of 2^-133, which takes a mask, and a head's query is scaled up by
+// a power of two to match (398 us; 415 with keys made like values).  A value's code is put into the mantissa of a one,
+// 1 + code / 16, and less 3/2: sums over thousands of tokens of centred codes come out near zero, while sums of ones would not
+// (off by 5e-4 of an output's norm over 131071 tokens, where tensor cores cut sums off; 7e-6 centred).  Values as whole numbers
+// too, weights scaled by the largest scale so far, took 1 % off for a rescaling and more spilled registers.
 #include <algorithm>
 
 #include "paged_decode.cuh"
@@ -423,7 +424,7 @@ struct __align__(16) Spot {
   uint32_t seen;
 };
 constexpr int kBatch = 16;  // tiles that a warp looks up at once; the spots of two batches are kept
-// ... and each token's 16 scale and offset - 16 scale, of its keys' groups and of its values', and the spots
+// ... and each token's factors, of its keys' groups and of its values', and the spots
 template <int D>
 constexpr int kFactors = 2 * kPair * (D / kGroup) * 8;
 template <int D>
@@ -447,8 +448,8 @@ __device__ __forceinline__ uint32_t centred(uint32_t w, uint32_t one) {
   return r;
 }
 
-// Nibbles m and m + 4 of a word as two bf16 numbers code * step<m>.  The last eight bits of a bf16 are a whole number of 2^-133
-// (subnormals and the first binade have the same step), so that a mask is all it takes, and a shift for two.
+// Nibbles m and m + 4 of a word as two bf16 numbers, code 2^-133 or (m odd) 16 times that: the last eight bits of a bf16 number,
+// the others zero, are a whole number of 2^-133 (subnormals and the first binade have the same step).
 template <int m>
 __device__ __forceinline__ uint32_t whole(uint32_t w, uint32_t w8) {  // w8: w >> 8
   return (m < 2 ? w : w8) & (m & 1 ? 0x00f000f0u : 0x000f000fu);
@@ -529,42 +530,50 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
 
   // ---- queries as operands: word e = 2 q4 + u of group g holds elements 64 g + 8 e + (0..7), whose pairs (m, m + 4) are a
   // product's neighbours; and the groups' sums of them
-  // The largest element of the group's heads becomes 2^120 to 2^121, so that products with 2^-133 stay in fp32's range.
-  int top = 0;
-  for (int e = lane; e < p.group * (D / 8); e += 32) {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q.ptr) + p.s * a.q.sb + (p.h0 + e / (D / 8)) * a.q.sh + e % (D / 8) * 8);
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) top = max(top, max((int)(x[i] & 0x7f80u) >> 7, (int)(x[i] >> 23 & 0xffu)));
-  }
-  top = min((int)__reduce_max_sync(kFullMask, (unsigned)top), 254);  // a biased exponent; of an infinity the largest finite one
-  const int up = min(374 - top, 254);  // 2^120 over the largest, as a biased exponent
-  const float q_up = __uint_as_float((uint32_t)up << 23);
-  // 2^133 / q_up in two factors, times what scores are multiplied by
-  const float q_down = __uint_as_float((uint32_t)((260 - up) / 2 + 127) << 23), q_down2 = __uint_as_float((uint32_t)(260 - up - (260 - up) / 2 + 127) << 23);
+  // Each head's largest element becomes 2^120 to 2^121 (larger from 2^121 on, and at most times 2^127), so that its products with
+  // whole numbers of 2^-133 are in the middle of fp32's range; scores are multiplied by 2^126 over that, the scales by 2^7.
+  float q_down[kRows];
   uint32_t qa[kGroups][2][4 * kRows];  // [group][word][m, row]
   float qs[kGroups][2] = {}, slope[2] = {0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int h = row + 8 * i;
     const T* q = static_cast<const T*>(a.q.ptr) + p.s * a.q.sb + (p.h0 + (h < p.group ? h : 0)) * a.q.sh;
+    uint4 words[kGroups][2];
+    int top = 0;  // the largest biased exponent
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint4& w = words[g][u];
+        w = make_uint4(0u, 0u, 0u, 0u);
+        if (h < p.group) w = *reinterpret_cast<const uint4*>(q + kGroup * g + 8 * (2 * q4 + u));
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max((int)(x[e] >> 7 & 0xffu), (int)(x[e] >> 23 & 0xffu)));
+      }
+    top = max(top, __shfl_xor_sync(kFullMask, top, 1));
+    top = max(top, __shfl_xor_sync(kFullMask, top, 2));
+    const int up = min(max(374 - top, 126), 254);  // biased exponents
+    const float q_up = __uint_as_float((uint32_t)up << 23);
+    q_down[i] = __uint_as_float((uint32_t)(380 - up) << 23) * score_scale(a);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       float sum = 0.f;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (h < p.group) w = *reinterpret_cast<const uint4*>(q + kGroup * g + 8 * (2 * q4 + u));
         float v[8];
-        unpack_vec(w, v);
-        // times q_up, and a sixteenth where the code is the upper one of its byte; powers of two, exact
+        unpack_vec(words[g][u], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= q_up;
+        // a sixteenth where the code is the upper one of its byte; powers of two, exact
         uint32_t x[4];  // pairs (0, 1) (2, 3) (4, 5) (6, 7)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = tc::pack2_bf16(v[2 * e] * q_up, v[2 * e + 1] * (q_up * 0.0625f));
+        for (int e = 0; e < 4; ++e) x[e] = tc::pack2_bf16(v[2 * e], v[2 * e + 1] * 0.0625f);
 #pragma unroll
         for (int m = 0; m < 4; ++m) qa[g][u][m * kRows + i] = __byte_perm(x[m / 2], x[2 + m / 2], m & 1 ? 0x7632 : 0x5410);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += v[e];
+        for (int e = 0; e < 8; ++e) sum = fmaf(v[e], 0x1p-126f, sum);
       }
       sum += __shfl_xor_sync(kFullMask, sum, 1);
       qs[g][i] = sum + __shfl_xor_sync(kFullMask, sum, 2);
@@ -573,7 +582,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
   }
   uint32_t one = 0x3f803f80u;
   asm volatile("" : "+r"(one));
-  const float scale = score_scale(a), inv_cap = 1.f / a.softcap;
+  const float inv_cap = 1.f / a.softcap;
   // tile t's column c is this token of the warp's 32, so that a lane's four weights of a 16-token product are tokens
   // q4, q4 + 4, q4 + 8, q4 + 12 of it
   auto token = [](int t, int c) { return (t >> 1) * kTile + (c >> 1) + 4 * (2 * (t & 1) + (c & 1)); };
@@ -616,7 +625,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
     const uint8_t* tile = region + stage * kTileBytes4<D>;
     const uint32_t* meta = reinterpret_cast<const uint32_t*>(tile + 2 * kCodes<D>);
     const uint32_t seen = spots[i % (2 * kBatch) * 2].seen | spots[i % (2 * kBatch) * 2 + 1].seen << 16;
-    // ---- a token a lane: 16 scale and offset - 16 scale of keys, times what scores are multiplied by, and offset + 8 scale of values
+    // ---- a token a lane: 2^7 scale and offset of keys, 16 scale and offset + 8 scale of values
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       uint32_t w[kGroups];
@@ -630,8 +639,8 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         const float step = __uint_as_float(w[g] << 16), offset = __uint_as_float(w[g] & 0xffff0000u);
-        f[2 * g] = v == 0 ? step * (q_down * scale) * q_down2 : 16.f * step;
-        f[2 * g + 1] = v == 0 ? offset * scale : fmaf(8.f, step, offset);
+        f[2 * g] = v == 0 ? 128.f * step : 16.f * step;
+        f[2 * g + 1] = v == 0 ? offset : fmaf(8.f, step, offset);
       }
       if (!(seen >> lane & 1u)) {
 #pragma unroll
@@ -701,7 +710,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
             sum = g == 0 ? f[1] * qs[0][u] : fmaf(f[2 * g + 1], qs[g][u], sum);
             sum = fmaf(f[2 * g], product, sum);
           }
-          x[t][2 * u + c] = sum;
+          x[t][2 * u + c] = sum * q_down[u];
         }
       }
     }

@@ -506,6 +506,22 @@ def test_scores_far_apart(dtype, bits):
     ref.check(got, o, bound)
 
 
+@pytest.mark.parametrize("dtype,bits,H,d", [(FP, 0, 4, 64), (BF, 0, 4, 64), (BF, 0, 16, 128), (BF, 4, 4, 64), (BF, 4, 8, 128), (BF, 4, 16, 128)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 3e38])
+def test_a_heads_query_is_its_own(dtype, bits, H, d, value):
+    """Small queries of large keys, beside a head whose query is huge or not finite: it reaches no other head."""
+    dev = cuda_device()
+    g = gen(31)
+    n, odd = 150, 1
+    pools, table = cache(g, [n], 16, 1, d, dtype, bits, scale=128.0)
+    q = randn(g, 1, H, d, dtype=dtype, scale=2.0 ** -7)
+    others = [h for h in range(H) if h != odd]
+    o, bound = ref.step(q[:, others], *pools, table, [n], 0, d ** -0.5, 0.0, None, FP)
+    q[:, odd] = value
+    got = la.la_paged_decode_step(*on(dev, q, *pools, table), longs(dev, [n]), out_dtype=FP)
+    ref.check(got[:, others], o, bound)
+
+
 @pytest.mark.parametrize("H", [4, 16])
 @pytest.mark.parametrize("dtype", [FP, BF])
 def test_values_that_are_not_finite(dtype, H):
