@@ -5,8 +5,8 @@
 // tiles of its block's part in turn, through a ring of its own in shared memory that asynchronous copies fill, with the
 // running maximum and sum of its tokens; no warp waits for another before the end, where their sums meet.  A tile's pages
 // are looked up one tile (4 bits: sixteen tiles) ahead of its copies.  256 sequences of up to 8192 tokens, 32 heads over 4 and
-// d = 128 in bf16 take 398 us, the measured copy rate; of up to 16384 tokens in 4 bits 398 us, 56 % of it: 940 warp
-// instructions for 32 tokens, of which 300 turn codes into bf16, at 2.1 a clock.
+// d = 128 in bf16 take 398 us, the measured copy rate; of up to 16384 tokens in 4 bits 398 us, 56 % of it: 920 warp
+// instructions for 32 tokens, of which 290 turn codes into bf16, at 2.2 a clock.
 //
 // The running maximum moves only where a score is more than 2^kSlack times beyond it: until then weights are up to 2^kSlack,
 // which costs fp32 sums nothing, and the sums of values need not be scaled.
