@@ -14,7 +14,8 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 2;   // rows of a lane on their way at once, of the keys and of the values, in an append
-constexpr int kReads = 4;  // and in a read
+constexpr int kReads = 4;  // and in a read, where a lane has as many of a tile's tokens
+constexpr int kTokens = 16;  // of a read's tile; a page holds a multiple
 
 int lanes_of(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : 16; }
 
@@ -258,21 +259,22 @@ paged_append_kernel(const PagedAppendLaunch a, const int per, const Divisor part
   values.store(a, a.c.v, place, h0, heads, turn);
 }
 
-// A warp reads 16 tokens of one head, keys or values.
+// A warp reads a tile of kTokens tokens, which lie in one page, of one head's keys or values.
 template <typename T, typename TOut, bool kFour, int LPR>
 __global__ void __launch_bounds__(kThreads)
 paged_read_kernel(const PagedReadLaunch a, const Divisor tiles, const Divisor heads2, const Divisor pages) {
-  constexpr int R = 32 / LPR;
+  constexpr int R = 32 / LPR, kLane = kTokens / R, kBatch = kReads < kLane ? kReads : kLane;  // a lane's rows of a tile, and at once
+  static_assert(kLane % kBatch == 0, "a whole tile's batches check no row");
   const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR;
   grid_dependents_trigger();
   grid_dependency_wait();
   const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), bhv = tiles(unit), b = heads2(bhv);
   if (b >= a.B) return;  // whole warps
-  const int n0 = (int)(unit - bhv * tiles.d) * 16;
+  const int n0 = (int)(unit - bhv * tiles.d) * kTokens;
   const bool values = bhv & 1;
   const int h = (int)(bhv - b * heads2.d) >> 1, d = a.c.d;
   const bool on = col * 8 < d, report = lane == 0 && h == 0 && !values;
-  const int len = (int)sequence_length(a.lens, b, a.N, a.c.status, report && n0 == 0), end = min(n0 + 16, (int)a.N);
+  const int len = (int)sequence_length(a.lens, b, a.N, a.c.status, report && n0 == 0), end = min(n0 + kTokens, (int)a.N);
   int have = max(n0, min(len, end));  // tokens below are in the cache
   int page = -1, slot = 0;
   if (n0 < have) {
@@ -300,10 +302,10 @@ paged_read_kernel(const PagedReadLaunch a, const Divisor tiles, const Divisor he
   asm volatile("" : "+r"(magic));
 
   auto batch = [&](auto all, int i0) {  // all: every row is there
-    [[maybe_unused]] Raw8<T> raw[kReads];
-    [[maybe_unused]] uint32_t codes[kReads], meta[kReads];
+    [[maybe_unused]] Raw8<T> raw[kBatch];
+    [[maybe_unused]] uint32_t codes[kBatch], meta[kBatch];
 #pragma unroll
-    for (int i = 0; i < kReads; ++i) {
+    for (int i = 0; i < kBatch; ++i) {
       if (!decltype(all)::value && there <= (i0 + i) * R) continue;
       if constexpr (kFour) {
         codes[i] = words[i * R * kWords];
@@ -312,11 +314,11 @@ paged_read_kernel(const PagedReadLaunch a, const Divisor tiles, const Divisor he
         raw[i].template load<true>(rows + i * R * d, at);
       }
     }
-    words += kReads * R * kWords;
-    metas += kReads * R * kGroups;
-    rows += kReads * R * d;
+    words += kBatch * R * kWords;
+    metas += kBatch * R * kGroups;
+    rows += kBatch * R * d;
 #pragma unroll
-    for (int i = 0; i < kReads; ++i, y += yr) {
+    for (int i = 0; i < kBatch; ++i, y += yr) {
       if (!decltype(all)::value && wanted <= (i0 + i) * R) continue;
       f32x2 v[4];
       Raw8<TOut> packed;
@@ -344,12 +346,12 @@ paged_read_kernel(const PagedReadLaunch a, const Divisor tiles, const Divisor he
       packed.template store<true>(y, at);
     }
   };
-  if (have == n0 + 16) {
+  if (have == n0 + kTokens) {
 #pragma unroll
-    for (int i0 = 0; i0 < 16 / R; i0 += kReads) batch(std::true_type{}, i0);
+    for (int i0 = 0; i0 < kLane; i0 += kBatch) batch(std::true_type{}, i0);
   } else {
 #pragma unroll 1
-    for (int i0 = 0; i0 < 16 / R; i0 += kReads) batch(std::false_type{}, i0);
+    for (int i0 = 0; i0 < kLane; i0 += kBatch) batch(std::false_type{}, i0);
   }
 }
 
@@ -374,7 +376,7 @@ cudaError_t append(const PagedAppendLaunch& a, cudaStream_t stream) {
 
 template <typename T, typename TOut, bool kFour, int LPR>
 cudaError_t read(const PagedReadLaunch& a, cudaStream_t stream) {
-  const int64_t tiles = (a.N + 15) / 16, blocks = (2 * a.B * a.c.Hkv * tiles + kWarps - 1) / kWarps;
+  const int64_t tiles = (a.N + kTokens - 1) / kTokens, blocks = (2 * a.B * a.c.Hkv * tiles + kWarps - 1) / kWarps;
   return launch_dependent(paged_read_kernel<T, TOut, kFour, LPR>, dim3((unsigned)blocks), kThreads, 0, stream, a, Divisor(tiles), Divisor(2 * a.c.Hkv), Divisor(a.c.page));
 }
 

@@ -265,6 +265,37 @@ def test_paged_append_and_read(B, N, Hkv, d, page, rot, interleaved, dtype, bits
             assert torch.all(kept[which][b, :, n:] == 3.0)
 
 
+@pytest.mark.parametrize("dtype,bits,d", [(t, 0, d) for t in (BF, FP) for d in (8, 16, 24, 32, 40, 72, 128)] + [(BF, 4, 64), (BF, 4, 128)])
+@pytest.mark.parametrize("page,N", [(16, 16), (16, 51), (48, 48), (48, 32)])
+def test_reads_stay_within_their_rows(dtype, bits, d, page, N):
+    """Lengths at, below and beyond whole tiles of 16 tokens, into views with other rows on every side of them."""
+    dev = cuda_device()
+    g = gen(d + page + N + bits)
+    Hkv = 3
+    lens = [n for n in (16, 0, 48, 17, 32, 15, 33, 1, 31, 51) if n <= N]
+    lens.append(lens[0])  # a whole tile at the end
+    table, count = table_of(g, lens, page, spare_pages=1)
+    pools = [randn(g, count, Hkv, page, d, dtype=dtype) for _ in range(2)]
+    if bits:
+        pools = [pack(x) for x in pools]
+    want = [ref.values(x, d)[0] for x in pools]
+    given = [on(dev, x)[0] for x in (*pools, table)]
+    B = len(lens)
+    for out in (BF, FP):
+        around = [torch.full((B + 2, Hkv + 2, N + 64, d + 8), 3.0, dtype=out, device=dev) for _ in range(2)]
+        k, v = (x[1:-1, 1:-1, 32:32 + N, :d] for x in around)
+        la.la_paged_read(*given, longs(dev, lens), N, k=k, v=v)
+        made = la.la_paged_read(*given, longs(dev, lens), N, out_dtype=out)
+        for which in range(2):
+            rows = torch.full(tuple(around[which].shape), 3.0, dtype=out)
+            alone = torch.zeros((B, Hkv, N, d), dtype=out)
+            for b, n in enumerate(lens):
+                x = torch.from_numpy(ref.gather(want[which], table, b, 0, n)).float().to(out)
+                rows[1 + b, 1:-1, 32:32 + n, :d], alone[b, :, :n] = x, x
+            assert torch.equal(around[which].cpu(), rows) and torch.equal(made[which].cpu(), alone)
+    assert la.la_device_status() == la.LA_OK
+
+
 def test_4bit_groups_at_the_ends():
     """Equal elements, tiny spreads, spreads beyond fp32, NaN and infinities: a group's own affair."""
     dev = cuda_device()
