@@ -11,6 +11,12 @@
 // The running maximum moves only where a score is more than 2^kSlack times beyond it: until then weights are up to 2^kSlack,
 // which costs fp32 sums nothing, and the sums of values need not be scaled.
 //
+// Weights (in 4 bits times their value's scale) are split into bf16 parts for their product with the values.  Two leave them
+// off by 2^-17, a 500th of a bf16 output's own half step.  An fp32 output would show it (1.5e-6 of an output's norm over
+// 8192 tokens, where PyTorch in fp32 is off by 6e-7), so it takes three, off by less than fp32's own rounding (5.5e-7): 395 us
+// instead of 391 for the bf16 batch below, 446 instead of 398 for the one in 4
+// bits; 5 % of bf16 steps with 16 heads a key head, 11 % with one of d = 64.
+//
 // 4 bits: scales and offsets meet whole sums of codes in fp32 (keys), and weights once per group (values):
 //   q.k = sum over groups of scale (q.code) + offset sum q
 //   sum_j p_j v_j = sum_j (16 scale_j p_j) (code_j - 8) / 16 + sum_j p_j (offset_j + 8 scale_j)
@@ -29,6 +35,9 @@ namespace {
 
 constexpr int kMostWarps = 4;  // of a block: this many, or one
 constexpr float kSlack = 8.f;
+constexpr uint32_t kTiny = 0x00010001u;  // two bf16 2^-133
+template <typename TOut>
+constexpr bool kThree = sizeof(TOut) == 4;  // weights in three parts, not two
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -59,6 +68,15 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 __device__ __forceinline__ void two_parts(float lo, float hi, uint32_t& major, uint32_t& minor) {
   major = tc::pack2_bf16(lo, hi);
   minor = tc::pack2_bf16(lo - __uint_as_float(major << 16), hi - __uint_as_float(major & 0xffff0000u));
+}
+
+// ... and what both leave, as bf16: together off by 2^-26 of a value.  `three` false: last stays as it is.
+template <bool three>
+__device__ __forceinline__ void in_parts(float lo, float hi, uint32_t& major, uint32_t& minor, uint32_t& last) {
+  two_parts(lo, hi, major, minor);
+  if constexpr (three)
+    last = tc::pack2_bf16(lo - __uint_as_float(major << 16) - __uint_as_float(minor << 16),
+                          hi - __uint_as_float(major & 0xffff0000u) - __uint_as_float(minor & 0xffff0000u));
 }
 
 // Two bf16 values, zero in the place of what is not finite.
@@ -134,7 +152,7 @@ __device__ __forceinline__ bool weigh(Running& r, float (&x)[T][4], float (&f)[2
 }
 
 // The warps' sums together and out: s_m, s_l [warp][16], `values` warp w's sums of row g at w * stride + g * d.
-template <int kWarps>
+template <typename TOut, int kWarps>
 __device__ __forceinline__ void finish(const PagedDecodeLaunch& a, const Part& p, const float (*s_m)[16], const float (*s_l)[16],
                                        const float* values, int stride) {
   const int d = a.c.d;
@@ -160,9 +178,9 @@ __device__ __forceinline__ void finish(const PagedDecodeLaunch& a, const Part& p
       continue;
     }
     sum = make_float2(mean_of(sum.x, total), mean_of(sum.y, total));
-    const int64_t at = p.s * a.o_sb + h * a.o_sh + c;
-    if (a.out_bf16) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at) = tc::pack2_bf16(sum.x, sum.y);
-    else *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = sum;
+    TOut* to = static_cast<TOut*>(a.out) + p.s * a.o_sb + h * a.o_sh + c;
+    if constexpr (sizeof(TOut) == 2) *reinterpret_cast<uint32_t*>(to) = tc::pack2_bf16(sum.x, sum.y);
+    else *reinterpret_cast<float2*>(to) = sum;
   }
 }
 
@@ -223,7 +241,7 @@ constexpr int kTileBytes = 2 * kTile * DP * 2;  // keys, then values
 template <int DP>
 constexpr int kSmem = kStages<DP> * kTileBytes<DP>;  // of a warp
 
-template <int DP, bool kSpare, int kWarps>
+template <typename TOut, int DP, bool kSpare, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps)
 paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
   using T = __nv_bfloat16;
@@ -340,11 +358,11 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[t][e] *= f[kSpare ? 0 : e >> 1];
       }
-      uint32_t w[4], z[4];  // first and second parts: rows row and row + 8 of tile 0, then of tile 1
+      uint32_t w[4], z[4], y[4];  // first, second and third parts: rows row and row + 8 of tile 0, then of tile 1
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) two_parts(x[t][2 * u], x[t][2 * u + 1], w[2 * t + u], z[2 * t + u]);
+        for (int u = 0; u < kRows; ++u) in_parts<kThree<TOut>>(x[t][2 * u], x[t][2 * u + 1], w[2 * t + u], z[2 * t + u], y[2 * t + u]);
       if constexpr (kSpare) {
         w[1] = z[0];
         w[3] = z[2];
@@ -355,6 +373,11 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
         ldmatrix_trans(b, vals + at(((lane >> 3) & 1) * 8 + (lane & 7), 2 * k + (lane >> 4)));
         mma16816(o[2 * k], w[0], w[1], w[2], w[3], b[0], b[1]);
         mma16816(o[2 * k + 1], w[0], w[1], w[2], w[3], b[2], b[3]);
+        if constexpr (kSpare && kThree<TOut>) {
+          // Third parts in the second ones' rows; what the other rows get is nothing beside a weight, and keeps infinities.
+          mma16816(o[2 * k], kTiny, y[0], kTiny, y[2], b[0], b[1]);
+          mma16816(o[2 * k + 1], kTiny, y[0], kTiny, y[2], b[2], b[3]);
+        }
         if constexpr (!kSpare) {
           if (guarded) {
 #pragma unroll
@@ -362,6 +385,10 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
           }
           mma16816(o[2 * k], z[0], z[1], z[2], z[3], b[0], b[1]);
           mma16816(o[2 * k + 1], z[0], z[1], z[2], z[3], b[2], b[3]);
+          if constexpr (kThree<TOut>) {
+            mma16816(o[2 * k], y[0], y[1], y[2], y[3], b[0], b[1]);
+            mma16816(o[2 * k + 1], y[0], y[1], y[2], y[3], b[2], b[3]);
+          }
         }
       }
     }
@@ -403,7 +430,7 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
     }
   }
   __syncthreads();
-  finish<kWarps>(a, p, s_m, s_l, reinterpret_cast<const float*>(pd_smem), kS * kTileBytes<DP> / 4);
+  finish<TOut, kWarps>(a, p, s_m, s_l, reinterpret_cast<const float*>(pd_smem), kS * kTileBytes<DP> / 4);
 }
 
 // ---------------------------------------------------------------------------------------------- 4 bits
@@ -462,7 +489,7 @@ __device__ __forceinline__ uint32_t place4(int r, int ch) {
   else return (uint32_t)((r >> 2) * 128 + ((r & 3) ^ ((r >> 1) & 2)) * 32 + ch * 16);
 }
 
-template <int D, bool kSpare, int kWarps>
+template <typename TOut, int D, bool kSpare, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps)
 paged_decode_four_kernel(const PagedDecodeLaunch a) {
   using T = __nv_bfloat16;
@@ -747,14 +774,14 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
       }
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        uint32_t major[kRows][2], minor[kRows][2];
+        uint32_t major[kRows][2], minor[kRows][2], last[kRows][2];
 #pragma unroll
         for (int u = 0; u < kRows; ++u)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const float pa = x[2 * ks + t][2 * u], pb = x[2 * ks + t][2 * u + 1];
             bias[g][u] = fmaf(pa, f[2 * t][2 * g + 1], fmaf(pb, f[2 * t + 1][2 * g + 1], bias[g][u]));
-            two_parts(pa * f[2 * t][2 * g], pb * f[2 * t + 1][2 * g], major[u][t], minor[u][t]);
+            in_parts<kThree<TOut>>(pa * f[2 * t][2 * g], pb * f[2 * t + 1][2 * g], major[u][t], minor[u][t], last[u][t]);
           }
         // words of two tokens side by side: elements 0 to 3 in `lo`, 4 to 7 in `hi`
         const uint32_t lo0 = __byte_perm(w[0][g], w[1][g], 0x5410), hi0 = __byte_perm(w[0][g], w[1][g], 0x7632);
@@ -764,6 +791,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
           for (int u = 0; u < kRows; ++u) {
             mma16816(o[u][4 * g + m], a0, a1, a2, a3, major[u][0], major[u][1]);
             mma16816(o[u][4 * g + m], a0, a1, a2, a3, minor[u][0], minor[u][1]);
+            if constexpr (kThree<TOut>) mma16816(o[u][4 * g + m], a0, a1, a2, a3, last[u][0], last[u][1]);
           }
         };
         product(0, centred<0>(lo0, one), centred<0>(hi0, one), centred<0>(lo1, one), centred<0>(hi1, one));
@@ -804,7 +832,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
     }
   }
   __syncthreads();
-  finish<kWarps>(a, p, s_m, s_l, reinterpret_cast<const float*>(pd_smem), kRing4<D> / 4);
+  finish<TOut, kWarps>(a, p, s_m, s_l, reinterpret_cast<const float*>(pd_smem), kRing4<D> / 4);
 }
 
 template <typename K>
@@ -818,29 +846,34 @@ cudaError_t launch(K kernel, int warps, int smem, std::atomic<uint64_t>& done, c
 // sequences of up to 20 tokens over 8 key heads, bf16: 28 us, 57 with four warps a block).
 bool one_warp(const PagedDecodeLaunch& a) { return a.S * a.c.Hkv * a.splits >= 152 * 16 && a.c.width * a.c.page / a.splits <= 512; }
 
-template <int DP, bool kSpare>
+template <typename TOut, int DP, bool kSpare>
 cudaError_t launch_bf16(const PagedDecodeLaunch& a, cudaStream_t stream) {
   static std::atomic<uint64_t> done[2];
   static_assert(kStages<DP> * kTileBytes<DP> >= 16 * DP * 4, "a warp's sums take the place of its ring");
-  return one_warp(a) ? launch(paged_decode_bf16_kernel<DP, kSpare, 1>, 1, kSmem<DP>, done[0], a, stream)
-                     : launch(paged_decode_bf16_kernel<DP, kSpare, kMostWarps>, kMostWarps, kSmem<DP>, done[1], a, stream);
+  return one_warp(a) ? launch(paged_decode_bf16_kernel<TOut, DP, kSpare, 1>, 1, kSmem<DP>, done[0], a, stream)
+                     : launch(paged_decode_bf16_kernel<TOut, DP, kSpare, kMostWarps>, kMostWarps, kSmem<DP>, done[1], a, stream);
 }
-template <int D, bool kSpare>
+template <typename TOut, int D, bool kSpare>
 cudaError_t launch_four(const PagedDecodeLaunch& a, cudaStream_t stream) {
   static std::atomic<uint64_t> done[2];
   static_assert(kRing4<D> >= 16 * D * 4, "a warp's sums take the place of its ring");
-  return one_warp(a) ? launch(paged_decode_four_kernel<D, kSpare, 1>, 1, kSmem4<D>, done[0], a, stream)
-                     : launch(paged_decode_four_kernel<D, kSpare, kMostWarps>, kMostWarps, kSmem4<D>, done[1], a, stream);
+  return one_warp(a) ? launch(paged_decode_four_kernel<TOut, D, kSpare, 1>, 1, kSmem4<D>, done[0], a, stream)
+                     : launch(paged_decode_four_kernel<TOut, D, kSpare, kMostWarps>, kMostWarps, kSmem4<D>, done[1], a, stream);
+}
+template <typename TOut, bool kSpare>
+cudaError_t by_width(const PagedDecodeLaunch& a, cudaStream_t stream) {
+  if (a.c.four) return a.c.d == 64 ? launch_four<TOut, 64, kSpare>(a, stream) : launch_four<TOut, 128, kSpare>(a, stream);
+  return a.c.d <= 64 ? launch_bf16<TOut, 64, kSpare>(a, stream) : launch_bf16<TOut, 128, kSpare>(a, stream);
+}
+template <typename TOut>
+cudaError_t by_group(const PagedDecodeLaunch& a, cudaStream_t stream) {
+  return a.H / a.c.Hkv <= 8 ? by_width<TOut, true>(a, stream) : by_width<TOut, false>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_decode_mma(const PagedDecodeLaunch& a, cudaStream_t stream) {
-  const bool spare = a.H / a.c.Hkv <= 8;
-  if (a.c.four && a.c.d == 64) return spare ? launch_four<64, true>(a, stream) : launch_four<64, false>(a, stream);
-  if (a.c.four) return spare ? launch_four<128, true>(a, stream) : launch_four<128, false>(a, stream);
-  if (a.c.d <= 64) return spare ? launch_bf16<64, true>(a, stream) : launch_bf16<64, false>(a, stream);
-  return spare ? launch_bf16<128, true>(a, stream) : launch_bf16<128, false>(a, stream);
+  return a.out_bf16 ? by_group<__nv_bfloat16>(a, stream) : by_group<float>(a, stream);
 }
 
 }  // namespace la

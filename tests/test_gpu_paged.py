@@ -478,6 +478,49 @@ def test_means_of_many_values_keep_their_bits(bits, d, H):
     assert (out[0] - want).norm() <= 2.0 ** -15 * want.norm()
 
 
+def two_tokens(g, dev, S, H, d, bits, low, high):
+    """S sequences of two tokens: a key of zeros with values of zeros, and one whose score x, low <= -x <= high, fp32 holds
+    exactly, with whole numbers as values, which 4 bits hold exactly.  Returns (x [S, H], values [d], the call's inputs)."""
+    k, v = torch.zeros((S, 1, 16, d)), torch.zeros((S, 1, 16, d))
+    c = (1 + torch.rand(S, generator=g)).to(BF)
+    u = (low + (high / 2 - low) * torch.rand((S, H), generator=g)).to(BF)
+    k[:, 0, 1] = c.float()[:, None]
+    v[:, 0, 1] = (torch.arange(d) % 16).float()
+    q = torch.zeros((S, H, d))
+    q[:, :, 0] = -u.float()
+    pools = [t.to(BF) for t in (k, v)]
+    if bits:
+        pools = [pack(t) for t in pools]
+    table = torch.randperm(S, generator=g).int()[:, None]
+    x = q[:, :, 0].double() * c.double()[table[:, 0].long()][:, None]
+    return x.numpy(), v[0, 0, 1].double().numpy(), [*on(dev, q.to(BF), *pools, table), longs(dev, [2] * S)]
+
+
+def check_two_tokens(got, s, es, v, bits):
+    """got [S, H, d] against the softmax of scores 0 and s, which is off by es; the rest of the bound is counted here."""
+    U = ref.U
+    p = np.exp(s)[..., None]
+    # of the second weight: the score in units of log2 (its factor's rounding and the product's), 2 ulp of the exponential;
+    # of the sum: the first weight is one, their sum's rounding; then the weight's three parts together (2^-26), four
+    # additions on the tensor cores that may cut off (2 U), the parts' and warps' sums, the quotient and its rounding
+    bound = es + 2 * U * np.abs(s) + (4 + 1 + 0.25 + 8 + 2 + 2) * U
+    mag = (np.abs(v - 8) + 8 if bits else v) * p / (1 + p)  # 4 bits: centred codes and what they were centred by
+    ref.check(got, p * v / (1 + p), bound[..., None] * mag)
+
+
+@pytest.mark.parametrize("bits,d,H", [(0, 64, 8), (0, 128, 3), (0, 128, 16), (0, 40, 9), (4, 64, 8), (4, 128, 2), (4, 128, 16)])
+def test_weights_of_fp32_outputs_keep_their_bits(bits, d, H):
+    """Weights that two bf16 parts would leave off by up to 2^-17, 128 half steps of fp32."""
+    dev = cuda_device()
+    x, v, inputs = two_tokens(gen(d + H), dev, 100, H, d, bits, 0.5, 3.0)
+    got = la.la_paged_decode_step(*inputs, scale=1.0, out_dtype=FP)
+    check_two_tokens(got, x, 0.0, v, bits)
+    rounded = la.la_paged_decode_step(*inputs, scale=1.0)  # bf16 outputs: two parts, less than a hundredth of their half step
+    p = np.exp(x)[..., None]
+    mag = (np.abs(v - 8) + 8 if bits else v) * p / (1 + p)
+    ref.check(rounded, p * v / (1 + p), 2.0 ** -8 * p * v / (1 + p) + 2.0 ** -16 * mag)
+
+
 @pytest.mark.parametrize("dtype,bits", [(FP, 0), (BF, 0), (BF, 4)])
 def test_steps_report_bad_lengths_and_pages(dtype, bits):
     dev = cuda_device()
