@@ -30,6 +30,18 @@ __device__ __forceinline__ SeenTokens seen_tokens(const PagedDecodeLaunch& a, in
 // The weighted mean; zero where no token has a weight: an empty sequence, pages that are not there, scores of -infinity alone.
 __device__ __forceinline__ float mean_of(float sum, float total) { return total == 0.f ? 0.f : sum / total; }
 
+// A capped score as by `capped`, which is off by ten half steps of fp32, to fp32: a fifth Chebyshev node leaves 2.6e-8 of the
+// polynomial's value, and the difference from the cap is that of the magnitude: at -cap a quotient near one would be taken from it.
+__device__ constexpr float kTanhFine[5] = {0.999999986757f, -0.333330679444f, 0.133247505048f, -0.0529842388285f, 0.0171313444313f};
+__device__ __forceinline__ float capped_fine(float x, float cap, float inv_cap) {
+  const float z = x * inv_cap, u = z * z;
+  float q = kTanhFine[4];
+#pragma unroll
+  for (int i = 3; i >= 0; --i) q = fmaf(q, u, kTanhFine[i]);
+  const float far = fmaf(-2.f * cap, rcp(1.f + ex2(fabsf(z) * (2.f * kLog2e))), cap);
+  return fabsf(z) <= kStraight ? x * q : copysignf(far, x);
+}
+
 // Places of a part's sums, greatest score and sum of weights in the workspace.
 __device__ __forceinline__ float* part_values(const PagedDecodeLaunch& a, int64_t s, int64_t h, int part) {
   return a.parts + ((s * a.H + h) * a.splits + part) * a.c.d;

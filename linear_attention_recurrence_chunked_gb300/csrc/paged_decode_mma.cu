@@ -14,8 +14,8 @@
 // Weights (in 4 bits times their value's scale) are split into bf16 parts for their product with the values.  Two leave them
 // off by 2^-17, a 500th of a bf16 output's own half step.  An fp32 output would show it (1.5e-6 of an output's norm over
 // 8192 tokens, where PyTorch in fp32 is off by 6e-7), so it takes three, off by less than fp32's own rounding (5.5e-7): 395 us
-// instead of 391 for the bf16 batch below, 446 instead of 398 for the one in 4
-// bits; 5 % of bf16 steps with 16 heads a key head, 11 % with one of d = 64.
+// instead of 391 for the bf16 batch above, 446 instead of 398 for the one in 4 bits; bf16 steps with 16 heads a key head 5 %,
+// with one of d = 64 11 %.  Its capped scores take a term more for the same reason (4e-6 of the norm with a cap of 30, 7e-7 so).
 //
 // 4 bits: scales and offsets meet whole sums of codes in fp32 (keys), and weights once per group (values):
 //   q.k = sum over groups of scale (q.code) + offset sum q
@@ -37,7 +37,7 @@ constexpr int kMostWarps = 4;  // of a block: this many, or one
 constexpr float kSlack = 8.f;
 constexpr uint32_t kTiny = 0x00010001u;  // two bf16 2^-133
 template <typename TOut>
-constexpr bool kThree = sizeof(TOut) == 4;  // weights in three parts, not two
+constexpr bool kFine = sizeof(TOut) == 4;  // weights in three parts, not two; caps to fp32
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -189,7 +189,7 @@ __device__ __forceinline__ float score_scale(const PagedDecodeLaunch& a) { retur
 
 // A warp's rows of scores: caps, biases and what is not seen.  tokens(t, e): of tile t, entry e's token's distance from the
 // warp tile's first one.
-template <int T, int kRowsUsed, typename Tokens>
+template <bool fine, int T, int kRowsUsed, typename Tokens>
 __device__ __forceinline__ void bias_and_mask(const PagedDecodeLaunch& a, float (&x)[T][4], const float (&slope)[2], float inv_cap, int age0,
                                               uint32_t seen, uint32_t whole, Tokens tokens) {
   auto each = [&](auto fn) {
@@ -200,7 +200,7 @@ __device__ __forceinline__ void bias_and_mask(const PagedDecodeLaunch& a, float 
 #pragma unroll
         for (int e = 2 * i; e < 2 * i + 2; ++e) x[t][e] = fn(x[t][e], i, t, e & 1);
   };
-  if (a.softcap != 0.f) each([&](float y, int, int, int) { return capped(y, a.softcap, inv_cap) * kLog2e; });
+  if (a.softcap != 0.f) each([&](float y, int, int, int) { return (fine ? capped_fine(y, a.softcap, inv_cap) : capped(y, a.softcap, inv_cap)) * kLog2e; });
   if (a.slopes) each([&](float y, int i, int t, int e) { return fmaf(-slope[i], (float)(age0 - tokens(t, e)), y); });
   if (seen != whole) each([&](float y, int, int t, int e) { return seen >> tokens(t, e) & 1u ? y : -INFINITY; });
 }
@@ -350,7 +350,7 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int e = 0; e < 2 * kRows; ++e) x[t][e] *= scale;
-      bias_and_mask<2, kRows>(a, x, slope, inv_cap, p.seen.hi - 1 - t0, seen, 0xffffu, [&](int t, int e) { return t * 8 + q4 * 2 + e; });
+      bias_and_mask<kFine<TOut>, 2, kRows>(a, x, slope, inv_cap, p.seen.hi - 1 - t0, seen, 0xffffu, [&](int t, int e) { return t * 8 + q4 * 2 + e; });
       float f[2];
       if (weigh<2, kRows>(run, x, f)) {
 #pragma unroll
@@ -362,7 +362,7 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) in_parts<kThree<TOut>>(x[t][2 * u], x[t][2 * u + 1], w[2 * t + u], z[2 * t + u], y[2 * t + u]);
+        for (int u = 0; u < kRows; ++u) in_parts<kFine<TOut>>(x[t][2 * u], x[t][2 * u + 1], w[2 * t + u], z[2 * t + u], y[2 * t + u]);
       if constexpr (kSpare) {
         w[1] = z[0];
         w[3] = z[2];
@@ -373,7 +373,7 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
         ldmatrix_trans(b, vals + at(((lane >> 3) & 1) * 8 + (lane & 7), 2 * k + (lane >> 4)));
         mma16816(o[2 * k], w[0], w[1], w[2], w[3], b[0], b[1]);
         mma16816(o[2 * k + 1], w[0], w[1], w[2], w[3], b[2], b[3]);
-        if constexpr (kSpare && kThree<TOut>) {
+        if constexpr (kSpare && kFine<TOut>) {
           // Third parts in the second ones' rows; what the other rows get is nothing beside a weight, and keeps infinities.
           mma16816(o[2 * k], kTiny, y[0], kTiny, y[2], b[0], b[1]);
           mma16816(o[2 * k + 1], kTiny, y[0], kTiny, y[2], b[2], b[3]);
@@ -385,7 +385,7 @@ paged_decode_bf16_kernel(const PagedDecodeLaunch a) {
           }
           mma16816(o[2 * k], z[0], z[1], z[2], z[3], b[0], b[1]);
           mma16816(o[2 * k + 1], z[0], z[1], z[2], z[3], b[2], b[3]);
-          if constexpr (kThree<TOut>) {
+          if constexpr (kFine<TOut>) {
             mma16816(o[2 * k], y[0], y[1], y[2], y[3], b[0], b[1]);
             mma16816(o[2 * k + 1], y[0], y[1], y[2], y[3], b[2], b[3]);
           }
@@ -742,7 +742,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
       }
     }
     const int t0 = p.first + (warp + i * kWarps) * kPair;
-    bias_and_mask<4, kRows>(a, x, slope, inv_cap, p.seen.hi - 1 - t0, seen, 0xffffffffu, [&](int t, int e) { return token(t, 2 * q4 + e); });
+    bias_and_mask<kFine<TOut>, 4, kRows>(a, x, slope, inv_cap, p.seen.hi - 1 - t0, seen, 0xffffffffu, [&](int t, int e) { return token(t, 2 * q4 + e); });
     float f[2];
     if (weigh<4, kRows>(run, x, f)) {
 #pragma unroll
@@ -781,7 +781,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
           for (int t = 0; t < 2; ++t) {
             const float pa = x[2 * ks + t][2 * u], pb = x[2 * ks + t][2 * u + 1];
             bias[g][u] = fmaf(pa, f[2 * t][2 * g + 1], fmaf(pb, f[2 * t + 1][2 * g + 1], bias[g][u]));
-            in_parts<kThree<TOut>>(pa * f[2 * t][2 * g], pb * f[2 * t + 1][2 * g], major[u][t], minor[u][t], last[u][t]);
+            in_parts<kFine<TOut>>(pa * f[2 * t][2 * g], pb * f[2 * t + 1][2 * g], major[u][t], minor[u][t], last[u][t]);
           }
         // words of two tokens side by side: elements 0 to 3 in `lo`, 4 to 7 in `hi`
         const uint32_t lo0 = __byte_perm(w[0][g], w[1][g], 0x5410), hi0 = __byte_perm(w[0][g], w[1][g], 0x7632);
@@ -791,7 +791,7 @@ paged_decode_four_kernel(const PagedDecodeLaunch a) {
           for (int u = 0; u < kRows; ++u) {
             mma16816(o[u][4 * g + m], a0, a1, a2, a3, major[u][0], major[u][1]);
             mma16816(o[u][4 * g + m], a0, a1, a2, a3, minor[u][0], minor[u][1]);
-            if constexpr (kThree<TOut>) mma16816(o[u][4 * g + m], a0, a1, a2, a3, last[u][0], last[u][1]);
+            if constexpr (kFine<TOut>) mma16816(o[u][4 * g + m], a0, a1, a2, a3, last[u][0], last[u][1]);
           }
         };
         product(0, centred<0>(lo0, one), centred<0>(hi0, one), centred<0>(lo1, one), centred<0>(hi1, one));

@@ -521,6 +521,24 @@ def test_weights_of_fp32_outputs_keep_their_bits(bits, d, H):
     ref.check(rounded, p * v / (1 + p), 2.0 ** -8 * p * v / (1 + p) + 2.0 ** -16 * mag)
 
 
+@pytest.mark.parametrize("bits,d,H", [(0, 64, 8), (0, 128, 16), (4, 64, 8), (4, 128, 16)])
+@pytest.mark.parametrize("low,high", [(4.0, 14.9), (15.5, 60.0)])
+def test_capped_scores_of_fp32_outputs_keep_their_bits(bits, d, H, low, high):
+    """Scores up to half of the cap, and beyond."""
+    dev = cuda_device()
+    U, cap = ref.U, 30.0
+    x, v, inputs = two_tokens(gen(d + H + int(low)), dev, 100, H, d, bits, low, high)
+    z = x / cap
+    s, a, r = cap * np.tanh(z), np.abs(z), 1 / (1 + np.exp(2 * np.abs(z)))
+    # up to half of the cap: the polynomial's 2.6e-8, and an argument off by 2 U twice, which reaches the value with a twelfth;
+    # its last term's rounding and the product's.  Beyond: an exponent off by 8 a U, 2 ulp of its exponential, a sum, 1 ulp of the
+    # reciprocal, and the difference's rounding.
+    near = (2.6e-8 + (5 / 12 + 0.1 + 2) * U) * np.abs(s)
+    far = 2 * cap * r * (8 * a + 4 + 1 + 2) * U + U * np.abs(s)
+    got = la.la_paged_decode_step(*inputs, scale=1.0, softcap=cap, out_dtype=FP)
+    check_two_tokens(got, s, np.where(a <= 0.5, near, far), v, bits)
+
+
 @pytest.mark.parametrize("dtype,bits", [(FP, 0), (BF, 0), (BF, 4)])
 def test_steps_report_bad_lengths_and_pages(dtype, bits):
     dev = cuda_device()
