@@ -162,6 +162,21 @@ def test_norms_of_rows_at_the_ends(dtype):
         assert torch.equal(got[:, [0, 6, 7]], la.la_qk_norm_rope(plain.to(dev), norm=norm)[0][:, [0, 6, 7]])
 
 
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("d", [8, 96, 256])
+def test_norms_of_the_largest_rows(dtype, norm, d):
+    """Rows whose length passes fp32, so that its reciprocal is a subnormal number, beside ordinary ones and small elements."""
+    dev = cuda_device()
+    g = gen(d)
+    size = torch.tensor([1.0, 1e18, 2e19, 1e30, 1e37, 1.2e38, 2.1e38, 3.2e38, 3.3e38, 2.7e38, 1e-3, 1e38]).view(1, 12, 1, 1)
+    x = (torch.rand((1, 12, 5, d), generator=g) * 0.3 + 0.7) * size * (1 - 2.0 * torch.randint(0, 2, (1, 12, 5, d), generator=g))
+    x[..., 3] *= 2.0 ** -60
+    x = x.to(dtype)
+    y, bound = ref.norm_rope(x, None, norm, 1e-6, None, None, None, False, None, FP)
+    ref.check(la.la_qk_norm_rope(x.to(dev), norm=norm, out_dtype=FP)[0], y, bound)
+
+
 def test_positions_outside_the_tables_are_skipped_and_reported():
     dev = cuda_device()
     cos, sin = on(dev, *ref.tables(10, 16))
