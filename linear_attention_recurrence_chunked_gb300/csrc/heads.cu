@@ -135,14 +135,15 @@ qk_norm_rope_kernel(const QkNormRopeLaunch a, const Plan p) {
           for (int i = 0; i < kRows; ++i) sum[i] += __shfl_xor_sync(kFullMask, sum[i], off);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-          scale[i] = rsqrtf(fmaf(sum[i], share, a.eps));
+          sum[i] = fmaf(sum[i], share, a.eps);
+          scale[i] = rsqrtf(sum[i]);
           beyond |= !(sum[i] <= 3.402823466e38f);
         }
         beyond = __any_sync(kFullMask, beyond);
         if (beyond) {
-          // Squares beyond fp32 (elements above 1e18): the same of the row's 2^-80th, whose squares stay below 2^96, so
-          // that eps no longer counts.  The factor keeps its bits: a 2^-80th of it would be a subnormal number for the largest
-          // rows, so it is marked by its sign, and the elements take both.  NaN and infinities stay what they are.
+          // Beyond fp32 (elements above 1e18): the same of the row's 2^-80th, whose squares stay below 2^96, and of eps's
+          // 2^-160th.  The factor keeps its bits: a 2^-80th of it would be a subnormal number for the largest rows, so it is
+          // marked by its sign, and the elements take both.  NaN and infinities stay what they are.
 #pragma unroll
           for (int i = 0; i < kRows; ++i) {
             f32x2 v[4], t = pack2(0.f, 0.f);
@@ -157,7 +158,7 @@ qk_norm_rope_kernel(const QkNormRopeLaunch a, const Plan p) {
             float small = lo + hi;
 #pragma unroll
             for (int off = LPR / 2; off >= 1; off /= 2) small += __shfl_xor_sync(kFullMask, small, off);
-            if (!(sum[i] <= 3.402823466e38f)) scale[i] = -rsqrtf(small * share);
+            if (!(sum[i] <= 3.402823466e38f)) scale[i] = -rsqrtf(fmaf(small, share, a.eps * 0x1p-80f * 0x1p-80f));
           }
         }
       }

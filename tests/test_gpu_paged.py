@@ -177,6 +177,18 @@ def test_norms_of_the_largest_rows(dtype, norm, d):
     ref.check(la.la_qk_norm_rope(x.to(dev), norm=norm, out_dtype=FP)[0], y, bound)
 
 
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+@pytest.mark.parametrize("d", [64, 256])
+def test_a_large_eps_counts_beside_squares_beyond_fp32(norm, d):
+    """Sums of squares just below and beyond fp32's range."""
+    dev = cuda_device()
+    x = randn(gen(d), 2, 8, 3, d) / d ** 0.5
+    x = x / x.norm(dim=-1, keepdim=True) * torch.tensor([0.9, 0.95, 0.99, 0.995, 1.01, 1.05, 1.3, 20.0]).view(1, 8, 1, 1) * 2.0 ** 64
+    for eps in (1e37, 1e33, 1e-6):
+        y, bound = ref.norm_rope(x, None, norm, eps, None, None, None, False, None, FP)
+        ref.check(la.la_qk_norm_rope(x.to(dev), norm=norm, eps=eps)[0], y, bound)
+
+
 def test_positions_outside_the_tables_are_skipped_and_reported():
     dev = cuda_device()
     cos, sin = on(dev, *ref.tables(10, 16))
