@@ -879,3 +879,51 @@ def test_offsets_beyond_32_bits(dtype, bits, page):
     if not bits:
         assert torch.equal(kr[0], k[0]) and torch.equal(kr[1, :, :N - 7], k[1, :, :N - 7])
     assert la.la_device_status() == la.LA_OK
+
+
+@pytest.mark.parametrize("dtype,bits,page", [(BF, 0, 64), (BF, 4, 4096), (FP, 0, 16)])
+def test_tokens_beyond_32_bits_are_where_the_table_says(dtype, bits, page):
+    """Appends into a pool of more than 2^32 bytes whose used pages held a pattern: the same bytes as in a small pool, in their
+    slots and nowhere else on these pages; read back, the same rows."""
+    dev = cuda_device()
+    Hkv, d, S, N = 2, 128, 2, 50
+    row = d * 9 // 16 if bits else d * (2 if dtype == BF else 4)
+    count = (5 << 30) // (Hkv * page * row) + 3
+    if not bits:
+        count = max(count, (1 << 31) // (Hkv * page * d) + 3)
+    need = -(-N // page)
+    assert (count - 2 * S * need) * Hkv * page * row > 1 << 32
+    g = gen(53)
+    far = torch.full((S, need + 1), -1, dtype=torch.int32)
+    for s in range(S):
+        far[s, :need] = torch.arange(count - 1 - s, count - 1 - s - 2 * need, -2).int()
+    near = torch.full((S, need + 1), -1, dtype=torch.int32)
+    near[:, :need] = torch.arange(S * need, dtype=torch.int32).view(S, need)
+    k, v = (randn(g, S, Hkv, N, d, dtype=dtype).to(dev) for _ in range(2))
+    lens, zero = longs(dev, [N, N - 7]), longs(dev, [0, 0])
+    last = row if bits else d
+    kind = torch.uint8 if bits else dtype
+    used = far[:, :need].flatten().long().to(dev)
+    large = [torch.empty((count, Hkv, page, last), dtype=kind, device=dev) for _ in range(2)]
+    small = [torch.empty((S * need, Hkv, page, last), dtype=kind, device=dev) for _ in range(2)]
+    for x, y in zip(large, small):
+        y.view(torch.uint8).fill_(0x5a)
+        x[used] = y
+    la.la_paged_append(k, v, *large, far.to(dev), zero, lens=lens)
+    la.la_paged_append(k, v, *small, near.to(dev), zero, lens=lens)
+    for x, y in zip(large, small):
+        assert torch.equal(x[used].view(torch.uint8), y.view(torch.uint8))
+    rows = la.la_paged_read(*large, far.to(dev), lens, N), la.la_paged_read(*small, near.to(dev), lens, N)
+    for x, y, given in zip(*rows, (k, v)):
+        assert torch.equal(x, y)
+        for b, n in enumerate((N, N - 7)):
+            if bits:  # half a step of a fifteenth of the spread, the scale's rounding for 15 codes, and the row's own
+                want = given[b, :, :n].float()
+                groups = want.unflatten(-1, (2, 64))
+                spread = (groups.amax(-1) - groups.amin(-1)).repeat_interleave(64, -1)
+                off = spread * (0.5 / 15 * (1 + 2.0 ** -8) + 2.0 ** -8)
+                assert torch.all((x[b, :, :n].float() - want).abs() <= off + (want.abs() + off) * 2.0 ** -8)
+            else:
+                assert torch.equal(x[b, :, :n], given[b, :, :n])
+            assert not x[b, :, n:].any()
+    assert la.la_device_status() == la.LA_OK
