@@ -676,10 +676,11 @@ la_status la_paged_read(const la_paged_read_args* args, void* stream);
  *   slopes, softcap, scale : as in la_swa_prefill
  * bf16 (bits 0 and 4): products on the tensor cores with fp32 sums and statistics, the softmax
  * weights in two bf16 parts for a bf16 output (off by 2^-17 of a weight), in three for an fp32 one
- * (less than fp32's own rounding).  fp32: fp32 throughout.  Few or long sequences are split along
- * their tokens; the parts meet in the workspace, which la_paged_decode_workspace_size sizes from the
- * other arguments (0 where nothing is split; 16-byte aligned, dead when the call's work has
- * finished).  A smaller one fails with LA_ERR_WORKSPACE.
+ * (less than fp32's own rounding).  fp32: fp32 throughout.  A weight in the fp32 sums is up to 2^8
+ * (fp32 pages: 1): they may overflow where values pass 2^119 divided by the number of tokens seen.
+ * Few or long sequences are split along their tokens; the parts meet in the workspace, which
+ * la_paged_decode_workspace_size sizes from the other arguments (0 where nothing is split; 16-byte
+ * aligned, dead when the call's work has finished).  A smaller one fails with LA_ERR_WORKSPACE.
  * Launched as a programmatic dependent, as la_decode_step. */
 typedef struct la_paged_decode_args {
   int64_t S, H, H_kv, d, window, page, pages, width;

@@ -1,8 +1,8 @@
 // paged_decode.cu -- attention of one token of each sequence over a paged cache:
 //   s_j = cap tanh(scale q.k_j / cap) - slope (n - 1 - j),   o = sum_j softmax_j(s_j) v_j,   max(0, n - window) <= j < n.
 // This file: the join of a split sequence's parts, the choice of the split, and the kernel of fp32 pages, on the CUDA cores
-// (64 sequences of up to 4096 tokens: 32 heads over 4 at d = 128 271 us, 37 % of the copy rate; 8 heads of their own at d = 64
-// 120 us, 82 %).
+// (64 sequences of up to 4096 tokens: 8 heads of their own at d = 64 120 us, 83 % of the copy rate; at d = 128 32 heads over 4
+// 280 us, 35 %, and 64 over 4, whose pages are read twice, 527 us, 19 %).
 //
 // A warp takes tiles of 32 tokens of its block's part in turn.  It scores them for a few query heads of the group, four
 // elements a lane and d / 4 lanes a row, takes their softmax a token a lane with the running maximum and sum of its
@@ -297,10 +297,12 @@ cudaError_t by_width(const PagedDecodeLaunch& a, cudaStream_t stream) {
 }  // namespace
 
 // Blocks of one part each would leave SMs idle, or end one long sequence after the others.  As many parts as make 16 blocks an SM,
-// so that sequences of unequal lengths even out (256 sequences of 4 key heads, bf16, 402 us; 405 with 8), of at least twice
-// kPartTokens tokens (64 sequences of up to 300 tokens over 8 key heads: 15 us, 21 with kPartTokens); of few sequences 5 blocks an
-// SM, since every part is written and read again (2 sequences of up to 262144 tokens: 137 us with 5, 145 with 16), of kPartTokens
-// or more (1 sequence of 2000 tokens: 9 us, 13 with twice as many).
+// so that sequences of unequal lengths even out (256 sequences of 4 key heads, bf16, 391 us; 396 with 8), and no more than the
+// table has twice kPartTokens tokens (64 sequences of up to 300 tokens over 8 key heads: 15 us, 20 with kPartTokens); of few
+// sequences 5 blocks an SM, since every part is written and read again (2 sequences of up to 262144 tokens: 129 us with 5, 140 with
+// 16), of kPartTokens or more (1 sequence of 2000 tokens: 9.4 us, 11.2 with twice as many).  The lengths are not known here: where
+// a table is much wider than its sequences are long, their parts are those of kPartTokens tokens that the device makes (the 64
+// sequences behind a table for 8192 tokens: 25 us).
 int paged_decode_splits(int64_t S, int64_t Hkv, int64_t tokens) {
   const int64_t blocks = S * Hkv, part = blocks < 152 ? kPartTokens : 2 * kPartTokens, most = (tokens + part - 1) / part;
   const int64_t want = (152 * (blocks < 152 ? 5 : 16) + blocks - 1) / blocks;

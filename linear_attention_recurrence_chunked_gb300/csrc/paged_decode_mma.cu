@@ -5,8 +5,9 @@
 // tiles of its block's part in turn, through a ring of its own in shared memory that asynchronous copies fill, with the
 // running maximum and sum of its tokens; no warp waits for another before the end, where their sums meet.  A tile's pages
 // are looked up one tile (4 bits: sixteen tiles) ahead of its copies.  256 sequences of up to 8192 tokens, 32 heads over 4 and
-// d = 128 in bf16 take 398 us, the measured copy rate; of up to 16384 tokens in 4 bits 398 us, 56 % of it: 920 warp
-// instructions for 32 tokens, of which 290 turn codes into bf16, at 2.2 a clock.
+// d = 128 in bf16 take 391 us, the measured copy rate; of up to 16384 tokens in 4 bits 398 us, 56 % of it: 920 warp
+// instructions for 32 tokens, of which 290 turn codes into bf16, at 2.2 a clock.  With 64 heads over 4, 128 sequences take
+// 231 us in bf16 (86 %) and 322 in 4 bits (35 %, 144 bytes a thread spilled).
 //
 // The running maximum moves only where a score is more than 2^kSlack times beyond it: until then weights are up to 2^kSlack,
 // which costs fp32 sums nothing, and the sums of values need not be scaled.
@@ -23,7 +24,7 @@
 // A key's code is the last bits of a bf16 number, a whole number of 2^-133, which takes a mask, and a head's query is scaled up by
 // a power of two to match (398 us; 415 with keys made like values).  A value's code is put into the mantissa of a one,
 // 1 + code / 16, and less 3/2: sums over thousands of tokens of centred codes come out near zero, while sums of ones would not
-// (off by 5e-4 of an output's norm over 131071 tokens, where tensor cores cut sums off; 7e-6 centred).  Values as whole numbers
+// (off by 5e-4 of an output's norm over 131071 tokens, where tensor cores cut sums off; 2 to 4e-6 centred, fp32 outputs).  Values as whole numbers
 // too, weights scaled by the largest scale so far, took 1 % off for a rescaling and more spilled registers.
 #include <algorithm>
 
@@ -843,7 +844,8 @@ cudaError_t launch(K kernel, int warps, int smem, std::atomic<uint64_t>& done, c
 }
 
 // Many blocks of few tokens: blocks of one warp, so that more sequences are in their chain of length, page and rows at once (512
-// sequences of up to 20 tokens over 8 key heads, bf16: 28 us, 57 with four warps a block).
+// sequences of up to 20 tokens over 8 key heads, bf16: 28 us, 56 with four warps a block).  Few by the table, as lengths are not
+// known here: behind a table for 4096 tokens the same sequences take the 56 us.
 bool one_warp(const PagedDecodeLaunch& a) { return a.S * a.c.Hkv * a.splits >= 152 * 16 && a.c.width * a.c.page / a.splits <= 512; }
 
 template <typename TOut, int DP, bool kSpare>
